@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libwcomp.so")
 # the debug build: kernels check their indexes before memory accesses
 LIB_DEBUG = os.path.join(HERE, "libwcomp_debug.so")
 BUILD_DEBUG = os.path.join(HERE, "_build_debug")
-SOURCES = ["container.cu", "encode.cu", "decode.cu", "gemv.cu"]
+SOURCES = ["container.cu", "encode.cu", "decode.cu", "gemv.cu", "q4.cu", "moe.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]

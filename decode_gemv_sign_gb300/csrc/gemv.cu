@@ -1476,7 +1476,8 @@ extern "C" int wcomp_device_check(void* stream) {
   uint32_t* base = nullptr;
   int st = scratch(dev, &base);
   if (st != WCOMP_OK) return st;
-  uint32_t* words[2] = {base + 2 * kSlots, noalloc_error_word(dev)};
+  uint32_t* const expert_word = work_error_word(dev);
+  uint32_t* words[3] = {base + 2 * kSlots, noalloc_error_word(dev), expert_word};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   bool failed = false;
   for (uint32_t* w : words) {
@@ -1487,7 +1488,9 @@ extern "C" int wcomp_device_check(void* stream) {
     if (e != cudaSuccess) return map_cuda(e);
     if (word) {
       failed = true;
-      e = cudaMemsetAsync(w, 0, sizeof(uint32_t), s);
+      // a grid barrier that ran out leaves its counters behind: they are
+      // cleared with the word
+      e = w == expert_word ? work_reset(dev, s) : cudaMemsetAsync(w, 0, sizeof(uint32_t), s);
       if (e == cudaSuccess) e = cudaStreamSynchronize(s);
       if (e != cudaSuccess) return map_cuda(e);
     }

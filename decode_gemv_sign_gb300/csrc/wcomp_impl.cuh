@@ -413,5 +413,9 @@ int sm_count(int device);
 uint64_t l2_size(int device);
 int map_cuda(cudaError_t e);
 void count_launches(uint64_t k);
+// The expert and 4-bit kernels' error word on device `dev` (null before their
+// first use), and the reset of it and of their work counters (q4.cu).
+uint32_t* work_error_word(int dev);
+cudaError_t work_reset(int dev, cudaStream_t s);
 
 }  // namespace wc

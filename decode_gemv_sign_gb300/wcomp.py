@@ -20,6 +20,8 @@ BYTESPLIT = 0
 K15 = 1
 SCHEMES = {"bytesplit": BYTESPLIT, "byte-split": BYTESPLIT, "k15": K15, BYTESPLIT: BYTESPLIT, K15: K15}
 
+SCORING = {"softmax": 0, "sigmoid": 1}
+
 OK, EINVAL, ENOMEM, ECORRUPT, ECUDA, EUNSUPPORTED, ETIMEOUT, EINTERNAL, EBOUNDS = 0, -1, -2, -3, -4, -5, -6, -7, -8
 
 
@@ -49,6 +51,22 @@ class Info(ctypes.Structure):
         d = {k: getattr(self, k) for k, _ in self._fields_ if k not in ("table", "pad_")}
         d["table"] = list(self.table)
         return d
+
+
+class Q4Info(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("group", ctypes.c_int32),
+                ("pad_", ctypes.c_int32), ("bytes", ctypes.c_uint64)]
+
+    def as_dict(self) -> dict:
+        return {k: getattr(self, k) for k, _ in self._fields_ if k != "pad_"}
+
+
+class MoeArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("d_x", "d_router", "d_bias", "d_gate", "d_up", "d_down", "q4_gate",
+                                               "q4_up", "q4_down", "d_y", "d_ids", "d_weights")] + [
+        ("H", ctypes.c_int64), ("F", ctypes.c_int64), ("T", ctypes.c_int32), ("E", ctypes.c_int32),
+        ("top_k", ctypes.c_int32), ("scoring", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+        ("factor", ctypes.c_float)]
 
 
 _lib = None
@@ -93,13 +111,26 @@ def lib():
     L.wcomp_device_check.restype = ctypes.c_int
     L.wcomp_debug_skip_first_copy.argtypes = [ctypes.c_int]
     L.wcomp_debug_skip_first_copy.restype = ctypes.c_int
+    L.wcomp_q4_encode.argtypes = [P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, P,
+                                  ctypes.POINTER(P)]
+    L.wcomp_q4_pack.argtypes = [P, P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, P,
+                                ctypes.POINTER(P)]
+    L.wcomp_q4_unpack.argtypes = [P, P, P, P]
+    L.wcomp_q4_decode.argtypes = [P, P, P]
+    L.wcomp_q4_gemv.argtypes = [P, P, ctypes.c_int, P, P]
+    L.wcomp_q4_info.argtypes = [P, ctypes.POINTER(Q4Info)]
+    L.wcomp_q4_free.argtypes = [P, P]
+    L.wcomp_q4_free.restype = None
+    L.wcomp_moe.argtypes = [ctypes.POINTER(MoeArgs), P]
     L.wcomp_launch_count.argtypes = []
     L.wcomp_launch_count.restype = ctypes.c_uint64
     for name in ("wcomp_encode", "wcomp_encode_batched", "wcomp_encode_hist_grid", "wcomp_decode", "wcomp_gemv", "wcomp_gemv_noalloc",
                  "wcomp_gemv_bf16", "wcomp_gemv_bf16_batched",
                  "wcomp_decode_batched",
                  "wcomp_gemv_batched", "wcomp_info", "wcomp_serialize", "wcomp_serialize_compact",
-                 "wcomp_deserialize", "wcomp_version", "wcomp_debug_skip_first_copy"):
+                 "wcomp_deserialize", "wcomp_version", "wcomp_debug_skip_first_copy", "wcomp_q4_encode",
+                 "wcomp_q4_pack", "wcomp_q4_unpack", "wcomp_q4_decode", "wcomp_q4_gemv", "wcomp_q4_info",
+                 "wcomp_moe"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -361,6 +392,173 @@ def deserialize(data: bytes, stream=None) -> Container:
     buf = ctypes.create_string_buffer(bytes(data), len(data))
     _check(lib().wcomp_deserialize(buf, len(data), P(_stream(stream)), ctypes.byref(h)), "wcomp_deserialize")
     return Container(h.value)
+
+
+class Q4:
+    """A weight in 4 bits with group scales, living on the GPU (owned by the library).
+
+    ``shape`` is (N, K), or (M, N, K) for M matrices held together.
+    """
+
+    def __init__(self, handle: int, shape, group: int):
+        self._h = handle
+        self.shape = tuple(shape)
+        self.group = group
+
+    @property
+    def handle(self) -> int:
+        if not self._h:
+            raise ValueError("weight was freed")
+        return self._h
+
+    def info(self) -> dict:
+        inf = Q4Info()
+        _check(lib().wcomp_q4_info(P(self.handle), ctypes.byref(inf)), "wcomp_q4_info")
+        return inf.as_dict()
+
+    def free(self, stream=None):
+        if self._h:
+            lib().wcomp_q4_free(P(self._h), P(_stream(stream)))
+            self._h = 0
+
+    def __del__(self):
+        try:
+            if self._h and torch.cuda.is_available():
+                self.free()
+        except Exception:
+            pass
+
+
+def _matrices(shape, what: str) -> tuple:
+    if len(shape) not in (2, 3):
+        raise ValueError(f"{what} must be 2-D [N, K] or 3-D [M, N, K]")
+    return tuple(shape) if len(shape) == 3 else (1, *shape)
+
+
+def q4_encode(w: torch.Tensor, group: int = 128, stream=None) -> Q4:
+    """Quantise BF16 weights W[N, K] or [M, N, K]: 4-bit codes, one BF16 scale per ``group`` columns."""
+    w = _bits16(w, "w")
+    M, N, K = _matrices(w.shape, "w")
+    h = P()
+    _check(lib().wcomp_q4_encode(P(w.data_ptr()), M, N, K, group, P(_stream(stream)), ctypes.byref(h)),
+           "wcomp_q4_encode")
+    return Q4(h.value, w.shape, group)
+
+
+def q4_pack(codes: torch.Tensor, scales: torch.Tensor, K: int, group: int = 128, stream=None) -> Q4:
+    """Take weights quantised elsewhere: a code c stands for (c - 8) * scale.
+
+    ``codes`` uint8 [(M,) N, ceil(K / 2)], the even column in the low nibble;
+    ``scales`` BF16 [(M,) N, ceil(K / group)].
+    """
+    if not isinstance(codes, torch.Tensor) or not codes.is_cuda or codes.dtype != torch.uint8:
+        raise TypeError("codes must be a CUDA uint8 tensor")
+    scales = _bits16(scales, "scales")
+    M, N, kb = _matrices(codes.shape, "codes")
+    if not codes.is_contiguous():
+        raise ValueError("codes must be contiguous")
+    if group not in (32, 64, 128) or K < 1 or kb != (K + 1) // 2:
+        raise ValueError("codes must have ceil(K / 2) bytes a row, and group be 32, 64 or 128")
+    if tuple(scales.shape) != (*codes.shape[:-1], -(-K // group)):
+        raise ValueError("scales must be [..., N, ceil(K / group)] like codes")
+    if scales.device != codes.device:
+        raise ValueError("codes and scales must be on one device")
+    h = P()
+    _check(lib().wcomp_q4_pack(P(codes.data_ptr()), P(scales.data_ptr()), M, N, K, group, P(_stream(stream)),
+                               ctypes.byref(h)), "wcomp_q4_pack")
+    return Q4(h.value, (*codes.shape[:-1], K), group)
+
+
+def q4_unpack(c: Q4, stream=None) -> tuple:
+    """(codes, scales) in the layout that q4_pack takes."""
+    K = c.shape[-1]
+    codes = torch.empty((*c.shape[:-1], (K + 1) // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((*c.shape[:-1], -(-K // c.group)), dtype=torch.bfloat16, device="cuda")
+    _check(lib().wcomp_q4_unpack(P(c.handle), P(codes.data_ptr()), P(scales.data_ptr()), P(_stream(stream))),
+           "wcomp_q4_unpack")
+    return codes, scales
+
+
+def q4_decode(c: Q4, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The weights' values rounded once to BF16, as an int16 tensor of their bits (``out`` if given)."""
+    if out is None:
+        out = torch.empty(c.shape, dtype=torch.int16, device="cuda")
+    out = _bits16(out, "out")
+    if tuple(out.shape) != c.shape:
+        raise ValueError("out has the wrong shape")
+    _check(lib().wcomp_q4_decode(P(c.handle), P(out.data_ptr()), P(_stream(stream))), "wcomp_q4_decode")
+    return out
+
+
+def q4_gemv(c: Q4, x: torch.Tensor, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y[B, N] (fp32) = x[B, K] @ W.T with the 4-bit weights expanded in registers, 1 <= B <= 16."""
+    x = _bits16(x, "x")
+    M, N, K = _matrices(c.shape, "c")
+    if M != 1:
+        raise ValueError("c must hold one matrix")
+    B = x.shape[0] if x.dim() == 2 else 1
+    if x.numel() != B * K:
+        raise ValueError("x has the wrong size")
+    if y is None:
+        y = torch.empty((B, N), dtype=torch.float32, device=x.device)
+    elif not y.is_cuda or y.dtype != torch.float32 or not y.is_contiguous() or y.numel() != B * N:
+        raise ValueError("y must be a contiguous float32 CUDA tensor of B*N elements")
+    _check(lib().wcomp_q4_gemv(P(c.handle), P(x.data_ptr()), B, P(y.data_ptr()), P(_stream(stream))), "wcomp_q4_gemv")
+    return y
+
+
+def moe(x: torch.Tensor, router: torch.Tensor, gate, up, down, top_k: int, *, scoring: str = "softmax",
+        bias: Optional[torch.Tensor] = None, renormalize: bool = True, factor: float = 1.0,
+        y: Optional[torch.Tensor] = None, ids: Optional[torch.Tensor] = None,
+        weights: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One mixture-of-experts layer for x[T, H], 1 <= T <= 16: y[T, H] in x's type.
+
+    ``router`` [E, H] gives the logits; the ``top_k`` experts of largest score
+    (softmax or sigmoid) plus ``bias`` [E] are weighted by their scores,
+    divided by the chosen scores' sum with ``renormalize``, times ``factor``.
+    ``gate``, ``up`` [E, F, H] and ``down`` [E, H, F] are BF16 tensors or Q4
+    weights.  ``ids`` (int32) and ``weights`` (float32) [T, top_k] receive the
+    choice if given.
+    """
+    x = _bits16(x, "x")
+    router = _bits16(router, "router")
+    if x.dim() != 2 or router.dim() != 2 or router.shape[1] != x.shape[1]:
+        raise ValueError("x must be [T, H] and router [E, H]")
+    (T, H), E = x.shape, router.shape[0]
+    if scoring not in SCORING:
+        raise ValueError("scoring must be 'softmax' or 'sigmoid'")
+    a = MoeArgs()
+    q4 = isinstance(gate, Q4)
+    F = gate.shape[1] if len(gate.shape) == 3 else 0
+    for name, w, shape in (("gate", gate, (E, F, H)), ("up", up, (E, F, H)), ("down", down, (E, H, F))):
+        if isinstance(w, Q4) != q4:
+            raise TypeError("gate, up and down must be all BF16 tensors or all Q4 weights")
+        if tuple(w.shape) != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(w.shape)}")
+        if q4:
+            setattr(a, "q4_" + name, w.handle)
+        else:
+            setattr(a, "d_" + name, _bits16(w, name).data_ptr())
+
+    def out(t, what, dtype, shape):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or not t.is_contiguous()                 or tuple(t.shape) != shape:
+            raise ValueError(f"{what} must be a contiguous {dtype} CUDA tensor of shape {list(shape)}")
+        return t.data_ptr()
+
+    if y is None:
+        y = torch.empty_like(x)
+    a.d_x, a.d_router, a.d_y = x.data_ptr(), router.data_ptr(), out(y, "y", y.dtype, (T, H))
+    _bits16(y, "y")
+    if bias is not None:
+        a.d_bias = out(bias, "bias", torch.float32, (E,))
+    if ids is not None:
+        a.d_ids = out(ids, "ids", torch.int32, (T, top_k))
+    if weights is not None:
+        a.d_weights = out(weights, "weights", torch.float32, (T, top_k))
+    a.H, a.F, a.T, a.E, a.top_k = H, F, T, E, top_k
+    a.scoring, a.renormalize, a.factor = SCORING[scoring], int(renormalize), factor
+    _check(lib().wcomp_moe(ctypes.byref(a), P(_stream(stream))), "wcomp_moe")
+    return y
 
 
 def version() -> int:

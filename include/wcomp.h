@@ -239,8 +239,8 @@ WCOMP_API int wcomp_gemv_batched(const wcomp_container* const* containers, const
 
 /*
  * Report and clear the device error words of the current device (the one
- * wcomp_gemv and the batched GEMVs use, and the one in wcomp_gemv_noalloc's
- * static array).  A GEMV kernel whose bounded wait on its own tensor copies
+ * wcomp_gemv and the batched GEMVs use, the one in wcomp_gemv_noalloc's
+ * static array, and the one of wcomp_moe's grid barriers).  A GEMV kernel whose bounded wait on its own tensor copies
  * runs out records it there and finishes without waiting instead of hanging;
  * its outputs are then undefined.  In a debug build (compiled with
  * WCOMP_DEBUG=1) the kernels also check their indexes before memory
@@ -330,6 +330,141 @@ WCOMP_API int wcomp_deserialize(const void* host_buf, uint64_t len, void* stream
  * no-op.  (Library housekeeping; the pages define no counterpart.)
  */
 WCOMP_API void wcomp_free(wcomp_container* c, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Weights in 4 bits with group scales.
+ *
+ * The lossy sibling of the containers above for callers who can spend the
+ * exactness: 4.125 to 4.5 bits per weight instead of 11 to 12, on the same
+ * streaming product.  (The pages describe lossless coding only; these entry
+ * points have no counterpart there.)
+ *
+ *   - A weight is M matrices W[N, K], row-major (M = 1 for a plain weight, the
+ *     number of experts for wcomp_moe).  Groups are `group` (32, 64 or 128)
+ *     consecutive columns of one row, the last one cut off at K.
+ *   - A group holds a BF16 scale s and a 4-bit code c (0..15) per weight, which
+ *     stands for (c - 8) * s.
+ *   - Limits: N and K below 2^31, M * ceil(N / 16) below 2^31; beyond them
+ *     WCOMP_EUNSUPPORTED.
+ *   - A wcomp_q4 is immutable, owned by the library, lives on the device that
+ *     was current when it was made (calls with it on another device return
+ *     WCOMP_EINVAL), takes its memory from the library's stream-ordered pool,
+ *     and is released with wcomp_q4_free.
+ * ------------------------------------------------------------------------ */
+typedef struct wcomp_q4 wcomp_q4;
+
+typedef struct {
+  int64_t M, N, K;
+  int32_t group;
+  int32_t pad_;
+  uint64_t bytes;  /* device memory: codes and scales, padded to 16 rows x 128 columns */
+} wcomp_q4_info_t;
+
+/*
+ * Quantise BF16 weights d_w, uint16[M*N*K] (any alignment; 16-byte aligned
+ * with K % 8 == 0 takes the vector path).  Per group s = bf16(max |w| / 7),
+ * c = clamp(rint(w / s), -7, 7) + 8 with ties to even; s = 0 (zero weights,
+ * or a scale that underflows) gives codes 8.  A group that holds an infinity
+ * or a NaN gets s = NaN, so what is computed from it is NaN.  Asynchronous.
+ */
+WCOMP_API int wcomp_q4_encode(const uint16_t* d_w, int64_t M, int64_t N, int64_t K, int group, void* stream,
+                              wcomp_q4** out);
+
+/*
+ * Take weights that were quantised elsewhere: d_codes uint8[M*N, ceil(K/2)]
+ * (column 2j in the low nibble of byte j, 2j + 1 in the high one) and d_scales
+ * BF16 bits [M*N, ceil(K/group)].  Every code and any scale is accepted.  The
+ * inputs are copied; they may be released in stream order after the call.
+ * wcomp_q4_unpack writes the same two arrays (the unused nibble of an odd K's
+ * last byte reads 8).
+ */
+WCOMP_API int wcomp_q4_pack(const uint8_t* d_codes, const uint16_t* d_scales, int64_t M, int64_t N, int64_t K,
+                            int group, void* stream, wcomp_q4** out);
+WCOMP_API int wcomp_q4_unpack(const wcomp_q4* c, uint8_t* d_codes, uint16_t* d_scales, void* stream);
+
+/*
+ * Read back: d_out, uint16[M*N*K], receives (c - 8) * s in BF16, the exact
+ * product rounded once to nearest even.
+ */
+WCOMP_API int wcomp_q4_decode(const wcomp_q4* c, uint16_t* d_out, void* stream);
+
+/*
+ * y[b, r] = sum_k x[b, k] * (c[r, k] - 8) * s[r, group of k], b < B, r < N, for
+ * a weight of one matrix (M == 1).  d_x uint16[B*K] BF16 bits, 1 <= B <= 16;
+ * d_y float[B*N], overwritten.  A group's sum of x * (c - 8) is exact products
+ * in fp32 on the tensor cores, then scaled and added in fp32 (so a group's
+ * sum must stay finite before its scale: |x| up to 2^110 is safe).  The order
+ * of the sums is fixed: repeated calls give identical bits.  K % 16 != 0 or an
+ * x not 32-byte aligned goes through a padded copy of x.  Memory: that copy
+ * and, where rows are split over thread blocks, their parts come from the
+ * library's stream-ordered pool for the duration of the call; work counters
+ * live in a buffer allocated with cudaMalloc on first use per device.
+ */
+WCOMP_API int wcomp_q4_gemv(const wcomp_q4* c, const uint16_t* d_x, int B, float* d_y, void* stream);
+
+/* Describe a weight (host-side, no device work). */
+WCOMP_API int wcomp_q4_info(const wcomp_q4* c, wcomp_q4_info_t* info);
+
+/*
+ * Release a weight: work queued earlier on `stream` may still use it.  NULL is
+ * a no-op.
+ */
+WCOMP_API void wcomp_q4_free(wcomp_q4* c, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A mixture-of-experts layer for a few tokens.
+ * ------------------------------------------------------------------------ */
+typedef enum { WCOMP_MOE_SOFTMAX = 0, WCOMP_MOE_SIGMOID = 1 } wcomp_moe_scoring;
+
+typedef struct {
+  /* x[T, H] and router[E, H], BF16 bits, row-major; bias[E] fp32 or NULL */
+  const uint16_t* d_x;
+  const uint16_t* d_router;
+  const float* d_bias;
+  /* experts, all three as BF16 rows (gate, up: [E, F, H]; down: [E, H, F]) or
+     all three in 4 bits with one group size (M = E); the other form NULL */
+  const uint16_t* d_gate;
+  const uint16_t* d_up;
+  const uint16_t* d_down;
+  const wcomp_q4* q4_gate;
+  const wcomp_q4* q4_up;
+  const wcomp_q4* q4_down;
+  /* y[T, H] BF16 bits, overwritten; may be x itself */
+  uint16_t* d_y;
+  /* optional outputs, [T, top_k]: the experts in the order of their choice and
+     the weights they got */
+  int32_t* d_ids;
+  float* d_weights;
+  int64_t H, F;
+  int32_t T, E, top_k;
+  int32_t scoring;      /* wcomp_moe_scoring */
+  int32_t renormalize;  /* divide the chosen scores by their sum (at least 1e-20) */
+  float factor;         /* multiplies the weights */
+} wcomp_moe_args;
+
+/*
+ * One layer for T tokens, 1 <= T <= 16, in one kernel:
+ *   l[t, e] = x[t] . router[e];  score = softmax over e, or sigmoid, of l;
+ *   the top_k experts of largest score + bias are chosen (bias only steers the
+ *   choice; ties go to the lowest index; a NaN ranks below everything; an
+ *   expert whose bias is -inf is chosen only when no other is left);
+ *   weight[t, j] = factor * score, divided by the chosen scores' sum if
+ *   renormalize;
+ *   y[t] = sum_j weight[t, j] * down_j (silu(gate_j x[t]) * (up_j x[t])).
+ * Sums, scores and the hidden values between the products are kept to fp32
+ * (hidden values as two BF16 parts, 16 significant bits); y is rounded once.
+ * The order of the sums is fixed: repeated calls give identical bits.
+ * 1 <= top_k <= min(E, 16), E <= 1024, H and F at most 2^24 (beyond:
+ * WCOMP_EUNSUPPORTED).  BF16 experts with H % 8 == 0, F % 8 == 0 and 16-byte
+ * aligned weights take the vector path, other shapes an element path with the
+ * same results.
+ * The kernel is launched cooperatively (its thread blocks meet at two grid
+ * barriers).  A barrier's wait is bounded: if it runs out, the kernel finishes
+ * with undefined outputs and wcomp_device_check reports WCOMP_ETIMEOUT.
+ * Memory: logits, hidden values and, for unaligned x, a padded copy come from
+ * the library's stream-ordered pool for the duration of the call.
+ */
+WCOMP_API int wcomp_moe(const wcomp_moe_args* args, void* stream);
 
 /* Human-readable text for a status code (static string). */
 WCOMP_API const char* wcomp_strerror(int status);
