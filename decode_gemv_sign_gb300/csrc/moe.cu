@@ -8,24 +8,29 @@
 // For a few tokens the layer streams the chosen experts' weights once and does
 // little with them, so the kernel is built around that stream: a persistent
 // cooperative grid runs three phases with a grid barrier between them, and the
-// barrier's wait is spent with the next phase's weights in flight where they
-// are known.
+// second barrier's wait is spent with the next phase's weights in flight.
 //
 //   A  router logits on the tensor cores, H split over warps and CTAs; each
-//      part goes to the workspace in fp32.
+//      part goes to the workspace in fp32.  For 4-bit experts x becomes fp16
+//      records here (tile.cuh).
 //   -- barrier; every CTA then adds the parts in order, chooses the experts
 //      and lists the (expert, token) pairs by expert, the same in every CTA.
-//   B  units of 16 gate rows and the 16 matching up rows of one chosen expert
+//   B  units of 32 gate rows and the 32 matching up rows of one chosen expert
 //      with all its tokens: the eight warps split H, their sums meet in shared
-//      memory, and h = silu(g) u leaves as two BF16 values, high and low part
-//      (16 significant bits, so h costs the result no visible rounding).
-//   -- barrier; the first copies of phase C are issued before it.
-//   C  units of 16 output rows: the warps split the chosen experts' k-steps,
-//      all experts in a row, evenly; at an expert's end a warp adds its sums,
-//      weighted, to its own [token][row] accumulators (fp32, shared memory),
-//      and at the unit's end the warps' accumulators are added in order.
+//      memory, and h = silu(g) u goes to the workspace, each pair's 32 values
+//      as fp16 under their own power of two (4-bit experts: 11 significant
+//      bits, an eighth of a BF16 step) or as two BF16 parts (BF16 experts: 16
+//      significant bits), so h costs the BF16 result no visible rounding.
+//   -- barrier.
+//   C  units of 32 output rows: the k-steps of all chosen experts, one expert
+//      after the other, split evenly over the warps; at an expert's end a warp
+//      adds its sums, weighted, to its own [token][row] accumulators (fp32,
+//      shared memory), and at the unit's end the warps' accumulators are added
+//      in order.
 //
-// Every sum has a fixed order: results repeat bit for bit.
+// Units of B (where there are few) and C are cut over the CTAs so that each
+// streams the same bytes (Cuts, tile.cuh).  Every sum has a fixed order:
+// results repeat bit for bit.
 #include <string.h>
 
 #include <algorithm>
@@ -42,33 +47,41 @@ constexpr int kMaxT = 16;
 constexpr int kMaxK = 16;
 constexpr int kMaxE = 1024;
 constexpr int kMaxPairs = kMaxT * kMaxK;
+constexpr uint32_t kSplits = 4;    // parts of a router logit (CTAs that share its H)
+constexpr uint32_t kMaxGrid = (kSlotWords - 8) / 2;
+constexpr uint32_t kPartFloats = 1024;  // of a unit: B 2 x 32 rows x 16 pairs, C 32 rows x 16 tokens
 constexpr uint64_t kBarrierNs = 1000000000ull;  // how long a CTA waits for the others (1 s)
 
 struct Weights {
   const uint8_t* p;       // 4-bit blocks, or BF16 rows
-  uint64_t expert_bytes;  // from one expert to the next
+  uint64_t expert_bytes;  // 4-bit: from one expert to the next
   uint32_t N, K;
 };
 
 struct MoeParams {
-  const uint16_t* x;  // as the caller gave it, [T, H]
-  const uint16_t* xs; // rows the products read: x, or its padded copy
-  uint64_t ldx;
-  uint32_t kx;
-  uint16_t* xpad;     // set: phase A fills the padded copy
+  const uint16_t* x;      // [T, H]
+  const uint8_t* xs;      // what the products read: x or its padded copy (BF16 rows), or records
+  float* xf;              // records' factors
+  uint64_t xs_bytes;      // from one token to the next
+  uint8_t* make;          // set: phase A makes xs here
   const uint16_t* router;
   const float* bias;
-  Weights gate, up, down;
+  Weights w[3];           // gate, up, down
   uint16_t* y;
-  int32_t* ids;       // optional [T, k]
-  float* weights;     // optional [T, k]
-  float* logits;      // [splits][T][E]
-  uint16_t* h;        // [pairs][2][Fp]
-  uint32_t T, E, k, H, F, Fp, splits;
-  int scoring, renorm;
+  int32_t* ids;           // optional [T, k]
+  float* weights;         // optional [T, k]
+  float* logits;          // [T][E][kSplits], parts of a logit
+  float* part;            // joins: 2 x kPartFloats per CTA, once for B and once for C
+  uint8_t* h;             // 4-bit: [pairs][Fp / 128] records; BF16: [pairs][2][Fp] values
+  float* hf;              // 4-bit: factors [Fp / 32][256]
+  uint32_t T, E, k, H, F, Fp;
+  int scoring, renorm, x_vec;
   float factor;
-  uint32_t* counters; // [0], [1] barriers, [2] CTAs done; zero
+  uint32_t* counters;     // [0], [1] barriers, [2] CTAs done, then one per CTA for each of B's and C's joins; zero
   uint32_t* err;
+};
+struct MoeMaps {
+  CUtensorMap m[3];       // BF16 experts' tensor maps: gate, up, down
 };
 
 // The chosen experts, built alike in every CTA.
@@ -87,12 +100,6 @@ struct Choice {  // before sorting, pair t * k + j
   uint16_t es[kMaxPairs];     // experts, sorted
 };
 
-__device__ __forceinline__ uint64_t now_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-
 // Wait until every CTA of the (cooperative, so resident) grid has arrived.
 // Bounded: after kBarrierNs the error word is set and false comes back, to
 // every thread of the CTA.
@@ -106,7 +113,7 @@ __device__ bool grid_barrier(uint32_t* counter, uint32_t* err, uint32_t* s_ok) {
     while (true) {
       asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
       if (v >= gridDim.x) break;
-      const uint64_t t = now_ns();
+      const uint64_t t = timer_ns();
       if (!deadline) deadline = t + kBarrierNs;
       if (t > deadline) {
         ok = 0u;
@@ -140,17 +147,19 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // Scores and choice of token t by one warp; sc: this warp's E scores in shared
-// memory.  Lane l owns experts l, l + 32, ... (at most 32 of them).
+// memory.  Lane l owns experts l, l + 32, ... (at most 32 of them) and keeps
+// its best one that is not taken, so a round is two warp reductions (the
+// largest key, then the lowest index that has it) and one lane's new search.
 __device__ void choose(const MoeParams& p, uint32_t t, int lane, float* sc, Choice& ch) {
   float mx = -INFINITY;
   for (uint32_t e = lane; e < p.E; e += 32) {
-    float l = 0.f;
-    for (uint32_t s = 0; s < p.splits; ++s) l += __ldcg(p.logits + (uint64_t(s) * p.T + t) * p.E + e);
+    const float4 l4 = __ldcg(reinterpret_cast<const float4*>(p.logits) + uint64_t(t) * p.E + e);
+    const float l = (l4.x + l4.y) + (l4.z + l4.w);
     sc[e] = l;
     mx = fmaxf(mx, l);
   }
-  mx = warp_max(mx);
   if (p.scoring == WCOMP_MOE_SOFTMAX) {
+    mx = warp_max(mx);
     float sum = 0.f;
     for (uint32_t e = lane; e < p.E; e += 32) {
       const float v = expf(sc[e] - mx);
@@ -162,31 +171,35 @@ __device__ void choose(const MoeParams& p, uint32_t t, int lane, float* sc, Choi
   } else {
     for (uint32_t e = lane; e < p.E; e += 32) sc[e] = 1.f / (1.f + expf(-sc[e]));
   }
-  uint32_t taken = 0u;  // bit i: this lane's i-th expert is chosen
-  float psum = 0.f;
-  for (uint32_t j = 0; j < p.k; ++j) {
-    uint64_t best = 0u;  // key, then the complement of the index: ties go to the lowest
+  uint32_t taken = 0u, key = 0u, at = 0xFFFFFFFFu;  // bit i of taken: this lane's i-th expert is chosen
+  auto search = [&]() {
+    key = 0u;
+    at = 0xFFFFFFFFu;
     uint32_t i = 0;
     for (uint32_t e = lane; e < p.E; e += 32, ++i) {
       if ((taken >> i) & 1u) continue;
-      const float by = p.bias ? sc[e] + p.bias[e] : sc[e];
-      const uint64_t key = (uint64_t(rank_key(by)) << 32) | (0xFFFFFFFFu - e);
-      best = key > best ? key : best;
+      const uint32_t kk = rank_key(p.bias ? sc[e] + p.bias[e] : sc[e]);
+      if (at == 0xFFFFFFFFu || kk > key) {
+        key = kk;
+        at = e;
+      }
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const uint64_t v = __shfl_xor_sync(0xffffffffu, best, o);
-      best = v > best ? v : best;
-    }
-    const uint32_t e = 0xFFFFFFFFu - uint32_t(best);  // E >= k: there is always one left
-    if ((e & 31u) == uint32_t(lane)) taken |= 1u << (e >> 5);
-    const float v = sc[e];
-    psum += v;
-    if (lane == 0) {
+  };
+  search();
+  float psum = 0.f;
+  for (uint32_t j = 0; j < p.k; ++j) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, key);
+    const uint32_t e = __reduce_min_sync(0xffffffffu, key == top ? at : 0xFFFFFFFFu);  // E >= k: one is left
+    if (e == at) {
+      taken |= 1u << (e >> 5);
+      const float v = sc[e];
       ch.e[t * p.k + j] = uint16_t(e);
       ch.w[t * p.k + j] = v;
+      search();
     }
   }
+  __syncwarp();
+  for (uint32_t j = 0; j < p.k; ++j) psum += ch.w[t * p.k + j];
   __syncwarp();
   const float mul = p.renorm ? p.factor / (psum != psum ? psum : fmaxf(psum, 1e-20f)) : p.factor;
   if (uint32_t(lane) < p.k) ch.w[t * p.k + lane] *= mul;
@@ -231,320 +244,433 @@ __device__ __forceinline__ void split_bf16(float v, uint16_t& hi, uint16_t& lo) 
   lo = (h & 0x7F80u) == 0x7F80u ? uint16_t(0) : uint16_t(round(__float_as_uint(v - __uint_as_float(h << 16))));
 }
 
+// Matrix i (gate, up, down) of expert e at k-step `step` of 32-row tile `tile`.
 template <class SRC>
-__device__ __forceinline__ typename SRC::Tile expert_tile(const Weights& w, uint32_t e, uint32_t tile) {
-  if constexpr (SRC::kCols == kQ4Cols) {
-    const uint64_t steps = cdiv(w.K, kQ4Cols);
-    return {w.p + e * w.expert_bytes + tile * steps * q4_block_bytes(SRC::NG)};
+__device__ __forceinline__ typename SRC::Cursor expert_at(const MoeParams& p, const MoeMaps& maps, int i, uint32_t e,
+                                                          uint32_t tile, uint32_t step) {
+  const Weights& w = p.w[i];
+  if constexpr (SRC::NG > 0) {
+    return SRC::at(w.p + e * w.expert_bytes, uint32_t(cdiv(w.K, kQ4Cols)), tile, step);
   } else {
-    const uint32_t r0 = tile * kTileRows;
-    return {reinterpret_cast<const uint16_t*>(w.p + e * w.expert_bytes) + uint64_t(r0) * w.K,
-            w.N - r0 < kTileRows ? w.N - r0 : uint32_t(kTileRows), w.K};
+    return {&maps.m[i], reinterpret_cast<const uint16_t*>(w.p), uint64_t(p.E) * w.N,
+            uint64_t(e) * w.N + tile * kTileRows, w.K, step * kBfCols};
   }
 }
 
+// Stages of a warp's ring.  What shared memory the rings leave is L1 for the
+// activations.
 template <class SRC>
-constexpr int moe_depth() { return SRC::kCols == kBfCols ? 2 : SRC::kStage > 1400 ? 3 : 4; }
+constexpr int moe_depth() { return SRC::NG > 0 ? 2 : 3; }
 template <class SRC>
-constexpr uint32_t moe_ring() { return moe_depth<SRC>() * 2 * SRC::kStage; }  // one warp's
-// Shared memory after the rings, used by one phase at a time: the scores
-// (8 warps x 1024), B's parts (2 x 8 warps x 2 tiles x 2 x 512 bytes), C's
-// accumulators (2 x 8 warps x 16 tokens x 16 rows)
-constexpr uint32_t kShare = 32768;
+constexpr uint32_t moe_ring() { return moe_depth<SRC>() * SRC::kStage; }  // one warp's
+// Shared memory after the rings: A's parts (8 warps x 16 x 16), B's sums (8
+// warps x 32 rows x 16 pairs, gate and up in turn), C's accumulators (8 warps x
+// 16 tokens x 32 rows).  The choice's scores (8 warps x 1024) use the rings,
+// idle then.
+constexpr uint32_t kShare = 16384;
+template <class SRC>
+constexpr uint32_t moe_smem() { return kWarps * moe_ring<SRC>() + kShare + kWarps * moe_depth<SRC>() * 8 + 1024; }
 
-template <class SRC, int NT, class ISSUE>
-__device__ __forceinline__ void run_gate_up(const MoeParams& p, const Lists& L, uint32_t a, uint32_t ft, uint32_t w0,
-                                            uint32_t w1, uint32_t ring, uint32_t& slot, int lane, int warp, float* part,
-                                            ISSUE& issue) {
-  constexpr int D = moe_depth<SRC>();
-  const uint32_t p0 = L.start[a], n = L.start[a + 1] - p0;
-  XRows<NT> x;
-  x.K = p.kx;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const uint32_t c = (uint32_t(lane) >> 2) + 8 * nt;
-    x.p[nt] = c < n ? p.xs + uint64_t(L.tok[p0 + c]) * p.ldx : nullptr;
+// A unit's 32 hidden values of pair `pair` (one a lane), rows 32 ft .. of h.
+template <class SRC>
+__device__ __forceinline__ void store_hidden(const MoeParams& p, uint32_t pair, uint32_t ft, int lane, float v) {
+  const uint32_t row = ft * kTileRows + lane;
+  if (row >= p.F) v = 0.f;
+  if constexpr (SRC::NG > 0) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu);
+    const int k = record_exponent(m);
+    const float s = m >= 0x7F800000u ? __uint_as_float(0x7FFFFFFFu) : v * power_of_two(k);
+    const uint32_t run = ft & 3, t = uint32_t(lane) >> 3, i = 2 * run + ((uint32_t(lane) >> 2) & 1), e = lane & 3;
+    uint16_t bits;
+    asm("cvt.rn.f16.f32 %0, %1;" : "=h"(bits) : "f"(s));
+    uint8_t* rec = p.h + (uint64_t(pair) * (p.Fp / kSub) + (ft >> 2)) * kRecord;
+    *reinterpret_cast<uint16_t*>(rec + (i >> 2) * 128 + t * 32 + (i & 3) * 8 + (e & 1) * 4 + (e >> 1) * 2) = bits;
+    if (lane == 0) p.hf[uint64_t(ft) * factor_pitch<4>() + pair] = power_of_two(-k);
+  } else {
+    uint16_t hi, lo;
+    split_bf16(v, hi, lo);
+    uint16_t* h = reinterpret_cast<uint16_t*>(p.h) + uint64_t(pair) * 2 * p.Fp + row;
+    h[0] = hi;
+    h[p.Fp] = lo;
   }
-  float acc[2][NT][4];
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) acc[m][nt][0] = acc[m][nt][1] = acc[m][nt][2] = acc[m][nt][3] = 0.f;
-  for (uint32_t s = w0; s < w1; ++s) {
-    cp_async_wait<D - 1>();
-    // x (or its copy made in phase A) was written before this grid's barrier
-    SRC::template step<2, NT, false>(ring + slot * 2 * SRC::kStage, s, lane, x, acc);
-    issue();
-    slot = slot + 1 == D ? 0 : slot + 1;
-  }
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      *reinterpret_cast<float4*>(part + ((warp * 2 + m) * 2 + nt) * 128 + lane * 4) =
-          make_float4(acc[m][nt][0], acc[m][nt][1], acc[m][nt][2], acc[m][nt][3]);
-  __syncthreads();
-  // thread (row j, pair c): add the warps in order
-  const uint32_t j = threadIdx.x % kTileRows, c = threadIdx.x / kTileRows;
-  if (c < n) {
-    const float* src = part + (c >> 3) * 128 + ((j & 7) * 4 + ((c & 7) >> 1)) * 4 + (j >> 3) * 2 + (c & 1);
-    float g = 0.f, u = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      g += src[w * 512];
-      u += src[w * 512 + 256];
+}
+
+// Phase B: this warp's k-steps [w0, w1) of the gate and up tiles for one
+// expert's n pairs from p0 on, then the unit's sums: thread i gets output i +
+// 256 j (row i % 32, pair i / 32 + 8 j) as g[j] and u[j].
+template <class SRC, int TILES, class RING, class ISSUE>
+__device__ __forceinline__ void gate_up(const MoeParams& p, const Lists& L, uint32_t p0, uint32_t n, uint32_t w0,
+                                        uint32_t w1, RING& ring, int lane, int warp, uint32_t magic, float* share,
+                                        ISSUE& issue, float (&g)[2], float (&u)[2]) {
+  const XRows<TILES> x = x_rows<TILES>(
+      n, lane, [&](uint32_t b) { return p.xs + L.tok[p0 + b] * p.xs_bytes; },
+      [&](uint32_t b) { return p.xf + L.tok[p0 + b]; });
+  float ag[2][TILES][4], au[2][TILES][4];
+  zero<TILES>(ag);
+  zero<TILES>(au);
+  if (w0 < w1) {
+    Product<SRC, TILES, 1> prod;
+    prod.begin(x, w0);
+    for (uint32_t k = w0; k < w1; ++k) {
+      prod.step(ring, k, k, lane, magic, x, ag, issue);
+      prod.step(ring, k, k + 1 < w1 ? k + 1 : k, lane, magic, x, au, issue);
     }
-    const uint32_t row = ft * kTileRows + j;
-    uint16_t hi = 0, lo = 0;
-    if (row < p.F) split_bf16(g / (1.f + expf(-g)) * u, hi, lo);
-    uint16_t* h = p.h + uint64_t(p0 + c) * 2 * p.Fp;
-    h[row] = hi;
-    h[p.Fp + row] = lo;
-    if (ft + 1 == cdiv(p.F, kTileRows))  // zeros up to the row's padded end
-      for (uint32_t f = row + kTileRows; f < p.Fp; f += kTileRows) h[f] = h[p.Fp + f] = 0;
+  }
+  float* mine = share + warp * (2 * TILES * 128);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    __syncthreads();  // what was in `share` is read
+    if (i == 0)
+      put_sums<TILES>(mine, lane, ag);
+    else
+      put_sums<TILES>(mine, lane, au);
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t b = warp + 8 * j;
+      float v = 0.f;
+      if (j < TILES && b < n) v = warp_sums<TILES>(share, kWarps, 2 * TILES * 128, lane, b);
+      if (i == 0)
+        g[j] = v;
+      else
+        u[j] = v;
+    }
   }
 }
 
-// One expert's share [k0, k1) of phase C for this warp, added to its
-// accumulators.  Columns 2c and 2c + 1 of the MMA are the high and low part of
-// pair c, so one lane holds both sums.
-template <class SRC, int NT, class ISSUE>
-__device__ __forceinline__ void run_down(const MoeParams& p, const Lists& L, uint32_t a, uint32_t k0, uint32_t k1,
-                                         uint32_t ring, uint32_t& slot, int lane, float* ys, ISSUE& issue) {
-  constexpr int D = 2 * moe_depth<SRC>();
-  const uint32_t p0 = L.start[a], n = L.start[a + 1] - p0;
-  XRows<NT> x;
-  x.K = p.Fp;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const uint32_t c = (uint32_t(lane) >> 2) + 8 * nt;
-    x.p[nt] = (c >> 1) < n ? p.h + (uint64_t(p0 + (c >> 1)) * 2 + (c & 1)) * p.Fp : nullptr;
-  }
-  float acc[1][NT][4];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) acc[0][nt][0] = acc[0][nt][1] = acc[0][nt][2] = acc[0][nt][3] = 0.f;
-  for (uint32_t s = k0; s < k1; ++s) {
-    cp_async_wait<D - 1>();
-    SRC::template step<1, NT, false>(ring + slot * SRC::kStage, s, lane, x, acc);
-    issue();
-    slot = slot + 1 == D ? 0 : slot + 1;
-  }
+// Phase C: the share [k0, k1) of one expert's k-steps that this warp takes,
+// added to its accumulators ys[token][32 rows].  4-bit: pair c is column c of
+// the MMA.  BF16: columns 2c and 2c + 1 are the parts of pair c, so one lane
+// holds both sums.
+template <class SRC, int TILES, class RING, class ISSUE>
+__device__ __forceinline__ void down(const MoeParams& p, const Lists& L, uint32_t p0, uint32_t n, uint32_t k0,
+                                     uint32_t k1, RING& ring, int lane, uint32_t magic, float* ys, ISSUE& issue) {
+  constexpr bool kQ4 = SRC::NG > 0;
+  const XRows<TILES> x = x_rows<TILES>(
+      kQ4 ? n : 2 * n, lane,
+      [&](uint32_t b) {
+        return kQ4 ? p.h + uint64_t(p0 + b) * (p.Fp / kSub) * kRecord : p.h + (uint64_t(p0) * 2 + b) * p.Fp * 2;
+      },
+      [&](uint32_t b) { return p.hf + p0 + b; });
+  float acc[2][TILES][4];
+  zero<TILES>(acc);
+  Product<SRC, TILES, 4> prod;
+  prod.begin(x, k0);
+  for (uint32_t k = k0; k < k1; ++k) prod.step(ring, k, k + 1 < k1 ? k + 1 : k, lane, magic, x, acc, issue);
   const uint32_t g = uint32_t(lane) >> 2, t = uint32_t(lane) & 3;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const uint32_t c = 4 * nt + t;
-    if (c < n) {
-      float* y = ys + L.tok[p0 + c] * kTileRows;
-      const float w = L.w[p0 + c];
-      y[g] = fmaf(w, acc[0][nt][0] + acc[0][nt][1], y[g]);
-      y[g + 8] = fmaf(w, acc[0][nt][2] + acc[0][nt][3], y[g + 8]);
+  for (int nt = 0; nt < TILES; ++nt) {
+#pragma unroll
+    for (int i = 0; i < (kQ4 ? 2 : 1); ++i) {
+      const uint32_t c = kQ4 ? 8 * nt + 2 * t + i : 4 * nt + t;
+      if (c < n) {
+        float* y = ys + L.tok[p0 + c] * 32 + g;
+        const float w = L.w[p0 + c];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const float lo = kQ4 ? acc[m][nt][i] : acc[m][nt][0] + acc[m][nt][1];
+          const float hi = kQ4 ? acc[m][nt][2 + i] : acc[m][nt][2] + acc[m][nt][3];
+          y[16 * m] = fmaf(w, lo, y[16 * m]);
+          y[16 * m + 8] = fmaf(w, hi, y[16 * m + 8]);
+        }
+      }
     }
   }
   __syncwarp();  // the next expert's pairs may touch the same tokens from other lanes
 }
 
-template <class SRC, bool RVEC>
-__global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant__ MoeParams p) {
-  extern __shared__ __align__(16) uint8_t smem[];
+// Phase A: units of 16 experts and a quarter of H.  Lane (g, t) takes columns
+// 16 t .. 16 t + 15 of a 64-column step of rows g and g + 8 and of tokens g (and
+// g + 8), straight from memory, two steps at a time.
+template <bool VEC>
+__device__ __forceinline__ void load16(const uint16_t* row, uint32_t c, uint32_t n, bool ok, uint32_t (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0u;
+  if (!ok) return;
+  if constexpr (VEC) {
+    if (c < n) ldg_v8(row + c, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (c + e < n) v[e >> 1] |= uint32_t(row[c + e]) << (16 * (e & 1));
+  }
+}
+template <int NT, bool VEC>
+__device__ __forceinline__ void router_logits(const MoeParams& p, float* share, int lane, int warp) {
+  const uint32_t tiles = uint32_t(cdiv(p.E, 16)), steps = uint32_t(cdiv(p.H, kBfCols));
+  const uint32_t g = uint32_t(lane) >> 2, t = uint32_t(lane) & 3;
+  constexpr int U = VEC ? 2 : 1;
+  for (uint32_t u = blockIdx.x; u < tiles * kSplits; u += gridDim.x) {
+    const uint32_t tile = u / kSplits, sp = u % kSplits, part_i = sp * kWarps + warp;
+    constexpr uint32_t parts = kSplits * kWarps;
+    const uint32_t k0 = uint32_t(uint64_t(steps) * part_i / parts), k1 = uint32_t(uint64_t(steps) * (part_i + 1) / parts);
+    const uint32_t e0 = tile * 16 + g;
+    float acc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+    for (uint32_t s0 = k0; s0 < k1; s0 += U) {
+      uint32_t wg[U][8], wh[U][8], xv[U][NT][8];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const uint32_t c = (s0 + i) * kBfCols + 16 * t;
+        const bool in = s0 + i < k1;
+        load16<VEC>(p.router + uint64_t(e0) * p.H, c, p.H, in && e0 < p.E, wg[i]);
+        load16<VEC>(p.router + uint64_t(e0 + 8) * p.H, c, p.H, in && e0 + 8 < p.E, wh[i]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          load16<VEC>(p.x + uint64_t(g + 8 * nt) * p.H, c, p.H, in && g + 8 * nt < p.T, xv[i][nt]);
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_bf16_k16(acc[nt], wg[i][2 * j], wh[i][2 * j], wg[i][2 * j + 1], wh[i][2 * j + 1], xv[i][nt][2 * j],
+                         xv[i][nt][2 * j + 1]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      *reinterpret_cast<float4*>(share + (warp * 2 + nt) * 128 + lane * 4) =
+          make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+    __syncthreads();
+    const uint32_t j = threadIdx.x % 16, b = threadIdx.x / 16, e = tile * 16 + j;
+    if (b < p.T && e < p.E) {
+      const float* src = share + (b >> 3) * 128 + ((j & 7) * 4 + ((b & 7) >> 1)) * 4 + (j >> 3) * 2 + (b & 1);
+      float v = 0.f;
+      for (int w = 0; w < kWarps; ++w) v += src[w * 256];
+      p.logits[(uint64_t(b) * p.E + e) * kSplits + sp] = v;
+    }
+  }
+}
+
+template <class SRC>
+__global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant__ MoeParams p,
+                                                          const __grid_constant__ MoeMaps maps) {
+  static_assert(moe_ring<SRC>() >= kMaxE * 4, "the rings hold the scores");
+  constexpr int D = moe_depth<SRC>();
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // boxes are swizzled in 1024 bytes
   __shared__ Lists L;
   __shared__ Choice ch;
-  __shared__ uint32_t s_ok;
+  __shared__ uint32_t s_flag;
+  const uint32_t magic = q4_magic();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t ring = smem_u32(smem) + uint32_t(warp) * moe_ring<SRC>();
   float* share = reinterpret_cast<float*>(smem + kWarps * moe_ring<SRC>());
+  Ring<SRC, D> ring(smem_u32(smem) + uint32_t(warp) * moe_ring<SRC>(),
+                    smem_u32(smem) + kWarps * moe_ring<SRC>() + kShare + uint32_t(warp) * D * 8, p.err, lane);
 
-  // ---- A: router logits
-  {
-    using R = BfSrc<RVEC>;
-    const Weights rw{reinterpret_cast<const uint8_t*>(p.router), 0, p.E, p.H};
-    const uint32_t tiles = uint32_t(cdiv(p.E, kTileRows)), steps = uint32_t(cdiv(p.H, kBfCols));
-    constexpr int D = int(moe_ring<SRC>() / R::kStage);
-    int par = 0;
-    for (uint32_t u = blockIdx.x; u < tiles * p.splits; u += gridDim.x) {
-      const uint32_t tile = u / p.splits, sp = u % p.splits;
-      const uint32_t part_i = sp * kWarps + warp, parts = p.splits * kWarps;
-      const uint32_t k0 = uint32_t(uint64_t(steps) * part_i / parts), k1 = uint32_t(uint64_t(steps) * (part_i + 1) / parts);
-      const auto t = expert_tile<R>(rw, 0, tile);
-      float acc[1][2][4];
+  // ---- A: router logits, and x in the form that the products take
+  if (p.x_vec) {
+    if (p.T <= 8)
+      router_logits<1, true>(p, share, lane, warp);
+    else
+      router_logits<2, true>(p, share, lane, warp);
+  } else {
+    router_logits<2, false>(p, share, lane, warp);
+  }
+  if (p.make) {
+    // from the last CTA on: the first ones have the router
+    const uint32_t first = (gridDim.x - 1 - blockIdx.x) * kWarps + warp, stride = gridDim.x * kWarps;
+    if constexpr (SRC::NG > 0) {
+      const uint32_t recs = uint32_t(p.xs_bytes / kRecord);
+      for (uint32_t i = first; i < p.T * recs; i += stride) {
+        const uint32_t b = i / recs, rec = i - b * recs, c = rec * kSub + 4 * lane;
+        float v[4];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) acc[0][nt][0] = acc[0][nt][1] = acc[0][nt][2] = acc[0][nt][3] = 0.f;
-      for (int i = 0; i < D; ++i) {
-        if (k0 + i < k1) R::issue(t, k0 + i, ring + i * R::kStage, lane);
-        cp_async_commit();
+        for (int e = 0; e < 4; ++e)
+          v[e] = c + e < p.H ? __uint_as_float(uint32_t(p.x[uint64_t(b) * p.H + c + e]) << 16) : 0.f;
+        record_store(p.make + i * uint64_t(kRecord), p.xf + uint64_t(rec) * factor_pitch<1>() + b, v, lane);
       }
-      for (uint32_t s = k0; s < k1; ++s) {
-        const uint32_t st = ring + (s - k0) % D * R::kStage;
-        cp_async_wait<D - 1>();
-        // activations of this k-step straight from x, whatever its alignment
-        uint32_t xv[2][8];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const uint32_t b = (uint32_t(lane) >> 2) + 8 * nt, c = s * kBfCols + 16 * (uint32_t(lane) & 3);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) xv[nt][i] = 0u;
-          if (b < p.T) {
-            const uint16_t* xr = p.x + uint64_t(b) * p.H;
-            if (!p.xpad) {
-              if (c < p.H) ld_x32<true>(xr + c, xv[nt]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (c + e < p.H) xv[nt][e >> 1] |= uint32_t(__ldg(xr + c + e)) << (16 * (e & 1));
-            }
-          }
-        }
-        const uint32_t sm = st + lane * 16;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 wg = lds_v4(sm + h * 512), wh = lds_v4(sm + 1024 + h * 512);
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            mma16816(acc[0][nt], wg.x, wh.x, wg.y, wh.y, xv[nt][4 * h], xv[nt][4 * h + 1]);
-            mma16816(acc[0][nt], wg.z, wh.z, wg.w, wh.w, xv[nt][4 * h + 2], xv[nt][4 * h + 3]);
-          }
-        }
-        if (s + D < k1) R::issue(t, s + D, st, lane);
-        cp_async_commit();
-      }
-      float* part = share + par * (kWarps * 256);
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-        *reinterpret_cast<float4*>(part + (warp * 2 + nt) * 128 + lane * 4) =
-            make_float4(acc[0][nt][0], acc[0][nt][1], acc[0][nt][2], acc[0][nt][3]);
-      __syncthreads();
-      par ^= 1;
-      const uint32_t j = threadIdx.x % kTileRows, b = threadIdx.x / kTileRows, e = tile * kTileRows + j;
-      if (b < p.T && e < p.E) {
-        const float* src = part + (b >> 3) * 128 + ((j & 7) * 4 + ((b & 7) >> 1)) * 4 + (j >> 3) * 2 + (b & 1);
-        float v = 0.f;
-        for (int w = 0; w < kWarps; ++w) v += src[w * 256];
-        p.logits[(uint64_t(sp) * p.T + b) * p.E + e] = v;
+    } else {
+      const uint32_t Hp = uint32_t(p.xs_bytes / 2);
+      uint16_t* out = reinterpret_cast<uint16_t*>(p.make);
+      for (uint32_t i = first * 32 + lane; i < p.T * Hp; i += stride * 32) {
+        const uint32_t b = i / Hp, c = i - b * Hp;
+        out[i] = c < p.H ? p.x[uint64_t(b) * p.H + c] : uint16_t(0);
       }
     }
-    if (p.xpad)
-      pad_rows(p.x, p.H, p.ldx, p.T, p.xpad, uint64_t(blockIdx.x) * kThreads + threadIdx.x,
-               uint64_t(gridDim.x) * kThreads);
   }
-  bool ok = grid_barrier(p.counters, p.err, &s_ok);
+  bool ok = grid_barrier(p.counters, p.err, &s_flag);
   if (ok) {
     // ---- the choice, alike in every CTA
-    for (uint32_t t = warp; t < p.T; t += kWarps) choose(p, t, lane, share + warp * kMaxE, ch);
+    for (uint32_t t = warp; t < p.T; t += kWarps) choose(p, t, lane, reinterpret_cast<float*>(smem) + warp * kMaxE, ch);
     __syncthreads();
     if (blockIdx.x == 0 && threadIdx.x < p.T * p.k) {
       if (p.ids) p.ids[threadIdx.x] = ch.e[threadIdx.x];
       if (p.weights) p.weights[threadIdx.x] = ch.w[threadIdx.x];
     }
     build_lists(p, ch, L);
+    // the scores were written to the rings by ordinary stores: order them
+    // before the copies that follow
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
 
     // ---- B: gate and up
+    const uint32_t ft_n = uint32_t(cdiv(p.F, kTileRows));
     {
-      const uint32_t ft_n = uint32_t(cdiv(p.F, kTileRows)), units = L.active * ft_n;
-      const uint32_t steps = uint32_t(cdiv(p.H, SRC::kCols));
-      const uint32_t w0 = uint32_t(uint64_t(steps) * warp / kWarps), w1 = uint32_t(uint64_t(steps) * (warp + 1) / kWarps);
-      constexpr int D = moe_depth<SRC>();
-      uint32_t iu = w0 < w1 ? blockIdx.x : units, is = w0, islot = 0;
-      typename SRC::Tile tg{}, tu{};
+      Cuts cuts{L.active * ft_n, uint32_t(cdiv(p.H, SRC::kCols)), 0, L.active * ft_n < 8 * gridDim.x, 0, 0};
+      cuts.spread(gridDim.x);
+      const uint64_t begin = cuts.begin(), end = cuts.end();
+      uint64_t iat = begin;
+      uint32_t ileft = 0;  // copies left of the cursor's part, gate and up in turn
+      typename SRC::Cursor cg{}, cu{};
       auto enter = [&]() {
-        if (iu >= units) return;
-        const uint32_t e = L.expert[iu / ft_n], ft = iu % ft_n;
-        tg = expert_tile<SRC>(p.gate, e, ft);
-        tu = expert_tile<SRC>(p.up, e, ft);
-      };
-      auto issue = [&]() {
-        if (iu < units) {
-          const uint32_t st = ring + islot * 2 * SRC::kStage;
-          SRC::issue(tg, is, st, lane);
-          SRC::issue(tu, is, st + SRC::kStage, lane);
-          if (++is == w1) {
-            is = w0;
-            iu += gridDim.x;
-            enter();
-          }
+        while (iat < end) {
+          const Seg s = seg_at(cuts, iat, end, warp, kWarps);
+          iat += s.k1 - s.k0;
+          if (s.w0 == s.w1) continue;
+          ileft = 2 * (s.w1 - s.w0);
+          const uint32_t e = L.expert[s.unit / ft_n], ft = s.unit % ft_n;
+          cg = expert_at<SRC>(p, maps, 0, e, ft, s.w0);
+          cu = expert_at<SRC>(p, maps, 1, e, ft, s.w0);
+          return;
         }
-        cp_async_commit();
-        islot = islot + 1 == D ? 0 : islot + 1;
+      };
+      auto issue = [&](uint32_t slot) {
+        if (ileft) {
+          if (ileft & 1)
+            ring.refill(slot, cu, lane);
+          else
+            ring.refill(slot, cg, lane);
+          if (--ileft == 0) enter();
+        }
       };
       enter();
-#pragma unroll
-      for (int i = 0; i < D; ++i) issue();
-      uint32_t slot = 0;
-      int par = 0;
-      for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const uint32_t a = u / ft_n, ft = u % ft_n;
-        float* part = share + par * (kWarps * 512);
-        par ^= 1;
-        if (L.start[a + 1] - L.start[a] <= 8)
-          run_gate_up<SRC, 1>(p, L, a, ft, w0, w1, ring, slot, lane, warp, part, issue);
+      for (uint32_t i = 0; i < D; ++i) issue((ring.slot + i) % D);
+      for (uint64_t at = begin; at < end;) {
+        const Seg s = seg_at(cuts, at, end, warp, kWarps);
+        const uint32_t a = s.unit / ft_n, ft = s.unit % ft_n, p0 = L.start[a], n = L.start[a + 1] - p0;
+        float g[2], u[2];
+        if (n <= 8)
+          gate_up<SRC, 1>(p, L, p0, n, s.w0, s.w1, ring, lane, warp, magic, share, issue, g, u);
         else
-          run_gate_up<SRC, 2>(p, L, a, ft, w0, w1, ring, slot, lane, warp, part, issue);
+          gate_up<SRC, 2>(p, L, p0, n, s.w0, s.w1, ring, lane, warp, magic, share, issue, g, u);
+        auto hidden = [&](int j, float gv, float uv) {
+          const uint32_t c = warp + 8 * j;
+          if (c >= n) return;
+          store_hidden<SRC>(p, p0 + c, ft, lane, gv / (1.f + expf(-gv)) * uv);
+          if (ft + 1 == ft_n)  // zeros up to the rows' padded end
+            for (uint32_t f = ft_n; f < p.Fp / kTileRows; ++f) store_hidden<SRC>(p, p0 + c, f, lane, 0.f);
+        };
+        if (s.k0 == 0 && s.k1 == cuts.steps) {
+          hidden(0, g[0], u[0]);
+          hidden(1, g[1], u[1]);
+        } else {
+          // thread i's four values are i + 256 q: gate of pairs 0..7, gate of 8..15, then up
+          float gs[2];
+          join_parts(
+              cuts, s, at == begin, p.part, kPartFloats, p.counters + 8, kPartFloats, &s_flag,
+              [&](uint32_t i) { return i < 256 ? g[0] : i < 512 ? g[1] : i < 768 ? u[0] : u[1]; },
+              [&](uint32_t i, float v) {
+                if (i < 256)
+                  gs[0] = v;
+                else if (i < 512)
+                  gs[1] = v;
+                else if (i < 768)
+                  hidden(0, gs[0], v);
+                else
+                  hidden(1, gs[1], v);
+              });
+        }
+        at += s.k1 - s.k0;
       }
-      cp_async_wait<0>();
     }
 
-    // ---- C: down and the weighted sum
+    // ---- C: down and the weighted sum.  A unit's k-steps are those of all
+    // chosen experts, one expert after the other.
     {
-      const uint32_t ht_n = uint32_t(cdiv(p.H, kTileRows)), steps = uint32_t(cdiv(p.F, SRC::kCols));
-      const uint32_t all = L.active * steps;
-      const uint32_t w0 = uint32_t(uint64_t(all) * warp / kWarps), w1 = uint32_t(uint64_t(all) * (warp + 1) / kWarps);
-      constexpr int D = 2 * moe_depth<SRC>();
-      uint32_t iu = w0 < w1 ? blockIdx.x : ht_n, is = w0, islot = 0, ik = 0, ia = 0;
-      typename SRC::Tile td{};
-      auto enter = [&]() {
-        ia = is / steps;
-        ik = is % steps;
-        td = expert_tile<SRC>(p.down, L.expert[ia], iu);
+      const uint32_t steps = uint32_t(cdiv(p.F, SRC::kCols));
+      Cuts cuts{uint32_t(cdiv(p.H, kTileRows)), L.active * steps, 0, 1, 0, 0};
+      cuts.spread(gridDim.x);
+      const uint64_t begin = cuts.begin(), end = cuts.end();
+      uint64_t iat = begin;
+      // the cursor's unit and place in it; ileft: k-steps to this expert's or the warp's end
+      uint32_t ik = 0, iend = 0, iunit = 0, ileft = 0;
+      typename SRC::Cursor cd{};
+      auto tile = [&]() {
+        const uint32_t a = ik / steps, k = ik - a * steps;
+        ileft = iend - ik < steps - k ? iend - ik : steps - k;
+        ik += ileft;
+        cd = expert_at<SRC>(p, maps, 2, L.expert[a], iunit, k);
       };
-      auto issue = [&]() {
-        if (iu < ht_n) {
-          SRC::issue(td, ik, ring + islot * SRC::kStage, lane);
-          ++ik;
-          if (++is == w1) {
-            is = w0;
-            iu += gridDim.x;
-            if (iu < ht_n) enter();
-          } else if (ik == steps) {
-            enter();
+      auto enter = [&]() {
+        while (iat < end) {
+          const Seg s = seg_at(cuts, iat, end, warp, kWarps);
+          iat += s.k1 - s.k0;
+          if (s.w0 == s.w1) continue;
+          ik = s.w0;
+          iend = s.w1;
+          iunit = s.unit;
+          tile();
+          return;
+        }
+      };
+      auto issue = [&](uint32_t slot) {
+        if (ileft) {
+          ring.refill(slot, cd, lane);
+          if (--ileft == 0) {
+            if (ik < iend)
+              tile();
+            else
+              enter();
           }
         }
-        cp_async_commit();
-        islot = islot + 1 == D ? 0 : islot + 1;
       };
-      if (iu < ht_n) enter();
-#pragma unroll
-      for (int i = 0; i < D; ++i) issue();
-      ok = grid_barrier(p.counters + 1, p.err, &s_ok);
+      enter();
+      for (uint32_t i = 0; i < D; ++i) issue((ring.slot + i) % D);
+      ok = grid_barrier(p.counters + 1, p.err, &s_flag);
       if (ok) {
-        uint32_t slot = 0;
-        int par = 0;
-        for (uint32_t u = blockIdx.x; u < ht_n; u += gridDim.x) {
-          float* acc0 = share + par * (kWarps * kMaxT * kTileRows);
-          float* ys = acc0 + warp * (kMaxT * kTileRows);
-          par ^= 1;
-          for (uint32_t i = lane; i < p.T * kTileRows; i += 32) ys[i] = 0.f;
+        float* ys = share + warp * (kMaxT * 32);
+        for (uint64_t at = begin; at < end;) {
+          const Seg s = seg_at(cuts, at, end, warp, kWarps);
+          __syncthreads();  // the previous unit's accumulators are read
+          for (uint32_t i = lane; i < p.T * 32; i += 32) ys[i] = 0.f;
           __syncwarp();
-          for (uint32_t s = w0; s < w1;) {
-            const uint32_t a = s / steps, k0 = s % steps;
-            const uint32_t k1 = w1 - s < steps - k0 ? k0 + (w1 - s) : steps;
-            const uint32_t n = L.start[a + 1] - L.start[a];
-            if (n <= 4)
-              run_down<SRC, 1>(p, L, a, k0, k1, ring, slot, lane, ys, issue);
-            else if (n <= 8)
-              run_down<SRC, 2>(p, L, a, k0, k1, ring, slot, lane, ys, issue);
-            else
-              run_down<SRC, 4>(p, L, a, k0, k1, ring, slot, lane, ys, issue);
-            s += k1 - k0;
+          for (uint32_t k = s.w0; k < s.w1;) {
+            const uint32_t a = k / steps, k0 = k - a * steps;
+            const uint32_t k1 = s.w1 - k < steps - k0 ? k0 + (s.w1 - k) : steps;
+            const uint32_t p0 = L.start[a], n = L.start[a + 1] - p0;
+            if constexpr (SRC::NG > 0) {
+              if (n <= 8)
+                down<SRC, 1>(p, L, p0, n, k0, k1, ring, lane, magic, ys, issue);
+              else
+                down<SRC, 2>(p, L, p0, n, k0, k1, ring, lane, magic, ys, issue);
+            } else {
+              if (n <= 4)
+                down<SRC, 1>(p, L, p0, n, k0, k1, ring, lane, magic, ys, issue);
+              else if (n <= 8)
+                down<SRC, 2>(p, L, p0, n, k0, k1, ring, lane, magic, ys, issue);
+              else
+                down<SRC, 4>(p, L, p0, n, k0, k1, ring, lane, magic, ys, issue);
+            }
+            k += k1 - k0;
           }
           __syncthreads();
-          const uint32_t j = threadIdx.x % kTileRows, t = threadIdx.x / kTileRows, row = u * kTileRows + j;
-          if (t < p.T && row < p.H) {
+          // output i: row i % 32 of the unit, token i / 32
+          auto value = [&](uint32_t i) {
             float v = 0.f;
-            for (int w = 0; w < kWarps; ++w) v += acc0[(w * kMaxT + t) * kTileRows + j];
-            const uint32_t b = __float_as_uint(v);
-            p.y[uint64_t(t) * p.H + row] =
-                (b & 0x7FFFFFFFu) > 0x7F800000u ? uint16_t(0x7FC0) : uint16_t((b + 0x7FFFu + ((b >> 16) & 1u)) >> 16);
+            for (int w = 0; w < kWarps; ++w) v += share[w * (kMaxT * 32) + i];
+            return v;
+          };
+          auto store = [&](uint32_t i, float v) {
+            const uint32_t row = s.unit * 32 + i % 32, b = __float_as_uint(v);
+            if (row < p.H)
+              p.y[uint64_t(i / 32) * p.H + row] =
+                  (b & 0x7FFFFFFFu) > 0x7F800000u ? uint16_t(0x7FC0) : uint16_t((b + 0x7FFFu + ((b >> 16) & 1u)) >> 16);
+          };
+          if (s.k0 == 0 && s.k1 == cuts.steps) {
+            for (uint32_t i = threadIdx.x; i < p.T * 32; i += kThreads) store(i, value(i));
+          } else {
+            join_parts(cuts, s, at == begin, p.part + 2 * uint64_t(gridDim.x) * kPartFloats, kPartFloats,
+                       p.counters + 8 + kMaxGrid, p.T * 32, &s_flag, value, store);
           }
+          at += s.k1 - s.k0;
         }
+      } else {
+        ring.abandon();
       }
-      cp_async_wait<0>();
     }
   }
   // the last CTA to finish leaves the counters at zero for their next launch
@@ -558,11 +684,11 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
   }
 }
 
-template <class SRC, bool RVEC>
-int launch_moe(MoeParams& p, int dev, cudaStream_t s) {
+template <class SRC>
+int launch_moe(MoeParams& p, const MoeMaps& maps, int dev, cudaStream_t s) {
   static std::atomic<int> cache[64];
-  auto kern = moe_kernel<SRC, RVEC>;
-  constexpr uint32_t smem = kWarps * moe_ring<SRC>() + kShare;
+  auto kern = moe_kernel<SRC>;
+  constexpr uint32_t smem = moe_smem<SRC>();
   int per_sm = cache[dev].load(std::memory_order_acquire);
   if (!per_sm) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
@@ -572,12 +698,25 @@ int launch_moe(MoeParams& p, int dev, cudaStream_t s) {
     if (per_sm < 1) return WCOMP_EUNSUPPORTED;
     cache[dev].store(per_sm, std::memory_order_release);
   }
-  const uint32_t grid = uint32_t(per_sm * sm_count(dev));
-  void* args[] = {&p};
+  const uint32_t grid = std::min(uint32_t(per_sm * sm_count(dev)), kMaxGrid);
+  void* args[] = {&p, const_cast<MoeMaps*>(&maps)};
   const cudaError_t e =
       cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kern), dim3(grid), dim3(kThreads), args, smem, s);
   count_launches(1);
   return map_cuda(e == cudaSuccess ? cudaGetLastError() : e);
+}
+
+// Boxes of 32 rows x 64 columns of a row-major BF16 matrix, 128-byte swizzled.
+bool box_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols) {
+  const EncodeTiledFn f = tensor_map_encoder();
+  if (!f || cols % 8 || (reinterpret_cast<uintptr_t>(base) & 15) || rows >= (uint64_t(1) << 31)) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {cols * 2};
+  const cuuint32_t box[2] = {uint32_t(kBfCols), uint32_t(kTileRows)};
+  const cuuint32_t es[2] = {1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -612,9 +751,7 @@ extern "C" int wcomp_moe(const wcomp_moe_args* a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   MoeParams p;
   memset(&p, 0, sizeof(p));
-  p.x = p.xs = a->d_x;
-  p.ldx = uint64_t(a->H);
-  p.kx = uint32_t(a->H);
+  p.x = a->d_x;
   p.router = a->d_router;
   p.bias = a->d_bias;
   p.y = a->d_y;
@@ -629,51 +766,56 @@ extern "C" int wcomp_moe(const wcomp_moe_args* a, void* stream) {
   p.scoring = a->scoring;
   p.renorm = a->renormalize;
   p.factor = a->factor;
-  Weights* out[3] = {&p.gate, &p.up, &p.down};
+  p.x_vec = p.H % 16 == 0 && aligned(a->d_x, 32) && aligned(a->d_router, 32);
+  MoeMaps maps;
+  memset(&maps, 0, sizeof(maps));
+  bool mapped = !q4;
   for (int i = 0; i < 3; ++i) {
-    Weights& t = *out[i];
+    Weights& t = p.w[i];
     t.N = i == 2 ? p.H : p.F;
     t.K = i == 2 ? p.F : p.H;
     t.p = q4 ? q[i]->d : reinterpret_cast<const uint8_t*>(w[i]);
-    t.expert_bytes = q4 ? q[i]->matrix_bytes() : uint64_t(2) * t.N * t.K;
+    t.expert_bytes = q4 ? q[i]->matrix_bytes() : 0;
+    if (!q4) mapped = mapped && box_map(&maps.m[i], w[i], uint64_t(p.E) * t.N, t.K);
   }
-  // the router's k-steps split over CTAs too, up to four ways where E's tiles
-  // are few; each part is one more term in every CTA's choice
-  const uint32_t tiles = uint32_t(cdiv(p.E, kTileRows)), steps = uint32_t(cdiv(p.H, kBfCols));
-  p.splits = std::max(1u, std::min({4u, uint32_t(sm_count(dev)) / tiles, steps / (2 * kWarps)}));
-  const bool pad = a->H % 16 != 0 || !aligned(a->d_x, 32);
-  const uint64_t Hp = cdiv(p.H, kQ4Cols) * kQ4Cols;
+  // x's form for the products: records, or BF16 rows of whole 64-column steps
+  // that start on 32-byte boundaries
+  const uint64_t Hp = q4 ? cdiv(p.H, kQ4Cols) * kQ4Cols : cdiv(p.H, kBfCols) * kBfCols;
+  const bool make = q4 || Hp != p.H || !aligned(a->d_x, 32);
+  p.xs_bytes = 2 * Hp;
   auto round = [](uint64_t b) { return (b + 255) & ~uint64_t(255); };
-  const uint64_t b_log = round(uint64_t(4) * p.splits * p.T * p.E), b_h = round(uint64_t(4) * p.T * p.k * p.Fp),
-                 b_pad = pad ? round(2 * p.T * Hp) : 0;
+  const uint64_t pairs = uint64_t(p.T) * p.k;
+  const uint64_t b_log = round(uint64_t(4) * kSplits * p.T * p.E), b_h = round(pairs * p.Fp * (q4 ? 2 : 4)),
+                 b_hf = q4 ? round(uint64_t(p.Fp) / 32 * factor_pitch<4>() * 4) : 0,
+                 b_part = uint64_t(2) * 2 * kMaxGrid * kPartFloats * sizeof(float),
+                 b_x = make ? round(p.T * p.xs_bytes) : 0, b_xf = q4 ? round(Hp / kSub * factor_pitch<1>() * 4) : 0;
   uint8_t* ws = nullptr;
-  e = pool_alloc(reinterpret_cast<void**>(&ws), b_log + b_h + b_pad, s);
+  e = pool_alloc(reinterpret_cast<void**>(&ws), b_log + b_h + b_hf + b_part + b_x + b_xf, s);
   if (e != cudaSuccess) return map_cuda(e);
-  p.logits = reinterpret_cast<float*>(ws);
-  p.h = reinterpret_cast<uint16_t*>(ws + b_log);
-  if (pad) {
-    p.xpad = reinterpret_cast<uint16_t*>(ws + b_log + b_h);
-    p.xs = p.xpad;
-    p.ldx = Hp;
-    p.kx = uint32_t(Hp);
-  }
+  uint8_t* at = ws;
+  auto take = [&](uint64_t bytes) {
+    uint8_t* r = at;
+    at += bytes;
+    return r;
+  };
+  p.logits = reinterpret_cast<float*>(take(b_log));
+  p.h = take(b_h);
+  p.hf = reinterpret_cast<float*>(take(b_hf));
+  p.part = reinterpret_cast<float*>(take(b_part));
+  p.make = make ? take(b_x) : nullptr;
+  p.xf = reinterpret_cast<float*>(take(b_xf));
+  p.xs = make ? p.make : reinterpret_cast<const uint8_t*>(a->d_x);
   int st = work_slot(dev, &p.counters, &p.err);
-  const bool rvec = p.H % 8 == 0 && aligned(a->d_router, 16);
-  const bool wvec = p.H % 8 == 0 && p.F % 8 == 0 && aligned(a->d_gate, 16) && aligned(a->d_up, 16) && aligned(a->d_down, 16);
-#define WCOMP_MOE(SRC) st = rvec ? launch_moe<SRC, true>(p, dev, s) : launch_moe<SRC, false>(p, dev, s)
   if (st == WCOMP_OK) {
-    if (!q4) {
-      if (wvec) WCOMP_MOE(BfSrc<true>);
-      else WCOMP_MOE(BfSrc<false>);
-    } else if (q[0]->ng == 1) {
-      WCOMP_MOE(Q4Src<1>);
-    } else if (q[0]->ng == 2) {
-      WCOMP_MOE(Q4Src<2>);
-    } else {
-      WCOMP_MOE(Q4Src<4>);
-    }
+    if (!q4)
+      st = mapped ? launch_moe<BfSrc<true>>(p, maps, dev, s) : launch_moe<BfSrc<false>>(p, maps, dev, s);
+    else if (q[0]->ng == 1)
+      st = launch_moe<Q4Src<1>>(p, maps, dev, s);
+    else if (q[0]->ng == 2)
+      st = launch_moe<Q4Src<2>>(p, maps, dev, s);
+    else
+      st = launch_moe<Q4Src<4>>(p, maps, dev, s);
   }
-#undef WCOMP_MOE
   cudaFreeAsync(ws, s);
   return st;
 }

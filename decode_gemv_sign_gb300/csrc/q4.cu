@@ -20,25 +20,36 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
 // ---------------------------------------------------------------------------
-// Quantise, read back, and the plain layouts.  One warp takes one block (16
-// rows x 128 columns); lane (g, t) holds the 32 columns of its four runs in
-// rows g and g + 8, so codes leave in the A-fragment order with no exchange,
-// and a group's largest magnitude needs two shuffles in a quad.
+// Quantise, read back, and the plain layouts.  One warp takes a quarter block
+// (16 rows x 128 columns: half s, 16-row half-tile m); lane (g, t) holds the 32
+// columns 32 q + 8 t .. + 7 (run q = 0..3) of rows g and g + 8, so codes leave
+// in the operands' order with no exchange, and a group's largest magnitude
+// needs two shuffles in a quad.
 // ---------------------------------------------------------------------------
 struct Blocks {
   uint8_t* d;
-  uint64_t N, K, tiles, blocks, total;  // total = M * tiles * blocks
+  uint64_t N, K, tiles, blocks, total;  // total = M * tiles * blocks * 4
 };
 
-// Block i of a batch of matrices: its first row and column, and the row index
-// of its first row over all matrices.
+// Quarter block i of a batch of matrices: its block, place in it, first row and
+// column in its matrix, and that row's index over all matrices.
 struct At {
-  uint64_t r0, k0, row;
+  uint64_t block, r0, k0, row;
+  uint32_t s, m;
 };
-__device__ __forceinline__ At block_at(const Blocks& b, uint64_t i) {
-  const uint64_t tile = i / b.blocks;
-  const uint64_t m = tile / b.tiles, t = tile % b.tiles;
-  return {t * kTileRows, (i % b.blocks) * kQ4Cols, m * b.N + t * kTileRows};
+__device__ __forceinline__ At quarter_at(const Blocks& b, uint64_t i) {
+  At a;
+  a.block = i >> 2;
+  a.s = (i >> 1) & 1;
+  a.m = i & 1;
+  const uint64_t tile = a.block / b.blocks, mat = tile / b.tiles;
+  a.r0 = (tile - mat * b.tiles) * kTileRows + 16 * a.m;
+  a.k0 = (a.block - tile * b.blocks) * kQ4Cols + kSub * a.s;
+  a.row = mat * b.N + a.r0;
+  return a;
+}
+__device__ __forceinline__ uint8_t* codes_at(uint8_t* block, const At& a, int lane) {
+  return block + (2 * a.s + a.m) * 1024 + lane * 16;
 }
 
 __device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {
@@ -93,20 +104,39 @@ __device__ __forceinline__ void load8(const uint16_t* __restrict__ row, uint64_t
   }
 }
 
+// Codes and scales of one quarter block to memory: columns 2 e and 2 e + 1 of
+// run q are a byte (low and high nibble) of word 2 q + e / 2, at bit 16 (e % 2)
+// for row g and 8 above it for row g + 8.
+template <int NG>
+__device__ __forceinline__ void store_quarter(uint8_t* block, const At& a, int lane, const uint32_t (&words)[8],
+                                              const uint32_t (&sc)[2][NG]) {
+  uint8_t* out = codes_at(block, a, lane);
+  *reinterpret_cast<uint4*>(out) = make_uint4(words[0], words[1], words[2], words[3]);
+  *reinterpret_cast<uint4*>(out + 512) = make_uint4(words[4], words[5], words[6], words[7]);
+  const uint32_t g = uint32_t(lane) >> 2, t = uint32_t(lane) & 3;
+  if (int(t) < NG) {  // lane t of a quad writes group t's scales
+    uint32_t s2 = sc[0][0] | (sc[1][0] << 16);
+#pragma unroll
+    for (int j = 1; j < NG; ++j)
+      if (int(t) == j) s2 = sc[0][j] | (sc[1][j] << 16);
+    *reinterpret_cast<uint32_t*>(block + q4_scale_at(NG, a.s, t, a.m, g)) = s2;
+  }
+}
+
 template <int NG, bool VEC>
 __global__ void __launch_bounds__(kThreads) q4_encode_kernel(const uint16_t* __restrict__ w,
                                                              const __grid_constant__ Blocks b) {
   const int lane = threadIdx.x & 31;
   const uint32_t g = uint32_t(lane) >> 2, t = uint32_t(lane) & 3;
   for (uint64_t i = uint64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < b.total; i += uint64_t(gridDim.x) * kWarps) {
-    const At a = block_at(b, i);
+    const At a = quarter_at(b, i);
     uint32_t v[2][4][4];  // row half, run, pairs
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const bool ok = a.r0 + g + 8 * r < b.N;
       const uint16_t* row = w + (a.row + g + 8 * r) * b.K;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) load8<VEC>(row, a.k0 + q4_col<NG>(q, t), b.K, ok, v[r][q]);
+      for (int q = 0; q < 4; ++q) load8<VEC>(row, a.k0 + 32 * q + 8 * t, b.K, ok, v[r][q]);
     }
     uint32_t sc[2][NG];
 #pragma unroll
@@ -134,30 +164,17 @@ __global__ void __launch_bounds__(kThreads) q4_encode_kernel(const uint16_t* __r
         if (s >= 0x1p-100f) {
           const float rs = __frcp_rn(s);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t p = uint32_t(r) + 2 * (e & 1);
-            words[2 * q + (e >> 1)] |= (code_fast(bf16_lo(v[r][q][e]), rs) << (4 * p)) |
-                                       (code_fast(bf16_hi(v[r][q][e]), rs) << (4 * p + 16));
-          }
+          for (int e = 0; e < 4; ++e)
+            words[2 * q + (e >> 1)] |= (code_fast(bf16_lo(v[r][q][e]), rs) << (16 * (e & 1) + 8 * r)) |
+                                       (code_fast(bf16_hi(v[r][q][e]), rs) << (16 * (e & 1) + 8 * r + 4));
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t p = uint32_t(r) + 2 * (e & 1);
-            words[2 * q + (e >> 1)] |= (code_slow(bf16_lo(v[r][q][e]), s) << (4 * p)) |
-                                       (code_slow(bf16_hi(v[r][q][e]), s) << (4 * p + 16));
-          }
+          for (int e = 0; e < 4; ++e)
+            words[2 * q + (e >> 1)] |= (code_slow(bf16_lo(v[r][q][e]), s) << (16 * (e & 1) + 8 * r)) |
+                                       (code_slow(bf16_hi(v[r][q][e]), s) << (16 * (e & 1) + 8 * r + 4));
         }
       }
-    uint8_t* out = b.d + i * q4_block_bytes(NG);
-    *reinterpret_cast<uint4*>(out + lane * 16) = make_uint4(words[0], words[1], words[2], words[3]);
-    *reinterpret_cast<uint4*>(out + 512 + lane * 16) = make_uint4(words[4], words[5], words[6], words[7]);
-    if (int(t) < NG) {  // lane t of a quad writes group t's scales
-      uint32_t s2 = sc[0][0] | (sc[1][0] << 16);
-#pragma unroll
-      for (int j = 1; j < NG; ++j)
-        if (int(t) == j) s2 = sc[0][j] | (sc[1][j] << 16);
-      *reinterpret_cast<uint32_t*>(out + 1024 + (g * NG + t) * 4) = s2;
-    }
+    store_quarter<NG>(b.d + a.block * q4_block_bytes(NG), a, lane, words, sc);
   }
 }
 
@@ -168,20 +185,22 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
 }
 
 // (c - 8) * s is an integer of at most 4 bits times an 8-bit significand: the
-// BF16 multiply rounds the exact product once.
+// BF16 multiply rounds the exact product once.  c | 0x4300 is the BF16 value
+// 128 + c, so taking 136 away leaves c - 8 exactly.
 template <int NG, bool VEC>
 __global__ void __launch_bounds__(kThreads) q4_decode_kernel(const __grid_constant__ Blocks b,
                                                              uint16_t* __restrict__ out) {
   const int lane = threadIdx.x & 31;
   const uint32_t g = uint32_t(lane) >> 2, t = uint32_t(lane) & 3;
   for (uint64_t i = uint64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < b.total; i += uint64_t(gridDim.x) * kWarps) {
-    const At a = block_at(b, i);
-    const uint8_t* in = b.d + i * q4_block_bytes(NG);
-    const uint4 c0 = ld_stream_v4(in + lane * 16), c1 = ld_stream_v4(in + 512 + lane * 16);
+    const At a = quarter_at(b, i);
+    uint8_t* block = b.d + a.block * q4_block_bytes(NG);
+    const uint8_t* in = codes_at(block, a, lane);
+    const uint4 c0 = ld_stream_v4(in), c1 = ld_stream_v4(in + 512);
     const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
     uint32_t sc[NG];
 #pragma unroll
-    for (int j = 0; j < NG; ++j) sc[j] = ld_stream_u32(in + 1024 + (g * NG + j) * 4);
+    for (int j = 0; j < NG; ++j) sc[j] = ld_stream_u32(block + q4_scale_at(NG, a.s, j, a.m, g));
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       if (a.r0 + g + 8 * r >= b.N) continue;
@@ -191,8 +210,18 @@ __global__ void __launch_bounds__(kThreads) q4_decode_kernel(const __grid_consta
         const uint32_t s2 = prmt(sc[q * NG / 4], 0u, r ? 0x3232u : 0x1010u);
         uint32_t v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = mul2(q4_pair(cw[2 * q + (e >> 1)], r + 2 * (e & 1)), s2);
-        const uint64_t c = a.k0 + q4_col<NG>(q, t);
+        for (int e = 0; e < 2; ++e) {
+          // columns 0, 2 and 1, 3 of the word as pairs, then in order
+          const uint32_t w = cw[2 * q + e] >> (8 * r);
+          uint32_t even, odd;
+          asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(even) : "r"((w & 0x000F000Fu) | 0x43004300u), "r"(0x43084308u));
+          asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(odd) : "r"(((w >> 4) & 0x000F000Fu) | 0x43004300u), "r"(0x43084308u));
+          even = mul2(even, s2);
+          odd = mul2(odd, s2);
+          v[2 * e] = prmt(even, odd, 0x5410u);
+          v[2 * e + 1] = prmt(even, odd, 0x7632u);
+        }
+        const uint64_t c = a.k0 + 32 * q + 8 * t;
         if constexpr (VEC) {
           if (c < b.K) *reinterpret_cast<uint4*>(row + c) = make_uint4(v[0], v[1], v[2], v[3]);
         } else {
@@ -214,10 +243,10 @@ __global__ void __launch_bounds__(kThreads) q4_pack_kernel(const uint8_t* __rest
                                                            const __grid_constant__ Blocks b) {
   const int lane = threadIdx.x & 31;
   const uint32_t g = uint32_t(lane) >> 2, t = uint32_t(lane) & 3;
-  const uint64_t pitch = (b.K + 1) / 2, groups = cdiv(b.K, kQ4Cols / NG);
+  const uint64_t pitch = (b.K + 1) / 2, groups = cdiv(b.K, kSub / NG);
   for (uint64_t i = uint64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < b.total; i += uint64_t(gridDim.x) * kWarps) {
-    const At a = block_at(b, i);
-    uint32_t words[8];
+    const At a = quarter_at(b, i);
+    uint32_t words[8], sc[2][NG];
 #pragma unroll
     for (int j = 0; j < 8; ++j) words[j] = 0u;
 #pragma unroll
@@ -226,32 +255,25 @@ __global__ void __launch_bounds__(kThreads) q4_pack_kernel(const uint8_t* __rest
       const uint8_t* row = codes + (a.row + g + 8 * r) * pitch;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const uint64_t c = a.k0 + q4_col<NG>(q, t);
+        const uint64_t c = a.k0 + 32 * q + 8 * t;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 4; ++e) {  // columns c + 2 e, c + 2 e + 1
           uint32_t lo = 8u, hi = 8u;
           if (ok && c + 2 * e < b.K) {
             const uint32_t byte = row[(c >> 1) + e];
             lo = byte & 15u;
             if (c + 2 * e + 1 < b.K) hi = byte >> 4;
           }
-          const uint32_t p = uint32_t(r) + 2 * (e & 1);
-          words[2 * q + (e >> 1)] |= (lo << (4 * p)) | (hi << (4 * p + 16));
+          words[2 * q + (e >> 1)] |= (lo | (hi << 4)) << (16 * (e & 1) + 8 * r);
         }
       }
-    }
-    uint8_t* out = b.d + i * q4_block_bytes(NG);
-    *reinterpret_cast<uint4*>(out + lane * 16) = make_uint4(words[0], words[1], words[2], words[3]);
-    *reinterpret_cast<uint4*>(out + 512 + lane * 16) = make_uint4(words[4], words[5], words[6], words[7]);
-    if (int(t) < NG) {
-      const uint64_t j = a.k0 / (kQ4Cols / NG) + t;
-      uint32_t s2 = 0u;
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-        if (a.r0 + g + 8 * r < b.N && j < groups)
-          s2 |= uint32_t(scales[(a.row + g + 8 * r) * groups + j]) << (16 * r);
-      *reinterpret_cast<uint32_t*>(out + 1024 + (g * NG + t) * 4) = s2;
+      for (int j = 0; j < NG; ++j) {
+        const uint64_t gr = a.k0 / (kSub / NG) + j;
+        sc[r][j] = ok && gr < groups ? uint32_t(scales[(a.row + g + 8 * r) * groups + gr]) : 0u;
+      }
     }
+    store_quarter<NG>(b.d + a.block * q4_block_bytes(NG), a, lane, words, sc);
   }
 }
 
@@ -261,11 +283,12 @@ __global__ void __launch_bounds__(kThreads) q4_unpack_kernel(const __grid_consta
                                                              uint16_t* __restrict__ scales) {
   const int lane = threadIdx.x & 31;
   const uint32_t g = uint32_t(lane) >> 2, t = uint32_t(lane) & 3;
-  const uint64_t pitch = (b.K + 1) / 2, groups = cdiv(b.K, kQ4Cols / NG);
+  const uint64_t pitch = (b.K + 1) / 2, groups = cdiv(b.K, kSub / NG);
   for (uint64_t i = uint64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < b.total; i += uint64_t(gridDim.x) * kWarps) {
-    const At a = block_at(b, i);
-    const uint8_t* in = b.d + i * q4_block_bytes(NG);
-    const uint4 c0 = ld_stream_v4(in + lane * 16), c1 = ld_stream_v4(in + 512 + lane * 16);
+    const At a = quarter_at(b, i);
+    uint8_t* block = b.d + a.block * q4_block_bytes(NG);
+    const uint8_t* in = codes_at(block, a, lane);
+    const uint4 c0 = ld_stream_v4(in), c1 = ld_stream_v4(in + 512);
     const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -273,201 +296,136 @@ __global__ void __launch_bounds__(kThreads) q4_unpack_kernel(const __grid_consta
       uint8_t* row = codes + (a.row + g + 8 * r) * pitch;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const uint64_t c = a.k0 + q4_col<NG>(q, t);
+        const uint64_t c = a.k0 + 32 * q + 8 * t;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint32_t p = uint32_t(r) + 2 * (e & 1), wv = cw[2 * q + (e >> 1)];
-          if (c + 2 * e < b.K) row[(c >> 1) + e] = uint8_t(((wv >> (4 * p)) & 15u) | (((wv >> (4 * p + 16)) & 15u) << 4));
+          if (c + 2 * e < b.K) row[(c >> 1) + e] = uint8_t(cw[2 * q + (e >> 1)] >> (16 * (e & 1) + 8 * r));
         }
       }
-      const uint64_t j = a.k0 / (kQ4Cols / NG) + t;
-      if (int(t) < NG && j < groups)
-        scales[(a.row + g + 8 * r) * groups + j] =
-            uint16_t(ld_stream_u32(in + 1024 + (g * NG + t) * 4) >> (16 * r));
+      const uint64_t gr = a.k0 / (kSub / NG) + t;
+      if (int(t) < NG && gr < groups)
+        scales[(a.row + g + 8 * r) * groups + gr] =
+            uint16_t(ld_stream_u32(block + q4_scale_at(NG, a.s, t, a.m, g)) >> (16 * r));
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// GEMV.  A CTA of 8 warps works on groups of WM x MT tiles; WK = 8 / WM warps
-// share a tile's k-steps.  The launch's k-steps, row group after row group,
-// are cut into one contiguous range per CTA: `split` cuts anywhere, otherwise
-// ranges end on whole row groups.  A row group that lies in one CTA goes
-// straight to y; of a cut one each CTA leaves its fp32 part in the workspace
-// and the CTA that arrives last adds them in the order of the CTAs, so the
-// result does not depend on which CTA that is.
+// GEMV.  A first kernel turns x into records (record_store).  The second is
+// launched to start before the first has ended: it fills its rings with
+// weights and only then waits for the records.  A unit is WM tiles; the 8
+// warps of a CTA are WM rows of warps whose WK = 8 / WM members share a tile's
+// k-steps.  The units' k-steps are cut over the CTAs (Cuts).
 // ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) q4_x_kernel(const uint16_t* __restrict__ x, uint64_t K, uint32_t recs, uint32_t B,
+                                                   uint8_t* __restrict__ out, float* __restrict__ factors) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const uint64_t i = uint64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (i >= uint64_t(B) * recs) return;
+  const uint64_t b = i / recs, k = (i - b * recs) * kSub + 4 * lane;
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = k + e < K ? __uint_as_float(uint32_t(x[b * K + k + e]) << 16) : 0.f;
+  record_store(out + i * kRecord, factors + (i - b * recs) * factor_pitch<1>() + b, v, lane);
+}
+
 struct GemvArgs {
   const uint8_t* w;
-  const uint16_t* x;
-  uint64_t ldx;         // columns per row of x
-  uint32_t kx;          // readable columns of a row of x, a multiple of 16
+  const uint8_t* xq;    // [B][2 * steps] records
+  const float* factors;
   float* y;
-  float* part;          // [2 * grid][B][rows of a group]
-  uint32_t* counters;   // one per row group, zero
+  float* part;          // 2 B rows-of-a-unit floats per CTA
+  uint32_t* counters;   // one per CTA, zero
+  uint32_t* err;
   uint64_t N;
-  uint32_t steps;       // k-steps (blocks) of a tile
-  uint32_t tiles, groups;
-  int B, wm, split;
+  Cuts cuts;
+  uint32_t tiles;
+  int B, wm;
 };
 
-__host__ __device__ inline uint64_t range_start(const GemvArgs& p, uint32_t cta, uint32_t grid) {
-  if (p.split) return uint64_t(p.groups) * p.steps * cta / grid;
-  return uint64_t(p.groups) * cta / grid * p.steps;
+constexpr int kDepth = 2;  // stages of a warp: a third takes L1 from the activations (16384 x 53248, B = 16: 126 -> 147 us)
+
+template <int NG, int TILES>
+constexpr uint32_t q4_smem() {
+  return kWarps * (kDepth * Q4Src<NG>::kStage + 2 * TILES * 512 + kDepth * 8) + 128;
 }
 
-constexpr int q4_depth(int ng, int mt) { return mt == 1 ? 6 : ng == 4 ? 3 : 4; }
-
-template <int NG, int MT>
-constexpr uint32_t q4_ring() { return kWarps * q4_depth(NG, MT) * MT * Q4Src<NG>::kStage; }
-
-template <int NG, int MT, int NT>
+template <int NG, int TILES>
 __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_constant__ GemvArgs p) {
   using S = Q4Src<NG>;
-  constexpr int D = q4_depth(NG, MT);
-  extern __shared__ __align__(16) uint8_t smem[];
-  float* part = reinterpret_cast<float*>(smem + q4_ring<NG, MT>());  // [2][warp][MT][NT][lane][4]
-  __shared__ uint32_t s_last;
+  const uint32_t magic = q4_magic();
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 127u);
+  float* part = reinterpret_cast<float*>(smem + kWarps * kDepth * S::kStage);  // [warp][half-tile][TILES][lane][4]
+  __shared__ uint32_t s_flag;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int wk_n = kWarps / p.wm, wm = warp / wk_n, wk = warp % wk_n;
-  const uint32_t ring = smem_u32(smem) + uint32_t(warp) * D * MT * S::kStage;
-  const uint64_t begin = range_start(p, blockIdx.x, gridDim.x), end = range_start(p, blockIdx.x + 1, gridDim.x);
-  XRows<NT> x;
-  x.K = p.kx;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int b = (lane >> 2) + 8 * nt;
-    x.p[nt] = b < p.B ? p.x + uint64_t(b) * p.ldx : nullptr;
-  }
-  const uint64_t tile_bytes = uint64_t(p.steps) * q4_block_bytes(NG);
-  // A row group's part of [begin, end), and this warp's k-steps of it.
-  struct Seg {
-    uint32_t rg, k0, k1, w0, w1;
-  };
-  auto seg_at = [&](uint64_t at) {
-    Seg s;
-    s.rg = uint32_t(at / p.steps);
-    s.k0 = uint32_t(at % p.steps);
-    const uint64_t left = end - at;
-    s.k1 = uint32_t(left < p.steps - s.k0 ? s.k0 + left : p.steps);
-    const uint32_t len = s.k1 - s.k0;
-    s.w0 = s.k0 + len * wk / wk_n;
-    s.w1 = s.k0 + len * (wk + 1) / wk_n;
-    if ((s.rg * p.wm + wm) * MT >= p.tiles) s.w1 = s.w0;  // no tile here
+  const uint64_t begin = p.cuts.begin(), end = p.cuts.end();
+  Ring<S, kDepth> ring(smem_u32(smem) + uint32_t(warp) * kDepth * S::kStage,
+                       smem_u32(part + kWarps * 2 * TILES * 128) + uint32_t(warp) * kDepth * 8, p.err, lane);
+  auto warp_seg = [&](uint64_t at) {
+    Seg s = seg_at(p.cuts, at, end, wk, wk_n);
+    if (s.unit * p.wm + wm >= p.tiles) s.w1 = s.w0;  // no tile here
     return s;
   };
-  auto tile_of = [&](const Seg& s, int m) {  // past the last tile: the last one again, its sums unused
-    const uint32_t i = (s.rg * p.wm + wm) * MT + m;
-    return typename S::Tile{p.w + uint64_t(i < p.tiles ? i : p.tiles - 1) * tile_bytes};
-  };
-  // The copy cursor runs D k-steps ahead of the sums, across row groups.
+  // The copy cursor runs kDepth k-steps ahead of the sums, across units.
   uint64_t iat = begin;
-  Seg is{};
-  typename S::Tile it[MT];
-  uint32_t ik = 0, islot = 0;
+  uint32_t ileft = 0;
+  typename S::Cursor it{};
   auto enter = [&]() {
     while (iat < end) {
-      is = seg_at(iat);
-      ik = is.w0;
-      if (is.w0 < is.w1) break;
-      iat += is.k1 - is.k0;
+      const Seg s = warp_seg(iat);
+      iat += s.k1 - s.k0;
+      if (s.w0 == s.w1) continue;
+      ileft = s.w1 - s.w0;
+      it = S::at(p.w, p.cuts.steps, s.unit * p.wm + wm, s.w0);
+      return;
     }
-    if (iat < end)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) it[m] = tile_of(is, m);
   };
-  auto issue = [&]() {
-    if (iat < end) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m) S::issue(it[m], ik, ring + (islot * MT + m) * S::kStage, lane);
-      if (++ik == is.w1) {
-        iat += is.k1 - is.k0;
-        enter();
-      }
+  auto issue = [&](uint32_t slot) {
+    if (ileft) {
+      ring.refill(slot, it, lane);
+      if (--ileft == 0) enter();
     }
-    cp_async_commit();
-    islot = islot + 1 == D ? 0 : islot + 1;
   };
   enter();
 #pragma unroll
-  for (int i = 0; i < D; ++i) issue();
-  uint32_t slot = 0;
-  int par = 0;
-  const uint32_t rows_g = uint32_t(p.wm) * MT * kTileRows;
+  for (int i = 0; i < kDepth; ++i) issue(i);
+  const uint64_t row_bytes = uint64_t(2) * p.cuts.steps * kRecord;
+  const XRows<TILES> x = x_rows<TILES>(uint32_t(p.B), lane, [&](uint32_t b) { return p.xq + b * row_bytes; },
+                                         [&](uint32_t b) { return p.factors + b; });
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the records are there
+  const uint32_t rows_g = uint32_t(p.wm) * kTileRows, outs = rows_g * p.B;
   for (uint64_t at = begin; at < end;) {
-    const Seg s = seg_at(at);
-    float acc[MT][NT][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) acc[m][nt][0] = acc[m][nt][1] = acc[m][nt][2] = acc[m][nt][3] = 0.f;
-    for (uint32_t k = s.w0; k < s.w1; ++k) {
-      cp_async_wait<D - 1>();
-      S::template step<MT, NT, true>(ring + slot * MT * S::kStage, k, lane, x, acc);
-      issue();
-      slot = slot + 1 == D ? 0 : slot + 1;
+    const Seg s = warp_seg(at);
+    float acc[2][TILES][4];
+    zero<TILES>(acc);
+    if (s.w0 < s.w1) {
+      Product<S, TILES, 1> prod;
+      prod.begin(x, s.w0);
+      for (uint32_t k = s.w0; k < s.w1; ++k) prod.step(ring, k, k + 1 < s.w1 ? k + 1 : k, lane, magic, x, acc, issue);
     }
-    // sum the warps of a tile in order; parts alternate by parity, so one
-    // barrier per row group suffices
-    float* pp = part + par * (kWarps * MT * NT * 128);
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        *reinterpret_cast<float4*>(pp + ((warp * MT + m) * NT + nt) * 128 + lane * 4) =
-            make_float4(acc[m][nt][0], acc[m][nt][1], acc[m][nt][2], acc[m][nt][3]);
+    __syncthreads();  // the previous unit's parts are read
+    put_sums<TILES>(part + warp * 2 * TILES * 128, lane, acc);
     __syncthreads();
-    par ^= 1;
-    const bool whole = s.k0 == 0 && s.k1 == p.steps;
-    const uint64_t row0 = uint64_t(s.rg) * rows_g;
-    float* ws = whole ? nullptr : p.part + (2 * uint64_t(blockIdx.x) + (at != begin)) * p.B * rows_g;
-    for (uint32_t o = threadIdx.x; o < rows_g * p.B; o += kThreads) {
+    const uint64_t row0 = uint64_t(s.unit) * rows_g;
+    // output o: row o % rows_g of the unit, batch row o / rows_g; the warps in order
+    auto value = [&](uint32_t o) {
       const uint32_t r = o % rows_g, b = o / rows_g;
-      const uint32_t m = (r / kTileRows) % MT, wmi = r / (kTileRows * MT), j = r % kTileRows;
-      const float* src = pp + ((wmi * wk_n * MT + m) * NT + (b >> 3)) * 128 + ((j & 7) * 4 + ((b & 7) >> 1)) * 4 +
-                         (j >> 3) * 2 + (b & 1);
-      float v = 0.f;
-      for (int w = 0; w < wk_n; ++w) v += src[w * MT * NT * 128];
-      if (!whole)
-        ws[o] = v;
-      else if (row0 + r < p.N)
-        p.y[uint64_t(b) * p.N + row0 + r] = v;
-    }
-    if (!whole) {
-      // CTAs with a share of this row group: first .. last
-      const uint64_t g0 = uint64_t(s.rg) * p.steps, g1 = g0 + p.steps;
-      uint32_t first = blockIdx.x, last = blockIdx.x;
-      while (first > 0 && range_start(p, first, gridDim.x) > g0) --first;
-      while (last + 1 < gridDim.x && range_start(p, last + 1, gridDim.x) < g1) ++last;
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        s_last = atomicAdd(p.counters + s.rg, 1u) == last - first;
-        __threadfence();
-      }
-      __syncthreads();
-      if (s_last) {
-        for (uint32_t o = threadIdx.x; o < rows_g * p.B; o += kThreads) {
-          const uint32_t r = o % rows_g, b = o / rows_g;
-          float v = 0.f;
-          for (uint32_t c = first; c <= last; ++c) {
-            // a CTA's part of this row group is its first unless its range began earlier
-            const uint32_t which = range_start(p, c, gridDim.x) < g0 ? 1u : 0u;
-            v += __ldcg(p.part + (2 * uint64_t(c) + which) * p.B * rows_g + o);
-          }
-          if (row0 + r < p.N) p.y[uint64_t(b) * p.N + row0 + r] = v;
-        }
-        if (threadIdx.x == 0) p.counters[s.rg] = 0u;
-      }
+      return warp_sums<TILES>(part + (r / kTileRows) * wk_n * (2 * TILES * 128), wk_n, 2 * TILES * 128, r % kTileRows, b);
+    };
+    auto store = [&](uint32_t o, float v) {
+      const uint64_t r = row0 + o % rows_g;
+      if (r < p.N) p.y[uint64_t(o / rows_g) * p.N + r] = v;
+    };
+    if (s.k0 == 0 && s.k1 == p.cuts.steps) {
+      for (uint32_t o = threadIdx.x; o < outs; o += kThreads) store(o, value(o));
+    } else {
+      join_parts(p.cuts, s, at == begin, p.part, outs, p.counters, outs, &s_flag, value, store);
     }
     at += s.k1 - s.k0;
   }
-  cp_async_wait<0>();
-}
-
-__global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t* __restrict__ x, uint64_t K, uint64_t Kp,
-                                                       uint32_t B, uint16_t* __restrict__ out) {
-  pad_rows(x, K, Kp, B, out, uint64_t(blockIdx.x) * 256 + threadIdx.x, uint64_t(gridDim.x) * 256);
 }
 
 // ---------------------------------------------------------------------------
@@ -478,13 +436,13 @@ std::mutex g_mu;
 uint32_t* g_work[64] = {nullptr};  // kSlots x kSlotWords counters, then the error word
 std::atomic<uint32_t> g_rr{0};
 
-template <int NG, int MT, int NT>
+template <int NG, int TILES>
 int prepare_gemv(int dev) {
   static std::atomic<int> cache[64];
-  const uint32_t smem = q4_ring<NG, MT>() + 2 * kWarps * MT * NT * 512;
   int per_sm = cache[dev].load(std::memory_order_acquire);
   if (!per_sm) {
-    auto kern = q4_gemv_kernel<NG, MT, NT>;
+    auto kern = q4_gemv_kernel<NG, TILES>;
+    constexpr uint32_t smem = q4_smem<NG, TILES>();
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess) return -1;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, smem) != cudaSuccess || per_sm < 1)
       return -1;
@@ -493,42 +451,55 @@ int prepare_gemv(int dev) {
   return per_sm;
 }
 
-template <int NG, int MT, int NT>
-int launch_gemv(GemvArgs& p, int dev, cudaStream_t s) {
-  const int per_sm = prepare_gemv<NG, MT, NT>(dev);
+template <int NG, int TILES>
+int launch_gemv(GemvArgs& p, const uint16_t* x, uint64_t K, int dev, cudaStream_t s) {
+  const int per_sm = prepare_gemv<NG, TILES>(dev);
   if (per_sm < 0) return map_cuda(cudaGetLastError());
-  const uint32_t smem = q4_ring<NG, MT>() + 2 * kWarps * MT * NT * 512;
-  const uint32_t rows_g = uint32_t(p.wm) * MT * kTileRows;
-  p.groups = uint32_t(cdiv(p.tiles, uint64_t(p.wm) * MT));
-  uint32_t grid = uint32_t(per_sm * sm_count(dev));
-  if (p.split && p.groups > kSlotWords) p.split = 0;
-  const uint64_t units = p.split ? uint64_t(p.groups) * p.steps : p.groups;
-  if (units < grid) grid = uint32_t(units);
-  if (p.split) {
-    uint32_t* err = nullptr;
-    const int st = work_slot(dev, &p.counters, &err);
-    if (st != WCOMP_OK) return st;
-    const cudaError_t e =
-        pool_alloc(reinterpret_cast<void**>(&p.part), uint64_t(2) * grid * p.B * rows_g * sizeof(float), s);
-    if (e != cudaSuccess) return map_cuda(e);
+  p.cuts.units = uint32_t(cdiv(p.tiles, uint64_t(p.wm)));
+  const uint32_t ctas = std::min(uint32_t(per_sm * sm_count(dev)), kSlotWords);
+  // Cut units anywhere where that shortens the longest CTA's run by more than
+  // the join costs, about 24 k-steps.  Measured, us with whole units /
+  // cut: 2048 x 6144 6.6 / 10.5, 6144 x 6144 9.7 / 13.3, 16384 x 6144 18.1 /
+  // 21.7, 16384 x 53248 85 / 79, 256 x 40576 (B = 7) 26 / 13.
+  const uint64_t whole = cdiv(p.cuts.units, ctas) * p.cuts.steps, cut = cdiv(uint64_t(p.cuts.units) * p.cuts.steps, ctas);
+  p.cuts.split = whole > cut + 24;
+  p.cuts.spread(ctas);
+  const int st = work_slot(dev, &p.counters, &p.err);
+  if (st != WCOMP_OK) return st;
+  const uint32_t recs = 2 * p.cuts.steps;
+  const uint64_t b_xq = uint64_t(p.B) * recs * kRecord, b_f = (recs * factor_pitch<1>() * 4 + 255) & ~uint64_t(255);
+  const uint64_t b_part = p.cuts.split ? uint64_t(2) * p.cuts.grid * p.B * p.wm * kTileRows * sizeof(float) : 0;
+  uint8_t* ws = nullptr;
+  cudaError_t e = pool_alloc(reinterpret_cast<void**>(&ws), b_xq + b_f + b_part, s);
+  if (e != cudaSuccess) return map_cuda(e);
+  p.xq = ws;
+  float* factors = reinterpret_cast<float*>(ws + b_xq);
+  p.factors = factors;
+  p.part = reinterpret_cast<float*>(ws + b_xq + b_f);
+  q4_x_kernel<<<uint32_t(cdiv(uint64_t(p.B) * recs, 8)), 256, 0, s>>>(x, K, recs, uint32_t(p.B), ws, factors);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.cuts.grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = q4_smem<NG, TILES>();
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, q4_gemv_kernel<NG, TILES>, p);
+    count_launches(2);
   }
-  q4_gemv_kernel<NG, MT, NT><<<grid, kThreads, smem, s>>>(p);
-  count_launches(1);
-  const cudaError_t e = cudaGetLastError();
-  if (p.part) cudaFreeAsync(p.part, s);
+  cudaFreeAsync(ws, s);
   return map_cuda(e);
 }
 
 template <int NG>
-int dispatch_gemv(GemvArgs& p, int dev, cudaStream_t s) {
-  if (p.B <= 8) {
-    p.wm = 1;
-    p.split = 0;
-    return launch_gemv<NG, 1, 1>(p, dev, s);
-  }
-  p.wm = 4;
-  p.split = 1;
-  return launch_gemv<NG, 2, 2>(p, dev, s);
+int dispatch_gemv(GemvArgs& p, const uint16_t* x, uint64_t K, int dev, cudaStream_t s) {
+  p.wm = 1;
+  return p.B <= 8 ? launch_gemv<NG, 1>(p, x, K, dev, s) : launch_gemv<NG, 2>(p, x, K, dev, s);
 }
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -549,7 +520,7 @@ int make_q4(int64_t M, int64_t N, int64_t K, int group, cudaStream_t s, wcomp_q4
   c->N = N;
   c->K = K;
   c->group = group;
-  c->ng = kQ4Cols / group;
+  c->ng = kSub / group;
   c->tiles = cdiv(uint64_t(N), kTileRows);
   c->blocks = cdiv(uint64_t(K), kQ4Cols);
   cudaGetDevice(&c->device);
@@ -563,7 +534,7 @@ int make_q4(int64_t M, int64_t N, int64_t K, int group, cudaStream_t s, wcomp_q4
 }
 
 Blocks blocks_of(const wcomp_q4* c) {
-  return {c->d, uint64_t(c->N), uint64_t(c->K), c->tiles, c->blocks, uint64_t(c->M) * c->tiles * c->blocks};
+  return {c->d, uint64_t(c->N), uint64_t(c->K), c->tiles, c->blocks, uint64_t(c->M) * c->tiles * c->blocks * 4};
 }
 
 uint32_t block_grid(const Blocks& b, int dev) {
@@ -700,29 +671,14 @@ extern "C" int wcomp_q4_gemv(const wcomp_q4* c, const uint16_t* d_x, int B, floa
   GemvArgs p;
   memset(&p, 0, sizeof(p));
   p.w = c->d;
-  p.x = d_x;
-  p.ldx = uint64_t(c->K);
-  p.kx = uint32_t(c->K);
   p.y = d_y;
   p.N = uint64_t(c->N);
-  p.steps = uint32_t(c->blocks);
+  p.cuts.steps = uint32_t(c->blocks);
   p.tiles = uint32_t(c->tiles);
   p.B = B;
-  uint16_t* pad = nullptr;
-  if (c->K % 16 != 0 || !aligned(d_x, 32)) {
-    const uint64_t Kp = c->blocks * kQ4Cols;
-    const cudaError_t e = pool_alloc(reinterpret_cast<void**>(&pad), uint64_t(B) * Kp * 2, s);
-    if (e != cudaSuccess) return map_cuda(e);
-    const uint32_t grid = uint32_t(std::min<uint64_t>(cdiv(uint64_t(B) * Kp, 256), uint64_t(sm_count(c->device)) * 4));
-    pad_rows_kernel<<<grid, 256, 0, s>>>(d_x, uint64_t(c->K), Kp, uint32_t(B), pad);
-    count_launches(1);
-    p.x = pad;
-    p.ldx = Kp;
-    p.kx = uint32_t(Kp);
-  }
-  const int st = c->ng == 1 ? dispatch_gemv<1>(p, c->device, s)
-                 : c->ng == 2 ? dispatch_gemv<2>(p, c->device, s) : dispatch_gemv<4>(p, c->device, s);
-  if (pad) cudaFreeAsync(pad, s);
+  const int st = c->ng == 1   ? dispatch_gemv<1>(p, d_x, uint64_t(c->K), c->device, s)
+                 : c->ng == 2 ? dispatch_gemv<2>(p, d_x, uint64_t(c->K), c->device, s)
+                              : dispatch_gemv<4>(p, d_x, uint64_t(c->K), c->device, s);
   return st;
 }
 

@@ -1,77 +1,98 @@
-// Warp-level weight tiles shared by the 4-bit GEMV and the mixture-of-experts
-// layer: 16 weight rows by a k-step of columns, brought into shared memory by
-// asynchronous copies and multiplied with up to 32 columns of activations on
-// BF16 mma.sync tiles (m16n8k16, fp32 accumulation).
+// Weight tiles shared by the 4-bit GEMV and the mixture-of-experts layer: 32
+// weight rows by a k-step of columns, copied to shared memory by TMA and
+// multiplied with a few columns of activations on warp-level tensor-core MMAs
+// (m16n8k16, fp32 accumulation).
 //
-// At 1..16 rows of x the product does 2..32 operations per weight and streams
-// every weight once, so moving the weights is the bound and the warp-level
-// MMA is ample: a k-step of 16 x 128 4-bit weights (1 KB) costs 8 MMAs per 8
-// columns of x, against about 44 cycles of an SM's share of the HBM rate.
+// At 1..16 rows of x the product streams every weight once and does little
+// with it: moving the weights is the bound, and the multiply has about 44
+// cycles of an SM per KB of weights before it falls behind the HBM.
 //
-// Layout of a 4-bit weight.  Tiles of 16 rows, each a run of blocks of 128
-// columns.  A block is 1024 bytes of codes in the MMA's A-fragment order (lane
-// l's words at 16 l of each 512-byte half), then 16 x NG scales (NG = 128 / G
-// groups per block): word g * NG + j holds the BF16 scales of rows g (low) and
-// g + 8 (high) of group j.  Codes and scales of a block are contiguous, so a
-// tile is read front to back.  Word 2q + i of lane (g = l / 4, t = l % 4) holds
-// the 16 x 4 weights of MMA i of column run q: rows g and g + 8, columns
-// c = q4_col(q, t) + 4 i + {0, 1, 2, 3}.  Nibble p (0..3) is the first and
-// nibble p + 4 the second column of the MMA's A register p: row g columns c,
-// c+1; row g + 8 the same; row g columns c+2, c+3; row g + 8 the same.  So
-// (w >> 4p) & 0x000F000F is a pair of codes, which under the exponent of 128
-// is the BF16 pair 128 + code; subtracting 136 leaves code - 8 exactly.
-//
-// Every lane copies the bytes that it will read itself, so a stage needs no
-// barrier, only the lane's own cp.async group wait.
+// 4-bit weights enter the MMA as exact fp16 integers: a code under the
+// exponent of 1024 is 1024 + c in the low four mantissa bits and 1024 + 16 c in
+// the next four, so a word of eight codes takes one shift and four bit
+// operations, and four fused multiply-adds on the other pipe leave c - 8.
+// (BF16, with 7 mantissa bits, takes three shifts; a BF16 form of the GEMV ran
+// at 0.70 of the HBM rate with its integer pipe 55 % busy.  FP8 operands need
+// no arithmetic at all, but their warp-level MMA is converted to fp16 again:
+// 12 conversions each, slower in all.  Codes as fp16 subnormals need none
+// either, but the MMA aligns them by their exponent field and drops bits.)
+// The activations are BF16 values brought to fp16 by a power of two per 128
+// columns (records, below), which loses nothing.
 #pragma once
 
 #include "wcomp_impl.cuh"
 
 namespace wc {
 
-constexpr int kTileRows = 16;     // weight rows of a tile (the MMA's M side)
-constexpr int kQ4Cols = 128;      // columns of a 4-bit block
-constexpr int kBfCols = 64;       // columns of a BF16 k-step
+constexpr int kTileRows = 32;    // rows of a tile: two MMAs' M side
+constexpr int kQ4Cols = 256;     // columns of a 4-bit block
+constexpr int kSub = 128;        // columns of half a block, and of an x record
+constexpr int kBfCols = 64;      // columns of a BF16 k-step
 
-__host__ __device__ constexpr uint32_t q4_block_bytes(int ng) { return 1024u + 32u * uint32_t(ng); }
-
-// First of the 8 columns of run q (0..3) that lane t of a quad owns.  Groups
-// of 32 columns must not share an MMA, whose sum runs over the quad, so they
-// take 32-column runs; wider groups take 16 columns a lane, which x gives in
-// one 32-byte load.
-template <int NG>
-__host__ __device__ constexpr uint32_t q4_col(uint32_t q, uint32_t t) {
-  return NG == 4 ? 32 * q + 8 * t : 64 * (q >> 1) + 16 * t + 8 * (q & 1);
+// A 4-bit block is 32 rows x 256 columns: 4096 bytes of codes, then the scales
+// (NG = 128 / group groups per half).  Codes: for half s, 16-row half-tile m
+// and quarter q, lane l's 16 bytes at ((2 s + m) 2 + q) 512 + 16 l: the words
+// of the MMAs i = 4 q .. 4 q + 3.  Lane (g = l / 4, t = l % 4) holds in the
+// word of MMA i the columns c .. c + 3, c = 32 (i / 2) + 8 t + 4 (i % 2): bytes
+// 0 and 2 are row g, bytes 1 and 3 row g + 8, columns c, c + 1 (low and high
+// nibble) in the first and c + 2, c + 3 in the second.  Scales: the word at
+// 4096 + 4 (((s NG + j) 2 + m) 8 + g) has the BF16 scales of rows g (low half)
+// and g + 8 of group j.  Sizes are multiples of 128 bytes: copies of 1056-byte
+// blocks ran at 0.62-0.8 of the HBM rate, of aligned ones at 0.94.
+__host__ __device__ constexpr uint32_t q4_block_bytes(int ng) { return 4096u + 128u * uint32_t(ng); }
+__host__ __device__ constexpr uint32_t q4_scale_at(int ng, uint32_t s, uint32_t j, uint32_t m, uint32_t g) {
+  return 4096u + 4u * (((s * uint32_t(ng) + j) * 2u + m) * 8u + g);
 }
 
 // ---------------------------------------------------------------------------
-// Asynchronous copies and loads.
+// Copies, barriers, loads.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+constexpr uint64_t kCopyNs = 1000000000ull;  // how long a wait for copies may take (1 s)
+
+__device__ __forceinline__ uint64_t timer_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
 }
-// The same with only the first `bytes` (0..16) read and the rest zero-filled.
-__device__ __forceinline__ void cp_async16_part(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void bar_init(uint32_t bar) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
 }
-template <int BYTES>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ bool bar_passed(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Wait for a phase; false if kCopyNs went by without it.
+__device__ __forceinline__ bool bar_wait_long(uint32_t bar, uint32_t parity) {
+  const uint64_t deadline = timer_ns() + kCopyNs;
+  while (!bar_passed(bar, parity))
+    if (timer_ns() > deadline) return false;
+  return true;
+}
+// `bytes` (a multiple of 16) contiguous bytes to shared memory, counted on bar.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+// A box of a 2-D tensor map at column c (a multiple of 8 BF16 values), row r.
+__device__ __forceinline__ void box_copy(uint32_t dst, const CUtensorMap* map, uint32_t c, uint32_t r, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(r), "r"(bar)
+      : "memory");
 }
 
 __device__ __forceinline__ uint4 lds_v4(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds_v2(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
 }
 __device__ __forceinline__ uint32_t lds_u32(uint32_t a) {
@@ -82,143 +103,203 @@ __device__ __forceinline__ uint32_t lds_u32(uint32_t a) {
 __device__ __forceinline__ void sts_v4(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-
-// Activations: 16 or 8 consecutive BF16 values.  CONST: the buffer is not
-// written while the kernel runs (read-only path); otherwise a plain load that
-// the compiler keeps after the grid barrier that orders it.
-template <bool CONST>
-__device__ __forceinline__ void ld_x32(const uint16_t* p, uint32_t (&r)[8]) {
-  if constexpr (CONST) {
-    asm("ld.global.nc.L1::evict_last.v8.u32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-        : "l"(p));
-  } else {
-    asm volatile("ld.global.v8.u32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "l"(p)
-                 : "memory");
-  }
+// 32 bytes from a 32-byte boundary.  Not the read-only path: activations may
+// be written by the same kernel, before a grid barrier.
+__device__ __forceinline__ void ldg_v8(const void* p, uint32_t (&r)[8]) {
+  asm volatile("ld.global.v8.u32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(p)
+               : "memory");
 }
-template <bool CONST>
-__device__ __forceinline__ void ld_x16(const uint16_t* p, uint32_t* r) {
-  if constexpr (CONST) {
-    asm("ld.global.nc.L1::evict_last.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "l"(p));
-  } else {
-    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "l"(p)
-                 : "memory");
-  }
+__device__ __forceinline__ float ldg_f(const void* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
 }
-
-// d = a b + d, and d = a b for the first MMA of a chain.
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+// d = a b + d: BF16, 16 x 16 times 16 x 8.
+__device__ __forceinline__ void mma_bf16_k16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                               uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+// The same in fp16, and its first of a chain.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Pair p of a code word as BF16 values code - 8 (exact).
-__device__ __forceinline__ uint32_t q4_pair(uint32_t w, int p) {
-  uint32_t v = ((w >> (4 * p)) & 0x000F000Fu) | 0x43004300u, d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(0x43084308u));
-  return d;
-}
-
-// The activations of one lane: a row pointer per 8 columns of x (null: that
-// column of x does not exist and counts as zero) and the valid columns of a
-// row, a multiple of 16.
-template <int NT>
-struct XRows {
-  const uint16_t* p[NT];
-  uint32_t K;
-};
-
-// Word w (0..3) of run h (0, 1) of half s: columns q4_col(2 s + h, t) ...
-template <int NG, int NT, bool CONST>
-__device__ __forceinline__ void load_x_half(const XRows<NT>& x, uint32_t col0, int s, uint32_t t,
-                                            uint32_t (&xv)[NT][8]) {
+// The MMA's A registers of a code word.  `magic` is the exponent pattern
+// 0x64006400 in a register the compiler cannot see through: with both patterns
+// as immediates each bit operation takes two instructions, on the pipe that
+// bounds the multiply.
+__device__ __forceinline__ uint32_t q4_magic() { return 0x64006400u | threadIdx.y; }  // blocks are one-dimensional
+__device__ __forceinline__ void q4_operand(uint32_t w, uint32_t magic, uint32_t (&a)[4]) {
+  const uint32_t w8 = w >> 8;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(a[0]) : "r"(w), "n"(0x000F000F), "r"(magic));
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(a[1]) : "r"(w8), "n"(0x000F000F), "r"(magic));
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(a[2]) : "r"(w), "n"(0x00F000F0), "r"(magic));
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(a[3]) : "r"(w8), "n"(0x00F000F0), "r"(magic));
+  // (1024 + c) - 1032 and (1024 + 16 c) / 16 - 72
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+  for (int i = 0; i < 2; ++i) asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(a[i]) : "r"(0x64086408u));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) xv[nt][i] = 0u;
-    if (!x.p[nt]) continue;
-    if constexpr (NG == 4) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t c = col0 + q4_col<4>(2 * s + h, t);
-        if (c < x.K) ld_x16<CONST>(x.p[nt] + c, &xv[nt][4 * h]);
-      }
-    } else {
-      const uint32_t c = col0 + q4_col<1>(2 * s, t);
-      if (c < x.K) ld_x32<CONST>(x.p[nt] + c, xv[nt]);
-    }
-  }
+  for (int i = 2; i < 4; ++i) asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(a[i]) : "r"(0x2C002C00u), "r"(0xD480D480u));
 }
 
 // ---------------------------------------------------------------------------
-// Sources.  A source says how a tile's k-step reaches its stage and how a
-// stage is multiplied; Tile is where one 16-row tile starts.
+// Activations for 4-bit weights.  128 values of one row become a record of 256
+// bytes: fp16 values under a power of two that brings the largest magnitude (of
+// all 128, or of each 32) to [2^14, 2^15), and its inverse, the factor, in a
+// separate array.  A BF16 value that is at least 2^-31 of that magnitude keeps
+// all its bits; what is smaller errs by less than 2^-39 of it, far below what
+// fp32 sums of the record keep.  MMA i's operand of columns c .. c + 3 (see the
+// block's layout) is (x[c], x[c + 2]), (x[c + 1], x[c + 3]) at 128 (i / 4) + 32
+// t + 8 (i % 4).  A record with an infinity or a NaN becomes NaN.
+//
+// Factors: NF per record, [record][NF][pitch] with one column per row of
+// activations, so that the rows' factors of a record share a line or two: NF =
+// 1 and pitch 16 for the layer's input, NF = 4 (each 32 values) and pitch 256
+// for the experts' hidden values.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kRecord = 256;
+template <int NF>
+constexpr uint32_t factor_pitch() { return NF == 1 ? 16 : 256; }
+
+// The scaling of values whose largest magnitude has the bits m.
+__device__ __forceinline__ int record_exponent(uint32_t m) {
+  const int k = 14 - (int(m >> 23) - 127);
+  return m >= 0x7F800000u || m == 0u ? 0 : k > 120 ? 120 : k;
+}
+__device__ __forceinline__ float power_of_two(int k) { return __uint_as_float(uint32_t(127 + k) << 23); }
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// One record of BF16 values by one warp: lane l gives columns 4 l .. 4 l + 3.
+__device__ __forceinline__ void record_store(uint8_t* rec, float* factor, const float (&v)[4], int lane) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  m = __reduce_max_sync(0xffffffffu, m);
+  const int k = record_exponent(m);
+  // an infinity or a NaN anywhere: the whole record is NaN
+  const float up = m >= 0x7F800000u ? __uint_as_float(0x7FFFFFFFu) : power_of_two(k);
+  const uint32_t i = (uint32_t(lane) >> 3) * 2 + (uint32_t(lane) & 1), t = (uint32_t(lane) & 7) >> 1;
+  *reinterpret_cast<uint2*>(rec + (i >> 2) * 128 + t * 32 + (i & 3) * 8) =
+      make_uint2(half2_bits(v[0] * up, v[2] * up), half2_bits(v[1] * up, v[3] * up));
+  if (lane == 0) *factor = power_of_two(-k);
+}
+
+// One warp's product with R rows of activations in TILES column tiles of the
+// MMA: row b is column b % 8 of tile b / 8.  Columns of rows that do not exist
+// read one that does; the MMA keeps columns apart and those sums are not used.
+template <int TILES>
+struct XRows {
+  const uint8_t* x[TILES];      // this lane's column, at its 32 bytes of a record
+  const float* f[TILES][2];     // the factors of the rows of this lane's two accumulator columns
+};
+// row(b): first record of row b (of R); column(b): its column of the factors.
+template <int TILES, class ROW, class COLUMN>
+__device__ __forceinline__ XRows<TILES> x_rows(uint32_t R, int lane, ROW row, COLUMN column) {
+  const uint32_t g = uint32_t(lane) >> 2, t = uint32_t(lane) & 3;
+  auto pick = [&](uint32_t b) { return b < R ? b : 0; };
+  XRows<TILES> x;
+#pragma unroll
+  for (int n = 0; n < TILES; ++n) {
+    x.x[n] = row(pick(8 * n + g)) + t * 32;
+    x.f[n][0] = column(pick(8 * n + 2 * t));
+    x.f[n][1] = column(pick(8 * n + 2 * t + 1));
+  }
+  return x;
+}
+
+// 64 columns of every row, from byte `at` of the rows.
+template <int TILES>
+struct XQuarter {
+  uint32_t b[TILES][8];
+  __device__ __forceinline__ void load(const XRows<TILES>& x, uint64_t at) {
+#pragma unroll
+    for (int n = 0; n < TILES; ++n) ldg_v8(x.x[n] + at, b[n]);
+  }
+};
+template <int TILES, int NF>
+struct XFactors {
+  float f[TILES][2][NF];
+  __device__ __forceinline__ void load(const XRows<TILES>& x, uint32_t rec) {
+    const uint64_t at = uint64_t(rec) * (NF * factor_pitch<NF>());
+#pragma unroll
+    for (int n = 0; n < TILES; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) f[n][i][j] = ldg_f(x.f[n][i] + at + j * factor_pitch<NF>());
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Sources: how a tile's k-step reaches its stage, and a stage its product.  A
+// Cursor is a place in one tile.
 // ---------------------------------------------------------------------------
 template <int NG_>
 struct Q4Src {
   static constexpr int NG = NG_;
   static constexpr int kCols = kQ4Cols;
-  static constexpr uint32_t kStage = 1024 + 128 * NG;  // every lane keeps its own copy of its two rows' scales
-  struct Tile {
+  static constexpr uint32_t kStage = q4_block_bytes(NG);
+  static constexpr bool kCopies = true;
+  struct Cursor {
     const uint8_t* p;
   };
-  static __device__ __forceinline__ void issue(const Tile& tile, uint32_t step, uint32_t st, int lane) {
-    const uint8_t* b = tile.p + uint64_t(step) * q4_block_bytes(NG);
-    cp_async16(st + lane * 16, b + lane * 16);
-    cp_async16(st + 512 + lane * 16, b + 512 + lane * 16);
-    cp_async_small<4 * NG>(st + 1024 + lane * 4 * NG, b + 1024 + (lane >> 2) * 4 * NG);
+  // K-step `step` of tile `tile` of a matrix at m whose tiles have `steps`.
+  static __device__ __forceinline__ Cursor at(const uint8_t* m, uint32_t steps, uint32_t tile, uint32_t step) {
+    return {m + (uint64_t(tile) * steps + step) * kStage};
   }
-  // MT tiles' stages at st, st + kStage, ... times the step's activations.
-  // Codes enter the MMA as exact integers; each group's sum is scaled in fp32.
-  template <int MT, int NT, bool CONST>
-  static __device__ __forceinline__ void step(uint32_t st, uint32_t stepi, int lane, const XRows<NT>& x,
-                                              float (&acc)[MT][NT][4]) {
-    const uint32_t t = uint32_t(lane) & 3;
-    float ga[MT][NT][4];
+  // Copy the cursor's block to the stage and move on to the next (one lane).
+  static __device__ __forceinline__ void issue(Cursor& c, uint32_t st, uint32_t bar) {
+    bulk_copy(st, c.p, kStage, bar);
+    c.p += kStage;
+  }
+  // Quarter q of half s of a stage times x.  A run of columns with one scale and
+  // one factor is summed in ga, then scaled in fp32; ga carries an open run.
+  template <int TILES, int NF>
+  static __device__ __forceinline__ void quarter(uint32_t st, int s, int q, int lane, uint32_t magic,
+                                                 const XQuarter<TILES>& x, const XFactors<TILES, NF>& f,
+                                                 float (&ga)[2][TILES][4], float (&acc)[2][TILES][4]) {
+    constexpr int RUNS = NG > NF ? NG : NF;  // runs per half: 8 / RUNS MMAs each
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      uint32_t xv[NT][8];
-      load_x_half<NG, NT, CONST>(x, stepi * kCols, s, t, xv);
+    for (int m = 0; m < 2; ++m) {
+      const uint4 w4 = lds_v4(st + ((2 * s + m) * 2 + q) * 512 + lane * 16);
+      const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const uint32_t sm = st + m * kStage;
-        const uint4 c4 = lds_v4(sm + s * 512 + lane * 16);
-        const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
+      for (int ii = 0; ii < 4; ++ii) {
+        const int i = 4 * q + ii;
+        uint32_t a[4];
+        q4_operand(w[ii], magic, a);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {  // word j: run h = j / 2, MMA j % 2
-          const uint32_t a0 = q4_pair(cw[j], 0), a1 = q4_pair(cw[j], 1), a2 = q4_pair(cw[j], 2), a3 = q4_pair(cw[j], 3);
-          const bool first = NG == 4 ? (j & 1) == 0 : NG == 2 ? j == 0 : j == 0 && s == 0;
-          const bool last = NG == 4 ? (j & 1) == 1 : NG == 2 ? j == 3 : j == 3 && s == 1;
+        for (int n = 0; n < TILES; ++n) {
+          if ((i * RUNS) % 8 == 0)
+            mma_f16_first(ga[m][n], a, x.b[n][2 * ii], x.b[n][2 * ii + 1]);
+          else
+            mma_f16(ga[m][n], a, x.b[n][2 * ii], x.b[n][2 * ii + 1]);
+        }
+        if (((i + 1) * RUNS) % 8 == 0) {
+          const int j = i * NG / 8, jf = i * NF / 8;
+          const uint32_t sc = lds_u32(st + q4_scale_at(NG, s, j, m, 0) + (lane >> 2) * 4);
+          const float sg = bf16_lo(sc), sh = bf16_hi(sc);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (first)
-              mma16816_first(ga[m][nt], a0, a1, a2, a3, xv[nt][2 * j], xv[nt][2 * j + 1]);
-            else
-              mma16816(ga[m][nt], a0, a1, a2, a3, xv[nt][2 * j], xv[nt][2 * j + 1]);
-          }
-          if (last) {
-            const uint32_t sc = lds_u32(sm + 1024 + lane * 4 * NG + 4 * (NG == 4 ? 2 * s + (j >> 1) : NG == 2 ? s : 0));
-            const float sg = bf16_lo(sc), sh = bf16_hi(sc);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              acc[m][nt][0] = fmaf(sg, ga[m][nt][0], acc[m][nt][0]);
-              acc[m][nt][1] = fmaf(sg, ga[m][nt][1], acc[m][nt][1]);
-              acc[m][nt][2] = fmaf(sh, ga[m][nt][2], acc[m][nt][2]);
-              acc[m][nt][3] = fmaf(sh, ga[m][nt][3], acc[m][nt][3]);
-            }
+          for (int n = 0; n < TILES; ++n) {
+            acc[m][n][0] = fmaf(sg * f.f[n][0][jf], ga[m][n][0], acc[m][n][0]);
+            acc[m][n][1] = fmaf(sg * f.f[n][1][jf], ga[m][n][1], acc[m][n][1]);
+            acc[m][n][2] = fmaf(sh * f.f[n][0][jf], ga[m][n][2], acc[m][n][2]);
+            acc[m][n][3] = fmaf(sh * f.f[n][1][jf], ga[m][n][3], acc[m][n][3]);
           }
         }
       }
@@ -226,69 +307,307 @@ struct Q4Src {
   }
 };
 
-// Row-major BF16 weights.  VEC: rows of a multiple of 8 columns from a 16-byte
-// aligned base, copied asynchronously; otherwise element loads.  A stage holds
-// four 512-byte pieces: rows g (pieces 0, 1) and g + 8 (2, 3), columns
-// 16 t + 0..7 (even pieces) and + 8..15 (odd pieces) of the step.
-template <bool VEC>
+// Row-major BF16 weights, viewed as one matrix of rows (all experts').
+// MAP: rows of a multiple of 8 columns from a 16-byte aligned base, copied as
+// boxes of 32 rows x 64 columns through a tensor map (zeros past the last
+// column and row), whose 128-byte swizzle puts 16-byte chunk c of row r at
+// chunk c ^ (r % 8): the lanes' reads meet no bank conflict.  Otherwise
+// element loads by the whole warp, stored in the same places.  A box may reach
+// past its expert's last row into the next one's: MMA rows do not mix, and the
+// sums of those are not used.
+template <bool MAP>
 struct BfSrc {
+  static constexpr int NG = 0;
   static constexpr int kCols = kBfCols;
-  static constexpr uint32_t kStage = 2048;
-  struct Tile {
-    const uint16_t* p;  // first row of the tile
-    uint32_t rows;      // valid rows (0..16)
-    uint32_t K;
+  static constexpr uint32_t kStage = 4096;
+  static constexpr bool kCopies = MAP;
+  struct Cursor {
+    const CUtensorMap* map;  // MAP
+    const uint16_t* w;       // otherwise: the matrix
+    uint64_t rows, row;      // of the matrix; first row of the tile
+    uint32_t K, col;         // columns of the matrix, first column of the step
   };
-  static __device__ __forceinline__ void issue(const Tile& tile, uint32_t step, uint32_t st, int lane) {
+  static __device__ __forceinline__ void issue(Cursor& c, uint32_t st, uint32_t bar) {
+    box_copy(st, c.map, c.col, uint32_t(c.row), bar);
+    c.col += kCols;
+  }
+  static __device__ __forceinline__ void load(Cursor& c, uint32_t st, int lane) {
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {  // 32 rows x 8 chunks, a chunk a lane
+      const uint32_t r = 4 * i + (uint32_t(lane) >> 3), ch = uint32_t(lane) & 7, k = c.col + 8 * ch;
+      uint32_t v[4] = {0u, 0u, 0u, 0u};
+      if (c.row + r < c.rows) {
+        const uint16_t* src = c.w + (c.row + r) * c.K + k;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (k + e < c.K) v[e >> 1] |= uint32_t(__ldg(src + e)) << (16 * (e & 1));
+      }
+      sts_v4(st + r * 128 + ((ch ^ (r & 7)) << 4), make_uint4(v[0], v[1], v[2], v[3]));
+    }
+    c.col += kCols;
+  }
+  // A stage times x: lane (g, t) holds columns 16 t .. 16 t + 15 of rows g,
+  // g + 8, ... and the same columns of its row of x.
+  template <int NT>
+  static __device__ __forceinline__ void multiply(uint32_t st, int lane, const XQuarter<NT>& x,
+                                                  float (&acc)[2][NT][4]) {
     const uint32_t g = uint32_t(lane) >> 2, t = uint32_t(lane) & 3;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t r = g + 8 * (i >> 1), c = step * kCols + 16 * t + 8 * (i & 1);
-      const uint16_t* src = tile.p + uint64_t(r) * tile.K + c;
-      const uint32_t dst = st + i * 512 + lane * 16;
-      if constexpr (VEC) {
-        const bool ok = r < tile.rows && c < tile.K;
-        cp_async16_part(dst, ok ? src : tile.p, ok ? 16u : 0u);
-      } else {
-        uint32_t v[4] = {0u, 0u, 0u, 0u};
-        if (r < tile.rows)
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (c + e < tile.K) v[e >> 1] |= uint32_t(__ldg(src + e)) << (16 * (e & 1));
-        sts_v4(dst, make_uint4(v[0], v[1], v[2], v[3]));
-      }
-    }
-  }
-  template <int MT, int NT, bool CONST>
-  static __device__ __forceinline__ void step(uint32_t st, uint32_t stepi, int lane, const XRows<NT>& x,
-                                              float (&acc)[MT][NT][4]) {
-    const uint32_t t = uint32_t(lane) & 3;
-    uint32_t xv[NT][8];
-    load_x_half<1, NT, CONST>(x, stepi * kCols, 0, t, xv);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const uint32_t sm = st + m * kStage + lane * 16;
+    for (int m = 0; m < 2; ++m) {
+      const uint32_t sm = st + m * 2048 + g * 128;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint4 wg = lds_v4(sm + h * 512), wh = lds_v4(sm + 1024 + h * 512);
+        const uint32_t at = sm + (((2 * t + h) ^ g) << 4);  // rows g and g + 8 have the same swizzle
+        const uint4 wg = lds_v4(at), wh = lds_v4(at + 1024);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma16816(acc[m][nt], wg.x, wh.x, wg.y, wh.y, xv[nt][4 * h], xv[nt][4 * h + 1]);
-          mma16816(acc[m][nt], wg.z, wh.z, wg.w, wh.w, xv[nt][4 * h + 2], xv[nt][4 * h + 3]);
+          mma_bf16_k16(acc[m][nt], wg.x, wh.x, wg.y, wh.y, x.b[nt][4 * h], x.b[nt][4 * h + 1]);
+          mma_bf16_k16(acc[m][nt], wg.z, wh.z, wg.w, wh.w, x.b[nt][4 * h + 2], x.b[nt][4 * h + 3]);
         }
       }
     }
   }
 };
 
-// x[B, K] copied to rows of Kp columns (a multiple of 128), zeros past K: for
-// an x whose rows do not start on 32-byte boundaries.
-__device__ __forceinline__ void pad_rows(const uint16_t* __restrict__ x, uint64_t K, uint64_t Kp, uint32_t B,
-                                         uint16_t* __restrict__ out, uint64_t first, uint64_t stride) {
-  for (uint64_t i = first; i < uint64_t(B) * Kp; i += stride) {
-    const uint64_t b = i / Kp, c = i % Kp;
-    out[i] = c < K ? x[b * K + c] : uint16_t(0);
+// One warp's ring of D stages, and the mbarrier of each.  `left` counts the
+// copies in flight.  A wait that runs out sets the error word and marks the
+// ring dead once what is in flight has had its time to land: no more copies
+// and waits, and the sums go on with whatever the stages hold.
+template <class SRC, int D>
+struct Ring {
+  uint32_t base, bars;
+  uint32_t* err;
+  uint32_t slot = 0, parity = 0, left = 0;
+  bool dead = false;
+
+  __device__ __forceinline__ Ring(uint32_t base_, uint32_t bars_, uint32_t* err_, int lane)
+      : base(base_), bars(bars_), err(err_) {
+    if (lane < D) bar_init(bars + 8 * lane);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
   }
+  __device__ __forceinline__ uint32_t stage() const { return base + slot * SRC::kStage; }
+  // Refill slot `at` with the cursor's next k-step.
+  __device__ __forceinline__ void refill(uint32_t at, typename SRC::Cursor& c, int lane) {
+    const uint32_t st = base + at * SRC::kStage;
+    if constexpr (SRC::kCopies) {
+      if (dead) return;
+      if (lane == 0) {
+        bar_expect(bars + 8 * at, SRC::kStage);
+        SRC::issue(c, st, bars + 8 * at);
+      }
+      ++left;
+    } else {
+      SRC::load(c, st, lane);
+    }
+  }
+  __device__ __forceinline__ void wait(int lane) {
+    if constexpr (SRC::kCopies) {
+      if (!dead) {
+        bool ok = bar_passed(bars + 8 * slot, parity);
+        if (!__all_sync(0xffffffffu, ok)) {
+          if (!ok) ok = bar_wait_long(bars + 8 * slot, parity);
+          if (!__all_sync(0xffffffffu, ok)) give_up(lane);
+        }
+        --left;
+      }
+    } else {
+      __syncwarp();  // the other lanes' stores
+    }
+  }
+  __device__ __forceinline__ void give_up(int lane) {
+    dead = true;
+    if (lane == 0) atomicOr(err, 1u);
+    uint32_t s = slot, q = parity;
+    for (uint32_t i = 0; i < left; ++i) {
+      bar_wait_long(bars + 8 * s, q);
+      if (++s == D) {
+        s = 0;
+        q ^= 1;
+      }
+    }
+    __syncwarp();
+  }
+  // Let what is in flight land without using it.
+  __device__ __forceinline__ void abandon() {
+    if (SRC::kCopies && !dead) {
+      dead = true;
+      for (; left; --left) {
+        bar_wait_long(bars + 8 * slot, parity);
+        next();
+      }
+    }
+  }
+  __device__ __forceinline__ void next() {
+    if (++slot == D) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+};
+
+// A warp's product of ring stages with its activations, one k-step after the
+// other: begin(k) loads the first activations, step(k, kn) multiplies the
+// ring's current stage, which holds k-step k, adds to acc, refills the slot by
+// issue(slot) with the copy cursor's next k-step and moves on; kn is the
+// k-step of the stage after it.  Activations are loaded 64 columns ahead of
+// their use, factors 128: their latency (L2's, for a first touch) would
+// otherwise stand in every step.
+template <class SRC, int TILES, int NF>
+struct Product {  // 4-bit
+  XQuarter<TILES> x0, x1;
+  XFactors<TILES, NF> fa, fb;
+  __device__ __forceinline__ void begin(const XRows<TILES>& x, uint32_t k) {
+    fa.load(x, 2 * k);
+    x0.load(x, uint64_t(2 * k) * kRecord);
+  }
+  template <class RING, class ISSUE>
+  __device__ __forceinline__ void step(RING& ring, uint32_t k, uint32_t kn, int lane, uint32_t magic,
+                                       const XRows<TILES>& x, float (&acc)[2][TILES][4], ISSUE& issue) {
+    const uint32_t st = ring.stage();
+    const uint64_t at = uint64_t(2 * k) * kRecord;
+    float ga[2][TILES][4];
+    ring.wait(lane);
+    x1.load(x, at + 128);
+    fb.load(x, 2 * k + 1);
+    SRC::template quarter<TILES, NF>(st, 0, 0, lane, magic, x0, fa, ga, acc);
+    x0.load(x, at + kRecord);
+    SRC::template quarter<TILES, NF>(st, 0, 1, lane, magic, x1, fa, ga, acc);
+    x1.load(x, at + kRecord + 128);
+    fa.load(x, 2 * kn);
+    SRC::template quarter<TILES, NF>(st, 1, 0, lane, magic, x0, fb, ga, acc);
+    x0.load(x, uint64_t(2 * kn) * kRecord);
+    SRC::template quarter<TILES, NF>(st, 1, 1, lane, magic, x1, fb, ga, acc);
+    __syncwarp();  // every lane has read the stage
+    issue(ring.slot);
+    ring.next();
+  }
+};
+template <bool MAP, int TILES, int NF>
+struct Product<BfSrc<MAP>, TILES, NF> {
+  XQuarter<TILES> x0;
+  __device__ __forceinline__ void begin(const XRows<TILES>& x, uint32_t k) { x0.load(x, uint64_t(k) * (2 * kBfCols)); }
+  template <class RING, class ISSUE>
+  __device__ __forceinline__ void step(RING& ring, uint32_t, uint32_t kn, int lane, uint32_t, const XRows<TILES>& x,
+                                       float (&acc)[2][TILES][4], ISSUE& issue) {
+    const uint32_t st = ring.stage();
+    XQuarter<TILES> x1;
+    x1.load(x, uint64_t(kn) * (2 * kBfCols));
+    ring.wait(lane);
+    BfSrc<MAP>::multiply(st, lane, x0, acc);
+    __syncwarp();
+    issue(ring.slot);
+    ring.next();
+    x0 = x1;
+  }
+};
+
+template <int N>
+__device__ __forceinline__ void zero(float (&acc)[2][N][4]) {
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int n = 0; n < N; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
+}
+// A warp's accumulators to its place in shared memory, [half-tile][TILES][lane][4].
+template <int N>
+__device__ __forceinline__ void put_sums(float* part, int lane, const float (&acc)[2][N][4]) {
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      *reinterpret_cast<float4*>(part + (m * N + n) * 128 + lane * 4) =
+          make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
+}
+
+// Row r (0..31) of a tile, column b: the sum over `warps` warps' accumulators,
+// [half-tile][TILES][lane][4] each and `stride` floats apart, in their order.
+template <int TILES>
+__device__ __forceinline__ float warp_sums(const float* part, int warps, uint32_t stride, uint32_t r, uint32_t b) {
+  const uint32_t m = r >> 4, j = r & 15;
+  const float* p = part + (m * TILES + (b >> 3)) * 128 + (j & 7) * 16 + ((b & 7) >> 1) * 4 + (j >> 3) * 2 + (b & 1);
+  float v = 0.f;
+  for (int w = 0; w < warps; ++w) v += p[w * stride];
+  return v;
+}
+
+// ---------------------------------------------------------------------------
+// Cutting work over the CTAs.  `units` units of `steps` k-steps each stand in
+// one row; CTA c takes k-steps [start(c), start(c + 1)).  With `split` the cuts
+// fall anywhere, so every CTA streams the same bytes; otherwise on whole units.
+// The part of a cut unit that a CTA holds goes to the workspace, and the CTA
+// that arrives last at the unit's counter adds the parts in the order of the
+// CTAs: the result does not depend on which one that is.
+// ---------------------------------------------------------------------------
+struct Cuts {
+  uint32_t units, steps, grid;  // grid: CTAs that have work, at most one per k-step (split) or unit
+  uint32_t split;
+  uint64_t quot;                // pieces (k-steps or units) per CTA; the first rem CTAs take one more
+  uint32_t rem;
+  __host__ __device__ void spread(uint32_t ctas) {
+    const uint64_t work = split ? uint64_t(units) * steps : units;
+    grid = work < ctas ? uint32_t(work) : ctas;
+    quot = work / grid;
+    rem = uint32_t(work - quot * grid);
+  }
+  __device__ __forceinline__ uint64_t start(uint32_t c) const {
+    const uint64_t v = quot * c + (c < rem ? c : rem);
+    return split ? v : v * steps;
+  }
+  // The CTA that has k-step s (split only).
+  __device__ __forceinline__ uint32_t owner(uint64_t s) const {
+    const uint64_t big = (quot + 1) * rem;
+    return s < big ? uint32_t(s / (quot + 1)) : rem + uint32_t((s - big) / quot);
+  }
+  // This CTA's range; empty past the grid.
+  __device__ __forceinline__ uint64_t begin() const { return start(blockIdx.x < grid ? blockIdx.x : grid); }
+  __device__ __forceinline__ uint64_t end() const { return start(blockIdx.x < grid ? blockIdx.x + 1 : grid); }
+};
+
+// A CTA's k-steps [k0, k1) of one unit, and a warp's share [w0, w1) of them.
+struct Seg {
+  uint32_t unit, k0, k1, w0, w1;
+};
+__device__ __forceinline__ Seg seg_at(const Cuts& c, uint64_t at, uint64_t end, uint32_t wk, uint32_t wk_n) {
+  Seg s;
+  s.unit = uint32_t(at / c.steps);
+  s.k0 = uint32_t(at - uint64_t(s.unit) * c.steps);
+  const uint64_t left = end - at;
+  s.k1 = left < c.steps - s.k0 ? s.k0 + uint32_t(left) : c.steps;
+  const uint32_t len = s.k1 - s.k0;
+  s.w0 = s.k0 + uint32_t(uint64_t(len) * wk / wk_n);
+  s.w1 = s.k0 + uint32_t(uint64_t(len) * (wk + 1) / wk_n);
+  return s;
+}
+
+// This CTA's part of a cut unit, n floats given by value(i), joined with the
+// others'; store(i, sum) runs in the last CTA to arrive.  part: 2 n_max floats
+// per CTA; counters: one per CTA, zero before and after.  All threads call it.
+template <class VALUE, class STORE>
+__device__ __forceinline__ void join_parts(const Cuts& c, const Seg& s, bool first_seg, float* part, uint32_t n_max,
+                                           uint32_t* counters, uint32_t n, uint32_t* s_flag, VALUE value, STORE store) {
+  const uint64_t g0 = uint64_t(s.unit) * c.steps, g1 = g0 + c.steps;
+  float* mine = part + (2 * uint64_t(blockIdx.x) + (first_seg ? 0 : 1)) * n_max;
+  for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) __stcg(mine + i, value(i));
+  const uint32_t first = c.owner(g0), last = c.owner(g1 - 1);
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    *s_flag = atomicAdd(counters + first, 1u) == last - first;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!*s_flag) return;
+  // the first CTA's range may have begun before the unit, which it then keeps second
+  const float* head = part + (2 * uint64_t(first) + (c.start(first) < g0 ? 1 : 0)) * n_max;
+  const float* rest = part + 2 * uint64_t(first + 1) * n_max;
+  for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) {
+    float v = __ldcg(head + i);
+#pragma unroll 4
+    for (uint32_t q = 0; q < last - first; ++q) v += __ldcg(rest + 2 * uint64_t(q) * n_max + i);
+    store(i, v);
+  }
+  if (threadIdx.x == 0) counters[first] = 0u;
 }
 
 }  // namespace wc
@@ -305,7 +624,7 @@ struct wcomp_q4 {
 
 namespace wc {
 // Work counters of the 4-bit and expert kernels on the current device, and
-// their error word (defined in q4.cu).  A launch that joins split sums or
+// their error word (defined in q4.cu).  A launch that joins cut units or
 // crosses a grid barrier takes a slot of kSlotWords zeroed counters, round
 // robin, and leaves them zero.
 constexpr uint32_t kSlotWords = 1024;
