@@ -93,11 +93,12 @@ struct Lists {
   uint32_t active;            // experts chosen by at least one token
 };
 
-struct Choice {  // before sorting, pair t * k + j
+struct Choice {  // pairs t * k + j as chosen
   float w[kMaxPairs];
   uint16_t e[kMaxPairs];
-  uint8_t first[kMaxPairs];   // sorted position starts an expert
-  uint16_t es[kMaxPairs];     // experts, sorted
+  alignas(16) uint16_t key[kMaxPairs];  // expert * 16 + token
+  uint16_t sorted[kMaxPairs];           // the experts, sorted
+  uint32_t firsts[kWarps];              // which sorted pairs begin an expert
 };
 
 // Wait until every CTA of the (cooperative, so resident) grid has arrived.
@@ -128,9 +129,9 @@ __device__ bool grid_barrier(uint32_t* counter, uint32_t* err, uint32_t* s_ok) {
   return *s_ok != 0u;
 }
 
-// Order-preserving integer of a score; NaN ranks below everything.
+// Order-preserving integer of a score, above 1; NaN ranks below everything.
 __device__ __forceinline__ uint32_t rank_key(float v) {
-  if (v != v) return 0u;
+  if (v != v) return 1u;
   const uint32_t u = __float_as_uint(v);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
@@ -146,91 +147,158 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Scores and choice of token t by one warp; sc: this warp's E scores in shared
-// memory.  Lane l owns experts l, l + 32, ... (at most 32 of them) and keeps
-// its best one that is not taken, so a round is two warp reductions (the
-// largest key, then the lowest index that has it) and one lane's new search.
-__device__ void choose(const MoeParams& p, uint32_t t, int lane, float* sc, Choice& ch) {
-  float mx = -INFINITY;
+// Scores and choice of token t by one warp.  Lane l owns experts l, l + 32, ...
+// A round of the choice is two warp reductions: the largest key, then the
+// lowest index that has it.  Up to 32 U experts stay in registers, which keeps
+// their loads in flight together and a round free of searches.
+__device__ __forceinline__ float logit_of(const MoeParams& p, uint32_t t, uint32_t e) {
+  const float4 v = __ldcg(reinterpret_cast<const float4*>(p.logits) + t * p.E + e);
+  return (v.x + v.y) + (v.z + v.w);
+}
+__device__ __forceinline__ void put_choice(const MoeParams& p, uint32_t t, uint32_t j, uint32_t e, float score,
+                                           Choice& ch) {
+  const uint32_t i = t * p.k + j;
+  ch.e[i] = uint16_t(e);
+  ch.key[i] = uint16_t(e * kMaxT + t);
+  ch.w[i] = score;
+}
+template <int U>
+__device__ __forceinline__ void choose(const MoeParams& p, uint32_t t, int lane, Choice& ch) {
+  const bool soft = p.scoring == WCOMP_MOE_SOFTMAX;
+  float sc[U];
+  uint32_t key[U];
+  float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const uint32_t e = lane + 32 * i;
+    sc[i] = e < p.E ? logit_of(p, t, e) : -INFINITY;
+    mx = fmaxf(mx, sc[i]);
+  }
+  mx = soft ? warp_max(mx) : 0.f;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const float v = expf(soft ? sc[i] - mx : -sc[i]);
+    sc[i] = v;
+    sum += lane + 32 * i < p.E ? v : 0.f;
+  }
+  sum = warp_sum(sum);
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const uint32_t e = lane + 32 * i;
+    sc[i] = __fdividef(soft ? sc[i] : 1.f, soft ? sum : 1.f + sc[i]);
+    key[i] = e < p.E ? rank_key(p.bias ? sc[i] + p.bias[e] : sc[i]) : 0u;
+  }
+#pragma unroll 1
+  for (uint32_t j = 0; j < p.k; ++j) {
+    uint32_t best = key[0], at = 0;
+#pragma unroll
+    for (int i = 1; i < U; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = i;
+      }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? lane + 32 * at : 0xFFFFFFFFu);
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (e == uint32_t(lane) + 32 * i) {  // E >= k: one is left
+        put_choice(p, t, j, e, sc[i], ch);
+        key[i] = 0u;
+      }
+  }
+}
+// Any E: scores and keys in shared memory (sc: kMaxE scores, then kMaxE keys).
+__device__ __forceinline__ void choose_many(const MoeParams& p, uint32_t t, int lane, float* sc, Choice& ch) {
+  const bool soft = p.scoring == WCOMP_MOE_SOFTMAX;
+  uint32_t* keys = reinterpret_cast<uint32_t*>(sc + kMaxE);
+  float mx = -INFINITY, sum = 0.f;
+#pragma unroll 4
   for (uint32_t e = lane; e < p.E; e += 32) {
-    const float4 l4 = __ldcg(reinterpret_cast<const float4*>(p.logits) + uint64_t(t) * p.E + e);
-    const float l = (l4.x + l4.y) + (l4.z + l4.w);
+    const float l = logit_of(p, t, e);
     sc[e] = l;
     mx = fmaxf(mx, l);
   }
-  if (p.scoring == WCOMP_MOE_SOFTMAX) {
-    mx = warp_max(mx);
-    float sum = 0.f;
-    for (uint32_t e = lane; e < p.E; e += 32) {
-      const float v = expf(sc[e] - mx);
-      sc[e] = v;
-      sum += v;
-    }
-    sum = warp_sum(sum);
-    for (uint32_t e = lane; e < p.E; e += 32) sc[e] = sc[e] / sum;
-  } else {
-    for (uint32_t e = lane; e < p.E; e += 32) sc[e] = 1.f / (1.f + expf(-sc[e]));
+  mx = soft ? warp_max(mx) : 0.f;
+  for (uint32_t e = lane; e < p.E; e += 32) {
+    const float v = expf(soft ? sc[e] - mx : -sc[e]);
+    sc[e] = v;
+    sum += v;
   }
-  uint32_t taken = 0u, key = 0u, at = 0xFFFFFFFFu;  // bit i of taken: this lane's i-th expert is chosen
-  auto search = [&]() {
-    key = 0u;
-    at = 0xFFFFFFFFu;
-    uint32_t i = 0;
-    for (uint32_t e = lane; e < p.E; e += 32, ++i) {
-      if ((taken >> i) & 1u) continue;
-      const uint32_t kk = rank_key(p.bias ? sc[e] + p.bias[e] : sc[e]);
-      if (at == 0xFFFFFFFFu || kk > key) {
-        key = kk;
-        at = e;
-      }
+  sum = warp_sum(sum);
+  uint32_t key = 0u, at = 0xFFFFFFFFu;
+  for (uint32_t e = lane; e < p.E; e += 32) {
+    const float v = __fdividef(soft ? sc[e] : 1.f, soft ? sum : 1.f + sc[e]);
+    const uint32_t kk = rank_key(p.bias ? v + p.bias[e] : v);
+    sc[e] = v;
+    keys[e] = kk;
+    if (kk > key) {
+      key = kk;
+      at = e;
     }
-  };
-  search();
-  float psum = 0.f;
+  }
   for (uint32_t j = 0; j < p.k; ++j) {
     const uint32_t top = __reduce_max_sync(0xffffffffu, key);
-    const uint32_t e = __reduce_min_sync(0xffffffffu, key == top ? at : 0xFFFFFFFFu);  // E >= k: one is left
+    const uint32_t e = __reduce_min_sync(0xffffffffu, key == top ? at : 0xFFFFFFFFu);
     if (e == at) {
-      taken |= 1u << (e >> 5);
-      const float v = sc[e];
-      ch.e[t * p.k + j] = uint16_t(e);
-      ch.w[t * p.k + j] = v;
-      search();
+      put_choice(p, t, j, e, sc[e], ch);
+      keys[e] = key = 0u;
+      at = 0xFFFFFFFFu;
+      for (uint32_t q = lane; q < p.E; q += 32)
+        if (keys[q] > key) {
+          key = keys[q];
+          at = q;
+        }
     }
   }
+}
+// The chosen scores of token t become weights.
+__device__ __forceinline__ void weigh(const MoeParams& p, uint32_t t, int lane, Choice& ch) {
   __syncwarp();
-  for (uint32_t j = 0; j < p.k; ++j) psum += ch.w[t * p.k + j];
-  __syncwarp();
-  const float mul = p.renorm ? p.factor / (psum != psum ? psum : fmaxf(psum, 1e-20f)) : p.factor;
-  if (uint32_t(lane) < p.k) ch.w[t * p.k + lane] *= mul;
+  float v = uint32_t(lane) < p.k ? ch.w[t * p.k + lane] : 0.f, sum = 0.f;
+  for (uint32_t j = 0; j < p.k; ++j) sum += __shfl_sync(0xffffffffu, v, j);  // in the order of the choice
+  v *= p.renorm ? p.factor / (sum != sum ? sum : fmaxf(sum, 1e-20f)) : p.factor;
+  if (uint32_t(lane) < p.k) ch.w[t * p.k + lane] = v;
 }
 
 // Pairs sorted by (expert, token), and where each chosen expert's pairs begin.
-__device__ void build_lists(const MoeParams& p, Choice& ch, Lists& L) {
+__device__ __forceinline__ void build_lists(const MoeParams& p, Choice& ch, Lists& L) {
   const uint32_t n = p.T * p.k, i = threadIdx.x;
-  uint32_t rank = 0;
+  if (i >= n) ch.key[i] = 0xFFFFu;  // past every key
+  __syncthreads();
   if (i < n) {
-    const uint32_t key = uint32_t(ch.e[i]) * kMaxT + i / p.k;
-    for (uint32_t j = 0; j < n; ++j) rank += uint32_t(ch.e[j]) * kMaxT + j / p.k < key;
+    const uint32_t key = ch.key[i];
+    uint32_t rank = 0;
+#pragma unroll 1
+    for (uint32_t j = 0; j < n; j += 8) {
+      const uint4 v = *reinterpret_cast<const uint4*>(&ch.key[j]);
+      const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) rank += uint32_t((q[c] & 0xFFFFu) < key) + uint32_t((q[c] >> 16) < key);
+    }
     L.w[rank] = ch.w[i];
-    L.tok[rank] = uint8_t(i / p.k);
-    ch.es[rank] = ch.e[i];
+    L.tok[rank] = uint8_t(key % kMaxT);
+    ch.sorted[rank] = uint16_t(key / kMaxT);
   }
   __syncthreads();
-  const bool first = i < n && (i == 0 || ch.es[i] != ch.es[i - 1]);
-  if (i < n) ch.first[i] = first;
+  const bool first = i < n && (i == 0 || ch.sorted[i] != ch.sorted[i - 1]);
+  const uint32_t mask = __ballot_sync(0xffffffffu, first);
+  if (i % 32 == 0) ch.firsts[i / 32] = mask;
   __syncthreads();
+  uint32_t before = 0, all = 0;
+#pragma unroll
+  for (uint32_t w = 0; w < kWarps; ++w) {
+    const uint32_t c = __popc(ch.firsts[w]);
+    if (w < i / 32) before += c;
+    all += c;
+  }
   if (first) {
-    uint32_t a = 0;
-    for (uint32_t j = 0; j < i; ++j) a += ch.first[j];
-    L.expert[a] = ch.es[i];
+    const uint32_t a = before + __popc(mask & ((1u << (i % 32)) - 1u));
+    L.expert[a] = ch.sorted[i];
     L.start[a] = uint16_t(i);
   }
-  if (i == n - 1) {
-    uint32_t a = 0;
-    for (uint32_t j = 0; j < n; ++j) a += ch.first[j];
-    L.active = a;
-    L.start[a] = uint16_t(n);
+  if (i == 0) {
+    L.active = all;
+    L.start[all] = uint16_t(n);
   }
   __syncthreads();
 }
@@ -257,16 +325,18 @@ __device__ __forceinline__ typename SRC::Cursor expert_at(const MoeParams& p, co
   }
 }
 
-// Stages of a warp's ring.  What shared memory the rings leave is L1 for the
-// activations.
+// Stages of a warp's ring.  4-bit: two, so that two CTAs fit an SM and L1 keeps
+// the activations (three leave one CTA: 52 -> 73 us for one token, 8 of 128
+// experts of 6144 x 2048).  BF16: three in one CTA per SM (two CTAs of two
+// stages: 112 -> 121 us).
 template <class SRC>
 constexpr int moe_depth() { return SRC::NG > 0 ? 2 : 3; }
 template <class SRC>
 constexpr uint32_t moe_ring() { return moe_depth<SRC>() * SRC::kStage; }  // one warp's
 // Shared memory after the rings: A's parts (8 warps x 16 x 16), B's sums (8
-// warps x 32 rows x 16 pairs, gate and up in turn), C's accumulators (8 warps x
-// 16 tokens x 32 rows).  The choice's scores (8 warps x 1024) use the rings,
-// idle then.
+// warps x 32 rows x 8 pairs of gate and up, or 16 of one of them), C's
+// accumulators (8 warps x 16 tokens x 32 rows).  The choice's scores and keys
+// (8 warps x 2 x 1024) use the rings, idle then.
 constexpr uint32_t kShare = 16384;
 template <class SRC>
 constexpr uint32_t moe_smem() { return kWarps * moe_ring<SRC>() + kShare + kWarps * moe_depth<SRC>() * 8 + 1024; }
@@ -316,24 +386,22 @@ __device__ __forceinline__ void gate_up(const MoeParams& p, const Lists& L, uint
       prod.step(ring, k, k + 1 < w1 ? k + 1 : k, lane, magic, x, au, issue);
     }
   }
-  float* mine = share + warp * (2 * TILES * 128);
+  // up to 8 pairs: gate and up together; else one after the other
+  constexpr uint32_t kEach = 2 * TILES * 128, kRounds = TILES, kStride = kEach * (3 - TILES);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (uint32_t i = 0; i < kRounds; ++i) {
     __syncthreads();  // what was in `share` is read
-    if (i == 0)
-      put_sums<TILES>(mine, lane, ag);
-    else
-      put_sums<TILES>(mine, lane, au);
+    float* mine = share + warp * kStride;
+    if (i == 0) put_sums<TILES>(mine, lane, ag);
+    if (i + 1 == kRounds) put_sums<TILES>(mine + (kRounds == 1 ? kEach : 0), lane, au);
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const uint32_t b = warp + 8 * j;
-      float v = 0.f;
-      if (j < TILES && b < n) v = warp_sums<TILES>(share, kWarps, 2 * TILES * 128, lane, b);
-      if (i == 0)
-        g[j] = v;
-      else
-        u[j] = v;
+      const bool ok = j < TILES && b < n;
+      if (i == 0) g[j] = ok ? warp_sums<TILES>(share, kWarps, kStride, lane, b) : 0.f;
+      if (i + 1 == kRounds)
+        u[j] = ok ? warp_sums<TILES>(share + (kRounds == 1 ? kEach : 0), kWarps, kStride, lane, b) : 0.f;
     }
   }
 }
@@ -448,7 +516,7 @@ __device__ __forceinline__ void router_logits(const MoeParams& p, float* share, 
 template <class SRC>
 __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant__ MoeParams p,
                                                           const __grid_constant__ MoeMaps maps) {
-  static_assert(moe_ring<SRC>() >= kMaxE * 4, "the rings hold the scores");
+  static_assert(moe_ring<SRC>() >= kMaxE * 8, "the rings hold the scores and keys");
   constexpr int D = moe_depth<SRC>();
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // boxes are swizzled in 1024 bytes
@@ -495,7 +563,15 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
   bool ok = grid_barrier(p.counters, p.err, &s_flag);
   if (ok) {
     // ---- the choice, alike in every CTA
-    for (uint32_t t = warp; t < p.T; t += kWarps) choose(p, t, lane, reinterpret_cast<float*>(smem) + warp * kMaxE, ch);
+    for (uint32_t t = warp; t < p.T; t += kWarps) {
+      if (p.E <= 128)
+        choose<4>(p, t, lane, ch);
+      else if (p.E <= 256)
+        choose<8>(p, t, lane, ch);
+      else
+        choose_many(p, t, lane, reinterpret_cast<float*>(smem + warp * moe_ring<SRC>()), ch);
+      weigh(p, t, lane, ch);
+    }
     __syncthreads();
     if (blockIdx.x == 0 && threadIdx.x < p.T * p.k) {
       if (p.ids) p.ids[threadIdx.x] = ch.e[threadIdx.x];
@@ -510,8 +586,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
     // ---- B: gate and up
     const uint32_t ft_n = uint32_t(cdiv(p.F, kTileRows));
     {
-      Cuts cuts{L.active * ft_n, uint32_t(cdiv(p.H, SRC::kCols)), 0, L.active * ft_n < 8 * gridDim.x, 0, 0};
-      cuts.spread(gridDim.x);
+      Cuts cuts{L.active * ft_n, uint32_t(cdiv(p.H, SRC::kCols)), 0, 0, 0, 0};
+      cuts.choose(gridDim.x, kJoinCopies / 2);
       const uint64_t begin = cuts.begin(), end = cuts.end();
       uint64_t iat = begin;
       uint32_t ileft = 0;  // copies left of the cursor's part, gate and up in turn
@@ -582,8 +658,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
     // chosen experts, one expert after the other.
     {
       const uint32_t steps = uint32_t(cdiv(p.F, SRC::kCols));
-      Cuts cuts{uint32_t(cdiv(p.H, kTileRows)), L.active * steps, 0, 1, 0, 0};
-      cuts.spread(gridDim.x);
+      Cuts cuts{uint32_t(cdiv(p.H, kTileRows)), L.active * steps, 0, 0, 0, 0};
+      cuts.choose(gridDim.x, kJoinCopies);
       const uint64_t begin = cuts.begin(), end = cuts.end();
       uint64_t iat = begin;
       // the cursor's unit and place in it; ileft: k-steps to this expert's or the warp's end
@@ -622,9 +698,9 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
       for (uint32_t i = 0; i < D; ++i) issue((ring.slot + i) % D);
       ok = grid_barrier(p.counters + 1, p.err, &s_flag);
       if (ok) {
-        float* ys = share + warp * (kMaxT * 32);
-        for (uint64_t at = begin; at < end;) {
+          for (uint64_t at = begin; at < end;) {
           const Seg s = seg_at(cuts, at, end, warp, kWarps);
+          float* ys = share + warp * (kMaxT * 32);
           __syncthreads();  // the previous unit's accumulators are read
           for (uint32_t i = lane; i < p.T * 32; i += 32) ys[i] = 0.f;
           __syncwarp();

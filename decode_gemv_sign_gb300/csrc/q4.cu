@@ -78,13 +78,16 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t m) {
 // it where w / s is; the second constant then rounds half to even.  Scales
 // below 2^-100 (reciprocals near overflow, quotients above 7) divide and clamp.
 constexpr float kSnap = 3072.f;        // 1.5 * 2^11: ulp 2^-12
+// Codes come as kBase + code, so that a word of eight is a sum of them times
+// powers of 16, less what the bases add up to: one integer multiply-add a code.
 constexpr float kRound = 12582920.f;   // 1.5 * 2^23 + 8: ulp 1, and the code's offset of 8
+constexpr uint32_t kBase = 0x4B400000u;  // the bits of 1.5 * 2^23
 __device__ __forceinline__ uint32_t code_fast(float w, float rs) {
-  return __float_as_uint(__fadd_rn(__fadd_rn(__fmaf_rn(w, rs, kSnap), -kSnap), kRound)) & 15u;
+  return __float_as_uint(__fadd_rn(__fadd_rn(__fmaf_rn(w, rs, kSnap), -kSnap), kRound));
 }
 __device__ __forceinline__ uint32_t code_slow(float w, float s) {
-  if (!(s > 0.f)) return 8u;  // scale 0 or NaN
-  return uint32_t(int(fminf(fmaxf(rintf(__fdiv_rn(w, s)), -7.f), 7.f)) + 8);
+  if (!(s > 0.f)) return kBase + 8u;  // scale 0 or NaN
+  return kBase + uint32_t(int(fminf(fmaxf(rintf(__fdiv_rn(w, s)), -7.f), 7.f)) + 8);
 }
 
 // 8 columns of row r from column c as BF16 pairs; zeros outside the matrix.
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) q4_encode_kernel(const uint16_t* __r
       }
     uint32_t words[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) words[j] = 0u;
+    for (int j = 0; j < 8; ++j) words[j] = 0u - kBase * 0x11111111u;
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -165,13 +168,13 @@ __global__ void __launch_bounds__(kThreads) q4_encode_kernel(const uint16_t* __r
           const float rs = __frcp_rn(s);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            words[2 * q + (e >> 1)] |= (code_fast(bf16_lo(v[r][q][e]), rs) << (16 * (e & 1) + 8 * r)) |
-                                       (code_fast(bf16_hi(v[r][q][e]), rs) << (16 * (e & 1) + 8 * r + 4));
+            words[2 * q + (e >> 1)] += code_fast(bf16_lo(v[r][q][e]), rs) * (1u << (16 * (e & 1) + 8 * r)) +
+                                       code_fast(bf16_hi(v[r][q][e]), rs) * (16u << (16 * (e & 1) + 8 * r));
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            words[2 * q + (e >> 1)] |= (code_slow(bf16_lo(v[r][q][e]), s) << (16 * (e & 1) + 8 * r)) |
-                                       (code_slow(bf16_hi(v[r][q][e]), s) << (16 * (e & 1) + 8 * r + 4));
+            words[2 * q + (e >> 1)] += code_slow(bf16_lo(v[r][q][e]), s) * (1u << (16 * (e & 1) + 8 * r)) +
+                                       code_slow(bf16_hi(v[r][q][e]), s) * (16u << (16 * (e & 1) + 8 * r));
         }
       }
     store_quarter<NG>(b.d + a.block * q4_block_bytes(NG), a, lane, words, sc);
@@ -457,13 +460,10 @@ int launch_gemv(GemvArgs& p, const uint16_t* x, uint64_t K, int dev, cudaStream_
   if (per_sm < 0) return map_cuda(cudaGetLastError());
   p.cuts.units = uint32_t(cdiv(p.tiles, uint64_t(p.wm)));
   const uint32_t ctas = std::min(uint32_t(per_sm * sm_count(dev)), kSlotWords);
-  // Cut units anywhere where that shortens the longest CTA's run by more than
-  // the join costs, about 24 k-steps.  Measured, us with whole units /
-  // cut: 2048 x 6144 6.6 / 10.5, 6144 x 6144 9.7 / 13.3, 16384 x 6144 18.1 /
-  // 21.7, 16384 x 53248 85 / 79, 256 x 40576 (B = 7) 26 / 13.
-  const uint64_t whole = cdiv(p.cuts.units, ctas) * p.cuts.steps, cut = cdiv(uint64_t(p.cuts.units) * p.cuts.steps, ctas);
-  p.cuts.split = whole > cut + 24;
-  p.cuts.spread(ctas);
+  // Measured, us with whole units / cut: 2048 x 6144 6.6 / 10.5, 6144 x 6144
+  // 9.7 / 13.3, 16384 x 6144 18.1 / 21.7, 16384 x 53248 85 / 79, 256 x 40576 (B
+  // = 7) 26 / 13.
+  p.cuts.choose(ctas, kJoinCopies);
   const int st = work_slot(dev, &p.counters, &p.err);
   if (st != WCOMP_OK) return st;
   const uint32_t recs = 2 * p.cuts.steps;

@@ -267,13 +267,18 @@ struct Q4Src {
     bulk_copy(st, c.p, kStage, bar);
     c.p += kStage;
   }
-  // Quarter q of half s of a stage times x.  A run of columns with one scale and
-  // one factor is summed in ga, then scaled in fp32; ga carries an open run.
+  // Quarter q of half s of a stage times x.  Columns with one scale and one
+  // factor are summed in ga by the MMAs, then multiplied in fp32: by the finer of
+  // scale and factor into gb, and gb by the coarser into acc where its range
+  // ends, so that each step costs one fused multiply-add a value.
   template <int TILES, int NF>
   static __device__ __forceinline__ void quarter(uint32_t st, int s, int q, int lane, uint32_t magic,
                                                  const XQuarter<TILES>& x, const XFactors<TILES, NF>& f,
-                                                 float (&ga)[2][TILES][4], float (&acc)[2][TILES][4]) {
-    constexpr int RUNS = NG > NF ? NG : NF;  // runs per half: 8 / RUNS MMAs each
+                                                 float (&ga)[2][TILES][4], float (&gb)[2][TILES][4],
+                                                 float (&acc)[2][TILES][4]) {
+    constexpr int RUNS = NG > NF ? NG : NF;    // runs per half: 8 / RUNS MMAs each
+    constexpr int WIDE = NG > NF ? NF : NG;    // ranges of the coarser per half
+    constexpr bool kTwo = RUNS > WIDE;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const uint4 w4 = lds_v4(st + ((2 * s + m) * 2 + q) * 512 + lane * 16);
@@ -290,16 +295,31 @@ struct Q4Src {
           else
             mma_f16(ga[m][n], a, x.b[n][2 * ii], x.b[n][2 * ii + 1]);
         }
-        if (((i + 1) * RUNS) % 8 == 0) {
-          const int j = i * NG / 8, jf = i * NF / 8;
+        if (((i + 1) * RUNS) % 8 != 0) continue;
+        const bool begins = ((i + 1) * WIDE) % 8 == (8 / RUNS * WIDE) % 8;  // first run of its range
+        const bool ends = ((i + 1) * WIDE) % 8 == 0;
+        const int j = i * NG / 8, jf = i * NF / 8;
+        float sg = 1.f, sh = 1.f;
+        if (NG >= NF || ends) {
           const uint32_t sc = lds_u32(st + q4_scale_at(NG, s, j, m, 0) + (lane >> 2) * 4);
-          const float sg = bf16_lo(sc), sh = bf16_hi(sc);
+          sg = bf16_lo(sc);
+          sh = bf16_hi(sc);
+        }
 #pragma unroll
-          for (int n = 0; n < TILES; ++n) {
-            acc[m][n][0] = fmaf(sg * f.f[n][0][jf], ga[m][n][0], acc[m][n][0]);
-            acc[m][n][1] = fmaf(sg * f.f[n][1][jf], ga[m][n][1], acc[m][n][1]);
-            acc[m][n][2] = fmaf(sh * f.f[n][0][jf], ga[m][n][2], acc[m][n][2]);
-            acc[m][n][3] = fmaf(sh * f.f[n][1][jf], ga[m][n][3], acc[m][n][3]);
+        for (int n = 0; n < TILES; ++n) {
+          float* a4 = acc[m][n];
+          float* b4 = gb[m][n];
+          const float* g4 = ga[m][n];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float sv = v < 2 ? sg : sh, fv = f.f[n][v & 1][jf];
+            if (!kTwo) {
+              a4[v] = fmaf(sv * fv, g4[v], a4[v]);
+            } else {
+              const float fine = NG > NF ? sv : fv, coarse = NG > NF ? fv : sv;
+              b4[v] = begins ? fine * g4[v] : fmaf(fine, g4[v], b4[v]);
+              if (ends) a4[v] = fmaf(coarse, b4[v], a4[v]);
+            }
           }
         }
       }
@@ -466,18 +486,18 @@ struct Product {  // 4-bit
                                        const XRows<TILES>& x, float (&acc)[2][TILES][4], ISSUE& issue) {
     const uint32_t st = ring.stage();
     const uint64_t at = uint64_t(2 * k) * kRecord;
-    float ga[2][TILES][4];
+    float ga[2][TILES][4], gb[2][TILES][4];
     ring.wait(lane);
     x1.load(x, at + 128);
     fb.load(x, 2 * k + 1);
-    SRC::template quarter<TILES, NF>(st, 0, 0, lane, magic, x0, fa, ga, acc);
+    SRC::template quarter<TILES, NF>(st, 0, 0, lane, magic, x0, fa, ga, gb, acc);
     x0.load(x, at + kRecord);
-    SRC::template quarter<TILES, NF>(st, 0, 1, lane, magic, x1, fa, ga, acc);
+    SRC::template quarter<TILES, NF>(st, 0, 1, lane, magic, x1, fa, ga, gb, acc);
     x1.load(x, at + kRecord + 128);
     fa.load(x, 2 * kn);
-    SRC::template quarter<TILES, NF>(st, 1, 0, lane, magic, x0, fb, ga, acc);
+    SRC::template quarter<TILES, NF>(st, 1, 0, lane, magic, x0, fb, ga, gb, acc);
     x0.load(x, uint64_t(2 * kn) * kRecord);
-    SRC::template quarter<TILES, NF>(st, 1, 1, lane, magic, x1, fb, ga, acc);
+    SRC::template quarter<TILES, NF>(st, 1, 1, lane, magic, x1, fb, ga, gb, acc);
     __syncwarp();  // every lane has read the stage
     issue(ring.slot);
     ring.next();
@@ -539,6 +559,7 @@ __device__ __forceinline__ float warp_sums(const float* part, int warps, uint32_
 // that arrives last at the unit's counter adds the parts in the order of the
 // CTAs: the result does not depend on which one that is.
 // ---------------------------------------------------------------------------
+constexpr uint32_t kJoinCopies = 24;  // what a join costs, in 4 KB copies of a CTA
 struct Cuts {
   uint32_t units, steps, grid;  // grid: CTAs that have work, at most one per k-step (split) or unit
   uint32_t split;
@@ -549,6 +570,13 @@ struct Cuts {
     grid = work < ctas ? uint32_t(work) : ctas;
     quot = work / grid;
     rem = uint32_t(work - quot * grid);
+  }
+  // Cut units anywhere where that shortens the longest CTA's run by more than a
+  // join costs, in k-steps.
+  __host__ __device__ void choose(uint32_t ctas, uint32_t join) {
+    const uint64_t whole = cdiv(units, ctas) * steps, cut = cdiv(uint64_t(units) * steps, ctas);
+    split = whole > cut + join;
+    spread(ctas);
   }
   __device__ __forceinline__ uint64_t start(uint32_t c) const {
     const uint64_t v = quot * c + (c < rem ? c : rem);

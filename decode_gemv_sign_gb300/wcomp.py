@@ -152,7 +152,8 @@ def _check(status: int, what: str):
 
 def _stream(stream=None) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the handle alone: making torch's stream object takes longer than a small launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -413,12 +414,12 @@ class Q4:
 
     def info(self) -> dict:
         inf = Q4Info()
-        _check(lib().wcomp_q4_info(P(self.handle), ctypes.byref(inf)), "wcomp_q4_info")
+        _check(lib().wcomp_q4_info(self.handle, ctypes.byref(inf)), "wcomp_q4_info")
         return inf.as_dict()
 
     def free(self, stream=None):
         if self._h:
-            lib().wcomp_q4_free(P(self._h), P(_stream(stream)))
+            lib().wcomp_q4_free(self._h, _stream(stream))
             self._h = 0
 
     def __del__(self):
@@ -435,13 +436,19 @@ def _matrices(shape, what: str) -> tuple:
     return tuple(shape) if len(shape) == 3 else (1, *shape)
 
 
+def _output(t: torch.Tensor, what: str, dtype: torch.dtype, shape: tuple) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or not t.is_contiguous() \
+            or t.shape != shape:
+        raise ValueError(f"{what} must be a contiguous {dtype} CUDA tensor of shape {list(shape)}")
+    return t.data_ptr()
+
+
 def q4_encode(w: torch.Tensor, group: int = 128, stream=None) -> Q4:
     """Quantise BF16 weights W[N, K] or [M, N, K]: 4-bit codes, one BF16 scale per ``group`` columns."""
     w = _bits16(w, "w")
     M, N, K = _matrices(w.shape, "w")
     h = P()
-    _check(lib().wcomp_q4_encode(P(w.data_ptr()), M, N, K, group, P(_stream(stream)), ctypes.byref(h)),
-           "wcomp_q4_encode")
+    _check(lib().wcomp_q4_encode(w.data_ptr(), M, N, K, group, _stream(stream), ctypes.byref(h)), "wcomp_q4_encode")
     return Q4(h.value, w.shape, group)
 
 
@@ -459,13 +466,13 @@ def q4_pack(codes: torch.Tensor, scales: torch.Tensor, K: int, group: int = 128,
         raise ValueError("codes must be contiguous")
     if group not in (32, 64, 128) or K < 1 or kb != (K + 1) // 2:
         raise ValueError("codes must have ceil(K / 2) bytes a row, and group be 32, 64 or 128")
-    if tuple(scales.shape) != (*codes.shape[:-1], -(-K // group)):
+    if scales.shape != (*codes.shape[:-1], -(-K // group)):
         raise ValueError("scales must be [..., N, ceil(K / group)] like codes")
     if scales.device != codes.device:
         raise ValueError("codes and scales must be on one device")
     h = P()
-    _check(lib().wcomp_q4_pack(P(codes.data_ptr()), P(scales.data_ptr()), M, N, K, group, P(_stream(stream)),
-                               ctypes.byref(h)), "wcomp_q4_pack")
+    _check(lib().wcomp_q4_pack(codes.data_ptr(), scales.data_ptr(), M, N, K, group, _stream(stream), ctypes.byref(h)),
+           "wcomp_q4_pack")
     return Q4(h.value, (*codes.shape[:-1], K), group)
 
 
@@ -474,8 +481,7 @@ def q4_unpack(c: Q4, stream=None) -> tuple:
     K = c.shape[-1]
     codes = torch.empty((*c.shape[:-1], (K + 1) // 2), dtype=torch.uint8, device="cuda")
     scales = torch.empty((*c.shape[:-1], -(-K // c.group)), dtype=torch.bfloat16, device="cuda")
-    _check(lib().wcomp_q4_unpack(P(c.handle), P(codes.data_ptr()), P(scales.data_ptr()), P(_stream(stream))),
-           "wcomp_q4_unpack")
+    _check(lib().wcomp_q4_unpack(c.handle, codes.data_ptr(), scales.data_ptr(), _stream(stream)), "wcomp_q4_unpack")
     return codes, scales
 
 
@@ -483,10 +489,11 @@ def q4_decode(c: Q4, out: Optional[torch.Tensor] = None, stream=None) -> torch.T
     """The weights' values rounded once to BF16, as an int16 tensor of their bits (``out`` if given)."""
     if out is None:
         out = torch.empty(c.shape, dtype=torch.int16, device="cuda")
-    out = _bits16(out, "out")
-    if tuple(out.shape) != c.shape:
-        raise ValueError("out has the wrong shape")
-    _check(lib().wcomp_q4_decode(P(c.handle), P(out.data_ptr()), P(_stream(stream))), "wcomp_q4_decode")
+    else:
+        out = _bits16(out, "out")
+        if out.shape != c.shape:
+            raise ValueError("out has the wrong shape")
+    _check(lib().wcomp_q4_decode(c.handle, out.data_ptr(), _stream(stream)), "wcomp_q4_decode")
     return out
 
 
@@ -503,7 +510,7 @@ def q4_gemv(c: Q4, x: torch.Tensor, y: Optional[torch.Tensor] = None, stream=Non
         y = torch.empty((B, N), dtype=torch.float32, device=x.device)
     elif not y.is_cuda or y.dtype != torch.float32 or not y.is_contiguous() or y.numel() != B * N:
         raise ValueError("y must be a contiguous float32 CUDA tensor of B*N elements")
-    _check(lib().wcomp_q4_gemv(P(c.handle), P(x.data_ptr()), B, P(y.data_ptr()), P(_stream(stream))), "wcomp_q4_gemv")
+    _check(lib().wcomp_q4_gemv(c.handle, x.data_ptr(), B, y.data_ptr(), _stream(stream)), "wcomp_q4_gemv")
     return y
 
 
@@ -527,37 +534,27 @@ def moe(x: torch.Tensor, router: torch.Tensor, gate, up, down, top_k: int, *, sc
     (T, H), E = x.shape, router.shape[0]
     if scoring not in SCORING:
         raise ValueError("scoring must be 'softmax' or 'sigmoid'")
-    a = MoeArgs()
     q4 = isinstance(gate, Q4)
+    if isinstance(up, Q4) != q4 or isinstance(down, Q4) != q4:
+        raise TypeError("gate, up and down must be all BF16 tensors or all Q4 weights")
     F = gate.shape[1] if len(gate.shape) == 3 else 0
-    for name, w, shape in (("gate", gate, (E, F, H)), ("up", up, (E, F, H)), ("down", down, (E, H, F))):
-        if isinstance(w, Q4) != q4:
-            raise TypeError("gate, up and down must be all BF16 tensors or all Q4 weights")
-        if tuple(w.shape) != shape:
-            raise ValueError(f"{name} must be {list(shape)}, got {list(w.shape)}")
-        if q4:
-            setattr(a, "q4_" + name, w.handle)
-        else:
-            setattr(a, "d_" + name, _bits16(w, name).data_ptr())
-
-    def out(t, what, dtype, shape):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or not t.is_contiguous()                 or tuple(t.shape) != shape:
-            raise ValueError(f"{what} must be a contiguous {dtype} CUDA tensor of shape {list(shape)}")
-        return t.data_ptr()
-
+    if gate.shape != (E, F, H) or up.shape != (E, F, H) or down.shape != (E, H, F):
+        raise ValueError(f"gate and up must be [{E}, F, {H}] and down [{E}, {H}, F], got {list(gate.shape)}, "
+                         f"{list(up.shape)}, {list(down.shape)}")
+    if q4:
+        ws = (None, None, None, gate.handle, up.handle, down.handle)
+    else:
+        ws = (_bits16(gate, "gate").data_ptr(), _bits16(up, "up").data_ptr(), _bits16(down, "down").data_ptr(),
+              None, None, None)
     if y is None:
         y = torch.empty_like(x)
-    a.d_x, a.d_router, a.d_y = x.data_ptr(), router.data_ptr(), out(y, "y", y.dtype, (T, H))
-    _bits16(y, "y")
-    if bias is not None:
-        a.d_bias = out(bias, "bias", torch.float32, (E,))
-    if ids is not None:
-        a.d_ids = out(ids, "ids", torch.int32, (T, top_k))
-    if weights is not None:
-        a.d_weights = out(weights, "weights", torch.float32, (T, top_k))
-    a.H, a.F, a.T, a.E, a.top_k = H, F, T, E, top_k
-    a.scoring, a.renormalize, a.factor = SCORING[scoring], int(renormalize), factor
-    _check(lib().wcomp_moe(ctypes.byref(a), P(_stream(stream))), "wcomp_moe")
+    else:
+        _output(_bits16(y, "y"), "y", y.dtype, (T, H))
+    a = MoeArgs(x.data_ptr(), router.data_ptr(), None if bias is None else _output(bias, "bias", torch.float32, (E,)),
+                *ws, y.data_ptr(), None if ids is None else _output(ids, "ids", torch.int32, (T, top_k)),
+                None if weights is None else _output(weights, "weights", torch.float32, (T, top_k)),
+                H, F, T, E, top_k, SCORING[scoring], renormalize, factor)
+    _check(lib().wcomp_moe(ctypes.byref(a), _stream(stream)), "wcomp_moe")
     return y
 
 
