@@ -26,54 +26,68 @@ constexpr int kWarps = kThreads / 32;
 // in the operands' order with no exchange, and a group's largest magnitude
 // needs two shuffles in a quad.
 // ---------------------------------------------------------------------------
+// A CTA takes a run of 8 x `run` quarter blocks of one tile, so that what needs
+// a division is found once for all of them.
 struct Blocks {
   uint8_t* d;
-  uint64_t N, K, tiles, blocks, total;  // total = M * tiles * blocks * 4
+  uint64_t N, K, tiles, blocks;
+  uint64_t runs;         // M * tiles * runs_per_tile
+  uint32_t runs_per_tile, run;
 };
 
-// Quarter block i of a batch of matrices: its block, place in it, first row and
-// column in its matrix, and that row's index over all matrices.
+// A quarter block: its block, place in it, first row and column in its matrix,
+// and that row's index over all matrices.
 struct At {
   uint64_t block, r0, k0, row;
   uint32_t s, m;
 };
-__device__ __forceinline__ At quarter_at(const Blocks& b, uint64_t i) {
-  At a;
-  a.block = i >> 2;
-  a.s = (i >> 1) & 1;
-  a.m = i & 1;
-  const uint64_t tile = a.block / b.blocks, mat = tile / b.tiles;
-  a.r0 = (tile - mat * b.tiles) * kTileRows + 16 * a.m;
-  a.k0 = (a.block - tile * b.blocks) * kQ4Cols + kSub * a.s;
-  a.row = mat * b.N + a.r0;
-  return a;
+// f(quarter) for this warp's quarter blocks of every run of its CTA.
+template <class F>
+__device__ __forceinline__ void each_quarter(const Blocks& b, F f) {
+  for (uint64_t run = blockIdx.x; run < b.runs; run += gridDim.x) {
+    const uint64_t tile = run / b.runs_per_tile, mat = tile / b.tiles;
+    const uint32_t first = uint32_t(run - tile * b.runs_per_tile) * (kWarps * b.run), end = uint32_t(b.blocks) * 4;
+    const uint64_t r0 = (tile - mat * b.tiles) * kTileRows;
+#pragma unroll 1
+    for (uint32_t j = 0; j < b.run; ++j) {
+      const uint32_t q = first + j * kWarps + (threadIdx.x >> 5);
+      if (q >= end) break;
+      At a;
+      a.s = (q >> 1) & 1;
+      a.m = q & 1;
+      a.block = tile * b.blocks + (q >> 2);
+      a.r0 = r0 + 16 * a.m;
+      a.k0 = uint64_t(q >> 2) * kQ4Cols + kSub * a.s;
+      a.row = mat * b.N + a.r0;
+      f(a);
+    }
+  }
 }
 __device__ __forceinline__ uint8_t* codes_at(uint8_t* block, const At& a, int lane) {
   return block + (2 * a.s + a.m) * 1024 + lane * 16;
 }
 
+// Larger magnitudes (NaN if there is one), with a sign that means nothing.
 __device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b & 0x7FFF7FFFu));
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
 // The BF16 scale of a group whose largest magnitude (BF16 bits, NaN if it
-// holds one) is m.  fp32 division and one rounding give the nearest BF16 to
-// m / 7: m has 8 significant bits, so m / 7 is never nearer than 2^-12 to a
-// midpoint of two BF16 values and the division's own rounding cannot cross it.
-// A group with an infinity or a NaN gets the scale NaN.
+// holds one) is m: the nearest BF16 to m / 7.  m has 8 significant bits, so
+// m / 7 is never nearer than 2^-12 of itself to a midpoint of two BF16 values,
+// and the rounding of 1 / 7 and of the product cannot cross it.  A group with
+// an infinity or a NaN gets the scale NaN.
 __device__ __forceinline__ uint32_t scale_of(uint32_t m) {
-  if (m >= 0x7F80u) return 0x7FC0u;
-  const float s = __fdiv_rn(__uint_as_float(m << 16), 7.f);
-  uint32_t u = __float_as_uint(s);
-  u += 0x7FFFu + ((u >> 16) & 1u);
-  return u >> 16;
+  uint16_t s;
+  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(s) : "f"(__fmul_rn(__uint_as_float(m << 16), 1.f / 7.f)));
+  return m >= 0x7F80u ? 0x7FC0u : s;
 }
 
 // Code of one weight.  w / s has a quotient of 8-bit significands: it is
 // either exactly halfway between integers or at least 2^-10 away from it, so
-// w * (1 / s) (2^-23 relative error), rounded to a multiple of 2^-12 by the
+// w * (1 / s) (2^-22 relative error), rounded to a multiple of 2^-12 by the
 // first constant, is on the right side of every halfway point, and exactly on
 // it where w / s is; the second constant then rounds half to even.  Scales
 // below 2^-100 (reciprocals near overflow, quotients above 7) divide and clamp.
@@ -86,23 +100,45 @@ __device__ __forceinline__ uint32_t code_fast(float w, float rs) {
   return __float_as_uint(__fadd_rn(__fadd_rn(__fmaf_rn(w, rs, kSnap), -kSnap), kRound));
 }
 __device__ __forceinline__ uint32_t code_slow(float w, float s) {
-  if (!(s > 0.f)) return kBase + 8u;  // scale 0 or NaN
-  return kBase + uint32_t(int(fminf(fmaxf(rintf(__fdiv_rn(w, s)), -7.f), 7.f)) + 8);
+  if (!(s > 0.f)) return 8u;  // scale 0 or NaN
+  return uint32_t(int(fminf(fmaxf(rintf(__fdiv_rn(w, s)), -7.f), 7.f)) + 8);
 }
 
 // 8 columns of row r from column c as BF16 pairs; zeros outside the matrix.
-template <bool VEC>
 __device__ __forceinline__ void load8(const uint16_t* __restrict__ row, uint64_t c, uint64_t K, bool ok, uint32_t* v) {
-  if constexpr (VEC) {
-    uint4 q = make_uint4(0u, 0u, 0u, 0u);
-    if (ok && c < K) q = ld_stream_v4(row + c);
-    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-  } else {
+  uint4 q = make_uint4(0u, 0u, 0u, 0u);
+  if (ok && c < K) q = ld_stream_v4(row + c);
+  v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+}
+
+// Rows that start anywhere (K % 8 != 0, or an unaligned tensor) pass through
+// shared memory, a warp's 16 x 128 values at kPitch: in memory a warp then
+// touches 64 consecutive bytes at a time instead of 2 bytes in each of 32
+// places (5001 x 7003: quantise 51 -> 25 us, read back 134 -> 18 us).
+constexpr uint32_t kPitch = 136;
+__device__ __forceinline__ void rows_in(const uint16_t* __restrict__ w, const At& a, const Blocks& b, uint16_t* tile,
+                                        int lane) {
+#pragma unroll 4
+  for (uint32_t r = 0; r < 16; ++r) {
+    const bool ok = a.r0 + r < b.N;
+    const uint16_t* row = w + (a.row + r) * b.K + a.k0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = ok && c + 2 * e < K ? uint32_t(__ldg(row + c + 2 * e)) : 0u;
-      const uint32_t hi = ok && c + 2 * e + 1 < K ? uint32_t(__ldg(row + c + 2 * e + 1)) : 0u;
-      v[e] = lo | (hi << 16);
+    for (uint32_t i = 0; i < 4; ++i) {
+      const uint32_t c = lane + 32 * i;
+      tile[r * kPitch + c] = ok && a.k0 + c < b.K ? __ldg(row + c) : uint16_t(0);
+    }
+  }
+}
+__device__ __forceinline__ void rows_out(uint16_t* __restrict__ out, const At& a, const Blocks& b, const uint16_t* tile,
+                                         int lane) {
+#pragma unroll 4
+  for (uint32_t r = 0; r < 16; ++r) {
+    if (a.r0 + r >= b.N) break;
+    uint16_t* row = out + (a.row + r) * b.K + a.k0;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) {
+      const uint32_t c = lane + 32 * i;
+      if (a.k0 + c < b.K) row[c] = tile[r * kPitch + c];
     }
   }
 }
@@ -126,20 +162,64 @@ __device__ __forceinline__ void store_quarter(uint8_t* block, const At& a, int l
   }
 }
 
+__device__ __forceinline__ float reciprocal(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+
+// The codes of a quarter block with a scale that code_fast does not take, from
+// the weights and the stored scales again: rare, and kept apart from the
+// kernel's registers and instruction cache.
+template <int NG>
+__device__ __noinline__ void slow_codes(const uint16_t* __restrict__ w, uint64_t K, uint32_t rows, uint64_t k0,
+                                        uint8_t* block, uint32_t s, uint32_t m, int lane) {
+  const uint32_t g = uint32_t(lane) >> 2, t = uint32_t(lane) & 3;
+#pragma unroll 1
+  for (uint32_t j = 0; j < 8; ++j) {
+    uint32_t word = 0u;
+#pragma unroll 1
+    for (uint32_t n = 0; n < 8; ++n) {  // nibble n: column 2 (n / 4) + n % 2 of four, row half n / 2 % 2
+      const uint32_t r = (n >> 1) & 1;
+      const uint64_t c = k0 + 32 * (j >> 1) + 8 * t + 4 * (j & 1) + 2 * (n >> 2) + (n & 1);
+      uint32_t code = 8u;
+      if (g + 8 * r < rows && c < K) {
+        const uint32_t sc = *reinterpret_cast<const volatile uint32_t*>(block + q4_scale_at(NG, s, (j >> 1) * NG / 4, m, g));
+        code = code_slow(__uint_as_float(uint32_t(w[uint64_t(g + 8 * r) * K + c]) << 16), r ? bf16_hi(sc) : bf16_lo(sc));
+      }
+      word |= code << (4 * n);
+    }
+    *reinterpret_cast<uint32_t*>(block + (2 * s + m) * 1024 + (j >> 2) * 512 + lane * 16 + (j & 3) * 4) = word;
+  }
+}
+
 template <int NG, bool VEC>
 __global__ void __launch_bounds__(kThreads) q4_encode_kernel(const uint16_t* __restrict__ w,
                                                              const __grid_constant__ Blocks b) {
+  __shared__ __align__(16) uint16_t tiles[VEC ? 1 : kWarps * 16 * kPitch];
   const int lane = threadIdx.x & 31;
   const uint32_t g = uint32_t(lane) >> 2, t = uint32_t(lane) & 3;
-  for (uint64_t i = uint64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < b.total; i += uint64_t(gridDim.x) * kWarps) {
-    const At a = quarter_at(b, i);
+  each_quarter(b, [&](const At& a) {
     uint32_t v[2][4][4];  // row half, run, pairs
+    uint16_t* tile = tiles + (VEC ? 0 : (threadIdx.x >> 5) * 16 * kPitch);
+    if (!VEC) {
+      __syncwarp();
+      rows_in(w, a, b, tile, lane);
+      __syncwarp();
+    }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const bool ok = a.r0 + g + 8 * r < b.N;
       const uint16_t* row = w + (a.row + g + 8 * r) * b.K;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) load8<VEC>(row, a.k0 + 32 * q + 8 * t, b.K, ok, v[r][q]);
+      for (int q = 0; q < 4; ++q) {
+        if constexpr (VEC) {
+          load8(row, a.k0 + 32 * q + 8 * t, b.K, ok, v[r][q]);
+        } else {
+          const uint4 u = *reinterpret_cast<const uint4*>(tile + (g + 8 * r) * kPitch + 32 * q + 8 * t);
+          v[r][q][0] = u.x; v[r][q][1] = u.y; v[r][q][2] = u.z; v[r][q][3] = u.w;
+        }
+      }
     }
     uint32_t sc[2][NG];
 #pragma unroll
@@ -153,8 +233,19 @@ __global__ void __launch_bounds__(kThreads) q4_encode_kernel(const uint16_t* __r
           for (int e = 0; e < 4; ++e) m = abs_max2(m, v[r][q][e]);
         m = abs_max2(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = abs_max2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        m = abs_max2(m, m >> 16) & 0xFFFFu;
+        m = abs_max2(m, m >> 16) & 0x7FFFu;
         sc[r][j] = scale_of(m);
+      }
+    float rs[2][NG];
+    bool slow = false;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        const float s = __uint_as_float(sc[r][j] << 16);
+        const bool fast = s >= 0x1p-100f;
+        slow |= !fast && s != 0.f;
+        rs[r][j] = fast ? reciprocal(s) : 0.f;  // scale 0: every code is 8
       }
     uint32_t words[8];
 #pragma unroll
@@ -162,23 +253,19 @@ __global__ void __launch_bounds__(kThreads) q4_encode_kernel(const uint16_t* __r
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float s = __uint_as_float(sc[r][q * NG / 4] << 16);
-        if (s >= 0x1p-100f) {
-          const float rs = __frcp_rn(s);
+      for (int q = 0; q < 4; ++q)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            words[2 * q + (e >> 1)] += code_fast(bf16_lo(v[r][q][e]), rs) * (1u << (16 * (e & 1) + 8 * r)) +
-                                       code_fast(bf16_hi(v[r][q][e]), rs) * (16u << (16 * (e & 1) + 8 * r));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            words[2 * q + (e >> 1)] += code_slow(bf16_lo(v[r][q][e]), s) * (1u << (16 * (e & 1) + 8 * r)) +
-                                       code_slow(bf16_hi(v[r][q][e]), s) * (16u << (16 * (e & 1) + 8 * r));
-        }
-      }
-    store_quarter<NG>(b.d + a.block * q4_block_bytes(NG), a, lane, words, sc);
-  }
+        for (int e = 0; e < 4; ++e)
+          words[2 * q + (e >> 1)] += code_fast(bf16_lo(v[r][q][e]), rs[r][q * NG / 4]) * (1u << (16 * (e & 1) + 8 * r)) +
+                                     code_fast(bf16_hi(v[r][q][e]), rs[r][q * NG / 4]) * (16u << (16 * (e & 1) + 8 * r));
+    uint8_t* block = b.d + a.block * q4_block_bytes(NG);
+    store_quarter<NG>(block, a, lane, words, sc);
+    if (__any_sync(0xffffffffu, slow)) {
+      __syncwarp();
+      slow_codes<NG>(w + a.row * b.K, b.K, uint32_t(a.r0 < b.N ? (b.N - a.r0 < 16 ? b.N - a.r0 : 16) : 0), a.k0, block,
+                     a.s, a.m, lane);
+    }
+  });
 }
 
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
@@ -193,10 +280,11 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
 template <int NG, bool VEC>
 __global__ void __launch_bounds__(kThreads) q4_decode_kernel(const __grid_constant__ Blocks b,
                                                              uint16_t* __restrict__ out) {
+  __shared__ __align__(16) uint16_t tiles[VEC ? 1 : kWarps * 16 * kPitch];
   const int lane = threadIdx.x & 31;
   const uint32_t g = uint32_t(lane) >> 2, t = uint32_t(lane) & 3;
-  for (uint64_t i = uint64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < b.total; i += uint64_t(gridDim.x) * kWarps) {
-    const At a = quarter_at(b, i);
+  uint16_t* tile = tiles + (VEC ? 0 : (threadIdx.x >> 5) * 16 * kPitch);
+  each_quarter(b, [&](const At& a) {
     uint8_t* block = b.d + a.block * q4_block_bytes(NG);
     const uint8_t* in = codes_at(block, a, lane);
     const uint4 c0 = ld_stream_v4(in), c1 = ld_stream_v4(in + 512);
@@ -206,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) q4_decode_kernel(const __grid_consta
     for (int j = 0; j < NG; ++j) sc[j] = ld_stream_u32(block + q4_scale_at(NG, a.s, j, a.m, g));
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      if (a.r0 + g + 8 * r >= b.N) continue;
+      if (VEC && a.r0 + g + 8 * r >= b.N) continue;
       uint16_t* row = out + (a.row + g + 8 * r) * b.K;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -228,13 +316,16 @@ __global__ void __launch_bounds__(kThreads) q4_decode_kernel(const __grid_consta
         if constexpr (VEC) {
           if (c < b.K) *reinterpret_cast<uint4*>(row + c) = make_uint4(v[0], v[1], v[2], v[3]);
         } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (c + e < b.K) row[c + e] = uint16_t(v[e >> 1] >> (16 * (e & 1)));
+          *reinterpret_cast<uint4*>(tile + (g + 8 * r) * kPitch + 32 * q + 8 * t) = make_uint4(v[0], v[1], v[2], v[3]);
         }
       }
     }
-  }
+    if (!VEC) {
+      __syncwarp();
+      rows_out(out, a, b, tile, lane);
+      __syncwarp();
+    }
+  });
 }
 
 // Plain layout to blocks and back.  Plain codes: row r's ceil(K / 2) bytes,
@@ -247,8 +338,7 @@ __global__ void __launch_bounds__(kThreads) q4_pack_kernel(const uint8_t* __rest
   const int lane = threadIdx.x & 31;
   const uint32_t g = uint32_t(lane) >> 2, t = uint32_t(lane) & 3;
   const uint64_t pitch = (b.K + 1) / 2, groups = cdiv(b.K, kSub / NG);
-  for (uint64_t i = uint64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < b.total; i += uint64_t(gridDim.x) * kWarps) {
-    const At a = quarter_at(b, i);
+  each_quarter(b, [&](const At& a) {
     uint32_t words[8], sc[2][NG];
 #pragma unroll
     for (int j = 0; j < 8; ++j) words[j] = 0u;
@@ -277,7 +367,7 @@ __global__ void __launch_bounds__(kThreads) q4_pack_kernel(const uint8_t* __rest
       }
     }
     store_quarter<NG>(b.d + a.block * q4_block_bytes(NG), a, lane, words, sc);
-  }
+  });
 }
 
 template <int NG>
@@ -287,8 +377,7 @@ __global__ void __launch_bounds__(kThreads) q4_unpack_kernel(const __grid_consta
   const int lane = threadIdx.x & 31;
   const uint32_t g = uint32_t(lane) >> 2, t = uint32_t(lane) & 3;
   const uint64_t pitch = (b.K + 1) / 2, groups = cdiv(b.K, kSub / NG);
-  for (uint64_t i = uint64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < b.total; i += uint64_t(gridDim.x) * kWarps) {
-    const At a = quarter_at(b, i);
+  each_quarter(b, [&](const At& a) {
     uint8_t* block = b.d + a.block * q4_block_bytes(NG);
     const uint8_t* in = codes_at(block, a, lane);
     const uint4 c0 = ld_stream_v4(in), c1 = ld_stream_v4(in + 512);
@@ -310,7 +399,7 @@ __global__ void __launch_bounds__(kThreads) q4_unpack_kernel(const __grid_consta
         scales[(a.row + g + 8 * r) * groups + gr] =
             uint16_t(ld_stream_u32(block + q4_scale_at(NG, a.s, t, a.m, g)) >> (16 * r));
     }
-  }
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -533,12 +622,17 @@ int make_q4(int64_t M, int64_t N, int64_t K, int group, cudaStream_t s, wcomp_q4
   return WCOMP_OK;
 }
 
-Blocks blocks_of(const wcomp_q4* c) {
-  return {c->d, uint64_t(c->N), uint64_t(c->K), c->tiles, c->blocks, uint64_t(c->M) * c->tiles * c->blocks * 4};
+// `most`: the longest run, where that still leaves 16 CTAs per SM (quantising
+// gains from runs of 8, reading back from none)
+Blocks blocks_of(const wcomp_q4* c, uint32_t most) {
+  const uint64_t ctas = cdiv(uint64_t(c->M) * c->tiles * c->blocks * 4, kWarps);
+  const uint32_t run = uint32_t(std::max<uint64_t>(1, std::min<uint64_t>(most, ctas / (uint64_t(sm_count(c->device)) * 16))));
+  const uint32_t per = uint32_t(cdiv(c->blocks * 4, kWarps * run));
+  return {c->d, uint64_t(c->N), uint64_t(c->K), c->tiles, c->blocks, uint64_t(c->M) * c->tiles * per, per, run};
 }
 
-uint32_t block_grid(const Blocks& b, int dev) {
-  return uint32_t(std::min<uint64_t>(cdiv(b.total, kWarps), uint64_t(sm_count(dev)) * 64));
+uint32_t block_grid(const Blocks& b) {
+  return uint32_t(std::min<uint64_t>(b.runs, uint64_t(1) << 30));
 }
 
 bool on_device(const wcomp_q4* c) {
@@ -592,8 +686,8 @@ extern "C" int wcomp_q4_encode(const uint16_t* d_w, int64_t M, int64_t N, int64_
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   wcomp_q4* c = nullptr;
   if ((st = make_q4(M, N, K, group, s, &c)) != WCOMP_OK) return st;
-  const Blocks b = blocks_of(c);
-  const uint32_t grid = block_grid(b, c->device);
+  const Blocks b = blocks_of(c, 8);
+  const uint32_t grid = block_grid(b);
   const bool vec = K % 8 == 0 && aligned(d_w, 16);
 #define WCOMP_ENC(NG)                                                          \
   (vec ? q4_encode_kernel<NG, true><<<grid, kThreads, 0, s>>>(d_w, b)          \
@@ -621,8 +715,8 @@ extern "C" int wcomp_q4_pack(const uint8_t* d_codes, const uint16_t* d_scales, i
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   wcomp_q4* c = nullptr;
   if ((st = make_q4(M, N, K, group, s, &c)) != WCOMP_OK) return st;
-  const Blocks b = blocks_of(c);
-  const uint32_t grid = block_grid(b, c->device);
+  const Blocks b = blocks_of(c, 1);
+  const uint32_t grid = block_grid(b);
   if (c->ng == 1) q4_pack_kernel<1><<<grid, kThreads, 0, s>>>(d_codes, d_scales, b);
   else if (c->ng == 2) q4_pack_kernel<2><<<grid, kThreads, 0, s>>>(d_codes, d_scales, b);
   else q4_pack_kernel<4><<<grid, kThreads, 0, s>>>(d_codes, d_scales, b);
@@ -639,8 +733,8 @@ extern "C" int wcomp_q4_pack(const uint8_t* d_codes, const uint16_t* d_scales, i
 extern "C" int wcomp_q4_unpack(const wcomp_q4* c, uint8_t* d_codes, uint16_t* d_scales, void* stream) {
   if (!c || !d_codes || !d_scales || !on_device(c)) return WCOMP_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const Blocks b = blocks_of(c);
-  const uint32_t grid = block_grid(b, c->device);
+  const Blocks b = blocks_of(c, 1);
+  const uint32_t grid = block_grid(b);
   if (c->ng == 1) q4_unpack_kernel<1><<<grid, kThreads, 0, s>>>(b, d_codes, d_scales);
   else if (c->ng == 2) q4_unpack_kernel<2><<<grid, kThreads, 0, s>>>(b, d_codes, d_scales);
   else q4_unpack_kernel<4><<<grid, kThreads, 0, s>>>(b, d_codes, d_scales);
@@ -651,8 +745,8 @@ extern "C" int wcomp_q4_unpack(const wcomp_q4* c, uint8_t* d_codes, uint16_t* d_
 extern "C" int wcomp_q4_decode(const wcomp_q4* c, uint16_t* d_out, void* stream) {
   if (!c || !d_out || !on_device(c)) return WCOMP_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const Blocks b = blocks_of(c);
-  const uint32_t grid = block_grid(b, c->device);
+  const Blocks b = blocks_of(c, 1);
+  const uint32_t grid = block_grid(b);
   const bool vec = c->K % 8 == 0 && aligned(d_out, 16);
 #define WCOMP_DEC(NG)                                                            \
   (vec ? q4_decode_kernel<NG, true><<<grid, kThreads, 0, s>>>(b, d_out)          \
