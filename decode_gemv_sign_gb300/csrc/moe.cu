@@ -381,9 +381,20 @@ __device__ __forceinline__ void gate_up(const MoeParams& p, const Lists& L, uint
   if (w0 < w1) {
     Product<SRC, TILES, 1> prod;
     prod.begin(x, w0);
-    for (uint32_t k = w0; k < w1; ++k) {
-      prod.step(ring, k, k, lane, magic, x, ag, issue);
-      prod.step(ring, k, k + 1 < w1 ? k + 1 : k, lane, magic, x, au, issue);
+    // gate and up in turn through one copy of the code: the accumulators change places
+#pragma unroll 1
+    for (uint32_t i = 2 * w0; i < 2 * w1; ++i) {
+      prod.step(ring, i >> 1, i + 1 < 2 * w1 ? (i + 1) >> 1 : i >> 1, lane, magic, x, ag, issue);
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < TILES; ++n)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float was = ag[m][n][v];
+            ag[m][n][v] = au[m][n][v];
+            au[m][n][v] = was;
+          }
     }
   }
   // up to 8 pairs: gate and up together; else one after the other
@@ -588,20 +599,24 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
     {
       Cuts cuts{L.active * ft_n, uint32_t(cdiv(p.H, SRC::kCols)), 0, 0, 0, 0};
       cuts.choose(gridDim.x, kJoinCopies / 2);
-      const uint64_t begin = cuts.begin(), end = cuts.end();
-      uint64_t iat = begin;
-      uint32_t ileft = 0;  // copies left of the cursor's part, gate and up in turn
+      Parts ahead(cuts);
+      uint32_t ileft = 0, ia = ahead.unit / ft_n, ift = ahead.unit - ia * ft_n;  // copies left, gate and up in turn
       typename SRC::Cursor cg{}, cu{};
       auto enter = [&]() {
-        while (iat < end) {
-          const Seg s = seg_at(cuts, iat, end, warp, kWarps);
-          iat += s.k1 - s.k0;
-          if (s.w0 == s.w1) continue;
-          ileft = 2 * (s.w1 - s.w0);
-          const uint32_t e = L.expert[s.unit / ft_n], ft = s.unit % ft_n;
-          cg = expert_at<SRC>(p, maps, 0, e, ft, s.w0);
-          cu = expert_at<SRC>(p, maps, 1, e, ft, s.w0);
-          return;
+        while (ahead.more()) {
+          const uint32_t w0 = ahead.w0(warp);
+          ileft = 2 * (ahead.w1(warp) - w0);
+          if (ileft) {
+            const uint32_t e = L.expert[ia];
+            cg = expert_at<SRC>(p, maps, 0, e, ift, w0);
+            cu = expert_at<SRC>(p, maps, 1, e, ift, w0);
+          }
+          ahead.next();
+          if (++ift == ft_n) {
+            ift = 0;
+            ++ia;
+          }
+          if (ileft) return;
         }
       };
       auto issue = [&](uint32_t slot) {
@@ -615,14 +630,15 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
       };
       enter();
       for (uint32_t i = 0; i < D; ++i) issue((ring.slot + i) % D);
-      for (uint64_t at = begin; at < end;) {
-        const Seg s = seg_at(cuts, at, end, warp, kWarps);
-        const uint32_t a = s.unit / ft_n, ft = s.unit % ft_n, p0 = L.start[a], n = L.start[a + 1] - p0;
+      Parts s(cuts);
+      uint32_t a = s.unit / ft_n, ft = s.unit - a * ft_n;
+      for (bool first_part = true; s.more(); s.next(), first_part = false) {
+        const uint32_t p0 = L.start[a], n = L.start[a + 1] - p0, w0 = s.w0(warp), w1 = s.w1(warp);
         float g[2], u[2];
         if (n <= 8)
-          gate_up<SRC, 1>(p, L, p0, n, s.w0, s.w1, ring, lane, warp, magic, share, issue, g, u);
+          gate_up<SRC, 1>(p, L, p0, n, w0, w1, ring, lane, warp, magic, share, issue, g, u);
         else
-          gate_up<SRC, 2>(p, L, p0, n, s.w0, s.w1, ring, lane, warp, magic, share, issue, g, u);
+          gate_up<SRC, 2>(p, L, p0, n, w0, w1, ring, lane, warp, magic, share, issue, g, u);
         auto hidden = [&](int j, float gv, float uv) {
           const uint32_t c = warp + 8 * j;
           if (c >= n) return;
@@ -630,27 +646,28 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
           if (ft + 1 == ft_n)  // zeros up to the rows' padded end
             for (uint32_t f = ft_n; f < p.Fp / kTileRows; ++f) store_hidden<SRC>(p, p0 + c, f, lane, 0.f);
         };
-        if (s.k0 == 0 && s.k1 == cuts.steps) {
-          hidden(0, g[0], u[0]);
-          hidden(1, g[1], u[1]);
+        if (s.whole()) {
+#pragma unroll 1
+          for (int j = 0; j < 2; ++j) hidden(j, j ? g[1] : g[0], j ? u[1] : u[0]);
         } else {
           // thread i's four values are i + 256 q: gate of pairs 0..7, gate of 8..15, then up
           float gs[2];
           join_parts(
-              cuts, s, at == begin, p.part, kPartFloats, p.counters + 8, kPartFloats, &s_flag,
+              cuts, s, first_part, p.part, kPartFloats, p.counters + 8, kPartFloats, &s_flag,
               [&](uint32_t i) { return i < 256 ? g[0] : i < 512 ? g[1] : i < 768 ? u[0] : u[1]; },
               [&](uint32_t i, float v) {
                 if (i < 256)
                   gs[0] = v;
                 else if (i < 512)
                   gs[1] = v;
-                else if (i < 768)
-                  hidden(0, gs[0], v);
                 else
-                  hidden(1, gs[1], v);
+                  hidden(i < 768 ? 0 : 1, i < 768 ? gs[0] : gs[1], v);
               });
         }
-        at += s.k1 - s.k0;
+        if (++ft == ft_n) {
+          ft = 0;
+          ++a;
+        }
       }
     }
 
@@ -660,37 +677,39 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
       const uint32_t steps = uint32_t(cdiv(p.F, SRC::kCols));
       Cuts cuts{uint32_t(cdiv(p.H, kTileRows)), L.active * steps, 0, 0, 0, 0};
       cuts.choose(gridDim.x, kJoinCopies);
-      const uint64_t begin = cuts.begin(), end = cuts.end();
-      uint64_t iat = begin;
-      // the cursor's unit and place in it; ileft: k-steps to this expert's or the warp's end
-      uint32_t ik = 0, iend = 0, iunit = 0, ileft = 0;
+      // the cursor's place: ileft k-steps to expert ia's or the warp's end, irest
+      // after those
+      Parts ahead(cuts);
+      uint32_t ia = 0, iunit = 0, ileft = 0, irest = 0;
       typename SRC::Cursor cd{};
-      auto tile = [&]() {
-        const uint32_t a = ik / steps, k = ik - a * steps;
-        ileft = iend - ik < steps - k ? iend - ik : steps - k;
-        ik += ileft;
-        cd = expert_at<SRC>(p, maps, 2, L.expert[a], iunit, k);
+      auto tile = [&](uint32_t k) {
+        ileft = irest < steps - k ? irest : steps - k;
+        irest -= ileft;
+        cd = expert_at<SRC>(p, maps, 2, L.expert[ia], iunit, k);
       };
       auto enter = [&]() {
-        while (iat < end) {
-          const Seg s = seg_at(cuts, iat, end, warp, kWarps);
-          iat += s.k1 - s.k0;
-          if (s.w0 == s.w1) continue;
-          ik = s.w0;
-          iend = s.w1;
-          iunit = s.unit;
-          tile();
-          return;
+        for (; ahead.more(); ahead.next()) {
+          const uint32_t w0 = ahead.w0(warp);
+          irest = ahead.w1(warp) - w0;
+          iunit = ahead.unit;
+          if (irest) {
+            ia = w0 / steps;
+            tile(w0 - ia * steps);
+            ahead.next();
+            return;
+          }
         }
       };
       auto issue = [&](uint32_t slot) {
         if (ileft) {
           ring.refill(slot, cd, lane);
           if (--ileft == 0) {
-            if (ik < iend)
-              tile();
-            else
+            if (irest) {
+              ++ia;
+              tile(0);
+            } else {
               enter();
+            }
           }
         }
       };
@@ -698,15 +717,16 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
       for (uint32_t i = 0; i < D; ++i) issue((ring.slot + i) % D);
       ok = grid_barrier(p.counters + 1, p.err, &s_flag);
       if (ok) {
-          for (uint64_t at = begin; at < end;) {
-          const Seg s = seg_at(cuts, at, end, warp, kWarps);
+          bool first_part = true;
+        for (Parts s(cuts); s.more(); s.next(), first_part = false) {
           float* ys = share + warp * (kMaxT * 32);
           __syncthreads();  // the previous unit's accumulators are read
           for (uint32_t i = lane; i < p.T * 32; i += 32) ys[i] = 0.f;
           __syncwarp();
-          for (uint32_t k = s.w0; k < s.w1;) {
-            const uint32_t a = k / steps, k0 = k - a * steps;
-            const uint32_t k1 = s.w1 - k < steps - k0 ? k0 + (s.w1 - k) : steps;
+          const uint32_t w1 = s.w1(warp);
+          uint32_t k = s.w0(warp), a = k / steps, k0 = k - a * steps;
+          for (; k < w1; ++a, k0 = 0) {
+            const uint32_t k1 = w1 - k < steps - k0 ? k0 + (w1 - k) : steps;
             const uint32_t p0 = L.start[a], n = L.start[a + 1] - p0;
             if constexpr (SRC::NG > 0) {
               if (n <= 8)
@@ -736,13 +756,12 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
               p.y[uint64_t(i / 32) * p.H + row] =
                   (b & 0x7FFFFFFFu) > 0x7F800000u ? uint16_t(0x7FC0) : uint16_t((b + 0x7FFFu + ((b >> 16) & 1u)) >> 16);
           };
-          if (s.k0 == 0 && s.k1 == cuts.steps) {
+          if (s.whole()) {
             for (uint32_t i = threadIdx.x; i < p.T * 32; i += kThreads) store(i, value(i));
           } else {
-            join_parts(cuts, s, at == begin, p.part + 2 * uint64_t(gridDim.x) * kPartFloats, kPartFloats,
+            join_parts(cuts, s, first_part, p.part + 2 * uint64_t(gridDim.x) * kPartFloats, kPartFloats,
                        p.counters + 8 + kMaxGrid, p.T * 32, &s_flag, value, store);
           }
-          at += s.k1 - s.k0;
         }
       } else {
         ring.abandon();

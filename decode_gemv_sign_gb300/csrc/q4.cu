@@ -405,9 +405,9 @@ __global__ void __launch_bounds__(kThreads) q4_unpack_kernel(const __grid_consta
 // ---------------------------------------------------------------------------
 // GEMV.  A first kernel turns x into records (record_store).  The second is
 // launched to start before the first has ended: it fills its rings with
-// weights and only then waits for the records.  A unit is WM tiles; the 8
-// warps of a CTA are WM rows of warps whose WK = 8 / WM members share a tile's
-// k-steps.  The units' k-steps are cut over the CTAs (Cuts).
+// weights and only then waits for the records.  A unit is a tile of 32 rows,
+// whose k-steps the warps of a CTA share; the units' k-steps are cut over the
+// CTAs (Cuts).
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) q4_x_kernel(const uint16_t* __restrict__ x, uint64_t K, uint32_t recs, uint32_t B,
                                                    uint8_t* __restrict__ out, float* __restrict__ factors) {
@@ -432,8 +432,7 @@ struct GemvArgs {
   uint32_t* err;
   uint64_t N;
   Cuts cuts;
-  uint32_t tiles;
-  int B, wm;
+  int B;
 };
 
 constexpr int kDepth = 2;  // stages of a warp: a third takes L1 from the activations (16384 x 53248, B = 16: 126 -> 147 us)
@@ -452,26 +451,19 @@ __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_const
   float* part = reinterpret_cast<float*>(smem + kWarps * kDepth * S::kStage);  // [warp][half-tile][TILES][lane][4]
   __shared__ uint32_t s_flag;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int wk_n = kWarps / p.wm, wm = warp / wk_n, wk = warp % wk_n;
-  const uint64_t begin = p.cuts.begin(), end = p.cuts.end();
   Ring<S, kDepth> ring(smem_u32(smem) + uint32_t(warp) * kDepth * S::kStage,
                        smem_u32(part + kWarps * 2 * TILES * 128) + uint32_t(warp) * kDepth * 8, p.err, lane);
-  auto warp_seg = [&](uint64_t at) {
-    Seg s = seg_at(p.cuts, at, end, wk, wk_n);
-    if (s.unit * p.wm + wm >= p.tiles) s.w1 = s.w0;  // no tile here
-    return s;
-  };
   // The copy cursor runs kDepth k-steps ahead of the sums, across units.
-  uint64_t iat = begin;
+  Parts ahead(p.cuts);
   uint32_t ileft = 0;
   typename S::Cursor it{};
   auto enter = [&]() {
-    while (iat < end) {
-      const Seg s = warp_seg(iat);
-      iat += s.k1 - s.k0;
-      if (s.w0 == s.w1) continue;
-      ileft = s.w1 - s.w0;
-      it = S::at(p.w, p.cuts.steps, s.unit * p.wm + wm, s.w0);
+    for (; ahead.more(); ahead.next()) {
+      const uint32_t w0 = ahead.w0(warp), w1 = ahead.w1(warp);
+      if (w0 == w1) continue;
+      ileft = w1 - w0;
+      it = S::at(p.w, p.cuts.steps, ahead.unit, w0);
+      ahead.next();
       return;
     }
   };
@@ -488,35 +480,31 @@ __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_const
   const XRows<TILES> x = x_rows<TILES>(uint32_t(p.B), lane, [&](uint32_t b) { return p.xq + b * row_bytes; },
                                          [&](uint32_t b) { return p.factors + b; });
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the records are there
-  const uint32_t rows_g = uint32_t(p.wm) * kTileRows, outs = rows_g * p.B;
-  for (uint64_t at = begin; at < end;) {
-    const Seg s = warp_seg(at);
+  const uint32_t outs = kTileRows * p.B;
+  bool first_part = true;
+  for (Parts s(p.cuts); s.more(); s.next(), first_part = false) {
+    const uint32_t w0 = s.w0(warp), w1 = s.w1(warp);
     float acc[2][TILES][4];
     zero<TILES>(acc);
-    if (s.w0 < s.w1) {
+    if (w0 < w1) {
       Product<S, TILES, 1> prod;
-      prod.begin(x, s.w0);
-      for (uint32_t k = s.w0; k < s.w1; ++k) prod.step(ring, k, k + 1 < s.w1 ? k + 1 : k, lane, magic, x, acc, issue);
+      prod.begin(x, w0);
+      for (uint32_t k = w0; k < w1; ++k) prod.step(ring, k, k + 1 < w1 ? k + 1 : k, lane, magic, x, acc, issue);
     }
     __syncthreads();  // the previous unit's parts are read
     put_sums<TILES>(part + warp * 2 * TILES * 128, lane, acc);
     __syncthreads();
-    const uint64_t row0 = uint64_t(s.unit) * rows_g;
-    // output o: row o % rows_g of the unit, batch row o / rows_g; the warps in order
-    auto value = [&](uint32_t o) {
-      const uint32_t r = o % rows_g, b = o / rows_g;
-      return warp_sums<TILES>(part + (r / kTileRows) * wk_n * (2 * TILES * 128), wk_n, 2 * TILES * 128, r % kTileRows, b);
-    };
+    // output o: row o % 32 of the tile, batch row o / 32; the warps in order
+    auto value = [&](uint32_t o) { return warp_sums<TILES>(part, kWarps, 2 * TILES * 128, o % kTileRows, o / kTileRows); };
     auto store = [&](uint32_t o, float v) {
-      const uint64_t r = row0 + o % rows_g;
-      if (r < p.N) p.y[uint64_t(o / rows_g) * p.N + r] = v;
+      const uint64_t r = uint64_t(s.unit) * kTileRows + o % kTileRows;
+      if (r < p.N) p.y[uint64_t(o / kTileRows) * p.N + r] = v;
     };
-    if (s.k0 == 0 && s.k1 == p.cuts.steps) {
+    if (s.whole()) {
       for (uint32_t o = threadIdx.x; o < outs; o += kThreads) store(o, value(o));
     } else {
-      join_parts(p.cuts, s, at == begin, p.part, outs, p.counters, outs, &s_flag, value, store);
+      join_parts(p.cuts, s, first_part, p.part, outs, p.counters, outs, &s_flag, value, store);
     }
-    at += s.k1 - s.k0;
   }
 }
 
@@ -536,7 +524,8 @@ int prepare_gemv(int dev) {
     auto kern = q4_gemv_kernel<NG, TILES>;
     constexpr uint32_t smem = q4_smem<NG, TILES>();
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess) return -1;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, smem) != cudaSuccess || per_sm < 1)
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, smem) != cudaSuccess ||
+        per_sm < 1)
       return -1;
     cache[dev].store(per_sm, std::memory_order_release);
   }
@@ -547,7 +536,6 @@ template <int NG, int TILES>
 int launch_gemv(GemvArgs& p, const uint16_t* x, uint64_t K, int dev, cudaStream_t s) {
   const int per_sm = prepare_gemv<NG, TILES>(dev);
   if (per_sm < 0) return map_cuda(cudaGetLastError());
-  p.cuts.units = uint32_t(cdiv(p.tiles, uint64_t(p.wm)));
   const uint32_t ctas = std::min(uint32_t(per_sm * sm_count(dev)), kSlotWords);
   // Measured, us with whole units / cut: 2048 x 6144 6.6 / 10.5, 6144 x 6144
   // 9.7 / 13.3, 16384 x 6144 18.1 / 21.7, 16384 x 53248 85 / 79, 256 x 40576 (B
@@ -557,7 +545,7 @@ int launch_gemv(GemvArgs& p, const uint16_t* x, uint64_t K, int dev, cudaStream_
   if (st != WCOMP_OK) return st;
   const uint32_t recs = 2 * p.cuts.steps;
   const uint64_t b_xq = uint64_t(p.B) * recs * kRecord, b_f = (recs * factor_pitch<1>() * 4 + 255) & ~uint64_t(255);
-  const uint64_t b_part = p.cuts.split ? uint64_t(2) * p.cuts.grid * p.B * p.wm * kTileRows * sizeof(float) : 0;
+  const uint64_t b_part = p.cuts.split ? uint64_t(2) * p.cuts.grid * p.B * kTileRows * sizeof(float) : 0;
   uint8_t* ws = nullptr;
   cudaError_t e = pool_alloc(reinterpret_cast<void**>(&ws), b_xq + b_f + b_part, s);
   if (e != cudaSuccess) return map_cuda(e);
@@ -587,7 +575,6 @@ int launch_gemv(GemvArgs& p, const uint16_t* x, uint64_t K, int dev, cudaStream_
 
 template <int NG>
 int dispatch_gemv(GemvArgs& p, const uint16_t* x, uint64_t K, int dev, cudaStream_t s) {
-  p.wm = 1;
   return p.B <= 8 ? launch_gemv<NG, 1>(p, x, K, dev, s) : launch_gemv<NG, 2>(p, x, K, dev, s);
 }
 
@@ -768,7 +755,7 @@ extern "C" int wcomp_q4_gemv(const wcomp_q4* c, const uint16_t* d_x, int B, floa
   p.y = d_y;
   p.N = uint64_t(c->N);
   p.cuts.steps = uint32_t(c->blocks);
-  p.tiles = uint32_t(c->tiles);
+  p.cuts.units = uint32_t(c->tiles);
   p.B = B;
   const int st = c->ng == 1   ? dispatch_gemv<1>(p, d_x, uint64_t(c->K), c->device, s)
                  : c->ng == 2 ? dispatch_gemv<2>(p, d_x, uint64_t(c->K), c->device, s)

@@ -272,7 +272,7 @@ struct Q4Src {
   // scale and factor into gb, and gb by the coarser into acc where its range
   // ends, so that each step costs one fused multiply-add a value.
   template <int TILES, int NF>
-  static __device__ __forceinline__ void quarter(uint32_t st, int s, int q, int lane, uint32_t magic,
+  static __device__ __forceinline__ void quarter(uint32_t st, uint32_t s, int q, int lane, uint32_t magic,
                                                  const XQuarter<TILES>& x, const XFactors<TILES, NF>& f,
                                                  float (&ga)[2][TILES][4], float (&gb)[2][TILES][4],
                                                  float (&acc)[2][TILES][4]) {
@@ -281,7 +281,7 @@ struct Q4Src {
     constexpr bool kTwo = RUNS > WIDE;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      const uint4 w4 = lds_v4(st + ((2 * s + m) * 2 + q) * 512 + lane * 16);
+      const uint4 w4 = lds_v4(st + s * 2048 + (m * 2 + q) * 512 + lane * 16);
       const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
       for (int ii = 0; ii < 4; ++ii) {
@@ -301,7 +301,7 @@ struct Q4Src {
         const int j = i * NG / 8, jf = i * NF / 8;
         float sg = 1.f, sh = 1.f;
         if (NG >= NF || ends) {
-          const uint32_t sc = lds_u32(st + q4_scale_at(NG, s, j, m, 0) + (lane >> 2) * 4);
+          const uint32_t sc = lds_u32(st + q4_scale_at(NG, 0, j, m, 0) + s * (64 * NG) + (lane >> 2) * 4);
           sg = bf16_lo(sc);
           sh = bf16_hi(sc);
         }
@@ -475,29 +475,32 @@ struct Ring {
 // otherwise stand in every step.
 template <class SRC, int TILES, int NF>
 struct Product {  // 4-bit
-  XQuarter<TILES> x0, x1;
-  XFactors<TILES, NF> fa, fb;
+  XQuarter<TILES> x0;
+  XFactors<TILES, NF> f;
   __device__ __forceinline__ void begin(const XRows<TILES>& x, uint32_t k) {
-    fa.load(x, 2 * k);
+    f.load(x, 2 * k);
     x0.load(x, uint64_t(2 * k) * kRecord);
   }
   template <class RING, class ISSUE>
   __device__ __forceinline__ void step(RING& ring, uint32_t k, uint32_t kn, int lane, uint32_t magic,
                                        const XRows<TILES>& x, float (&acc)[2][TILES][4], ISSUE& issue) {
     const uint32_t st = ring.stage();
-    const uint64_t at = uint64_t(2 * k) * kRecord;
-    float ga[2][TILES][4], gb[2][TILES][4];
     ring.wait(lane);
-    x1.load(x, at + 128);
-    fb.load(x, 2 * k + 1);
-    SRC::template quarter<TILES, NF>(st, 0, 0, lane, magic, x0, fa, ga, gb, acc);
-    x0.load(x, at + kRecord);
-    SRC::template quarter<TILES, NF>(st, 0, 1, lane, magic, x1, fa, ga, gb, acc);
-    x1.load(x, at + kRecord + 128);
-    fa.load(x, 2 * kn);
-    SRC::template quarter<TILES, NF>(st, 1, 0, lane, magic, x0, fb, ga, gb, acc);
-    x0.load(x, uint64_t(2 * kn) * kRecord);
-    SRC::template quarter<TILES, NF>(st, 1, 1, lane, magic, x1, fb, ga, gb, acc);
+    // rolled: the kernels that use this have several products in them, and
+    // their code has to stay in the instruction caches
+#pragma unroll 1
+    for (uint32_t s = 0; s < 2; ++s) {
+      const uint32_t rec = 2 * k + s, next = s ? 2 * kn : rec + 1;
+      float ga[2][TILES][4], gb[2][TILES][4];
+      XQuarter<TILES> x1;
+      XFactors<TILES, NF> fn;
+      x1.load(x, uint64_t(rec) * kRecord + 128);
+      fn.load(x, next);
+      SRC::template quarter<TILES, NF>(st, s, 0, lane, magic, x0, f, ga, gb, acc);
+      x0.load(x, uint64_t(next) * kRecord);
+      SRC::template quarter<TILES, NF>(st, s, 1, lane, magic, x1, f, ga, gb, acc);
+      f = fn;
+    }
     __syncwarp();  // every lane has read the stage
     issue(ring.slot);
     ring.next();
@@ -575,49 +578,60 @@ struct Cuts {
   // join costs, in k-steps.
   __host__ __device__ void choose(uint32_t ctas, uint32_t join) {
     const uint64_t whole = cdiv(units, ctas) * steps, cut = cdiv(uint64_t(units) * steps, ctas);
-    split = whole > cut + join;
+    split = whole > cut + join && uint64_t(units) * steps < (uint64_t(1) << 32);
     spread(ctas);
   }
   __device__ __forceinline__ uint64_t start(uint32_t c) const {
     const uint64_t v = quot * c + (c < rem ? c : rem);
     return split ? v : v * steps;
   }
-  // The CTA that has k-step s (split only).
-  __device__ __forceinline__ uint32_t owner(uint64_t s) const {
-    const uint64_t big = (quot + 1) * rem;
-    return s < big ? uint32_t(s / (quot + 1)) : rem + uint32_t((s - big) / quot);
+  // The CTA that has k-step s (split only; `choose` splits work below 2^32).
+  __device__ __forceinline__ uint32_t owner(uint32_t s) const {
+    const uint32_t q = uint32_t(quot), big = (q + 1) * rem;
+    return s < big ? s / (q + 1) : rem + (s - big) / q;
   }
-  // This CTA's range; empty past the grid.
-  __device__ __forceinline__ uint64_t begin() const { return start(blockIdx.x < grid ? blockIdx.x : grid); }
-  __device__ __forceinline__ uint64_t end() const { return start(blockIdx.x < grid ? blockIdx.x + 1 : grid); }
 };
 
-// A CTA's k-steps [k0, k1) of one unit, and a warp's share [w0, w1) of them.
-struct Seg {
-  uint32_t unit, k0, k1, w0, w1;
+// The units' parts of this CTA's range, one after the other: part [k0, k1) of
+// `unit`, and a warp's share [w0, w1) of it.
+struct Parts {
+  uint32_t steps, unit, k0, k1, left;
+  __device__ __forceinline__ explicit Parts(const Cuts& c) : steps(c.steps) {
+    const uint64_t begin = c.start(blockIdx.x < c.grid ? blockIdx.x : c.grid);
+    const uint64_t end = c.start(blockIdx.x < c.grid ? blockIdx.x + 1 : c.grid);
+    unit = uint32_t(begin / c.steps);
+    k0 = uint32_t(begin - uint64_t(unit) * c.steps);
+    left = uint32_t(end - begin);  // k-steps, of 4 KB: never 2^32 of them
+    cut();
+  }
+  __device__ __forceinline__ void cut() { k1 = left < steps - k0 ? k0 + left : steps; }
+  __device__ __forceinline__ bool more() const { return left != 0; }
+  __device__ __forceinline__ bool whole() const { return k0 == 0 && k1 == steps; }
+  __device__ __forceinline__ void next() {
+    left -= k1 - k0;
+    ++unit;
+    k0 = 0;
+    cut();
+  }
+  __device__ __forceinline__ uint32_t w0(uint32_t warp) const { return k0 + share(warp); }
+  __device__ __forceinline__ uint32_t w1(uint32_t warp) const { return k0 + share(warp + 1); }
+  // len * i / 8 without overflow (8 warps share a part)
+  __device__ __forceinline__ uint32_t share(uint32_t i) const {
+    const uint32_t len = k1 - k0;
+    return (len >> 3) * i + (((len & 7) * i) >> 3);
+  }
 };
-__device__ __forceinline__ Seg seg_at(const Cuts& c, uint64_t at, uint64_t end, uint32_t wk, uint32_t wk_n) {
-  Seg s;
-  s.unit = uint32_t(at / c.steps);
-  s.k0 = uint32_t(at - uint64_t(s.unit) * c.steps);
-  const uint64_t left = end - at;
-  s.k1 = left < c.steps - s.k0 ? s.k0 + uint32_t(left) : c.steps;
-  const uint32_t len = s.k1 - s.k0;
-  s.w0 = s.k0 + uint32_t(uint64_t(len) * wk / wk_n);
-  s.w1 = s.k0 + uint32_t(uint64_t(len) * (wk + 1) / wk_n);
-  return s;
-}
 
 // This CTA's part of a cut unit, n floats given by value(i), joined with the
 // others'; store(i, sum) runs in the last CTA to arrive.  part: 2 n_max floats
 // per CTA; counters: one per CTA, zero before and after.  All threads call it.
 template <class VALUE, class STORE>
-__device__ __forceinline__ void join_parts(const Cuts& c, const Seg& s, bool first_seg, float* part, uint32_t n_max,
+__device__ __forceinline__ void join_parts(const Cuts& c, const Parts& s, bool first_part, float* part, uint32_t n_max,
                                            uint32_t* counters, uint32_t n, uint32_t* s_flag, VALUE value, STORE store) {
-  const uint64_t g0 = uint64_t(s.unit) * c.steps, g1 = g0 + c.steps;
-  float* mine = part + (2 * uint64_t(blockIdx.x) + (first_seg ? 0 : 1)) * n_max;
+  const uint32_t g0 = s.unit * c.steps;
+  float* mine = part + (2 * uint64_t(blockIdx.x) + (first_part ? 0 : 1)) * n_max;
   for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) __stcg(mine + i, value(i));
-  const uint32_t first = c.owner(g0), last = c.owner(g1 - 1);
+  const uint32_t first = c.owner(g0), last = c.owner(g0 + c.steps - 1);
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
