@@ -367,7 +367,9 @@ __device__ __forceinline__ void store_hidden(const MoeParams& p, uint32_t pair, 
 
 // Phase B: this warp's k-steps [w0, w1) of the gate and up tiles for one
 // expert's n pairs from p0 on, then the unit's sums: thread i gets output i +
-// 256 j (row i % 32, pair i / 32 + 8 j) as g[j] and u[j].
+// 256 j (row i % 32, pair i / 32 + 8 j) as g[j] and u[j].  Up to 8 pairs take
+// gate and up steps in turn, so that x comes from L1 for one of them; more take
+// all gate steps, then all up steps, with one set of accumulators.
 template <class SRC, int TILES, class RING, class ISSUE>
 __device__ __forceinline__ void gate_up(const MoeParams& p, const Lists& L, uint32_t p0, uint32_t n, uint32_t w0,
                                         uint32_t w1, RING& ring, int lane, int warp, uint32_t magic, float* share,
@@ -375,44 +377,56 @@ __device__ __forceinline__ void gate_up(const MoeParams& p, const Lists& L, uint
   const XRows<TILES> x = x_rows<TILES>(
       n, lane, [&](uint32_t b) { return p.xs + L.tok[p0 + b] * p.xs_bytes; },
       [&](uint32_t b) { return p.xf + L.tok[p0 + b]; });
-  float ag[2][TILES][4], au[2][TILES][4];
-  zero<TILES>(ag);
-  zero<TILES>(au);
-  if (w0 < w1) {
-    Product<SRC, TILES, 1> prod;
-    prod.begin(x, w0);
-    // gate and up in turn through one copy of the code: the accumulators change places
+  if constexpr (TILES == 1) {
+    float ag[2][1][4], au[2][1][4];
+    zero<1>(ag);
+    zero<1>(au);
+    if (w0 < w1) {
+      Product<SRC, 1, 1> prod;
+      prod.begin(x, w0);
+      // through one copy of the code: the accumulators change places
 #pragma unroll 1
-    for (uint32_t i = 2 * w0; i < 2 * w1; ++i) {
-      prod.step(ring, i >> 1, i + 1 < 2 * w1 ? (i + 1) >> 1 : i >> 1, lane, magic, x, ag, issue);
+      for (uint32_t i = 2 * w0; i < 2 * w1; ++i) {
+        prod.step(ring, i >> 1, i + 1 < 2 * w1 ? (i + 1) >> 1 : i >> 1, lane, magic, x, ag, issue);
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int n = 0; n < TILES; ++n)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const float was = ag[m][n][v];
-            ag[m][n][v] = au[m][n][v];
-            au[m][n][v] = was;
-          }
+        for (int v = 0; v < 8; ++v) {
+          const float was = ag[v >> 2][0][v & 3];
+          ag[v >> 2][0][v & 3] = au[v >> 2][0][v & 3];
+          au[v >> 2][0][v & 3] = was;
+        }
+      }
     }
-  }
-  // up to 8 pairs: gate and up together; else one after the other
-  constexpr uint32_t kEach = 2 * TILES * 128, kRounds = TILES, kStride = kEach * (3 - TILES);
-#pragma unroll
-  for (uint32_t i = 0; i < kRounds; ++i) {
     __syncthreads();  // what was in `share` is read
-    float* mine = share + warp * kStride;
-    if (i == 0) put_sums<TILES>(mine, lane, ag);
-    if (i + 1 == kRounds) put_sums<TILES>(mine + (kRounds == 1 ? kEach : 0), lane, au);
+    put_sums<1>(share + warp * 512, lane, ag);
+    put_sums<1>(share + warp * 512 + 256, lane, au);
     __syncthreads();
+    const bool ok = uint32_t(warp) < n;
+    g[0] = ok ? warp_sums<1>(share, kWarps, 512, lane, warp) : 0.f;
+    u[0] = ok ? warp_sums<1>(share + 256, kWarps, 512, lane, warp) : 0.f;
+    g[1] = u[1] = 0.f;
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      float acc[2][TILES][4];
+      zero<TILES>(acc);
+      if (w0 < w1) {
+        Product<SRC, TILES, 1> prod;
+        prod.begin(x, w0);
+#pragma unroll 1
+        for (uint32_t k = w0; k < w1; ++k) prod.step(ring, k, k + 1 < w1 ? k + 1 : k, lane, magic, x, acc, issue);
+      }
+      __syncthreads();
+      put_sums<TILES>(share + warp * 512, lane, acc);
+      __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t b = warp + 8 * j;
-      const bool ok = j < TILES && b < n;
-      if (i == 0) g[j] = ok ? warp_sums<TILES>(share, kWarps, kStride, lane, b) : 0.f;
-      if (i + 1 == kRounds)
-        u[j] = ok ? warp_sums<TILES>(share + (kRounds == 1 ? kEach : 0), kWarps, kStride, lane, b) : 0.f;
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t b = warp + 8 * j;
+        const float v = b < n ? warp_sums<TILES>(share, kWarps, 512, lane, b) : 0.f;
+        if (i == 0)
+          g[j] = v;
+        else
+          u[j] = v;
+      }
     }
   }
 }
@@ -460,7 +474,7 @@ __device__ __forceinline__ void down(const MoeParams& p, const Lists& L, uint32_
 
 // Phase A: units of 16 experts and a quarter of H.  Lane (g, t) takes columns
 // 16 t .. 16 t + 15 of a 64-column step of rows g and g + 8 and of tokens g (and
-// g + 8), straight from memory, two steps at a time.
+// g + 8), straight from memory, several steps at a time.
 template <bool VEC>
 __device__ __forceinline__ void load16(const uint16_t* row, uint32_t c, uint32_t n, bool ok, uint32_t (&v)[8]) {
 #pragma unroll
@@ -478,7 +492,7 @@ template <int NT, bool VEC>
 __device__ __forceinline__ void router_logits(const MoeParams& p, float* share, int lane, int warp) {
   const uint32_t tiles = uint32_t(cdiv(p.E, 16)), steps = uint32_t(cdiv(p.H, kBfCols));
   const uint32_t g = uint32_t(lane) >> 2, t = uint32_t(lane) & 3;
-  constexpr int U = VEC ? 2 : 1;
+  constexpr int U = VEC ? 4 / NT : 1;
   for (uint32_t u = blockIdx.x; u < tiles * kSplits; u += gridDim.x) {
     const uint32_t tile = u / kSplits, sp = u % kSplits, part_i = sp * kWarps + warp;
     constexpr uint32_t parts = kSplits * kWarps;
@@ -524,7 +538,9 @@ __device__ __forceinline__ void router_logits(const MoeParams& p, float* share, 
   }
 }
 
-template <class SRC>
+// WIDE: more than 8 tokens, whose experts may have more than 8 pairs.  The
+// narrow kernel is smaller by the products for those.
+template <class SRC, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant__ MoeParams p,
                                                           const __grid_constant__ MoeMaps maps) {
   static_assert(moe_ring<SRC>() >= kMaxE * 8, "the rings hold the scores and keys");
@@ -541,14 +557,10 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
                     smem_u32(smem) + kWarps * moe_ring<SRC>() + kShare + uint32_t(warp) * D * 8, p.err, lane);
 
   // ---- A: router logits, and x in the form that the products take
-  if (p.x_vec) {
-    if (p.T <= 8)
-      router_logits<1, true>(p, share, lane, warp);
-    else
-      router_logits<2, true>(p, share, lane, warp);
-  } else {
-    router_logits<2, false>(p, share, lane, warp);
-  }
+  if (p.x_vec)
+    router_logits<WIDE ? 2 : 1, true>(p, share, lane, warp);
+  else
+    router_logits<WIDE ? 2 : 1, false>(p, share, lane, warp);
   if (p.make) {
     // from the last CTA on: the first ones have the router
     const uint32_t first = (gridDim.x - 1 - blockIdx.x) * kWarps + warp, stride = gridDim.x * kWarps;
@@ -597,10 +609,10 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
     // ---- B: gate and up
     const uint32_t ft_n = uint32_t(cdiv(p.F, kTileRows));
     {
-      Cuts cuts{L.active * ft_n, uint32_t(cdiv(p.H, SRC::kCols)), 0, 0, 0, 0};
-      cuts.choose(gridDim.x, kJoinCopies / 2);
+      const Cuts cuts(L.active * ft_n, uint32_t(cdiv(p.H, SRC::kCols)), gridDim.x, kJoinCopies / 2);
       Parts ahead(cuts);
-      uint32_t ileft = 0, ia = ahead.unit / ft_n, ift = ahead.unit - ia * ft_n;  // copies left, gate and up in turn
+      // copies left: gate and up in turn, or (many pairs) all gate, then `iup` up
+      uint32_t ileft = 0, iup = 0, ia = ahead.unit / ft_n, ift = ahead.unit - ia * ft_n;
       typename SRC::Cursor cg{}, cu{};
       auto enter = [&]() {
         while (ahead.more()) {
@@ -608,6 +620,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
           ileft = 2 * (ahead.w1(warp) - w0);
           if (ileft) {
             const uint32_t e = L.expert[ia];
+            if (WIDE) iup = L.start[ia + 1] - L.start[ia] > 8 ? ileft / 2 : 0;
             cg = expert_at<SRC>(p, maps, 0, e, ift, w0);
             cu = expert_at<SRC>(p, maps, 1, e, ift, w0);
           }
@@ -621,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
       };
       auto issue = [&](uint32_t slot) {
         if (ileft) {
-          if (ileft & 1)
+          if (WIDE && iup ? ileft <= iup : ileft & 1)
             ring.refill(slot, cu, lane);
           else
             ring.refill(slot, cg, lane);
@@ -635,9 +648,9 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
       for (bool first_part = true; s.more(); s.next(), first_part = false) {
         const uint32_t p0 = L.start[a], n = L.start[a + 1] - p0, w0 = s.w0(warp), w1 = s.w1(warp);
         float g[2], u[2];
-        if (n <= 8)
+        if (!WIDE || n <= 8)
           gate_up<SRC, 1>(p, L, p0, n, w0, w1, ring, lane, warp, magic, share, issue, g, u);
-        else
+        else if constexpr (WIDE)
           gate_up<SRC, 2>(p, L, p0, n, w0, w1, ring, lane, warp, magic, share, issue, g, u);
         auto hidden = [&](int j, float gv, float uv) {
           const uint32_t c = warp + 8 * j;
@@ -675,8 +688,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
     // chosen experts, one expert after the other.
     {
       const uint32_t steps = uint32_t(cdiv(p.F, SRC::kCols));
-      Cuts cuts{uint32_t(cdiv(p.H, kTileRows)), L.active * steps, 0, 0, 0, 0};
-      cuts.choose(gridDim.x, kJoinCopies);
+      const Cuts cuts(uint32_t(cdiv(p.H, kTileRows)), L.active * steps, gridDim.x, kJoinCopies);
       // the cursor's place: ileft k-steps to expert ia's or the warp's end, irest
       // after those
       Parts ahead(cuts);
@@ -729,16 +741,16 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
             const uint32_t k1 = w1 - k < steps - k0 ? k0 + (w1 - k) : steps;
             const uint32_t p0 = L.start[a], n = L.start[a + 1] - p0;
             if constexpr (SRC::NG > 0) {
-              if (n <= 8)
+              if (!WIDE || n <= 8)
                 down<SRC, 1>(p, L, p0, n, k0, k1, ring, lane, magic, ys, issue);
-              else
+              else if constexpr (WIDE)
                 down<SRC, 2>(p, L, p0, n, k0, k1, ring, lane, magic, ys, issue);
             } else {
               if (n <= 4)
                 down<SRC, 1>(p, L, p0, n, k0, k1, ring, lane, magic, ys, issue);
-              else if (n <= 8)
+              else if (!WIDE || n <= 8)
                 down<SRC, 2>(p, L, p0, n, k0, k1, ring, lane, magic, ys, issue);
-              else
+              else if constexpr (WIDE)
                 down<SRC, 4>(p, L, p0, n, k0, k1, ring, lane, magic, ys, issue);
             }
             k += k1 - k0;
@@ -779,10 +791,10 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
   }
 }
 
-template <class SRC>
-int launch_moe(MoeParams& p, const MoeMaps& maps, int dev, cudaStream_t s) {
+template <class SRC, bool WIDE>
+int launch_moe_as(MoeParams& p, const MoeMaps& maps, int dev, cudaStream_t s) {
   static std::atomic<int> cache[64];
-  auto kern = moe_kernel<SRC>;
+  auto kern = moe_kernel<SRC, WIDE>;
   constexpr uint32_t smem = moe_smem<SRC>();
   int per_sm = cache[dev].load(std::memory_order_acquire);
   if (!per_sm) {
@@ -799,6 +811,11 @@ int launch_moe(MoeParams& p, const MoeMaps& maps, int dev, cudaStream_t s) {
       cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kern), dim3(grid), dim3(kThreads), args, smem, s);
   count_launches(1);
   return map_cuda(e == cudaSuccess ? cudaGetLastError() : e);
+}
+
+template <class SRC>
+int launch_moe(MoeParams& p, const MoeMaps& maps, int dev, cudaStream_t s) {
+  return p.T > 8 ? launch_moe_as<SRC, true>(p, maps, dev, s) : launch_moe_as<SRC, false>(p, maps, dev, s);
 }
 
 // Boxes of 32 rows x 64 columns of a row-major BF16 matrix, 128-byte swizzled.

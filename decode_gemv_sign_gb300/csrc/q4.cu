@@ -431,7 +431,7 @@ struct GemvArgs {
   uint32_t* counters;   // one per CTA, zero
   uint32_t* err;
   uint64_t N;
-  Cuts cuts;
+  Cuts cuts{1, 1, 1, 0};
   int B;
 };
 
@@ -540,7 +540,7 @@ int launch_gemv(GemvArgs& p, const uint16_t* x, uint64_t K, int dev, cudaStream_
   // Measured, us with whole units / cut: 2048 x 6144 6.6 / 10.5, 6144 x 6144
   // 9.7 / 13.3, 16384 x 6144 18.1 / 21.7, 16384 x 53248 85 / 79, 256 x 40576 (B
   // = 7) 26 / 13.
-  p.cuts.choose(ctas, kJoinCopies);
+  p.cuts = Cuts(p.cuts.units, p.cuts.steps, ctas, kJoinCopies);
   const int st = work_slot(dev, &p.counters, &p.err);
   if (st != WCOMP_OK) return st;
   const uint32_t recs = 2 * p.cuts.steps;
@@ -749,8 +749,7 @@ extern "C" int wcomp_q4_decode(const wcomp_q4* c, uint16_t* d_out, void* stream)
 extern "C" int wcomp_q4_gemv(const wcomp_q4* c, const uint16_t* d_x, int B, float* d_y, void* stream) {
   if (!c || !d_x || !d_y || B < 1 || B > 16 || c->M != 1 || !on_device(c)) return WCOMP_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  GemvArgs p;
-  memset(&p, 0, sizeof(p));
+  GemvArgs p{};
   p.w = c->d;
   p.y = d_y;
   p.N = uint64_t(c->N);

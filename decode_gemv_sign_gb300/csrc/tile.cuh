@@ -478,7 +478,7 @@ struct Product {  // 4-bit
   XQuarter<TILES> x0;
   XFactors<TILES, NF> f;
   __device__ __forceinline__ void begin(const XRows<TILES>& x, uint32_t k) {
-    f.load(x, 2 * k);
+    if (TILES == 1 || NF == 1) f.load(x, 2 * k);
     x0.load(x, uint64_t(2 * k) * kRecord);
   }
   template <class RING, class ISSUE>
@@ -494,12 +494,16 @@ struct Product {  // 4-bit
       float ga[2][TILES][4], gb[2][TILES][4];
       XQuarter<TILES> x1;
       XFactors<TILES, NF> fn;
+      constexpr bool kAhead = TILES == 1 || NF == 1;  // sixteen rows' four factors: no registers left to load ahead
       x1.load(x, uint64_t(rec) * kRecord + 128);
-      fn.load(x, next);
+      if (kAhead)
+        fn.load(x, next);
+      else
+        f.load(x, rec);
       SRC::template quarter<TILES, NF>(st, s, 0, lane, magic, x0, f, ga, gb, acc);
       x0.load(x, uint64_t(next) * kRecord);
       SRC::template quarter<TILES, NF>(st, s, 1, lane, magic, x1, f, ga, gb, acc);
-      f = fn;
+      if (kAhead) f = fn;
     }
     __syncwarp();  // every lane has read the stage
     issue(ring.slot);
@@ -515,13 +519,16 @@ struct Product<BfSrc<MAP>, TILES, NF> {
                                        float (&acc)[2][TILES][4], ISSUE& issue) {
     const uint32_t st = ring.stage();
     XQuarter<TILES> x1;
-    x1.load(x, uint64_t(kn) * (2 * kBfCols));
+    if (TILES < 4) x1.load(x, uint64_t(kn) * (2 * kBfCols));
     ring.wait(lane);
     BfSrc<MAP>::multiply(st, lane, x0, acc);
     __syncwarp();
     issue(ring.slot);
     ring.next();
-    x0 = x1;
+    if (TILES < 4)
+      x0 = x1;
+    else
+      x0.load(x, uint64_t(kn) * (2 * kBfCols));
   }
 };
 
@@ -563,32 +570,30 @@ __device__ __forceinline__ float warp_sums(const float* part, int warps, uint32_
 // CTAs: the result does not depend on which one that is.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kJoinCopies = 24;  // what a join costs, in 4 KB copies of a CTA
+__host__ __device__ __forceinline__ uint32_t cdiv32(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
 struct Cuts {
-  uint32_t units, steps, grid;  // grid: CTAs that have work, at most one per k-step (split) or unit
-  uint32_t split;
-  uint64_t quot;                // pieces (k-steps or units) per CTA; the first rem CTAs take one more
-  uint32_t rem;
-  __host__ __device__ void spread(uint32_t ctas) {
-    const uint64_t work = split ? uint64_t(units) * steps : units;
-    grid = work < ctas ? uint32_t(work) : ctas;
-    quot = work / grid;
-    rem = uint32_t(work - quot * grid);
-  }
+  uint32_t units, steps, split;
+  uint32_t grid;        // CTAs that have work, at most one per k-step (split) or unit
+  uint32_t quot, rem;   // pieces (k-steps or units) per CTA; the first rem CTAs take one more
   // Cut units anywhere where that shortens the longest CTA's run by more than a
-  // join costs, in k-steps.
-  __host__ __device__ void choose(uint32_t ctas, uint32_t join) {
-    const uint64_t whole = cdiv(units, ctas) * steps, cut = cdiv(uint64_t(units) * steps, ctas);
-    split = whole > cut + join && uint64_t(units) * steps < (uint64_t(1) << 32);
-    spread(ctas);
+  // join costs, in k-steps.  Work is cut by k-steps only below 2^32 of them, so
+  // that 32-bit divisions do (a 64-bit one takes most of a microsecond, and
+  // several would stand before the first copy of a phase).
+  __host__ __device__ Cuts(uint32_t units_, uint32_t steps_, uint32_t ctas, uint32_t join) : units(units_), steps(steps_) {
+    const uint64_t all = uint64_t(units) * steps;
+    const uint32_t rounds = cdiv32(units, ctas);
+    split = (all >> 31) == 0 && uint64_t(rounds) * steps > cdiv32(uint32_t(all), ctas) + join;
+    const uint32_t work = split ? uint32_t(all) : units;
+    grid = work < ctas ? work : ctas;
+    quot = work / grid;
+    rem = work - quot * grid;
   }
-  __device__ __forceinline__ uint64_t start(uint32_t c) const {
-    const uint64_t v = quot * c + (c < rem ? c : rem);
-    return split ? v : v * steps;
-  }
-  // The CTA that has k-step s (split only; `choose` splits work below 2^32).
+  // First piece of CTA c.
+  __device__ __forceinline__ uint32_t start(uint32_t c) const { return quot * c + (c < rem ? c : rem); }
+  // The CTA that has k-step s (split only).
   __device__ __forceinline__ uint32_t owner(uint32_t s) const {
-    const uint32_t q = uint32_t(quot), big = (q + 1) * rem;
-    return s < big ? s / (q + 1) : rem + (s - big) / q;
+    const uint32_t big = (quot + 1) * rem;
+    return s < big ? s / (quot + 1) : rem + (s - big) / quot;
   }
 };
 
@@ -597,11 +602,11 @@ struct Cuts {
 struct Parts {
   uint32_t steps, unit, k0, k1, left;
   __device__ __forceinline__ explicit Parts(const Cuts& c) : steps(c.steps) {
-    const uint64_t begin = c.start(blockIdx.x < c.grid ? blockIdx.x : c.grid);
-    const uint64_t end = c.start(blockIdx.x < c.grid ? blockIdx.x + 1 : c.grid);
-    unit = uint32_t(begin / c.steps);
-    k0 = uint32_t(begin - uint64_t(unit) * c.steps);
-    left = uint32_t(end - begin);  // k-steps, of 4 KB: never 2^32 of them
+    const uint32_t cta = blockIdx.x < c.grid ? blockIdx.x : c.grid, begin = c.start(cta);
+    const uint32_t pieces = blockIdx.x < c.grid ? c.start(cta + 1) - begin : 0u;
+    unit = c.split ? begin / c.steps : begin;
+    k0 = c.split ? begin - unit * c.steps : 0u;
+    left = c.split ? pieces : pieces * c.steps;  // k-steps, of 4 KB: never 2^32 of them
     cut();
   }
   __device__ __forceinline__ void cut() { k1 = left < steps - k0 ? k0 + left : steps; }
