@@ -320,8 +320,8 @@ __device__ __forceinline__ typename SRC::Cursor expert_at(const MoeParams& p, co
   if constexpr (SRC::NG > 0) {
     return SRC::at(w.p + e * w.expert_bytes, uint32_t(cdiv(w.K, kQ4Cols)), tile, step);
   } else {
-    return {&maps.m[i], reinterpret_cast<const uint16_t*>(w.p), uint64_t(p.E) * w.N,
-            uint64_t(e) * w.N + tile * kTileRows, w.K, step * kBfCols};
+    return SRC::at(&maps.m[i], reinterpret_cast<const uint16_t*>(w.p), uint64_t(p.E) * w.N,
+                   uint64_t(e) * w.N + tile * kTileRows, w.K, step * kBfCols);
   }
 }
 
@@ -330,7 +330,7 @@ __device__ __forceinline__ typename SRC::Cursor expert_at(const MoeParams& p, co
 // experts of 6144 x 2048).  BF16: three in one CTA per SM (two CTAs of two
 // stages: 112 -> 121 us).
 template <class SRC>
-constexpr int moe_depth() { return SRC::NG > 0 ? 2 : 3; }
+constexpr int moe_depth() { return SRC::NG > 0 || !SRC::kCopies ? 2 : 3; }
 template <class SRC>
 constexpr uint32_t moe_ring() { return moe_depth<SRC>() * SRC::kStage; }  // one warp's
 // Shared memory after the rings: A's parts (8 warps x 16 x 16), B's sums (8
@@ -359,7 +359,7 @@ __device__ __forceinline__ void store_hidden(const MoeParams& p, uint32_t pair, 
   } else {
     uint16_t hi, lo;
     split_bf16(v, hi, lo);
-    uint16_t* h = reinterpret_cast<uint16_t*>(p.h) + uint64_t(pair) * 2 * p.Fp + row;
+    uint16_t* h = reinterpret_cast<uint16_t*>(p.h) + uint64_t(pair) * 2 * p.Fp + (SRC::kCopies ? row : bf_place(row));
     h[0] = hi;
     h[p.Fp] = lo;
   }
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
       uint16_t* out = reinterpret_cast<uint16_t*>(p.make);
       for (uint32_t i = first * 32 + lane; i < p.T * Hp; i += stride * 32) {
         const uint32_t b = i / Hp, c = i - b * Hp;
-        out[i] = c < p.H ? p.x[uint64_t(b) * p.H + c] : uint16_t(0);
+        out[SRC::kCopies ? i : b * Hp + bf_place(c)] = c < p.H ? p.x[uint64_t(b) * p.H + c] : uint16_t(0);
       }
     }
   }
@@ -893,7 +893,7 @@ extern "C" int wcomp_moe(const wcomp_moe_args* a, void* stream) {
   // x's form for the products: records, or BF16 rows of whole 64-column steps
   // that start on 32-byte boundaries
   const uint64_t Hp = q4 ? cdiv(p.H, kQ4Cols) * kQ4Cols : cdiv(p.H, kBfCols) * kBfCols;
-  const bool make = q4 || Hp != p.H || !aligned(a->d_x, 32);
+  const bool make = q4 || !mapped || Hp != p.H || !aligned(a->d_x, 32);
   p.xs_bytes = 2 * Hp;
   auto round = [](uint64_t b) { return (b + 255) & ~uint64_t(255); };
   const uint64_t pairs = uint64_t(p.T) * p.k;

@@ -327,43 +327,30 @@ struct Q4Src {
   }
 };
 
-// Row-major BF16 weights, viewed as one matrix of rows (all experts').
+// Row-major BF16 weights, viewed as one matrix of rows (all experts').  A box may
+// reach past its expert's last row into the next one's: MMA rows do not mix, and
+// the sums of those are not used.
+//
 // MAP: rows of a multiple of 8 columns from a 16-byte aligned base, copied as
 // boxes of 32 rows x 64 columns through a tensor map (zeros past the last
 // column and row), whose 128-byte swizzle puts 16-byte chunk c of row r at
-// chunk c ^ (r % 8): the lanes' reads meet no bank conflict.  Otherwise
-// element loads by the whole warp, stored in the same places.  A box may reach
-// past its expert's last row into the next one's: MMA rows do not mix, and the
-// sums of those are not used.
+// chunk c ^ (r % 8): the lanes' reads meet no bank conflict.
 template <bool MAP>
 struct BfSrc {
   static constexpr int NG = 0;
   static constexpr int kCols = kBfCols;
   static constexpr uint32_t kStage = 4096;
-  static constexpr bool kCopies = MAP;
+  static constexpr bool kCopies = true;
   struct Cursor {
-    const CUtensorMap* map;  // MAP
-    const uint16_t* w;       // otherwise: the matrix
-    uint64_t rows, row;      // of the matrix; first row of the tile
-    uint32_t K, col;         // columns of the matrix, first column of the step
+    const CUtensorMap* map;
+    uint32_t row, col;  // first row of the tile, first column of the step
   };
-  static __device__ __forceinline__ void issue(Cursor& c, uint32_t st, uint32_t bar) {
-    box_copy(st, c.map, c.col, uint32_t(c.row), bar);
-    c.col += kCols;
+  static __device__ __forceinline__ Cursor at(const CUtensorMap* map, const uint16_t*, uint64_t, uint64_t row, uint32_t,
+                                              uint32_t col) {
+    return {map, uint32_t(row), col};
   }
-  static __device__ __forceinline__ void load(Cursor& c, uint32_t st, int lane) {
-#pragma unroll 2
-    for (int i = 0; i < 8; ++i) {  // 32 rows x 8 chunks, a chunk a lane
-      const uint32_t r = 4 * i + (uint32_t(lane) >> 3), ch = uint32_t(lane) & 7, k = c.col + 8 * ch;
-      uint32_t v[4] = {0u, 0u, 0u, 0u};
-      if (c.row + r < c.rows) {
-        const uint16_t* src = c.w + (c.row + r) * c.K + k;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (k + e < c.K) v[e >> 1] |= uint32_t(__ldg(src + e)) << (16 * (e & 1));
-      }
-      sts_v4(st + r * 128 + ((ch ^ (r & 7)) << 4), make_uint4(v[0], v[1], v[2], v[3]));
-    }
+  static __device__ __forceinline__ void issue(Cursor& c, uint32_t st, uint32_t bar) {
+    box_copy(st, c.map, c.col, c.row, bar);
     c.col += kCols;
   }
   // A stage times x: lane (g, t) holds columns 16 t .. 16 t + 15 of rows g,
@@ -384,6 +371,98 @@ struct BfSrc {
           mma_bf16_k16(acc[m][nt], wg.x, wh.x, wg.y, wh.y, x.b[nt][4 * h], x.b[nt][4 * h + 1]);
           mma_bf16_k16(acc[m][nt], wg.z, wh.z, wg.w, wh.w, x.b[nt][4 * h + 2], x.b[nt][4 * h + 3]);
         }
+      }
+    }
+  }
+};
+
+// Any row length and any 2-byte aligned base, in 4-byte asynchronous copies: row
+// r's stage has the 33 words that cover its 64 columns from the word boundary at
+// or before the first, a lane a word, at a pitch of 36 words; word 34 is the
+// number of columns before the row's end, word 35 whether the row starts in the
+// middle of a word, which the reader then undoes.  Lane t of a quad takes the
+// words 4 i + t (i = 0..7): no two lanes of a warp meet in a bank.  x and h are
+// kept in the same order, word 4 i + t of 64 columns at 8 t + i (bf_place).
+// (Element loads of the same shape: 1556 x 2014 x 14 experts, 15 tokens, 321 ->
+// 118 us.)
+__host__ __device__ __forceinline__ uint32_t bf_place(uint32_t c) {  // of column c, in columns
+  const uint32_t w = (c & 63) >> 1;
+  return (c & ~63u) | ((w & 3) << 4) | ((w >> 2) << 1) | (c & 1);
+}
+template <>
+struct BfSrc<false> {
+  static constexpr int NG = 0;
+  static constexpr int kCols = kBfCols;
+  static constexpr uint32_t kPitch = 144, kStage = 32 * kPitch;
+  static constexpr bool kCopies = false;
+  struct Cursor {
+    const uint16_t* w;   // the matrix
+    uint64_t n, row;     // its values; first row of the tile
+    uint32_t K, col;
+  };
+  static __device__ __forceinline__ Cursor at(const CUtensorMap*, const uint16_t* w, uint64_t rows, uint64_t row,
+                                              uint32_t K, uint32_t col) {
+    return {w, rows * K, row, K, col};
+  }
+  // 4 bytes, of which `bytes` (0, 2 or 4) are read and the rest zero.
+  static __device__ __forceinline__ void copy4(uint32_t dst, uint64_t src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  }
+  static __device__ __forceinline__ void load(Cursor& c, uint32_t st, int lane) {
+    const uint64_t base = reinterpret_cast<uint64_t>(c.w), end = base + 2 * c.n;
+    uint64_t at = base + 2 * (c.row * c.K + c.col);
+    // the word of address a, as far as it lies in the matrix
+    auto word = [&](uint32_t dst, uint64_t a) {
+      if (a >= base) {
+        copy4(dst, a < end ? a : base, a >= end ? 0u : end - a < 4 ? uint32_t(end - a) : 4u);
+      } else {  // the first word of an unaligned matrix: its upper half
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(a + 2 < end && a + 2 >= base ? uint32_t(c.w[0]) << 16 : 0u)
+                     : "memory");
+      }
+    };
+    const uint64_t mine = at + uint64_t(lane) * 2 * c.K;  // row `lane`: its last word and its marks
+    word(st + lane * kPitch + 128, (mine & ~uint64_t(3)) + 128);
+    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(st + lane * kPitch + 136), "r"(c.K - c.col),
+                 "r"(uint32_t(mine >> 1) & 1u)
+                 : "memory");
+    const uint64_t row = 2 * uint64_t(c.K);
+    at += 4 * lane;
+    if ((at & ~uint64_t(3)) >= base && at + 31 * row + 4 <= end) {
+#pragma unroll 8
+      for (int r = 0; r < 32; ++r, at += row) copy4(st + r * kPitch + lane * 4, at & ~uint64_t(3), 4u);
+    } else {
+#pragma unroll 1
+      for (int r = 0; r < 32; ++r, at += row) word(st + r * kPitch + lane * 4, at & ~uint64_t(3));
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    c.col += kCols;
+  }
+  template <int NT>
+  static __device__ __forceinline__ void multiply(uint32_t st, int lane, const XQuarter<NT>& x,
+                                                  float (&acc)[2][NT][4]) {
+    const uint32_t g = uint32_t(lane) >> 2, t = uint32_t(lane) & 3;
+    const uint32_t cols = lds_u32(st + g * kPitch + 136), odd = lds_u32(st + g * kPitch + 140);  // 8 rows on: the same
+    const bool any = __any_sync(0xffffffffu, odd != 0u);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t a[4];  // rows g, g + 8 of word 2 j, then of word 2 j + 1
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const uint32_t i = 4 * (2 * j + (v >> 1)) + t, from = st + (16 * m + 8 * (v & 1) + g) * kPitch + i * 4;
+          a[v] = lds_u32(from);
+          if (any) a[v] = __funnelshift_r(a[v], lds_u32(from + 4), odd * 16);
+          if (cols < kBfCols) {  // past the row's end: the next row's values
+            if (2 * i >= cols)
+              a[v] = 0u;
+            else if (2 * i + 1 >= cols)
+              a[v] &= 0xFFFFu;
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_bf16_k16(acc[m][nt], a[0], a[1], a[2], a[3], x.b[nt][2 * j], x.b[nt][2 * j + 1]);
       }
     }
   }
@@ -419,6 +498,7 @@ struct Ring {
       ++left;
     } else {
       SRC::load(c, st, lane);
+      ++left;
     }
   }
   __device__ __forceinline__ void wait(int lane) {
@@ -432,7 +512,13 @@ struct Ring {
         --left;
       }
     } else {
-      __syncwarp();  // the other lanes' stores
+      // the lanes' copies in groups: the oldest of D, or all of fewer
+      if (left == D)
+        asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+      else
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      --left;
+      __syncwarp();
     }
   }
   __device__ __forceinline__ void give_up(int lane) {
@@ -450,7 +536,9 @@ struct Ring {
   }
   // Let what is in flight land without using it.
   __device__ __forceinline__ void abandon() {
-    if (SRC::kCopies && !dead) {
+    if constexpr (!SRC::kCopies) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    } else if (!dead) {
       dead = true;
       for (; left; --left) {
         bar_wait_long(bars + 8 * slot, parity);
