@@ -279,24 +279,15 @@ struct Q4Src {
     constexpr int RUNS = NG > NF ? NG : NF;    // runs per half: 8 / RUNS MMAs each
     constexpr int WIDE = NG > NF ? NF : NG;    // ranges of the coarser per half
     constexpr bool kTwo = RUNS > WIDE;
-    // the two half-tiles in turn: an MMA's latency (20 cycles) is then covered by
-    // the other chain's
-    uint32_t w[2][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const uint4 w4 = lds_v4(st + s * 2048 + (m * 2 + q) * 512 + lane * 16);
-      w[m][0] = w4.x;
-      w[m][1] = w4.y;
-      w[m][2] = w4.z;
-      w[m][3] = w4.w;
-    }
+      const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-    for (int ii = 0; ii < 4; ++ii) {
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
+      for (int ii = 0; ii < 4; ++ii) {
         const int i = 4 * q + ii;
         uint32_t a[4];
-        q4_operand(w[m][ii], magic, a);
+        q4_operand(w[ii], magic, a);
 #pragma unroll
         for (int n = 0; n < TILES; ++n) {
           if ((i * RUNS) % 8 == 0)
