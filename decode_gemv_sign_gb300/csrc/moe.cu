@@ -349,7 +349,7 @@ __device__ __forceinline__ void store_hidden(const MoeParams& p, uint32_t pair, 
   if constexpr (SRC::NG > 0) {
     const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu);
     const int k = record_exponent(m);
-    const float s = m >= 0x7F800000u ? __uint_as_float(0x7FFFFFFFu) : v * power_of_two(k);
+    const float s = v * power_of_two(k);
     const uint32_t run = ft & 3, t = uint32_t(lane) >> 3, i = 2 * run + ((uint32_t(lane) >> 2) & 1), e = lane & 3;
     uint16_t bits;
     asm("cvt.rn.f16.f32 %0, %1;" : "=h"(bits) : "f"(s));

@@ -161,7 +161,8 @@ __device__ __forceinline__ void q4_operand(uint32_t w, uint32_t magic, uint32_t 
 // all its bits; what is smaller errs by less than 2^-39 of it, far below what
 // fp32 sums of the record keep.  MMA i's operand of columns c .. c + 3 (see the
 // block's layout) is (x[c], x[c + 2]), (x[c + 1], x[c + 3]) at 128 (i / 4) + 32
-// t + 8 (i % 4).  A record with an infinity or a NaN becomes NaN.
+// t + 8 (i % 4).  An infinity or a NaN keeps its place (finite values beside it
+// lose bits, in sums that are not finite).
 //
 // Factors: NF per record, [record][NF][pitch] with one column per row of
 // activations, so that the rows' factors of a record share a line or two: NF =
@@ -175,7 +176,7 @@ constexpr uint32_t factor_pitch() { return NF == 1 ? 16 : 256; }
 // The scaling of values whose largest magnitude has the bits m.
 __device__ __forceinline__ int record_exponent(uint32_t m) {
   const int k = 14 - (int(m >> 23) - 127);
-  return m >= 0x7F800000u || m == 0u ? 0 : k > 120 ? 120 : k;
+  return m == 0u ? 0 : k > 120 ? 120 : k;
 }
 __device__ __forceinline__ float power_of_two(int k) { return __uint_as_float(uint32_t(127 + k) << 23); }
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
@@ -191,8 +192,7 @@ __device__ __forceinline__ void record_store(uint8_t* rec, float* factor, const 
   for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
   m = __reduce_max_sync(0xffffffffu, m);
   const int k = record_exponent(m);
-  // an infinity or a NaN anywhere: the whole record is NaN
-  const float up = m >= 0x7F800000u ? __uint_as_float(0x7FFFFFFFu) : power_of_two(k);
+  const float up = power_of_two(k);
   const uint32_t i = (uint32_t(lane) >> 3) * 2 + (uint32_t(lane) & 1), t = (uint32_t(lane) & 7) >> 1;
   *reinterpret_cast<uint2*>(rec + (i >> 2) * 128 + t * 32 + (i & 3) * 8) =
       make_uint2(half2_bits(v[0] * up, v[2] * up), half2_bits(v[1] * up, v[3] * up));

@@ -90,13 +90,19 @@ def scores(x, router, scoring):
     return s, s * (dl + 8 * EPS)
 
 
-def moe(x, gate, up, down, ids, weights):
+TWO_BF16 = 2.0 ** -16  # what holding a hidden value as two BF16 parts may lose of it: 2^-8 of 2^-8
+FP16 = 2.0 ** -11  # in fp16 under a power of two: 11 significant bits
+
+
+def moe(x, gate, up, down, ids, weights, held=TWO_BF16):
     """y [T, H] for a given choice and its weights, in 64 bits, and the fp32 kernel's error bound.
 
     gate, up [E, F, H] and down [E, H, F] are values; ids, weights [T, k].
-    The hidden values are held as two BF16 parts (an error of at most 2^-8 of
-    2^-8 of each), sums in fp32; y is rounded once to BF16, whose 8 significant
-    bits err by at most 2^-8 of a value (1 + 2^-8 rounds to 1).
+    The hidden values lose at most `held` of themselves between the products
+    (TWO_BF16 for BF16 experts, FP16 for 4-bit ones, where a value below 2^-31
+    of the largest of its 32 neighbours also errs by 2^-39 of that); sums are in
+    fp32; y is rounded once to BF16, whose 8 significant bits err by at most
+    2^-8 of a value (1 + 2^-8 rounds to 1).
     """
     xv = f64(x)
     T, H = xv.shape
@@ -109,7 +115,7 @@ def moe(x, gate, up, down, ids, weights):
             dg, du = eh * (np.abs(gate[e]) @ np.abs(xv[t])), eh * (np.abs(up[e]) @ np.abs(xv[t]))
             h = silu(g) * u
             # |silu'| <= 1.1
-            dh = 1.1 * dg * (np.abs(u) + du) + (np.abs(silu(g)) + 1.1 * dg) * du + (2.0 ** -16 + 16 * EPS) * np.abs(h)
+            dh = 1.1 * dg * (np.abs(u) + du) + (np.abs(silu(g)) + 1.1 * dg) * du + (held + 16 * EPS) * np.abs(h) + 2.0 ** -39 * np.abs(h).max()
             y[t] += v * (down[e] @ h)
             dy[t] += abs(v) * (np.abs(down[e]) @ (dh + ef * np.abs(h)))
     return y, dy + 2.0 ** -8 * (np.abs(y) + dy) + 1e-38

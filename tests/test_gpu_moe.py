@@ -38,6 +38,7 @@ class Layer:
         def draw(shape, sigma):
             return Q.bf16(rng.standard_normal(shape) * sigma)
 
+        self.held = Q.TWO_BF16 if form == "bf16" else Q.FP16
         self.x = draw((T, H), 1.0)
         self.router = draw((E, H), 2.0 / np.sqrt(H))
         ws = [draw((E, F, H), 1.0 / np.sqrt(H)), draw((E, F, H), 1.0 / np.sqrt(H)), draw((E, H, F), 1.0 / np.sqrt(F))]
@@ -83,7 +84,7 @@ def check(W, layer, k, scoring="softmax", bias=None, renormalize=True, factor=1.
         want, dw = factor * p, abs(factor) * (ds[rows, ids] + 4 * Q.EPS * p)
     assert (np.abs(weights - want) <= dw).all()
     # the layer's output for that choice and those weights
-    want, tol = Q.moe(x, *layer.values, ids, weights)
+    want, tol = Q.moe(x, *layer.values, ids, weights, layer.held)
     assert (np.abs(Q.f64(bits(y)) - want) <= tol).all()
     # the same bits again
     assert torch.equal(W.moe(xd, dev(layer.router), *layer.dev, k, **kw).view(torch.int16), y.view(torch.int16))
@@ -96,6 +97,52 @@ def check(W, layer, k, scoring="softmax", bias=None, renormalize=True, factor=1.
     (2, 130, 16, 96, 40), (16, 8, 2, 256, 512), (5, 12, 3, 1001, 333), (9, 7, 4, 520, 264), (1, 64, 8, 1024, 256)])
 def test_layer(W, T, E, k, H, F, form):
     check(W, Layer(W, T, E, H, F, form, seed=T + E + H), k)
+
+
+@pytest.mark.parametrize("T,E,k", [(16, 129, 3), (3, 256, 16), (7, 257, 8), (2, 300, 1), (16, 1024, 16)])
+def test_many_experts(W, T, E, k):
+    check(W, Layer(W, T, E, 72, 8, "bf16", seed=E), k)
+    rng = np.random.default_rng(E)
+    layer = Layer(W, T, E, 64, 8, 32, seed=E + 1)
+    check(W, layer, k, "sigmoid", rng.standard_normal(E).astype(np.float32))
+
+
+@pytest.mark.parametrize("form", ["bf16", 32, 128])
+@pytest.mark.parametrize("T,E,k,H,F", [(1, 2, 1, 8192, 40), (1, 2, 1, 40, 8200), (16, 2, 2, 4100, 32), (9, 3, 2, 33, 5001),
+                                       (16, 3, 3, 2048, 70)])
+def test_few_long_rows(W, T, E, k, H, F, form):
+    """Fewer tiles than thread blocks: their sums are cut along the rows and joined."""
+    check(W, Layer(W, T, E, H, F, form, seed=H + F), k)
+
+
+@pytest.mark.parametrize("H,F", [(64, 64), (40, 72), (1001, 333), (33, 35)])
+def test_what_is_not_chosen_is_not_read_into_the_sums(W, H, F):
+    """Experts that no token chose, and the rows next to a tile's edge, may hold anything."""
+    layer = Layer(W, 10, 5, H, F, "bf16", seed=H)
+    bias = np.array([0, -np.inf, 0, -np.inf, 0], np.float32)
+    for w in layer.dev:
+        w[1] = float("nan")
+        w[3] = float("inf")
+    check(W, layer, 3, "sigmoid", bias)
+    # one row of `down`: one column of y
+    row = H // 2
+    layer.dev[2][:, row] = float("nan")
+    y = W.moe(dev(layer.x), dev(layer.router), *layer.dev, 3, scoring="sigmoid", bias=torch.from_numpy(bias).cuda())
+    bad = torch.isnan(y)
+    assert bad[:, row].all() and bad.sum() == 10
+
+
+@pytest.mark.parametrize("form", ["bf16", 64])
+def test_infinite_hidden_values_keep_their_sign(W, form):
+    """A gate and an up row of large weights overflow one hidden value: y is what 64 bits call infinite."""
+    layer = Layer(W, 1, 1, 64, 64, "bf16", seed=2)
+    layer.x[:] = 0x3F80
+    w = [Q.bf16(np.clip(v, -0.5, 0.5)) for v in layer.values]
+    w[0][0, 5] = w[1][0, 5] = 0x7E00  # 64 of them: 2.7e39
+    w[2][:] = Q.bf16(np.where(np.arange(64) % 2, 0.5, -0.5))[None, :, None]
+    weights = [dev(a) if form == "bf16" else W.q4_encode(dev(a), form) for a in w]
+    y = W.moe(dev(layer.x), dev(layer.router), *weights, 1).float().cpu().numpy()[0]
+    assert (y == np.where(np.arange(64) % 2, np.inf, -np.inf)).all()
 
 
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])

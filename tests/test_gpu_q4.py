@@ -186,6 +186,55 @@ def test_gemv_infinite_and_nan_x_stay_in_their_row(W):
     assert torch.equal(y[keep], clean[keep])
 
 
+def test_gemv_infinite_x_has_the_weights_signs(W):
+    N, K, group = 40, 700, 64
+    codes = np.random.default_rng(3).integers(0, 16, (N, K)).astype(np.uint8)
+    scales = Q.bf16(np.full((N, -(-K // group)), 0.01))
+    c = W.q4_pack(torch.from_numpy(Q.pack_codes(codes)).cuda(), dev(scales).view(torch.bfloat16), K, group)
+    x = synth.gen_x_np(10, K, 9)
+    x[0, 130], x[9, 699] = 0x7F80, 0xFF80
+    y = W.q4_gemv(c, dev(x)).cpu().numpy()
+    for b, col, sign in ((0, 130, 1), (9, 699, -1)):
+        v = codes[:, col].astype(int) - 8
+        want = np.where(v == 0, np.nan, np.inf * sign * np.sign(v + (v == 0)))
+        assert np.array_equal(y[b], want.astype(np.float32), equal_nan=True)
+    assert np.isfinite(y[1:9]).all()
+
+
+@pytest.mark.parametrize("B", [1, 13])
+@pytest.mark.parametrize("shape", [(32, 40576), (257, 20000), (1000, 9001)])
+def test_gemv_of_few_long_rows(W, shape, B):
+    """Fewer tiles than thread blocks: their sums are cut along the rows and joined."""
+    N, K = shape
+    w = draw(N, K, seed=N)
+    for group in (32, 128):
+        c = W.q4_encode(dev(w), group)
+        x = synth.gen_x_np(B, K, B)
+        want, tol = Q.gemv(Q.q4_values(*Q.q4_encode(w, group), group), x, group)
+        y = W.q4_gemv(c, dev(x))
+        assert (np.abs(y.cpu().numpy() - want) <= tol).all()
+        assert torch.equal(W.q4_gemv(c, dev(x)), y)
+    W.device_check()
+
+
+@pytest.mark.parametrize("B", [1, 10])
+def test_gemv_of_x_over_a_wide_range(W, B):
+    """Magnitudes from 2^-100 to 2^100 in one row: a value keeps its 8 bits down to 2^-31 of the largest of its 128
+    columns, and errs by at most 2^-39 of that below."""
+    N, K, group = 70, 1100, 32
+    rng = np.random.default_rng(B)
+    w = draw(N, K, seed=77)
+    c = W.q4_encode(dev(w), group)
+    x = Q.bf16(rng.standard_normal((B, K)) * 2.0 ** rng.integers(-100, 101, (B, K)))
+    x[0, :128] = 0
+    v = Q.q4_values(*Q.q4_encode(w, group), group)
+    want, tol = Q.gemv(v, x, group)
+    xv = np.abs(Q.f64(x))
+    for k in range(0, K, 128):
+        tol = tol + 2.0 ** -39 * xv[:, k:k + 128].max(1, keepdims=True) * np.abs(v[:, k:k + 128]).sum(1)
+    assert (np.abs(W.q4_gemv(c, dev(x)).cpu().numpy() - want) <= tol).all()
+
+
 def test_calls_on_two_streams_do_not_disturb_each_other(W):
     """Split sums take their own counters and workspace per call."""
     N, K, B = 4096, 4096, 16
