@@ -359,7 +359,7 @@ __device__ __forceinline__ void store_hidden(const MoeParams& p, uint32_t pair, 
   } else {
     uint16_t hi, lo;
     split_bf16(v, hi, lo);
-    uint16_t* h = reinterpret_cast<uint16_t*>(p.h) + uint64_t(pair) * 2 * p.Fp + (SRC::kCopies ? row : bf_place(row));
+    uint16_t* h = reinterpret_cast<uint16_t*>(p.h) + uint64_t(pair) * 2 * p.Fp + row;
     h[0] = hi;
     h[p.Fp] = lo;
   }
@@ -481,7 +481,12 @@ __device__ __forceinline__ void load16(const uint16_t* row, uint32_t c, uint32_t
   for (int i = 0; i < 8; ++i) v[i] = 0u;
   if (!ok) return;
   if constexpr (VEC) {
-    if (c < n) ldg_v8(row + c, v);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (c + 8 * h < n) {
+        const uint4 u = *reinterpret_cast<const uint4*>(row + c + 8 * h);
+        v[4 * h] = u.x; v[4 * h + 1] = u.y; v[4 * h + 2] = u.z; v[4 * h + 3] = u.w;
+      }
   } else {
 #pragma unroll
     for (int e = 0; e < 16; ++e)
@@ -579,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
       uint16_t* out = reinterpret_cast<uint16_t*>(p.make);
       for (uint32_t i = first * 32 + lane; i < p.T * Hp; i += stride * 32) {
         const uint32_t b = i / Hp, c = i - b * Hp;
-        out[SRC::kCopies ? i : b * Hp + bf_place(c)] = c < p.H ? p.x[uint64_t(b) * p.H + c] : uint16_t(0);
+        out[i] = c < p.H ? p.x[uint64_t(b) * p.H + c] : uint16_t(0);
       }
     }
   }
@@ -878,7 +883,7 @@ extern "C" int wcomp_moe(const wcomp_moe_args* a, void* stream) {
   p.scoring = a->scoring;
   p.renorm = a->renormalize;
   p.factor = a->factor;
-  p.x_vec = p.H % 16 == 0 && aligned(a->d_x, 32) && aligned(a->d_router, 32);
+  p.x_vec = p.H % 8 == 0 && aligned(a->d_x, 16) && aligned(a->d_router, 16);
   MoeMaps maps;
   memset(&maps, 0, sizeof(maps));
   bool mapped = !q4;
@@ -893,7 +898,7 @@ extern "C" int wcomp_moe(const wcomp_moe_args* a, void* stream) {
   // x's form for the products: records, or BF16 rows of whole 64-column steps
   // that start on 32-byte boundaries
   const uint64_t Hp = q4 ? cdiv(p.H, kQ4Cols) * kQ4Cols : cdiv(p.H, kBfCols) * kBfCols;
-  const bool make = q4 || !mapped || Hp != p.H || !aligned(a->d_x, 32);
+  const bool make = q4 || Hp != p.H || !aligned(a->d_x, 32);
   p.xs_bytes = 2 * Hp;
   auto round = [](uint64_t b) { return (b + 255) & ~uint64_t(255); };
   const uint64_t pairs = uint64_t(p.T) * p.k;

@@ -378,61 +378,66 @@ struct BfSrc {
 
 // Any row length and any 2-byte aligned base, in 4-byte asynchronous copies: row
 // r's stage has the 33 words that cover its 64 columns from the word boundary at
-// or before the first, a lane a word, at a pitch of 36 words; word 34 is the
-// number of columns before the row's end, word 35 whether the row starts in the
-// middle of a word, which the reader then undoes.  Lane t of a quad takes the
-// words 4 i + t (i = 0..7): no two lanes of a warp meet in a bank.  x and h are
-// kept in the same order, word 4 i + t of 64 columns at 8 t + i (bf_place).
-// (Element loads of the same shape: 1556 x 2014 x 14 experts, 15 tokens, 321 ->
-// 118 us.)
-__host__ __device__ __forceinline__ uint32_t bf_place(uint32_t c) {  // of column c, in columns
-  const uint32_t w = (c & 63) >> 1;
-  return (c & ~63u) | ((w & 3) << 4) | ((w >> 2) << 1) | (c & 1);
-}
+// or before the first, a lane a word, at a pitch of 33 words, so that the lanes'
+// reads (eight words of their own, and the one after) meet no bank conflict.
+// After the rows stand the number of columns left to their end and which rows
+// start in the middle of a word: the reader undoes that, and clears in the stage
+// what lies past the rows' end.
+// (us with element loads / with both undone word by word / so: 15 tokens, 4 of 14
+// experts of 2014 x 1556: 321 / 118 / 97; 5 tokens, 3 of 12 of 1001 x 333: - / 33 /
+// 26, where 1000 x 328 takes 19 through boxes.)
 template <>
 struct BfSrc<false> {
   static constexpr int NG = 0;
   static constexpr int kCols = kBfCols;
-  static constexpr uint32_t kPitch = 144, kStage = 32 * kPitch;
+  static constexpr uint32_t kPitch = 132, kMarks = 32 * kPitch, kStage = kMarks + 16;
   static constexpr bool kCopies = false;
   struct Cursor {
-    const uint16_t* w;   // the matrix
-    uint64_t n, row;     // its values; first row of the tile
+    const uint16_t* w;    // the matrix
+    uint64_t rows, row;   // its rows; the first of the tile
     uint32_t K, col;
   };
   static __device__ __forceinline__ Cursor at(const CUtensorMap*, const uint16_t* w, uint64_t rows, uint64_t row,
                                               uint32_t K, uint32_t col) {
-    return {w, rows * K, row, K, col};
+    return {w, rows, row, K, col};
   }
   // 4 bytes, of which `bytes` (0, 2 or 4) are read and the rest zero.
   static __device__ __forceinline__ void copy4(uint32_t dst, uint64_t src, uint32_t bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
   }
   static __device__ __forceinline__ void load(Cursor& c, uint32_t st, int lane) {
-    const uint64_t base = reinterpret_cast<uint64_t>(c.w), end = base + 2 * c.n;
-    uint64_t at = base + 2 * (c.row * c.K + c.col);
-    // the word of address a, as far as it lies in the matrix
-    auto word = [&](uint32_t dst, uint64_t a) {
-      if (a >= base) {
-        copy4(dst, a < end ? a : base, a >= end ? 0u : end - a < 4 ? uint32_t(end - a) : 4u);
-      } else {  // the first word of an unaligned matrix: its upper half
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(a + 2 < end && a + 2 >= base ? uint32_t(c.w[0]) << 16 : 0u)
-                     : "memory");
-      }
-    };
-    const uint64_t mine = at + uint64_t(lane) * 2 * c.K;  // row `lane`: its last word and its marks
-    word(st + lane * kPitch + 128, (mine & ~uint64_t(3)) + 128);
-    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(st + lane * kPitch + 136), "r"(c.K - c.col),
-                 "r"(uint32_t(mine >> 1) & 1u)
-                 : "memory");
-    const uint64_t row = 2 * uint64_t(c.K);
-    at += 4 * lane;
-    if ((at & ~uint64_t(3)) >= base && at + 31 * row + 4 <= end) {
-#pragma unroll 8
-      for (int r = 0; r < 32; ++r, at += row) copy4(st + r * kPitch + lane * 4, at & ~uint64_t(3), 4u);
-    } else {
+    const uint64_t row = 2 * uint64_t(c.K), base = reinterpret_cast<uint64_t>(c.w), end = base + c.rows * row;
+    const uint64_t at = base + c.row * row + 2 * c.col, mine = at + lane * row;
+    auto word_of = [](uint64_t a) { return a & ~uint64_t(3); };
+    if (lane == 0)
+      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(st + kMarks), "r"(c.K - c.col),
+                   "r"((uint32_t(at >> 1) & 1u) | (c.K & 1u) << 1)
+                   : "memory");
+    // rows whose 33 words lie in the matrix, and the others that it has
+    const bool inside = word_of(mine) >= base && mine + 132 <= end;
+    const uint32_t rows = __ballot_sync(0xffffffffu, inside);
+    uint32_t rest = __ballot_sync(0xffffffffu, !inside && c.row + lane < c.rows);
+    if (inside) copy4(st + lane * kPitch + 128, word_of(mine) + 128, 4u);
+    const uint32_t dst = st + lane * 4;
+    uint64_t even = word_of(at) + 4 * lane, odd = word_of(at + row) + 4 * lane;  // two rows are whole words
+#pragma unroll
+    for (int r = 0; r < 32; r += 2, even += 2 * row, odd += 2 * row) {
+      if (rows >> r & 1) copy4(dst + r * kPitch, even, 4u);
+      if (rows >> r & 2) copy4(dst + (r + 1) * kPitch, odd, 4u);
+    }
+    // at the matrix's ends: each word as far as it lies in it
 #pragma unroll 1
-      for (int r = 0; r < 32; ++r, at += row) word(st + r * kPitch + lane * 4, at & ~uint64_t(3));
+    for (; rest; rest &= rest - 1) {
+      const uint32_t r = __ffs(rest) - 1;
+#pragma unroll 1
+      for (uint32_t i = lane; i < 33; i += 32) {
+        const uint64_t a = word_of(at + r * row) + 4 * i;
+        const uint32_t to = st + r * kPitch + i * 4;
+        if (a >= base)
+          copy4(to, a < end ? a : word_of(base) + 4, a >= end ? 0u : end - a < 4 ? uint32_t(end - a) : 4u);
+        else  // the first word of an unaligned matrix: its upper half
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(uint32_t(c.w[0]) << 16) : "memory");
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     c.col += kCols;
@@ -441,28 +446,36 @@ struct BfSrc<false> {
   static __device__ __forceinline__ void multiply(uint32_t st, int lane, const XQuarter<NT>& x,
                                                   float (&acc)[2][NT][4]) {
     const uint32_t g = uint32_t(lane) >> 2, t = uint32_t(lane) & 3;
-    const uint32_t cols = lds_u32(st + g * kPitch + 136), odd = lds_u32(st + g * kPitch + 140);  // 8 rows on: the same
-    const bool any = __any_sync(0xffffffffu, odd != 0u);
+    const uint32_t cols = lds_u32(st + kMarks), marks = lds_u32(st + kMarks + 4);
+    auto odd = [&](uint32_t r) { return (marks ^ (marks >> 1 & r)) & 1u; };  // row r starts in mid-word
+    if (cols < kBfCols) {
+      const uint32_t row = st + lane * kPitch, h = cols + odd(lane);
+      if (h & 1) asm volatile("st.shared.u16 [%0], %1;" ::"r"(row + h * 2), "h"(uint16_t(0)) : "memory");
+#pragma unroll 1
+      for (uint32_t i = (h + 1) >> 1; i < 33; ++i)
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(row + i * 4), "r"(0u) : "memory");
+      __syncwarp();
+    }
+    const uint32_t shift = odd(g) * 16;  // rows 8 apart start alike
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
+      const uint32_t sm = st + (16 * m + g) * kPitch + t * 32;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t a[4];  // rows g, g + 8 of word 2 j, then of word 2 j + 1
+      for (int h = 0; h < 2; ++h) {
+        uint32_t a[2][5];  // rows g and g + 8: four words and the one after
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const uint32_t i = 4 * (2 * j + (v >> 1)) + t, from = st + (16 * m + 8 * (v & 1) + g) * kPitch + i * 4;
-          a[v] = lds_u32(from);
-          if (any) a[v] = __funnelshift_r(a[v], lds_u32(from + 4), odd * 16);
-          if (cols < kBfCols) {  // past the row's end: the next row's values
-            if (2 * i >= cols)
-              a[v] = 0u;
-            else if (2 * i + 1 >= cols)
-              a[v] &= 0xFFFFu;
-          }
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int i = 0; i < 5; ++i) a[r][i] = lds_u32(sm + r * 8 * kPitch + (4 * h + i) * 4);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[r][i] = __funnelshift_r(a[r][i], a[r][i + 1], shift);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_bf16_k16(acc[m][nt], a[0][0], a[1][0], a[0][1], a[1][1], x.b[nt][4 * h], x.b[nt][4 * h + 1]);
+          mma_bf16_k16(acc[m][nt], a[0][2], a[1][2], a[0][3], a[1][3], x.b[nt][4 * h + 2], x.b[nt][4 * h + 3]);
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma_bf16_k16(acc[m][nt], a[0], a[1], a[2], a[3], x.b[nt][2 * j], x.b[nt][2 * j + 1]);
       }
     }
   }
