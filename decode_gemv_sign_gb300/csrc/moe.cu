@@ -693,7 +693,11 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
     // chosen experts, one expert after the other.
     {
       const uint32_t steps = uint32_t(cdiv(p.F, SRC::kCols));
-      const Cuts cuts(uint32_t(cdiv(p.H, kTileRows)), L.active * steps, gridDim.x, kJoinCopies);
+      // half of what a join costs elsewhere: a run of copies is longer here by each
+      // expert's beginning and end (us with whole / half the cost, 6 of 12 4-bit
+      // experts: 512 x 512, 4 tokens 20.6 / 18.7; 461 x 474, 16 tokens 30.9 / 28.3;
+      // with a quarter, 2 of 8 BF16 ones of 1024 x 512, 1 token: 13.7 -> 17.5)
+      const Cuts cuts(uint32_t(cdiv(p.H, kTileRows)), L.active * steps, gridDim.x, kJoinCopies / 2);
       // the cursor's place: ileft k-steps to expert ia's or the warp's end, irest
       // after those
       Parts ahead(cuts);

@@ -751,8 +751,15 @@ __device__ __forceinline__ void join_parts(const Cuts& c, const Parts& s, bool f
   const float* rest = part + 2 * uint64_t(first + 1) * n_max;
   for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) {
     float v = __ldcg(head + i);
-#pragma unroll 4
-    for (uint32_t q = 0; q < last - first; ++q) v += __ldcg(rest + 2 * uint64_t(q) * n_max + i);
+#pragma unroll 1
+    for (uint32_t q0 = 0; q0 < last - first; q0 += 16) {  // 16 loads in flight
+      float t[16];
+#pragma unroll
+      for (uint32_t q = 0; q < 16; ++q)
+        t[q] = q0 + q < last - first ? __ldcg(rest + 2 * uint64_t(q0 + q) * n_max + i) : 0.f;
+#pragma unroll
+      for (uint32_t q = 0; q < 16; ++q) v += t[q];
+    }
     store(i, v);
   }
   if (threadIdx.x == 0) counters[first] = 0u;
