@@ -64,7 +64,7 @@
 #include <new>
 #include <vector>
 
-#include "wcomp_impl.cuh"
+#include "host_shared.cuh"
 
 namespace wc {
 namespace {

@@ -28,9 +28,18 @@
 //      shared memory), and at the unit's end the warps' accumulators are added
 //      in order.
 //
-// Units of B (where there are few) and C are cut over the CTAs so that each
-// streams the same bytes (Cuts, tile.cuh).  Every sum has a fixed order:
+// Units of B and C are cut over the CTAs, where that pays for the joins, so that
+// each streams the same bytes (Cuts, tile.cuh).  Every sum has a fixed order:
 // results repeat bit for bit.
+//
+// Measured, us (in brackets the chosen weights' bytes at a plain copy's rate):
+// 8 of 128 experts of 6144 x 2048: one token BF16 108 (89), 4-bit with groups of
+// 128 50 (23), 16 tokens 4-bit with groups of 32 364 (258); 2 of 8 of 4096 x
+// 11008, 16 tokens, BF16 359 (316); 2 of 8 of 1024 x 512, one token 13.8 (0.9).
+// Large layers are bound by the stream.  Small ones by the chain of phases: of
+// one token's 50 us with 4-bit experts, 3.5 are the router, 1.5 each barrier,
+// 2.4 the choice and the lists, 4 the first copies of B and C, and 6 the last
+// CTAs of B, of which some have two units and some one.
 #include <string.h>
 
 #include <algorithm>

@@ -408,6 +408,16 @@ __global__ void __launch_bounds__(kThreads) q4_unpack_kernel(const __grid_consta
 // weights and only then waits for the records.  A unit is a tile of 32 rows,
 // whose k-steps the warps of a CTA share; the units' k-steps are cut over the
 // CTAs (Cuts).
+//
+// Measured on 16384 x 53248 (450 MB at groups of 128: 66 us at the rate of a
+// plain copy): 78.5 us for one row of x (0.84 of that rate), 80 for 4, 83 for 8,
+// 111 for 16; 89 and 129 for 8 and 16 rows at groups of 32.  Up to 8 rows what
+// is left is the start, the joins (5 us together) and the issue of some 120
+// instructions per KB, two thirds of them the codes' expansion.  At 16 rows no
+// unit is over half busy (tensor cores 42 %): the latency of twice the MMAs with
+// the 16 warps that 128 registers leave an SM.  x is not it (with all of it in
+// one line of L1 the time does not fall), nor are more warps (10 or 12 of a CTA
+// spill).
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) q4_x_kernel(const uint16_t* __restrict__ x, uint64_t K, uint32_t recs, uint32_t B,
                                                    uint8_t* __restrict__ out, float* __restrict__ factors) {
@@ -537,9 +547,9 @@ int launch_gemv(GemvArgs& p, const uint16_t* x, uint64_t K, int dev, cudaStream_
   const int per_sm = prepare_gemv<NG, TILES>(dev);
   if (per_sm < 0) return map_cuda(cudaGetLastError());
   const uint32_t ctas = std::min(uint32_t(per_sm * sm_count(dev)), kSlotWords);
-  // Measured, us with whole units / cut: 2048 x 6144 6.6 / 10.5, 6144 x 6144
-  // 9.7 / 13.3, 16384 x 6144 18.1 / 21.7, 16384 x 53248 85 / 79, 256 x 40576 (B
-  // = 7) 26 / 13.
+  // Measured, us with whole units / cut: 2048 x 6144 6.4 / 9.2, 6144 x 6144 9.0 /
+  // 12.3, 16384 x 6144 15.6 / 19.4, 16384 x 53248 85 / 79, 256 x 40576 (B = 7) 26 /
+  // 11.
   p.cuts = Cuts(p.cuts.units, p.cuts.steps, ctas, kJoinCopies);
   const int st = work_slot(dev, &p.counters, &p.err);
   if (st != WCOMP_OK) return st;

@@ -20,7 +20,7 @@
 // columns (records, below), which loses nothing.
 #pragma once
 
-#include "wcomp_impl.cuh"
+#include "host_shared.cuh"
 
 namespace wc {
 

@@ -412,16 +412,6 @@ cudaError_t pool_alloc(void** p, size_t bytes, cudaStream_t s);
 int sm_count(int device);
 uint64_t l2_size(int device);
 int map_cuda(cudaError_t e);
-// The driver's tensor-map encoder, reached through the runtime (no link against
-// the driver library); null where it is missing.
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn tensor_map_encoder();
 void count_launches(uint64_t k);
-// The expert and 4-bit kernels' error word on device `dev` (null before their
-// first use), and the reset of it and of their work counters (q4.cu).
-uint32_t* work_error_word(int dev);
-cudaError_t work_reset(int dev, cudaStream_t s);
 
 }  // namespace wc

@@ -10,7 +10,11 @@ Inputs, drawn on the device:
     larger than L2), or the first `--tensors` of them;
   * gemv / gemv_bf16: the first `--rows` rows of the 16384x53248 GEMV weight
     (all of them by default; 4096 rows are 436 MB of BF16), or with
-    `--dense12` the escape-free weight of the same shape.
+    `--dense12` the escape-free weight of the same shape;
+  * q4_encode / q4_decode / q4_gemv: the same rows in 4 bits with one scale per
+    `--group` columns;
+  * moe: a layer of `--experts` experts of 6144 x 2048, 8 of them a token, for
+    `--batch` tokens, its experts in 4 bits, or in BF16 with `--group 0`.
 The operation runs `--reps` times after the containers are built, one
 batched launch per repetition.  Exits non-zero if a decode is not bit-exact
 or a GEMV kernel reports an error.
@@ -34,6 +38,49 @@ def layer_specs(count: int):
     return synth.checkpoint_batch(0)[2:2 + count]
 
 
+def run_q4(W, a, w, x):
+    import torch
+
+    held = W.q4_encode(w, a.group)
+    for _ in range(a.reps):
+        if a.op == "q4_encode":
+            W.q4_encode(w, a.group).free()
+        elif a.op == "q4_decode":
+            W.q4_decode(held)
+        else:
+            W.q4_gemv(held, x)
+    torch.cuda.synchronize()
+    W.device_check()
+    (N, K), G = w.shape, a.group
+    codes = N * K // 2 + 2 * N * -(-K // G)
+    other = 2 * (K * a.batch) + 4 * N * a.batch if a.op == "q4_gemv" else 2 * N * K
+    print(json.dumps({"op": a.op, "algorithmic_bytes_per_rep": codes + other}))
+
+
+def run_moe(W, a, dev):
+    import torch
+
+    g = torch.Generator(device=dev)
+    g.manual_seed(1)
+    E, H, F, k = a.experts, 6144, 2048, 8
+
+    def draw(*shape):
+        return torch.empty(*shape, dtype=torch.bfloat16, device=dev).normal_(0, 0.02, generator=g)
+
+    x, router = draw(a.batch, H) * 50, draw(E, H)
+    experts = [draw(E, F, H), draw(E, F, H), draw(E, H, F)]
+    if a.group:
+        experts = [W.q4_encode(w, a.group) for w in experts]
+    ids = torch.empty(a.batch, k, dtype=torch.int32, device=dev)
+    for _ in range(a.reps):
+        W.moe(x, router, *experts, k, ids=ids)
+    torch.cuda.synchronize()
+    W.device_check()
+    one = 3 * (H * F // 2 + 2 * H * F // a.group) if a.group else 6 * H * F
+    print(json.dumps({"op": a.op, "algorithmic_bytes_per_rep":
+                      len(set(ids.flatten().tolist())) * one + 2 * E * H + 4 * a.batch * H}))
+
+
 def main():
     import torch
 
@@ -41,23 +88,30 @@ def main():
     from decode_gemv_sign_gb300 import wcomp as W
 
     ap = argparse.ArgumentParser()
-    ap.add_argument("--op", choices=["encode", "decode", "gemv", "gemv_bf16"], required=True)
+    ap.add_argument("--op", choices=["encode", "decode", "gemv", "gemv_bf16", "q4_encode", "q4_decode", "q4_gemv", "moe"],
+                    required=True)
     ap.add_argument("--scheme", choices=["bytesplit", "k15", "both"], default="bytesplit",
                     help="both: every tensor in both schemes, one batch (the benchmark's encode and decode)")
     ap.add_argument("--batch", type=int, default=1)
     ap.add_argument("--tensors", type=int, default=17)
     ap.add_argument("--rows", type=int, default=16384)
     ap.add_argument("--dense12", action="store_true")
+    ap.add_argument("--group", type=int, default=128)
+    ap.add_argument("--experts", type=int, default=16)
     ap.add_argument("--reps", type=int, default=3)
     a = ap.parse_args()
     build.build()
     dev = torch.device("cuda")
-    if a.op in ("gemv", "gemv_bf16"):
+    if a.op == "moe":
+        return run_moe(W, a, dev)
+    if a.op in ("gemv", "gemv_bf16", "q4_encode", "q4_decode", "q4_gemv"):
         base = synth.dense12_spec() if a.dense12 else synth.checkpoint_gemv_spec()
         specs = [dataclasses.replace(base, N=min(a.rows, base.N))]
     else:
         specs = layer_specs(a.tensors)
     ws = [synth.gen_weights_torch(s, dev) for s in specs]
+    if a.op.startswith("q4"):
+        return run_q4(W, a, ws[0], synth.gen_x_torch(a.batch, specs[0].K, 5, dev))
     if a.scheme == "both":
         specs = [s for s in specs for _ in (0, 1)]
         ws = [w for w in ws for _ in (0, 1)]

@@ -240,11 +240,13 @@ WCOMP_API int wcomp_gemv_batched(const wcomp_container* const* containers, const
 /*
  * Report and clear the device error words of the current device (the one
  * wcomp_gemv and the batched GEMVs use, the one in wcomp_gemv_noalloc's
- * static array, and the one of wcomp_moe's grid barriers).  A GEMV kernel whose bounded wait on its own tensor copies
- * runs out records it there and finishes without waiting instead of hanging;
- * its outputs are then undefined.  In a debug build (compiled with
- * WCOMP_DEBUG=1) the kernels also check their indexes before memory
- * accesses, skip an access that fails and record it.  Synchronizes `stream`.
+ * static array, and the one of wcomp_q4_gemv and wcomp_moe).  A kernel whose
+ * bounded wait on its own tensor copies, or on its other thread blocks, runs
+ * out records it there and finishes without waiting instead of hanging; its
+ * outputs are then undefined.  In a debug build (compiled with WCOMP_DEBUG=1)
+ * the kernels on containers and plain weights also check their indexes before
+ * memory accesses, skip an access that fails and record it.  Synchronizes
+ * `stream`.
  * Returns WCOMP_OK, WCOMP_ETIMEOUT or WCOMP_EBOUNDS.
  */
 WCOMP_API int wcomp_device_check(void* stream);
@@ -391,14 +393,18 @@ WCOMP_API int wcomp_q4_decode(const wcomp_q4* c, uint16_t* d_out, void* stream);
 /*
  * y[b, r] = sum_k x[b, k] * (c[r, k] - 8) * s[r, group of k], b < B, r < N, for
  * a weight of one matrix (M == 1).  d_x uint16[B*K] BF16 bits, 1 <= B <= 16;
- * d_y float[B*N], overwritten.  A group's sum of x * (c - 8) is exact products
- * in fp32 on the tensor cores, then scaled and added in fp32 (so a group's
- * sum must stay finite before its scale: |x| up to 2^110 is safe).  The order
- * of the sums is fixed: repeated calls give identical bits.  K % 16 != 0 or an
- * x not 32-byte aligned goes through a padded copy of x.  Memory: that copy
- * and, where rows are split over thread blocks, their parts come from the
- * library's stream-ordered pool for the duration of the call; work counters
- * live in a buffer allocated with cudaMalloc on first use per device.
+ * d_y float[B*N], overwritten.  Any alignment of d_x.
+ * Numbers: x is taken in blocks of 128 columns as fp16 under the power of two
+ * that its largest magnitude asks for.  A BF16 value keeps all its bits down to
+ * 2^-31 of that; smaller ones err by at most 2^-39 of it.  Products with c - 8
+ * are then exact and summed in fp32 on the tensor cores; a group's sum is scaled
+ * and added in fp32.  Infinities and NaN stay in their row of x and follow the
+ * definition (scale times magnitude of x below 2^128 elsewhere).  The order of
+ * the sums is fixed: repeated calls give identical bits.
+ * Memory: that form of x and, where rows are split over thread blocks, their
+ * parts come from the library's stream-ordered pool for the duration of the
+ * call; work counters live in a buffer allocated with cudaMalloc on first use
+ * per device.
  */
 WCOMP_API int wcomp_q4_gemv(const wcomp_q4* c, const uint16_t* d_x, int B, float* d_y, void* stream);
 
@@ -451,18 +457,22 @@ typedef struct {
  *   weight[t, j] = factor * score, divided by the chosen scores' sum if
  *   renormalize;
  *   y[t] = sum_j weight[t, j] * down_j (silu(gate_j x[t]) * (up_j x[t])).
- * Sums, scores and the hidden values between the products are kept to fp32
- * (hidden values as two BF16 parts, 16 significant bits); y is rounded once.
- * The order of the sums is fixed: repeated calls give identical bits.
+ * Sums and scores are in fp32.  The hidden values between the products are held
+ * as two BF16 parts (BF16 experts: 16 significant bits) or in fp16 under a power
+ * of two for each 32 of them (4-bit experts: 11 bits, an eighth of a step of the
+ * result; x as in wcomp_q4_gemv).  y is rounded once.  The order of the sums is
+ * fixed: repeated calls give identical bits.
  * 1 <= top_k <= min(E, 16), E <= 1024, H and F at most 2^24 (beyond:
- * WCOMP_EUNSUPPORTED).  BF16 experts with H % 8 == 0, F % 8 == 0 and 16-byte
- * aligned weights take the vector path, other shapes an element path with the
- * same results.
+ * WCOMP_EUNSUPPORTED).  Any alignment and widths; BF16 experts with H % 8 == 0,
+ * F % 8 == 0 and 16-byte aligned weights are copied in boxes through tensor
+ * maps, others in 4-byte words, with the same results to the order of a sum.
+ * Experts that no token chose are not read.
  * The kernel is launched cooperatively (its thread blocks meet at two grid
- * barriers).  A barrier's wait is bounded: if it runs out, the kernel finishes
- * with undefined outputs and wcomp_device_check reports WCOMP_ETIMEOUT.
- * Memory: logits, hidden values and, for unaligned x, a padded copy come from
- * the library's stream-ordered pool for the duration of the call.
+ * barriers).  Waits are bounded: if one runs out, the kernel finishes with
+ * undefined outputs and wcomp_device_check reports WCOMP_ETIMEOUT.
+ * Memory: logits, hidden values, parts of sums and (unless x can be read as it
+ * is) a copy of x come from the library's stream-ordered pool for the duration
+ * of the call.
  */
 WCOMP_API int wcomp_moe(const wcomp_moe_args* args, void* stream);
 
