@@ -919,8 +919,13 @@ extern "C" int wcomp_moe(const wcomp_moe_args* a, void* stream) {
                  b_hf = q4 ? round(uint64_t(p.Fp) / 32 * factor_pitch<4>() * 4) : 0,
                  b_part = uint64_t(2) * 2 * kMaxGrid * kPartFloats * sizeof(float),
                  b_x = make ? round(p.T * p.xs_bytes) : 0, b_xf = q4 ? round(Hp / kSub * factor_pitch<1>() * 4) : 0;
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if ((e = cudaStreamIsCapturing(s, &capture)) != cudaSuccess) return map_cuda(e);
+  int st = work_slot(dev, capture != cudaStreamCaptureStatusNone, &p.counters, &p.err);
+  if (st != WCOMP_OK) return st;
+  const uint64_t b_count = p.counters ? 0 : kSlotWords * sizeof(uint32_t);
   uint8_t* ws = nullptr;
-  e = pool_alloc(reinterpret_cast<void**>(&ws), b_log + b_h + b_hf + b_part + b_x + b_xf, s);
+  e = pool_alloc(reinterpret_cast<void**>(&ws), b_log + b_h + b_hf + b_part + b_x + b_xf + b_count, s);
   if (e != cudaSuccess) return map_cuda(e);
   uint8_t* at = ws;
   auto take = [&](uint64_t bytes) {
@@ -935,7 +940,10 @@ extern "C" int wcomp_moe(const wcomp_moe_args* a, void* stream) {
   p.make = make ? take(b_x) : nullptr;
   p.xf = reinterpret_cast<float*>(take(b_xf));
   p.xs = make ? p.make : reinterpret_cast<const uint8_t*>(a->d_x);
-  int st = work_slot(dev, &p.counters, &p.err);
+  if (!p.counters) {
+    p.counters = reinterpret_cast<uint32_t*>(take(b_count));
+    st = map_cuda(cudaMemsetAsync(p.counters, 0, b_count, s));
+  }
   if (st == WCOMP_OK) {
     if (!q4)
       st = mapped ? launch_moe<BfSrc<true>>(p, maps, dev, s) : launch_moe<BfSrc<false>>(p, maps, dev, s);

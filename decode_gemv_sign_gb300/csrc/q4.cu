@@ -420,8 +420,11 @@ __global__ void __launch_bounds__(kThreads) q4_unpack_kernel(const __grid_consta
 // spill).
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) q4_x_kernel(const uint16_t* __restrict__ x, uint64_t K, uint32_t recs, uint32_t B,
-                                                   uint8_t* __restrict__ out, float* __restrict__ factors) {
+                                                   uint8_t* __restrict__ out, float* __restrict__ factors,
+                                                   uint32_t* __restrict__ counters, uint32_t n_counters) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (blockIdx.x == 0)  // the joins' counters, for after the GEMV's wait
+    for (uint32_t j = threadIdx.x; j < n_counters; j += blockDim.x) counters[j] = 0u;
   const int lane = threadIdx.x & 31;
   const uint64_t i = uint64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (i >= uint64_t(B) * recs) return;
@@ -438,7 +441,7 @@ struct GemvArgs {
   const float* factors;
   float* y;
   float* part;          // 2 B rows-of-a-unit floats per CTA
-  uint32_t* counters;   // one per CTA, zero
+  uint32_t* counters;   // one per CTA, zero at the first join
   uint32_t* err;
   uint64_t N;
   Cuts cuts{1, 1, 1, 0};
@@ -521,10 +524,15 @@ __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_const
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-constexpr uint32_t kSlots = 256;
+// Counters: kSlots slots that launches take in turn, then kKept that captured
+// launches keep; after them the error word.
+constexpr uint64_t kSlots = 1024, kKept = 4096, kCounters = (kSlots + kKept) * kSlotWords;
+constexpr size_t kWorkBytes = (kCounters + 32) * sizeof(uint32_t);
 std::mutex g_mu;
-uint32_t* g_work[64] = {nullptr};  // kSlots x kSlotWords counters, then the error word
-std::atomic<uint32_t> g_rr{0};
+struct Work {
+  uint32_t* p = nullptr;
+  uint64_t turn = 0, kept = 0;
+} g_work[64];
 
 template <int NG, int TILES>
 int prepare_gemv(int dev) {
@@ -546,24 +554,27 @@ template <int NG, int TILES>
 int launch_gemv(GemvArgs& p, const uint16_t* x, uint64_t K, int dev, cudaStream_t s) {
   const int per_sm = prepare_gemv<NG, TILES>(dev);
   if (per_sm < 0) return map_cuda(cudaGetLastError());
-  const uint32_t ctas = std::min(uint32_t(per_sm * sm_count(dev)), kSlotWords);
+  const uint32_t ctas = uint32_t(per_sm * sm_count(dev));
   // Measured, us with whole units / cut: 2048 x 6144 6.4 / 9.2, 6144 x 6144 9.0 /
   // 12.3, 16384 x 6144 15.6 / 19.4, 16384 x 53248 85 / 79, 256 x 40576 (B = 7) 26 /
   // 11.
   p.cuts = Cuts(p.cuts.units, p.cuts.steps, ctas, kJoinCopies);
-  const int st = work_slot(dev, &p.counters, &p.err);
+  const int st = work_slot(dev, false, nullptr, &p.err);
   if (st != WCOMP_OK) return st;
   const uint32_t recs = 2 * p.cuts.steps;
   const uint64_t b_xq = uint64_t(p.B) * recs * kRecord, b_f = (recs * factor_pitch<1>() * 4 + 255) & ~uint64_t(255);
   const uint64_t b_part = p.cuts.split ? uint64_t(2) * p.cuts.grid * p.B * kTileRows * sizeof(float) : 0;
+  const uint32_t n_counters = p.cuts.split ? p.cuts.grid : 0;
   uint8_t* ws = nullptr;
-  cudaError_t e = pool_alloc(reinterpret_cast<void**>(&ws), b_xq + b_f + b_part, s);
+  cudaError_t e = pool_alloc(reinterpret_cast<void**>(&ws), b_xq + b_f + b_part + n_counters * sizeof(uint32_t), s);
   if (e != cudaSuccess) return map_cuda(e);
   p.xq = ws;
   float* factors = reinterpret_cast<float*>(ws + b_xq);
   p.factors = factors;
   p.part = reinterpret_cast<float*>(ws + b_xq + b_f);
-  q4_x_kernel<<<uint32_t(cdiv(uint64_t(p.B) * recs, 8)), 256, 0, s>>>(x, K, recs, uint32_t(p.B), ws, factors);
+  p.counters = reinterpret_cast<uint32_t*>(ws + b_xq + b_f + b_part);
+  q4_x_kernel<<<uint32_t(cdiv(uint64_t(p.B) * recs, 8)), 256, 0, s>>>(x, K, recs, uint32_t(p.B), ws, factors,
+                                                                     p.counters, n_counters);
   e = cudaGetLastError();
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
@@ -639,35 +650,38 @@ bool on_device(const wcomp_q4* c) {
 
 }  // namespace
 
-int work_slot(int dev, uint32_t** slot, uint32_t** err) {
+int work_slot(int dev, bool captured, uint32_t** slot, uint32_t** err) {
   if (dev < 0 || dev >= 64) return WCOMP_EUNSUPPORTED;
   std::lock_guard<std::mutex> g(g_mu);
-  if (!g_work[dev]) {
+  Work& w = g_work[dev];
+  if (!w.p) {
     uint32_t* p = nullptr;
-    const size_t bytes = (kSlots * kSlotWords + 32) * sizeof(uint32_t);
-    cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&p), bytes);
-    if (e == cudaSuccess) e = cudaMemset(p, 0, bytes);
+    cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&p), kWorkBytes);
+    if (e == cudaSuccess) e = cudaMemset(p, 0, kWorkBytes);
     if (e != cudaSuccess) {
       if (p) cudaFree(p);
       return map_cuda(e);
     }
-    g_work[dev] = p;
+    w.p = p;
   }
-  *slot = g_work[dev] + uint64_t(g_rr.fetch_add(1, std::memory_order_relaxed) % kSlots) * kSlotWords;
-  *err = g_work[dev] + kSlots * kSlotWords;
+  if (slot && captured)
+    *slot = w.kept < kKept ? w.p + (kSlots + w.kept++) * kSlotWords : nullptr;
+  else if (slot)
+    *slot = w.p + (w.turn++ % kSlots) * kSlotWords;
+  *err = w.p + kCounters;
   return WCOMP_OK;
 }
 
 uint32_t* work_error_word(int dev) {
   if (dev < 0 || dev >= 64) return nullptr;
   std::lock_guard<std::mutex> g(g_mu);
-  return g_work[dev] ? g_work[dev] + kSlots * kSlotWords : nullptr;
+  return g_work[dev].p ? g_work[dev].p + kCounters : nullptr;
 }
 
 cudaError_t work_reset(int dev, cudaStream_t s) {
   uint32_t* e = work_error_word(dev);
   if (!e) return cudaSuccess;
-  return cudaMemsetAsync(e - kSlots * kSlotWords, 0, (kSlots * kSlotWords + 32) * sizeof(uint32_t), s);
+  return cudaMemsetAsync(e - kCounters, 0, kWorkBytes, s);
 }
 
 }  // namespace wc

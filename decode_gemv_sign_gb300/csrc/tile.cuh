@@ -778,10 +778,12 @@ struct wcomp_q4 {
 };
 
 namespace wc {
-// Work counters of the 4-bit and expert kernels on the current device, and
-// their error word (defined in q4.cu).  A launch that joins cut units or
-// crosses a grid barrier takes a slot of kSlotWords zeroed counters, round
-// robin, and leaves them zero.
+// The 4-bit and expert kernels' error word on the current device, and kSlotWords
+// zero counters for a launch that crosses grid barriers (slot, unless null),
+// which it leaves zero: in turn, or, for a launch that is captured, for good,
+// since it may run next to any other as often as its graph does (null when
+// those are used up: the caller clears counters of its own, in the graph).
+// Defined in q4.cu.
 constexpr uint32_t kSlotWords = 1024;
-int work_slot(int dev, uint32_t** slot, uint32_t** err);
+int work_slot(int dev, bool captured, uint32_t** slot, uint32_t** err);
 }  // namespace wc

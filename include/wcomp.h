@@ -403,8 +403,8 @@ WCOMP_API int wcomp_q4_decode(const wcomp_q4* c, uint16_t* d_out, void* stream);
  * the sums is fixed: repeated calls give identical bits.
  * Memory: that form of x and, where rows are split over thread blocks, their
  * parts come from the library's stream-ordered pool for the duration of the
- * call; work counters live in a buffer allocated with cudaMalloc on first use
- * per device.
+ * call.  The device's error word is allocated with cudaMalloc on first use: make
+ * the first call before any stream capture.
  */
 WCOMP_API int wcomp_q4_gemv(const wcomp_q4* c, const uint16_t* d_x, int B, float* d_y, void* stream);
 
@@ -472,7 +472,10 @@ typedef struct {
  * undefined outputs and wcomp_device_check reports WCOMP_ETIMEOUT.
  * Memory: logits, hidden values, parts of sums and (unless x can be read as it
  * is) a copy of x come from the library's stream-ordered pool for the duration
- * of the call.
+ * of the call.  The counters of the barriers are one of 1024 sets, in turn,
+ * allocated with cudaMalloc on first use (20 MB; make the first call before any
+ * stream capture).  The first 4096 calls that are captured keep sets of their
+ * own; later ones clear their own in the graph, which takes it 4 us longer.
  */
 WCOMP_API int wcomp_moe(const wcomp_moe_args* args, void* stream);
 

@@ -313,6 +313,58 @@ def test_in_a_graph(W):
     W.device_check()
 
 
+def test_a_graph_next_to_many_calls(W):
+    """A captured call has counters of its own, whatever runs next to it."""
+    layer = Layer(W, 2, 16, 512, 256, 64, seed=31)
+    x, router = dev(layer.x), dev(layer.router)
+    want = W.moe(x, router, *layer.dev, 4)
+    c = W.q4_encode(torch.randn(64, 40000, device="cuda").bfloat16(), 64)  # rows cut and joined
+    v = torch.randn(2, 40000, device="cuda").bfloat16()
+    product = W.q4_gemv(c, v)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        y, z = torch.zeros_like(x), torch.zeros_like(product)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(10):
+                W.moe(x, router, *layer.dev, 4, y=y)
+                W.q4_gemv(c, v, z)
+        graphs.append((g, y, z, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    out = []
+    for i in range(120):
+        for g, y, z, s in graphs:
+            with torch.cuda.stream(s):
+                if i % 4 == 0:
+                    y.zero_()
+                    z.zero_()
+                g.replay()
+        out += [W.moe(x, router, *layer.dev, 4) for _ in range(10)] + [W.q4_gemv(c, v)]
+    torch.cuda.synchronize()
+    W.device_check()
+    assert all(torch.equal(o, want if o.shape == want.shape else product) for o in out)
+    for _, y, z, _ in graphs:
+        assert torch.equal(y, want) and torch.equal(z, product)
+
+
+def test_more_captured_calls_than_kept_counters(W):
+    layer = Layer(W, 1, 2, 8, 8, 32, seed=32)
+    x, router = dev(layer.x), dev(layer.router)
+    want = W.moe(x, router, *layer.dev, 1)
+    torch.cuda.synchronize()
+    for _ in range(11):
+        y = torch.zeros_like(x)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(400):
+                W.moe(x, router, *layer.dev, 1, y=y)
+        g.replay()
+        assert torch.equal(y, want)
+        del g
+    W.device_check()
+
+
 def test_refusals(W):
     T, E, H, F = 2, 6, 64, 32
     x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
