@@ -403,9 +403,10 @@ __global__ void __launch_bounds__(kThreads) q4_unpack_kernel(const __grid_consta
 }
 
 // ---------------------------------------------------------------------------
-// GEMV.  A first kernel turns x into records (record_store).  The second is
-// launched to start before the first has ended: it fills its rings with
-// weights and only then waits for the records.  A unit is a tile of 32 rows,
+// GEMV.  x becomes records (record_store): where they are few, in every block's
+// shared memory, while its first weights are on their way; otherwise by a kernel
+// of their own, before the end of which the GEMV is launched, to fill its rings
+// with weights and only then wait for the records.  A unit is a tile of 32 rows,
 // whose k-steps the warps of a CTA share; the units' k-steps are cut over the
 // CTAs (Cuts).
 //
@@ -437,7 +438,9 @@ __global__ void __launch_bounds__(256) q4_x_kernel(const uint16_t* __restrict__ 
 
 struct GemvArgs {
   const uint8_t* w;
-  const uint8_t* xq;    // [B][2 * steps] records
+  const uint16_t* x;    // records in shared memory: x[B, K]
+  uint64_t K;
+  const uint8_t* xq;    // records in memory: [B][2 * steps]
   const float* factors;
   float* y;
   float* part;          // 2 B rows-of-a-unit floats per CTA
@@ -450,12 +453,21 @@ struct GemvArgs {
 
 constexpr int kDepth = 2;  // stages of a warp: a third takes L1 from the activations (16384 x 53248, B = 16: 126 -> 147 us)
 
-template <int NG, int TILES>
+// Records in shared memory: at most eight a warp, rows 16 bytes further apart
+// than their records, for the banks, then the factors.  For up to 8 rows of x
+// and no more units than blocks.  us on the GPU / on the host for a kernel of
+// its own, and so: 2048 x 6144 6.4 / 6.7, 5.9 / 4.4; 1024 x 4096 4.9 / 6.7, 4.6 /
+// 4.4; 6144 x 6144 9.0 / 6.7, 9.4 / 4.3; with more units than blocks, 16384 x
+// 6144 15.7 / 6.7, 16.4 / 4.3.
+constexpr uint32_t kXRecords = 8 * kWarps;
+constexpr uint32_t kXShared = kXRecords * (kRecord + 16 + factor_pitch<1>() * 4);
+
+template <int NG, int TILES, bool SHARED>
 constexpr uint32_t q4_smem() {
-  return kWarps * (kDepth * Q4Src<NG>::kStage + 2 * TILES * 512 + kDepth * 8) + 128;
+  return kWarps * (kDepth * Q4Src<NG>::kStage + 2 * TILES * 512 + kDepth * 8) + 128 + (SHARED ? kXShared : 0);
 }
 
-template <int NG, int TILES>
+template <int NG, int TILES, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_constant__ GemvArgs p) {
   using S = Q4Src<NG>;
   const uint32_t magic = q4_magic();
@@ -489,10 +501,45 @@ __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_const
   enter();
 #pragma unroll
   for (int i = 0; i < kDepth; ++i) issue(i);
-  const uint64_t row_bytes = uint64_t(2) * p.cuts.steps * kRecord;
-  const XRows<TILES> x = x_rows<TILES>(uint32_t(p.B), lane, [&](uint32_t b) { return p.xq + b * row_bytes; },
-                                         [&](uint32_t b) { return p.factors + b; });
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the records are there
+  // records in shared memory, or from memory
+  uint8_t* const xs = reinterpret_cast<uint8_t*>(part + kWarps * 2 * TILES * 128) + kWarps * kDepth * 8;
+  const uint32_t recs = 2 * p.cuts.steps;
+  const uint64_t pitch = SHARED ? recs * kRecord + 16 : recs * uint64_t(kRecord);
+  const uint8_t* const rows = SHARED ? xs : p.xq;
+  float* const fs = reinterpret_cast<float*>(xs + p.B * pitch);
+  const float* const factors = SHARED ? fs : p.factors;
+  if constexpr (SHARED) {
+    const uint32_t n = p.B * recs;
+    const bool words = p.K % 4 == 0 && (reinterpret_cast<uintptr_t>(p.x) & 7) == 0;
+    uint2 v[8];  // all of a warp's records in flight
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t i = warp + j * kWarps, b = i / recs, k = (i - b * recs) * kSub + 4 * lane;
+      const uint16_t* from = p.x + uint64_t(b) * p.K + k;
+      v[j] = make_uint2(0u, 0u);
+      if (i < n && k < p.K) {
+        if (words) {
+          v[j] = *reinterpret_cast<const uint2*>(from);
+        } else {
+          const uint32_t left = uint32_t(p.K) - k;
+          v[j].x = from[0] | (left > 1 ? uint32_t(from[1]) << 16 : 0u);
+          v[j].y = (left > 2 ? uint32_t(from[2]) : 0u) | (left > 3 ? uint32_t(from[3]) << 16 : 0u);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t i = warp + j * kWarps, b = i / recs, rec = i - b * recs;
+      if (i < n) {
+        const float f[4] = {bf16_lo(v[j].x), bf16_hi(v[j].x), bf16_lo(v[j].y), bf16_hi(v[j].y)};
+        record_store(xs + b * pitch + rec * kRecord, fs + rec * factor_pitch<1>() + b, f, lane);
+      }
+    }
+    __syncthreads();
+  }
+  const XRows<TILES> x = x_rows<TILES>(uint32_t(p.B), lane, [&](uint32_t b) { return rows + b * pitch; },
+                                       [&](uint32_t b) { return factors + b; });
+  if constexpr (!SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");  // the records are there
   const uint32_t outs = kTileRows * p.B;
   bool first_part = true;
   for (Parts s(p.cuts); s.more(); s.next(), first_part = false) {
@@ -500,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_const
     float acc[2][TILES][4];
     zero<TILES>(acc);
     if (w0 < w1) {
-      Product<S, TILES, 1> prod;
+      Product<S, TILES, 1, SHARED> prod;
       prod.begin(x, w0);
       for (uint32_t k = w0; k < w1; ++k) prod.step(ring, k, k + 1 < w1 ? k + 1 : k, lane, magic, x, acc, issue);
     }
@@ -534,13 +581,13 @@ struct Work {
   uint64_t turn = 0, kept = 0;
 } g_work[64];
 
-template <int NG, int TILES>
+template <int NG, int TILES, bool SHARED>
 int prepare_gemv(int dev) {
   static std::atomic<int> cache[64];
   int per_sm = cache[dev].load(std::memory_order_acquire);
   if (!per_sm) {
-    auto kern = q4_gemv_kernel<NG, TILES>;
-    constexpr uint32_t smem = q4_smem<NG, TILES>();
+    auto kern = q4_gemv_kernel<NG, TILES, SHARED>;
+    constexpr uint32_t smem = q4_smem<NG, TILES, SHARED>();
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess) return -1;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, smem) != cudaSuccess ||
         per_sm < 1)
@@ -550,53 +597,63 @@ int prepare_gemv(int dev) {
   return per_sm;
 }
 
-template <int NG, int TILES>
-int launch_gemv(GemvArgs& p, const uint16_t* x, uint64_t K, int dev, cudaStream_t s) {
-  const int per_sm = prepare_gemv<NG, TILES>(dev);
+template <int NG, int TILES, bool SHARED>
+int launch_gemv(GemvArgs& p, int dev, cudaStream_t s) {
+  const int per_sm = prepare_gemv<NG, TILES, SHARED>(dev);
   if (per_sm < 0) return map_cuda(cudaGetLastError());
   const uint32_t ctas = uint32_t(per_sm * sm_count(dev));
   // Measured, us with whole units / cut: 2048 x 6144 6.4 / 9.2, 6144 x 6144 9.0 /
   // 12.3, 16384 x 6144 15.6 / 19.4, 16384 x 53248 85 / 79, 256 x 40576 (B = 7) 26 /
   // 11.
-  p.cuts = Cuts(p.cuts.units, p.cuts.steps, ctas, kJoinCopies);
+  const Cuts cuts(p.cuts.units, p.cuts.steps, ctas, kJoinCopies);
+  if (SHARED && (cuts.split || cuts.units > ctas)) return launch_gemv<NG, TILES, false>(p, dev, s);
+  p.cuts = cuts;
   const int st = work_slot(dev, false, nullptr, &p.err);
   if (st != WCOMP_OK) return st;
-  const uint32_t recs = 2 * p.cuts.steps;
-  const uint64_t b_xq = uint64_t(p.B) * recs * kRecord, b_f = (recs * factor_pitch<1>() * 4 + 255) & ~uint64_t(255);
-  const uint64_t b_part = p.cuts.split ? uint64_t(2) * p.cuts.grid * p.B * kTileRows * sizeof(float) : 0;
-  const uint32_t n_counters = p.cuts.split ? p.cuts.grid : 0;
-  uint8_t* ws = nullptr;
-  cudaError_t e = pool_alloc(reinterpret_cast<void**>(&ws), b_xq + b_f + b_part + n_counters * sizeof(uint32_t), s);
-  if (e != cudaSuccess) return map_cuda(e);
-  p.xq = ws;
-  float* factors = reinterpret_cast<float*>(ws + b_xq);
-  p.factors = factors;
-  p.part = reinterpret_cast<float*>(ws + b_xq + b_f);
-  p.counters = reinterpret_cast<uint32_t*>(ws + b_xq + b_f + b_part);
-  q4_x_kernel<<<uint32_t(cdiv(uint64_t(p.B) * recs, 8)), 256, 0, s>>>(x, K, recs, uint32_t(p.B), ws, factors,
-                                                                     p.counters, n_counters);
-  e = cudaGetLastError();
-  if (e == cudaSuccess) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.cuts.grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = q4_smem<NG, TILES>();
-    cfg.stream = s;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, q4_gemv_kernel<NG, TILES>, p);
-    count_launches(2);
+  constexpr uint32_t smem = q4_smem<NG, TILES, SHARED>();
+  if constexpr (SHARED) {
+    q4_gemv_kernel<NG, TILES, SHARED><<<p.cuts.grid, kThreads, smem, s>>>(p);
+    count_launches(1);
+    return map_cuda(cudaGetLastError());
+  } else {
+    const uint32_t recs = 2 * p.cuts.steps;
+    const uint64_t b_xq = uint64_t(p.B) * recs * kRecord, b_f = (recs * factor_pitch<1>() * 4 + 255) & ~uint64_t(255);
+    const uint64_t b_part = p.cuts.split ? uint64_t(2) * p.cuts.grid * p.B * kTileRows * sizeof(float) : 0;
+    const uint32_t n_counters = p.cuts.split ? p.cuts.grid : 0;
+    uint8_t* ws = nullptr;
+    cudaError_t e = pool_alloc(reinterpret_cast<void**>(&ws), b_xq + b_f + b_part + n_counters * sizeof(uint32_t), s);
+    if (e != cudaSuccess) return map_cuda(e);
+    p.xq = ws;
+    float* factors = reinterpret_cast<float*>(ws + b_xq);
+    p.factors = factors;
+    p.part = reinterpret_cast<float*>(ws + b_xq + b_f);
+    p.counters = reinterpret_cast<uint32_t*>(ws + b_xq + b_f + b_part);
+    q4_x_kernel<<<uint32_t(cdiv(uint64_t(p.B) * recs, 8)), 256, 0, s>>>(p.x, p.K, recs, uint32_t(p.B), ws, factors,
+                                                                       p.counters, n_counters);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(p.cuts.grid);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = smem;
+      cfg.stream = s;
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr.val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      e = cudaLaunchKernelEx(&cfg, q4_gemv_kernel<NG, TILES, SHARED>, p);
+      count_launches(2);
+    }
+    cudaFreeAsync(ws, s);
+    return map_cuda(e);
   }
-  cudaFreeAsync(ws, s);
-  return map_cuda(e);
 }
 
 template <int NG>
-int dispatch_gemv(GemvArgs& p, const uint16_t* x, uint64_t K, int dev, cudaStream_t s) {
-  return p.B <= 8 ? launch_gemv<NG, 1>(p, x, K, dev, s) : launch_gemv<NG, 2>(p, x, K, dev, s);
+int dispatch_gemv(GemvArgs& p, int dev, cudaStream_t s) {
+  if (p.B <= 8 && uint64_t(p.B) * p.cuts.steps * 2 <= kXRecords) return launch_gemv<NG, 1, true>(p, dev, s);
+  return p.B <= 8 ? launch_gemv<NG, 1, false>(p, dev, s) : launch_gemv<NG, 2, false>(p, dev, s);
 }
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -780,10 +837,11 @@ extern "C" int wcomp_q4_gemv(const wcomp_q4* c, const uint16_t* d_x, int B, floa
   p.cuts.steps = uint32_t(c->blocks);
   p.cuts.units = uint32_t(c->tiles);
   p.B = B;
-  const int st = c->ng == 1   ? dispatch_gemv<1>(p, d_x, uint64_t(c->K), c->device, s)
-                 : c->ng == 2 ? dispatch_gemv<2>(p, d_x, uint64_t(c->K), c->device, s)
-                              : dispatch_gemv<4>(p, d_x, uint64_t(c->K), c->device, s);
-  return st;
+  p.x = d_x;
+  p.K = uint64_t(c->K);
+  return c->ng == 1   ? dispatch_gemv<1>(p, c->device, s)
+         : c->ng == 2 ? dispatch_gemv<2>(p, c->device, s)
+                      : dispatch_gemv<4>(p, c->device, s);
 }
 
 extern "C" int wcomp_q4_info(const wcomp_q4* c, wcomp_q4_info_t* info) {

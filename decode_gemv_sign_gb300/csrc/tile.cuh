@@ -222,16 +222,26 @@ __device__ __forceinline__ XRows<TILES> x_rows(uint32_t R, int lane, ROW row, CO
   return x;
 }
 
-// 64 columns of every row, from byte `at` of the rows.
-template <int TILES>
+// 64 columns of every row, from byte `at` of the rows.  SHARED: x's records and
+// factors are in shared memory.
+template <int TILES, bool SHARED = false>
 struct XQuarter {
   uint32_t b[TILES][8];
   __device__ __forceinline__ void load(const XRows<TILES>& x, uint64_t at) {
 #pragma unroll
-    for (int n = 0; n < TILES; ++n) ldg_v8(x.x[n] + at, b[n]);
+    for (int n = 0; n < TILES; ++n) {
+      if constexpr (SHARED) {
+        const uint4* p = reinterpret_cast<const uint4*>(x.x[n] + uint32_t(at));
+        const uint4 lo = p[0], hi = p[1];
+        b[n][0] = lo.x; b[n][1] = lo.y; b[n][2] = lo.z; b[n][3] = lo.w;
+        b[n][4] = hi.x; b[n][5] = hi.y; b[n][6] = hi.z; b[n][7] = hi.w;
+      } else {
+        ldg_v8(x.x[n] + at, b[n]);
+      }
+    }
   }
 };
-template <int TILES, int NF>
+template <int TILES, int NF, bool SHARED = false>
 struct XFactors {
   float f[TILES][2][NF];
   __device__ __forceinline__ void load(const XRows<TILES>& x, uint32_t rec) {
@@ -241,7 +251,10 @@ struct XFactors {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < NF; ++j) f[n][i][j] = ldg_f(x.f[n][i] + at + j * factor_pitch<NF>());
+        for (int j = 0; j < NF; ++j) {
+          const float* p = x.f[n][i] + at + j * factor_pitch<NF>();
+          f[n][i][j] = SHARED ? *p : ldg_f(p);
+        }
   }
 };
 
@@ -271,9 +284,10 @@ struct Q4Src {
   // factor are summed in ga by the MMAs, then multiplied in fp32: by the finer of
   // scale and factor into gb, and gb by the coarser into acc where its range
   // ends, so that each step costs one fused multiply-add a value.
-  template <int TILES, int NF>
+  template <int TILES, int NF, bool SHARED>
   static __device__ __forceinline__ void quarter(uint32_t st, uint32_t s, int q, int lane, uint32_t magic,
-                                                 const XQuarter<TILES>& x, const XFactors<TILES, NF>& f,
+                                                 const XQuarter<TILES, SHARED>& x,
+                                                 const XFactors<TILES, NF, SHARED>& f,
                                                  float (&ga)[2][TILES][4], float (&gb)[2][TILES][4],
                                                  float (&acc)[2][TILES][4]) {
     constexpr int RUNS = NG > NF ? NG : NF;    // runs per half: 8 / RUNS MMAs each
@@ -574,10 +588,10 @@ struct Ring {
 // k-step of the stage after it.  Activations are loaded 64 columns ahead of
 // their use, factors 128: their latency (L2's, for a first touch) would
 // otherwise stand in every step.
-template <class SRC, int TILES, int NF>
+template <class SRC, int TILES, int NF, bool SHARED = false>
 struct Product {  // 4-bit
-  XQuarter<TILES> x0;
-  XFactors<TILES, NF> f;
+  XQuarter<TILES, SHARED> x0;
+  XFactors<TILES, NF, SHARED> f;
   __device__ __forceinline__ void begin(const XRows<TILES>& x, uint32_t k) {
     if (TILES == 1 || NF == 1) f.load(x, 2 * k);
     x0.load(x, uint64_t(2 * k) * kRecord);
@@ -593,17 +607,17 @@ struct Product {  // 4-bit
     for (uint32_t s = 0; s < 2; ++s) {
       const uint32_t rec = 2 * k + s, next = s ? 2 * kn : rec + 1;
       float ga[2][TILES][4], gb[2][TILES][4];
-      XQuarter<TILES> x1;
-      XFactors<TILES, NF> fn;
+      XQuarter<TILES, SHARED> x1;
+      XFactors<TILES, NF, SHARED> fn;
       constexpr bool kAhead = TILES == 1 || NF == 1;  // sixteen rows' four factors: no registers left to load ahead
       x1.load(x, uint64_t(rec) * kRecord + 128);
       if (kAhead)
         fn.load(x, next);
       else
         f.load(x, rec);
-      SRC::template quarter<TILES, NF>(st, s, 0, lane, magic, x0, f, ga, gb, acc);
+      SRC::template quarter<TILES, NF, SHARED>(st, s, 0, lane, magic, x0, f, ga, gb, acc);
       x0.load(x, uint64_t(next) * kRecord);
-      SRC::template quarter<TILES, NF>(st, s, 1, lane, magic, x1, f, ga, gb, acc);
+      SRC::template quarter<TILES, NF, SHARED>(st, s, 1, lane, magic, x1, f, ga, gb, acc);
       if (kAhead) f = fn;
     }
     __syncwarp();  // every lane has read the stage
@@ -612,7 +626,7 @@ struct Product {  // 4-bit
   }
 };
 template <bool MAP, int TILES, int NF>
-struct Product<BfSrc<MAP>, TILES, NF> {
+struct Product<BfSrc<MAP>, TILES, NF, false> {
   XQuarter<TILES> x0;
   __device__ __forceinline__ void begin(const XRows<TILES>& x, uint32_t k) { x0.load(x, uint64_t(k) * (2 * kBfCols)); }
   template <class RING, class ISSUE>

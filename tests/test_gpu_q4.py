@@ -201,6 +201,24 @@ def test_gemv_infinite_x_has_the_weights_signs(W):
     assert np.isfinite(y[1:9]).all()
 
 
+@pytest.mark.parametrize("off", [0, 1, 2, 4])
+@pytest.mark.parametrize("B,K", [(1, 8192), (1, 8193), (1, 8190), (8, 1024), (8, 1025), (3, 2559), (5, 1), (2, 258)])
+def test_gemv_around_the_most_x_that_blocks_prepare_themselves(W, B, K, off):
+    """Up to 64 blocks of 128 columns of x, from any alignment, with an infinity in its row and nowhere else."""
+    N, group = 100, 128
+    w = draw(N, K, seed=K)
+    c = W.q4_encode(dev(w), group)
+    x = synth.gen_x_np(B, K, B + off)
+    want, tol = Q.gemv(Q.q4_values(*Q.q4_encode(w, group), group), x, group)
+    buf = torch.full((B * K + off + 8,), 0x7F80, dtype=torch.int16, device="cuda")
+    view = buf[off:off + B * K].view(B, K)
+    view.copy_(dev(x))
+    assert (np.abs(W.q4_gemv(c, view).cpu().numpy() - want) <= tol).all()
+    view[B - 1, K - 1] = 0x7FC0
+    y = W.q4_gemv(c, view).cpu().numpy()
+    assert np.isnan(y[B - 1]).all() and (np.abs(y[:B - 1] - want[:B - 1]) <= tol[:B - 1]).all()
+
+
 @pytest.mark.parametrize("B", [1, 13])
 @pytest.mark.parametrize("shape", [(32, 40576), (257, 20000), (1000, 9001)])
 def test_gemv_of_few_long_rows(W, shape, B):
