@@ -34,7 +34,7 @@
 //
 // Measured, us (in brackets the chosen weights' bytes at a plain copy's rate):
 // 8 of 128 experts of 6144 x 2048: one token BF16 108 (89), 4-bit with groups of
-// 128 50 (23), 16 tokens 4-bit with groups of 32 364 (258); 2 of 8 of 4096 x
+// 128 50 (23), 16 tokens 4-bit with groups of 32 341 (258); 2 of 8 of 4096 x
 // 11008, 16 tokens, BF16 359 (316); 2 of 8 of 1024 x 512, one token 13.8 (0.9).
 // Large layers are bound by the stream.  Small ones by the chain of phases: of
 // one token's 50 us with 4-bit experts, 3.5 are the router, 1.5 each barrier,

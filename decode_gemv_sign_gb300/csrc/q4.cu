@@ -411,12 +411,13 @@ __global__ void __launch_bounds__(kThreads) q4_unpack_kernel(const __grid_consta
 // CTAs (Cuts).
 //
 // Measured on 16384 x 53248 (450 MB at groups of 128: 66 us at the rate of a
-// plain copy): 78.5 us for one row of x (0.84 of that rate), 80 for 4, 83 for 8,
-// 111 for 16; 89 and 129 for 8 and 16 rows at groups of 32.  Up to 8 rows what
-// is left is the start, the joins (5 us together) and the issue of some 120
-// instructions per KB, two thirds of them the codes' expansion.  At 16 rows no
-// unit is over half busy (tensor cores 42 %): the latency of twice the MMAs with
-// the 16 warps that 128 registers leave an SM.  x is not it (with all of it in
+// plain copy): 75.5 us for one row of x (0.88 of that rate), 77 for 4, 79.5 for
+// 8, 111 for 16; 86 and 129 for 8 and 16 rows at groups of 32.  Up to 8 rows what
+// is left is the start, the joins (5 us together) and each warp's chain through
+// some 120 instructions per KB, two thirds of them the codes' expansion: a k-step
+// takes a warp 1.0 us with 8 warps on half of the SMs, 1.6 with 16 on all, with
+// rings of any depth.  At 16 rows no unit is over half busy (tensor cores 42 %):
+// the latency of twice the MMAs with the 16 warps that 128 registers leave an SM.  x is not it (with all of it in
 // one line of L1 the time does not fall), nor are more warps (10 or 12 of a CTA
 // spill).
 // ---------------------------------------------------------------------------
@@ -602,9 +603,9 @@ int launch_gemv(GemvArgs& p, int dev, cudaStream_t s) {
   const int per_sm = prepare_gemv<NG, TILES, SHARED>(dev);
   if (per_sm < 0) return map_cuda(cudaGetLastError());
   const uint32_t ctas = uint32_t(per_sm * sm_count(dev));
-  // Measured, us with whole units / cut: 2048 x 6144 6.4 / 9.2, 6144 x 6144 9.0 /
-  // 12.3, 16384 x 6144 15.6 / 19.4, 16384 x 53248 85 / 79, 256 x 40576 (B = 7) 26 /
-  // 11.
+  // Measured, us with whole units / cut (before the halves of a step were
+  // unrolled): 2048 x 6144 6.4 / 9.2, 6144 x 6144 9.0 / 12.3, 16384 x 6144 15.6 /
+  // 19.4, 16384 x 53248 85 / 79, 256 x 40576 (B = 7) 26 / 11.
   const Cuts cuts(p.cuts.units, p.cuts.steps, ctas, kJoinCopies);
   if (SHARED && (cuts.split || cuts.units > ctas)) return launch_gemv<NG, TILES, false>(p, dev, s);
   p.cuts = cuts;

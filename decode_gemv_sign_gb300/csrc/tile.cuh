@@ -601,9 +601,10 @@ struct Product {  // 4-bit
                                        const XRows<TILES>& x, float (&acc)[2][TILES][4], ISSUE& issue) {
     const uint32_t st = ring.stage();
     ring.wait(lane);
-    // rolled: the kernels that use this have several products in them, and
-    // their code has to stay in the instruction caches
-#pragma unroll 1
+    // unrolled, where registers allow, for the scheduler to find independent
+    // work: a warp's own chain of dependencies is what bounds a step (us rolled /
+    // unrolled: 16384 x 53248, B = 1 78.5 / 75.6; two tiles, which spill: 111 / 117)
+#pragma unroll (TILES == 1 ? 2 : 1)
     for (uint32_t s = 0; s < 2; ++s) {
       const uint32_t rec = 2 * k + s, next = s ? 2 * kn : rec + 1;
       float ga[2][TILES][4], gb[2][TILES][4];
