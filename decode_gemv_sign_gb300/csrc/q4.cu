@@ -407,8 +407,8 @@ __global__ void __launch_bounds__(kThreads) q4_unpack_kernel(const __grid_consta
 // shared memory, while its first weights are on their way; otherwise by a kernel
 // of their own, before the end of which the GEMV is launched, to fill its rings
 // with weights and only then wait for the records.  A unit is a tile of 32 rows,
-// whose k-steps the warps of a CTA share; the units' k-steps are cut over the
-// CTAs (Cuts).
+// whose k-steps the warps of a CTA share; the units' k-steps fall on the CTAs as
+// plan() says.
 //
 // Measured on 16384 x 53248 (450 MB at groups of 128: 66 us at the rate of a
 // plain copy): 75.5 us for one row of x (0.88 of that rate), 77 for 4, 79.5 for
@@ -452,23 +452,38 @@ struct GemvArgs {
   int B;
 };
 
-constexpr int kDepth = 2;  // stages of a warp: a third takes L1 from the activations (16384 x 53248, B = 16: 126 -> 147 us)
+constexpr int kDepth = 2;  // stages of a warp: a third takes L1 from the activations (16384 x 53248, B = 16: 111 -> 130 us)
 
 // Records in shared memory: at most eight a warp, rows 16 bytes further apart
 // than their records, for the banks, then the factors.  For up to 8 rows of x
-// and no more units than blocks.  us on the GPU / on the host for a kernel of
+// and one part of a unit a block.  us on the GPU / on the host for a kernel of
 // its own, and so: 2048 x 6144 6.4 / 6.7, 5.9 / 4.4; 1024 x 4096 4.9 / 6.7, 4.6 /
 // 4.4; 6144 x 6144 9.0 / 6.7, 9.4 / 4.3; with more units than blocks, 16384 x
 // 6144 15.7 / 6.7, 16.4 / 4.3.
 constexpr uint32_t kXRecords = 8 * kWarps;
 constexpr uint32_t kXShared = kXRecords * (kRecord + 16 + factor_pitch<1>() * 4);
 
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A float of the cluster's CTA `rank` at the place that `a` has in this one.
+__device__ __forceinline__ float cluster_lds(uint32_t a, uint32_t rank) {
+  float v;
+  asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.f32 %0, [r];\n\t}"
+               : "=f"(v)
+               : "r"(a), "r"(rank)
+               : "memory");
+  return v;
+}
+
 template <int NG, int TILES, bool SHARED>
 constexpr uint32_t q4_smem() {
   return kWarps * (kDepth * Q4Src<NG>::kStage + 2 * TILES * 512 + kDepth * 8) + 128 + (SHARED ? kXShared : 0);
 }
 
-template <int NG, int TILES, bool SHARED>
+// SHARED: x's records in shared memory; TEAM: a unit is shared by a cluster.
+template <int NG, int TILES, bool SHARED, bool TEAM>
 __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_constant__ GemvArgs p) {
   using S = Q4Src<NG>;
   const uint32_t magic = q4_magic();
@@ -480,7 +495,9 @@ __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_const
   Ring<S, kDepth> ring(smem_u32(smem) + uint32_t(warp) * kDepth * S::kStage,
                        smem_u32(part + kWarps * 2 * TILES * 128) + uint32_t(warp) * kDepth * 8, p.err, lane);
   // The copy cursor runs kDepth k-steps ahead of the sums, across units.
-  Parts ahead(p.cuts);
+  Parts ahead(p.cuts, TEAM);
+  const uint32_t r0 = SHARED ? 2 * ahead.k0 : 0;  // first record of x
+  const uint32_t recs = SHARED ? 2 * (ahead.k1 - ahead.k0) : 2 * p.cuts.steps;
   uint32_t ileft = 0;
   typename S::Cursor it{};
   auto enter = [&]() {
@@ -504,7 +521,6 @@ __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_const
   for (int i = 0; i < kDepth; ++i) issue(i);
   // records in shared memory, or from memory
   uint8_t* const xs = reinterpret_cast<uint8_t*>(part + kWarps * 2 * TILES * 128) + kWarps * kDepth * 8;
-  const uint32_t recs = 2 * p.cuts.steps;
   const uint64_t pitch = SHARED ? recs * kRecord + 16 : recs * uint64_t(kRecord);
   const uint8_t* const rows = SHARED ? xs : p.xq;
   float* const fs = reinterpret_cast<float*>(xs + p.B * pitch);
@@ -515,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_const
     uint2 v[8];  // all of a warp's records in flight
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t i = warp + j * kWarps, b = i / recs, k = (i - b * recs) * kSub + 4 * lane;
+      const uint32_t i = warp + j * kWarps, b = i / recs, k = (r0 + i - b * recs) * kSub + 4 * lane;
       const uint16_t* from = p.x + uint64_t(b) * p.K + k;
       v[j] = make_uint2(0u, 0u);
       if (i < n && k < p.K) {
@@ -538,12 +554,13 @@ __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_const
     }
     __syncthreads();
   }
-  const XRows<TILES> x = x_rows<TILES>(uint32_t(p.B), lane, [&](uint32_t b) { return rows + b * pitch; },
-                                       [&](uint32_t b) { return factors + b; });
+  const XRows<TILES> x =
+      x_rows<TILES>(uint32_t(p.B), lane, [&](uint32_t b) { return rows + b * pitch - r0 * kRecord; },
+                    [&](uint32_t b) { return factors + b - r0 * factor_pitch<1>(); });
   if constexpr (!SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");  // the records are there
   const uint32_t outs = kTileRows * p.B;
   bool first_part = true;
-  for (Parts s(p.cuts); s.more(); s.next(), first_part = false) {
+  for (Parts s(p.cuts, TEAM); s.more(); s.next(), first_part = false) {
     const uint32_t w0 = s.w0(warp), w1 = s.w1(warp);
     float acc[2][TILES][4];
     zero<TILES>(acc);
@@ -561,7 +578,18 @@ __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_const
       const uint64_t r = uint64_t(s.unit) * kTileRows + o % kTileRows;
       if (r < p.N) p.y[uint64_t(o / kTileRows) * p.N + r] = v;
     };
-    if (s.whole()) {
+    if constexpr (TEAM) {  // the only part: the rings are idle, and their place takes its sums
+      float* const mine = reinterpret_cast<float*>(smem);
+      for (uint32_t o = threadIdx.x; o < outs; o += kThreads) mine[o] = value(o);
+      cluster_sync();
+      if (blockIdx.x == s.unit * p.cuts.team)  // the first CTA adds all, in their order
+        for (uint32_t o = threadIdx.x; o < outs; o += kThreads) {
+          float v = mine[o];
+          for (uint32_t r = 1; r < p.cuts.team; ++r) v += cluster_lds(smem_u32(mine + o), r);
+          store(o, v);
+        }
+      cluster_sync();  // they are read
+    } else if (s.whole()) {
       for (uint32_t o = threadIdx.x; o < outs; o += kThreads) store(o, value(o));
     } else {
       join_parts(p.cuts, s, first_part, p.part, outs, p.counters, outs, &s_flag, value, store);
@@ -582,12 +610,12 @@ struct Work {
   uint64_t turn = 0, kept = 0;
 } g_work[64];
 
-template <int NG, int TILES, bool SHARED>
+template <int NG, int TILES, bool SHARED, bool TEAM>
 int prepare_gemv(int dev) {
   static std::atomic<int> cache[64];
   int per_sm = cache[dev].load(std::memory_order_acquire);
   if (!per_sm) {
-    auto kern = q4_gemv_kernel<NG, TILES, SHARED>;
+    auto kern = q4_gemv_kernel<NG, TILES, SHARED, TEAM>;
     constexpr uint32_t smem = q4_smem<NG, TILES, SHARED>();
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess) return -1;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, smem) != cudaSuccess ||
@@ -598,24 +626,28 @@ int prepare_gemv(int dev) {
   return per_sm;
 }
 
-template <int NG, int TILES, bool SHARED>
+template <int NG, int TILES, bool SHARED, bool TEAM>
 int launch_gemv(GemvArgs& p, int dev, cudaStream_t s) {
-  const int per_sm = prepare_gemv<NG, TILES, SHARED>(dev);
-  if (per_sm < 0) return map_cuda(cudaGetLastError());
-  const uint32_t ctas = uint32_t(per_sm * sm_count(dev));
-  // Measured, us with whole units / cut (before the halves of a step were
-  // unrolled): 2048 x 6144 6.4 / 9.2, 6144 x 6144 9.0 / 12.3, 16384 x 6144 15.6 /
-  // 19.4, 16384 x 53248 85 / 79, 256 x 40576 (B = 7) 26 / 11.
-  const Cuts cuts(p.cuts.units, p.cuts.steps, ctas, kJoinCopies);
-  if (SHARED && (cuts.split || cuts.units > ctas)) return launch_gemv<NG, TILES, false>(p, dev, s);
-  p.cuts = cuts;
-  const int st = work_slot(dev, false, nullptr, &p.err);
+  if (prepare_gemv<NG, TILES, SHARED, TEAM>(dev) < 0) return map_cuda(cudaGetLastError());
+  int st = work_slot(dev, false, nullptr, &p.err);
   if (st != WCOMP_OK) return st;
-  constexpr uint32_t smem = q4_smem<NG, TILES, SHARED>();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.cuts.grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = q4_smem<NG, TILES, SHARED>();
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  if constexpr (TEAM) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = p.cuts.team;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
   if constexpr (SHARED) {
-    q4_gemv_kernel<NG, TILES, SHARED><<<p.cuts.grid, kThreads, smem, s>>>(p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, q4_gemv_kernel<NG, TILES, SHARED, TEAM>, p);
     count_launches(1);
-    return map_cuda(cudaGetLastError());
+    return map_cuda(e);
   } else {
     const uint32_t recs = 2 * p.cuts.steps;
     const uint64_t b_xq = uint64_t(p.B) * recs * kRecord, b_f = (recs * factor_pitch<1>() * 4 + 255) & ~uint64_t(255);
@@ -633,17 +665,10 @@ int launch_gemv(GemvArgs& p, int dev, cudaStream_t s) {
                                                                        p.counters, n_counters);
     e = cudaGetLastError();
     if (e == cudaSuccess) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(p.cuts.grid);
-      cfg.blockDim = dim3(kThreads);
-      cfg.dynamicSmemBytes = smem;
-      cfg.stream = s;
-      cudaLaunchAttribute attr;
-      attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      attr.val.programmaticStreamSerializationAllowed = 1;
-      cfg.attrs = &attr;
-      cfg.numAttrs = 1;
-      e = cudaLaunchKernelEx(&cfg, q4_gemv_kernel<NG, TILES, SHARED>, p);
+      attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+      ++cfg.numAttrs;
+      e = cudaLaunchKernelEx(&cfg, q4_gemv_kernel<NG, TILES, SHARED, TEAM>, p);
       count_launches(2);
     }
     cudaFreeAsync(ws, s);
@@ -651,10 +676,51 @@ int launch_gemv(GemvArgs& p, int dev, cudaStream_t s) {
   }
 }
 
+// How the units' k-steps fall on the CTAs: whole, cut anywhere and joined
+// through memory, or (up to 8 rows) shared by clusters of 2 to 8 and joined
+// through shared memory: by the longest CTA's run in k-steps, eight of which its
+// warps take at once, and by what else each costs.  us whole / cut / shared by
+// clusters: 2048 x 6144 5.4 / 8.8 / 5.7; 4096 x 4096, 8 rows 6.0 / 10.8 / 7.1; 512
+// x 8192, 3 rows - / 6.5 / 4.9; 2048 x 16384 12.3 / 11.7 / 8.8; 256 x 40576, 7 rows
+// 26 / 10.7 / 7.7; 6144 x 16384, 4 rows 17.1 / 18.0 / -; 16384 x 6144 15.2 / 18.7 /
+// -; 16384 x 53248 85 / 75.5 / -.
+constexpr uint32_t kCutCost = 40, kTeamCost = 16;  // k-steps; 8 are about 1 us
+constexpr uint32_t kXCost = 8;                     // the kernel for x
+bool x_shared(const Cuts& c, int B, uint32_t ctas) {  // one part a CTA, of few records
+  return B <= 8 && !c.split && c.units <= ctas && uint64_t(B) * 2 * cdiv32(c.steps, c.team) <= kXRecords;
+}
+Cuts plan(uint32_t units, uint32_t steps, int B, uint32_t ctas) {
+  auto at_once = [](uint64_t k) { return cdiv(k, kWarps) * kWarps; };
+  Cuts best(units, steps, ctas, kCutCost);
+  uint64_t cost = best.split ? at_once(cdiv(uint64_t(units) * steps, ctas)) + kCutCost
+                             : at_once(steps) * cdiv32(units, ctas);
+  cost += x_shared(best, B, ctas) ? 0 : kXCost;
+  for (uint32_t team = 2; B <= 8 && team <= 8 && team <= steps && uint64_t(units) * team <= ctas; team *= 2) {
+    Cuts c = best;
+    c.team = team;
+    c.split = 0;
+    c.grid = units * team;
+    const uint64_t with = at_once(cdiv32(steps, team)) + kTeamCost + (x_shared(c, B, ctas) ? 0 : kXCost);
+    if (with < cost) {
+      cost = with;
+      best = c;
+    }
+  }
+  return best;
+}
+
 template <int NG>
 int dispatch_gemv(GemvArgs& p, int dev, cudaStream_t s) {
-  if (p.B <= 8 && uint64_t(p.B) * p.cuts.steps * 2 <= kXRecords) return launch_gemv<NG, 1, true>(p, dev, s);
-  return p.B <= 8 ? launch_gemv<NG, 1, false>(p, dev, s) : launch_gemv<NG, 2, false>(p, dev, s);
+  const int per_sm = p.B <= 8 ? prepare_gemv<NG, 1, false, false>(dev) : prepare_gemv<NG, 2, false, false>(dev);
+  if (per_sm < 0) return map_cuda(cudaGetLastError());
+  const uint32_t ctas = uint32_t(per_sm * sm_count(dev));
+  p.cuts = plan(p.cuts.units, p.cuts.steps, p.B, ctas);
+  if (p.B > 8) return launch_gemv<NG, 2, false, false>(p, dev, s);
+  if (p.cuts.team > 1)
+    return x_shared(p.cuts, p.B, ctas) ? launch_gemv<NG, 1, true, true>(p, dev, s)
+                                       : launch_gemv<NG, 1, false, true>(p, dev, s);
+  return x_shared(p.cuts, p.B, ctas) ? launch_gemv<NG, 1, true, false>(p, dev, s)
+                                     : launch_gemv<NG, 1, false, false>(p, dev, s);
 }
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }

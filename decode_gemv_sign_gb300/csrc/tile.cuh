@@ -683,12 +683,13 @@ __device__ __forceinline__ float warp_sums(const float* part, int warps, uint32_
 // fall anywhere, so every CTA streams the same bytes; otherwise on whole units.
 // The part of a cut unit that a CTA holds goes to the workspace, and the CTA
 // that arrives last at the unit's counter adds the parts in the order of the
-// CTAs: the result does not depend on which one that is.
+// CTAs: the result does not depend on which one that is.  Or, where there are few
+// units, each is shared by a `team` of CTAs (a cluster), the k-steps evenly.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kJoinCopies = 24;  // what a join costs, in 4 KB copies of a CTA
 __host__ __device__ __forceinline__ uint32_t cdiv32(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
 struct Cuts {
-  uint32_t units, steps, split;
+  uint32_t units, steps, split, team = 1;
   uint32_t grid;        // CTAs that have work, at most one per k-step (split) or unit
   uint32_t quot, rem;   // pieces (k-steps or units) per CTA; the first rem CTAs take one more
   // Cut units anywhere where that shortens the longest CTA's run by more than a
@@ -717,7 +718,15 @@ struct Cuts {
 // `unit`, and a warp's share [w0, w1) of it.
 struct Parts {
   uint32_t steps, unit, k0, k1, left;
-  __device__ __forceinline__ explicit Parts(const Cuts& c) : steps(c.steps) {
+  __device__ __forceinline__ explicit Parts(const Cuts& c, bool teams = false) : steps(c.steps) {
+    if (teams) {  // one part, of at least one k-step
+      unit = blockIdx.x / c.team;
+      const uint32_t rank = blockIdx.x - unit * c.team;
+      k0 = steps * rank / c.team;
+      k1 = steps * (rank + 1) / c.team;
+      left = k1 - k0;
+      return;
+    }
     const uint32_t cta = blockIdx.x < c.grid ? blockIdx.x : c.grid, begin = c.start(cta);
     const uint32_t pieces = blockIdx.x < c.grid ? c.start(cta + 1) - begin : 0u;
     unit = c.split ? begin / c.steps : begin;

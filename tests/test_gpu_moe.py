@@ -319,7 +319,7 @@ def test_a_graph_next_to_many_calls(W):
     x, router = dev(layer.x), dev(layer.router)
     want = W.moe(x, router, *layer.dev, 4)
     c = W.q4_encode(torch.randn(64, 40000, device="cuda").bfloat16(), 64)  # rows cut and joined
-    v = torch.randn(2, 40000, device="cuda").bfloat16()
+    v = torch.randn(12, 40000, device="cuda").bfloat16()
     product = W.q4_gemv(c, v)
     torch.cuda.synchronize()
     graphs = []

@@ -219,10 +219,10 @@ def test_gemv_around_the_most_x_that_blocks_prepare_themselves(W, B, K, off):
     assert np.isnan(y[B - 1]).all() and (np.abs(y[:B - 1] - want[:B - 1]) <= tol[:B - 1]).all()
 
 
-@pytest.mark.parametrize("B", [1, 13])
-@pytest.mark.parametrize("shape", [(32, 40576), (257, 20000), (1000, 9001)])
+@pytest.mark.parametrize("B", [1, 7, 13])
+@pytest.mark.parametrize("shape", [(32, 40576), (257, 20000), (1000, 9001), (2000, 16300), (4800, 8200)])
 def test_gemv_of_few_long_rows(W, shape, B):
-    """Fewer tiles than thread blocks: their sums are cut along the rows and joined."""
+    """Fewer tiles than thread blocks: clusters share them, or their sums are cut along the rows and joined."""
     N, K = shape
     w = draw(N, K, seed=N)
     for group in (32, 128):
