@@ -677,12 +677,12 @@ int launch_gemv(GemvArgs& p, int dev, cudaStream_t s) {
 }
 
 // How the units' k-steps fall on the CTAs: whole, cut anywhere and joined
-// through memory, or (up to 8 rows) shared by clusters of 2 to 8 and joined
-// through shared memory: by the longest CTA's run in k-steps, eight of which its
+// through memory, or shared by clusters of 2 to 8 and joined through shared
+// memory: by the longest CTA's run in k-steps, eight of which its
 // warps take at once, and by what else each costs.  us whole / cut / shared by
 // clusters: 2048 x 6144 5.4 / 8.8 / 5.7; 4096 x 4096, 8 rows 6.0 / 10.8 / 7.1; 512
 // x 8192, 3 rows - / 6.5 / 4.9; 2048 x 16384 12.3 / 11.7 / 8.8; 256 x 40576, 7 rows
-// 26 / 10.7 / 7.7; 6144 x 16384, 4 rows 17.1 / 18.0 / -; 16384 x 6144 15.2 / 18.7 /
+// 26 / 10.7 / 7.7; 2048 x 16384, 16 rows - / 16.8 / 12.0; 6144 x 16384, 4 rows 17.1 / 18.0 / -; 16384 x 6144 15.2 / 18.7 /
 // -; 16384 x 53248 85 / 75.5 / -.
 constexpr uint32_t kCutCost = 40, kTeamCost = 16;  // k-steps; 8 are about 1 us
 constexpr uint32_t kXCost = 8;                     // the kernel for x
@@ -695,7 +695,7 @@ Cuts plan(uint32_t units, uint32_t steps, int B, uint32_t ctas) {
   uint64_t cost = best.split ? at_once(cdiv(uint64_t(units) * steps, ctas)) + kCutCost
                              : at_once(steps) * cdiv32(units, ctas);
   cost += x_shared(best, B, ctas) ? 0 : kXCost;
-  for (uint32_t team = 2; B <= 8 && team <= 8 && team <= steps && uint64_t(units) * team <= ctas; team *= 2) {
+  for (uint32_t team = 2; team <= 8 && team <= steps && uint64_t(units) * team <= ctas; team *= 2) {
     Cuts c = best;
     c.team = team;
     c.split = 0;
@@ -715,7 +715,8 @@ int dispatch_gemv(GemvArgs& p, int dev, cudaStream_t s) {
   if (per_sm < 0) return map_cuda(cudaGetLastError());
   const uint32_t ctas = uint32_t(per_sm * sm_count(dev));
   p.cuts = plan(p.cuts.units, p.cuts.steps, p.B, ctas);
-  if (p.B > 8) return launch_gemv<NG, 2, false, false>(p, dev, s);
+  if (p.B > 8)
+    return p.cuts.team > 1 ? launch_gemv<NG, 2, false, true>(p, dev, s) : launch_gemv<NG, 2, false, false>(p, dev, s);
   if (p.cuts.team > 1)
     return x_shared(p.cuts, p.B, ctas) ? launch_gemv<NG, 1, true, true>(p, dev, s)
                                        : launch_gemv<NG, 1, false, true>(p, dev, s);

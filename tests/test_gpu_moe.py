@@ -318,34 +318,35 @@ def test_a_graph_next_to_many_calls(W):
     layer = Layer(W, 2, 16, 512, 256, 64, seed=31)
     x, router = dev(layer.x), dev(layer.router)
     want = W.moe(x, router, *layer.dev, 4)
-    c = W.q4_encode(torch.randn(64, 40000, device="cuda").bfloat16(), 64)  # rows cut and joined
-    v = torch.randn(12, 40000, device="cuda").bfloat16()
-    product = W.q4_gemv(c, v)
+    # rows shared by clusters, and rows cut and joined in memory
+    cs = [W.q4_encode(torch.randn(*shape, device="cuda").bfloat16(), 64) for shape in ((64, 40000), (9744, 14350))]
+    vs = [torch.randn(12, 40000, device="cuda").bfloat16(), torch.randn(1, 14350, device="cuda").bfloat16()]
+    products = [W.q4_gemv(c, v) for c, v in zip(cs, vs)]
     torch.cuda.synchronize()
     graphs = []
     for _ in range(2):
-        y, z = torch.zeros_like(x), torch.zeros_like(product)
+        y, zs = torch.zeros_like(x), [torch.zeros_like(p) for p in products]
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             for _ in range(10):
                 W.moe(x, router, *layer.dev, 4, y=y)
-                W.q4_gemv(c, v, z)
-        graphs.append((g, y, z, torch.cuda.Stream()))
+                for c, v, z in zip(cs, vs, zs):
+                    W.q4_gemv(c, v, z)
+        graphs.append((g, [y, *zs], torch.cuda.Stream()))
     torch.cuda.synchronize()
     out = []
     for i in range(120):
-        for g, y, z, s in graphs:
+        for g, held, s in graphs:
             with torch.cuda.stream(s):
                 if i % 4 == 0:
-                    y.zero_()
-                    z.zero_()
+                    for t in held:
+                        t.zero_()
                 g.replay()
-        out += [W.moe(x, router, *layer.dev, 4) for _ in range(10)] + [W.q4_gemv(c, v)]
+        out.append([W.moe(x, router, *layer.dev, 4) for _ in range(10)][-1:] + [W.q4_gemv(c, v) for c, v in zip(cs, vs)])
     torch.cuda.synchronize()
     W.device_check()
-    assert all(torch.equal(o, want if o.shape == want.shape else product) for o in out)
-    for _, y, z, _ in graphs:
-        assert torch.equal(y, want) and torch.equal(z, product)
+    for held in (*out, *(held for _, held, _ in graphs)):
+        assert all(torch.equal(a, b) for a, b in zip(held, [want, *products]))
 
 
 def test_more_captured_calls_than_kept_counters(W):

@@ -235,6 +235,28 @@ def test_gemv_of_few_long_rows(W, shape, B):
     W.device_check()
 
 
+@pytest.mark.parametrize("B", [1, 8, 11])
+def test_gemv_with_rows_cut_over_blocks(W, B):
+    """A few more tiles than blocks and long rows: every block takes the same number of columns, rows are joined in
+    memory.  The definition in 64 bits on the GPU, by elementary operations."""
+    N, K, group = 9744, 14350, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(B)
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda", generator=g)
+    scales = (torch.rand(N, -(-K // group), device="cuda", generator=g) * 0.02).bfloat16()
+    x = torch.randn(B, K, device="cuda", generator=g).bfloat16()
+    c = W.q4_pack(codes, scales, K, group)
+    y = W.q4_gemv(c, x)
+    assert torch.equal(W.q4_gemv(c, x), y)
+    W.device_check()
+    steps = -(-K // group) + 64
+    for r in range(0, N, 1218):
+        v = torch.stack([codes[r:r + 1218] & 15, codes[r:r + 1218] >> 4], -1).flatten(1).double() - 8
+        v *= scales[r:r + 1218].double().repeat_interleave(group, 1)[:, :K]
+        want, tol = x.double() @ v.T, steps * Q.EPS * (x.double().abs() @ v.abs().T)
+        assert ((y[:, r:r + 1218].double() - want).abs() <= tol).all()
+
+
 @pytest.mark.parametrize("B", [1, 10])
 def test_gemv_of_x_over_a_wide_range(W, B):
     """Magnitudes from 2^-100 to 2^100 in one row: a value keeps its 8 bits down to 2^-31 of the largest of its 128
