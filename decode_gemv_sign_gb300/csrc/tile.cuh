@@ -281,22 +281,21 @@ struct Q4Src {
     c.p += kStage;
   }
   // Quarter q of half s of a stage times x.  Columns with one scale and one
-  // factor are summed in ga by the MMAs, then multiplied in fp32: by the finer of
-  // scale and factor into gb, and gb by the coarser into acc where its range
-  // ends, so that each step costs one fused multiply-add a value.
+  // factor are summed in ga by the MMAs; the sum enters acc under scale times
+  // factor.  That product, of 8 bits and a power of two, comes first: it is exact,
+  // while the sum times one of the two alone may pass fp32's range although the
+  // result does not (scales of 2^110 with x of 2^-100).
   template <int TILES, int NF, bool SHARED>
   static __device__ __forceinline__ void quarter(uint32_t st, uint32_t s, int q, int lane, uint32_t magic,
                                                  const XQuarter<TILES, SHARED>& x,
                                                  const XFactors<TILES, NF, SHARED>& f,
-                                                 float (&ga)[2][TILES][4], float (&gb)[2][TILES][4],
-                                                 float (&acc)[2][TILES][4]) {
+                                                 float (&ga)[2][TILES][4], float (&acc)[2][TILES][4]) {
     constexpr int RUNS = NG > NF ? NG : NF;    // runs per half: 8 / RUNS MMAs each
-    constexpr int WIDE = NG > NF ? NF : NG;    // ranges of the coarser per half
-    constexpr bool kTwo = RUNS > WIDE;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const uint4 w4 = lds_v4(st + s * 2048 + (m * 2 + q) * 512 + lane * 16);
       const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+      float sg = 1.f, sh = 1.f;
 #pragma unroll
       for (int ii = 0; ii < 4; ++ii) {
         const int i = 4 * q + ii;
@@ -310,32 +309,16 @@ struct Q4Src {
             mma_f16(ga[m][n], a, x.b[n][2 * ii], x.b[n][2 * ii + 1]);
         }
         if (((i + 1) * RUNS) % 8 != 0) continue;
-        const bool begins = ((i + 1) * WIDE) % 8 == (8 / RUNS * WIDE) % 8;  // first run of its range
-        const bool ends = ((i + 1) * WIDE) % 8 == 0;
-        const int j = i * NG / 8, jf = i * NF / 8;
-        float sg = 1.f, sh = 1.f;
-        if (NG >= NF || ends) {
-          const uint32_t sc = lds_u32(st + q4_scale_at(NG, 0, j, m, 0) + s * (64 * NG) + (lane >> 2) * 4);
+        if (NG > 2 || RUNS == 1 || ii + 1 == 8 / RUNS) {  // a quarter has one scale a row, or (NG = 4) two
+          const uint32_t sc = lds_u32(st + q4_scale_at(NG, 0, i * NG / 8, m, 0) + s * (64 * NG) + (lane >> 2) * 4);
           sg = bf16_lo(sc);
           sh = bf16_hi(sc);
         }
 #pragma unroll
-        for (int n = 0; n < TILES; ++n) {
-          float* a4 = acc[m][n];
-          float* b4 = gb[m][n];
-          const float* g4 = ga[m][n];
+        for (int n = 0; n < TILES; ++n)
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const float sv = v < 2 ? sg : sh, fv = f.f[n][v & 1][jf];
-            if (!kTwo) {
-              a4[v] = fmaf(sv * fv, g4[v], a4[v]);
-            } else {
-              const float fine = NG > NF ? sv : fv, coarse = NG > NF ? fv : sv;
-              b4[v] = begins ? fine * g4[v] : fmaf(fine, g4[v], b4[v]);
-              if (ends) a4[v] = fmaf(coarse, b4[v], a4[v]);
-            }
-          }
-        }
+          for (int v = 0; v < 4; ++v)
+            acc[m][n][v] = fmaf((v < 2 ? sg : sh) * f.f[n][v & 1][i * NF / 8], ga[m][n][v], acc[m][n][v]);
       }
     }
   }
@@ -607,7 +590,7 @@ struct Product {  // 4-bit
 #pragma unroll (TILES == 1 ? 2 : 1)
     for (uint32_t s = 0; s < 2; ++s) {
       const uint32_t rec = 2 * k + s, next = s ? 2 * kn : rec + 1;
-      float ga[2][TILES][4], gb[2][TILES][4];
+      float ga[2][TILES][4];
       XQuarter<TILES, SHARED> x1;
       XFactors<TILES, NF, SHARED> fn;
       constexpr bool kAhead = TILES == 1 || NF == 1;  // sixteen rows' four factors: no registers left to load ahead
@@ -616,9 +599,9 @@ struct Product {  // 4-bit
         fn.load(x, next);
       else
         f.load(x, rec);
-      SRC::template quarter<TILES, NF, SHARED>(st, s, 0, lane, magic, x0, f, ga, gb, acc);
+      SRC::template quarter<TILES, NF, SHARED>(st, s, 0, lane, magic, x0, f, ga, acc);
       x0.load(x, uint64_t(next) * kRecord);
-      SRC::template quarter<TILES, NF, SHARED>(st, s, 1, lane, magic, x1, f, ga, gb, acc);
+      SRC::template quarter<TILES, NF, SHARED>(st, s, 1, lane, magic, x1, f, ga, acc);
       if (kAhead) f = fn;
     }
     __syncwarp();  // every lane has read the stage

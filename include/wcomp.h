@@ -397,10 +397,14 @@ WCOMP_API int wcomp_q4_decode(const wcomp_q4* c, uint16_t* d_out, void* stream);
  * Numbers: x is taken in blocks of 128 columns as fp16 under the power of two
  * that its largest magnitude asks for.  A BF16 value keeps all its bits down to
  * 2^-31 of that; smaller ones err by at most 2^-39 of it.  Products with c - 8
- * are then exact and summed in fp32 on the tensor cores; a group's sum is scaled
- * and added in fp32.  Infinities and NaN stay in their row of x and follow the
- * definition (scale times magnitude of x below 2^128 elsewhere).  The order of
- * the sums is fixed: repeated calls give identical bits.
+ * are then exact and summed in fp32 on the tensor cores; a group's sum enters
+ * the fp32 result under scale times power of two, which is exact.  So a scale
+ * may be large where x is small, and small where x is large: what is asked is
+ * that scale times the largest magnitude of x in its 128 columns be below 2^128;
+ * where that is below 2^-128 a group errs by up to 2^-125.  Infinities and NaN of
+ * x stay in their row of x and follow the definition; an infinite or NaN scale
+ * makes its row of the weight infinite or NaN.  The order of the sums is fixed:
+ * repeated calls give identical bits.
  * Memory: that form of x and, where rows are split over thread blocks, their
  * parts come from the library's stream-ordered pool for the duration of the
  * call.  The device's error word is allocated with cudaMalloc on first use: make
