@@ -171,10 +171,20 @@ __device__ __forceinline__ void put_choice(const MoeParams& p, uint32_t t, uint3
   ch.key[i] = uint16_t(e * kMaxT + t);
   ch.w[i] = score;
 }
+// exp of a logit under the row's largest (softmax), or of its negated magnitude
+// (sigmoid), and the score that follows from it.  Neither overflows, so sigmoid's
+// scores keep their order down to logits of -103, where fp32 ends (1 / (1 +
+// exp(-l)) would be 0 from -87 on, and a choice among such experts fall to their
+// index), and the divisor is 1 to 1024, where the approximate division is right
+// to two units in the last place (the exact one: 0.6 us of a small layer's 14).
+__device__ __forceinline__ float score_exp(bool soft, float l, float mx) { return expf(soft ? l - mx : -fabsf(l)); }
+__device__ __forceinline__ float score_of(bool soft, float l, float ex, float sum) {
+  return __fdividef(soft || l < 0.f ? ex : 1.f, soft ? sum : 1.f + ex);
+}
 template <int U>
 __device__ __forceinline__ void choose(const MoeParams& p, uint32_t t, int lane, Choice& ch) {
   const bool soft = p.scoring == WCOMP_MOE_SOFTMAX;
-  float sc[U];
+  float sc[U], ex[U];
   uint32_t key[U];
   float mx = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -186,15 +196,14 @@ __device__ __forceinline__ void choose(const MoeParams& p, uint32_t t, int lane,
   mx = soft ? warp_max(mx) : 0.f;
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const float v = expf(soft ? sc[i] - mx : -sc[i]);
-    sc[i] = v;
-    sum += lane + 32 * i < p.E ? v : 0.f;
+    ex[i] = score_exp(soft, sc[i], mx);
+    sum += lane + 32 * i < p.E ? ex[i] : 0.f;
   }
   sum = warp_sum(sum);
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const uint32_t e = lane + 32 * i;
-    sc[i] = __fdividef(soft ? sc[i] : 1.f, soft ? sum : 1.f + sc[i]);
+    sc[i] = score_of(soft, sc[i], ex[i], sum);
     key[i] = e < p.E ? rank_key(p.bias ? sc[i] + p.bias[e] : sc[i]) : 0u;
   }
 #pragma unroll 1
@@ -228,15 +237,12 @@ __device__ __forceinline__ void choose_many(const MoeParams& p, uint32_t t, int 
     mx = fmaxf(mx, l);
   }
   mx = soft ? warp_max(mx) : 0.f;
-  for (uint32_t e = lane; e < p.E; e += 32) {
-    const float v = expf(soft ? sc[e] - mx : -sc[e]);
-    sc[e] = v;
-    sum += v;
-  }
+  if (soft)
+    for (uint32_t e = lane; e < p.E; e += 32) sum += score_exp(true, sc[e], mx);
   sum = warp_sum(sum);
   uint32_t key = 0u, at = 0xFFFFFFFFu;
   for (uint32_t e = lane; e < p.E; e += 32) {
-    const float v = __fdividef(soft ? sc[e] : 1.f, soft ? sum : 1.f + sc[e]);
+    const float v = score_of(soft, sc[e], score_exp(soft, sc[e], mx), sum);
     const uint32_t kk = rank_key(p.bias ? v + p.bias[e] : v);
     sc[e] = v;
     keys[e] = kk;

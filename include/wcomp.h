@@ -461,7 +461,8 @@ typedef struct {
  *   weight[t, j] = factor * score, divided by the chosen scores' sum if
  *   renormalize;
  *   y[t] = sum_j weight[t, j] * down_j (silu(gate_j x[t]) * (up_j x[t])).
- * Sums and scores are in fp32.  The hidden values between the products are held
+ * Sums and scores are in fp32 (experts whose scores are 0 there, logits of -104
+ * under the largest or, for sigmoid, under zero, count as ties).  The hidden values between the products are held
  * as two BF16 parts (BF16 experts: 16 significant bits) or in fp16 under a power
  * of two for each 32 of them (4-bit experts: 11 bits, an eighth of a step of the
  * result; x as in wcomp_q4_gemv).  y is rounded once.  The order of the sums is
