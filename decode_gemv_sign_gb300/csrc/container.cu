@@ -56,6 +56,23 @@ cudaError_t pool_alloc(void** p, size_t bytes, cudaStream_t s) {
   return cudaMallocFromPoolAsync(p, bytes, pools[dev], s);
 }
 
+cudaError_t zeroed_alloc(uint32_t** out, size_t bytes) {
+  uint32_t* p = nullptr;
+  cudaStream_t s = nullptr;
+  cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&p), bytes);
+  if (e != cudaSuccess) return e;
+  e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+  if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, bytes, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (s) cudaStreamDestroy(s);
+  if (e != cudaSuccess) {
+    cudaFree(p);
+    return e;
+  }
+  *out = p;
+  return cudaSuccess;
+}
+
 int sm_count(int device) {
   static std::mutex mu;
   static int cache[64] = {0};

@@ -1160,8 +1160,7 @@ int scratch(int dev, uint32_t** base) {
   if (!g_scratch[dev]) {
     uint32_t* p = nullptr;
     const size_t bytes = (kSlots * 2 + 32) * sizeof(uint32_t);
-    cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&p), bytes);
-    if (e == cudaSuccess) e = cudaMemset(p, 0, bytes);
+    const cudaError_t e = zeroed_alloc(&p, bytes);
     if (e != cudaSuccess) return map_cuda(e);
     g_scratch[dev] = p;
   }

@@ -781,12 +781,8 @@ int work_slot(int dev, bool captured, uint32_t** slot, uint32_t** err) {
   Work& w = g_work[dev];
   if (!w.p) {
     uint32_t* p = nullptr;
-    cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&p), kWorkBytes);
-    if (e == cudaSuccess) e = cudaMemset(p, 0, kWorkBytes);
-    if (e != cudaSuccess) {
-      if (p) cudaFree(p);
-      return map_cuda(e);
-    }
+    const cudaError_t e = zeroed_alloc(&p, kWorkBytes);
+    if (e != cudaSuccess) return map_cuda(e);
     w.p = p;
   }
   if (slot && captured)

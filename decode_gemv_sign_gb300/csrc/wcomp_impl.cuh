@@ -409,6 +409,11 @@ uint32_t debug_take_gemv();
 // device (created on first use; it keeps freed blocks for reuse instead of
 // returning them to the driver at every synchronization).
 cudaError_t pool_alloc(void** p, size_t bytes, cudaStream_t s);
+// Device memory that holds zeros when the call returns, for launches on any
+// stream: cleared on a stream of its own that the host waits for.  (A memset on
+// the default stream may still be queued then, behind the program's work, and
+// non-blocking streams do not wait for it.)
+cudaError_t zeroed_alloc(uint32_t** p, size_t bytes);
 int sm_count(int device);
 uint64_t l2_size(int device);
 int map_cuda(cudaError_t e);
