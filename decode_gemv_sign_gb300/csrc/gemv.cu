@@ -1469,8 +1469,7 @@ extern "C" int wcomp_device_check(void* stream) {
   uint32_t* base = nullptr;
   int st = scratch(dev, &base);
   if (st != WCOMP_OK) return st;
-  uint32_t* const expert_word = work_error_word(dev);
-  uint32_t* words[3] = {base + 2 * kSlots, noalloc_error_word(dev), expert_word};
+  uint32_t* words[3] = {base + 2 * kSlots, noalloc_error_word(dev), work_error_word(dev)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   bool failed = false;
   for (uint32_t* w : words) {
@@ -1481,9 +1480,9 @@ extern "C" int wcomp_device_check(void* stream) {
     if (e != cudaSuccess) return map_cuda(e);
     if (word) {
       failed = true;
-      // a grid barrier that ran out leaves its counters behind: they are
-      // cleared with the word
-      e = w == expert_word ? work_reset(dev, s) : cudaMemsetAsync(w, 0, sizeof(uint32_t), s);
+      // nothing but the word: the kernels leave their counters in order, and
+      // others may be running on them
+      e = cudaMemsetAsync(w, 0, sizeof(uint32_t), s);
       if (e == cudaSuccess) e = cudaStreamSynchronize(s);
       if (e != cudaSuccess) return map_cuda(e);
     }
@@ -1495,8 +1494,10 @@ extern "C" int wcomp_device_check(void* stream) {
 
 extern "C" int wcomp_debug_skip_first_copy(int on) {
 #if WCOMP_DEBUG
-  const uint32_t v = on ? 1u : 0u;
-  const cudaError_t e = cudaMemcpyToSymbol(g_debug_skip_first_copy, &v, sizeof(v));
+  const uint32_t v = uint32_t(on) & 1u;
+  cudaError_t e = cudaMemcpyToSymbol(g_debug_skip_first_copy, &v, sizeof(v));
+  if (e == cudaSuccess) e = debug_hooks_q4(uint32_t(on));
+  if (e == cudaSuccess) e = debug_hooks_moe(uint32_t(on));
   if (e == cudaSuccess) {
     const cudaError_t e2 = cudaDeviceSynchronize();
     if (e2 != cudaSuccess) return map_cuda(e2);

@@ -12,9 +12,11 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn tensor_map_encoder();
-// The expert and 4-bit kernels' error word on device `dev` (null before their
-// first use), and the reset of it and of their work counters (q4.cu).
+// The expert and 4-bit kernels' error word on device `dev`, null before their
+// first use (q4.cu).
 uint32_t* work_error_word(int dev);
-cudaError_t work_reset(int dev, cudaStream_t s);
+// Debug builds: which test hooks the launches of q4.cu and moe.cu follow.
+cudaError_t debug_hooks_q4(uint32_t bits);
+cudaError_t debug_hooks_moe(uint32_t bits);
 
 }  // namespace wc

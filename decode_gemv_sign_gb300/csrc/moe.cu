@@ -86,7 +86,8 @@ struct MoeParams {
   uint32_t T, E, k, H, F, Fp;
   int scoring, renorm, x_vec;
   float factor;
-  uint32_t* counters;     // [0], [1] barriers, [2] CTAs done, then one per CTA for each of B's and C's joins; zero
+  uint32_t* counters;     // [0], [1] barriers, [2] CTAs done, [3] a barrier ran out; from [8] one per CTA for each of
+                          // B's and C's joins; zero before and after
   uint32_t* err;
 };
 struct MoeMaps {
@@ -111,11 +112,16 @@ struct Choice {  // pairs t * k + j as chosen
 };
 
 // Wait until every CTA of the (cooperative, so resident) grid has arrived.
-// Bounded: after kBarrierNs the error word is set and false comes back, to
-// every thread of the CTA.
-__device__ bool grid_barrier(uint32_t* counter, uint32_t* err, uint32_t* s_ok) {
+// Bounded: after kBarrierNs the error word and counters[3] are set and false
+// comes back, to every thread of the CTA.
+__device__ bool grid_barrier(uint32_t* counters, uint32_t which, uint32_t* err, uint32_t* s_ok) {
   __syncthreads();
   if (threadIdx.x == 0) {
+    uint32_t* const counter = counters + which;
+#if WCOMP_DEBUG
+    if ((g_debug_hooks & 2u) && which == 0 && blockIdx.x == 0)  // come when the others have given up
+      for (const uint64_t t = timer_ns() + kBarrierNs + kBarrierNs / 2; timer_ns() < t;) {}
+#endif
     __threadfence();
     atomicAdd(counter, 1u);
     uint32_t v, ok = 1u;
@@ -128,6 +134,7 @@ __device__ bool grid_barrier(uint32_t* counter, uint32_t* err, uint32_t* s_ok) {
       if (t > deadline) {
         ok = 0u;
         atomicOr(err, 1u);
+        atomicOr(counters + 3, 1u);
         break;
       }
     }
@@ -613,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
       }
     }
   }
-  bool ok = grid_barrier(p.counters, p.err, &s_flag);
+  bool ok = grid_barrier(p.counters, 0, p.err, &s_flag);
   if (ok) {
     // ---- the choice, alike in every CTA
     for (uint32_t t = warp; t < p.T; t += kWarps) {
@@ -761,9 +768,9 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
       };
       enter();
       for (uint32_t i = 0; i < D; ++i) issue((ring.slot + i) % D);
-      ok = grid_barrier(p.counters + 1, p.err, &s_flag);
+      ok = grid_barrier(p.counters, 1, p.err, &s_flag);
       if (ok) {
-          bool first_part = true;
+        bool first_part = true;
         for (Parts s(cuts); s.more(); s.next(), first_part = false) {
           float* ys = share + warp * (kMaxT * 32);
           __syncthreads();  // the previous unit's accumulators are read
@@ -814,15 +821,17 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
       }
     }
   }
-  // the last CTA to finish leaves the counters at zero for their next launch
+  // the last CTA to finish leaves the counters at zero for their next launch:
+  // after a barrier that ran out also those of joins that not every CTA came to
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
-    if (atomicAdd(p.counters + 2, 1u) == gridDim.x - 1) {
-      p.counters[0] = p.counters[1] = p.counters[2] = 0u;
-      __threadfence();
-    }
+    const bool last = atomicAdd(p.counters + 2, 1u) == gridDim.x - 1;
+    __threadfence();
+    s_flag = !last ? 0u : __ldcg(p.counters + 3) ? kSlotWords : 4u;
   }
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < s_flag; i += kThreads) p.counters[i] = 0u;
 }
 
 template <class SRC, bool WIDE>
@@ -868,6 +877,8 @@ bool box_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols) {
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 }  // namespace
+
+WCOMP_DEBUG_HOOKS(debug_hooks_moe)
 }  // namespace wc
 
 using namespace wc;

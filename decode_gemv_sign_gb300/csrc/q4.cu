@@ -799,12 +799,7 @@ uint32_t* work_error_word(int dev) {
   return g_work[dev].p ? g_work[dev].p + kCounters : nullptr;
 }
 
-cudaError_t work_reset(int dev, cudaStream_t s) {
-  uint32_t* e = work_error_word(dev);
-  if (!e) return cudaSuccess;
-  return cudaMemsetAsync(e - kCounters, 0, kWorkBytes, s);
-}
-
+WCOMP_DEBUG_HOOKS(debug_hooks_q4)
 }  // namespace wc
 
 using namespace wc;

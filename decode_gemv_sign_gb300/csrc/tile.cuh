@@ -24,6 +24,18 @@
 
 namespace wc {
 
+// What a debug build's launches of this translation unit leave out or delay
+// (wcomp_debug_skip_first_copy): bit 0 a ring's first copy, bit 1 the first
+// block's arrival at a grid barrier.
+#if WCOMP_DEBUG
+static __device__ uint32_t g_debug_hooks;
+#define WCOMP_DEBUG_HOOKS(fn) \
+  cudaError_t fn(uint32_t bits) { return cudaMemcpyToSymbol(g_debug_hooks, &bits, sizeof(bits)); }
+#else
+#define WCOMP_DEBUG_HOOKS(fn) \
+  cudaError_t fn(uint32_t) { return cudaSuccess; }
+#endif
+
 constexpr int kTileRows = 32;    // rows of a tile: two MMAs' M side
 constexpr int kQ4Cols = 256;     // columns of a 4-bit block
 constexpr int kSub = 128;        // columns of half a block, and of an x record
@@ -488,6 +500,11 @@ struct Ring {
   uint32_t* err;
   uint32_t slot = 0, parity = 0, left = 0;
   bool dead = false;
+#if WCOMP_DEBUG
+  bool skip = g_debug_hooks & 1u;  // the first copy is left out
+#else
+  static constexpr bool skip = false;
+#endif
 
   __device__ __forceinline__ Ring(uint32_t base_, uint32_t bars_, uint32_t* err_, int lane)
       : base(base_), bars(bars_), err(err_) {
@@ -501,10 +518,13 @@ struct Ring {
     const uint32_t st = base + at * SRC::kStage;
     if constexpr (SRC::kCopies) {
       if (dead) return;
-      if (lane == 0) {
+      if (lane == 0 && !skip) {
         bar_expect(bars + 8 * at, SRC::kStage);
         SRC::issue(c, st, bars + 8 * at);
       }
+#if WCOMP_DEBUG
+      skip = false;
+#endif
       ++left;
     } else {
       SRC::load(c, st, lane);

@@ -243,7 +243,8 @@ WCOMP_API int wcomp_gemv_batched(const wcomp_container* const* containers, const
  * static array, and the one of wcomp_q4_gemv and wcomp_moe).  A kernel whose
  * bounded wait on its own tensor copies, or on its other thread blocks, runs
  * out records it there and finishes without waiting instead of hanging; its
- * outputs are then undefined.  In a debug build (compiled with WCOMP_DEBUG=1)
+ * outputs are then undefined, those of other and later calls are not touched by
+ * it nor by this check, which may be made while others run.  In a debug build (compiled with WCOMP_DEBUG=1)
  * the kernels on containers and plain weights also check their indexes before
  * memory accesses, skip an access that fails and record it.  Synchronizes
  * `stream`.
@@ -252,16 +253,18 @@ WCOMP_API int wcomp_gemv_batched(const wcomp_container* const* containers, const
 WCOMP_API int wcomp_device_check(void* stream);
 
 /*
- * Test hook for the bounded waits, in debug builds only (compiled with
- * WCOMP_DEBUG=1).  While `on` is non-zero, every warp of a GEMV launch
- * (fused or plain) leaves the first of its tensor copies unissued but still
- * waits for it: the wait runs out after about a second, the warp stops
- * copying and waiting, lets the copies it has in flight land and finishes,
- * and wcomp_device_check then reports WCOMP_ETIMEOUT.  The outputs of such a
- * launch are undefined; the context stays usable.  Applies to the current
- * device and synchronizes it.  Release builds do nothing and return
- * WCOMP_EUNSUPPORTED.  (Library housekeeping; the pages define no
- * counterpart.)
+ * Test hooks for the bounded waits, in debug builds only (compiled with
+ * WCOMP_DEBUG=1).  While `on` has bit 0 set, every warp of a GEMV launch (fused,
+ * plain or 4-bit) or of wcomp_moe (but for BF16 experts that no tensor map
+ * takes) leaves the first of its tensor copies unissued but still waits for it:
+ * the wait runs out after about a second, the warp stops copying and waiting,
+ * lets the copies it has in flight land and finishes, and wcomp_device_check
+ * then reports WCOMP_ETIMEOUT.  With bit 1 set, the first thread block of
+ * wcomp_moe comes to its first grid barrier half a second after the others gave
+ * up on it.  The outputs of such a launch are undefined; the context stays
+ * usable.  Applies to the current device and synchronizes it.  Release builds do
+ * nothing and return WCOMP_EUNSUPPORTED.  (Library housekeeping; the pages
+ * define no counterpart.)
  */
 WCOMP_API int wcomp_debug_skip_first_copy(int on);
 
