@@ -21,8 +21,11 @@
 
 namespace wc {
 
+// The runtime keeps a failed call's error until it is asked for, and the check
+// after a later launch would find it: it ends here.
 int map_cuda(cudaError_t e) {
   if (e == cudaSuccess) return WCOMP_OK;
+  cudaGetLastError();
   if (e == cudaErrorMemoryAllocation) return WCOMP_ENOMEM;
   return WCOMP_ECUDA;
 }
