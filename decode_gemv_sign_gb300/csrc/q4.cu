@@ -600,15 +600,20 @@ __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_const
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-// Counters: kSlots slots that launches take in turn, then kKept that captured
-// launches keep; after them the error word.
-constexpr uint64_t kSlots = 1024, kKept = 4096, kCounters = (kSlots + kKept) * kSlotWords;
-constexpr size_t kWorkBytes = (kCounters + 32) * sizeof(uint32_t);
+// Sets of counters: kSlots slots that launches take in turn, then kKept that
+// captured launches keep.
+constexpr uint64_t kSlots = 1024, kKept = 4096;
 std::mutex g_mu;
 struct Work {
-  uint32_t* p = nullptr;
+  uint32_t* err = nullptr;
+  uint32_t* sets = nullptr;
   uint64_t turn = 0, kept = 0;
 } g_work[64];
+
+// Zeroed memory at *p, allocated on first use.
+int first_use(uint32_t** p, size_t bytes) {
+  return *p ? int(WCOMP_OK) : map_cuda(zeroed_alloc(p, bytes));
+}
 
 template <int NG, int TILES, bool SHARED, bool TEAM>
 int prepare_gemv(int dev) {
@@ -629,7 +634,7 @@ int prepare_gemv(int dev) {
 template <int NG, int TILES, bool SHARED, bool TEAM>
 int launch_gemv(GemvArgs& p, int dev, cudaStream_t s) {
   if (prepare_gemv<NG, TILES, SHARED, TEAM>(dev) < 0) return map_cuda(cudaGetLastError());
-  int st = work_slot(dev, false, nullptr, &p.err);
+  int st = work_error(dev, &p.err);
   if (st != WCOMP_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.cuts.grid);
@@ -775,28 +780,31 @@ bool on_device(const wcomp_q4* c) {
 
 }  // namespace
 
-int work_slot(int dev, bool captured, uint32_t** slot, uint32_t** err) {
+int work_error(int dev, uint32_t** err) {
+  if (dev < 0 || dev >= 64) return WCOMP_EUNSUPPORTED;
+  std::lock_guard<std::mutex> g(g_mu);
+  const int st = first_use(&g_work[dev].err, 128);
+  *err = g_work[dev].err;
+  return st;
+}
+
+int work_slot(int dev, bool captured, uint32_t** slot) {
   if (dev < 0 || dev >= 64) return WCOMP_EUNSUPPORTED;
   std::lock_guard<std::mutex> g(g_mu);
   Work& w = g_work[dev];
-  if (!w.p) {
-    uint32_t* p = nullptr;
-    const cudaError_t e = zeroed_alloc(&p, kWorkBytes);
-    if (e != cudaSuccess) return map_cuda(e);
-    w.p = p;
-  }
-  if (slot && captured)
-    *slot = w.kept < kKept ? w.p + (kSlots + w.kept++) * kSlotWords : nullptr;
-  else if (slot)
-    *slot = w.p + (w.turn++ % kSlots) * kSlotWords;
-  *err = w.p + kCounters;
+  const int st = first_use(&w.sets, (kSlots + kKept) * kSlotWords * sizeof(uint32_t));
+  if (st != WCOMP_OK) return st;
+  if (captured)
+    *slot = w.kept < kKept ? w.sets + (kSlots + w.kept++) * kSlotWords : nullptr;
+  else
+    *slot = w.sets + (w.turn++ % kSlots) * kSlotWords;
   return WCOMP_OK;
 }
 
 uint32_t* work_error_word(int dev) {
   if (dev < 0 || dev >= 64) return nullptr;
   std::lock_guard<std::mutex> g(g_mu);
-  return g_work[dev].p ? g_work[dev].p + kCounters : nullptr;
+  return g_work[dev].err;
 }
 
 WCOMP_DEBUG_HOOKS(debug_hooks_q4)

@@ -1,0 +1,37 @@
+"""Device memory that the library keeps outside its pool."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+CHILD = r"""
+import sys
+import torch
+sys.path.insert(0, sys.argv[1])
+from decode_gemv_sign_gb300 import build, wcomp as W
+build.build()
+x = torch.randn(2, 4096, device="cuda").bfloat16()
+weights = [W.q4_encode(torch.randn(N, 4096, device="cuda").bfloat16(), 64) for N in (64, 9744)]
+W.q4_encode(torch.zeros(32768, 4096, dtype=torch.bfloat16, device="cuda"), 64).free()  # 72 MB that the pool keeps
+y = [torch.empty(2, N, device="cuda") for N in (64, 9744)]
+torch.cuda.synchronize()
+before = torch.cuda.mem_get_info()[0]
+for w, out in zip(weights, y):
+    W.q4_gemv(w, x, out)
+torch.cuda.synchronize()
+print(before - torch.cuda.mem_get_info()[0])
+"""
+
+
+def test_products_keep_no_counters():
+    """4-bit products alone keep an error word (and their code, a few MB), not the expert layer's 20 MB of counters."""
+    r = subprocess.run([sys.executable, "-c", CHILD, ROOT], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-4000:]
+    print(r.stdout)
+    assert int(r.stdout.split()[-1]) < 12 << 20, r.stdout
