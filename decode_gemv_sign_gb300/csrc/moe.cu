@@ -949,7 +949,7 @@ extern "C" int wcomp_moe(const wcomp_moe_args* a, void* stream) {
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
   if ((e = cudaStreamIsCapturing(s, &capture)) != cudaSuccess) return map_cuda(e);
   int st = work_error(dev, &p.err);
-  if (st == WCOMP_OK) st = work_slot(dev, capture != cudaStreamCaptureStatusNone, &p.counters);
+  if (st == WCOMP_OK) st = work_slot(dev, s, capture != cudaStreamCaptureStatusNone, &p.counters);
   if (st != WCOMP_OK) return st;
   const uint64_t b_count = p.counters ? 0 : kSlotWords * sizeof(uint32_t);
   uint8_t* ws = nullptr;

@@ -600,14 +600,21 @@ __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_const
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-// Sets of counters: kSlots slots that launches take in turn, then kKept that
-// captured launches keep.
-constexpr uint64_t kSlots = 1024, kKept = 4096;
+// Sets of counters: one for each of kStreams streams, whose launches follow one
+// another, then kKept that captured launches keep.  (Sets in turn for launches on
+// any stream would be shared by two that run together when one stream is that
+// many launches ahead.)
+constexpr uint64_t kStreams = 1024, kKept = 4096;
 std::mutex g_mu;
 struct Work {
   uint32_t* err = nullptr;
   uint32_t* sets = nullptr;
-  uint64_t turn = 0, kept = 0;
+  uint64_t kept = 0;
+  uint32_t streams = 0;
+  struct {
+    unsigned long long id;  // of the stream, never used again for another one
+    uint32_t set;           // and 1
+  } table[2 * kStreams] = {};
 } g_work[64];
 
 // Zeroed memory at *p, allocated on first use.
@@ -788,16 +795,29 @@ int work_error(int dev, uint32_t** err) {
   return st;
 }
 
-int work_slot(int dev, bool captured, uint32_t** slot) {
+int work_slot(int dev, cudaStream_t s, bool captured, uint32_t** slot) {
   if (dev < 0 || dev >= 64) return WCOMP_EUNSUPPORTED;
+  unsigned long long id = 0;
+  if (!captured) {
+    const cudaError_t e = cudaStreamGetId(s, &id);
+    if (e != cudaSuccess) return map_cuda(e);
+  }
   std::lock_guard<std::mutex> g(g_mu);
   Work& w = g_work[dev];
-  const int st = first_use(&w.sets, (kSlots + kKept) * kSlotWords * sizeof(uint32_t));
+  const int st = first_use(&w.sets, (kStreams + kKept) * kSlotWords * sizeof(uint32_t));
   if (st != WCOMP_OK) return st;
-  if (captured)
-    *slot = w.kept < kKept ? w.sets + (kSlots + w.kept++) * kSlotWords : nullptr;
-  else
-    *slot = w.sets + (w.turn++ % kSlots) * kSlotWords;
+  *slot = nullptr;
+  if (captured) {
+    if (w.kept < kKept) *slot = w.sets + (kStreams + w.kept++) * kSlotWords;
+    return WCOMP_OK;
+  }
+  uint64_t i = id % (2 * kStreams);
+  while (w.table[i].set && w.table[i].id != id) i = (i + 1) % (2 * kStreams);  // half of the table stays empty
+  if (!w.table[i].set) {
+    if (w.streams == kStreams) return WCOMP_OK;
+    w.table[i] = {id, ++w.streams};
+  }
+  *slot = w.sets + uint64_t(w.table[i].set - 1) * kSlotWords;
   return WCOMP_OK;
 }
 

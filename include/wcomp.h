@@ -480,10 +480,12 @@ typedef struct {
  * undefined outputs and wcomp_device_check reports WCOMP_ETIMEOUT.
  * Memory: logits, hidden values, parts of sums and (unless x can be read as it
  * is) a copy of x come from the library's stream-ordered pool for the duration
- * of the call.  The counters of the barriers are one of 1024 sets, in turn,
- * allocated with cudaMalloc on first use (20 MB; make the first call before any
- * stream capture).  The first 4096 calls that are captured keep sets of their
- * own; later ones clear their own in the graph, which takes it 4 us longer.
+ * of the call.  The counters of the barriers are allocated with cudaMalloc on
+ * first use (20 MB; make the first call before any stream capture): a set for each
+ * of the first 1024 streams that the device's calls are made on, and a set for
+ * each of the first 4096 calls that are captured, so that calls on different
+ * streams and graphs may run next to one another.  Others clear counters of their
+ * own, which takes them 4 us longer.
  */
 WCOMP_API int wcomp_moe(const wcomp_moe_args* args, void* stream);
 
