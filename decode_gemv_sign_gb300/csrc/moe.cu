@@ -86,8 +86,8 @@ struct MoeParams {
   uint32_t T, E, k, H, F, Fp;
   int scoring, renorm, x_vec;
   float factor;
-  uint32_t* counters;     // [0], [1] barriers, [2] CTAs done, [3] a barrier ran out; from [8] one per CTA for each of
-                          // B's and C's joins; zero before and after
+  uint32_t* counters;     // [0], [1] barriers, [2] CTAs done, and in its upper half those whose barrier ran out; from [8]
+                          // one per CTA for each of B's and C's joins; zero before and after
   uint32_t* err;
 };
 struct MoeMaps {
@@ -112,14 +112,13 @@ struct Choice {  // pairs t * k + j as chosen
 };
 
 // Wait until every CTA of the (cooperative, so resident) grid has arrived.
-// Bounded: after kBarrierNs the error word and counters[3] are set and false
-// comes back, to every thread of the CTA.
-__device__ bool grid_barrier(uint32_t* counters, uint32_t which, uint32_t* err, uint32_t* s_ok) {
+// Bounded: after kBarrierNs the error word is set and false comes back, to
+// every thread of the CTA.
+__device__ bool grid_barrier(uint32_t* counter, uint32_t* err, uint32_t* s_ok, [[maybe_unused]] bool first) {
   __syncthreads();
   if (threadIdx.x == 0) {
-    uint32_t* const counter = counters + which;
 #if WCOMP_DEBUG
-    if ((g_debug_hooks & 2u) && which == 0 && blockIdx.x == 0)  // come when the others have given up
+    if ((g_debug_hooks & 2u) && first && blockIdx.x == 0)  // come when the others have given up
       for (const uint64_t t = timer_ns() + kBarrierNs + kBarrierNs / 2; timer_ns() < t;) {}
 #endif
     __threadfence();
@@ -134,7 +133,6 @@ __device__ bool grid_barrier(uint32_t* counters, uint32_t which, uint32_t* err, 
       if (t > deadline) {
         ok = 0u;
         atomicOr(err, 1u);
-        atomicOr(counters + 3, 1u);
         break;
       }
     }
@@ -620,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
       }
     }
   }
-  bool ok = grid_barrier(p.counters, 0, p.err, &s_flag);
+  bool ok = grid_barrier(p.counters, p.err, &s_flag, true);
   if (ok) {
     // ---- the choice, alike in every CTA
     for (uint32_t t = warp; t < p.T; t += kWarps) {
@@ -768,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
       };
       enter();
       for (uint32_t i = 0; i < D; ++i) issue((ring.slot + i) % D);
-      ok = grid_barrier(p.counters, 1, p.err, &s_flag);
+      ok = grid_barrier(p.counters + 1, p.err, &s_flag, false);
       if (ok) {
         bool first_part = true;
         for (Parts s(cuts); s.more(); s.next(), first_part = false) {
@@ -826,12 +824,12 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
-    const bool last = atomicAdd(p.counters + 2, 1u) == gridDim.x - 1;
-    __threadfence();
-    s_flag = !last ? 0u : __ldcg(p.counters + 3) ? kSlotWords : 4u;
+    const uint32_t done = atomicAdd(p.counters + 2, ok ? 1u : 0x10001u) + (ok ? 1u : 0x10001u);
+    if ((done & 0xFFFFu) == gridDim.x) {
+      __threadfence();
+      for (uint32_t i = 0; i < (done >> 16 ? kSlotWords : 3u); ++i) p.counters[i] = 0u;
+    }
   }
-  __syncthreads();
-  for (uint32_t i = threadIdx.x; i < s_flag; i += kThreads) p.counters[i] = 0u;
 }
 
 template <class SRC, bool WIDE>
