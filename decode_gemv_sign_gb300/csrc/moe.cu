@@ -944,10 +944,8 @@ extern "C" int wcomp_moe(const wcomp_moe_args* a, void* stream) {
                  b_hf = q4 ? round(uint64_t(p.Fp) / 32 * factor_pitch<4>() * 4) : 0,
                  b_part = uint64_t(2) * 2 * kMaxGrid * kPartFloats * sizeof(float),
                  b_x = make ? round(p.T * p.xs_bytes) : 0, b_xf = q4 ? round(Hp / kSub * factor_pitch<1>() * 4) : 0;
-  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-  if ((e = cudaStreamIsCapturing(s, &capture)) != cudaSuccess) return map_cuda(e);
   int st = work_error(dev, &p.err);
-  if (st == WCOMP_OK) st = work_slot(dev, s, capture != cudaStreamCaptureStatusNone, &p.counters);
+  if (st == WCOMP_OK) st = work_slot(dev, s, &p.counters);
   if (st != WCOMP_OK) return st;
   const uint64_t b_count = p.counters ? 0 : kSlotWords * sizeof(uint32_t);
   uint8_t* ws = nullptr;

@@ -601,7 +601,8 @@ __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_const
 // Host side.
 // ---------------------------------------------------------------------------
 // Sets of counters: one for each of kStreams streams, whose launches follow one
-// another, then kKept that captured launches keep.  (Sets in turn for launches on
+// another, then kKept that captured launches keep while their graph, or an
+// executable one made of it, is there.  (Sets in turn for launches on
 // any stream would be shared by two that run together when one stream is that
 // many launches ahead.)
 constexpr uint64_t kStreams = 1024, kKept = 4096;
@@ -609,7 +610,9 @@ std::mutex g_mu;
 struct Work {
   uint32_t* err = nullptr;
   uint32_t* sets = nullptr;
-  uint64_t kept = 0;
+  uint32_t kept = 0;          // of the kept sets, those that were ever taken
+  uint32_t back = 0;          // and those that came back since
+  uint16_t returned[kKept];
   uint32_t streams = 0;
   struct {
     unsigned long long id;  // of the stream, never used again for another one
@@ -795,29 +798,74 @@ int work_error(int dev, uint32_t** err) {
   return st;
 }
 
-int work_slot(int dev, cudaStream_t s, bool captured, uint32_t** slot) {
-  if (dev < 0 || dev >= 64) return WCOMP_EUNSUPPORTED;
-  unsigned long long id = 0;
-  if (!captured) {
-    const cudaError_t e = cudaStreamGetId(s, &id);
-    if (e != cudaSuccess) return map_cuda(e);
-  }
+namespace {
+
+// A kept set comes back: the destructor of the object that its graphs hold, run
+// when the last of them is gone and its last launch has finished.  The object's
+// pointer is the device and the set.
+void CUDART_CB give_back(void* object) {
+  const uintptr_t v = reinterpret_cast<uintptr_t>(object);
   std::lock_guard<std::mutex> g(g_mu);
+  Work& w = g_work[v / kKept];
+  w.returned[w.back++] = uint16_t(v % kKept);
+}
+
+// A set that `graph`, under capture, keeps; null if there is none left.
+uint32_t* kept_set(int dev, cudaGraph_t graph) {
   Work& w = g_work[dev];
-  const int st = first_use(&w.sets, (kStreams + kKept) * kSlotWords * sizeof(uint32_t));
-  if (st != WCOMP_OK) return st;
+  uint64_t set;
+  {
+    std::lock_guard<std::mutex> g(g_mu);
+    if (w.back)
+      set = w.returned[--w.back];
+    else if (w.kept < kKept)
+      set = w.kept++;
+    else
+      return nullptr;
+  }
+  void* const object = reinterpret_cast<void*>(uintptr_t(dev) * kKept + set);
+  cudaUserObject_t o = nullptr;
+  if (cudaUserObjectCreate(&o, object, give_back, 1, cudaUserObjectNoDestructorSync) != cudaSuccess) {
+    cudaGetLastError();
+    give_back(object);
+    return nullptr;
+  }
+  if (cudaGraphRetainUserObject(graph, o, 1, cudaGraphUserObjectMove) != cudaSuccess) {
+    cudaGetLastError();
+    cudaUserObjectRelease(o, 1);  // gives it back
+    return nullptr;
+  }
+  return w.sets + (kStreams + set) * kSlotWords;
+}
+
+}  // namespace
+
+int work_slot(int dev, cudaStream_t s, uint32_t** slot) {
+  if (dev < 0 || dev >= 64) return WCOMP_EUNSUPPORTED;
   *slot = nullptr;
-  if (captured) {
-    if (w.kept < kKept) *slot = w.sets + (kStreams + w.kept++) * kSlotWords;
-    return WCOMP_OK;
+  Work& w = g_work[dev];
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  cudaGraph_t graph = nullptr;
+  cudaError_t e = cudaStreamGetCaptureInfo(s, &capture, nullptr, &graph);
+  if (e != cudaSuccess) return map_cuda(e);
+  unsigned long long id = 0;
+  if (capture == cudaStreamCaptureStatusNone && (e = cudaStreamGetId(s, &id)) != cudaSuccess) return map_cuda(e);
+  {
+    std::lock_guard<std::mutex> g(g_mu);
+    const int st = first_use(&w.sets, (kStreams + kKept) * kSlotWords * sizeof(uint32_t));
+    if (st != WCOMP_OK) return st;
+    if (capture == cudaStreamCaptureStatusNone) {
+      uint64_t i = id % (2 * kStreams);
+      while (w.table[i].set && w.table[i].id != id) i = (i + 1) % (2 * kStreams);  // half of the table stays empty
+      if (!w.table[i].set) {
+        if (w.streams == kStreams) return WCOMP_OK;
+        w.table[i] = {id, ++w.streams};
+      }
+      *slot = w.sets + uint64_t(w.table[i].set - 1) * kSlotWords;
+      return WCOMP_OK;
+    }
   }
-  uint64_t i = id % (2 * kStreams);
-  while (w.table[i].set && w.table[i].id != id) i = (i + 1) % (2 * kStreams);  // half of the table stays empty
-  if (!w.table[i].set) {
-    if (w.streams == kStreams) return WCOMP_OK;
-    w.table[i] = {id, ++w.streams};
-  }
-  *slot = w.sets + uint64_t(w.table[i].set - 1) * kSlotWords;
+  if (capture == cudaStreamCaptureStatusActive) *slot = kept_set(dev, graph);
   return WCOMP_OK;
 }
 

@@ -483,9 +483,9 @@ typedef struct {
  * of the call.  The counters of the barriers are allocated with cudaMalloc on
  * first use (20 MB; make the first call before any stream capture): a set for each
  * of the first 1024 streams that the device's calls are made on, and a set for
- * each of the first 4096 calls that are captured, so that calls on different
- * streams and graphs may run next to one another.  Others clear counters of their
- * own, which takes them 4 us longer.
+ * each of 4096 captured calls while their graphs are there, so that calls on
+ * different streams and graphs may run next to one another.  Others clear counters
+ * of their own, which takes them 4 us longer.
  */
 WCOMP_API int wcomp_moe(const wcomp_moe_args* args, void* stream);
 

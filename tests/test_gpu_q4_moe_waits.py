@@ -102,14 +102,20 @@ for turn in range(3):
     streams = [torch.cuda.Stream() for _ in layers]
     got = [[] for _ in layers]
     y.zero_()
-    for i, s in enumerate(streams):
+    under_way = torch.cuda.Event()
+    for s in streams:
         with torch.cuda.stream(s):
-            torch.cuda._sleep(2_000_000)
-            for _ in range(400):
+            torch.cuda._sleep(100_000_000)  # 50 ms, in which the calls are queued
+    for i in (1, 0):
+        with torch.cuda.stream(streams[i]):
+            for _ in range(100):
                 got[i].append(W.moe(*layers[i], 4))
+                if i == 0 and len(got[0]) == 5:
+                    under_way.record()
             if i == 0:
-                for _ in range(400):
+                for _ in range(100):
                     graph.replay()
+    under_way.synchronize()
     assert not streams[0].query()  # they are still at it
     assert L.wcomp_device_check(None) == W.ETIMEOUT
     torch.cuda.synchronize()
