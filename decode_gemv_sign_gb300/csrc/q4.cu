@@ -601,18 +601,22 @@ __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_const
 // Host side.
 // ---------------------------------------------------------------------------
 // Sets of counters: one for each of kStreams streams, whose launches follow one
-// another, then kKept that captured launches keep while their graph, or an
-// executable one made of it, is there.  (Sets in turn for launches on
-// any stream would be shared by two that run together when one stream is that
-// many launches ahead.)
-constexpr uint64_t kStreams = 1024, kKept = 4096;
+// another, then those of captured launches.  (Sets in turn for launches on any
+// stream would be shared by two that run together when one stream is that many
+// launches ahead.)  The first kKept captured launches keep theirs for good; the
+// next take kLent more, which come back with their graph.  What a graph holds for
+// that costs each of its launches 2.3 us and 0.14 us a call (2 of 8 experts of 1024
+// x 512 as a graph of one call, 16.9 -> 19.2 us), too much for the few graphs that
+// most programs make once, and less than clearing counters in the graph, 4 us a
+// call.
+constexpr uint64_t kStreams = 1024, kKept = 1024, kLent = 3072;
 std::mutex g_mu;
 struct Work {
   uint32_t* err = nullptr;
   uint32_t* sets = nullptr;
-  uint32_t kept = 0;          // of the kept sets, those that were ever taken
-  uint32_t back = 0;          // and those that came back since
-  uint16_t returned[kKept];
+  uint32_t taken = 0;         // of the captured launches' sets, how many were ever taken
+  uint32_t back = 0;          // lent ones that came back
+  uint16_t returned[kLent];
   uint32_t streams = 0;
   struct {
     unsigned long long id;  // of the stream, never used again for another one
@@ -800,30 +804,32 @@ int work_error(int dev, uint32_t** err) {
 
 namespace {
 
-// A kept set comes back: the destructor of the object that its graphs hold, run
+// A lent set comes back: the destructor of the object that its graphs hold, run
 // when the last of them is gone and its last launch has finished.  The object's
 // pointer is the device and the set.
 void CUDART_CB give_back(void* object) {
   const uintptr_t v = reinterpret_cast<uintptr_t>(object);
   std::lock_guard<std::mutex> g(g_mu);
-  Work& w = g_work[v / kKept];
-  w.returned[w.back++] = uint16_t(v % kKept);
+  Work& w = g_work[v / kLent];
+  w.returned[w.back++] = uint16_t(v % kLent);
 }
 
-// A set that `graph`, under capture, keeps; null if there is none left.
-uint32_t* kept_set(int dev, cudaGraph_t graph) {
+// A set for a launch captured in `graph`; null if there is none left.
+uint32_t* captured_set(int dev, cudaGraph_t graph) {
   Work& w = g_work[dev];
-  uint64_t set;
+  uint32_t* const first = w.sets + kStreams * kSlotWords;
+  uint64_t lent;
   {
     std::lock_guard<std::mutex> g(g_mu);
+    if (w.taken < kKept) return first + w.taken++ * kSlotWords;
     if (w.back)
-      set = w.returned[--w.back];
-    else if (w.kept < kKept)
-      set = w.kept++;
+      lent = w.returned[--w.back];
+    else if (w.taken < kKept + kLent)
+      lent = w.taken++ - kKept;
     else
       return nullptr;
   }
-  void* const object = reinterpret_cast<void*>(uintptr_t(dev) * kKept + set);
+  void* const object = reinterpret_cast<void*>(uintptr_t(dev) * kLent + lent);
   cudaUserObject_t o = nullptr;
   if (cudaUserObjectCreate(&o, object, give_back, 1, cudaUserObjectNoDestructorSync) != cudaSuccess) {
     cudaGetLastError();
@@ -835,7 +841,7 @@ uint32_t* kept_set(int dev, cudaGraph_t graph) {
     cudaUserObjectRelease(o, 1);  // gives it back
     return nullptr;
   }
-  return w.sets + (kStreams + set) * kSlotWords;
+  return first + (kKept + lent) * kSlotWords;
 }
 
 }  // namespace
@@ -852,7 +858,7 @@ int work_slot(int dev, cudaStream_t s, uint32_t** slot) {
   if (capture == cudaStreamCaptureStatusNone && (e = cudaStreamGetId(s, &id)) != cudaSuccess) return map_cuda(e);
   {
     std::lock_guard<std::mutex> g(g_mu);
-    const int st = first_use(&w.sets, (kStreams + kKept) * kSlotWords * sizeof(uint32_t));
+    const int st = first_use(&w.sets, (kStreams + kKept + kLent) * kSlotWords * sizeof(uint32_t));
     if (st != WCOMP_OK) return st;
     if (capture == cudaStreamCaptureStatusNone) {
       uint64_t i = id % (2 * kStreams);
@@ -865,7 +871,7 @@ int work_slot(int dev, cudaStream_t s, uint32_t** slot) {
       return WCOMP_OK;
     }
   }
-  if (capture == cudaStreamCaptureStatusActive) *slot = kept_set(dev, graph);
+  if (capture == cudaStreamCaptureStatusActive) *slot = captured_set(dev, graph);
   return WCOMP_OK;
 }
 

@@ -807,10 +807,10 @@ struct wcomp_q4 {
 namespace wc {
 // The 4-bit and expert kernels' error word on device `dev`, and kSlotWords zero
 // counters for a launch on stream s that crosses grid barriers, which it leaves
-// zero: the stream's, or, for a launch that is captured, its own as long as its
-// graph is there, since it may run next to any other as often as that does.  Null
-// when those are used up: the caller clears counters of its own in front of the
-// launch.  Defined in q4.cu.
+// zero: the stream's, or, for a launch that is captured, a set of its own as long
+// as its graph is there, since it may run next to any other as often as that
+// does.  Null when those are used up: the caller clears counters of its own in
+// front of the launch.  Defined in q4.cu.
 constexpr uint32_t kSlotWords = 1024;
 int work_error(int dev, uint32_t** err);
 int work_slot(int dev, cudaStream_t s, uint32_t** slot);
