@@ -150,10 +150,16 @@ def _check(status: int, what: str):
         raise WcompError(status, what)
 
 
+# The current stream's handle alone: making torch's stream object takes longer
+# than a small launch.  Not part of torch's documented interface, so it may be gone.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None) -> int:
     if stream is None:
-        # the handle alone: making torch's stream object takes longer than a small launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if _raw_stream is None:
+            return int(torch.cuda.current_stream().cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
