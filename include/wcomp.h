@@ -349,7 +349,7 @@ WCOMP_API void wcomp_free(wcomp_container* c, void* stream);
  *     consecutive columns of one row, the last one cut off at K.
  *   - A group holds a BF16 scale s and a 4-bit code c (0..15) per weight, which
  *     stands for (c - 8) * s.
- *   - Limits: N and K below 2^31, M * ceil(N / 16) below 2^31; beyond them
+ *   - Limits: M, N and K below 2^31, M * ceil(N / 32) below 2^31; beyond them
  *     WCOMP_EUNSUPPORTED.
  *   - A wcomp_q4 is immutable, owned by the library, lives on the device that
  *     was current when it was made (calls with it on another device return
@@ -362,7 +362,9 @@ typedef struct {
   int64_t M, N, K;
   int32_t group;
   int32_t pad_;
-  uint64_t bytes;  /* device memory: codes and scales, padded to 16 rows x 128 columns */
+  /* device memory: M * ceil(N / 32) * ceil(K / 256) blocks of 32 rows x 256
+     columns, each 4096 bytes of codes and 16384 / group bytes of scales */
+  uint64_t bytes;
 } wcomp_q4_info_t;
 
 /*

@@ -35,3 +35,17 @@ def test_products_keep_no_counters():
     assert r.returncode == 0, r.stderr[-4000:]
     print(r.stdout)
     assert int(r.stdout.split()[-1]) < 12 << 20, r.stdout
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("shape", [(1, 1), (32, 256), (33, 257), (3, 40, 300)])
+def test_the_size_of_a_held_weight(shape, group):
+    """M * ceil(N / 32) * ceil(K / 256) blocks of 4096 bytes of codes and 16384 / group of scales, as the header says."""
+    import torch
+
+    from decode_gemv_sign_gb300 import build, wcomp
+
+    build.build()
+    c = wcomp.q4_encode(torch.zeros(*shape, dtype=torch.bfloat16, device="cuda"), group)
+    M, N, K = (1, *shape)[-3:]
+    assert c.info()["bytes"] == M * -(-N // 32) * -(-K // 256) * (4096 + 16384 // group)
