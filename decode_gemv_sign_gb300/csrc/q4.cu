@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_const
 // x 512 as a graph of one call, 16.9 -> 19.2 us), too much for the few graphs that
 // most programs make once, and less than clearing counters in the graph, 4 us a
 // call.
-constexpr uint64_t kStreams = 1024, kKept = 1024, kLent = 3072;
+constexpr uint64_t kStreams = 1024, kKept = 1024, kLent = 4096;
 std::mutex g_mu;
 struct Work {
   uint32_t* err = nullptr;

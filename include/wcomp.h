@@ -483,9 +483,9 @@ typedef struct {
  * Memory: logits, hidden values, parts of sums and (unless x can be read as it
  * is) a copy of x come from the library's stream-ordered pool for the duration
  * of the call.  The counters of the barriers are allocated with cudaMalloc on
- * first use (20 MB; make the first call before any stream capture): a set for each
+ * first use (25 MB; make the first call before any stream capture): a set for each
  * of the first 1024 streams that the device's calls are made on, one for good for
- * each of the first 1024 captured calls, and one for each of 3072 others while
+ * each of the first 1024 captured calls, and one for each of 4096 others while
  * their graphs are there (which costs a graph's launch 2.3 us and 0.14 us a call),
  * so that calls on different streams and graphs may run next to one another.
  * Calls beyond these clear counters of their own, which takes them 4 us longer.

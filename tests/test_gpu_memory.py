@@ -30,7 +30,7 @@ print(before - torch.cuda.mem_get_info()[0])
 
 
 def test_products_keep_no_counters():
-    """4-bit products alone keep an error word (and their code, a few MB), not the expert layer's 20 MB of counters."""
+    """4-bit products alone keep an error word (and their code, a few MB), not the expert layer's 25 MB of counters."""
     r = subprocess.run([sys.executable, "-c", CHILD, ROOT], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-4000:]
     print(r.stdout)

@@ -94,7 +94,7 @@ def test_more_live_calls_than_sets(W, layer):
     args, want = layer
     streams = [torch.cuda.Stream() for _ in range(2)]
     ys = [torch.zeros_like(want) for _ in range(3)]
-    many = Graph(streams[0], lambda s: W.moe(*args, y=ys[0], stream=s), 4200)
+    many = Graph(streams[0], lambda s: W.moe(*args, y=ys[0], stream=s), 5400)
     over = Graph(streams[1], lambda s: W.moe(*args, y=ys[1], stream=s))
     few = over.nodes
     torch.cuda.synchronize()
