@@ -77,7 +77,9 @@ __device__ uint32_t g_debug_skip_first_copy;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSlots = 1024;   // work-counter slots per device (one per launch, round robin)
+// Work-counter pairs per device: one for each stream, then those that captured
+// launches and launches on further streams take in turn.
+constexpr uint32_t kTurns = 1 << 16, kSlots = StreamNumbers::kStreams + kTurns;
 constexpr int kRows = 16;      // weight rows per unit (the MMA's M side)
 constexpr int kKBlock = 128;   // columns per k-block (4 lanes x 32)
 constexpr int kCtasPerSm = 2;
@@ -1147,12 +1149,16 @@ __global__ void __launch_bounds__(kThreads) gemv_generic_kernel(const __grid_con
 // ---------------------------------------------------------------------------
 int pow2_batch(int B) { return B <= 1 ? 1 : B <= 2 ? 2 : B <= 4 ? 4 : B <= 8 ? 8 : 16; }
 
-// Per-device scratch: kSlots work-counter pairs, zeroed once at allocation;
-// each launch takes the next slot and its last CTA zeroes the slot again.
-// The word after the slots is the device error word.
+// Per-device scratch: kSlots work-counter pairs, zeroed once at allocation; a
+// launch's last CTA zeroes its pair again.  Launches that may run at the same time
+// need different pairs: a stream has one of its own, and a captured launch, which
+// may run next to any other as often as its graph does, one that no other gets
+// before kTurns more were captured.  The word after the pairs is the device error
+// word.
 std::mutex g_scratch_mu;
 uint32_t* g_scratch[64] = {nullptr};
-std::atomic<uint32_t> g_slot_rr{0};
+StreamNumbers g_streams[64];
+uint32_t g_turn[64] = {0};
 
 int scratch(int dev, uint32_t** base) {
   if (dev < 0 || dev >= 64) return WCOMP_EUNSUPPORTED;
@@ -1168,11 +1174,18 @@ int scratch(int dev, uint32_t** base) {
   return WCOMP_OK;
 }
 
-int counter_slot(int dev, uint32_t** slot) {
+int counter_slot(int dev, cudaStream_t s, uint32_t** slot) {
   uint32_t* base = nullptr;
   const int st = scratch(dev, &base);
   if (st != WCOMP_OK) return st;
-  *slot = base + 2 * (g_slot_rr.fetch_add(1, std::memory_order_relaxed) % kSlots);
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  cudaGraph_t graph = nullptr;
+  unsigned long long id = 0;
+  const cudaError_t e = stream_state(s, &capture, &graph, &id);
+  if (e != cudaSuccess) return map_cuda(e);
+  std::lock_guard<std::mutex> g(g_scratch_mu);
+  const int number = capture == cudaStreamCaptureStatusNone ? g_streams[dev].of(id) : -1;
+  *slot = base + 2 * (number >= 0 ? uint32_t(number) : StreamNumbers::kStreams + g_turn[dev]++ % kTurns);
   return WCOMP_OK;
 }
 
@@ -1267,7 +1280,7 @@ int launch(GemvBatch& b, const TmaBatch& tm, const int64_t* Ns, int B, int dev, 
   int st = scratch(dev, &base);
   if (st != WCOMP_OK) return st;
   uint32_t* slot = nullptr;
-  if ((st = counter_slot(dev, &slot)) != WCOMP_OK) return st;
+  if ((st = counter_slot(dev, s, &slot)) != WCOMP_OK) return st;
   const int per_sm = prepare_kernel<SRC, NT, XW>(dev);
   if (per_sm < 0) return map_cuda(cudaGetLastError());
   XtBatch xt;

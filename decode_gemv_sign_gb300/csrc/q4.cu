@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 2) q4_gemv_kernel(const __grid_const
 // x 512 as a graph of one call, 16.9 -> 19.2 us), too much for the few graphs that
 // most programs make once, and less than clearing counters in the graph, 4 us a
 // call.
-constexpr uint64_t kStreams = 1024, kKept = 1024, kLent = 4096;
+constexpr uint64_t kStreams = StreamNumbers::kStreams, kKept = 1024, kLent = 4096;
 std::mutex g_mu;
 struct Work {
   uint32_t* err = nullptr;
@@ -617,11 +617,7 @@ struct Work {
   uint32_t taken = 0;         // of the captured launches' sets, how many were ever taken
   uint32_t back = 0;          // lent ones that came back
   uint16_t returned[kLent];
-  uint32_t streams = 0;
-  struct {
-    unsigned long long id;  // of the stream, never used again for another one
-    uint32_t set;           // and 1
-  } table[2 * kStreams] = {};
+  StreamNumbers streams;
 } g_work[64];
 
 // Zeroed memory at *p, allocated on first use.
@@ -852,22 +848,16 @@ int work_slot(int dev, cudaStream_t s, uint32_t** slot) {
   Work& w = g_work[dev];
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
   cudaGraph_t graph = nullptr;
-  cudaError_t e = cudaStreamGetCaptureInfo(s, &capture, nullptr, &graph);
-  if (e != cudaSuccess) return map_cuda(e);
   unsigned long long id = 0;
-  if (capture == cudaStreamCaptureStatusNone && (e = cudaStreamGetId(s, &id)) != cudaSuccess) return map_cuda(e);
+  const cudaError_t e = stream_state(s, &capture, &graph, &id);
+  if (e != cudaSuccess) return map_cuda(e);
   {
     std::lock_guard<std::mutex> g(g_mu);
     const int st = first_use(&w.sets, (kStreams + kKept + kLent) * kSlotWords * sizeof(uint32_t));
     if (st != WCOMP_OK) return st;
     if (capture == cudaStreamCaptureStatusNone) {
-      uint64_t i = id % (2 * kStreams);
-      while (w.table[i].set && w.table[i].id != id) i = (i + 1) % (2 * kStreams);  // half of the table stays empty
-      if (!w.table[i].set) {
-        if (w.streams == kStreams) return WCOMP_OK;
-        w.table[i] = {id, ++w.streams};
-      }
-      *slot = w.sets + uint64_t(w.table[i].set - 1) * kSlotWords;
+      const int number = w.streams.of(id);
+      if (number >= 0) *slot = w.sets + uint64_t(number) * kSlotWords;
       return WCOMP_OK;
     }
   }
