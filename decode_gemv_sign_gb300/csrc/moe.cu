@@ -389,11 +389,8 @@ __device__ __forceinline__ void store_hidden(const MoeParams& p, uint32_t pair, 
 // expert's n pairs from p0 on, then the unit's sums: thread i gets output i +
 // 256 j (row i % 32, pair i / 32 + 8 j) as g[j] and u[j].  Up to 8 pairs take
 // gate and up steps in turn, so that x comes from L1 for one of them; more take
-// all gate steps, then all up steps, with one set of accumulators.  ONE: one copy
-// of the product's code for gate and up, for kernels with more products in them
-// (us one / two copies: 4 tokens, 8 of 128 4-bit experts of 6144 x 2048 122 / 117;
-// 16 tokens 341 / 367).
-template <class SRC, int TILES, bool ONE, class RING, class ISSUE>
+// all gate steps, then all up steps, with one set of accumulators.
+template <class SRC, int TILES, class RING, class ISSUE>
 __device__ __forceinline__ void gate_up(const MoeParams& p, const Lists& L, uint32_t p0, uint32_t n, uint32_t w0,
                                         uint32_t w1, RING& ring, int lane, int warp, uint32_t magic, float* share,
                                         ISSUE& issue, float (&g)[2], float (&u)[2]) {
@@ -407,23 +404,10 @@ __device__ __forceinline__ void gate_up(const MoeParams& p, const Lists& L, uint
     if (w0 < w1) {
       Product<SRC, 1, 1> prod;
       prod.begin(x, w0);
-      if constexpr (ONE) {  // through one copy of the code: the accumulators change places
 #pragma unroll 1
-        for (uint32_t i = 2 * w0; i < 2 * w1; ++i) {
-          prod.step(ring, i >> 1, i + 1 < 2 * w1 ? (i + 1) >> 1 : i >> 1, lane, magic, x, ag, issue);
-#pragma unroll
-          for (int v = 0; v < 8; ++v) {
-            const float was = ag[v >> 2][0][v & 3];
-            ag[v >> 2][0][v & 3] = au[v >> 2][0][v & 3];
-            au[v >> 2][0][v & 3] = was;
-          }
-        }
-      } else {
-#pragma unroll 1
-        for (uint32_t k = w0; k < w1; ++k) {
-          prod.step(ring, k, k, lane, magic, x, ag, issue);
-          prod.step(ring, k, k + 1 < w1 ? k + 1 : k, lane, magic, x, au, issue);
-        }
+      for (uint32_t k = w0; k < w1; ++k) {
+        prod.step(ring, k, k, lane, magic, x, ag, issue);
+        prod.step(ring, k, k + 1 < w1 ? k + 1 : k, lane, magic, x, au, issue);
       }
     }
     __syncthreads();  // what was in `share` is read
@@ -684,9 +668,9 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
         const uint32_t p0 = L.start[a], n = L.start[a + 1] - p0, w0 = s.w0(warp), w1 = s.w1(warp);
         float g[2], u[2];
         if (!WIDE || n <= 8)
-          gate_up<SRC, 1, WIDE>(p, L, p0, n, w0, w1, ring, lane, warp, magic, share, issue, g, u);
+          gate_up<SRC, 1>(p, L, p0, n, w0, w1, ring, lane, warp, magic, share, issue, g, u);
         else if constexpr (WIDE)
-          gate_up<SRC, 2, true>(p, L, p0, n, w0, w1, ring, lane, warp, magic, share, issue, g, u);
+          gate_up<SRC, 2>(p, L, p0, n, w0, w1, ring, lane, warp, magic, share, issue, g, u);
         auto hidden = [&](int j, float gv, float uv) {
           const uint32_t c = warp + 8 * j;
           if (c >= n) return;
