@@ -34,10 +34,11 @@
 //
 // Measured, us (in brackets the chosen weights' bytes at a plain copy's rate):
 // 8 of 128 experts of 6144 x 2048: one token BF16 108 (89), 4-bit with groups of
-// 128 49 (23), 16 tokens 4-bit with groups of 32 341 (258); 2 of 8 of 4096 x
-// 11008, 16 tokens, BF16 359 (316); 2 of 8 of 1024 x 512, one token 13.8 (0.9).
+// 128 50 (23), 16 tokens 4-bit with groups of 32 339 (258 for the experts chosen on
+// average, about 280 for these); 2 of 8 of 4096 x 11008, 16 tokens, BF16 347-360
+// (316); 2 of 8 of 1024 x 512, one token 13.6 (0.9).
 // Large layers are bound by the stream.  Small ones by the chain of phases: of
-// one token's 49 us with 4-bit experts, 3.5 are the router, 1.5 each barrier,
+// one token's 50 us with 4-bit experts, 3.5 are the router, 1.5 each barrier,
 // 2.4 the choice and the lists, 4 the first copies of B and C, and 6 the last
 // CTAs of B, of which some have two units and some one.
 #include <string.h>
@@ -628,7 +629,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
     // ---- B: gate and up
     const uint32_t ft_n = uint32_t(cdiv(p.F, kTileRows));
     {
-      const Cuts cuts(L.active * ft_n, uint32_t(cdiv(p.H, SRC::kCols)), gridDim.x, kJoinCopies / 2);
+      const Cuts cuts(L.active * ft_n, uint32_t(cdiv(p.H, SRC::kCols)), gridDim.x,
+                      kJoinCopies / 2);  // a k-step is two copies
       Parts ahead(cuts);
       // copies left: gate and up in turn, or (many pairs) all gate, then `iup` up
       uint32_t ileft = 0, iup = 0, ia = ahead.unit / ft_n, ift = ahead.unit - ia * ft_n;
@@ -707,9 +709,9 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
     // chosen experts, one expert after the other.
     {
       const uint32_t steps = uint32_t(cdiv(p.F, SRC::kCols));
-      // half of what a join costs elsewhere: a run of copies is longer here by each
-      // expert's beginning and end (us with whole / half the cost, 6 of 12 4-bit
-      // experts: 512 x 512, 4 tokens 20.6 / 18.7; 461 x 474, 16 tokens 30.9 / 28.3;
+      // a k-step is one copy, but half of a join's cost is taken: a run of copies is
+      // longer here by each expert's beginning and end (us with whole / half the cost,
+      // 6 of 12 4-bit experts: 512 x 512, 4 tokens 20.6 / 18.7; 461 x 474, 16 tokens 30.9 / 28.3;
       // with a quarter, 2 of 8 BF16 ones of 1024 x 512, 1 token: 13.7 -> 17.5)
       const Cuts cuts(uint32_t(cdiv(p.H, kTileRows)), L.active * steps, gridDim.x, kJoinCopies / 2);
       // the cursor's place: ileft k-steps to expert ia's or the warp's end, irest

@@ -411,15 +411,15 @@ __global__ void __launch_bounds__(kThreads) q4_unpack_kernel(const __grid_consta
 // plan() says.
 //
 // Measured on 16384 x 53248 (450 MB at groups of 128: 66 us at the rate of a
-// plain copy): 75.5 us for one row of x (0.88 of that rate), 77 for 4, 79.5 for
-// 8, 111 for 16; 86 and 129 for 8 and 16 rows at groups of 32.  Up to 8 rows what
-// is left is the start, the joins (5 us together) and each warp's chain through
-// some 120 instructions per KB, two thirds of them the codes' expansion: a k-step
-// takes a warp 1.0 us with 8 warps on half of the SMs, 1.6 with 16 on all, with
-// rings of any depth.  At 16 rows no unit is over half busy (tensor cores 42 %):
-// the latency of twice the MMAs with the 16 warps that 128 registers leave an SM.  x is not it (with all of it in
-// one line of L1 the time does not fall), nor are more warps (10 or 12 of a CTA
-// spill).
+// plain copy): 76 us for one row of x (0.87 of that rate), 77 for 4, 79.5 for
+// 8, 111 for 16; 90 and 133 for 8 and 16 rows at groups of 32 (73 us).  Up to 8
+// rows what is left is the start, the joins (5 us together) and each warp's chain
+// through some 120 instructions per KB, two thirds of them the codes' expansion: a
+// k-step takes a warp 1.0 us with 8 warps on half of the SMs, 1.6 with 16 on all,
+// with rings of any depth.  At 16 rows no unit is over half busy (tensor cores 43 %):
+// the latency of twice the MMAs with the 16 warps that 128 registers leave an SM.
+// x is not it (with all of it in one line of L1 the time does not fall), nor are
+// more warps (10 or 12 of a CTA spill).
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) q4_x_kernel(const uint16_t* __restrict__ x, uint64_t K, uint32_t recs, uint32_t B,
                                                    uint8_t* __restrict__ out, float* __restrict__ factors,
@@ -457,9 +457,9 @@ constexpr int kDepth = 2;  // stages of a warp: a third takes L1 from the activa
 // Records in shared memory: at most eight a warp, rows 16 bytes further apart
 // than their records, for the banks, then the factors.  For up to 8 rows of x
 // and one part of a unit a block.  us on the GPU / on the host for a kernel of
-// its own, and so: 2048 x 6144 6.4 / 6.7, 5.9 / 4.4; 1024 x 4096 4.9 / 6.7, 4.6 /
-// 4.4; 6144 x 6144 9.0 / 6.7, 9.4 / 4.3; with more units than blocks, 16384 x
-// 6144 15.7 / 6.7, 16.4 / 4.3.
+// its own, and so: 2048 x 6144 6.0 / 7.6, 5.4 / 4.5; 1024 x 4096 4.6 / 7.8, 4.3 /
+// 4.3; 6144 x 6144 8.8 / 7.1, 8.8 / 4.4; 2048 x 16384 in clusters 8.6 / 7.4, 8.8 /
+// 4.4; with more units than blocks it lost 0.7 us on the GPU (16384 x 6144).
 constexpr uint32_t kXRecords = 8 * kWarps;
 constexpr uint32_t kXShared = kXRecords * (kRecord + 16 + factor_pitch<1>() * 4);
 
@@ -693,13 +693,15 @@ int launch_gemv(GemvArgs& p, int dev, cudaStream_t s) {
 
 // How the units' k-steps fall on the CTAs: whole, cut anywhere and joined
 // through memory, or shared by clusters of 2 to 8 and joined through shared
-// memory: by the longest CTA's run in k-steps, eight of which its
-// warps take at once, and by what else each costs.  us whole / cut / shared by
-// clusters: 2048 x 6144 5.4 / 8.8 / 5.7; 4096 x 4096, 8 rows 6.0 / 10.8 / 7.1; 512
-// x 8192, 3 rows - / 6.5 / 4.9; 2048 x 16384 12.3 / 11.7 / 8.8; 256 x 40576, 7 rows
-// 26 / 10.7 / 7.7; 2048 x 16384, 16 rows - / 16.8 / 12.0; 6144 x 16384, 4 rows 17.1 / 18.0 / -; 16384 x 6144 15.2 / 18.7 /
-// -; 16384 x 53248 85 / 75.5 / -.
-constexpr uint32_t kCutCost = 40, kTeamCost = 16;  // k-steps; 8 are about 1 us
+// memory: by the longest CTA's run in k-steps, eight of which its warps take at
+// once, in 1 us where half of the SMs have work and 1.6 where all have, and by what
+// else each costs: a cut some 5 us on a half-filled GPU (2048 x 6144: 16 k-steps
+// fewer, 3.7 us longer) and 3 on a full one (6144 x 16384: 16 fewer, 0.6 longer).
+// us whole / cut / shared by clusters: 2048 x 6144 5.3 / 9.0 / 5.4; 4096 x 4096, 8
+// rows 6.1 / 11.3 / 7.0; 512 x 8192, 3 rows 6.9 / 6.4 / 5.0; 2048 x 16384 10.7 / 11.7 /
+// 8.8, 16 rows 15.8 / 16.4 / 12.0; 256 x 40576, 7 rows 24.9 / 10.0 / 7.7; 6144 x 16384,
+// 4 rows 17.7 / 18.3 / -; 16384 x 6144 14.2 / 17.7 / -; 16384 x 53248 82 / 76 / -.
+constexpr uint32_t kCutCost = 40, kTeamCost = 16;  // k-steps
 constexpr uint32_t kXCost = 8;                     // the kernel for x
 bool x_shared(const Cuts& c, int B, uint32_t ctas) {  // one part a CTA, of few records
   return B <= 8 && !c.split && c.units <= ctas && uint64_t(B) * 2 * cdiv32(c.steps, c.team) <= kXRecords;

@@ -7,17 +7,18 @@
 // with it: moving the weights is the bound, and the multiply has about 44
 // cycles of an SM per KB of weights before it falls behind the HBM.
 //
-// 4-bit weights enter the MMA as exact fp16 integers: a code under the
-// exponent of 1024 is 1024 + c in the low four mantissa bits and 1024 + 16 c in
-// the next four, so a word of eight codes takes one shift and four bit
-// operations, and four fused multiply-adds on the other pipe leave c - 8.
+// 4-bit weights enter the MMA as exact fp16 integers, by the method published for
+// matrix products of 4-bit and fp16 operands: a code under the exponent of 1024 is
+// 1024 + c in the low four mantissa bits and 1024 + 16 c in the next four, so a
+// word of eight codes takes one shift and four bit operations, and four fused
+// multiply-adds on the other pipe leave c - 8.
 // (BF16, with 7 mantissa bits, takes three shifts; a BF16 form of the GEMV ran
 // at 0.70 of the HBM rate with its integer pipe 55 % busy.  FP8 operands need
 // no arithmetic at all, but their warp-level MMA is converted to fp16 again:
 // 12 conversions each, slower in all.  Codes as fp16 subnormals need none
 // either, but the MMA aligns them by their exponent field and drops bits.)
 // The activations are BF16 values brought to fp16 by a power of two per 128
-// columns (records, below), which loses nothing.
+// columns (records, below), which loses nothing down to 2^-31 of the largest.
 #pragma once
 
 #include "host_shared.cuh"
@@ -606,7 +607,7 @@ struct Product {  // 4-bit
     ring.wait(lane);
     // unrolled, where registers allow, for the scheduler to find independent
     // work: a warp's own chain of dependencies is what bounds a step (us rolled /
-    // unrolled: 16384 x 53248, B = 1 78.5 / 75.6; two tiles, which spill: 111 / 117)
+    // unrolled: 16384 x 53248, B = 1 78.9 / 76.0, 8 83.1 / 79.4; two tiles, which spill: 111 / 117)
 #pragma unroll (TILES == 1 ? 2 : 1)
     for (uint32_t s = 0; s < 2; ++s) {
       const uint32_t rec = 2 * k + s, next = s ? 2 * kn : rec + 1;
@@ -689,7 +690,7 @@ __device__ __forceinline__ float warp_sums(const float* part, int warps, uint32_
 // CTAs: the result does not depend on which one that is.  Or, where there are few
 // units, each is shared by a `team` of CTAs (a cluster), the k-steps evenly.
 // ---------------------------------------------------------------------------
-constexpr uint32_t kJoinCopies = 24;  // what a join costs, in 4 KB copies of a CTA
+constexpr uint32_t kJoinCopies = 24;  // what a join of gate and up parts costs, in 4 KB copies of a CTA
 __host__ __device__ __forceinline__ uint32_t cdiv32(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
 struct Cuts {
   uint32_t units, steps, split, team = 1;

@@ -404,7 +404,9 @@ def deserialize(data: bytes, stream=None) -> Container:
 class Q4:
     """A weight in 4 bits with group scales, living on the GPU (owned by the library).
 
-    ``shape`` is (N, K), or (M, N, K) for M matrices held together.
+    ``shape`` is (N, K), or (M, N, K) for M matrices held together.  ``free``, and
+    dropping the last reference, return its memory in the order of the (current)
+    stream: have that wait for other streams whose calls still use the weight.
     """
 
     def __init__(self, handle: int, shape, group: int):

@@ -246,8 +246,8 @@ WCOMP_API int wcomp_gemv_batched(const wcomp_container* const* containers, const
  * static array, and the one of wcomp_q4_gemv and wcomp_moe).  A kernel whose
  * bounded wait on its own tensor copies, or on its other thread blocks, runs
  * out records it there and finishes without waiting instead of hanging; its
- * outputs are then undefined, those of other and later calls are not touched by
- * it nor by this check, which may be made while others run.  In a debug build (compiled with WCOMP_DEBUG=1)
+ * outputs are then undefined.  Those of other and later calls are not touched, by
+ * it or by this check, which may be made while others run.  In a debug build (compiled with WCOMP_DEBUG=1)
  * the kernels on containers and plain weights also check their indexes before
  * memory accesses, skip an access that fails and record it.  Synchronizes
  * `stream`.
@@ -469,12 +469,12 @@ typedef struct {
  *   weight[t, j] = factor * score, divided by the chosen scores' sum if
  *   renormalize;
  *   y[t] = sum_j weight[t, j] * down_j (silu(gate_j x[t]) * (up_j x[t])).
- * Sums and scores are in fp32 (experts whose scores are 0 there, logits of -104
- * under the largest or, for sigmoid, under zero, count as ties).  The hidden values between the products are held
- * as two BF16 parts (BF16 experts: 16 significant bits) or in fp16 under a power
- * of two for each 32 of them (4-bit experts: 11 bits, an eighth of a step of the
- * result; x as in wcomp_q4_gemv).  y is rounded once.  The order of the sums is
- * fixed: repeated calls give identical bits.
+ * Sums and scores are in fp32 (experts whose scores are 0 there, from logits of
+ * 104 under the largest or, for sigmoid, under zero on, count as ties).  The hidden
+ * values between the products are held as two BF16 parts (BF16 experts: 16
+ * significant bits) or in fp16 under a power of two for each 32 of them (4-bit
+ * experts: 11 bits, an eighth of a step of the result; x as in wcomp_q4_gemv).  y is
+ * rounded once.  The order of the sums is fixed: repeated calls give identical bits.
  * 1 <= top_k <= min(E, 16), E <= 1024, H and F at most 2^24 (beyond:
  * WCOMP_EUNSUPPORTED).  Any alignment and widths; BF16 experts with H % 8 == 0,
  * F % 8 == 0 and 16-byte aligned weights are copied in boxes through tensor
