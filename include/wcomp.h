@@ -173,12 +173,12 @@ WCOMP_API int wcomp_decode(const wcomp_container* c, uint16_t* d_out, void* stre
  * contract.
  * Memory: the work counters live in a device buffer the library allocates
  * with cudaMalloc on first use per device (0.5 MB): a pair for each of the
- * first 1024 streams, and 65536 that captured calls take in turn, so that
- * calls on different streams and graphs may run next to one another (a graph
- * next to one captured 65536 calls later may not); a K15 container at B >= 3 also
- * takes a transposed copy of x (K * 4..16 * 2 bytes) from the library's
- * stream-ordered pool for the duration of the call.  wcomp_gemv_noalloc
- * allocates nothing.
+ * first 1024 streams, and 65536 that captured calls (and calls on further
+ * streams) take in turn, so that calls on different streams and graphs may run
+ * next to one another (a graph next to one captured 65536 calls later may not).
+ * A K15 container at B >= 3 also takes a transposed copy of x (K * 4..16 * 2
+ * bytes) from the library's stream-ordered pool for the duration of the call.
+ * wcomp_gemv_noalloc allocates nothing.
  * Errors found on the device (a copy that never completed) do not fail the
  * call: the kernel records them and stops waiting; wcomp_device_check
  * reports them.
