@@ -1484,7 +1484,7 @@ extern "C" int wcomp_device_check(void* stream) {
   if (st != WCOMP_OK) return st;
   uint32_t* words[3] = {base + 2 * kSlots, noalloc_error_word(dev), work_error_word(dev)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  bool failed = false;
+  uint32_t found = 0;
   for (uint32_t* w : words) {
     if (!w) continue;
     uint32_t word = 0;
@@ -1492,7 +1492,7 @@ extern "C" int wcomp_device_check(void* stream) {
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return map_cuda(e);
     if (word) {
-      failed = true;
+      found |= w == words[2] ? word : 1u;
       // nothing but the word: the kernels leave their counters in order, and
       // others may be running on them
       e = cudaMemsetAsync(w, 0, sizeof(uint32_t), s);
@@ -1500,9 +1500,9 @@ extern "C" int wcomp_device_check(void* stream) {
       if (e != cudaSuccess) return map_cuda(e);
     }
   }
-  if (failed) return WCOMP_ETIMEOUT;
+  if (found & 1u) return WCOMP_ETIMEOUT;
   const uint32_t dbg = debug_take_decode() | debug_take_encode() | debug_take_gemv();
-  return dbg ? WCOMP_EBOUNDS : WCOMP_OK;
+  return dbg || (found & kErrBounds) ? WCOMP_EBOUNDS : WCOMP_OK;
 }
 
 extern "C" int wcomp_debug_skip_first_copy(int on) {

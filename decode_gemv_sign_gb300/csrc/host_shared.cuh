@@ -41,8 +41,10 @@ inline cudaError_t stream_state(cudaStream_t s, cudaStreamCaptureStatus* capture
   const cudaError_t e = cudaStreamGetCaptureInfo(s, capture, nullptr, graph);
   return e != cudaSuccess || *capture != cudaStreamCaptureStatusNone ? e : cudaStreamGetId(s, id);
 }
-// The expert and 4-bit kernels' error word on device `dev`, null before their
-// first use (q4.cu).
+// The error word of the expert and 4-bit kernels on device `dev`, null before their
+// first use (q4.cu): bit 0 a wait that ran out, kErrBounds an index of the 4-bit
+// cache's calls that was out of range.
+constexpr uint32_t kErrBounds = 2;
 uint32_t* work_error_word(int dev);
 // Debug builds: which test hooks the launches of q4.cu and moe.cu follow.
 cudaError_t debug_hooks_q4(uint32_t bits);

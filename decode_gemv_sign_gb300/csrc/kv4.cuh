@@ -1,0 +1,99 @@
+// The 4-bit key/value cache: its layout, and where a call's rows stand in it.
+// Shared by the calls that write and read it (kv4.cu) and by the attention over
+// it (kv4_attend.cu).
+#pragma once
+
+#include "tile.cuh"
+
+struct wcomp_kv4 {
+  int64_t pages = 0;
+  int heads = 0, dim = 0;
+  int device = 0;
+  uint8_t* d = nullptr;
+};
+
+namespace wc {
+
+constexpr int kPage = 64;       // tokens of a page
+constexpr int kKvGroup = 32;    // columns that share a scale
+
+// A page holds one block per head: 64 rows of key codes, 64 rows of value codes
+// (dim / 2 bytes each), the key scales [dim / 32][64] and the value scales
+// [dim / 32][64], BF16.  A block is one bulk copy of the attention and a multiple
+// of 128 bytes; a row is made of whole 16-byte pieces, so that a token can be
+// written and moved by itself.
+//
+// In a key row the 8 columns 32 g + 8 q .. + 7 are the word q * G + g (G = dim /
+// 32; column i of them in bits 4 i .. 4 i + 3): lane q of a quad of the MMA finds its
+// columns of every group in consecutive words.  In a value row word r * G / 2 + a
+// holds the columns 64 a + 4 r .. + 3 in its low and 64 a + 32 + 4 r .. + 3 in its
+// high half: lane r of the MMA's eight rows finds its columns of every group in
+// consecutive words.
+//
+// The attention's lane (r, q) reads the key row of token 16 (r / 2) + 2 j + r % 2
+// and the value rows of the tokens 16 q + i; a token's row is swizzled so that
+// both spread over all banks.
+template <int D>
+struct Kv {
+  static constexpr int G = D / kKvGroup;
+  static constexpr uint32_t kRow = D / 2;
+  static constexpr uint32_t kCodes = kPage * kRow;
+  static constexpr uint32_t kScales = G * kPage * 2;
+  static constexpr uint32_t kBlock = 2 * (kCodes + kScales);
+  static constexpr uint32_t kKeyScales = 2 * kCodes, kValueScales = 2 * kCodes + kScales;
+  // Byte b of token t's row, from the start of the keys or the values.
+  static __host__ __device__ __forceinline__ uint32_t at(uint32_t t, uint32_t b) {
+    const uint32_t turn = ((t >> 5) & 1) | ((t >> 3) & 2);  // the two bits of t / 16, exchanged
+    return (t * kRow + b) ^ (turn << 5) ^ (D == 256 ? (t & 1) << 4 : 0);
+  }
+  static __host__ __device__ __forceinline__ uint32_t scale(uint32_t t, uint32_t g) { return 2 * (g * kPage + t); }
+};
+
+// The rows of a call (wcomp_kv4_seqs) on the device.
+struct KvSeqs {
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* starts;  // or null
+  int B, width;
+  uint32_t pages, heads;  // of the cache
+  uint32_t* err;
+};
+
+__device__ __forceinline__ void kv_bad(uint32_t* err) { atomicOr(err, kErrBounds); }
+
+// Tokens that sequence b holds.
+__device__ __forceinline__ int kv_length(const KvSeqs& s, int b) {
+  const int n = s.lengths[b];
+  if (n <= s.width * kPage) return n < 0 ? 0 : n;
+  kv_bad(s.err);
+  return s.width * kPage;
+}
+// Page number `at` of sequence b, -1 if there is no such page.
+__device__ __forceinline__ int kv_page(const KvSeqs& s, int b, int at) {
+  const int p = s.table[int64_t(b) * s.width + at];
+  if (uint32_t(p) < s.pages) return p;
+  kv_bad(s.err);
+  return -1;
+}
+// Sequence of row i, or -1.
+__device__ __forceinline__ int kv_sequence(const KvSeqs& s, int64_t i) {
+  if (!s.starts) return i < s.B ? int(i) : -1;
+  if (i < s.starts[0] || i >= s.starts[s.B]) return -1;
+  int lo = 0, hi = s.B;  // starts[lo] <= i < starts[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s.starts[mid] <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+// Position of row i of sequence b, which holds n tokens; below 0: none.
+__device__ __forceinline__ int64_t kv_position(const KvSeqs& s, int b, int64_t i, int n) {
+  return s.starts ? int64_t(n) - (s.starts[b + 1] - i) : int64_t(n) - 1;
+}
+
+// Checks of a call's sequences on the host.
+int kv_check(const wcomp_kv4* c, const wcomp_kv4_seqs& s, int64_t T);
+int kv_seqs(const wcomp_kv4* c, const wcomp_kv4_seqs& s, KvSeqs* out);
+
+}  // namespace wc

@@ -61,6 +61,39 @@ class Q4Info(ctypes.Structure):
         return {k: getattr(self, k) for k, _ in self._fields_ if k != "pad_"}
 
 
+class Kv4Info(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int64), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("bytes", ctypes.c_uint64)]
+
+    def as_dict(self) -> dict:
+        return {k: getattr(self, k) for k, _ in self._fields_}
+
+
+class Kv4Seqs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("d_table", "d_lengths", "d_starts")] + [
+        ("B", ctypes.c_int32), ("width", ctypes.c_int32)]
+
+
+class Kv4AttendArgs(ctypes.Structure):
+    _fields_ = [("s", Kv4Seqs), ("d_q", ctypes.c_void_p), ("q_row", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("d_out", ctypes.c_void_p), ("d_lse", ctypes.c_void_p), ("d_mass", ctypes.c_void_p),
+                ("T", ctypes.c_int64), ("q_heads", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class Kv4EvictArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("d_table", "d_lengths", "d_mass", "d_table_out", "d_lengths_out",
+                                               "d_mass_out", "d_kept")] + [
+        (n, ctypes.c_int32) for n in ("B", "width", "width_out", "keep", "recent")]
+
+
+class LogprobsArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("d_logits", "d_ids", "d_logprob", "d_entropy", "d_lse",
+                                               "d_top_logprobs", "d_top_ids")] + [
+        ("T", ctypes.c_int64), ("V", ctypes.c_int64), ("row", ctypes.c_int64), ("dtype", ctypes.c_int32),
+        ("top_k", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 class MoeArgs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("d_x", "d_router", "d_bias", "d_gate", "d_up", "d_down", "q4_gate",
                                                "q4_up", "q4_down", "d_y", "d_ids", "d_weights")] + [
@@ -122,6 +155,16 @@ def lib():
     L.wcomp_q4_free.argtypes = [P, P]
     L.wcomp_q4_free.restype = None
     L.wcomp_moe.argtypes = [ctypes.POINTER(MoeArgs), P]
+    L.wcomp_kv4_create.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int, P, ctypes.POINTER(P)]
+    L.wcomp_kv4_append.argtypes = [P, ctypes.POINTER(Kv4Seqs), P, ctypes.c_int64, ctypes.c_int64, P, ctypes.c_int64,
+                                   ctypes.c_int64, ctypes.c_int64, P]
+    L.wcomp_kv4_read.argtypes = [P, ctypes.POINTER(Kv4Seqs), P, P, ctypes.c_int64, P]
+    L.wcomp_kv4_attend.argtypes = [P, ctypes.POINTER(Kv4AttendArgs), P]
+    L.wcomp_kv4_evict.argtypes = [P, ctypes.POINTER(Kv4EvictArgs), P]
+    L.wcomp_kv4_info.argtypes = [P, ctypes.POINTER(Kv4Info)]
+    L.wcomp_kv4_free.argtypes = [P, P]
+    L.wcomp_kv4_free.restype = None
+    L.wcomp_logprobs.argtypes = [ctypes.POINTER(LogprobsArgs), P]
     L.wcomp_launch_count.argtypes = []
     L.wcomp_launch_count.restype = ctypes.c_uint64
     for name in ("wcomp_encode", "wcomp_encode_batched", "wcomp_encode_hist_grid", "wcomp_decode", "wcomp_gemv", "wcomp_gemv_noalloc",
@@ -130,7 +173,8 @@ def lib():
                  "wcomp_gemv_batched", "wcomp_info", "wcomp_serialize", "wcomp_serialize_compact",
                  "wcomp_deserialize", "wcomp_version", "wcomp_debug_skip_first_copy", "wcomp_q4_encode",
                  "wcomp_q4_pack", "wcomp_q4_unpack", "wcomp_q4_decode", "wcomp_q4_gemv", "wcomp_q4_info",
-                 "wcomp_moe"):
+                 "wcomp_moe", "wcomp_kv4_create", "wcomp_kv4_append", "wcomp_kv4_read", "wcomp_kv4_attend",
+                 "wcomp_kv4_evict", "wcomp_kv4_info", "wcomp_logprobs"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -564,6 +608,207 @@ def moe(x: torch.Tensor, router: torch.Tensor, gate, up, down, top_k: int, *, sc
                 H, F, T, E, top_k, SCORING[scoring], renormalize, factor)
     _check(lib().wcomp_moe(ctypes.byref(a), _stream(stream)), "wcomp_moe")
     return y
+
+
+class KV4:
+    """A cache of keys and values in 4 bits, living on the GPU (owned by the library).
+
+    ``pages`` pages of 64 tokens with ``heads`` rows of ``dim`` columns of keys and of values each, one BF16
+    scale per 32 columns.  ``free``, and dropping the last reference, return its memory in the order of the
+    (current) stream: have that wait for other streams whose calls still use the cache.
+
+    The calls on it take ``table`` (int32 [B, width]: the pages of each sequence; position p is place p % 64 of
+    page table[b, p // 64]), ``lengths`` (int32 [B]: the tokens that each sequence holds, the call's own rows
+    among them) and ``starts`` (int32 [B + 1]: rows starts[b] to starts[b + 1] - 1 are the newest tokens of
+    sequence b; None: one row a sequence).  All three are on the device; a page, length or row out of range is
+    skipped there and reported by ``device_check``.
+    """
+
+    def __init__(self, handle: int, pages: int, heads: int, dim: int, device: torch.device):
+        self._h = handle
+        self.pages, self.heads, self.dim, self.device = pages, heads, dim, device
+
+    @property
+    def handle(self) -> int:
+        if not self._h:
+            raise ValueError("cache was freed")
+        return self._h
+
+    def info(self) -> dict:
+        inf = Kv4Info()
+        _check(lib().wcomp_kv4_info(self.handle, ctypes.byref(inf)), "wcomp_kv4_info")
+        return inf.as_dict()
+
+    def free(self, stream=None):
+        if self._h:
+            lib().wcomp_kv4_free(self._h, _stream(stream))
+            self._h = 0
+
+    def __del__(self):
+        try:
+            if self._h and torch.cuda.is_available():
+                self.free()
+        except Exception:
+            pass
+
+
+def kv4_create(pages: int, heads: int, dim: int, stream=None) -> KV4:
+    """A new cache on the current device; ``dim`` is 64, 128 or 256.  Its rows read as zeros."""
+    h = P()
+    _check(lib().wcomp_kv4_create(pages, heads, dim, _stream(stream), ctypes.byref(h)), "wcomp_kv4_create")
+    return KV4(h.value, pages, heads, dim, torch.device("cuda", torch.cuda.current_device()))
+
+
+def _array(t: torch.Tensor, what: str, dtype: torch.dtype, shape: tuple, device: torch.device) -> int:
+    """The address of a contiguous tensor of that type and shape on that device."""
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype or not t.is_contiguous() \
+            or t.shape != shape:
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {list(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _kv4_seqs(c: KV4, table: torch.Tensor, lengths: torch.Tensor, starts: Optional[torch.Tensor]) -> Kv4Seqs:
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be [B, width]")
+    B, width = table.shape
+    return Kv4Seqs(_array(table, "table", torch.int32, (B, width), c.device),
+                   _array(lengths, "lengths", torch.int32, (B,), c.device),
+                   None if starts is None else _array(starts, "starts", torch.int32, (B + 1,), c.device), B, width)
+
+
+def _kv4_rows(c: KV4, t: torch.Tensor, what: str, heads: Optional[int] = None) -> tuple:
+    """Address and strides of BF16 rows [T, heads, dim] whose columns are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.device != c.device:
+        raise TypeError(f"{what} must be a CUDA tensor on {c.device}")
+    if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+        raise TypeError(f"{what} must hold BF16 bits (bfloat16, int16 or uint16), got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != c.dim or t.stride(2) != 1 or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{what} must be [T, {'heads' if heads is None else heads}, {c.dim}] with contiguous columns")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def kv4_append(c: KV4, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor,
+               starts: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Quantise rows k, v [T, heads, dim] (BF16, any strides between rows and heads) into the cache."""
+    s = _kv4_seqs(c, table, lengths, starts)
+    kp, vp = _kv4_rows(c, k, "k", c.heads), _kv4_rows(c, v, "v", c.heads)
+    T = k.shape[0]
+    if v.shape[0] != T or (starts is None and T != s.B):
+        raise ValueError("k and v must have the same rows, one a sequence without starts")
+    _check(lib().wcomp_kv4_append(c.handle, ctypes.byref(s), *kp, *vp, T, _stream(stream)), "wcomp_kv4_append")
+
+
+def kv4_read(c: KV4, table: torch.Tensor, lengths: torch.Tensor, starts: Optional[torch.Tensor] = None, *,
+             rows: Optional[int] = None, k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+             stream=None) -> tuple:
+    """(k, v): the newest tokens of each sequence as BF16 rows [rows, heads, dim].
+
+    ``rows`` is starts[B] (the number of sequences without starts).  Rows without a position read as zeros; rows
+    of ``k`` and ``v``, where they are given, that belong to no sequence are left as they were.
+    """
+    s = _kv4_seqs(c, table, lengths, starts)
+    if rows is None:
+        given = k if k is not None else v
+        if given is None and starts is not None:
+            raise ValueError("rows must be given with starts")
+        rows = s.B if given is None else given.shape[0]
+    if starts is None and rows != s.B:
+        raise ValueError("without starts there is one row a sequence")
+    shape = (rows, c.heads, c.dim)
+    k, v = (torch.empty(shape, dtype=torch.bfloat16, device=c.device) if t is None else t for t in (k, v))
+    _check(lib().wcomp_kv4_read(c.handle, ctypes.byref(s), _array(_bits16(k, "k"), "k", k.dtype, shape, c.device),
+                                _array(_bits16(v, "v"), "v", v.dtype, shape, c.device), rows, _stream(stream)),
+           "wcomp_kv4_read")
+    return k, v
+
+
+def kv4_attend(c: KV4, q: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor,
+               starts: Optional[torch.Tensor] = None, *, scale: Optional[float] = None, window: int = 0,
+               out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+               mass: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of query rows q [T, q_heads, dim] over the cache: BF16 rows of the same shape.
+
+    Each row sees the tokens of its sequence up to its own position (append its keys and values first), the last
+    ``window`` of them if that is not 0.  ``scale`` is dim ** -0.5 by default.  ``lse`` (float32 [T, q_heads])
+    receives the log of the sum of exponentials, and ``mass`` (float32 [B, heads, width * 64]) is added the
+    attention weight of each cached token, as ``kv4_evict`` takes it.  A row that sees nothing gets zeros.
+    """
+    s = _kv4_seqs(c, table, lengths, starts)
+    qp = _kv4_rows(c, q, "q")
+    T, Hq = q.shape[:2]
+    if Hq < 1 or Hq % c.heads or (starts is None and T != s.B):
+        raise ValueError("q must have a multiple of the cache's heads, and one row a sequence without starts")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=c.device)
+    a = Kv4AttendArgs(s, *qp, _array(_bits16(out, "out"), "out", out.dtype, (T, Hq, c.dim), c.device),
+                      None if lse is None else _array(lse, "lse", torch.float32, (T, Hq), c.device),
+                      None if mass is None else _array(mass, "mass", torch.float32, (s.B, c.heads, s.width * 64),
+                                                       c.device),
+                      T, Hq, window, c.dim ** -0.5 if scale is None else scale)
+    _check(lib().wcomp_kv4_attend(c.handle, ctypes.byref(a), _stream(stream)), "wcomp_kv4_attend")
+    return out
+
+
+def kv4_evict(c: KV4, table: torch.Tensor, lengths: torch.Tensor, mass: torch.Tensor, keep: int, recent: int,
+              table_out: torch.Tensor, *, lengths_out: Optional[torch.Tensor] = None,
+              mass_out: Optional[torch.Tensor] = None, kept: Optional[torch.Tensor] = None, stream=None) -> tuple:
+    """Bring sequences down to ``keep`` tokens a head: the last ``recent`` and those of largest ``mass``.
+
+    They are copied in their order to the pages of ``table_out`` (int32 [B, width_out], none of them in
+    ``table``).  Returns (lengths, mass) of the sequences there, as the other calls take them.  ``kept``
+    (int32 [B, heads, keep]) receives the positions that were kept, then -1.
+    """
+    s = _kv4_seqs(c, table, lengths, None)
+    if not isinstance(table_out, torch.Tensor) or table_out.dim() != 2:
+        raise ValueError("table_out must be [B, width_out]")
+    wide = table_out.shape[1]
+    if keep < 1 or not 0 <= recent <= keep or wide * 64 < keep:
+        raise ValueError("keep must be above 0, recent within 0..keep, and table_out have pages for keep tokens")
+    if lengths_out is None:
+        lengths_out = torch.empty_like(lengths)
+    if mass_out is None:
+        mass_out = torch.empty((s.B, c.heads, wide * 64), dtype=torch.float32, device=c.device)
+    a = Kv4EvictArgs(s.d_table, s.d_lengths,
+                     _array(mass, "mass", torch.float32, (s.B, c.heads, s.width * 64), c.device),
+                     _array(table_out, "table_out", torch.int32, (s.B, wide), c.device),
+                     _array(lengths_out, "lengths_out", torch.int32, (s.B,), c.device),
+                     _array(mass_out, "mass_out", torch.float32, (s.B, c.heads, wide * 64), c.device),
+                     None if kept is None else _array(kept, "kept", torch.int32, (s.B, c.heads, keep), c.device),
+                     s.B, s.width, wide, keep, recent)
+    _check(lib().wcomp_kv4_evict(c.handle, ctypes.byref(a), _stream(stream)), "wcomp_kv4_evict")
+    return lengths_out, mass_out
+
+
+def logprobs(logits: torch.Tensor, ids: Optional[torch.Tensor] = None, top_k: int = 0, *, scale: float = 1.0,
+             lse: Optional[torch.Tensor] = None, stream=None) -> tuple:
+    """(logprob [T], entropy [T], top_logprobs [T, top_k], top_ids [T, top_k]) of logits [T, V] times ``scale``.
+
+    ``logits`` are float32 (what ``gemv`` gives) or bfloat16, a row's columns contiguous; ``ids`` (int64 [T]) are
+    the given tokens: a negative one gets logprob 0, one beyond the vocabulary NaN.  logprob is None without
+    ids.  ``top_k`` (at most 64) alternatives, the largest first, ties by the lowest index; ids are int32.
+    ``lse`` (float32 [T]) receives the log of the sum of exponentials.
+    """
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise TypeError("logits must be a CUDA tensor")
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [T, V] with contiguous columns")
+    if top_k < 0 or top_k > logits.shape[1]:
+        raise ValueError("top_k must be within 0..V")
+    (T, V), dev = logits.shape, logits.device
+    row = logits.stride(0) if T > 1 else V
+    entropy = torch.empty(T, dtype=torch.float32, device=dev)
+    logprob = None if ids is None else torch.empty(T, dtype=torch.float32, device=dev)
+    top = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    top_ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    a = LogprobsArgs(logits.data_ptr(), None if ids is None else _array(ids, "ids", torch.int64, (T,), dev),
+                     None if ids is None else logprob.data_ptr(), entropy.data_ptr(),
+                     None if lse is None else _array(lse, "lse", torch.float32, (T,), dev),
+                     top.data_ptr() if top_k else None, top_ids.data_ptr() if top_k else None, T, V, row,
+                     0 if logits.dtype == torch.float32 else 1, top_k, scale)
+    _check(lib().wcomp_logprobs(ctypes.byref(a), _stream(stream)), "wcomp_logprobs")
+    return logprob, entropy, top, top_ids
 
 
 def version() -> int:

@@ -70,7 +70,8 @@ typedef enum {
   WCOMP_EUNSUPPORTED = -5,  /* size outside the supported range */
   WCOMP_ETIMEOUT = -6,      /* a kernel's bounded wait on its own copies ran out */
   WCOMP_EINTERNAL = -7,     /* an internal consistency check failed; no result was returned */
-  WCOMP_EBOUNDS = -8        /* a debug build's index check failed inside a kernel (the access was skipped) */
+  WCOMP_EBOUNDS = -8        /* an index check failed inside a kernel (the access was skipped): in a debug build, or
+                               a page, length or row of the 4-bit cache's calls outside its range */
 } wcomp_status;
 
 typedef struct wcomp_container wcomp_container;
@@ -243,11 +244,12 @@ WCOMP_API int wcomp_gemv_batched(const wcomp_container* const* containers, const
 /*
  * Report and clear the device error words of the current device (the one
  * wcomp_gemv and the batched GEMVs use, the one in wcomp_gemv_noalloc's
- * static array, and the one of wcomp_q4_gemv and wcomp_moe).  A kernel whose
+ * static array, and the one of wcomp_q4_gemv, wcomp_moe and wcomp_kv4_*).  A kernel whose
  * bounded wait on its own tensor copies, or on its other thread blocks, runs
  * out records it there and finishes without waiting instead of hanging; its
- * outputs are then undefined.  Those of other and later calls are not touched, by
- * it or by this check, which may be made while others run.  In a debug build (compiled with WCOMP_DEBUG=1)
+ * outputs are then undefined.  The calls on a 4-bit key/value cache record there
+ * a page, length or row that is out of range.  Other and later calls are not
+ * touched, by it or by this check, which may be made while others run.  In a debug build (compiled with WCOMP_DEBUG=1)
  * the kernels on containers and plain weights also check their indexes before
  * memory accesses, skip an access that fails and record it.  Synchronizes
  * `stream`.
@@ -494,6 +496,175 @@ typedef struct {
  * Calls beyond these clear counters of their own, which takes them 4 us longer.
  */
 WCOMP_API int wcomp_moe(const wcomp_moe_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A cache of keys and values in 4 bits, and attention over it.
+ *
+ *   - A cache is `pages` pages of 64 tokens; each holds, for every one of `heads`
+ *     heads, 64 rows of keys and 64 rows of values of `dim` columns (64, 128 or
+ *     256).  A row is held as the 4-bit weights above are, in groups of 32
+ *     columns: a code c in 0..15 stands for (c - 8) * s, s the group's BF16 scale
+ *     (72 * dim bytes for a page and head: 4.5 bits a value).
+ *   - Which pages hold a sequence's tokens is the caller's choice: position p of
+ *     sequence b is in page table[b][p / 64], place p % 64.  Sequences may share
+ *     pages that are only read.
+ *   - A cache is owned by the library, lives on the device that was current when
+ *     it was made (calls on another device return WCOMP_EINVAL), takes its memory
+ *     from the library's stream-ordered pool, and is released with wcomp_kv4_free.
+ *     Calls that write to it are ordered by the caller against others on it, as
+ *     for any buffer.
+ *   - Limits: pages * heads below 2^31, B, rows and width * 64 below 2^31; beyond
+ *     them WCOMP_EUNSUPPORTED.
+ * ------------------------------------------------------------------------ */
+typedef struct wcomp_kv4 wcomp_kv4;
+
+typedef struct {
+  int64_t pages;
+  int32_t heads, dim;
+  uint64_t bytes; /* device memory: pages * heads * 72 * dim */
+} wcomp_kv4_info_t;
+
+/*
+ * The sequences that a call deals with, all on the device.  A call has T rows
+ * (of keys, values or queries): rows starts[b] .. starts[b + 1] - 1 belong to
+ * sequence b and are its newest tokens, so row starts[b + 1] - 1 - i stands at
+ * position lengths[b] - 1 - i.  With d_starts == NULL every sequence has one row
+ * (T == B).  A row whose position is negative has no place: nothing is written
+ * for it to the cache, it reads as zeros, and its attention is empty.  Rows that
+ * are no sequence's (from starts[B] on) are left as they were.
+ * What cannot be checked on the host is checked in the kernels: a length above
+ * width * 64 is taken as width * 64, a page outside the cache as if its tokens
+ * were not there, and wcomp_device_check then reports WCOMP_EBOUNDS.
+ */
+typedef struct {
+  const int32_t* d_table;   /* [B, width] pages */
+  const int32_t* d_lengths; /* [B] tokens that each sequence holds, the call's rows among them */
+  const int32_t* d_starts;  /* [B + 1], ascending from 0, or NULL */
+  int32_t B, width;
+} wcomp_kv4_seqs;
+
+/* A new cache whose rows read as zeros. */
+WCOMP_API int wcomp_kv4_create(int64_t pages, int heads, int dim, void* stream, wcomp_kv4** out);
+
+/*
+ * Quantise T rows of keys and values into their places, by the rule of
+ * wcomp_q4_encode for groups of 32 columns.  d_k, d_v: BF16 bits, [T, heads, dim] with
+ * the columns of a row contiguous and the given strides (in elements) between
+ * rows and between heads; any alignment (16-byte aligned rows are read faster).
+ * A place that two rows of one call share (pages named twice) receives one of
+ * them or parts of both.  Asynchronous; T may be 0.
+ */
+WCOMP_API int wcomp_kv4_append(wcomp_kv4* c, const wcomp_kv4_seqs* s, const uint16_t* d_k, int64_t k_row,
+                               int64_t k_head, const uint16_t* d_v, int64_t v_row, int64_t v_head, int64_t T,
+                               void* stream);
+
+/*
+ * Read T rows back: d_k, d_v uint16[T, heads, dim], contiguous, receive
+ * (c - 8) * s in BF16, the exact product rounded once to nearest even.
+ */
+WCOMP_API int wcomp_kv4_read(const wcomp_kv4* c, const wcomp_kv4_seqs* s, uint16_t* d_k, uint16_t* d_v, int64_t T,
+                             void* stream);
+
+typedef struct {
+  wcomp_kv4_seqs s;
+  /* q[T, q_heads, dim], BF16 bits, with strides in elements between rows and heads */
+  const uint16_t* d_q;
+  int64_t q_row, q_head;
+  uint16_t* d_out; /* BF16 bits [T, q_heads, dim], contiguous, overwritten; not q's memory */
+  float* d_lse;    /* [T, q_heads] or NULL */
+  float* d_mass;   /* [B, heads, width * 64], added to, or NULL */
+  int64_t T;
+  int32_t q_heads; /* a multiple of the cache's heads; query head i reads head i / (q_heads / heads) */
+  int32_t window;  /* positions that a row sees, its own among them; 0: all */
+  float scale;
+} wcomp_kv4_attend_args;
+
+/*
+ * Attention of T query rows over the cache.  A row at position p sees the
+ * positions from max(0, p - window + 1) (0 without a window) to p:
+ *   z[j] = scale * q . k[j];  lse = log(sum_j exp(z[j]));
+ *   out = sum_j exp(z[j] - lse) * v[j];
+ *   mass[b, h, j] += sum over the sequence's rows and the query heads of head h of
+ *   exp(z[j] - lse).
+ * A row that sees nothing gets out = 0 and lse = -inf and adds nothing.
+ * Numbers: products with codes are exact and summed in fp32 on the tensor cores,
+ * q as fp16 under a power of two for each row (a BF16 value that is at least 2^-31 of
+ * the row's largest keeps its bits); softmax statistics and sums are fp32.  The
+ * weights that multiply V are rounded to fp16 times the values' scales under a
+ * power of two (half a step: 2^-11 of each).  Infinities and NaN follow the
+ * definition, those of tokens that a row does not see change nothing.  The sums
+ * of |q k| have to stay below 2^112.  The order of the sums is fixed: repeated calls
+ * give identical bits.
+ * Memory: parts of sums come from the library's stream-ordered pool for the
+ * duration of the call.  The device's error word is allocated with cudaMalloc on
+ * first use (of any call on a cache or a 4-bit product): make the first call before any stream
+ * capture.  T may be 0.
+ */
+WCOMP_API int wcomp_kv4_attend(const wcomp_kv4* c, const wcomp_kv4_attend_args* args, void* stream);
+
+typedef struct {
+  const int32_t* d_table;     /* [B, width] */
+  const int32_t* d_lengths;   /* [B] */
+  const float* d_mass;        /* [B, heads, width * 64] */
+  const int32_t* d_table_out; /* [B, width_out], width_out * 64 >= keep: other pages than any in d_table */
+  int32_t* d_lengths_out;     /* [B]: min(length, keep) */
+  float* d_mass_out;          /* [B, heads, width_out * 64]: of what was kept; 0 behind it */
+  int32_t* d_kept;            /* [B, heads, keep] or NULL: the positions that were kept, then -1 */
+  int32_t B, width, width_out;
+  int32_t keep, recent;       /* 1 <= keep, 0 <= recent <= keep */
+} wcomp_kv4_evict_args;
+
+/*
+ * Evict: of every sequence and head with more than `keep` tokens keep the last
+ * `recent` and, of the others, the keep - recent of largest mass (ties go to the
+ * lowest position; a NaN ranks below everything), of shorter ones all.  What is
+ * kept is copied bit for bit, in ascending order of its positions, to positions
+ * 0, 1, ... of the pages in table_out, each head by its own choice; the old pages
+ * are left as they are and may be shared with other sequences.  d_table_out ==
+ * d_table is refused; pages that are in both tables leave the results undefined.
+ * mass may be mass_out of an earlier call but not of this one.  Asynchronous.
+ */
+WCOMP_API int wcomp_kv4_evict(wcomp_kv4* c, const wcomp_kv4_evict_args* args, void* stream);
+
+/* Describe a cache (host-side, no device work). */
+WCOMP_API int wcomp_kv4_info(const wcomp_kv4* c, wcomp_kv4_info_t* info);
+
+/* Release a cache: work queued earlier on `stream` may still use it.  NULL is a no-op. */
+WCOMP_API void wcomp_kv4_free(wcomp_kv4* c, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Log probabilities from logits.
+ * ------------------------------------------------------------------------ */
+typedef enum { WCOMP_FP32 = 0, WCOMP_BF16 = 1 } wcomp_dtype;
+
+typedef struct {
+  const void* d_logits;  /* [T, V], fp32 or BF16 bits, `row` elements from one row to the next (at least V) */
+  const int64_t* d_ids;  /* [T]: the given tokens, or NULL */
+  float* d_logprob;      /* [T]; NULL where d_ids is */
+  float* d_entropy;      /* [T] or NULL */
+  float* d_lse;          /* [T] or NULL */
+  float* d_top_logprobs; /* [T, top_k]; NULL if top_k == 0 */
+  int32_t* d_top_ids;    /* [T, top_k]; NULL if top_k == 0 */
+  int64_t T, V, row;
+  int32_t dtype;         /* wcomp_dtype */
+  int32_t top_k;         /* 0 <= top_k <= min(V, 64) */
+  float scale;           /* multiplies the logits (1 / temperature); above 0 */
+} wcomp_logprobs_args;
+
+/*
+ * For each row of logits, z = scale * logits:
+ *   lse = log(sum_j exp(z[j]));  logprob = z[id] - lse;
+ *   entropy = -sum_j p[j] log p[j], p = exp(z - lse), in nats (p = 0 adds nothing);
+ *   the top_k largest logits, in descending order (ties go to the lowest index; a
+ *   NaN ranks below everything), and their log probabilities.
+ * A negative id names no token and gets logprob 0; one of V or above gets NaN.  A
+ * logit of -inf is a token that cannot come (log probability -inf); a row with a NaN or
+ * +inf, or with nothing but -inf, has NaN results, and its top_ids all the same.
+ * Sums are fp32 and leave the row's largest term out until the end, so that small
+ * entropies and log probabilities near 0 keep their bits.  The order of
+ * the sums is fixed: repeated calls give identical bits.  V below 2^31.  T may be 0.
+ */
+WCOMP_API int wcomp_logprobs(const wcomp_logprobs_args* args, void* stream);
 
 /* Human-readable text for a status code (static string). */
 WCOMP_API const char* wcomp_strerror(int status);
