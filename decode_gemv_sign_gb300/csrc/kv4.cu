@@ -111,10 +111,9 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(KvSeqs s, uint8_t*
       if (part) w = value_word(w, u);
       if (block) {
         const uint32_t index = part ? value_index<D>(u) : key_index<D>(u);
-        *reinterpret_cast<uint32_t*>(block + part * Kv<D>::kCodes + Kv<D>::at(t, 4 * index)) = w;
+        *reinterpret_cast<uint32_t*>(block + part * Kv<D>::kHalf + Kv<D>::at(t, 4 * index)) = w;
         if ((u & 3) == 0)
-          *reinterpret_cast<uint16_t*>(block + (part ? Kv<D>::kValueScales : Kv<D>::kKeyScales) +
-                                       Kv<D>::scale(t, u >> 2)) = uint16_t(scale);
+          *reinterpret_cast<uint16_t*>(block + part * Kv<D>::kHalf + Kv<D>::scale(t, u >> 2)) = uint16_t(scale);
       }
     }
   }
@@ -144,9 +143,8 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(KvSeqs s, const uint
       uint32_t w = 0x88888888u, scale = 0;
       if (block) {
         const uint32_t index = part ? value_index<D>(u) : key_index<D>(u);
-        w = *reinterpret_cast<const uint32_t*>(block + part * Kv<D>::kCodes + Kv<D>::at(t, 4 * index));
-        scale = *reinterpret_cast<const uint16_t*>(block + (part ? Kv<D>::kValueScales : Kv<D>::kKeyScales) +
-                                                   Kv<D>::scale(t, u >> 2));
+        w = *reinterpret_cast<const uint32_t*>(block + part * Kv<D>::kHalf + Kv<D>::at(t, 4 * index));
+        scale = *reinterpret_cast<const uint16_t*>(block + part * Kv<D>::kHalf + Kv<D>::scale(t, u >> 2));
       }
       if (part) w = value_word(w, u);
       uint32_t x[4];
@@ -312,15 +310,15 @@ __global__ void __launch_bounds__(kThreads) kv4_move_kernel(EvictArgs a) {
     for (uint32_t j = threadIdx.x; j < kPage * kPieces; j += kThreads) {
       const uint32_t t = j / kPieces, piece = j % kPieces;
       if (s_src[t] < 0) continue;
-      const uint32_t part = piece / (kPieces / 2) * L::kCodes, byte = piece % (kPieces / 2) * 16;
+      const uint32_t part = piece / (kPieces / 2) * L::kHalf, byte = piece % (kPieces / 2) * 16;
       *reinterpret_cast<uint4*>(dst + part + L::at(t, byte)) =
           *reinterpret_cast<const uint4*>(a.cache + s_src[t] + part + L::at(s_at[t], byte));
     }
     for (uint32_t j = threadIdx.x; j < kPage * 2 * L::G; j += kThreads) {
-      const uint32_t t = j % kPage, g = j / kPage;  // key groups, then value groups
+      const uint32_t t = j % kPage, g = j / kPage % L::G, part = j / kPage / L::G * L::kHalf;
       if (s_src[t] < 0) continue;
-      *reinterpret_cast<uint16_t*>(dst + L::kKeyScales + L::scale(t, g)) =
-          *reinterpret_cast<const uint16_t*>(a.cache + s_src[t] + L::kKeyScales + L::scale(s_at[t], g));
+      *reinterpret_cast<uint16_t*>(dst + part + L::scale(t, g)) =
+          *reinterpret_cast<const uint16_t*>(a.cache + s_src[t] + part + L::scale(s_at[t], g));
     }
   }
 }

@@ -17,11 +17,11 @@ namespace wc {
 constexpr int kPage = 64;       // tokens of a page
 constexpr int kKvGroup = 32;    // columns that share a scale
 
-// A page holds one block per head: 64 rows of key codes, 64 rows of value codes
-// (dim / 2 bytes each), the key scales [dim / 32][64] and the value scales
-// [dim / 32][64], BF16.  A block is one bulk copy of the attention and a multiple
-// of 128 bytes; a row is made of whole 16-byte pieces, so that a token can be
-// written and moved by itself.
+// A page holds one block per head, its first half the keys and its second the
+// values: 64 rows of codes (dim / 2 bytes each) and the scales [dim / 32][64],
+// BF16.  A block is one bulk copy of the attention and a multiple of 128 bytes; a
+// row is made of whole 16-byte pieces, so that a token can be written and moved
+// by itself.
 //
 // In a key row the 8 columns 32 g + 8 q .. + 7 are the word q * G + g (G = dim /
 // 32; column i of them in bits 4 i .. 4 i + 3): lane q of a quad of the MMA finds its
@@ -38,15 +38,17 @@ struct Kv {
   static constexpr int G = D / kKvGroup;
   static constexpr uint32_t kRow = D / 2;
   static constexpr uint32_t kCodes = kPage * kRow;
-  static constexpr uint32_t kScales = G * kPage * 2;
-  static constexpr uint32_t kBlock = 2 * (kCodes + kScales);
-  static constexpr uint32_t kKeyScales = 2 * kCodes, kValueScales = 2 * kCodes + kScales;
-  // Byte b of token t's row, from the start of the keys or the values.
+  static constexpr uint32_t kHalf = kCodes + G * kPage * 2;
+  static constexpr uint32_t kBlock = 2 * kHalf;
+  // From the start of the keys or the values: byte b of token t's row, and its
+  // scale of group g.
   static __host__ __device__ __forceinline__ uint32_t at(uint32_t t, uint32_t b) {
     const uint32_t turn = ((t >> 5) & 1) | ((t >> 3) & 2);  // the two bits of t / 16, exchanged
     return (t * kRow + b) ^ (turn << 5) ^ (D == 256 ? (t & 1) << 4 : 0);
   }
-  static __host__ __device__ __forceinline__ uint32_t scale(uint32_t t, uint32_t g) { return 2 * (g * kPage + t); }
+  static __host__ __device__ __forceinline__ uint32_t scale(uint32_t t, uint32_t g) {
+    return kCodes + 2 * (g * kPage + t);
+  }
 };
 
 // The rows of a call (wcomp_kv4_seqs) on the device.

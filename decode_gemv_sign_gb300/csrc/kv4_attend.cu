@@ -1,4 +1,27 @@
 // Attention over the 4-bit key/value cache.
+//
+// One pass with the running maximum and sum of a softmax.  At a few query rows a
+// cached head the cache is read once and little is done with it: moving it is the
+// bound, and a block of 64 tokens and 128 columns (9216 bytes) leaves an SM some
+// 390 cycles before the arithmetic falls behind the HBM.  So both products run on
+// warp-level tensor-core MMAs with the codes as exact fp16 integers (tile.cuh):
+//
+//   S[row, token] = sum over groups of ks[token, group] * (Q[row, group] . Ck[token, group])
+//     M = 16 rows, N = 8 tokens: a group's codes are two MMAs, whose sum enters S
+//     under the group's scale; scores are as exact as fp32 sums of the products.
+//   O^T[column, row] += Cv^T[column, token] * (P[row, token] * vs[token, group])
+//     M = 16 columns of a group, N = 8 rows: the accumulators of S are the B
+//     operand's places without an exchange, and the group's scale goes into them.
+//
+// A value row is read by token and transposed by a byte permutation of two
+// tokens' words.  P * vs is rounded to fp16 under a power of two that follows the
+// largest scale seen, which the sums O are kept under: one rounding of 2^-11, full
+// precision for products down to 2^-29 of the largest scale's.
+//
+// Each warp takes an equal run of the call's (sequence, tile of rows, head, page)
+// units through a ring of its own; parts of a softmax that fall on several warps are
+// joined in warp order by a second kernel.  Lengths are on the device, so every
+// block sums up the work of all sequences first.
 #include <algorithm>
 #include <cmath>
 
@@ -7,7 +30,7 @@
 namespace wc {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttendArgs {
   KvSeqs s;
@@ -15,110 +38,803 @@ struct AttendArgs {
   const uint16_t* q;
   int64_t q_row, q_head;
   uint16_t* out;
-  float* lse;
-  float* mass;
+  float* lse;   // or null
+  float* mass;  // or null
   int64_t T;
-  int q_heads, window;
+  int q_heads, share, window, q_vec;
   float scale;
+  // workspace
+  uint64_t* prefix;  // [B + 1]: units before each sequence
+  float* lse2;       // [T, q_heads], in base 2 (with mass)
+  float* part;       // [2 warps][rows][D]: sums
+  float2* part_ml;   // [2 warps][rows]: maximum (base 2) and sum
+  uint32_t warps;    // of the attention kernel
 };
 
-// Code and scale of column c of token t in a block, as a value.
-template <int D>
-__device__ __forceinline__ float kv_value(const uint8_t* block, bool value, uint32_t t, uint32_t c) {
-  using L = Kv<D>;
-  const uint32_t g = c / 32, in = c % 32;
-  const uint32_t word = value ? in / 4 * (L::G / 2) + g / 2 : in / 8 * L::G + g;
-  const uint32_t nibble = value ? in % 4 + 4 * (g % 2) : in % 8;
-  const uint32_t w =
-      *reinterpret_cast<const uint32_t*>(block + (value ? L::kCodes : 0) + L::at(t, 4 * word));
-  const uint32_t s = *reinterpret_cast<const uint16_t*>(block + (value ? L::kValueScales : L::kKeyScales) +
-                                                        L::scale(t, g));
-  return float(int((w >> (4 * nibble)) & 15) - 8) * __uint_as_float(s << 16);
+// ---------------------------------------------------------------------------
+// Units.
+// ---------------------------------------------------------------------------
+struct Seq {
+  int n, rows;     // tokens, and rows of the call
+  int64_t first;   // first row
+  int tiles;       // of R (row, head of the group) pairs
+  int page0, pages;
+};
+
+// TILES: every tile of rows is work of its own; else a page is one unit for all of
+// them.  A sequence with rows has at least one page, also where it has no token.
+template <int R, bool TILES>
+__device__ __forceinline__ Seq load_seq(const AttendArgs& a, int b) {
+  Seq q;
+  q.n = kv_length(a.s, b);
+  if (a.s.starts) {
+    q.first = a.s.starts[b];
+    const int64_t rows = a.s.starts[b + 1] - q.first;
+    q.rows = int(rows < 0 ? 0 : rows > a.T ? a.T : rows);
+  } else {
+    q.first = b;
+    q.rows = 1;
+  }
+  q.tiles = TILES ? (q.rows * a.share + R - 1) / R : q.rows ? 1 : 0;
+  const int lo = a.window ? max(0, q.n - q.rows - a.window + 1) : 0;
+  q.page0 = min(lo, max(q.n - 1, 0)) / kPage;
+  q.pages = max(1, (q.n + kPage - 1) / kPage - q.page0);
+  return q;
+}
+__device__ __forceinline__ uint64_t seq_units(const AttendArgs& a, const Seq& q) {
+  return uint64_t(q.tiles) * a.s.heads * uint64_t(q.pages);
 }
 
-// One warp takes a row and query head through its tokens.
-template <int D>
-__global__ void __launch_bounds__(kThreads) kv4_attend_kernel(AttendArgs a) {
-  constexpr int kPer = D / 32;
-  const int lane = threadIdx.x % 32;
-  const int64_t units = a.T * a.q_heads;
-  const int share = a.q_heads / int(a.s.heads);
-  for (int64_t unit = int64_t(blockIdx.x) * kWarps + threadIdx.x / 32; unit < units;
-       unit += int64_t(gridDim.x) * kWarps) {
-    const int64_t i = unit / a.q_heads;
-    const int hq = int(unit % a.q_heads), h = hq / share;
-    const int b = kv_sequence(a.s, i);
-    if (b < 0) continue;
-    const int64_t pos = kv_position(a.s, b, i, kv_length(a.s, b));
-    float q[kPer], o[kPer];
+// Units before the sequences of each thread's share, [threads + 1] in shared
+// memory.  `out` gets those before each sequence.
+template <int THREADS, int R, bool TILES>
+__device__ __forceinline__ void sum_units(const AttendArgs& a, uint64_t* s_before, uint64_t* s_warp, uint64_t* out) {
+  const int per = (a.s.B + THREADS - 1) / THREADS;
+  const int b0 = min(a.s.B, int(threadIdx.x) * per), b1 = min(a.s.B, b0 + per);
+  uint64_t sum = 0;
+  for (int b = b0; b < b1; ++b) sum += seq_units(a, load_seq<R, TILES>(a, b));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint64_t x = sum;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      q[j] = __uint_as_float(uint32_t(a.q[i * a.q_row + hq * a.q_head + lane + 32 * j]) << 16) * a.scale;
-      o[j] = 0.f;
+  for (int d = 1; d < 32; d *= 2) {
+    const uint64_t y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  uint64_t before = x - sum;
+  for (int w = 0; w < warp; ++w) before += s_warp[w];
+  s_before[threadIdx.x] = before;
+  if (threadIdx.x == THREADS - 1) s_before[THREADS] = before + sum;
+  if (out) {
+    for (int b = b0; b < b1; ++b) {
+      out[b] = before;
+      before += seq_units(a, load_seq<R, TILES>(a, b));
     }
-    float m = -INFINITY, l = 0.f;
-    const int64_t first = a.window ? max(int64_t(0), pos - a.window + 1) : 0;
-    for (int64_t p = first; p <= pos; ++p) {
-      const int page = kv_page(a.s, b, int(p / kPage));
-      if (page < 0) continue;
-      const uint8_t* block = a.cache + (uint64_t(page) * a.s.heads + h) * Kv<D>::kBlock;
-      float z = 0.f;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) z += q[j] * kv_value<D>(block, false, p % kPage, lane + 32 * j);
-#pragma unroll
-      for (int d = 16; d; d /= 2) z += __shfl_xor_sync(0xffffffffu, z, d);
-      const float next = fmaxf(m, z);
-      const float down = m == -INFINITY ? 0.f : expf(m - next), e = expf(z - next);
-      l = l * down + e;
-      m = next;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) o[j] = o[j] * down + e * kv_value<D>(block, true, p % kPage, lane + 32 * j);
+    if (threadIdx.x == THREADS - 1) out[a.s.B] = before;
+  }
+  __syncthreads();
+}
+
+// A place in the units' order: sequence, (tile, head) and page, pages fastest.
+template <int THREADS, int R, bool TILES>
+struct Walk {
+  int b, page;
+  uint32_t seg, segs;
+  Seq q;
+  __device__ __forceinline__ void enter(const AttendArgs& a) {
+    q = load_seq<R, TILES>(a, b);
+    segs = uint32_t(q.tiles) * a.s.heads;
+  }
+  __device__ __forceinline__ void find(const AttendArgs& a, const uint64_t* s_before, uint64_t u) {
+    int lo = 0, hi = THREADS;  // s_before[lo] <= u < s_before[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_before[mid] <= u) lo = mid;
+      else hi = mid;
     }
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      uint16_t bits;
-      asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(bits) : "f"(l == 0.f ? 0.f : o[j] / l));
-      a.out[(i * a.q_heads + hq) * D + lane + 32 * j] = bits;
+    b = lo * ((a.s.B + THREADS - 1) / THREADS);
+    u -= s_before[lo];
+    enter(a);
+    for (uint64_t w; u >= (w = seq_units(a, q));) {
+      u -= w;
+      ++b;
+      enter(a);
     }
-    if (lane == 0) a.lse[i * a.q_heads + hq] = m + logf(l);
+    seg = uint32_t(u / uint32_t(q.pages));
+    page = int(u % uint32_t(q.pages));
+  }
+  // The next unit, which there is.
+  __device__ __forceinline__ void next(const AttendArgs& a) {
+    if (++page < q.pages) return;
+    page = 0;
+    if (++seg < segs) return;
+    seg = 0;
+    do {
+      ++b;
+      enter(a);
+    } while (segs == 0);
+  }
+};
+
+template <int D, bool KEYS>
+struct KvSrc {
+  static constexpr uint32_t kStage = KEYS ? Kv<D>::kHalf : Kv<D>::kBlock;
+  static constexpr bool kCopies = true;
+  typedef const uint8_t* Cursor;
+  static __device__ __forceinline__ void issue(Cursor& c, uint32_t st, uint32_t bar) { bulk_copy(st, c, kStage, bar); }
+};
+
+// The blocks of a warp's units through its ring, ahead of their use.
+template <class RING, class WALK>
+struct Pages {
+  WALK it;
+  uint64_t left;
+  int base = -1, in = -1, id;  // page `base` + lane of sequence `in` is id
+  uint32_t there = 0;          // bit per slot: its page exists
+  __device__ __forceinline__ void start(const AttendArgs& a, const uint64_t* s_before, uint64_t u, uint64_t count) {
+    it.find(a, s_before, u);
+    left = count;
+  }
+  // Copy the next unit's block to `slot`.  A page that does not exist is stood in for
+  // by the cache's first, which nothing is read of.
+  __device__ __forceinline__ void issue(const AttendArgs& a, RING& ring, uint32_t slot, uint32_t block, int lane) {
+    if (!left) return;
+    const int at = it.q.page0 + it.page;
+    if (in != it.b || at < base || at >= base + 32) {
+      in = it.b;
+      base = at;
+      id = at + lane < (it.q.n + kPage - 1) / kPage ? kv_page(a.s, it.b, at + lane) : -1;
+    }
+    const int page = __shfl_sync(0xffffffffu, id, at - base);
+    there = page >= 0 ? there | 1u << slot : there & ~(1u << slot);
+    const uint8_t* p = a.cache + (uint64_t(max(page, 0)) * a.s.heads + it.seg % a.s.heads) * block;
+    ring.refill(slot, p, lane);
+    if (--left) it.next(a);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Products.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint2 lds_v2(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    w[0] = lds_u32(a);
+  } else if constexpr (N == 2) {
+    const uint2 v = lds_v2(a);
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    const uint4 v = lds_v4(a);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  }
+}
+// The words of a row at byte b: 16-byte pieces may be apart (Kv::at).
+template <int D, int N>
+__device__ __forceinline__ void row_words(uint32_t st, uint32_t t, uint32_t b, uint32_t (&w)[N]) {
+  if constexpr (N <= 4) {
+    lds_words<N>(st + Kv<D>::at(t, b), w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 v = lds_v4(st + Kv<D>::at(t, b + 4 * i));
+      w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+    }
   }
 }
 
-// One warp adds to a token's weight what the rows of its sequence give it.
-template <int D>
-__global__ void __launch_bounds__(kThreads) kv4_mass_kernel(AttendArgs a) {
-  const int lane = threadIdx.x % 32;
-  const int share = a.q_heads / int(a.s.heads);
-  const int64_t tokens = int64_t(a.s.width) * kPage;
-  const int64_t units = int64_t(a.s.B) * a.s.heads * tokens;
-  for (int64_t unit = int64_t(blockIdx.x) * kWarps + threadIdx.x / 32; unit < units;
-       unit += int64_t(gridDim.x) * kWarps) {
-    const int64_t p = unit % tokens;
-    const int h = int(unit / tokens % a.s.heads), b = int(unit / tokens / a.s.heads);
-    const int n = kv_length(a.s, b);
-    if (p >= n) continue;
-    const int page = kv_page(a.s, b, int(p / kPage));
-    if (page < 0) continue;
-    const uint8_t* block = a.cache + (uint64_t(page) * a.s.heads + h) * Kv<D>::kBlock;
-    const int64_t i0 = a.s.starts ? max(0, a.s.starts[b]) : b;
-    const int64_t i1 = a.s.starts ? min(a.T, int64_t(a.s.starts[b + 1])) : b + 1;
-    float sum = 0.f;
-    for (int64_t i = i0; i < i1; ++i) {
-      const int64_t pos = kv_position(a.s, b, i, n);
-      if (p > pos || (a.window && p <= pos - a.window)) continue;
-      for (int hq = h * share; hq < (h + 1) * share; ++hq) {
-        float z = 0.f;
+// A tile's rows: R = 8 NT (row, head of the group) pairs; lane (r, q) has those of
+// r and r + 8.
+template <int D, int NT>
+struct Tile {
+  static constexpr int G = Kv<D>::G;
+  uint32_t a[NT][G][4];     // A operands: the pairs of columns (0, 4), (2, 6), (1, 5), (3, 7) of 32 g + 8 q ..
+  float c[NT];              // what brings a score to base 2: scale, log2 e and the row's power of two
+  int64_t row[NT];          // index of (row, query head) in out and lse, or -1
+  int lo[NT], hi[NT];       // positions that it sees
+  int lo0, lo1, hi0, hi1;   // least and greatest of the tile's
+
+  __device__ __forceinline__ void load(const AttendArgs& p, const Seq& s, uint32_t seg, int lane) {
+    const int tile = int(seg / p.s.heads), h = int(seg % p.s.heads);
+    const int r = lane >> 2, q = lane & 3;
+    const int pairs = s.rows * p.share;
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j)
-          z += __uint_as_float(uint32_t(a.q[i * a.q_row + hq * a.q_head + lane + 32 * j]) << 16) * a.scale *
-               kv_value<D>(block, false, p % kPage, lane + 32 * j);
+    for (int n = 0; n < NT; ++n) {
+      const int x = tile * 8 * NT + 8 * n + r, tok = x / p.share;
+      const int64_t i = s.first + tok;
+      const int hq = h * p.share + (x - tok * p.share);
+      const bool ok = x < pairs && i >= 0 && i < p.T;
+      row[n] = ok ? i * p.q_heads + hq : -1;
+      see(p, s, tok, lo[n], hi[n]);
+      if (!ok) lo[n] = hi[n] = 0;
+      const uint16_t* src = p.q + i * p.q_row + hq * p.q_head + 8 * q;
+      uint32_t m = 0;
+      uint32_t v[G][4];
 #pragma unroll
-        for (int d = 16; d; d /= 2) z += __shfl_xor_sync(0xffffffffu, z, d);
-        sum += expf(z - a.lse[i * a.q_heads + hq]);
+      for (int g = 0; g < G; ++g) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[g][k] = 0;
+        if (ok) {
+          if (p.q_vec) {
+            const uint4 y = *reinterpret_cast<const uint4*>(src + 32 * g);
+            v[g][0] = y.x; v[g][1] = y.y; v[g][2] = y.z; v[g][3] = y.w;
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[g][k] = src[32 * g + 2 * k] | uint32_t(src[32 * g + 2 * k + 1]) << 16;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m = max(m, max(v[g][k] & 0x7FFFu, (v[g][k] >> 16) & 0x7FFFu));
+      }
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const int e = record_exponent(m << 16);
+      const float up = power_of_two(e);
+      c[n] = p.scale * kLog2e * power_of_two(-e);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {  // columns 2 k, 2 k + 1 in v[g][k]
+        a[n][g][0] = half2_bits(bf16_lo(v[g][0]) * up, bf16_lo(v[g][2]) * up);
+        a[n][g][1] = half2_bits(bf16_lo(v[g][1]) * up, bf16_lo(v[g][3]) * up);
+        a[n][g][2] = half2_bits(bf16_hi(v[g][0]) * up, bf16_hi(v[g][2]) * up);
+        a[n][g][3] = half2_bits(bf16_hi(v[g][1]) * up, bf16_hi(v[g][3]) * up);
       }
     }
-    if (lane == 0) a.mass[unit] += sum;
+    see(p, s, tile * 8 * NT / p.share, lo0, hi0);
+    see(p, s, (min(pairs, (tile + 1) * 8 * NT) - 1) / p.share, lo1, hi1);
   }
+  // What row `tok` of the sequence sees.
+  static __device__ __forceinline__ void see(const AttendArgs& p, const Seq& s, int tok, int& lo, int& hi) {
+    hi = max(0, s.n - s.rows + tok + 1);
+    lo = p.window ? max(0, hi - p.window) : 0;
+  }
+  __device__ __forceinline__ bool sees_none(int page) const { return page * kPage >= hi1 || (page + 1) * kPage <= lo0; }
+  __device__ __forceinline__ bool sees_all(int page) const { return page * kPage >= lo1 && (page + 1) * kPage <= hi0; }
+  // Which of the lane's 16 tokens of a page, 16 q .., row n of it sees.
+  __device__ __forceinline__ uint32_t seen(int n, int page, int lane) const {
+    const int at = page * kPage + 16 * (lane & 3);
+    return bits_below(hi[n] - at) & ~bits_below(lo[n] - at);
+  }
+  static __device__ __forceinline__ uint32_t bits_below(int k) { return k <= 0 ? 0u : k >= 16 ? 0xFFFFu : (1u << k) - 1u; }
+
+  // Scores, times c, of the keys at st: z[j][2 n + e] of row n and token 16 q + 2 j + e.
+  __device__ __forceinline__ void scores(uint32_t st, int lane, uint32_t magic, float (&z)[8][2 * NT]) const {
+    const uint32_t r = uint32_t(lane) >> 2, q = uint32_t(lane) & 3;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t sc[G][4];  // scales of the tokens 16 q + 8 half .., in pairs
+#pragma unroll
+      for (int g = 0; g < G; ++g) lds_words<4>(st + Kv<D>::scale(16 * q + 8 * half, g), sc[g]);
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        const int j = 4 * half + jj;
+        uint32_t w[G];
+        row_words<D, G>(st, 16 * (r >> 1) + (r & 1) + 2 * j, q * G * 4, w);
+        float s[2 * NT] = {};
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          uint32_t b[4];
+          q4_operand(w[g], magic, b);
+          float d[4];
+          const uint32_t a0[4] = {a[0][g][0], NT == 2 ? a[NT - 1][g][0] : 0u, a[0][g][1], NT == 2 ? a[NT - 1][g][1] : 0u};
+          const uint32_t a1[4] = {a[0][g][2], NT == 2 ? a[NT - 1][g][2] : 0u, a[0][g][3], NT == 2 ? a[NT - 1][g][3] : 0u};
+          mma_f16_first(d, a0, b[0], b[1]);
+          mma_f16(d, a1, b[2], b[3]);
+          const float s0 = bf16_lo(sc[g][jj]), s1 = bf16_hi(sc[g][jj]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            s[2 * n] += s0 * d[2 * n];
+            s[2 * n + 1] += s1 * d[2 * n + 1];
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          z[j][2 * n] = s[2 * n] * c[n];
+          z[j][2 * n + 1] = s[2 * n + 1] * c[n];
+        }
+      }
+    }
+  }
+};
+
+// Sums of a tile so far, and the softmax's state: maximum (base 2) and, per lane, sum.
+template <int D, int NT>
+struct Sums {
+  static constexpr int G = Kv<D>::G;
+  static constexpr int kNoScale = 120;
+  float m[NT], l[NT];
+  float o[2 * G][NT][4];  // tile 2 g + i: columns 32 g + 4 r + 2 i (+ 1: the last two) of the rows 2 q, 2 q + 1 (+ 8 n)
+  int k;                  // o is under 2^k
+
+  __device__ __forceinline__ void clear() {
+    k = kNoScale;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n] = -INFINITY;
+      l[n] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2 * G; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][n][e] = 0.f;
+    }
+  }
+  __device__ __forceinline__ void scale(float f) {
+#pragma unroll
+    for (int i = 0; i < 2 * G; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][n][e] *= f;
+  }
+
+  // Add a page: scores z, values at st.  `all`: every row sees every token.
+  __device__ __forceinline__ void add(const Tile<D, NT>& t, int page, bool all, uint32_t st, int lane, uint32_t magic,
+                                      float (&z)[8][2 * NT]) {
+    const uint32_t r = uint32_t(lane) >> 2, q = uint32_t(lane) & 3;
+    uint32_t see[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) see[n] = 0xFFFFu;
+    if (!all) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        see[n] = t.seen(n, page, lane);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (!(see[n] >> (2 * j + e) & 1)) z[j][2 * n + e] = -INFINITY;
+      }
+    }
+    bool more = false;
+    float next[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float x = m[n];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x = fmaxf(x, fmaxf(z[j][2 * n], z[j][2 * n + 1]));
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+      next[n] = x;
+      more |= x > m[n];
+    }
+    if (__any_sync(0xffffffffu, more)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float down = next[n] > m[n] ? exp2_approx(m[n] - next[n]) : 1.f;
+        l[n] *= down;
+        m[n] = next[n];
+        const float f0 = __shfl_sync(0xffffffffu, down, 8 * q), f1 = __shfl_sync(0xffffffffu, down, 8 * q + 4);
+#pragma unroll
+        for (int i = 0; i < 2 * G; ++i) {
+          o[i][n][0] *= f0;
+          o[i][n][1] *= f1;
+          o[i][n][2] *= f0;
+          o[i][n][3] *= f1;
+        }
+      }
+    }
+    // the largest scale of a value that some row sees: G words a lane, 2 tokens each
+    uint32_t top[G];
+    row_words_linear(st + Kv<D>::kCodes + 4 * G * lane, top);
+    if (!all) {
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const int at = page * kPage + 2 * ((G * lane + i) % 32);
+        if (at < t.lo0 || at >= t.hi1) top[i] &= 0xFFFF0000u;
+        if (at + 1 < t.lo0 || at + 1 >= t.hi1) top[i] &= 0xFFFFu;
+      }
+    }
+#pragma unroll
+    for (int i = 1; i < G; ++i)  // a NaN loses against a number
+      asm("max.bf16x2 %0, %0, %1;" : "+r"(top[0]) : "r"(top[i]));
+    uint32_t hi = top[0] >> 16, lo = top[0] & 0xFFFFu;
+    if (hi > 0x7F80u) hi = 0;
+    if (lo > 0x7F80u) lo = 0;
+    const uint32_t largest = __reduce_max_sync(0xffffffffu, max(hi, lo));
+    if (largest) {
+      int to = 14 - (int(largest >> 7) - 127);
+      to = to > kNoScale ? kNoScale : to;
+      if (to < k) {
+        const int d = to - k;
+        scale(power_of_two(d / 2));
+        scale(power_of_two(d - d / 2));
+        k = to;
+      }
+    }
+    const float up = power_of_two(k);
+    float p[8][2 * NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float from = m[n] == -INFINITY ? 0.f : m[n];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x = exp2_approx(z[j][2 * n + e] - from);
+          l[n] += x;
+          p[j][2 * n + e] = x * up;
+        }
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t sc[G][4];
+#pragma unroll
+      for (int g = 0; g < G; ++g) lds_words<4>(st + Kv<D>::scale(16 * q + 8 * half, g), sc[g]);
+#pragma unroll
+      for (int ii = 0; ii < 2; ++ii) {
+        const int i = 2 * half + ii;  // the tokens 16 q + 4 i ..
+        uint32_t w[4][G / 2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) row_words<D, G / 2>(st, 16 * q + 4 * i + e, r * (G / 2) * 4, w[e]);
+#pragma unroll
+        for (int a = 0; a < G / 2; ++a) {
+#pragma unroll
+          for (int side = 0; side < 2; ++side) {  // groups 2 a and 2 a + 1
+            const int g = 2 * a + side;
+            uint32_t b[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float x[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t s = sc[g][2 * ii + e / 2];
+                x[e] = p[2 * i + e / 2][2 * n + e % 2] * (e % 2 ? bf16_hi(s) : bf16_lo(s));
+              }
+              if (!all) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (!(see[n] >> (4 * i + e) & 1)) x[e] = 0.f;  // also where the scale is NaN
+              }
+              b[n][0] = half2_bits(x[0], x[1]);
+              b[n][1] = half2_bits(x[2], x[3]);
+            }
+            const uint32_t pick = side ? 0x7632 : 0x5410;
+            uint32_t u[4], v[4];
+            q4_operand(prmt(w[0][a], w[1][a], pick), magic, u);  // columns 0, 2, 1, 3 of two tokens
+            q4_operand(prmt(w[2][a], w[3][a], pick), magic, v);
+            const uint32_t a0[4] = {u[0], u[2], v[0], v[2]}, a1[4] = {u[1], u[3], v[1], v[3]};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma_f16(o[2 * g][n], a0, b[n][0], b[n][1]);
+              mma_f16(o[2 * g + 1][n], a1, b[n][0], b[n][1]);
+            }
+          }
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ void row_words_linear(uint32_t at, uint32_t (&w)[G]) {
+    if constexpr (G <= 4) {
+      lds_words<G>(at, w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < G; i += 4) {
+        const uint4 v = lds_v4(at + 4 * i);
+        w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ void store_lse(const AttendArgs& a, int64_t row, float m, float l) {
+  const float y = m + log2f(l);  // -inf where nothing is seen
+  if (a.lse) a.lse[row] = y * kLn2;
+  if (a.mass) a.lse2[row] = y;
+}
+
+// Warps, ring stages and rows of a tile.  The rings fill an SM's shared memory.
+template <int D>
+struct Shape {
+  static constexpr int kWarps = D == 64 ? 12 : D == 128 ? 8 : 6;
+  static constexpr int kDepth = D == 64 ? 4 : D == 128 ? 3 : 2;
+  static constexpr int kThreads = 32 * kWarps;
+};
+template <int D, bool KEYS>
+constexpr uint32_t attend_smem() {
+  return Shape<D>::kWarps * Shape<D>::kDepth * (KvSrc<D, KEYS>::kStage + 8) + 128;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Shape<D>::kThreads, 1) kv4_attend_kernel(const __grid_constant__ AttendArgs a) {
+  constexpr int kThreads = Shape<D>::kThreads, kWarps = Shape<D>::kWarps, kDepth = Shape<D>::kDepth, R = 8 * NT;
+  using Src = KvSrc<D, false>;
+  using W = Walk<kThreads, R, true>;
+  __shared__ uint64_t s_before[kThreads + 1], s_warp[kWarps];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t smem = smem_u32(smem_raw) + (-smem_u32(smem_raw) & 127u);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t magic = q4_magic();
+  Ring<Src, kDepth> ring(smem + uint32_t(warp) * kDepth * Src::kStage,
+                         smem + kWarps * kDepth * Src::kStage + uint32_t(warp) * kDepth * 8, a.s.err, lane);
+  sum_units<kThreads, R, true>(a, s_before, s_warp, blockIdx.x == 0 ? a.prefix : nullptr);
+  const uint64_t total = s_before[kThreads];
+  const uint64_t per = (total + a.warps - 1) / a.warps;
+  const uint32_t me = blockIdx.x + uint32_t(warp) * gridDim.x;  // neighbours on different SMs: few units spread
+  uint64_t u = per * me;
+  const uint64_t end = min(total, u + per);
+  if (u >= end) return;
+  Pages<Ring<Src, kDepth>, W> pages;
+  pages.start(a, s_before, u, end - u);
+#pragma unroll 1
+  for (int i = 0; i < kDepth; ++i) pages.issue(a, ring, uint32_t(i), Src::kStage, lane);
+  W at;
+  at.find(a, s_before, u);
+  Tile<D, NT> tile;
+  Sums<D, NT> sums;
+  const uint32_t q = uint32_t(lane) & 3, r = uint32_t(lane) >> 2;
+  while (u < end) {
+    // a tile's pages, or those of them that fall on this warp
+    const bool first = at.page == 0;
+    const int stop = int(min(uint64_t(at.q.pages), uint64_t(at.page) + (end - u)));
+    const bool last = stop == at.q.pages;
+    tile.load(a, at.q, at.seg, lane);
+    sums.clear();
+    u += uint64_t(stop - at.page);
+#pragma unroll 1
+    for (; at.page < stop; ++at.page) {
+      ring.wait(lane);
+      const int page = at.q.page0 + at.page;
+      if ((pages.there >> ring.slot & 1) && !tile.sees_none(page)) {
+        float z[8][2 * NT];
+        tile.scores(ring.stage(), lane, magic, z);
+        sums.add(tile, page, tile.sees_all(page), ring.stage() + Kv<D>::kHalf, lane, magic, z);
+      }
+      __syncwarp();
+      pages.issue(a, ring, ring.slot, Src::kStage, lane);
+      ring.next();
+    }
+    const bool whole = first && last;
+    const float back = power_of_two(-sums.k);
+    float* part = a.part + (uint64_t(2 * me + first) * R) * D;
+    float2* ml = a.part_ml + uint64_t(2 * me + first) * R;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float l = sums.l[n];
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+      if (q == 0 && tile.row[n] >= 0) {
+        if (whole) store_lse(a, tile.row[n], sums.m[n], l);
+        else ml[8 * n + r] = make_float2(sums.m[n], l);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {  // row 8 n + 2 q + e
+        const int from = 8 * int(q) + 4 * e;
+        const float g = __shfl_sync(0xffffffffu, f, from);
+        const int64_t row = __shfl_sync(0xffffffffu, tile.row[n], from);
+        if (row < 0) continue;
+#pragma unroll
+        for (int i = 0; i < Kv<D>::G; ++i) {
+          float x[4] = {sums.o[2 * i][n][e], sums.o[2 * i][n][2 + e], sums.o[2 * i + 1][n][e], sums.o[2 * i + 1][n][2 + e]};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = x[k] * back * g;
+          if (whole)
+            *reinterpret_cast<uint2*>(a.out + row * D + 32 * i + 4 * r) =
+                make_uint2(bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3]));
+          else
+            *reinterpret_cast<float4*>(part + (8 * n + 2 * q + e) * D + 32 * i + 4 * r) =
+                make_float4(x[0], x[1], x[2], x[3]);
+        }
+      }
+    }
+    if (u < end) {
+      --at.page;  // the tile's last page
+      at.next(a);
+    }
+  }
+}
+
+// Join the parts of a (row, query head): one block.
+constexpr int kJoinWarps = 8;
+template <int D, int NT, int THREADS>
+__global__ void __launch_bounds__(32 * kJoinWarps) kv4_join_kernel(const __grid_constant__ AttendArgs a) {
+  constexpr int R = 8 * NT, V = D / 32;
+  __shared__ float s_o[kJoinWarps][D], s_l[kJoinWarps], s_m[kJoinWarps];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint64_t per = (a.prefix[a.s.B] + a.warps - 1) / a.warps;
+  const int64_t units = a.T * a.q_heads;
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int64_t i = unit / a.q_heads;
+    const int hq = int(unit % a.q_heads), h = hq / a.share;
+    const int b = kv_sequence(a.s, i);
+    if (b < 0) continue;
+    const Seq s = load_seq<R, true>(a, b);
+    const int64_t x = (i - s.first) * a.share + (hq - h * a.share);
+    if (x < 0 || x >= int64_t(s.rows) * a.share) continue;  // starts out of order
+    const uint64_t f0 = a.prefix[b] + (uint64_t(x / R) * a.s.heads + h) * uint32_t(s.pages), f1 = f0 + uint32_t(s.pages);
+    const uint64_t w0 = f0 / per, w1 = (f1 - 1) / per;
+    if (w0 == w1 || w1 >= a.warps) continue;
+    const int row = int(x % R);
+    auto slot = [&](uint64_t w) { return (2 * w + (w * per <= f0 ? 1 : 0)) * R + row; };
+    float m = -INFINITY;
+    for (uint64_t w = w0 + threadIdx.x; w <= w1; w += 32 * kJoinWarps) m = fmaxf(m, a.part_ml[slot(w)].x);
+#pragma unroll
+    for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    __syncthreads();
+    if (lane == 0) s_m[warp] = m;
+    __syncthreads();
+    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_m[w]);
+    const float from = m == -INFINITY ? 0.f : m;
+    float o[V] = {}, l = 0.f;
+#pragma unroll 4
+    for (uint64_t w = w0 + warp; w <= w1; w += kJoinWarps) {
+      const float2 ml = a.part_ml[slot(w)];
+      const float f = exp2f(ml.x - from);
+      const float* part = a.part + slot(w) * D + V * lane;
+      float y[V];
+      if constexpr (V == 2) {
+        const float2 t = *reinterpret_cast<const float2*>(part);
+        y[0] = t.x; y[1] = t.y;
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; k += 4) {
+          const float4 t = *reinterpret_cast<const float4*>(part + k);
+          y[k] = t.x; y[k + 1] = t.y; y[k + 2] = t.z; y[k + 3] = t.w;
+        }
+      }
+      l += f * ml.y;
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] += f * y[k];
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) s_o[warp][V * lane + k] = o[k];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    l = 0.f;
+    for (int w = 0; w < kJoinWarps; ++w) l += s_l[w];
+    for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps) {
+      float y = 0.f;
+      for (int w = 0; w < kJoinWarps; ++w) y += s_o[w][d];
+      a.out[unit * D + d] = uint16_t(bf16x2_bits(l == 0.f ? 0.f : y / l, 0.f));
+    }
+    if (threadIdx.x == 0) store_lse(a, unit, m, l);
+    __syncthreads();
+  }
+}
+
+// The weight of every token: the scores again, from the keys alone, against the
+// rows' log-sum-exps.
+template <int D, int NT>
+__global__ void __launch_bounds__(Shape<D>::kThreads, 1) kv4_mass_kernel(const __grid_constant__ AttendArgs a) {
+  constexpr int kThreads = Shape<D>::kThreads, kWarps = Shape<D>::kWarps, kDepth = Shape<D>::kDepth, R = 8 * NT;
+  using Src = KvSrc<D, true>;
+  using W = Walk<kThreads, R, false>;
+  __shared__ uint64_t s_before[kThreads + 1], s_warp[kWarps];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  const uint32_t smem = smem_u32(smem_raw) + (-smem_u32(smem_raw) & 127u);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t magic = q4_magic();
+  Ring<Src, kDepth> ring(smem + uint32_t(warp) * kDepth * Src::kStage,
+                         smem + kWarps * kDepth * Src::kStage + uint32_t(warp) * kDepth * 8, a.s.err, lane);
+  sum_units<kThreads, R, false>(a, s_before, s_warp, nullptr);
+  const uint64_t total = s_before[kThreads];
+  const uint64_t per = (total + a.warps - 1) / a.warps;
+  uint64_t u = per * (blockIdx.x + uint32_t(warp) * gridDim.x);
+  const uint64_t end = min(total, u + per);
+  Pages<Ring<Src, kDepth>, W> pages;
+  W at;
+  if (u < end) {
+    pages.start(a, s_before, u, end - u);
+#pragma unroll 1
+    for (int i = 0; i < kDepth; ++i) pages.issue(a, ring, uint32_t(i), Kv<D>::kBlock, lane);
+    at.find(a, s_before, u);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the log-sum-exps are there
+  Tile<D, NT> tile;
+  float lse[NT];
+  int b = -1;
+  uint32_t seg = 0;  // what the tile holds
+  const uint32_t r = uint32_t(lane) >> 2, q = uint32_t(lane) & 3;
+  for (; u < end; ++u) {
+    ring.wait(lane);
+    const int page = at.q.page0 + at.page;
+    if (pages.there >> ring.slot & 1) {
+      float sum[16] = {};
+      const int tiles = (at.q.rows * a.share + R - 1) / R;
+      for (int t = 0; t < tiles; ++t) {
+        const uint32_t want = uint32_t(t) * a.s.heads + at.seg;
+        if (b != at.b || seg != want) {
+          b = at.b;
+          seg = want;
+          tile.load(a, at.q, seg, lane);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) lse[n] = tile.row[n] >= 0 ? a.lse2[tile.row[n]] : 0.f;
+        }
+        if (tile.sees_none(page)) continue;
+        float z[8][2 * NT];
+        tile.scores(ring.stage(), lane, magic, z);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint32_t see = tile.seen(n, page, lane);
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (see >> k & 1) sum[k] += exp2_approx(z[k / 2][2 * n + k % 2] - lse[n]);
+        }
+      }
+      // over the eight rows: after each exchange a lane goes on with half of the tokens
+#pragma unroll
+      for (int d = 8, bit = 4; d >= 2; d /= 2, bit *= 2) {
+#pragma unroll
+        for (int k = 0; k < d; ++k) {
+          const float keep = (lane & bit) ? sum[k + d] : sum[k], give = (lane & bit) ? sum[k] : sum[k + d];
+          sum[k] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
+        }
+      }
+      // rows r: bit 0 of r chose tokens 8 .., bit 1 4 .., bit 2 2 ..
+      const int pos = page * kPage + 16 * int(q) + 8 * int(r & 1) + 4 * int(r >> 1 & 1) + 2 * int(r >> 2);
+      float* mass = a.mass + (uint64_t(at.b) * a.s.heads + at.seg) * (uint64_t(a.s.width) * kPage) + pos;
+      if (pos < at.q.n) mass[0] += sum[0];
+      if (pos + 1 < at.q.n) mass[1] += sum[1];
+    }
+    __syncwarp();
+    pages.issue(a, ring, ring.slot, Kv<D>::kBlock, lane);
+    ring.next();
+    if (u + 1 < end) at.next(a);
+  }
+}
+
+template <class K>
+cudaError_t launch(K kernel, uint32_t grid, int threads, uint32_t smem, bool dependent, const AttendArgs& a,
+                   cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(uint32_t(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  count_launches(1);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <int D, int NT>
+int attend(AttendArgs& a, int dev, cudaStream_t s) {
+  constexpr int kThreads = Shape<D>::kThreads;
+  const uint32_t sms = uint32_t(sm_count(dev));
+  constexpr uint32_t smem = attend_smem<D, false>(), smem_keys = attend_smem<D, true>();
+  cudaError_t e = cudaFuncSetAttribute(kv4_attend_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e == cudaSuccess && a.mass)
+    e = cudaFuncSetAttribute(kv4_mass_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem_keys));
+  if (e != cudaSuccess) return map_cuda(e);
+  a.warps = sms * Shape<D>::kWarps;
+  auto up = [](uint64_t x) { return (x + 255) & ~uint64_t(255); };
+  const uint64_t slots = uint64_t(2) * a.warps * 8 * NT;
+  const uint64_t b_prefix = up((uint64_t(a.s.B) + 1) * 8), b_lse = a.mass ? up(uint64_t(a.T) * a.q_heads * 4) : 0,
+                 b_ml = up(slots * 8), b_part = slots * D * 4;
+  uint8_t* ws = nullptr;
+  e = pool_alloc(reinterpret_cast<void**>(&ws), b_prefix + b_lse + b_ml + b_part, s);
+  if (e != cudaSuccess) return map_cuda(e);
+  a.prefix = reinterpret_cast<uint64_t*>(ws);
+  a.lse2 = reinterpret_cast<float*>(ws + b_prefix);
+  a.part_ml = reinterpret_cast<float2*>(ws + b_prefix + b_lse);
+  a.part = reinterpret_cast<float*>(ws + b_prefix + b_lse + b_ml);
+  e = launch(kv4_attend_kernel<D, NT>, sms, kThreads, smem, false, a, s);
+  const uint32_t joins = uint32_t(std::min<int64_t>(a.T * a.q_heads, int64_t(sms) * 32));
+  if (e == cudaSuccess)
+    e = launch(kv4_join_kernel<D, NT, kThreads>, joins, 32 * kJoinWarps, 0, true, a, s);
+  if (e == cudaSuccess && a.mass) e = launch(kv4_mass_kernel<D, NT>, sms, kThreads, smem_keys, true, a, s);
+  cudaFreeAsync(ws, s);
+  return map_cuda(e);
 }
 
 }  // namespace
@@ -143,30 +859,18 @@ extern "C" int wcomp_kv4_attend(const wcomp_kv4* c, const wcomp_kv4_attend_args*
   p.q = a.d_q;
   p.q_row = a.q_row;
   p.q_head = a.q_head;
+  p.q_vec = reinterpret_cast<uintptr_t>(a.d_q) % 16 == 0 && a.q_row % 8 == 0 && a.q_head % 8 == 0;
   p.out = a.d_out;
   p.lse = a.d_lse;
   p.mass = a.d_mass;
   p.T = a.T;
   p.q_heads = a.q_heads;
+  p.share = a.q_heads / c->heads;
   p.window = a.window;
   p.scale = a.scale;
-  void* ws = nullptr;
-  const uint64_t b_lse = uint64_t(a.T) * a.q_heads * sizeof(float);
-  cudaError_t e = pool_alloc(&ws, b_lse, s);
-  if (e != cudaSuccess) return map_cuda(e);
-  if (!p.lse) p.lse = static_cast<float*>(ws);
-  const uint32_t grid = uint32_t(std::min<int64_t>(int64_t(cdiv(a.T * a.q_heads, kWarps)), sm_count(c->device) * 64));
-#define CALL(D)                                                                                              \
-  do {                                                                                                       \
-    kv4_attend_kernel<D><<<grid, kThreads, 0, s>>>(p);                                                       \
-    if (p.mass) kv4_mass_kernel<D><<<uint32_t(sm_count(c->device)) * 8, kThreads, 0, s>>>(p);                \
-  } while (0)
-  if (c->dim == 64) CALL(64);
-  else if (c->dim == 128) CALL(128);
-  else CALL(256);
-#undef CALL
-  e = cudaGetLastError();
-  count_launches(p.mass ? 2 : 1);
-  cudaFreeAsync(ws, s);
-  return map_cuda(e);
+  // one tile of 8 where a sequence has no more rows; dim 256 has no registers for 16
+  const bool one = !a.s.d_starts && p.share <= 8;
+  if (c->dim == 64) return one ? attend<64, 1>(p, c->device, s) : attend<64, 2>(p, c->device, s);
+  if (c->dim == 128) return one ? attend<128, 1>(p, c->device, s) : attend<128, 2>(p, c->device, s);
+  return attend<256, 1>(p, c->device, s);
 }

@@ -591,7 +591,8 @@ typedef struct {
  * q as fp16 under a power of two for each row (a BF16 value that is at least 2^-31 of
  * the row's largest keeps its bits); softmax statistics and sums are fp32.  The
  * weights that multiply V are rounded to fp16 times the values' scales under a
- * power of two (half a step: 2^-11 of each).  Infinities and NaN follow the
+ * power of two (half a step: 2^-11 of each; a product that is below 2^-28 of the
+ * sequence's largest scale may err by 2^-39 of that).  Infinities and NaN follow the
  * definition, those of tokens that a row does not see change nothing.  The sums
  * of |q k| have to stay below 2^112.  The order of the sums is fixed: repeated calls
  * give identical bits.

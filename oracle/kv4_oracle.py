@@ -33,6 +33,13 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float, window: in
     over D / 32 scaled groups of at most two steps each and scaled (D / 4 + 8 steps of
     at most EPS of the sum of magnitudes, an exponential's 2^-21 besides); sums over n tokens are fp32
     (n EPS); the weights that multiply v are rounded to fp16 (2^-11), out to BF16 (2^-8).
+
+    Those weights are x = p * s under a power of two 2^k that brings the largest scale of the
+    sequence's values, s_max in [2^E, 2^(E + 1)), to [2^14, 2^15): k = 14 - E.  Below
+    2^-14 fp16 has steps of 2^-24, so x errs by up to 2^-25, which is 2^(-25 - k) = 2^(E - 39) <= 2^-39
+    s_max before the power of two.  Times a code of at most 7 that is 2^-39 of the largest value
+    of the head, 7 s_max; the scale's own rounding to BF16 adds 2^-8 of that.  Each of the n terms
+    may err by as much, and the sum is divided by one of at least 1.
     """
     T, Hq, D = q.shape
     n, H, _ = k.shape
@@ -57,6 +64,7 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float, window: in
                 out[i, hq] = p @ v[lo:hi, h]
                 lse[i, hq] = m + np.log(e.sum())
                 out_tol[i, hq] = 2.0 ** -8 * np.abs(out[i, hq]) + (p * (dz + 2 * off + 2.0 ** -11)) @ np.abs(v[lo:hi, h])
+                out_tol[i, hq] += (hi - lo) * 2.0 ** -39 * (1 + 2.0 ** -8) * np.nanmax(np.abs(v[:, h]))
                 lse_tol[i, hq] = 2 * off + dz.max() + 4 * EPS * (abs(m) + abs(lse[i, hq]))
                 mass[h, lo:hi] += p
                 mass_tol[h, lo:hi] += p * (dz + lse_tol[i, hq] + T * share * EPS)
