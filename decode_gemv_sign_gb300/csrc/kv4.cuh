@@ -30,9 +30,9 @@ constexpr int kKvGroup = 32;    // columns that share a scale
 // high half: lane r of the MMA's eight rows finds its columns of every group in
 // consecutive words.
 //
-// The attention's lane (r, q) reads the key row of token 16 (r / 2) + 2 j + r % 2
-// and the value rows of the tokens 16 q + i; a token's row is swizzled so that
-// both spread over all banks.
+// The attention's lane (r, q) reads key rows of the tokens 8 i + r and value rows of
+// 8 i + 2 q and 8 i + 2 q + 1; a token's row is swizzled so that both spread over
+// all banks, and the scales of the tokens r, 8 + r, 16 + r, ... lie together.
 template <int D>
 struct Kv {
   static constexpr int G = D / kKvGroup;
@@ -43,11 +43,11 @@ struct Kv {
   // From the start of the keys or the values: byte b of token t's row, and its
   // scale of group g.
   static __host__ __device__ __forceinline__ uint32_t at(uint32_t t, uint32_t b) {
-    const uint32_t turn = ((t >> 5) & 1) | ((t >> 3) & 2);  // the two bits of t / 16, exchanged
+    const uint32_t turn = D == 64 ? (t >> 2) & 1 : (t >> 1) & 3;
     return (t * kRow + b) ^ (turn << 5) ^ (D == 256 ? (t & 1) << 4 : 0);
   }
   static __host__ __device__ __forceinline__ uint32_t scale(uint32_t t, uint32_t g) {
-    return kCodes + 2 * (g * kPage + t);
+    return kCodes + 2 * (g * kPage + (t & 7) * 8 + (t >> 3));
   }
 };
 

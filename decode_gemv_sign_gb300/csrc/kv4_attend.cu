@@ -6,17 +6,19 @@
 // 390 cycles before the arithmetic falls behind the HBM.  So both products run on
 // warp-level tensor-core MMAs with the codes as exact fp16 integers (tile.cuh):
 //
-//   S[row, token] = sum over groups of ks[token, group] * (Q[row, group] . Ck[token, group])
-//     M = 16 rows, N = 8 tokens: a group's codes are two MMAs, whose sum enters S
+//   S^T[token, row] = sum over groups of ks[token, group] * (Ck[token, group] . Q[row, group])
+//     M = 16 tokens, N = 8 rows: a group's codes are two MMAs, whose sum enters S
 //     under the group's scale; scores are as exact as fp32 sums of the products.
-//   O^T[column, row] += Cv^T[column, token] * (P[row, token] * vs[token, group])
-//     M = 16 columns of a group, N = 8 rows: the accumulators of S are the B
-//     operand's places without an exchange, and the group's scale goes into them.
+//   O^T[column, row] += Cv^T[column, token] * (vs[token, group] * P^T[token, row])
+//     M = 16 columns of a group, N = 8 rows: the group's scale goes into P, which
+//     one transposition of 8 x 8 turns from the accumulators' into the operand's order.
 //
 // A value row is read by token and transposed by a byte permutation of two
-// tokens' words.  P * vs is rounded to fp16 under a power of two that follows the
+// tokens' words.  vs * P is rounded to fp16 under a power of two that follows the
 // largest scale seen, which the sums O are kept under: one rounding of 2^-11, full
-// precision for products down to 2^-29 of the largest scale's.
+// precision for products down to 2^-28 of the largest scale's.  The softmax's
+// reference is the running maximum rounded up to a whole power of two, so that
+// going over to another scales exactly, by powers of two.
 //
 // Each warp takes an equal run of the call's (sequence, tile of rows, head, page)
 // units through a ring of its own; parts of a softmax that fall on several warps are
@@ -116,16 +118,12 @@ __device__ __forceinline__ void sum_units(const AttendArgs& a, uint64_t* s_befor
   __syncthreads();
 }
 
-// A place in the units' order: sequence, (tile, head) and page, pages fastest.
+// A place in the units' order: sequence, tile, head and page, pages fastest.
 template <int THREADS, int R, bool TILES>
 struct Walk {
-  int b, page;
-  uint32_t seg, segs;
+  int b, page, tile;
+  uint32_t head;
   Seq q;
-  __device__ __forceinline__ void enter(const AttendArgs& a) {
-    q = load_seq<R, TILES>(a, b);
-    segs = uint32_t(q.tiles) * a.s.heads;
-  }
   __device__ __forceinline__ void find(const AttendArgs& a, const uint64_t* s_before, uint64_t u) {
     int lo = 0, hi = THREADS;  // s_before[lo] <= u < s_before[hi]
     while (hi - lo > 1) {
@@ -135,61 +133,73 @@ struct Walk {
     }
     b = lo * ((a.s.B + THREADS - 1) / THREADS);
     u -= s_before[lo];
-    enter(a);
+    q = load_seq<R, TILES>(a, b);
     for (uint64_t w; u >= (w = seq_units(a, q));) {
       u -= w;
-      ++b;
-      enter(a);
+      q = load_seq<R, TILES>(a, ++b);
     }
-    seg = uint32_t(u / uint32_t(q.pages));
+    const uint64_t seg = u / uint32_t(q.pages);
     page = int(u % uint32_t(q.pages));
+    tile = int(seg / a.s.heads);
+    head = uint32_t(seg % a.s.heads);
   }
   // The next unit, which there is.
   __device__ __forceinline__ void next(const AttendArgs& a) {
     if (++page < q.pages) return;
     page = 0;
-    if (++seg < segs) return;
-    seg = 0;
-    do {
-      ++b;
-      enter(a);
-    } while (segs == 0);
+    if (++head < a.s.heads) return;
+    head = 0;
+    if (++tile < q.tiles) return;
+    tile = 0;
+    do q = load_seq<R, TILES>(a, ++b);
+    while (q.tiles == 0);
   }
 };
 
-template <int D, bool KEYS>
+template <int D>
 struct KvSrc {
-  static constexpr uint32_t kStage = KEYS ? Kv<D>::kHalf : Kv<D>::kBlock;
+  static constexpr uint32_t kStage = Kv<D>::kHalf;
   static constexpr bool kCopies = true;
   typedef const uint8_t* Cursor;
   static __device__ __forceinline__ void issue(Cursor& c, uint32_t st, uint32_t bar) { bulk_copy(st, c, kStage, bar); }
 };
 
-// The blocks of a warp's units through its ring, ahead of their use.
-template <class RING, class WALK>
+// The blocks of a warp's units through its ring, ahead of their use: keys, then
+// values (VALUES).
+template <int D, class RING, class WALK, bool VALUES>
 struct Pages {
   WALK it;
   uint64_t left;
   int base = -1, in = -1, id;  // page `base` + lane of sequence `in` is id
   uint32_t there = 0;          // bit per slot: its page exists
+  const uint8_t* values = nullptr;
   __device__ __forceinline__ void start(const AttendArgs& a, const uint64_t* s_before, uint64_t u, uint64_t count) {
     it.find(a, s_before, u);
     left = count;
   }
-  // Copy the next unit's block to `slot`.  A page that does not exist is stood in for
-  // by the cache's first, which nothing is read of.
-  __device__ __forceinline__ void issue(const AttendArgs& a, RING& ring, uint32_t slot, uint32_t block, int lane) {
+  // Copy the next half of a block to `slot`.  A page that does not exist is stood in
+  // for by the cache's first, which nothing is read of.
+  __device__ __forceinline__ void issue(const AttendArgs& a, RING& ring, uint32_t slot, int lane) {
     if (!left) return;
-    const int at = it.q.page0 + it.page;
-    if (in != it.b || at < base || at >= base + 32) {
-      in = it.b;
-      base = at;
-      id = at + lane < (it.q.n + kPage - 1) / kPage ? kv_page(a.s, it.b, at + lane) : -1;
+    if (VALUES && values) {
+      ring.refill(slot, values, lane);
+      values = nullptr;
+    } else {
+      const int at = it.q.page0 + it.page;
+      if (in != it.b || at < base || at >= base + 32) {
+        in = it.b;
+        base = at;
+        id = at + lane < (it.q.n + kPage - 1) / kPage ? kv_page(a.s, it.b, at + lane) : -1;
+      }
+      const int page = __shfl_sync(0xffffffffu, id, at - base);
+      there = page >= 0 ? there | 1u << slot : there & ~(1u << slot);
+      const uint8_t* p = a.cache + (uint64_t(max(page, 0)) * a.s.heads + it.head) * Kv<D>::kBlock;
+      ring.refill(slot, p, lane);
+      if (VALUES) {
+        values = p + Kv<D>::kHalf;
+        return;
+      }
     }
-    const int page = __shfl_sync(0xffffffffu, id, at - base);
-    there = page >= 0 ? there | 1u << slot : there & ~(1u << slot);
-    const uint8_t* p = a.cache + (uint64_t(max(page, 0)) * a.s.heads + it.seg % a.s.heads) * block;
-    ring.refill(slot, p, lane);
     if (--left) it.next(a);
   }
 };
@@ -233,31 +243,34 @@ __device__ __forceinline__ void row_words(uint32_t st, uint32_t t, uint32_t b, u
   }
 }
 
-// A tile's rows: R = 8 NT (row, head of the group) pairs; lane (r, q) has those of
-// r and r + 8.
+// 8 x 8 16-bit values across the warp, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// A tile's rows: R = 8 NT (row, head of the group) pairs.  Lane (r, q) holds the
+// operand's part of row 8 n + r and the state of the rows 8 n + 2 q + e.
 template <int D, int NT>
 struct Tile {
   static constexpr int G = Kv<D>::G;
-  uint32_t a[NT][G][4];     // A operands: the pairs of columns (0, 4), (2, 6), (1, 5), (3, 7) of 32 g + 8 q ..
-  float c[NT];              // what brings a score to base 2: scale, log2 e and the row's power of two
-  int64_t row[NT];          // index of (row, query head) in out and lse, or -1
-  int lo[NT], hi[NT];       // positions that it sees
-  int lo0, lo1, hi0, hi1;   // least and greatest of the tile's
+  uint32_t b[NT][G][4];        // the pairs of columns (0, 4), (2, 6), (1, 5), (3, 7) of 32 g + 8 q ..
+  float c[NT][2];              // what brings a score to base 2: |scale|, log2 e and the row's power of two
+  int64_t row[NT][2];          // index of (row, query head) in out and lse, or -1
+  int lo[NT][2], hi[NT][2];    // positions that it sees
+  int lo0, lo1, hi0, hi1;      // least and greatest of the tile's
 
-  __device__ __forceinline__ void load(const AttendArgs& p, const Seq& s, uint32_t seg, int lane) {
-    const int tile = int(seg / p.s.heads), h = int(seg % p.s.heads);
+  __device__ __forceinline__ void load(const AttendArgs& p, const Seq& s, int tile, int head, int lane) {
     const int r = lane >> 2, q = lane & 3;
     const int pairs = s.rows * p.share;
+    const uint32_t flip = p.scale < 0.f ? 0x80000000u : 0u;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int x = tile * 8 * NT + 8 * n + r, tok = x / p.share;
       const int64_t i = s.first + tok;
-      const int hq = h * p.share + (x - tok * p.share);
       const bool ok = x < pairs && i >= 0 && i < p.T;
-      row[n] = ok ? i * p.q_heads + hq : -1;
-      see(p, s, tok, lo[n], hi[n]);
-      if (!ok) lo[n] = hi[n] = 0;
-      const uint16_t* src = p.q + i * p.q_row + hq * p.q_head + 8 * q;
+      const uint16_t* src = p.q + i * p.q_row + (head * p.share + x - tok * p.share) * p.q_head + 8 * q;
       uint32_t m = 0;
       uint32_t v[G][4];
 #pragma unroll
@@ -279,14 +292,25 @@ struct Tile {
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const int e = record_exponent(m << 16);
-      const float up = power_of_two(e);
-      c[n] = p.scale * kLog2e * power_of_two(-e);
+      const float up = __uint_as_float(__float_as_uint(power_of_two(e)) | flip);
+      // above 0 also where the scale is 0 or underflows: -inf times it stays
+      const float factor = fmaxf(fabsf(p.scale) * kLog2e * power_of_two(-e), 0x1p-126f);
 #pragma unroll
       for (int g = 0; g < G; ++g) {  // columns 2 k, 2 k + 1 in v[g][k]
-        a[n][g][0] = half2_bits(bf16_lo(v[g][0]) * up, bf16_lo(v[g][2]) * up);
-        a[n][g][1] = half2_bits(bf16_lo(v[g][1]) * up, bf16_lo(v[g][3]) * up);
-        a[n][g][2] = half2_bits(bf16_hi(v[g][0]) * up, bf16_hi(v[g][2]) * up);
-        a[n][g][3] = half2_bits(bf16_hi(v[g][1]) * up, bf16_hi(v[g][3]) * up);
+        b[n][g][0] = half2_bits(bf16_lo(v[g][0]) * up, bf16_lo(v[g][2]) * up);
+        b[n][g][1] = half2_bits(bf16_lo(v[g][1]) * up, bf16_lo(v[g][3]) * up);
+        b[n][g][2] = half2_bits(bf16_hi(v[g][0]) * up, bf16_hi(v[g][2]) * up);
+        b[n][g][3] = half2_bits(bf16_hi(v[g][1]) * up, bf16_hi(v[g][3]) * up);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        c[n][k] = __shfl_sync(0xffffffffu, factor, 8 * q + 4 * k);
+        const int y = tile * 8 * NT + 8 * n + 2 * q + k, t = y / p.share;
+        const int64_t j = s.first + t;
+        const bool there = y < pairs && j >= 0 && j < p.T;
+        row[n][k] = there ? j * p.q_heads + head * p.share + (y - t * p.share) : -1;
+        see(p, s, t, lo[n][k], hi[n][k]);
+        if (!there) lo[n][k] = hi[n][k] = 0;
       }
     }
     see(p, s, tile * 8 * NT / p.share, lo0, hi0);
@@ -299,138 +323,132 @@ struct Tile {
   }
   __device__ __forceinline__ bool sees_none(int page) const { return page * kPage >= hi1 || (page + 1) * kPage <= lo0; }
   __device__ __forceinline__ bool sees_all(int page) const { return page * kPage >= lo1 && (page + 1) * kPage <= hi0; }
-  // Which of the lane's 16 tokens of a page, 16 q .., row n of it sees.
-  __device__ __forceinline__ uint32_t seen(int n, int page, int lane) const {
-    const int at = page * kPage + 16 * (lane & 3);
-    return bits_below(hi[n] - at) & ~bits_below(lo[n] - at);
-  }
-  static __device__ __forceinline__ uint32_t bits_below(int k) { return k <= 0 ? 0u : k >= 16 ? 0xFFFFu : (1u << k) - 1u; }
+  // Whether row (n, k) sees position p.
+  __device__ __forceinline__ bool sees(int n, int k, int p) const { return p >= lo[n][k] && p < hi[n][k]; }
 
-  // Scores, times c, of the keys at st: z[j][2 n + e] of row n and token 16 q + 2 j + e.
-  __device__ __forceinline__ void scores(uint32_t st, int lane, uint32_t magic, float (&z)[8][2 * NT]) const {
+  // Scores (before c) of the keys at st: z[i][n][k + 2 h] of token 16 i + 8 h + r and row 8 n + 2 q + k.
+  __device__ __forceinline__ void scores(uint32_t st, int lane, uint32_t magic, float (&z)[4][NT][4]) const {
     const uint32_t r = uint32_t(lane) >> 2, q = uint32_t(lane) & 3;
+    uint32_t sc[G][4];  // word i: the scales of the tokens 16 i + r and 16 i + 8 + r
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint32_t sc[G][4];  // scales of the tokens 16 q + 8 half .., in pairs
+    for (int g = 0; g < G; ++g) lds_words<4>(st + Kv<D>::scale(r, g), sc[g]);
 #pragma unroll
-      for (int g = 0; g < G; ++g) lds_words<4>(st + Kv<D>::scale(16 * q + 8 * half, g), sc[g]);
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[2][G];
+      row_words<D, G>(st, 16 * i + r, q * G * 4, w[0]);
+      row_words<D, G>(st, 16 * i + 8 + r, q * G * 4, w[1]);
 #pragma unroll
-      for (int jj = 0; jj < 4; ++jj) {
-        const int j = 4 * half + jj;
-        uint32_t w[G];
-        row_words<D, G>(st, 16 * (r >> 1) + (r & 1) + 2 * j, q * G * 4, w);
-        float s[2 * NT] = {};
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          uint32_t b[4];
-          q4_operand(w[g], magic, b);
-          float d[4];
-          const uint32_t a0[4] = {a[0][g][0], NT == 2 ? a[NT - 1][g][0] : 0u, a[0][g][1], NT == 2 ? a[NT - 1][g][1] : 0u};
-          const uint32_t a1[4] = {a[0][g][2], NT == 2 ? a[NT - 1][g][2] : 0u, a[0][g][3], NT == 2 ? a[NT - 1][g][3] : 0u};
-          mma_f16_first(d, a0, b[0], b[1]);
-          mma_f16(d, a1, b[2], b[3]);
-          const float s0 = bf16_lo(sc[g][jj]), s1 = bf16_hi(sc[g][jj]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            s[2 * n] += s0 * d[2 * n];
-            s[2 * n + 1] += s1 * d[2 * n + 1];
-          }
-        }
+      for (int g = 0; g < G; ++g) {
+        uint32_t x[4], y[4];
+        q4_operand(w[0][g], magic, x);
+        q4_operand(w[1][g], magic, y);
+        const uint32_t a0[4] = {x[0], y[0], x[1], y[1]}, a1[4] = {x[2], y[2], x[3], y[3]};
+        const float s0 = bf16_lo(sc[g][i]), s1 = bf16_hi(sc[g][i]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          z[j][2 * n] = s[2 * n] * c[n];
-          z[j][2 * n + 1] = s[2 * n + 1] * c[n];
+          float d[4];
+          mma_f16_first(d, a0, b[n][g][0], b[n][g][1]);
+          mma_f16(d, a1, b[n][g][2], b[n][g][3]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) z[i][n][k] = g ? z[i][n][k] + (k < 2 ? s0 : s1) * d[k] : (k < 2 ? s0 : s1) * d[k];
         }
       }
     }
   }
 };
 
-// Sums of a tile so far, and the softmax's state: maximum (base 2) and, per lane, sum.
+// Sums of a tile so far, and the softmax's state.
 template <int D, int NT>
 struct Sums {
   static constexpr int G = Kv<D>::G;
   static constexpr int kNoScale = 120;
-  float m[NT], l[NT];
-  float o[2 * G][NT][4];  // tile 2 g + i: columns 32 g + 4 r + 2 i (+ 1: the last two) of the rows 2 q, 2 q + 1 (+ 8 n)
-  int k;                  // o is under 2^k
+  float m[NT][2], l[NT][2];  // reference (base 2, whole, or -inf) and, of the lane's tokens, sum
+  float o[2 * G][NT][4];     // tile 2 g + i: column 32 g + 4 r + 2 i (+ 1: the last two) of the rows 2 q, 2 q + 1 (+ 8 n)
+  int k;                     // o is under 2^k
 
   __device__ __forceinline__ void clear() {
     k = kNoScale;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      m[n] = -INFINITY;
-      l[n] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[n][e] = -INFINITY;
+        l[n][e] = 0.f;
+      }
 #pragma unroll
       for (int i = 0; i < 2 * G; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][n][e] = 0.f;
     }
   }
-  __device__ __forceinline__ void scale(float f) {
+  __device__ __forceinline__ void scale(int n, float f0, float f1) {
 #pragma unroll
-    for (int i = 0; i < 2 * G; ++i)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][n][e] *= f;
+    for (int i = 0; i < 2 * G; ++i) {
+      o[i][n][0] *= f0;
+      o[i][n][1] *= f1;
+      o[i][n][2] *= f0;
+      o[i][n][3] *= f1;
+    }
   }
 
   // Add a page: scores z, values at st.  `all`: every row sees every token.
   __device__ __forceinline__ void add(const Tile<D, NT>& t, int page, bool all, uint32_t st, int lane, uint32_t magic,
-                                      float (&z)[8][2 * NT]) {
+                                      float (&z)[4][NT][4]) {
     const uint32_t r = uint32_t(lane) >> 2, q = uint32_t(lane) & 3;
-    uint32_t see[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) see[n] = 0xFFFFu;
     if (!all) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        see[n] = t.seen(n, page, lane);
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (!(see[n] >> (2 * j + e) & 1)) z[j][2 * n + e] = -INFINITY;
-      }
+          for (int e = 0; e < 4; ++e)
+            if (!t.sees(n, e % 2, page * kPage + 16 * i + 8 * (e / 2) + int(r))) z[i][n][e] = -INFINITY;
     }
     bool more = false;
-    float next[NT];
+    float next[NT][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float x = m[n];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x = fmaxf(x, fmaxf(z[j][2 * n], z[j][2 * n + 1]));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-      next[n] = x;
-      more |= x > m[n];
-    }
+      for (int e = 0; e < 2; ++e) {
+        float x = fmaxf(z[0][n][e], z[0][n][e + 2]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) x = fmaxf(x, fmaxf(z[i][n][e], z[i][n][e + 2]));
+#pragma unroll
+        for (int d = 4; d <= 16; d *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+        next[n][e] = fmaxf(m[n][e], ceilf(x * t.c[n][e]));
+        more |= next[n][e] > m[n][e];
+      }
     if (__any_sync(0xffffffffu, more)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float down = next[n] > m[n] ? exp2_approx(m[n] - next[n]) : 1.f;
-        l[n] *= down;
-        m[n] = next[n];
-        const float f0 = __shfl_sync(0xffffffffu, down, 8 * q), f1 = __shfl_sync(0xffffffffu, down, 8 * q + 4);
+        float f[2];
 #pragma unroll
-        for (int i = 0; i < 2 * G; ++i) {
-          o[i][n][0] *= f0;
-          o[i][n][1] *= f1;
-          o[i][n][2] *= f0;
-          o[i][n][3] *= f1;
+        for (int e = 0; e < 2; ++e) {
+          f[e] = next[n][e] > m[n][e] ? exp2_approx(m[n][e] - next[n][e]) : 1.f;
+          m[n][e] = next[n][e];
+          l[n][e] *= f[e];
         }
+        scale(n, f[0], f[1]);
       }
     }
     // the largest scale of a value that some row sees: G words a lane, 2 tokens each
     uint32_t top[G];
-    row_words_linear(st + Kv<D>::kCodes + 4 * G * lane, top);
+    if constexpr (G <= 4) {
+      lds_words<G>(st + Kv<D>::kCodes + 4 * G * lane, top);
+    } else {
+#pragma unroll
+      for (int i = 0; i < G; i += 4) {
+        const uint4 v = lds_v4(st + Kv<D>::kCodes + 4 * (G * lane + i));
+        top[i] = v.x; top[i + 1] = v.y; top[i + 2] = v.z; top[i + 3] = v.w;
+      }
+    }
     if (!all) {
 #pragma unroll
       for (int i = 0; i < G; ++i) {
-        const int at = page * kPage + 2 * ((G * lane + i) % 32);
+        const int e = 2 * ((G * lane + i) % 32);  // place of the first in its group (Kv::scale)
+        const int at = page * kPage + (e >> 3) + 8 * (e & 7);
         if (at < t.lo0 || at >= t.hi1) top[i] &= 0xFFFF0000u;
-        if (at + 1 < t.lo0 || at + 1 >= t.hi1) top[i] &= 0xFFFFu;
+        if (at + 8 < t.lo0 || at + 8 >= t.hi1) top[i] &= 0xFFFFu;
       }
     }
 #pragma unroll
@@ -441,85 +459,73 @@ struct Sums {
     if (lo > 0x7F80u) lo = 0;
     const uint32_t largest = __reduce_max_sync(0xffffffffu, max(hi, lo));
     if (largest) {
-      int to = 14 - (int(largest >> 7) - 127);
-      to = to > kNoScale ? kNoScale : to;
+      const int to = min(kNoScale, 14 - (int(largest >> 7) - 127));
       if (to < k) {
         const int d = to - k;
-        scale(power_of_two(d / 2));
-        scale(power_of_two(d - d / 2));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          scale(n, power_of_two(d / 2), power_of_two(d / 2));
+          scale(n, power_of_two(d - d / 2), power_of_two(d - d / 2));
+        }
         k = to;
       }
     }
-    const float up = power_of_two(k);
-    float p[8][2 * NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float from = m[n] == -INFINITY ? 0.f : m[n];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int e = 0; e < 2; ++e) {
+        const float shift = float(k) - (m[n][e] == -INFINITY ? 0.f : m[n][e]);
+        float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float x = exp2_approx(z[j][2 * n + e] - from);
-          l[n] += x;
-          p[j][2 * n + e] = x * up;
-        }
-    }
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint32_t sc[G][4];
+          for (int h = 0; h < 4; h += 2) {
+            const float x = exp2_approx(__fmaf_rn(z[i][n][e + h], t.c[n][e], shift));
+            sum += x;
+            z[i][n][e + h] = x;
+          }
+        l[n][e] = __fmaf_rn(sum, power_of_two(-k), l[n][e]);
+      }
+    uint32_t sc[G][4];
 #pragma unroll
-      for (int g = 0; g < G; ++g) lds_words<4>(st + Kv<D>::scale(16 * q + 8 * half, g), sc[g]);
+    for (int g = 0; g < G; ++g) lds_words<4>(st + Kv<D>::scale(r, g), sc[g]);
 #pragma unroll
-      for (int ii = 0; ii < 2; ++ii) {
-        const int i = 2 * half + ii;  // the tokens 16 q + 4 i ..
-        uint32_t w[4][G / 2];
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[4][G / 2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) row_words<D, G / 2>(st, 16 * q + 4 * i + e, r * (G / 2) * 4, w[e]);
+      for (int e = 0; e < 4; ++e)
+        row_words<D, G / 2>(st, 16 * i + 8 * (e / 2) + 2 * q + e % 2, r * (G / 2) * 4, w[e]);
 #pragma unroll
-        for (int a = 0; a < G / 2; ++a) {
+      for (int a = 0; a < G / 2; ++a) {
 #pragma unroll
-          for (int side = 0; side < 2; ++side) {  // groups 2 a and 2 a + 1
-            const int g = 2 * a + side;
-            uint32_t b[NT][2];
+        for (int side = 0; side < 2; ++side) {  // groups 2 a and 2 a + 1
+          const int g = 2 * a + side;
+          const float s0 = bf16_lo(sc[g][i]), s1 = bf16_hi(sc[g][i]);
+          uint32_t b[NT][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              float x[4];
+          for (int n = 0; n < NT; ++n) {
+            float x[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t s = sc[g][2 * ii + e / 2];
-                x[e] = p[2 * i + e / 2][2 * n + e % 2] * (e % 2 ? bf16_hi(s) : bf16_lo(s));
-              }
-              if (!all) {
+            for (int e = 0; e < 4; ++e) x[e] = z[i][n][e] * (e < 2 ? s0 : s1);
+            if (!all) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (!(see[n] >> (4 * i + e) & 1)) x[e] = 0.f;  // also where the scale is NaN
-              }
-              b[n][0] = half2_bits(x[0], x[1]);
-              b[n][1] = half2_bits(x[2], x[3]);
+              for (int e = 0; e < 4; ++e)  // also where the scale is NaN
+                if (!t.sees(n, e % 2, page * kPage + 16 * i + 8 * (e / 2) + int(r))) x[e] = 0.f;
             }
-            const uint32_t pick = side ? 0x7632 : 0x5410;
-            uint32_t u[4], v[4];
-            q4_operand(prmt(w[0][a], w[1][a], pick), magic, u);  // columns 0, 2, 1, 3 of two tokens
-            q4_operand(prmt(w[2][a], w[3][a], pick), magic, v);
-            const uint32_t a0[4] = {u[0], u[2], v[0], v[2]}, a1[4] = {u[1], u[3], v[1], v[3]};
+            b[n][0] = transpose8(half2_bits(x[0], x[1]));
+            b[n][1] = transpose8(half2_bits(x[2], x[3]));
+          }
+          const uint32_t pick = side ? 0x7632 : 0x5410;
+          uint32_t u[4], v[4];
+          q4_operand(prmt(w[0][a], w[1][a], pick), magic, u);  // columns 0, 2, 1, 3 of two tokens
+          q4_operand(prmt(w[2][a], w[3][a], pick), magic, v);
+          const uint32_t a0[4] = {u[0], u[2], v[0], v[2]}, a1[4] = {u[1], u[3], v[1], v[3]};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma_f16(o[2 * g][n], a0, b[n][0], b[n][1]);
-              mma_f16(o[2 * g + 1][n], a1, b[n][0], b[n][1]);
-            }
+          for (int n = 0; n < NT; ++n) {
+            mma_f16(o[2 * g][n], a0, b[n][0], b[n][1]);
+            mma_f16(o[2 * g + 1][n], a1, b[n][0], b[n][1]);
           }
         }
-      }
-    }
-  }
-  static __device__ __forceinline__ void row_words_linear(uint32_t at, uint32_t (&w)[G]) {
-    if constexpr (G <= 4) {
-      lds_words<G>(at, w);
-    } else {
-#pragma unroll
-      for (int i = 0; i < G; i += 4) {
-        const uint4 v = lds_v4(at + 4 * i);
-        w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
       }
     }
   }
@@ -536,22 +542,19 @@ __device__ __forceinline__ void store_lse(const AttendArgs& a, int64_t row, floa
   if (a.mass) a.lse2[row] = y;
 }
 
-// Warps, ring stages and rows of a tile.  The rings fill an SM's shared memory.
-template <int D>
+// Warps, and half blocks of a warp's ring.  The rings fill an SM's shared memory.
+template <int D, int NT>
 struct Shape {
-  static constexpr int kWarps = D == 64 ? 12 : D == 128 ? 8 : 6;
-  static constexpr int kDepth = D == 64 ? 4 : D == 128 ? 3 : 2;
+  static constexpr int kWarps = D == 64 ? (NT == 1 ? 16 : 12) : D == 128 ? (NT == 1 ? 12 : 8) : 8;
+  static constexpr int kDepth = D == 64 ? (NT == 1 ? 6 : 8) : D == 128 ? (NT == 1 ? 4 : 6) : 3;
   static constexpr int kThreads = 32 * kWarps;
+  static constexpr uint32_t kSmem = kWarps * kDepth * (Kv<D>::kHalf + 8) + 128;
 };
-template <int D, bool KEYS>
-constexpr uint32_t attend_smem() {
-  return Shape<D>::kWarps * Shape<D>::kDepth * (KvSrc<D, KEYS>::kStage + 8) + 128;
-}
 
 template <int D, int NT>
-__global__ void __launch_bounds__(Shape<D>::kThreads, 1) kv4_attend_kernel(const __grid_constant__ AttendArgs a) {
-  constexpr int kThreads = Shape<D>::kThreads, kWarps = Shape<D>::kWarps, kDepth = Shape<D>::kDepth, R = 8 * NT;
-  using Src = KvSrc<D, false>;
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(const __grid_constant__ AttendArgs a) {
+  constexpr int kThreads = Shape<D, NT>::kThreads, kWarps = Shape<D, NT>::kWarps, kDepth = Shape<D, NT>::kDepth, R = 8 * NT;
+  using Src = KvSrc<D>;
   using W = Walk<kThreads, R, true>;
   __shared__ uint64_t s_before[kThreads + 1], s_warp[kWarps];
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -568,10 +571,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) kv4_attend_kernel(const
   uint64_t u = per * me;
   const uint64_t end = min(total, u + per);
   if (u >= end) return;
-  Pages<Ring<Src, kDepth>, W> pages;
+  Pages<D, Ring<Src, kDepth>, W, true> pages;
   pages.start(a, s_before, u, end - u);
 #pragma unroll 1
-  for (int i = 0; i < kDepth; ++i) pages.issue(a, ring, uint32_t(i), Src::kStage, lane);
+  for (int i = 0; i < kDepth; ++i) pages.issue(a, ring, uint32_t(i), lane);
   W at;
   at.find(a, s_before, u);
   Tile<D, NT> tile;
@@ -582,20 +585,23 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) kv4_attend_kernel(const
     const bool first = at.page == 0;
     const int stop = int(min(uint64_t(at.q.pages), uint64_t(at.page) + (end - u)));
     const bool last = stop == at.q.pages;
-    tile.load(a, at.q, at.seg, lane);
+    tile.load(a, at.q, at.tile, int(at.head), lane);
     sums.clear();
     u += uint64_t(stop - at.page);
 #pragma unroll 1
     for (; at.page < stop; ++at.page) {
-      ring.wait(lane);
       const int page = at.q.page0 + at.page;
-      if ((pages.there >> ring.slot & 1) && !tile.sees_none(page)) {
-        float z[8][2 * NT];
-        tile.scores(ring.stage(), lane, magic, z);
-        sums.add(tile, page, tile.sees_all(page), ring.stage() + Kv<D>::kHalf, lane, magic, z);
-      }
+      const bool look = (pages.there >> ring.slot & 1) && !tile.sees_none(page);
+      float z[4][NT][4];
+      ring.wait(lane);
+      if (look) tile.scores(ring.stage(), lane, magic, z);
       __syncwarp();
-      pages.issue(a, ring, ring.slot, Src::kStage, lane);
+      pages.issue(a, ring, ring.slot, lane);
+      ring.next();
+      ring.wait(lane);
+      if (look) sums.add(tile, page, tile.sees_all(page), ring.stage(), lane, magic, z);
+      __syncwarp();
+      pages.issue(a, ring, ring.slot, lane);
       ring.next();
     }
     const bool whole = first && last;
@@ -604,25 +610,23 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) kv4_attend_kernel(const
     float2* ml = a.part_ml + uint64_t(2 * me + first) * R;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float l = sums.l[n];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-      if (q == 0 && tile.row[n] >= 0) {
-        if (whole) store_lse(a, tile.row[n], sums.m[n], l);
-        else ml[8 * n + r] = make_float2(sums.m[n], l);
-      }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {  // row 8 n + 2 q + e
-        const int from = 8 * int(q) + 4 * e;
-        const float g = __shfl_sync(0xffffffffu, f, from);
-        const int64_t row = __shfl_sync(0xffffffffu, tile.row[n], from);
+        float l = sums.l[n][e];
+#pragma unroll
+        for (int d = 4; d <= 16; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
+        const int64_t row = tile.row[n][e];
         if (row < 0) continue;
+        if (r == 0) {
+          if (whole) store_lse(a, row, sums.m[n][e], l);
+          else ml[8 * n + 2 * q + e] = make_float2(sums.m[n][e], l);
+        }
+        const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
 #pragma unroll
         for (int i = 0; i < Kv<D>::G; ++i) {
           float x[4] = {sums.o[2 * i][n][e], sums.o[2 * i][n][2 + e], sums.o[2 * i + 1][n][e], sums.o[2 * i + 1][n][2 + e]};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = x[k] * back * g;
+          for (int k = 0; k < 4; ++k) x[k] = x[k] * back * f;
           if (whole)
             *reinterpret_cast<uint2*>(a.out + row * D + 32 * i + 4 * r) =
                 make_uint2(bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3]));
@@ -641,7 +645,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) kv4_attend_kernel(const
 
 // Join the parts of a (row, query head): one block.
 constexpr int kJoinWarps = 8;
-template <int D, int NT, int THREADS>
+template <int D, int NT>
 __global__ void __launch_bounds__(32 * kJoinWarps) kv4_join_kernel(const __grid_constant__ AttendArgs a) {
   constexpr int R = 8 * NT, V = D / 32;
   __shared__ float s_o[kJoinWarps][D], s_l[kJoinWarps], s_m[kJoinWarps];
@@ -712,9 +716,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv4_join_kernel(const __grid_
 // The weight of every token: the scores again, from the keys alone, against the
 // rows' log-sum-exps.
 template <int D, int NT>
-__global__ void __launch_bounds__(Shape<D>::kThreads, 1) kv4_mass_kernel(const __grid_constant__ AttendArgs a) {
-  constexpr int kThreads = Shape<D>::kThreads, kWarps = Shape<D>::kWarps, kDepth = Shape<D>::kDepth, R = 8 * NT;
-  using Src = KvSrc<D, true>;
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(const __grid_constant__ AttendArgs a) {
+  constexpr int kThreads = Shape<D, NT>::kThreads, kWarps = Shape<D, NT>::kWarps, kDepth = Shape<D, NT>::kDepth, R = 8 * NT;
+  using Src = KvSrc<D>;
   using W = Walk<kThreads, R, false>;
   __shared__ uint64_t s_before[kThreads + 1], s_warp[kWarps];
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -728,63 +732,65 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) kv4_mass_kernel(const _
   const uint64_t per = (total + a.warps - 1) / a.warps;
   uint64_t u = per * (blockIdx.x + uint32_t(warp) * gridDim.x);
   const uint64_t end = min(total, u + per);
-  Pages<Ring<Src, kDepth>, W> pages;
+  Pages<D, Ring<Src, kDepth>, W, false> pages;
   W at;
   if (u < end) {
     pages.start(a, s_before, u, end - u);
 #pragma unroll 1
-    for (int i = 0; i < kDepth; ++i) pages.issue(a, ring, uint32_t(i), Kv<D>::kBlock, lane);
+    for (int i = 0; i < kDepth; ++i) pages.issue(a, ring, uint32_t(i), lane);
     at.find(a, s_before, u);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the log-sum-exps are there
   Tile<D, NT> tile;
-  float lse[NT];
-  int b = -1;
-  uint32_t seg = 0;  // what the tile holds
+  float lse[NT][2];
+  int b = -1, held = 0;
+  uint32_t head = 0;  // what the tile holds
   const uint32_t r = uint32_t(lane) >> 2, q = uint32_t(lane) & 3;
   for (; u < end; ++u) {
     ring.wait(lane);
     const int page = at.q.page0 + at.page;
     if (pages.there >> ring.slot & 1) {
-      float sum[16] = {};
+      float sum[8] = {};  // of the tokens 8 k + r
       const int tiles = (at.q.rows * a.share + R - 1) / R;
       for (int t = 0; t < tiles; ++t) {
-        const uint32_t want = uint32_t(t) * a.s.heads + at.seg;
-        if (b != at.b || seg != want) {
+        if (b != at.b || head != at.head || held != t) {
           b = at.b;
-          seg = want;
-          tile.load(a, at.q, seg, lane);
+          head = at.head;
+          held = t;
+          tile.load(a, at.q, t, int(head), lane);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) lse[n] = tile.row[n] >= 0 ? a.lse2[tile.row[n]] : 0.f;
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) lse[n][e] = tile.row[n][e] >= 0 ? a.lse2[tile.row[n][e]] : 0.f;
         }
         if (tile.sees_none(page)) continue;
-        float z[8][2 * NT];
+        float z[4][NT][4];
         tile.scores(ring.stage(), lane, magic, z);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint32_t see = tile.seen(n, page, lane);
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            if (see >> k & 1) sum[k] += exp2_approx(z[k / 2][2 * n + k % 2] - lse[n]);
-        }
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (tile.sees(n, e, page * kPage + 8 * k + int(r)))
+                sum[k] += exp2_approx(__fmaf_rn(z[k / 2][n][e + 2 * (k % 2)], tile.c[n][e], -lse[n][e]));
       }
-      // over the eight rows: after each exchange a lane goes on with half of the tokens
+      // over the four lanes of a token: after each exchange a lane goes on with half of them
 #pragma unroll
-      for (int d = 8, bit = 4; d >= 2; d /= 2, bit *= 2) {
+      for (int d = 4, bit = 1; d >= 2; d /= 2, bit *= 2) {
 #pragma unroll
         for (int k = 0; k < d; ++k) {
           const float keep = (lane & bit) ? sum[k + d] : sum[k], give = (lane & bit) ? sum[k] : sum[k + d];
           sum[k] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
         }
       }
-      // rows r: bit 0 of r chose tokens 8 .., bit 1 4 .., bit 2 2 ..
-      const int pos = page * kPage + 16 * int(q) + 8 * int(r & 1) + 4 * int(r >> 1 & 1) + 2 * int(r >> 2);
-      float* mass = a.mass + (uint64_t(at.b) * a.s.heads + at.seg) * (uint64_t(a.s.width) * kPage) + pos;
+      const int pos = page * kPage + 8 * (4 * int(q & 1) + 2 * int(q >> 1)) + int(r);
+      float* mass = a.mass + (uint64_t(at.b) * a.s.heads + at.head) * (uint64_t(a.s.width) * kPage) + pos;
       if (pos < at.q.n) mass[0] += sum[0];
-      if (pos + 1 < at.q.n) mass[1] += sum[1];
+      if (pos + 8 < at.q.n) mass[8] += sum[1];
     }
     __syncwarp();
-    pages.issue(a, ring, ring.slot, Kv<D>::kBlock, lane);
+    pages.issue(a, ring, ring.slot, lane);
     ring.next();
     if (u + 1 < end) at.next(a);
   }
@@ -809,14 +815,14 @@ cudaError_t launch(K kernel, uint32_t grid, int threads, uint32_t smem, bool dep
 
 template <int D, int NT>
 int attend(AttendArgs& a, int dev, cudaStream_t s) {
-  constexpr int kThreads = Shape<D>::kThreads;
+  constexpr int kThreads = Shape<D, NT>::kThreads;
   const uint32_t sms = uint32_t(sm_count(dev));
-  constexpr uint32_t smem = attend_smem<D, false>(), smem_keys = attend_smem<D, true>();
+  constexpr uint32_t smem = Shape<D, NT>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(kv4_attend_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e == cudaSuccess && a.mass)
-    e = cudaFuncSetAttribute(kv4_mass_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem_keys));
+    e = cudaFuncSetAttribute(kv4_mass_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return map_cuda(e);
-  a.warps = sms * Shape<D>::kWarps;
+  a.warps = sms * Shape<D, NT>::kWarps;
   auto up = [](uint64_t x) { return (x + 255) & ~uint64_t(255); };
   const uint64_t slots = uint64_t(2) * a.warps * 8 * NT;
   const uint64_t b_prefix = up((uint64_t(a.s.B) + 1) * 8), b_lse = a.mass ? up(uint64_t(a.T) * a.q_heads * 4) : 0,
@@ -831,8 +837,8 @@ int attend(AttendArgs& a, int dev, cudaStream_t s) {
   e = launch(kv4_attend_kernel<D, NT>, sms, kThreads, smem, false, a, s);
   const uint32_t joins = uint32_t(std::min<int64_t>(a.T * a.q_heads, int64_t(sms) * 32));
   if (e == cudaSuccess)
-    e = launch(kv4_join_kernel<D, NT, kThreads>, joins, 32 * kJoinWarps, 0, true, a, s);
-  if (e == cudaSuccess && a.mass) e = launch(kv4_mass_kernel<D, NT>, sms, kThreads, smem_keys, true, a, s);
+    e = launch(kv4_join_kernel<D, NT>, joins, 32 * kJoinWarps, 0, true, a, s);
+  if (e == cudaSuccess && a.mass) e = launch(kv4_mass_kernel<D, NT>, sms, kThreads, smem, true, a, s);
   cudaFreeAsync(ws, s);
   return map_cuda(e);
 }

@@ -14,7 +14,11 @@ Inputs, drawn on the device:
   * q4_encode / q4_decode / q4_gemv: the same rows in 4 bits with one scale per
     `--group` columns;
   * moe: a layer of `--experts` experts of 6144 x 2048, 8 of them a token, for
-    `--batch` tokens, its experts in 4 bits, or in BF16 with `--group 0`.
+    `--batch` tokens, its experts in 4 bits, or in BF16 with `--group 0`;
+  * kv4_append / kv4_read / kv4_attend / kv4_evict: a cache of 8 heads of `--dim`
+    columns with `--batch` sequences of `--tokens` tokens, `--share` query heads
+    to a cached one; evicted to half;
+  * logprobs: `--rows` rows of fp32 logits over 151552 tokens, top 20.
 The operation runs `--reps` times after the containers are built, one
 batched launch per repetition.  Exits non-zero if a decode is not bit-exact
 or a GEMV kernel reports an error.
@@ -81,6 +85,52 @@ def run_moe(W, a, dev):
                       len(set(ids.flatten().tolist())) * one + 2 * E * H + 4 * a.batch * H}))
 
 
+def run_kv4(W, a, dev):
+    import torch
+
+    g = torch.Generator(device=dev)
+    g.manual_seed(1)
+    B, L, H, D = a.batch, a.tokens, 8, a.dim
+    wide = -(-L // 64)
+    pages = torch.randperm(2 * B * wide, device=dev, generator=g).to(torch.int32).view(2, B, wide)
+    lengths = torch.full((B,), L, dtype=torch.int32, device=dev)
+    starts = torch.arange(0, B * L + 1, L, dtype=torch.int32, device=dev)
+
+    def draw(*shape):
+        return torch.empty(*shape, dtype=torch.bfloat16, device=dev).normal_(0, 1, generator=g)
+
+    k, v, q = draw(B * L, H, D), draw(B * L, H, D), draw(B, H * a.share, D)
+    cache = W.kv4_create(2 * B * wide, H, D)
+    W.kv4_append(cache, k, v, pages[0], lengths, starts)
+    mass = torch.zeros(B, H, wide * 64, device=dev)
+    W.kv4_attend(cache, q, pages[0], lengths, mass=mass)
+    for _ in range(a.reps):
+        if a.op == "kv4_append":
+            W.kv4_append(cache, k, v, pages[0], lengths, starts)
+        elif a.op == "kv4_read":
+            W.kv4_read(cache, pages[0], lengths, starts, k=k, v=v)
+        elif a.op == "kv4_attend":
+            W.kv4_attend(cache, q, pages[0], lengths)
+        else:
+            W.kv4_evict(cache, pages[0], lengths, mass, L // 2, L // 16, pages[1])
+    torch.cuda.synchronize()
+    W.device_check()
+    held = H * D * 9 // 8
+    per = {"kv4_attend": held, "kv4_evict": held + 4 * H}.get(a.op, held + 4 * H * D)
+    print(json.dumps({"op": a.op, "algorithmic_bytes_per_rep": B * L * per}))
+
+
+def run_logprobs(W, a, dev):
+    import torch
+
+    logits = torch.empty(a.rows, 151552, device=dev).normal_(0, 3)
+    ids = torch.zeros(a.rows, dtype=torch.int64, device=dev)
+    for _ in range(a.reps):
+        W.logprobs(logits, ids, 20)
+    torch.cuda.synchronize()
+    print(json.dumps({"op": a.op, "algorithmic_bytes_per_rep": 4 * logits.numel()}))
+
+
 def main():
     import torch
 
@@ -88,8 +138,8 @@ def main():
     from decode_gemv_sign_gb300 import wcomp as W
 
     ap = argparse.ArgumentParser()
-    ap.add_argument("--op", choices=["encode", "decode", "gemv", "gemv_bf16", "q4_encode", "q4_decode", "q4_gemv", "moe"],
-                    required=True)
+    ap.add_argument("--op", choices=["encode", "decode", "gemv", "gemv_bf16", "q4_encode", "q4_decode", "q4_gemv", "moe",
+                                     "kv4_append", "kv4_read", "kv4_attend", "kv4_evict", "logprobs"], required=True)
     ap.add_argument("--scheme", choices=["bytesplit", "k15", "both"], default="bytesplit",
                     help="both: every tensor in both schemes, one batch (the benchmark's encode and decode)")
     ap.add_argument("--batch", type=int, default=1)
@@ -98,12 +148,19 @@ def main():
     ap.add_argument("--dense12", action="store_true")
     ap.add_argument("--group", type=int, default=128)
     ap.add_argument("--experts", type=int, default=16)
+    ap.add_argument("--tokens", type=int, default=8192)
+    ap.add_argument("--dim", type=int, default=128)
+    ap.add_argument("--share", type=int, default=8)
     ap.add_argument("--reps", type=int, default=3)
     a = ap.parse_args()
     build.build()
     dev = torch.device("cuda")
     if a.op == "moe":
         return run_moe(W, a, dev)
+    if a.op.startswith("kv4"):
+        return run_kv4(W, a, dev)
+    if a.op == "logprobs":
+        return run_logprobs(W, a, dev)
     if a.op in ("gemv", "gemv_bf16", "q4_encode", "q4_decode", "q4_gemv"):
         base = synth.dense12_spec() if a.dense12 else synth.checkpoint_gemv_spec()
         specs = [dataclasses.replace(base, N=min(a.rows, base.N))]
