@@ -156,51 +156,54 @@ struct Walk {
   }
 };
 
-template <int D>
+template <int D, bool VALUES>
 struct KvSrc {
-  static constexpr uint32_t kStage = Kv<D>::kHalf;
+  static constexpr uint32_t kStage = VALUES ? Kv<D>::kBlock : Kv<D>::kHalf;
   static constexpr bool kCopies = true;
   typedef const uint8_t* Cursor;
   static __device__ __forceinline__ void issue(Cursor& c, uint32_t st, uint32_t bar) { bulk_copy(st, c, kStage, bar); }
 };
 
-// The blocks of a warp's units through its ring, ahead of their use: keys, then
-// values (VALUES).
-template <int D, class RING, class WALK, bool VALUES>
+// The blocks (or, without VALUES, their keys) of a warp's units through its ring,
+// ahead of their use.
+template <int D, class RING, class WALK>
 struct Pages {
   WALK it;
-  uint64_t left;
-  int base = -1, in = -1, id;  // page `base` + lane of sequence `in` is id
-  uint32_t there = 0;          // bit per slot: its page exists
-  const uint8_t* values = nullptr;
+  uint64_t left = 0;      // units to come
+  uint32_t run = 0;       // of which the next are the pages `id` of lanes from, from + 1, ...
+  int from = 0, id = 0;
+  int base = -1, in = -1; // lane l's id is that of page base + l of sequence `in`
+  uint32_t there = 0;     // bit per slot: its page exists
+  const uint8_t* head = nullptr;
   __device__ __forceinline__ void start(const AttendArgs& a, const uint64_t* s_before, uint64_t u, uint64_t count) {
     it.find(a, s_before, u);
     left = count;
   }
-  // Copy the next half of a block to `slot`.  A page that does not exist is stood in
-  // for by the cache's first, which nothing is read of.
+  __device__ __forceinline__ void enter(const AttendArgs& a) {
+    const int lane = threadIdx.x & 31, at = it.q.page0 + it.page;
+    if (in != it.b || at < base || at >= base + 32) {
+      in = it.b;
+      base = at;
+      id = at + lane < (it.q.n + kPage - 1) / kPage ? kv_page(a.s, it.b, at + lane) : -1;
+    }
+    from = at - base;
+    run = uint32_t(min(left, uint64_t(min(32 - from, it.q.pages - it.page))));
+    head = a.cache + uint64_t(it.head) * Kv<D>::kBlock;
+    // the unit after the run
+    it.page += int(run) - 1;
+    if (left > run) it.next(a);
+  }
+  // Copy the next unit's block to `slot`.  A page that does not exist is stood in for
+  // by the cache's first, which nothing is read of.
   __device__ __forceinline__ void issue(const AttendArgs& a, RING& ring, uint32_t slot, int lane) {
     if (!left) return;
-    if (VALUES && values) {
-      ring.refill(slot, values, lane);
-      values = nullptr;
-    } else {
-      const int at = it.q.page0 + it.page;
-      if (in != it.b || at < base || at >= base + 32) {
-        in = it.b;
-        base = at;
-        id = at + lane < (it.q.n + kPage - 1) / kPage ? kv_page(a.s, it.b, at + lane) : -1;
-      }
-      const int page = __shfl_sync(0xffffffffu, id, at - base);
-      there = page >= 0 ? there | 1u << slot : there & ~(1u << slot);
-      const uint8_t* p = a.cache + (uint64_t(max(page, 0)) * a.s.heads + it.head) * Kv<D>::kBlock;
-      ring.refill(slot, p, lane);
-      if (VALUES) {
-        values = p + Kv<D>::kHalf;
-        return;
-      }
-    }
-    if (--left) it.next(a);
+    if (!run) enter(a);
+    const int page = __shfl_sync(0xffffffffu, id, from++);
+    there = page >= 0 ? there | 1u << slot : there & ~(1u << slot);
+    const uint8_t* p = head + uint64_t(uint32_t(max(page, 0))) * (a.s.heads * Kv<D>::kBlock);
+    ring.refill(slot, p, lane);
+    --left;
+    --run;
   }
 };
 
@@ -391,11 +394,12 @@ struct Sums {
     }
   }
 
-  // Add a page: scores z, values at st.  `all`: every row sees every token.
-  __device__ __forceinline__ void add(const Tile<D, NT>& t, int page, bool all, uint32_t st, int lane, uint32_t magic,
+  // Add a page: scores z, values at st.  ALL: every row sees every token.
+  template <bool ALL>
+  __device__ __forceinline__ void add(const Tile<D, NT>& t, int page, uint32_t st, int lane, uint32_t magic,
                                       float (&z)[4][NT][4]) {
     const uint32_t r = uint32_t(lane) >> 2, q = uint32_t(lane) & 3;
-    if (!all) {
+    if (!ALL) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -442,7 +446,7 @@ struct Sums {
         top[i] = v.x; top[i + 1] = v.y; top[i + 2] = v.z; top[i + 3] = v.w;
       }
     }
-    if (!all) {
+    if (!ALL) {
 #pragma unroll
       for (int i = 0; i < G; ++i) {
         const int e = 2 * ((G * lane + i) % 32);  // place of the first in its group (Kv::scale)
@@ -507,7 +511,7 @@ struct Sums {
             float x[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] = z[i][n][e] * (e < 2 ? s0 : s1);
-            if (!all) {
+            if (!ALL) {
 #pragma unroll
               for (int e = 0; e < 4; ++e)  // also where the scale is NaN
                 if (!t.sees(n, e % 2, page * kPage + 16 * i + 8 * (e / 2) + int(r))) x[e] = 0.f;
@@ -542,19 +546,19 @@ __device__ __forceinline__ void store_lse(const AttendArgs& a, int64_t row, floa
   if (a.mass) a.lse2[row] = y;
 }
 
-// Warps, and half blocks of a warp's ring.  The rings fill an SM's shared memory.
+// Warps, and blocks of a warp's ring.  The rings fill an SM's shared memory.
 template <int D, int NT>
 struct Shape {
-  static constexpr int kWarps = D == 64 ? (NT == 1 ? 16 : 12) : D == 128 ? (NT == 1 ? 12 : 8) : 8;
-  static constexpr int kDepth = D == 64 ? (NT == 1 ? 6 : 8) : D == 128 ? (NT == 1 ? 4 : 6) : 3;
+  static constexpr int kWarps = D == 64 ? (NT == 1 ? 16 : 12) : D == 128 ? (NT == 1 ? 12 : 8) : 6;
+  static constexpr int kDepth = D == 64 ? (NT == 1 ? 3 : 4) : D == 128 ? (NT == 1 ? 2 : 3) : 2;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr uint32_t kSmem = kWarps * kDepth * (Kv<D>::kHalf + 8) + 128;
+  static constexpr uint32_t kSmem = kWarps * kDepth * (Kv<D>::kBlock + 8) + 128;
 };
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(const __grid_constant__ AttendArgs a) {
   constexpr int kThreads = Shape<D, NT>::kThreads, kWarps = Shape<D, NT>::kWarps, kDepth = Shape<D, NT>::kDepth, R = 8 * NT;
-  using Src = KvSrc<D>;
+  using Src = KvSrc<D, true>;
   using W = Walk<kThreads, R, true>;
   __shared__ uint64_t s_before[kThreads + 1], s_warp[kWarps];
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -571,7 +575,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
   uint64_t u = per * me;
   const uint64_t end = min(total, u + per);
   if (u >= end) return;
-  Pages<D, Ring<Src, kDepth>, W, true> pages;
+  Pages<D, Ring<Src, kDepth>, W> pages;
   pages.start(a, s_before, u, end - u);
 #pragma unroll 1
   for (int i = 0; i < kDepth; ++i) pages.issue(a, ring, uint32_t(i), lane);
@@ -591,15 +595,13 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
 #pragma unroll 1
     for (; at.page < stop; ++at.page) {
       const int page = at.q.page0 + at.page;
-      const bool look = (pages.there >> ring.slot & 1) && !tile.sees_none(page);
-      float z[4][NT][4];
       ring.wait(lane);
-      if (look) tile.scores(ring.stage(), lane, magic, z);
-      __syncwarp();
-      pages.issue(a, ring, ring.slot, lane);
-      ring.next();
-      ring.wait(lane);
-      if (look) sums.add(tile, page, tile.sees_all(page), ring.stage(), lane, magic, z);
+      if ((pages.there >> ring.slot & 1) && !tile.sees_none(page)) {
+        float z[4][NT][4];
+        tile.scores(ring.stage(), lane, magic, z);
+        if (tile.sees_all(page)) sums.template add<true>(tile, page, ring.stage() + Kv<D>::kHalf, lane, magic, z);
+        else sums.template add<false>(tile, page, ring.stage() + Kv<D>::kHalf, lane, magic, z);
+      }
       __syncwarp();
       pages.issue(a, ring, ring.slot, lane);
       ring.next();
@@ -717,8 +719,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv4_join_kernel(const __grid_
 // rows' log-sum-exps.
 template <int D, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(const __grid_constant__ AttendArgs a) {
-  constexpr int kThreads = Shape<D, NT>::kThreads, kWarps = Shape<D, NT>::kWarps, kDepth = Shape<D, NT>::kDepth, R = 8 * NT;
-  using Src = KvSrc<D>;
+  // twice the stages: they hold keys alone
+  constexpr int kThreads = Shape<D, NT>::kThreads, kWarps = Shape<D, NT>::kWarps, kDepth = 2 * Shape<D, NT>::kDepth - 1,
+                R = 8 * NT;
+  using Src = KvSrc<D, false>;
   using W = Walk<kThreads, R, false>;
   __shared__ uint64_t s_before[kThreads + 1], s_warp[kWarps];
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -732,7 +736,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(con
   const uint64_t per = (total + a.warps - 1) / a.warps;
   uint64_t u = per * (blockIdx.x + uint32_t(warp) * gridDim.x);
   const uint64_t end = min(total, u + per);
-  Pages<D, Ring<Src, kDepth>, W, false> pages;
+  Pages<D, Ring<Src, kDepth>, W> pages;
   W at;
   if (u < end) {
     pages.start(a, s_before, u, end - u);
