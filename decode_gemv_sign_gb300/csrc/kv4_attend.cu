@@ -118,7 +118,9 @@ __device__ __forceinline__ void sum_units(const AttendArgs& a, uint64_t* s_befor
   __syncthreads();
 }
 
-// A place in the units' order: sequence, tile, head and page, pages fastest.
+// A place in the units' order: sequence, tile, head and page, pages fastest.  Kept
+// in shared memory, one for a warp's sums and one for its copies, and moved on by
+// lane 0: registers are what the products want.
 template <int THREADS, int R, bool TILES>
 struct Walk {
   int b, page, tile;
@@ -168,19 +170,17 @@ struct KvSrc {
 // ahead of their use.
 template <int D, class RING, class WALK>
 struct Pages {
-  WALK it;
+  WALK& it;
   uint64_t left = 0;      // units to come
   uint32_t run = 0;       // of which the next are the pages `id` of lanes from, from + 1, ...
   int from = 0, id = 0;
   int base = -1, in = -1; // lane l's id is that of page base + l of sequence `in`
   uint32_t there = 0;     // bit per slot: its page exists
   const uint8_t* head = nullptr;
-  __device__ __forceinline__ void start(const AttendArgs& a, const uint64_t* s_before, uint64_t u, uint64_t count) {
-    it.find(a, s_before, u);
-    left = count;
-  }
-  __device__ __forceinline__ void enter(const AttendArgs& a) {
-    const int lane = threadIdx.x & 31, at = it.q.page0 + it.page;
+  __device__ __forceinline__ Pages(WALK& walk, uint64_t count) : it(walk), left(count) {}
+  __device__ __forceinline__ void enter(const AttendArgs& a, int lane) {
+    __syncwarp();
+    const int at = it.q.page0 + it.page;
     if (in != it.b || at < base || at >= base + 32) {
       in = it.b;
       base = at;
@@ -189,15 +189,18 @@ struct Pages {
     from = at - base;
     run = uint32_t(min(left, uint64_t(min(32 - from, it.q.pages - it.page))));
     head = a.cache + uint64_t(it.head) * Kv<D>::kBlock;
-    // the unit after the run
-    it.page += int(run) - 1;
-    if (left > run) it.next(a);
+    __syncwarp();
+    if (lane == 0) {  // the unit after the run
+      it.page += int(run) - 1;
+      if (left > run) it.next(a);
+    }
+    __syncwarp();
   }
   // Copy the next unit's block to `slot`.  A page that does not exist is stood in for
   // by the cache's first, which nothing is read of.
   __device__ __forceinline__ void issue(const AttendArgs& a, RING& ring, uint32_t slot, int lane) {
     if (!left) return;
-    if (!run) enter(a);
+    if (!run) enter(a, lane);
     const int page = __shfl_sync(0xffffffffu, id, from++);
     there = page >= 0 ? there | 1u << slot : there & ~(1u << slot);
     const uint8_t* p = head + uint64_t(uint32_t(max(page, 0))) * (a.s.heads * Kv<D>::kBlock);
@@ -260,9 +263,7 @@ struct Tile {
   static constexpr int G = Kv<D>::G;
   uint32_t b[NT][G][4];        // the pairs of columns (0, 4), (2, 6), (1, 5), (3, 7) of 32 g + 8 q ..
   float c[NT][2];              // what brings a score to base 2: |scale|, log2 e and the row's power of two
-  int64_t row[NT][2];          // index of (row, query head) in out and lse, or -1
-  int lo[NT][2], hi[NT][2];    // positions that it sees
-  int lo0, lo1, hi0, hi1;      // least and greatest of the tile's
+  int lo0, lo1, hi0, hi1;      // first and one past the last position seen: least and greatest of the tile's rows
 
   __device__ __forceinline__ void load(const AttendArgs& p, const Seq& s, int tile, int head, int lane) {
     const int r = lane >> 2, q = lane & 3;
@@ -306,15 +307,7 @@ struct Tile {
         b[n][g][3] = half2_bits(bf16_hi(v[g][1]) * up, bf16_hi(v[g][3]) * up);
       }
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        c[n][k] = __shfl_sync(0xffffffffu, factor, 8 * q + 4 * k);
-        const int y = tile * 8 * NT + 8 * n + 2 * q + k, t = y / p.share;
-        const int64_t j = s.first + t;
-        const bool there = y < pairs && j >= 0 && j < p.T;
-        row[n][k] = there ? j * p.q_heads + head * p.share + (y - t * p.share) : -1;
-        see(p, s, t, lo[n][k], hi[n][k]);
-        if (!there) lo[n][k] = hi[n][k] = 0;
-      }
+      for (int k = 0; k < 2; ++k) c[n][k] = __shfl_sync(0xffffffffu, factor, 8 * q + 4 * k);
     }
     see(p, s, tile * 8 * NT / p.share, lo0, hi0);
     see(p, s, (min(pairs, (tile + 1) * 8 * NT) - 1) / p.share, lo1, hi1);
@@ -326,8 +319,16 @@ struct Tile {
   }
   __device__ __forceinline__ bool sees_none(int page) const { return page * kPage >= hi1 || (page + 1) * kPage <= lo0; }
   __device__ __forceinline__ bool sees_all(int page) const { return page * kPage >= lo1 && (page + 1) * kPage <= hi0; }
-  // Whether row (n, k) sees position p.
-  __device__ __forceinline__ bool sees(int n, int k, int p) const { return p >= lo[n][k] && p < hi[n][k]; }
+  // Index of row 8 n + 2 q + k in lse (and, times D, in out), or -1; what it sees.
+  static __device__ __forceinline__ int64_t row(const AttendArgs& p, const Seq& s, int tile, int head, int n, int k,
+                                                int lane, int& lo, int& hi) {
+    const int y = tile * 8 * NT + 8 * n + 2 * (lane & 3) + k, t = y / p.share;
+    const int64_t j = s.first + t;
+    see(p, s, t, lo, hi);
+    if (y < s.rows * p.share && j >= 0 && j < p.T) return j * p.q_heads + head * p.share + (y - t * p.share);
+    lo = hi = 0;
+    return -1;
+  }
 
   // Scores (before c) of the keys at st: z[i][n][k + 2 h] of token 16 i + 8 h + r and row 8 n + 2 q + k.
   __device__ __forceinline__ void scores(uint32_t st, int lane, uint32_t magic, float (&z)[4][NT][4]) const {
@@ -395,18 +396,27 @@ struct Sums {
   }
 
   // Add a page: scores z, values at st.  ALL: every row sees every token.
-  template <bool ALL>
-  __device__ __forceinline__ void add(const Tile<D, NT>& t, int page, uint32_t st, int lane, uint32_t magic,
-                                      float (&z)[4][NT][4]) {
+  template <bool ALL, class WALK>
+  __device__ __forceinline__ void add(const AttendArgs& p, const WALK& at, const Tile<D, NT>& t, int page, uint32_t st,
+                                      int lane, uint32_t magic, float (&z)[4][NT][4]) {
     const uint32_t r = uint32_t(lane) >> 2, q = uint32_t(lane) & 3;
+    uint32_t seen[NT][2];  // bit 2 i + h: the token 16 i + 8 h + r
     if (!ALL) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int e = 0; e < 2; ++e) {
+          int lo, hi;
+          Tile<D, NT>::row(p, at.q, at.tile, int(at.head), n, e, lane, lo, hi);
+          seen[n][e] = 0;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (!t.sees(n, e % 2, page * kPage + 16 * i + 8 * (e / 2) + int(r))) z[i][n][e] = -INFINITY;
+          for (int k = 0; k < 8; ++k) {
+            const int pos = page * kPage + 8 * k + int(r);
+            const bool see = pos >= lo && pos < hi;
+            seen[n][e] |= uint32_t(see) << k;
+            if (!see) z[k / 2][n][e + 2 * (k % 2)] = -INFINITY;
+          }
+        }
     }
     bool more = false;
     float next[NT][2];
@@ -514,7 +524,7 @@ struct Sums {
             if (!ALL) {
 #pragma unroll
               for (int e = 0; e < 4; ++e)  // also where the scale is NaN
-                if (!t.sees(n, e % 2, page * kPage + 16 * i + 8 * (e / 2) + int(r))) x[e] = 0.f;
+                if (!(seen[n][e % 2] >> (2 * i + e / 2) & 1)) x[e] = 0.f;
             }
             b[n][0] = transpose8(half2_bits(x[0], x[1]));
             b[n][1] = transpose8(half2_bits(x[2], x[3]));
@@ -561,6 +571,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
   using Src = KvSrc<D, true>;
   using W = Walk<kThreads, R, true>;
   __shared__ uint64_t s_before[kThreads + 1], s_warp[kWarps];
+  __shared__ W s_at[kWarps][2];
   extern __shared__ __align__(128) uint8_t smem_raw[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t smem = smem_u32(smem_raw) + (-smem_u32(smem_raw) & 127u);
@@ -575,38 +586,40 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
   uint64_t u = per * me;
   const uint64_t end = min(total, u + per);
   if (u >= end) return;
-  Pages<D, Ring<Src, kDepth>, W> pages;
-  pages.start(a, s_before, u, end - u);
+  W& at = s_at[warp][0];
+  if (lane == 0) {
+    at.find(a, s_before, u);
+    s_at[warp][1] = at;
+  }
+  __syncwarp();
+  Pages<D, Ring<Src, kDepth>, W> pages(s_at[warp][1], end - u);
 #pragma unroll 1
   for (int i = 0; i < kDepth; ++i) pages.issue(a, ring, uint32_t(i), lane);
-  W at;
-  at.find(a, s_before, u);
   Tile<D, NT> tile;
   Sums<D, NT> sums;
   const uint32_t q = uint32_t(lane) & 3, r = uint32_t(lane) >> 2;
   while (u < end) {
     // a tile's pages, or those of them that fall on this warp
     const bool first = at.page == 0;
-    const int stop = int(min(uint64_t(at.q.pages), uint64_t(at.page) + (end - u)));
-    const bool last = stop == at.q.pages;
+    int page = at.q.page0 + at.page;
+    const int stop = int(min(int64_t(at.q.page0 + at.q.pages), int64_t(page) + int64_t(end - u)));
+    const bool whole = first && stop == at.q.page0 + at.q.pages;
     tile.load(a, at.q, at.tile, int(at.head), lane);
     sums.clear();
-    u += uint64_t(stop - at.page);
+    u += uint64_t(stop - page);
 #pragma unroll 1
-    for (; at.page < stop; ++at.page) {
-      const int page = at.q.page0 + at.page;
+    for (; page < stop; ++page) {
       ring.wait(lane);
       if ((pages.there >> ring.slot & 1) && !tile.sees_none(page)) {
         float z[4][NT][4];
         tile.scores(ring.stage(), lane, magic, z);
-        if (tile.sees_all(page)) sums.template add<true>(tile, page, ring.stage() + Kv<D>::kHalf, lane, magic, z);
-        else sums.template add<false>(tile, page, ring.stage() + Kv<D>::kHalf, lane, magic, z);
+        if (tile.sees_all(page)) sums.template add<true>(a, at, tile, page, ring.stage() + Kv<D>::kHalf, lane, magic, z);
+        else sums.template add<false>(a, at, tile, page, ring.stage() + Kv<D>::kHalf, lane, magic, z);
       }
       __syncwarp();
       pages.issue(a, ring, ring.slot, lane);
       ring.next();
     }
-    const bool whole = first && last;
     const float back = power_of_two(-sums.k);
     float* part = a.part + (uint64_t(2 * me + first) * R) * D;
     float2* ml = a.part_ml + uint64_t(2 * me + first) * R;
@@ -617,7 +630,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
         float l = sums.l[n][e];
 #pragma unroll
         for (int d = 4; d <= 16; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
-        const int64_t row = tile.row[n][e];
+        int lo, hi;
+        const int64_t row = Tile<D, NT>::row(a, at.q, at.tile, int(at.head), n, e, lane, lo, hi);
         if (row < 0) continue;
         if (r == 0) {
           if (whole) store_lse(a, row, sums.m[n][e], l);
@@ -638,10 +652,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
         }
       }
     }
-    if (u < end) {
-      --at.page;  // the tile's last page
+    __syncwarp();
+    if (lane == 0 && u < end) {
+      at.page = at.q.pages - 1;
       at.next(a);
     }
+    __syncwarp();
   }
 }
 
@@ -725,6 +741,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(con
   using Src = KvSrc<D, false>;
   using W = Walk<kThreads, R, false>;
   __shared__ uint64_t s_before[kThreads + 1], s_warp[kWarps];
+  __shared__ W s_at[kWarps][2];
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const uint32_t smem = smem_u32(smem_raw) + (-smem_u32(smem_raw) & 127u);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -736,17 +753,19 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(con
   const uint64_t per = (total + a.warps - 1) / a.warps;
   uint64_t u = per * (blockIdx.x + uint32_t(warp) * gridDim.x);
   const uint64_t end = min(total, u + per);
-  Pages<D, Ring<Src, kDepth>, W> pages;
-  W at;
-  if (u < end) {
-    pages.start(a, s_before, u, end - u);
-#pragma unroll 1
-    for (int i = 0; i < kDepth; ++i) pages.issue(a, ring, uint32_t(i), lane);
+  W& at = s_at[warp][0];
+  if (lane == 0 && u < end) {
     at.find(a, s_before, u);
+    s_at[warp][1] = at;
   }
+  __syncwarp();
+  Pages<D, Ring<Src, kDepth>, W> pages(s_at[warp][1], u < end ? end - u : 0);
+#pragma unroll 1
+  for (int i = 0; i < kDepth; ++i) pages.issue(a, ring, uint32_t(i), lane);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the log-sum-exps are there
   Tile<D, NT> tile;
   float lse[NT][2];
+  int lo[NT][2], hi[NT][2];
   int b = -1, held = 0;
   uint32_t head = 0;  // what the tile holds
   const uint32_t r = uint32_t(lane) >> 2, q = uint32_t(lane) & 3;
@@ -765,7 +784,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(con
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) lse[n][e] = tile.row[n][e] >= 0 ? a.lse2[tile.row[n][e]] : 0.f;
+            for (int e = 0; e < 2; ++e) {
+              const int64_t row = Tile<D, NT>::row(a, at.q, t, int(head), n, e, lane, lo[n][e], hi[n][e]);
+              lse[n][e] = row >= 0 ? a.lse2[row] : 0.f;
+            }
         }
         if (tile.sees_none(page)) continue;
         float z[4][NT][4];
@@ -776,7 +798,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(con
           for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              if (tile.sees(n, e, page * kPage + 8 * k + int(r)))
+              if (page * kPage + 8 * k + int(r) >= lo[n][e] && page * kPage + 8 * k + int(r) < hi[n][e])
                 sum[k] += exp2_approx(__fmaf_rn(z[k / 2][n][e + 2 * (k % 2)], tile.c[n][e], -lse[n][e]));
       }
       // over the four lanes of a token: after each exchange a lane goes on with half of them
@@ -796,7 +818,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(con
     __syncwarp();
     pages.issue(a, ring, ring.slot, lane);
     ring.next();
-    if (u + 1 < end) at.next(a);
+    if (lane == 0 && u + 1 < end) at.next(a);
+    __syncwarp();
   }
 }
 
