@@ -16,13 +16,16 @@ __device__ __forceinline__ uint32_t bf16_bits(float v) {
   return h;
 }
 
-// A row of keys or values is handled by D / 8 neighbouring threads, thread u the
-// columns 8 u .. 8 u + 7; four of them share a group.  The threads of a row are in
-// one warp, which handles 256 / D rows at a time.
+// A row of keys or values is handled by D / 8 neighbouring lanes, lane u the columns
+// 8 u .. 8 u + 7; four of them share a group.  A warp takes one row of the call,
+// whose place it looks up once, and kRound items of it at a time: the keys and
+// values of a head, one after the other.
 template <int D>
-struct RowThreads {
+struct Items {
   static constexpr int kPer = D / 8;
-  static constexpr int kRows = kThreads / kPer;  // of a block
+  static constexpr int kLanes = 32 / kPer;    // items that a warp takes side by side
+  static constexpr int kSteps = 4;            // and one after the other, their loads in flight together
+  static constexpr int kRound = kLanes * kSteps;
 };
 
 // Quantise 8 columns; four lanes share the group's largest magnitude.  `w` gets the
@@ -72,96 +75,110 @@ struct Rows {
   int vec;  // rows are 16-byte aligned
 };
 
-// One warp's unit: 256 / D (token, head) pairs, keys and then values of each.
+// The place of row i: its page's first block, or null, and the token in it.
+// `mine`: whether the row is a sequence's at all.
+__device__ __forceinline__ uint8_t* row_place(const KvSeqs& s, uint8_t* cache, uint64_t page_bytes, int64_t i, uint32_t& t,
+                                              bool& mine) {
+  const int b = kv_sequence(s, i);
+  mine = b >= 0;
+  if (!mine) return nullptr;
+  const int64_t pos = kv_position(s, b, i, kv_length(s, b));
+  const int page = pos < 0 ? -1 : kv_page(s, b, int(pos / kPage));
+  t = uint32_t(pos) % kPage;
+  return page < 0 ? nullptr : cache + uint64_t(page) * page_bytes;
+}
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(KvSeqs s, uint8_t* cache, Rows k, Rows v, int64_t T) {
-  const uint32_t u = threadIdx.x % RowThreads<D>::kPer;
-  const int64_t n = T * s.heads;
-  const int64_t step = int64_t(gridDim.x) * RowThreads<D>::kRows;
-  const int64_t rounds = (n + step - 1) / step;
-  int64_t at = int64_t(blockIdx.x) * RowThreads<D>::kRows + threadIdx.x / RowThreads<D>::kPer;
-  for (int64_t round = 0; round < rounds; ++round, at += step) {
-    // every lane takes part in the exchanges
-    const int64_t i = at / s.heads, h = at % s.heads;
-    const int b = at < n ? kv_sequence(s, i) : -1;
-    uint8_t* block = nullptr;
+__global__ void __launch_bounds__(kThreads) kv4_append_kernel(KvSeqs s, uint8_t* cache, Rows k, Rows v, int64_t T,
+                                                              uint32_t rounds) {
+  using I = Items<D>;
+  const int lane = threadIdx.x % 32;
+  const uint32_t u = uint32_t(lane) % I::kPer;
+  const int64_t units = T * rounds;
+  for (int64_t unit = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; unit < units;
+       unit += int64_t(gridDim.x) * (kThreads / 32)) {
+    const int64_t i = unit / rounds;
+    const uint32_t first = uint32_t(unit % rounds) * I::kRound + uint32_t(lane) / I::kPer;
     uint32_t t = 0;
-    if (b >= 0) {
-      const int64_t pos = kv_position(s, b, i, kv_length(s, b));
-      const int page = pos < 0 ? -1 : kv_page(s, b, int(pos / kPage));
-      t = uint32_t(pos) % kPage;
-      if (page >= 0) block = cache + (uint64_t(page) * s.heads + h) * Kv<D>::kBlock;
+    bool mine;
+    uint8_t* page = row_place(s, cache, uint64_t(s.heads) * Kv<D>::kBlock, i, t, mine);
+    if (!page) continue;
+    uint32_t x[I::kSteps][4];
+#pragma unroll
+    for (int j = 0; j < I::kSteps; ++j) {
+      const uint32_t item = first + j * I::kLanes, h = item / 2;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[j][e] = 0;
+      if (h >= s.heads) continue;
+      const Rows& r = item % 2 ? v : k;
+      const uint16_t* p = r.p + i * r.row + h * r.head + 8 * u;
+      if (r.vec) {
+        const uint4 y = *reinterpret_cast<const uint4*>(p);
+        x[j][0] = y.x; x[j][1] = y.y; x[j][2] = y.z; x[j][3] = y.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[j][e] = p[2 * e] | uint32_t(p[2 * e + 1]) << 16;
+      }
     }
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      const Rows& r = part ? v : k;
-      uint32_t x[4] = {0, 0, 0, 0};
-      if (block) {
-        const uint16_t* p = r.p + i * r.row + h * r.head + 8 * u;
-        if (r.vec) {
-          const uint4 y = *reinterpret_cast<const uint4*>(p);
-          x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = p[2 * j] | uint32_t(p[2 * j + 1]) << 16;
-        }
-      }
+    for (int j = 0; j < I::kSteps; ++j) {
+      const uint32_t item = first + j * I::kLanes, h = item / 2, part = item % 2;
       uint32_t w;
-      const uint32_t scale = quantise8(x, w);
-      if (part) w = value_word(w, u);
-      if (block) {
-        const uint32_t index = part ? value_index<D>(u) : key_index<D>(u);
-        *reinterpret_cast<uint32_t*>(block + part * Kv<D>::kHalf + Kv<D>::at(t, 4 * index)) = w;
-        if ((u & 3) == 0)
-          *reinterpret_cast<uint16_t*>(block + part * Kv<D>::kHalf + Kv<D>::scale(t, u >> 2)) = uint16_t(scale);
-      }
+      const uint32_t scale = quantise8(x[j], w);  // every lane takes part in the exchanges
+      const uint32_t by_value = value_word(w, u);
+      if (h >= s.heads) continue;
+      uint8_t* half = page + h * Kv<D>::kBlock + part * Kv<D>::kHalf;
+      const uint32_t index = part ? value_index<D>(u) : key_index<D>(u);
+      *reinterpret_cast<uint32_t*>(half + Kv<D>::at(t, 4 * index)) = part ? by_value : w;
+      if ((u & 3) == 0) *reinterpret_cast<uint16_t*>(half + Kv<D>::scale(t, u >> 2)) = uint16_t(scale);
     }
   }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(KvSeqs s, const uint8_t* cache, uint16_t* k, uint16_t* v,
-                                                            int64_t T, int vec) {
-  const uint32_t u = threadIdx.x % RowThreads<D>::kPer;
-  const int64_t n = T * s.heads;
-  const int64_t step = int64_t(gridDim.x) * RowThreads<D>::kRows;
-  const int64_t rounds = (n + step - 1) / step;
-  int64_t at = int64_t(blockIdx.x) * RowThreads<D>::kRows + threadIdx.x / RowThreads<D>::kPer;
-  for (int64_t round = 0; round < rounds; ++round, at += step) {
-    const int64_t i = at / s.heads, h = at % s.heads;
-    const int b = at < n ? kv_sequence(s, i) : -1;
-    const uint8_t* block = nullptr;
+                                                            int64_t T, uint32_t rounds, int vec) {
+  using I = Items<D>;
+  const int lane = threadIdx.x % 32;
+  const uint32_t u = uint32_t(lane) % I::kPer;
+  const int64_t units = T * rounds;
+  for (int64_t unit = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; unit < units;
+       unit += int64_t(gridDim.x) * (kThreads / 32)) {
+    const int64_t i = unit / rounds;
+    const uint32_t first = uint32_t(unit % rounds) * I::kRound + uint32_t(lane) / I::kPer;
     uint32_t t = 0;
-    if (b >= 0) {
-      const int64_t pos = kv_position(s, b, i, kv_length(s, b));
-      const int page = pos < 0 ? -1 : kv_page(s, b, int(pos / kPage));
-      t = uint32_t(pos) % kPage;
-      if (page >= 0) block = cache + (uint64_t(page) * s.heads + h) * Kv<D>::kBlock;
+    bool mine;
+    const uint8_t* page = row_place(s, const_cast<uint8_t*>(cache), uint64_t(s.heads) * Kv<D>::kBlock, i, t, mine);
+    if (!mine) continue;
+    uint32_t w[I::kSteps], scale[I::kSteps];
+#pragma unroll
+    for (int j = 0; j < I::kSteps; ++j) {
+      const uint32_t item = first + j * I::kLanes, h = item / 2, part = item % 2;
+      w[j] = 0x88888888u;
+      scale[j] = 0;
+      if (!page || h >= s.heads) continue;
+      const uint8_t* half = page + h * Kv<D>::kBlock + part * Kv<D>::kHalf;
+      w[j] = *reinterpret_cast<const uint32_t*>(half + Kv<D>::at(t, 4 * (part ? value_index<D>(u) : key_index<D>(u))));
+      scale[j] = *reinterpret_cast<const uint16_t*>(half + Kv<D>::scale(t, u >> 2));
     }
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      uint32_t w = 0x88888888u, scale = 0;
-      if (block) {
-        const uint32_t index = part ? value_index<D>(u) : key_index<D>(u);
-        w = *reinterpret_cast<const uint32_t*>(block + part * Kv<D>::kHalf + Kv<D>::at(t, 4 * index));
-        scale = *reinterpret_cast<const uint16_t*>(block + part * Kv<D>::kHalf + Kv<D>::scale(t, u >> 2));
-      }
-      if (part) w = value_word(w, u);
+    for (int j = 0; j < I::kSteps; ++j) {
+      const uint32_t item = first + j * I::kLanes, h = item / 2, part = item % 2;
+      const uint32_t by_value = value_word(w[j], u);
+      if (h >= s.heads) continue;
+      const uint32_t c = part ? by_value : w[j];
+      const float f = bf16_value(scale[j]);
       uint32_t x[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float f = bf16_value(scale);
-        x[j] = bf16_bits(float(int((w >> (8 * j)) & 15) - 8) * f) |
-               bf16_bits(float(int((w >> (8 * j + 4)) & 15) - 8) * f) << 16;
-      }
-      if (b >= 0) {
-        uint16_t* p = (part ? v : k) + at * D + 8 * u;
-        if (vec) {
-          *reinterpret_cast<uint4*>(p) = make_uint4(x[0], x[1], x[2], x[3]);
-        } else {
+      for (int e = 0; e < 4; ++e)
+        x[e] = bf16_bits(float(int((c >> (8 * e)) & 15) - 8) * f) |
+               bf16_bits(float(int((c >> (8 * e + 4)) & 15) - 8) * f) << 16;
+      uint16_t* p = (part ? v : k) + (i * s.heads + h) * D + 8 * u;
+      if (vec) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(x[0], x[1], x[2], x[3]);
+      } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) p[j] = uint16_t(x[j / 2] >> (16 * (j % 2)));
-        }
+        for (int e = 0; e < 8; ++e) p[e] = uint16_t(x[e / 2] >> (16 * (e % 2)));
       }
     }
   }
@@ -182,7 +199,9 @@ struct EvictArgs {
   int width_out, keep, recent;
 };
 
-constexpr int kChoose = 1024;
+constexpr int kChoose = 1024, kChooseWarps = kChoose / 32;
+constexpr int kHeld = 16;   // keys that a thread holds in registers: 16384 tokens a block
+constexpr int kMaxTeam = 8; // blocks that share a sequence and head
 
 // A mass as a number that orders as it does: NaN lowest, -0 and 0 alike.
 __device__ __forceinline__ uint32_t mass_key(float m) {
@@ -191,98 +210,174 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive sum over the block of a count; `total` gets the sum of all.
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* s_warp, uint32_t& total) {
-  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t x = v;
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= uint32_t(d)) x += y;
-  }
-  __syncthreads();  // s_warp may still be read
-  if (lane == 31) s_warp[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    uint32_t y = s_warp[lane];
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const uint32_t z = __shfl_up_sync(0xffffffffu, y, d);
-      if (lane >= uint32_t(d)) y += z;
-    }
-    s_warp[lane] = y;
-  }
-  __syncthreads();
-  total = s_warp[31];
-  return x - v + (warp ? s_warp[warp - 1] : 0u);
+__device__ __forceinline__ uint32_t team_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void team_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A word of block `rank`'s shared memory, at the place that p has in this one.
+__device__ __forceinline__ uint32_t team_load(const uint32_t* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.u32 %0, [r];\n\t}"
+               : "=r"(v)
+               : "r"(smem_u32(p)), "r"(rank)
+               : "memory");
+  return v;
 }
 
-// The `want` largest keys of the first n0 tokens, by a radix selection of 8 bits at
-// a time: the key of the last one taken, and how many of those that equal it.
-__global__ void __launch_bounds__(kChoose) kv4_choose_kernel(EvictArgs a) {
-  __shared__ uint32_t s_bins[256], s_warp[32], s_pick[2];
-  const uint32_t tid = threadIdx.x;
-  const int64_t units = int64_t(a.s.B) * a.s.heads;
-  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int b = int(unit / a.s.heads);
-    const int n = kv_length(a.s, b);
-    const int m = min(n, a.keep);
-    const float* mass = a.mass + unit * a.s.width * kPage;
-    float* mass_out = a.mass_out + unit * a.width_out * kPage;
-    int32_t* kept = a.kept + unit * a.keep;
-    if (unit % a.s.heads == 0 && tid == 0) a.lengths_out[b] = m;
-    const int n0 = m < n ? n - a.recent : 0;         // tokens to choose from; those behind are kept
-    uint32_t want = m < n ? uint32_t(a.keep - a.recent) : 0u;
-    uint32_t prefix = 0, ties = 0;
-    if (want) {
-      for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) s_bins[tid] = 0;
-        __syncthreads();
-        for (int i = int(tid); i < n0; i += kChoose) {
-          const uint32_t k = mass_key(mass[i]);
-          if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&s_bins[(k >> shift) & 255], 1u);
-        }
-        __syncthreads();
-        if (tid == 0) {
-          uint32_t left = want;
-          int d = 255;
-          while (d > 0 && s_bins[d] < left) left -= s_bins[d--];
-          s_pick[0] = uint32_t(d);
-          s_pick[1] = left;
-        }
-        __syncthreads();
-        prefix = prefix << 8 | s_pick[0];
-        want = s_pick[1];
-      }
-      ties = want;
+// The tokens of one sequence and head that are kept: one block, or a cluster of
+// them for long sequences.  A warp has a run of consecutive tokens, their keys in
+// registers as far as those go, so a step of the search for the last key taken is
+// comparisons and one sum over the block: two bits of the key a step.  (A radix
+// selection took 45 us for 256 sequences and heads of up to 16384 tokens: few
+// exponents, so its counters in shared memory are fought over.)
+struct Choose {
+  uint32_t sums[2][kChooseWarps][3];  // by the parity of the step
+  uint32_t team[2][3];                // this block's
+  uint32_t below[2][kChooseWarps];
+};
+
+__global__ void __launch_bounds__(kChoose) kv4_choose_kernel(EvictArgs a, uint32_t team) {
+  __shared__ Choose sh;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = team > 1 ? team_rank() : 0;
+  const int64_t unit = blockIdx.x / team;
+  const int b = int(unit / a.s.heads);
+  const int n = kv_length(a.s, b);
+  const int m = min(n, a.keep);
+  const float* mass = a.mass + unit * (int64_t(a.s.width) * kPage);
+  float* mass_out = a.mass_out + unit * (int64_t(a.width_out) * kPage);
+  int32_t* kept = a.kept + unit * a.keep;
+  if (unit % a.s.heads == 0 && tid == 0 && rank == 0) a.lengths_out[b] = m;
+  const bool all = m == n;
+  const int n0 = all ? 0 : n - a.recent;              // tokens to choose from; those behind are kept
+  const uint32_t want = all ? 0 : uint32_t(a.keep - a.recent);
+  // this warp's tokens: i0 + 32 k + lane below i1
+  const int run = ((n + 31) / 32 + int(team * kChooseWarps) - 1) / int(team * kChooseWarps) * 32;
+  const int64_t start = int64_t(rank * kChooseWarps + warp) * run;
+  const int i0 = int(min(int64_t(n), start)), i1 = min(n, i0 + run), steps = run / 32;
+  uint32_t held[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int i = i0 + 32 * k + int(lane);
+    held[k] = i < i1 ? mass_key(mass[i]) : 0u;
+  }
+  auto key_at = [&](int k) {
+    const int i = i0 + 32 * k + int(lane);
+    return i < i1 ? mass_key(mass[i]) : 0u;
+  };
+  // keys of the tokens to choose from, others 0: no candidate below is 0
+  auto candidates = [&](auto f) {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) f(i0 + 32 * k + int(lane) < min(i1, n0) ? held[k] : 0u);
+    for (int k = kHeld; k < steps; ++k) f(i0 + 32 * k + int(lane) < min(i1, n0) ? key_at(k) : 0u);
+  };
+  // the sum of three counts over all tokens
+  uint32_t parity = 0;
+  auto sum3 = [&](uint32_t (&c)[3]) {
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      c[j] = __reduce_add_sync(0xffffffffu, c[j]);
+      if (lane == 0) sh.sums[parity][warp][j] = c[j];
     }
-    // in order: above the last key, or equal to it while there are some to take
-    uint32_t done = 0, seen = 0;
-    for (int i0 = 0; i0 < n; i0 += kChoose) {
-      const int i = i0 + int(tid);
-      const float x = i < n ? mass[i] : 0.f;
-      const uint32_t k = mass_key(x);
-      const bool tie = i < n0 && ties && k == prefix;
-      uint32_t all_ties = 0, all = 0;
-      const uint32_t before = block_scan(tie, s_warp, all_ties);
-      const bool take = i < n && (m == n || i >= n0 || (ties && k > prefix) || (tie && seen + before < ties));
-      const uint32_t place = done + block_scan(take, s_warp, all);
-      if (take) {
-        kept[place] = i;
-        mass_out[place] = x;
-      }
-      done += all;
-      seen += all_ties;
-    }
-    for (int i = m + int(tid); i < a.keep; i += kChoose) kept[i] = -1;
-    for (int i = m + int(tid); i < a.width_out * kPage; i += kChoose) mass_out[i] = 0.f;
     __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 3; ++j) c[j] = __reduce_add_sync(0xffffffffu, sh.sums[parity][lane][j]);
+    if (team > 1) {
+      if (tid < 3) sh.team[parity][tid] = c[tid];
+      team_sync();
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        c[j] = __reduce_add_sync(0xffffffffu, lane < team ? team_load(&sh.team[parity][j], lane) : 0u);
+    }
+    parity ^= 1;
+  };
+  // the largest key that at least `want` tokens reach
+  uint32_t key = 0;
+  if (want) {
+    for (int shift = 30; shift >= 0; shift -= 2) {
+      uint32_t c[3] = {0, 0, 0};
+      candidates([&](uint32_t k) {
+#pragma unroll
+        for (uint32_t j = 0; j < 3; ++j) c[j] += k >= (key | (j + 1) << shift);
+      });
+      sum3(c);
+      key |= (c[2] >= want ? 3u : c[1] >= want ? 2u : c[0] >= want ? 1u : 0u) << shift;
+    }
   }
+  // above it all are taken; of those that equal it, the first ones
+  const bool some = want != 0;
+  uint32_t above = 0, equal = 0;
+  auto count = [&](int i, uint32_t k) {
+    const bool in = i < min(i1, n0) && some;
+    above += __popc(__ballot_sync(0xffffffffu, (i < i1 && i >= n0) || (in && k > key)));
+    equal += __popc(__ballot_sync(0xffffffffu, in && k == key));
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) count(i0 + 32 * k + int(lane), held[k]);
+  for (int k = kHeld; k < steps; ++k) count(i0 + 32 * k + int(lane), key_at(k));
+  // sums over the warps before this one, and the number taken above the key
+  uint32_t before[2] = {0, 0}, taken;
+  {
+    if (lane == 0) {
+      sh.below[0][warp] = above;
+      sh.below[1][warp] = equal;
+    }
+    uint32_t c[3] = {lane == 0 ? above : 0u, lane == 0 ? equal : 0u, 0u};
+    uint32_t own[2];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      own[j] = __reduce_add_sync(0xffffffffu, sh.below[j][lane]);
+      before[j] = __reduce_add_sync(0xffffffffu, lane < warp ? sh.below[j][lane] : 0u);
+    }
+    if (team > 1) {
+      if (tid < 2) sh.team[parity][tid] = own[tid];
+      team_sync();
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t v = lane < team ? team_load(&sh.team[parity][j], lane) : 0u;
+        before[j] += __reduce_add_sync(0xffffffffu, lane < rank ? v : 0u);
+        c[j] = __reduce_add_sync(0xffffffffu, v);
+      }
+    } else {
+      c[0] = own[0];
+    }
+    taken = c[0];
+  }
+  const uint32_t ties = some ? uint32_t(m) - taken : 0u;  // of the equal ones, the first `ties`
+  uint32_t seen = before[1], place = before[0] + min(before[1], ties);
+  auto emit = [&](int i, uint32_t k) {
+    const bool in = i < min(i1, n0) && some;
+    const bool tie = in && k == key;
+    const uint32_t tied = __ballot_sync(0xffffffffu, tie), lower = (1u << lane) - 1u;
+    const bool take = (i < i1 && i >= n0) || (in && k > key) || (tie && seen + __popc(tied & lower) < ties);
+    const uint32_t takes = __ballot_sync(0xffffffffu, take);
+    if (take) {
+      const uint32_t to = place + __popc(takes & lower);
+      kept[to] = i;
+      mass_out[to] = mass[i];
+    }
+    seen += __popc(tied);
+    place += __popc(takes);
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) emit(i0 + 32 * k + int(lane), held[k]);
+  for (int k = kHeld; k < steps; ++k) emit(i0 + 32 * k + int(lane), key_at(k));
+  for (int i = m + int(rank * kChoose + tid); i < a.keep; i += int(team * kChoose)) kept[i] = -1;
+  for (int i = m + int(rank * kChoose + tid); i < a.width_out * kPage; i += int(team * kChoose)) mass_out[i] = 0.f;
+  if (team > 1) team_sync();  // a block's shared memory stays while others read it
 }
 
+constexpr int kMove = 128;
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv4_move_kernel(EvictArgs a) {
+__global__ void __launch_bounds__(kMove) kv4_move_kernel(EvictArgs a) {
   using L = Kv<D>;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ int64_t s_src[kPage];  // the block's source, or -1, and the token in it
   __shared__ uint32_t s_at[kPage];
   const int64_t tiles = (a.keep + kPage - 1) / kPage;
@@ -307,14 +402,14 @@ __global__ void __launch_bounds__(kThreads) kv4_move_kernel(EvictArgs a) {
     }
     uint8_t* dst = a.cache + (uint64_t(out) * a.s.heads + h) * L::kBlock;
     constexpr int kPieces = 2 * L::kRow / 16;  // 16-byte pieces of a token's keys and values
-    for (uint32_t j = threadIdx.x; j < kPage * kPieces; j += kThreads) {
+    for (uint32_t j = threadIdx.x; j < kPage * kPieces; j += kMove) {
       const uint32_t t = j / kPieces, piece = j % kPieces;
       if (s_src[t] < 0) continue;
       const uint32_t part = piece / (kPieces / 2) * L::kHalf, byte = piece % (kPieces / 2) * 16;
       *reinterpret_cast<uint4*>(dst + part + L::at(t, byte)) =
           *reinterpret_cast<const uint4*>(a.cache + s_src[t] + part + L::at(s_at[t], byte));
     }
-    for (uint32_t j = threadIdx.x; j < kPage * 2 * L::G; j += kThreads) {
+    for (uint32_t j = threadIdx.x; j < kPage * 2 * L::G; j += kMove) {
       const uint32_t t = j % kPage, g = j / kPage % L::G, part = j / kPage / L::G * L::kHalf;
       if (s_src[t] < 0) continue;
       *reinterpret_cast<uint16_t*>(dst + part + L::scale(t, g)) =
@@ -341,7 +436,7 @@ bool rows_vec(const uint16_t* p, int64_t row, int64_t head) {
 int kv_check(const wcomp_kv4* c, const wcomp_kv4_seqs& s, int64_t T) {
   if (!c || s.B < 0 || s.width < 1 || T < 0 || (s.B && (!s.d_table || !s.d_lengths))) return WCOMP_EINVAL;
   if (!s.d_starts && T != s.B) return WCOMP_EINVAL;
-  if (int64_t(s.width) * kPage >= (int64_t(1) << 31) || T >= (int64_t(1) << 31)) return WCOMP_EUNSUPPORTED;
+  if (int64_t(s.width) * kPage > (int64_t(1) << 30) || T >= (int64_t(1) << 31)) return WCOMP_EUNSUPPORTED;
   return WCOMP_OK;
 }
 
@@ -402,9 +497,12 @@ extern "C" int wcomp_kv4_append(wcomp_kv4* c, const wcomp_kv4_seqs* seqs, const 
   if ((st = kv_seqs(c, *seqs, &s)) != WCOMP_OK) return st;
   if (T == 0 || s.B == 0) return WCOMP_OK;
   const Rows k{d_k, k_row, k_head, rows_vec(d_k, k_row, k_head)}, v{d_v, v_row, v_head, rows_vec(d_v, v_row, v_head)};
-#define CALL(D)                                                                                             \
-  kv4_append_kernel<D><<<grid_of(cdiv(T * c->heads, RowThreads<D>::kRows), c->device), kThreads, 0,         \
-                         static_cast<cudaStream_t>(stream)>>>(s, c->d, k, v, T)
+#define CALL(D)                                                                                            \
+  do {                                                                                                     \
+    const uint32_t rounds = uint32_t(cdiv(2 * uint64_t(c->heads), Items<D>::kRound));                      \
+    kv4_append_kernel<D><<<grid_of(int64_t(cdiv(T * rounds, kThreads / 32)), c->device), kThreads, 0,      \
+                           static_cast<cudaStream_t>(stream)>>>(s, c->d, k, v, T, rounds);                 \
+  } while (0)
   WCOMP_KV_DIM(c->dim, CALL);
 #undef CALL
   count_launches(1);
@@ -420,9 +518,12 @@ extern "C" int wcomp_kv4_read(const wcomp_kv4* c, const wcomp_kv4_seqs* seqs, ui
   if ((st = kv_seqs(c, *seqs, &s)) != WCOMP_OK) return st;
   if (T == 0 || s.B == 0) return WCOMP_OK;
   const int vec = rows_vec(d_k, 0, 0) && rows_vec(d_v, 0, 0);
-#define CALL(D)                                                                                           \
-  kv4_read_kernel<D><<<grid_of(cdiv(T * c->heads, RowThreads<D>::kRows), c->device), kThreads, 0,         \
-                       static_cast<cudaStream_t>(stream)>>>(s, c->d, d_k, d_v, T, vec)
+#define CALL(D)                                                                                          \
+  do {                                                                                                   \
+    const uint32_t rounds = uint32_t(cdiv(2 * uint64_t(c->heads), Items<D>::kRound));                    \
+    kv4_read_kernel<D><<<grid_of(int64_t(cdiv(T * rounds, kThreads / 32)), c->device), kThreads, 0,      \
+                         static_cast<cudaStream_t>(stream)>>>(s, c->d, d_k, d_v, T, rounds, vec);        \
+  } while (0)
   WCOMP_KV_DIM(c->dim, CALL);
 #undef CALL
   count_launches(1);
@@ -440,7 +541,8 @@ extern "C" int wcomp_kv4_evict(wcomp_kv4* c, const wcomp_kv4_evict_args* args, v
     return WCOMP_EINVAL;
   int st = kv_check(c, {a.d_table, a.d_lengths, nullptr, a.B, a.width}, a.B);
   if (st != WCOMP_OK) return st;
-  if (int64_t(a.width_out) * kPage >= (int64_t(1) << 31)) return WCOMP_EUNSUPPORTED;
+  if (int64_t(a.width_out) * kPage > (int64_t(1) << 30) || int64_t(a.B) * c->heads >= (int64_t(1) << 28))
+    return WCOMP_EUNSUPPORTED;
   EvictArgs p{};
   if ((st = kv_seqs(c, {a.d_table, a.d_lengths, nullptr, a.B, a.width}, &p.s)) != WCOMP_OK) return st;
   if (a.B == 0) return WCOMP_OK;
@@ -462,13 +564,31 @@ extern "C" int wcomp_kv4_evict(wcomp_kv4* c, const wcomp_kv4_evict_args* args, v
       return map_cuda(e);
     }
   }
-  kv4_choose_kernel<<<grid_of(units, c->device), kChoose, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  // blocks share a long sequence while that leaves each something and the GPU has room
+  uint32_t team = 1;
+  while (team < kMaxTeam && int64_t(a.width) * kPage > int64_t(team) * kChoose * kHeld &&
+         units * team * 2 <= sm_count(c->device) * 2)
+    team *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(uint32_t(units) * team);
+  cfg.blockDim = dim3(kChoose);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = team;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = team > 1 ? 1 : 0;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_choose_kernel, p, team);
   if (e == cudaSuccess) {
-#define CALL(D) kv4_move_kernel<D><<<grid_of(units * int64_t(cdiv(a.keep, kPage)), c->device), kThreads, 0, s>>>(p)
+    cfg.gridDim = dim3(grid_of(units * int64_t(cdiv(a.keep, kPage)), c->device));
+    cfg.blockDim = dim3(kMove);
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+#define CALL(D) e = cudaLaunchKernelEx(&cfg, kv4_move_kernel<D>, p)
     WCOMP_KV_DIM(c->dim, CALL);
 #undef CALL
-    e = cudaGetLastError();
     count_launches(2);
   }
   if (!a.d_kept) cudaFreeAsync(p.kept, s);

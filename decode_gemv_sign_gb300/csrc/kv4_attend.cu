@@ -21,9 +21,10 @@
 // going over to another scales exactly, by powers of two.
 //
 // Each warp takes an equal run of the call's (sequence, tile of rows, head, page)
-// units through a ring of its own; parts of a softmax that fall on several warps are
-// joined in warp order by a second kernel.  Lengths are on the device, so every
-// block sums up the work of all sequences first.
+// units through a ring of its own.  Where a tile's pages fall on several warps, a
+// block joins its warps' parts in shared memory and a second kernel those of
+// blocks, always in the same order.  Lengths are on the device, so every block sums
+// up the work of all sequences first.
 #include <algorithm>
 #include <cmath>
 
@@ -156,6 +157,15 @@ struct Walk {
     do q = load_seq<R, TILES>(a, ++b);
     while (q.tiles == 0);
   }
+};
+
+// The units of warp w of W: first(w) .. first(w + 1).  With fewer units than warps
+// every block has some.
+struct Runs {
+  uint64_t total;
+  uint32_t W;
+  __device__ __forceinline__ uint64_t first(uint32_t w) const { return total * w / W; }
+  __device__ __forceinline__ uint32_t of(uint64_t unit) const { return uint32_t(((unit + 1) * W - 1) / total); }
 };
 
 template <int D, bool VALUES>
@@ -572,6 +582,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
   using W = Walk<kThreads, R, true>;
   __shared__ uint64_t s_before[kThreads + 1], s_warp[kWarps];
   __shared__ W s_at[kWarps][2];
+  __shared__ int s_inner[kWarps];  // whether the warp's run begins and ends within one tile
+  __shared__ float2 s_ml[kWarps][R];
   extern __shared__ __align__(128) uint8_t smem_raw[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t smem = smem_u32(smem_raw) + (-smem_u32(smem_raw) & 127u);
@@ -580,17 +592,16 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
   Ring<Src, kDepth> ring(smem + uint32_t(warp) * kDepth * Src::kStage,
                          smem + kWarps * kDepth * Src::kStage + uint32_t(warp) * kDepth * 8, a.s.err, lane);
   sum_units<kThreads, R, true>(a, s_before, s_warp, blockIdx.x == 0 ? a.prefix : nullptr);
-  const uint64_t total = s_before[kThreads];
-  const uint64_t per = (total + a.warps - 1) / a.warps;
-  const uint32_t me = blockIdx.x + uint32_t(warp) * gridDim.x;  // neighbours on different SMs: few units spread
-  uint64_t u = per * me;
-  const uint64_t end = min(total, u + per);
-  if (u >= end) return;
+  const Runs runs{s_before[kThreads], a.warps};
+  const uint32_t me = blockIdx.x * kWarps + uint32_t(warp);
+  uint64_t u = runs.first(me);
+  const uint64_t end = runs.first(me + 1);
   W& at = s_at[warp][0];
-  if (lane == 0) {
+  if (lane == 0 && u < end) {
     at.find(a, s_before, u);
     s_at[warp][1] = at;
   }
+  if (lane == 0) s_inner[warp] = 0;
   __syncwarp();
   Pages<D, Ring<Src, kDepth>, W> pages(s_at[warp][1], end - u);
 #pragma unroll 1
@@ -603,7 +614,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
     const bool first = at.page == 0;
     int page = at.q.page0 + at.page;
     const int stop = int(min(int64_t(at.q.page0 + at.q.pages), int64_t(page) + int64_t(end - u)));
-    const bool whole = first && stop == at.q.page0 + at.q.pages;
+    const bool last = stop == at.q.page0 + at.q.pages, whole = first && last, inner = !first && !last;
     tile.load(a, at.q, at.tile, int(at.head), lane);
     sums.clear();
     u += uint64_t(stop - page);
@@ -621,8 +632,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
       ring.next();
     }
     const float back = power_of_two(-sums.k);
-    float* part = a.part + (uint64_t(2 * me + first) * R) * D;
-    float2* ml = a.part_ml + uint64_t(2 * me + first) * R;
+    // an inner part goes to the warp's own stages, which nothing is copied to any more
+    float* part = inner ? reinterpret_cast<float*>(smem_raw + (smem - smem_u32(smem_raw)) + warp * kDepth * Src::kStage)
+                        : a.part + (uint64_t(2 * me + first) * R) * D;
+    float2* ml = inner ? s_ml[warp] : a.part_ml + uint64_t(2 * me + first) * R;
+    if (inner && lane == 0) s_inner[warp] = 1;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -632,7 +646,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
         for (int d = 4; d <= 16; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
         int lo, hi;
         const int64_t row = Tile<D, NT>::row(a, at.q, at.tile, int(at.head), n, e, lane, lo, hi);
-        if (row < 0) continue;
+        if (row < 0) {
+          if (inner && r == 0) ml[8 * n + 2 * q + e] = make_float2(-INFINITY, 0.f);
+          continue;
+        }
         if (r == 0) {
           if (whole) store_lse(a, row, sums.m[n][e], l);
           else ml[8 * n + 2 * q + e] = make_float2(sums.m[n][e], l);
@@ -659,75 +676,116 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
     }
     __syncwarp();
   }
+  // Join the inner parts of neighbouring warps, which are one tile's: each of them takes
+  // some rows; the result is the first one's.
+  __syncthreads();
+  if (!s_inner[warp]) return;
+  auto same = [&](int w) {
+    return s_inner[w] && s_at[w][0].b == at.b && s_at[w][0].tile == at.tile && s_at[w][0].head == at.head;
+  };
+  int w0 = warp, w1 = warp + 1;
+  // warps without a unit lie between the others where units are few
+  for (int w = warp - 1; w >= 0 && (same(w) || runs.first(blockIdx.x * kWarps + w) == runs.first(blockIdx.x * kWarps + w + 1)); --w)
+    if (s_inner[w]) w0 = w;
+  for (int w = warp + 1; w < kWarps && (same(w) || runs.first(blockIdx.x * kWarps + w) == runs.first(blockIdx.x * kWarps + w + 1)); ++w)
+    if (s_inner[w]) w1 = w + 1;
+  int parts = 0, mine = 0;
+  for (int w = w0; w < w1; ++w) {
+    if (w < warp) mine += s_inner[w];
+    parts += s_inner[w];
+  }
+  const uint64_t out = uint64_t(2 * (blockIdx.x * kWarps + w0)) * R;
+  constexpr int V = D / 32;
+  for (int row = mine; row < R; row += parts) {
+    float m = -INFINITY, l = 0.f, o[V] = {};
+    for (int w = w0; w < w1; ++w)
+      if (s_inner[w]) m = fmaxf(m, s_ml[w][row].x);
+    const float from = m == -INFINITY ? 0.f : m;
+    for (int w = w0; w < w1; ++w) {
+      if (!s_inner[w]) continue;
+      const float2 ml = s_ml[w][row];
+      const float f = exp2_approx(ml.x - from);
+      l += f * ml.y;
+      const float* x = reinterpret_cast<const float*>(smem_raw + (smem - smem_u32(smem_raw)) + w * kDepth * Src::kStage) +
+                       row * D + lane;
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] += f * x[32 * k];
+    }
+    if (lane == 0) a.part_ml[out + row] = make_float2(m, l);
+#pragma unroll
+    for (int k = 0; k < V; ++k) a.part[(out + row) * D + lane + 32 * k] = o[k];
+  }
 }
 
-// Join the parts of a (row, query head): one block.
-constexpr int kJoinWarps = 8;
+// Join the blocks' parts of a tile and head: one block.  They are those of the first
+// and the last warp that have pages of it and, for every block between or around
+// them, of its first warp with none but the tile's.
+constexpr int kJoin = 256;
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * kJoinWarps) kv4_join_kernel(const __grid_constant__ AttendArgs a) {
-  constexpr int R = 8 * NT, V = D / 32;
-  __shared__ float s_o[kJoinWarps][D], s_l[kJoinWarps], s_m[kJoinWarps];
+__global__ void __launch_bounds__(kJoin) kv4_join_kernel(const __grid_constant__ AttendArgs a, int64_t tiles) {
+  constexpr int R = 8 * NT, K = Shape<D, NT>::kWarps, kItems = R * D / 4;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint64_t per = (a.prefix[a.s.B] + a.warps - 1) / a.warps;
-  const int64_t units = a.T * a.q_heads;
-  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int64_t i = unit / a.q_heads;
-    const int hq = int(unit % a.q_heads), h = hq / a.share;
-    const int b = kv_sequence(a.s, i);
-    if (b < 0) continue;
-    const Seq s = load_seq<R, true>(a, b);
-    const int64_t x = (i - s.first) * a.share + (hq - h * a.share);
-    if (x < 0 || x >= int64_t(s.rows) * a.share) continue;  // starts out of order
-    const uint64_t f0 = a.prefix[b] + (uint64_t(x / R) * a.s.heads + h) * uint32_t(s.pages), f1 = f0 + uint32_t(s.pages);
-    const uint64_t w0 = f0 / per, w1 = (f1 - 1) / per;
-    if (w0 == w1 || w1 >= a.warps) continue;
-    const int row = int(x % R);
-    auto slot = [&](uint64_t w) { return (2 * w + (w * per <= f0 ? 1 : 0)) * R + row; };
-    float m = -INFINITY;
-    for (uint64_t w = w0 + threadIdx.x; w <= w1; w += 32 * kJoinWarps) m = fmaxf(m, a.part_ml[slot(w)].x);
-#pragma unroll
-    for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    __syncthreads();
-    if (lane == 0) s_m[warp] = m;
-    __syncthreads();
-    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_m[w]);
-    const float from = m == -INFINITY ? 0.f : m;
-    float o[V] = {}, l = 0.f;
-#pragma unroll 4
-    for (uint64_t w = w0 + warp; w <= w1; w += kJoinWarps) {
-      const float2 ml = a.part_ml[slot(w)];
-      const float f = exp2f(ml.x - from);
-      const float* part = a.part + slot(w) * D + V * lane;
-      float y[V];
-      if constexpr (V == 2) {
-        const float2 t = *reinterpret_cast<const float2*>(part);
-        y[0] = t.x; y[1] = t.y;
-      } else {
-#pragma unroll
-        for (int k = 0; k < V; k += 4) {
-          const float4 t = *reinterpret_cast<const float4*>(part + k);
-          y[k] = t.x; y[k + 1] = t.y; y[k + 2] = t.z; y[k + 3] = t.w;
-        }
+  const Runs runs{a.prefix[a.s.B], a.warps};
+  for (int64_t unit = blockIdx.x; unit < tiles * a.s.heads; unit += gridDim.x) {
+    const uint32_t head = uint32_t(unit % a.s.heads);
+    const int64_t place = unit / a.s.heads;
+    // sequence b has the places from its first row's pairs / R + b on
+    int b = 0, tile;
+    if (a.s.starts) {
+      auto first = [&](int i) { return int64_t(max(a.s.starts[i], 0)) * a.share / R + i; };
+      int lo = 0, hi = a.s.B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first(mid) <= place) lo = mid;
+        else hi = mid;
       }
-      l += f * ml.y;
-#pragma unroll
-      for (int k = 0; k < V; ++k) o[k] += f * y[k];
+      b = lo;
+      tile = int(place - first(b));
+    } else {
+      const int per = (a.share + R - 1) / R;
+      b = int(place / per);
+      tile = int(place % per);
     }
-#pragma unroll
-    for (int k = 0; k < V; ++k) s_o[warp][V * lane + k] = o[k];
-    if (lane == 0) s_l[warp] = l;
-    __syncthreads();
-    l = 0.f;
-    for (int w = 0; w < kJoinWarps; ++w) l += s_l[w];
-    for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps) {
-      float y = 0.f;
-      for (int w = 0; w < kJoinWarps; ++w) y += s_o[w][d];
-      a.out[unit * D + d] = uint16_t(bf16x2_bits(l == 0.f ? 0.f : y / l, 0.f));
+    const Seq s = load_seq<R, true>(a, b);
+    if (tile < 0 || tile >= s.tiles) continue;
+    const uint64_t f0 = a.prefix[b] + (uint64_t(tile) * a.s.heads + head) * uint32_t(s.pages), f1 = f0 + uint32_t(s.pages);
+    const uint32_t w0 = runs.of(f0), w1 = runs.of(f1 - 1);
+    if (w0 == w1 || w1 >= a.warps) continue;
+    const uint32_t c0 = w0 / K, blocks = w1 / K - c0 + 1;
+    // part p's place, or -1
+    auto place_of = [&](uint32_t p) -> int64_t {
+      if (p == 0) return int64_t(2 * w0 + 1) * R;
+      if (p == 1) return int64_t(2 * w1) * R;
+      const uint32_t lo = max(w0 + 1, (c0 + p - 2) * K), w = runs.of(runs.first(lo));
+      return w < min(w1, (c0 + p - 1) * K) ? int64_t(2 * w) * R : -1;
+    };
+    for (int item = threadIdx.x; item < kItems; item += kJoin) {
+      const int row = 4 * item / D, col = 4 * item % D;
+      int lo, hi;
+      const int64_t to = Tile<D, NT>::row(a, s, tile, int(head), row / 8, row % 2, row % 8 / 2, lo, hi);
+      if (to < 0) continue;
+      float m = -INFINITY, l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (uint32_t p = 0; p < blocks + 2; ++p) {
+        const int64_t at = place_of(p);
+        if (at < 0) continue;
+        const float2 ml = a.part_ml[at + row];
+        const float4 x = *reinterpret_cast<const float4*>(a.part + (at + row) * D + col);
+        const float next = fmaxf(m, ml.x), from = next == -INFINITY ? 0.f : next;
+        const float down = exp2f(m - from), f = exp2f(ml.x - from);
+        m = next;
+        l = l * down + ml.y * f;
+        o.x = o.x * down + x.x * f;
+        o.y = o.y * down + x.y * f;
+        o.z = o.z * down + x.z * f;
+        o.w = o.w * down + x.w * f;
+      }
+      const float f = l == 0.f ? 0.f : 1.f / l;
+      *reinterpret_cast<uint2*>(a.out + to * D + col) = make_uint2(bf16x2_bits(o.x * f, o.y * f), bf16x2_bits(o.z * f, o.w * f));
+      if (col == 0) store_lse(a, to, m, l);
     }
-    if (threadIdx.x == 0) store_lse(a, unit, m, l);
-    __syncthreads();
   }
 }
 
@@ -749,17 +807,16 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(con
   Ring<Src, kDepth> ring(smem + uint32_t(warp) * kDepth * Src::kStage,
                          smem + kWarps * kDepth * Src::kStage + uint32_t(warp) * kDepth * 8, a.s.err, lane);
   sum_units<kThreads, R, false>(a, s_before, s_warp, nullptr);
-  const uint64_t total = s_before[kThreads];
-  const uint64_t per = (total + a.warps - 1) / a.warps;
-  uint64_t u = per * (blockIdx.x + uint32_t(warp) * gridDim.x);
-  const uint64_t end = min(total, u + per);
+  const Runs runs{s_before[kThreads], a.warps};
+  uint64_t u = runs.first(blockIdx.x * kWarps + uint32_t(warp));
+  const uint64_t end = runs.first(blockIdx.x * kWarps + uint32_t(warp) + 1);
   W& at = s_at[warp][0];
   if (lane == 0 && u < end) {
     at.find(a, s_before, u);
     s_at[warp][1] = at;
   }
   __syncwarp();
-  Pages<D, Ring<Src, kDepth>, W> pages(s_at[warp][1], u < end ? end - u : 0);
+  Pages<D, Ring<Src, kDepth>, W> pages(s_at[warp][1], end - u);
 #pragma unroll 1
   for (int i = 0; i < kDepth; ++i) pages.issue(a, ring, uint32_t(i), lane);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the log-sum-exps are there
@@ -823,9 +880,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(con
   }
 }
 
-template <class K>
-cudaError_t launch(K kernel, uint32_t grid, int threads, uint32_t smem, bool dependent, const AttendArgs& a,
-                   cudaStream_t s) {
+template <class K, class... ARGS>
+cudaError_t launch(K kernel, uint32_t grid, int threads, uint32_t smem, bool dependent, cudaStream_t s,
+                   const ARGS&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(uint32_t(threads));
@@ -837,7 +894,7 @@ cudaError_t launch(K kernel, uint32_t grid, int threads, uint32_t smem, bool dep
   cfg.attrs = &attr;
   cfg.numAttrs = dependent ? 1 : 0;
   count_launches(1);
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <int D, int NT>
@@ -861,11 +918,13 @@ int attend(AttendArgs& a, int dev, cudaStream_t s) {
   a.lse2 = reinterpret_cast<float*>(ws + b_prefix);
   a.part_ml = reinterpret_cast<float2*>(ws + b_prefix + b_lse);
   a.part = reinterpret_cast<float*>(ws + b_prefix + b_lse + b_ml);
-  e = launch(kv4_attend_kernel<D, NT>, sms, kThreads, smem, false, a, s);
-  const uint32_t joins = uint32_t(std::min<int64_t>(a.T * a.q_heads, int64_t(sms) * 32));
-  if (e == cudaSuccess)
-    e = launch(kv4_join_kernel<D, NT>, joins, 32 * kJoinWarps, 0, true, a, s);
-  if (e == cudaSuccess && a.mass) e = launch(kv4_mass_kernel<D, NT>, sms, kThreads, smem, true, a, s);
+  e = launch(kv4_attend_kernel<D, NT>, sms, kThreads, smem, false, s, a);
+  // places for the tiles of all sequences (kv4_join_kernel)
+  const int64_t tiles = a.s.starts ? a.T * a.share / (8 * NT) + a.s.B + 1
+                                   : int64_t(a.s.B) * int64_t(cdiv(a.share, 8 * NT));
+  const uint32_t joins = uint32_t(std::min<int64_t>(tiles * a.s.heads, int64_t(sms) * 64));
+  if (e == cudaSuccess) e = launch(kv4_join_kernel<D, NT>, joins, kJoin, 0, true, s, a, tiles);
+  if (e == cudaSuccess && a.mass) e = launch(kv4_mass_kernel<D, NT>, sms, kThreads, smem, true, s, a);
   cudaFreeAsync(ws, s);
   return map_cuda(e);
 }

@@ -513,7 +513,8 @@ WCOMP_API int wcomp_moe(const wcomp_moe_args* args, void* stream);
  *     from the library's stream-ordered pool, and is released with wcomp_kv4_free.
  *     Calls that write to it are ordered by the caller against others on it, as
  *     for any buffer.
- *   - Limits: pages * heads below 2^31, B, rows and width * 64 below 2^31; beyond
+ *   - Limits: pages * heads and the rows of a call (times the query heads) below
+ *     2^31, width * 64 at most 2^30, B * heads of an eviction below 2^28; beyond
  *     them WCOMP_EUNSUPPORTED.
  * ------------------------------------------------------------------------ */
 typedef struct wcomp_kv4 wcomp_kv4;
