@@ -3,6 +3,7 @@
 #include <new>
 
 #include "kv4.cuh"
+#include "q4_rule.cuh"
 
 namespace wc {
 namespace {
@@ -28,29 +29,30 @@ struct Items {
   static constexpr int kRound = kLanes * kSteps;
 };
 
-// Quantise 8 columns; four lanes share the group's largest magnitude.  `w` gets the
-// codes, 4 bits each; returns the scale's bits.
+// Quantise 8 columns, whose group's other columns the three neighbouring lanes have.
+// `w` gets the codes, 4 bits each; returns the scale's bits.
 __device__ __forceinline__ uint32_t quantise8(const uint32_t (&v)[4], uint32_t& w) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = max(m, max(v[i] & 0x7FFFu, (v[i] >> 16) & 0x7FFFu));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  w = 0x88888888u;
-  if (m > 0x7F7Fu) return 0x7FC0u;  // an infinity or a NaN
-  const uint32_t sb = bf16_bits(bf16_value(m) / 7.f);
-  if (sb == 0u) return 0u;
-  const float s = bf16_value(sb);
-  w = 0;
+  for (int i = 0; i < 4; ++i) m = abs_max2(m, v[i]);
+  m = abs_max2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = abs_max2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  m = abs_max2(m, m >> 16) & 0x7FFFu;
+  const uint32_t bits = scale_of(m);
+  const float s = bf16_value(bits);
+  if (s >= 0x1p-100f) {
+    const float rs = reciprocal(s);
+    w = 0u - kBase * 0x11111111u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float x = bf16_value((v[i / 2] >> (16 * (i % 2))) & 0xFFFFu);
-    // a quotient of 8-bit significands is a midpoint or well off one: its fp32
-    // rounding does not move it over an edge
-    const int c = max(-7, min(7, __float2int_rn(x / s))) + 8;
-    w |= uint32_t(c) << (4 * i);
+    for (int i = 0; i < 4; ++i)
+      w += code_fast(bf16_lo(v[i]), rs) * (1u << (8 * i)) + code_fast(bf16_hi(v[i]), rs) * (16u << (8 * i));
+  } else {
+    w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w |= code_slow(bf16_lo(v[i]), s) << (8 * i) | code_slow(bf16_hi(v[i]), s) << (8 * i + 4);
   }
-  return sb;
+  return bits;
 }
 
 // The words of a value row hold four columns of two groups each: lanes u and u ^ 4
@@ -199,8 +201,8 @@ struct EvictArgs {
   int width_out, keep, recent;
 };
 
-constexpr int kChoose = 1024, kChooseWarps = kChoose / 32;
-constexpr int kHeld = 16;   // keys that a thread holds in registers: 16384 tokens a block
+constexpr int kChoose = 512, kChooseWarps = kChoose / 32;
+constexpr int kHeld = 16;   // keys that a thread holds in registers: 8192 tokens a block
 constexpr int kMaxTeam = 8; // blocks that share a sequence and head
 
 // A mass as a number that orders as it does: NaN lowest, -0 and 0 alike.
@@ -240,7 +242,7 @@ struct Choose {
   uint32_t below[2][kChooseWarps];
 };
 
-__global__ void __launch_bounds__(kChoose) kv4_choose_kernel(EvictArgs a, uint32_t team) {
+__global__ void __launch_bounds__(kChoose, 2) kv4_choose_kernel(EvictArgs a, uint32_t team) {
   __shared__ Choose sh;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -273,7 +275,8 @@ __global__ void __launch_bounds__(kChoose) kv4_choose_kernel(EvictArgs a, uint32
   // keys of the tokens to choose from, others 0: no candidate below is 0
   auto candidates = [&](auto f) {
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) f(i0 + 32 * k + int(lane) < min(i1, n0) ? held[k] : 0u);
+    for (int k = 0; k < kHeld; ++k)
+      if (k < steps) f(i0 + 32 * k + int(lane) < min(i1, n0) ? held[k] : 0u);
     for (int k = kHeld; k < steps; ++k) f(i0 + 32 * k + int(lane) < min(i1, n0) ? key_at(k) : 0u);
   };
   // the sum of three counts over all tokens
@@ -286,7 +289,8 @@ __global__ void __launch_bounds__(kChoose) kv4_choose_kernel(EvictArgs a, uint32
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 3; ++j) c[j] = __reduce_add_sync(0xffffffffu, sh.sums[parity][lane][j]);
+    for (int j = 0; j < 3; ++j)
+      c[j] = __reduce_add_sync(0xffffffffu, lane < kChooseWarps ? sh.sums[parity][lane][j] : 0u);
     if (team > 1) {
       if (tid < 3) sh.team[parity][tid] = c[tid];
       team_sync();
@@ -296,17 +300,19 @@ __global__ void __launch_bounds__(kChoose) kv4_choose_kernel(EvictArgs a, uint32
     }
     parity ^= 1;
   };
-  // the largest key that at least `want` tokens reach
-  uint32_t key = 0;
+  // the largest key that at least `want` tokens reach, or one that just `want` do
+  uint32_t key = 0, reach = 0;
   if (want) {
-    for (int shift = 30; shift >= 0; shift -= 2) {
+    for (int shift = 30; shift >= 0 && reach != want; shift -= 2) {
       uint32_t c[3] = {0, 0, 0};
       candidates([&](uint32_t k) {
 #pragma unroll
         for (uint32_t j = 0; j < 3; ++j) c[j] += k >= (key | (j + 1) << shift);
       });
       sum3(c);
-      key |= (c[2] >= want ? 3u : c[1] >= want ? 2u : c[0] >= want ? 1u : 0u) << shift;
+      const uint32_t digit = c[2] >= want ? 3u : c[1] >= want ? 2u : c[0] >= want ? 1u : 0u;
+      key |= digit << shift;
+      if (digit) reach = c[digit - 1];
     }
   }
   // above it all are taken; of those that equal it, the first ones
@@ -318,7 +324,8 @@ __global__ void __launch_bounds__(kChoose) kv4_choose_kernel(EvictArgs a, uint32
     equal += __popc(__ballot_sync(0xffffffffu, in && k == key));
   };
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k) count(i0 + 32 * k + int(lane), held[k]);
+  for (int k = 0; k < kHeld; ++k)
+    if (k < steps) count(i0 + 32 * k + int(lane), held[k]);
   for (int k = kHeld; k < steps; ++k) count(i0 + 32 * k + int(lane), key_at(k));
   // sums over the warps before this one, and the number taken above the key
   uint32_t before[2] = {0, 0}, taken;
@@ -332,8 +339,9 @@ __global__ void __launch_bounds__(kChoose) kv4_choose_kernel(EvictArgs a, uint32
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      own[j] = __reduce_add_sync(0xffffffffu, sh.below[j][lane]);
-      before[j] = __reduce_add_sync(0xffffffffu, lane < warp ? sh.below[j][lane] : 0u);
+      const uint32_t v = lane < kChooseWarps ? sh.below[j][lane] : 0u;
+      own[j] = __reduce_add_sync(0xffffffffu, v);
+      before[j] = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0u);
     }
     if (team > 1) {
       if (tid < 2) sh.team[parity][tid] = own[tid];
@@ -366,7 +374,8 @@ __global__ void __launch_bounds__(kChoose) kv4_choose_kernel(EvictArgs a, uint32
     place += __popc(takes);
   };
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k) emit(i0 + 32 * k + int(lane), held[k]);
+  for (int k = 0; k < kHeld; ++k)
+    if (k < steps) emit(i0 + 32 * k + int(lane), held[k]);
   for (int k = kHeld; k < steps; ++k) emit(i0 + 32 * k + int(lane), key_at(k));
   for (int i = m + int(rank * kChoose + tid); i < a.keep; i += int(team * kChoose)) kept[i] = -1;
   for (int i = m + int(rank * kChoose + tid); i < a.width_out * kPage; i += int(team * kChoose)) mass_out[i] = 0.f;
@@ -567,7 +576,7 @@ extern "C" int wcomp_kv4_evict(wcomp_kv4* c, const wcomp_kv4_evict_args* args, v
   // blocks share a long sequence while that leaves each something and the GPU has room
   uint32_t team = 1;
   while (team < kMaxTeam && int64_t(a.width) * kPage > int64_t(team) * kChoose * kHeld &&
-         units * team * 2 <= sm_count(c->device) * 2)
+         units * team * 2 <= sm_count(c->device) * 4)
     team *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(uint32_t(units) * team);

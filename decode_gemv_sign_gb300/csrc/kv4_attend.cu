@@ -582,6 +582,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
   using W = Walk<kThreads, R, true>;
   __shared__ uint64_t s_before[kThreads + 1], s_warp[kWarps];
   __shared__ W s_at[kWarps][2];
+  __shared__ uint64_t s_first[kWarps + 1];
   __shared__ int s_inner[kWarps];  // whether the warp's run begins and ends within one tile
   __shared__ float2 s_ml[kWarps][R];
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -594,8 +595,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
   sum_units<kThreads, R, true>(a, s_before, s_warp, blockIdx.x == 0 ? a.prefix : nullptr);
   const Runs runs{s_before[kThreads], a.warps};
   const uint32_t me = blockIdx.x * kWarps + uint32_t(warp);
-  uint64_t u = runs.first(me);
-  const uint64_t end = runs.first(me + 1);
+  if (threadIdx.x <= kWarps) s_first[threadIdx.x] = runs.first(blockIdx.x * kWarps + threadIdx.x);
+  __syncthreads();
+  uint64_t u = s_first[warp];
+  const uint64_t end = s_first[warp + 1];
   W& at = s_at[warp][0];
   if (lane == 0 && u < end) {
     at.find(a, s_before, u);
@@ -685,9 +688,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
   };
   int w0 = warp, w1 = warp + 1;
   // warps without a unit lie between the others where units are few
-  for (int w = warp - 1; w >= 0 && (same(w) || runs.first(blockIdx.x * kWarps + w) == runs.first(blockIdx.x * kWarps + w + 1)); --w)
+  for (int w = warp - 1; w >= 0 && (same(w) || s_first[w] == s_first[w + 1]); --w)
     if (s_inner[w]) w0 = w;
-  for (int w = warp + 1; w < kWarps && (same(w) || runs.first(blockIdx.x * kWarps + w) == runs.first(blockIdx.x * kWarps + w + 1)); ++w)
+  for (int w = warp + 1; w < kWarps && (same(w) || s_first[w] == s_first[w + 1]); ++w)
     if (s_inner[w]) w1 = w + 1;
   int parts = 0, mine = 0;
   for (int w = w0; w < w1; ++w) {
@@ -726,6 +729,7 @@ __global__ void __launch_bounds__(kJoin) kv4_join_kernel(const __grid_constant__
   constexpr int R = 8 * NT, K = Shape<D, NT>::kWarps, kItems = R * D / 4;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ int s_place[kJoin];  // of part p, or -1
   const Runs runs{a.prefix[a.s.B], a.warps};
   for (int64_t unit = blockIdx.x; unit < tiles * a.s.heads; unit += gridDim.x) {
     const uint32_t head = uint32_t(unit % a.s.heads);
@@ -753,13 +757,17 @@ __global__ void __launch_bounds__(kJoin) kv4_join_kernel(const __grid_constant__
     const uint32_t w0 = runs.of(f0), w1 = runs.of(f1 - 1);
     if (w0 == w1 || w1 >= a.warps) continue;
     const uint32_t c0 = w0 / K, blocks = w1 / K - c0 + 1;
-    // part p's place, or -1
-    auto place_of = [&](uint32_t p) -> int64_t {
-      if (p == 0) return int64_t(2 * w0 + 1) * R;
-      if (p == 1) return int64_t(2 * w1) * R;
-      const uint32_t lo = max(w0 + 1, (c0 + p - 2) * K), w = runs.of(runs.first(lo));
-      return w < min(w1, (c0 + p - 1) * K) ? int64_t(2 * w) * R : -1;
-    };
+    __syncthreads();
+    if (threadIdx.x < blocks + 2) {
+      const uint32_t p = threadIdx.x;
+      int at = int(p == 0 ? (2 * w0 + 1) * R : 2 * w1 * R);
+      if (p > 1) {
+        const uint32_t lo = max(w0 + 1, (c0 + p - 2) * K), w = runs.of(runs.first(lo));
+        at = w < min(w1, (c0 + p - 1) * K) ? int(2 * w * R) : -1;
+      }
+      s_place[p] = at;
+    }
+    __syncthreads();
     for (int item = threadIdx.x; item < kItems; item += kJoin) {
       const int row = 4 * item / D, col = 4 * item % D;
       int lo, hi;
@@ -769,10 +777,10 @@ __global__ void __launch_bounds__(kJoin) kv4_join_kernel(const __grid_constant__
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
       for (uint32_t p = 0; p < blocks + 2; ++p) {
-        const int64_t at = place_of(p);
+        const int at = s_place[p];
         if (at < 0) continue;
         const float2 ml = a.part_ml[at + row];
-        const float4 x = *reinterpret_cast<const float4*>(a.part + (at + row) * D + col);
+        const float4 x = *reinterpret_cast<const float4*>(a.part + int64_t(at + row) * D + col);
         const float next = fmaxf(m, ml.x), from = next == -INFINITY ? 0.f : next;
         const float down = exp2f(m - from), f = exp2f(ml.x - from);
         m = next;
@@ -900,7 +908,7 @@ cudaError_t launch(K kernel, uint32_t grid, int threads, uint32_t smem, bool dep
 template <int D, int NT>
 int attend(AttendArgs& a, int dev, cudaStream_t s) {
   constexpr int kThreads = Shape<D, NT>::kThreads;
-  const uint32_t sms = uint32_t(sm_count(dev));
+  const uint32_t sms = uint32_t(std::min(sm_count(dev), kJoin - 2));  // a part a block, and two
   constexpr uint32_t smem = Shape<D, NT>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(kv4_attend_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e == cudaSuccess && a.mass)

@@ -11,6 +11,7 @@
 #include <mutex>
 #include <new>
 
+#include "q4_rule.cuh"
 #include "tile.cuh"
 
 namespace wc {
@@ -65,43 +66,6 @@ __device__ __forceinline__ void each_quarter(const Blocks& b, F f) {
 }
 __device__ __forceinline__ uint8_t* codes_at(uint8_t* block, const At& a, int lane) {
   return block + (2 * a.s + a.m) * 1024 + lane * 16;
-}
-
-// Larger magnitudes (NaN if there is one), with a sign that means nothing.
-__device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-// The BF16 scale of a group whose largest magnitude (BF16 bits, NaN if it
-// holds one) is m: the nearest BF16 to m / 7.  m has 8 significant bits, so
-// m / 7 is never nearer than 2^-12 of itself to a midpoint of two BF16 values,
-// and the rounding of 1 / 7 and of the product cannot cross it.  A group with
-// an infinity or a NaN gets the scale NaN.
-__device__ __forceinline__ uint32_t scale_of(uint32_t m) {
-  uint16_t s;
-  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(s) : "f"(__fmul_rn(__uint_as_float(m << 16), 1.f / 7.f)));
-  return m >= 0x7F80u ? 0x7FC0u : s;
-}
-
-// Code of one weight.  w / s has a quotient of 8-bit significands: it is
-// either exactly halfway between integers or at least 2^-10 away from it, so
-// w * (1 / s) (2^-22 relative error), rounded to a multiple of 2^-12 by the
-// first constant, is on the right side of every halfway point, and exactly on
-// it where w / s is; the second constant then rounds half to even.  Scales
-// below 2^-100 (reciprocals near overflow, quotients above 7) divide and clamp.
-constexpr float kSnap = 3072.f;        // 1.5 * 2^11: ulp 2^-12
-// Codes come as kBase + code, so that a word of eight is a sum of them times
-// powers of 16, less what the bases add up to: one integer multiply-add a code.
-constexpr float kRound = 12582920.f;   // 1.5 * 2^23 + 8: ulp 1, and the code's offset of 8
-constexpr uint32_t kBase = 0x4B400000u;  // the bits of 1.5 * 2^23
-__device__ __forceinline__ uint32_t code_fast(float w, float rs) {
-  return __float_as_uint(__fadd_rn(__fadd_rn(__fmaf_rn(w, rs, kSnap), -kSnap), kRound));
-}
-__device__ __forceinline__ uint32_t code_slow(float w, float s) {
-  if (!(s > 0.f)) return 8u;  // scale 0 or NaN
-  return uint32_t(int(fminf(fmaxf(rintf(__fdiv_rn(w, s)), -7.f), 7.f)) + 8);
 }
 
 // 8 columns of row r from column c as BF16 pairs; zeros outside the matrix.
@@ -160,12 +124,6 @@ __device__ __forceinline__ void store_quarter(uint8_t* block, const At& a, int l
       if (int(t) == j) s2 = sc[0][j] | (sc[1][j] << 16);
     *reinterpret_cast<uint32_t*>(block + q4_scale_at(NG, a.s, t, a.m, g)) = s2;
   }
-}
-
-__device__ __forceinline__ float reciprocal(float s) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-  return r;
 }
 
 // The codes of a quarter block with a scale that code_fast does not take, from
