@@ -19,15 +19,32 @@ __device__ __forceinline__ uint32_t bf16_bits(float v) {
 
 // A row of keys or values is handled by D / 8 neighbouring lanes, lane u the columns
 // 8 u .. 8 u + 7; four of them share a group.  A warp takes one row of the call,
-// whose place it looks up once, and kRound items of it at a time: the keys and
-// values of a head, one after the other.
+// whose place it looks up once, and kRound heads of it: kLanes side by side, kSteps
+// one after the other, the loads of their keys and values in flight together.
 template <int D>
 struct Items {
   static constexpr int kPer = D / 8;
-  static constexpr int kLanes = 32 / kPer;    // items that a warp takes side by side
-  static constexpr int kSteps = 4;            // and one after the other, their loads in flight together
+  static constexpr int kLanes = 32 / kPer;
+  static constexpr int kSteps = 4;
   static constexpr int kRound = kLanes * kSteps;
 };
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 
 // Quantise 8 columns, whose group's other columns the three neighbouring lanes have.
 // `w` gets the codes, 4 bits each; returns the scale's bits.
@@ -41,11 +58,15 @@ __device__ __forceinline__ uint32_t quantise8(const uint32_t (&v)[4], uint32_t& 
   const uint32_t bits = scale_of(m);
   const float s = bf16_value(bits);
   if (s >= 0x1p-100f) {
+    // code_fast for two columns at a time
     const float rs = reciprocal(s);
+    const uint64_t rs2 = pair(rs, rs), snap = pair(kSnap, kSnap), back = pair(-kSnap, -kSnap), round = pair(kRound, kRound);
     w = 0u - kBase * 0x11111111u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w += code_fast(bf16_lo(v[i]), rs) * (1u << (8 * i)) + code_fast(bf16_hi(v[i]), rs) * (16u << (8 * i));
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t c = add2(add2(fma2(pair(bf16_lo(v[i]), bf16_hi(v[i])), rs2, snap), back), round);
+      w += uint32_t(c) * (1u << (8 * i)) + uint32_t(c >> 32) * (16u << (8 * i));
+    }
   } else {
     w = 0;
 #pragma unroll
@@ -94,93 +115,116 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(KvSeqs s, uint8_t* cache, Rows k, Rows v, int64_t T,
                                                               uint32_t rounds) {
   using I = Items<D>;
-  const int lane = threadIdx.x % 32;
-  const uint32_t u = uint32_t(lane) % I::kPer;
+  using L = Kv<D>;
+  const uint32_t lane = threadIdx.x % 32, u = lane % I::kPer;
+  const uint32_t key_byte = 4 * key_index<D>(u), value_byte = 4 * value_index<D>(u);
   const int64_t units = T * rounds;
   for (int64_t unit = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; unit < units;
        unit += int64_t(gridDim.x) * (kThreads / 32)) {
     const int64_t i = unit / rounds;
-    const uint32_t first = uint32_t(unit % rounds) * I::kRound + uint32_t(lane) / I::kPer;
+    const uint32_t h0 = uint32_t(unit % rounds) * I::kRound + lane / I::kPer;
     uint32_t t = 0;
     bool mine;
-    uint8_t* page = row_place(s, cache, uint64_t(s.heads) * Kv<D>::kBlock, i, t, mine);
+    uint8_t* page = row_place(s, cache, uint64_t(s.heads) * L::kBlock, i, t, mine);
     if (!page) continue;
-    uint32_t x[I::kSteps][4];
+    uint32_t x[2][I::kSteps][4];
 #pragma unroll
-    for (int j = 0; j < I::kSteps; ++j) {
-      const uint32_t item = first + j * I::kLanes, h = item / 2;
+    for (int part = 0; part < 2; ++part) {
+      const Rows& r = part ? v : k;
+      const uint16_t* p = r.p + i * r.row + h0 * r.head + 8 * u;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[j][e] = 0;
-      if (h >= s.heads) continue;
-      const Rows& r = item % 2 ? v : k;
-      const uint16_t* p = r.p + i * r.row + h * r.head + 8 * u;
-      if (r.vec) {
-        const uint4 y = *reinterpret_cast<const uint4*>(p);
-        x[j][0] = y.x; x[j][1] = y.y; x[j][2] = y.z; x[j][3] = y.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[j][e] = p[2 * e] | uint32_t(p[2 * e + 1]) << 16;
+      for (int j = 0; j < I::kSteps; ++j, p += I::kLanes * r.head) {
+        uint4 y = make_uint4(0, 0, 0, 0);
+        if (h0 + j * I::kLanes < s.heads) {
+          if (r.vec) {
+            y = ld_stream_v4(p);
+          } else {
+            y.x = p[0] | uint32_t(p[1]) << 16;
+            y.y = p[2] | uint32_t(p[3]) << 16;
+            y.z = p[4] | uint32_t(p[5]) << 16;
+            y.w = p[6] | uint32_t(p[7]) << 16;
+          }
+        }
+        x[part][j][0] = y.x; x[part][j][1] = y.y; x[part][j][2] = y.z; x[part][j][3] = y.w;
       }
     }
 #pragma unroll
-    for (int j = 0; j < I::kSteps; ++j) {
-      const uint32_t item = first + j * I::kLanes, h = item / 2, part = item % 2;
-      uint32_t w;
-      const uint32_t scale = quantise8(x[j], w);  // every lane takes part in the exchanges
-      const uint32_t by_value = value_word(w, u);
-      if (h >= s.heads) continue;
-      uint8_t* half = page + h * Kv<D>::kBlock + part * Kv<D>::kHalf;
-      const uint32_t index = part ? value_index<D>(u) : key_index<D>(u);
-      *reinterpret_cast<uint32_t*>(half + Kv<D>::at(t, 4 * index)) = part ? by_value : w;
-      if ((u & 3) == 0) *reinterpret_cast<uint16_t*>(half + Kv<D>::scale(t, u >> 2)) = uint16_t(scale);
+    for (int part = 0; part < 2; ++part) {
+      uint8_t* half = page + h0 * L::kBlock + part * L::kHalf;
+      uint8_t* codes = half + L::at(t, part ? value_byte : key_byte);
+      uint8_t* scales = half + L::scale(t, u >> 2);
+#pragma unroll
+      for (int j = 0; j < I::kSteps; ++j) {
+        uint32_t w;
+        const uint32_t scale = quantise8(x[part][j], w);  // every lane takes part in the exchanges
+        if (part) w = value_word(w, u);
+        if (h0 + j * I::kLanes >= s.heads) continue;
+        *reinterpret_cast<uint32_t*>(codes + j * I::kLanes * L::kBlock) = w;
+        if ((u & 3) == 0) *reinterpret_cast<uint16_t*>(scales + j * I::kLanes * L::kBlock) = uint16_t(scale);
+      }
     }
   }
+}
+
+// Eight codes times a scale, in pairs of BF16: a code under the exponent of 128 is 128
+// + c, less 136 exactly c - 8, and the product is rounded once.
+__device__ __forceinline__ uint4 values8(uint32_t w, uint32_t scale) {
+  const uint32_t s = prmt(scale, scale, 0x1010);
+  uint32_t x[4];  // columns i and i + 4
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(x[i]) : "r"(0x43084308u));
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x[i]) : "r"(s));
+  }
+  return make_uint4(prmt(x[0], x[1], 0x5410), prmt(x[2], x[3], 0x5410), prmt(x[0], x[1], 0x7632), prmt(x[2], x[3], 0x7632));
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(KvSeqs s, const uint8_t* cache, uint16_t* k, uint16_t* v,
                                                             int64_t T, uint32_t rounds, int vec) {
   using I = Items<D>;
-  const int lane = threadIdx.x % 32;
-  const uint32_t u = uint32_t(lane) % I::kPer;
+  using L = Kv<D>;
+  const uint32_t lane = threadIdx.x % 32, u = lane % I::kPer;
+  const uint32_t key_byte = 4 * key_index<D>(u), value_byte = 4 * value_index<D>(u);
   const int64_t units = T * rounds;
   for (int64_t unit = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; unit < units;
        unit += int64_t(gridDim.x) * (kThreads / 32)) {
     const int64_t i = unit / rounds;
-    const uint32_t first = uint32_t(unit % rounds) * I::kRound + uint32_t(lane) / I::kPer;
+    const uint32_t h0 = uint32_t(unit % rounds) * I::kRound + lane / I::kPer;
     uint32_t t = 0;
     bool mine;
-    const uint8_t* page = row_place(s, const_cast<uint8_t*>(cache), uint64_t(s.heads) * Kv<D>::kBlock, i, t, mine);
+    const uint8_t* page = row_place(s, const_cast<uint8_t*>(cache), uint64_t(s.heads) * L::kBlock, i, t, mine);
     if (!mine) continue;
-    uint32_t w[I::kSteps], scale[I::kSteps];
+    uint32_t w[2][I::kSteps], scale[2][I::kSteps];
 #pragma unroll
-    for (int j = 0; j < I::kSteps; ++j) {
-      const uint32_t item = first + j * I::kLanes, h = item / 2, part = item % 2;
-      w[j] = 0x88888888u;
-      scale[j] = 0;
-      if (!page || h >= s.heads) continue;
-      const uint8_t* half = page + h * Kv<D>::kBlock + part * Kv<D>::kHalf;
-      w[j] = *reinterpret_cast<const uint32_t*>(half + Kv<D>::at(t, 4 * (part ? value_index<D>(u) : key_index<D>(u))));
-      scale[j] = *reinterpret_cast<const uint16_t*>(half + Kv<D>::scale(t, u >> 2));
+    for (int part = 0; part < 2; ++part) {
+      const uint8_t* half = page + h0 * L::kBlock + part * L::kHalf;
+      const uint8_t* codes = half + L::at(t, part ? value_byte : key_byte);
+      const uint8_t* scales = half + L::scale(t, u >> 2);
+#pragma unroll
+      for (int j = 0; j < I::kSteps; ++j) {
+        w[part][j] = 0x88888888u;
+        scale[part][j] = 0;
+        if (!page || h0 + j * I::kLanes >= s.heads) continue;
+        w[part][j] = *reinterpret_cast<const uint32_t*>(codes + j * I::kLanes * L::kBlock);
+        scale[part][j] = *reinterpret_cast<const uint16_t*>(scales + j * I::kLanes * L::kBlock);
+      }
     }
 #pragma unroll
-    for (int j = 0; j < I::kSteps; ++j) {
-      const uint32_t item = first + j * I::kLanes, h = item / 2, part = item % 2;
-      const uint32_t by_value = value_word(w[j], u);
-      if (h >= s.heads) continue;
-      const uint32_t c = part ? by_value : w[j];
-      const float f = bf16_value(scale[j]);
-      uint32_t x[4];
+    for (int part = 0; part < 2; ++part) {
+      uint16_t* p = (part ? v : k) + (i * s.heads + h0) * D + 8 * u;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        x[e] = bf16_bits(float(int((c >> (8 * e)) & 15) - 8) * f) |
-               bf16_bits(float(int((c >> (8 * e + 4)) & 15) - 8) * f) << 16;
-      uint16_t* p = (part ? v : k) + (i * s.heads + h) * D + 8 * u;
-      if (vec) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(x[0], x[1], x[2], x[3]);
-      } else {
+      for (int j = 0; j < I::kSteps; ++j, p += I::kLanes * D) {
+        const uint4 x = values8(part ? value_word(w[part][j], u) : w[part][j], scale[part][j]);
+        if (h0 + j * I::kLanes >= s.heads) continue;
+        if (vec) {
+          *reinterpret_cast<uint4*>(p) = x;
+        } else {
+          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = uint16_t(x[e / 2] >> (16 * (e % 2)));
+          for (int e = 0; e < 8; ++e) p[e] = uint16_t(y[e / 2] >> (16 * (e % 2)));
+        }
       }
     }
   }
@@ -202,7 +246,8 @@ struct EvictArgs {
 };
 
 constexpr int kChoose = 512, kChooseWarps = kChoose / 32;
-constexpr int kHeld = 16;   // keys that a thread holds in registers: 8192 tokens a block
+constexpr int kHeld = 16;   // keys that a thread holds in registers, 8192 a block,
+constexpr int kShared = 22; // and in shared memory, 11264 more
 constexpr int kMaxTeam = 8; // blocks that share a sequence and head
 
 // A mass as a number that orders as it does: NaN lowest, -0 and 0 alike.
@@ -240,6 +285,7 @@ struct Choose {
   uint32_t sums[2][kChooseWarps][3];  // by the parity of the step
   uint32_t team[2][3];                // this block's
   uint32_t below[2][kChooseWarps];
+  uint32_t keys[kShared][kChoose];
 };
 
 __global__ void __launch_bounds__(kChoose, 2) kv4_choose_kernel(EvictArgs a, uint32_t team) {
@@ -262,22 +308,28 @@ __global__ void __launch_bounds__(kChoose, 2) kv4_choose_kernel(EvictArgs a, uin
   const int run = ((n + 31) / 32 + int(team * kChooseWarps) - 1) / int(team * kChooseWarps) * 32;
   const int64_t start = int64_t(rank * kChooseWarps + warp) * run;
   const int i0 = int(min(int64_t(n), start)), i1 = min(n, i0 + run), steps = run / 32;
+  // keys of the tokens to choose from, others 0: nothing that is searched for is
   uint32_t held[kHeld];
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k) {
+  auto load = [&](int k) {
     const int i = i0 + 32 * k + int(lane);
-    held[k] = i < i1 ? mass_key(mass[i]) : 0u;
-  }
-  auto key_at = [&](int k) {
-    const int i = i0 + 32 * k + int(lane);
-    return i < i1 ? mass_key(mass[i]) : 0u;
+    return i < min(i1, n0) ? mass_key(mass[i]) : 0u;
   };
-  // keys of the tokens to choose from, others 0: no candidate below is 0
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) held[k] = load(k);
+  for (int k = kHeld; k < min(steps, kHeld + kShared); ++k) sh.keys[k - kHeld][tid] = load(k);
+  auto key_at = [&](int k) {  // beyond the registers
+    return k < kHeld + kShared ? sh.keys[k - kHeld][tid] : load(k);
+  };
   auto candidates = [&](auto f) {
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k)
-      if (k < steps) f(i0 + 32 * k + int(lane) < min(i1, n0) ? held[k] : 0u);
-    for (int k = kHeld; k < steps; ++k) f(i0 + 32 * k + int(lane) < min(i1, n0) ? key_at(k) : 0u);
+    for (int k = 0; k < kHeld; k += 4)
+      if (k < steps) {
+        f(held[k]);
+        f(held[k + 1]);
+        f(held[k + 2]);
+        f(held[k + 3]);
+      }
+    for (int k = kHeld; k < steps; ++k) f(key_at(k));
   };
   // the sum of three counts over all tokens
   uint32_t parity = 0;
@@ -410,19 +462,33 @@ __global__ void __launch_bounds__(kMove) kv4_move_kernel(EvictArgs a) {
       continue;
     }
     uint8_t* dst = a.cache + (uint64_t(out) * a.s.heads + h) * L::kBlock;
+    // every load of a round is in flight before the first store
     constexpr int kPieces = 2 * L::kRow / 16;  // 16-byte pieces of a token's keys and values
-    for (uint32_t j = threadIdx.x; j < kPage * kPieces; j += kMove) {
-      const uint32_t t = j / kPieces, piece = j % kPieces;
-      if (s_src[t] < 0) continue;
+    constexpr int kRounds = kPage * kPieces / kMove, kScaleRounds = kPage * 2 * L::G / kMove;
+    uint4 x[kRounds];
+    uint16_t y[kScaleRounds];
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+      const uint32_t j = threadIdx.x + k * kMove, t = j / kPieces, piece = j % kPieces;
       const uint32_t part = piece / (kPieces / 2) * L::kHalf, byte = piece % (kPieces / 2) * 16;
-      *reinterpret_cast<uint4*>(dst + part + L::at(t, byte)) =
-          *reinterpret_cast<const uint4*>(a.cache + s_src[t] + part + L::at(s_at[t], byte));
+      if (s_src[t] >= 0) x[k] = *reinterpret_cast<const uint4*>(a.cache + s_src[t] + part + L::at(s_at[t], byte));
     }
-    for (uint32_t j = threadIdx.x; j < kPage * 2 * L::G; j += kMove) {
-      const uint32_t t = j % kPage, g = j / kPage % L::G, part = j / kPage / L::G * L::kHalf;
-      if (s_src[t] < 0) continue;
-      *reinterpret_cast<uint16_t*>(dst + part + L::scale(t, g)) =
-          *reinterpret_cast<const uint16_t*>(a.cache + s_src[t] + part + L::scale(s_at[t], g));
+#pragma unroll
+    for (int k = 0; k < kScaleRounds; ++k) {
+      const uint32_t j = threadIdx.x + k * kMove, t = j % kPage, g = j / kPage;
+      if (s_src[t] >= 0)
+        y[k] = *reinterpret_cast<const uint16_t*>(a.cache + s_src[t] + g / L::G * L::kHalf + L::scale(s_at[t], g % L::G));
+    }
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+      const uint32_t j = threadIdx.x + k * kMove, t = j / kPieces, piece = j % kPieces;
+      const uint32_t part = piece / (kPieces / 2) * L::kHalf, byte = piece % (kPieces / 2) * 16;
+      if (s_src[t] >= 0) *reinterpret_cast<uint4*>(dst + part + L::at(t, byte)) = x[k];
+    }
+#pragma unroll
+    for (int k = 0; k < kScaleRounds; ++k) {
+      const uint32_t j = threadIdx.x + k * kMove, t = j % kPage, g = j / kPage;
+      if (s_src[t] >= 0) *reinterpret_cast<uint16_t*>(dst + g / L::G * L::kHalf + L::scale(t, g % L::G)) = y[k];
     }
   }
 }
@@ -508,7 +574,7 @@ extern "C" int wcomp_kv4_append(wcomp_kv4* c, const wcomp_kv4_seqs* seqs, const 
   const Rows k{d_k, k_row, k_head, rows_vec(d_k, k_row, k_head)}, v{d_v, v_row, v_head, rows_vec(d_v, v_row, v_head)};
 #define CALL(D)                                                                                            \
   do {                                                                                                     \
-    const uint32_t rounds = uint32_t(cdiv(2 * uint64_t(c->heads), Items<D>::kRound));                      \
+    const uint32_t rounds = uint32_t(cdiv(uint64_t(c->heads), Items<D>::kRound));                      \
     kv4_append_kernel<D><<<grid_of(int64_t(cdiv(T * rounds, kThreads / 32)), c->device), kThreads, 0,      \
                            static_cast<cudaStream_t>(stream)>>>(s, c->d, k, v, T, rounds);                 \
   } while (0)
@@ -529,7 +595,7 @@ extern "C" int wcomp_kv4_read(const wcomp_kv4* c, const wcomp_kv4_seqs* seqs, ui
   const int vec = rows_vec(d_k, 0, 0) && rows_vec(d_v, 0, 0);
 #define CALL(D)                                                                                          \
   do {                                                                                                   \
-    const uint32_t rounds = uint32_t(cdiv(2 * uint64_t(c->heads), Items<D>::kRound));                    \
+    const uint32_t rounds = uint32_t(cdiv(uint64_t(c->heads), Items<D>::kRound));                    \
     kv4_read_kernel<D><<<grid_of(int64_t(cdiv(T * rounds, kThreads / 32)), c->device), kThreads, 0,      \
                          static_cast<cudaStream_t>(stream)>>>(s, c->d, d_k, d_v, T, rounds, vec);        \
   } while (0)
@@ -575,7 +641,7 @@ extern "C" int wcomp_kv4_evict(wcomp_kv4* c, const wcomp_kv4_evict_args* args, v
   }
   // blocks share a long sequence while that leaves each something and the GPU has room
   uint32_t team = 1;
-  while (team < kMaxTeam && int64_t(a.width) * kPage > int64_t(team) * kChoose * kHeld &&
+  while (team < kMaxTeam && int64_t(a.width) * kPage > int64_t(team) * kChoose * (kHeld + kShared) &&
          units * team * 2 <= sm_count(c->device) * 4)
     team *= 2;
   cudaLaunchConfig_t cfg = {};

@@ -25,6 +25,11 @@
 // block joins its warps' parts in shared memory and a second kernel those of
 // blocks, always in the same order.  Lengths are on the device, so every block sums
 // up the work of all sequences first.
+//
+// Where the tables leave a warp few pages even if a tile is given to one block or
+// one cluster, that is done instead: one kernel without a workspace, the parts
+// joined through the cluster's shared memory.  One sequence of 4097 tokens, 32 query
+// and 8 cached heads: TEAM_FIGURES.
 #include <algorithm>
 #include <cmath>
 
@@ -720,6 +725,31 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
   }
 }
 
+// The sequence and tile of a place in the order of tiles: sequence b has those from
+// its first row's pairs / R + b on.  False where there is no tile.
+template <int R>
+__device__ __forceinline__ bool tile_at(const AttendArgs& a, int64_t place, int& b, int& tile, Seq& s) {
+  if (a.s.starts) {
+    auto first = [&](int i) { return int64_t(max(a.s.starts[i], 0)) * a.share / R + i; };
+    int lo = 0, hi = a.s.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first(mid) <= place) lo = mid;
+      else hi = mid;
+    }
+    b = lo;
+    place -= first(b);
+    if (place < 0 || place >= (int64_t(1) << 31)) return false;
+    tile = int(place);
+  } else {
+    const int per = (a.share + R - 1) / R;
+    b = int(place / per);
+    tile = int(place % per);
+  }
+  s = load_seq<R, true>(a, b);
+  return tile < s.tiles;
+}
+
 // Join the blocks' parts of a tile and head: one block.  They are those of the first
 // and the last warp that have pages of it and, for every block between or around
 // them, of its first warp with none but the tile's.
@@ -734,25 +764,9 @@ __global__ void __launch_bounds__(kJoin) kv4_join_kernel(const __grid_constant__
   for (int64_t unit = blockIdx.x; unit < tiles * a.s.heads; unit += gridDim.x) {
     const uint32_t head = uint32_t(unit % a.s.heads);
     const int64_t place = unit / a.s.heads;
-    // sequence b has the places from its first row's pairs / R + b on
-    int b = 0, tile;
-    if (a.s.starts) {
-      auto first = [&](int i) { return int64_t(max(a.s.starts[i], 0)) * a.share / R + i; };
-      int lo = 0, hi = a.s.B;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first(mid) <= place) lo = mid;
-        else hi = mid;
-      }
-      b = lo;
-      tile = int(place - first(b));
-    } else {
-      const int per = (a.share + R - 1) / R;
-      b = int(place / per);
-      tile = int(place % per);
-    }
-    const Seq s = load_seq<R, true>(a, b);
-    if (tile < 0 || tile >= s.tiles) continue;
+    int b, tile;
+    Seq s;
+    if (!tile_at<R>(a, place, b, tile, s)) continue;
     const uint64_t f0 = a.prefix[b] + (uint64_t(tile) * a.s.heads + head) * uint32_t(s.pages), f1 = f0 + uint32_t(s.pages);
     const uint32_t w0 = runs.of(f0), w1 = runs.of(f1 - 1);
     if (w0 == w1 || w1 >= a.warps) continue;
@@ -775,7 +789,7 @@ __global__ void __launch_bounds__(kJoin) kv4_join_kernel(const __grid_constant__
       if (to < 0) continue;
       float m = -INFINITY, l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
       for (uint32_t p = 0; p < blocks + 2; ++p) {
         const int at = s_place[p];
         if (at < 0) continue;
@@ -795,6 +809,182 @@ __global__ void __launch_bounds__(kJoin) kv4_join_kernel(const __grid_constant__
       if (col == 0) store_lse(a, to, m, l);
     }
   }
+}
+
+// A tile and head by one block, or by a cluster of up to 16: every warp takes every
+// (blocks x warps)-th page.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A float of block `rank` at the shared-memory address that `at` is in this one.
+__device__ __forceinline__ float cluster_lds(uint32_t at, uint32_t rank) {
+  float v;
+  asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.f32 %0, [r];\n\t}"
+               : "=f"(v)
+               : "r"(at), "r"(rank)
+               : "memory");
+  return v;
+}
+constexpr uint32_t kMaxTeam = 16;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
+    kv4_attend_team_kernel(const __grid_constant__ AttendArgs a, uint32_t team) {
+  constexpr int kWarps = Shape<D, NT>::kWarps, kDepth = Shape<D, NT>::kDepth, R = 8 * NT, V = D / 32;
+  using Src = KvSrc<D, true>;
+  struct At {
+    Seq q;
+    int tile;
+    uint32_t head;
+  };
+  __shared__ float2 s_ml[kWarps][R], s_joined[R];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t smem = smem_u32(smem_raw) + (-smem_u32(smem_raw) & 127u);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t magic = q4_magic();
+  const uint32_t rank = team > 1 ? cluster_rank() : 0;
+  Ring<Src, kDepth> ring(smem + uint32_t(warp) * kDepth * Src::kStage,
+                         smem + kWarps * kDepth * Src::kStage + uint32_t(warp) * kDepth * 8, a.s.err, lane);
+  At at;
+  int b;
+  at.head = blockIdx.x / team % a.s.heads;
+  // the same for all of a cluster
+  if (!tile_at<R>(a, blockIdx.x / team / a.s.heads, b, at.tile, at.q)) return;
+  // a warp's pages in the sequence: first + k * stride; the ids of 32 of them at a time
+  const int first = int(rank * kWarps) + warp, stride = int(team * kWarps);
+  const int count = max(0, (at.q.pages - first + stride - 1) / stride), pages = (at.q.n + kPage - 1) / kPage;
+  const uint8_t* const head = a.cache + uint64_t(at.head) * Kv<D>::kBlock;
+  int id = -1, ahead = 0;
+  uint32_t there = 0;
+  auto issue = [&](uint32_t slot) {
+    if (ahead == count) return;
+    if (ahead % 32 == 0) {
+      const int page = at.q.page0 + first + (ahead + lane) * stride;
+      id = ahead + lane < count && page < pages ? kv_page(a.s, b, page) : -1;
+    }
+    const int page = __shfl_sync(0xffffffffu, id, ahead % 32);
+    there = page >= 0 ? there | 1u << slot : there & ~(1u << slot);
+    const uint8_t* p = head + uint64_t(uint32_t(max(page, 0))) * (a.s.heads * Kv<D>::kBlock);
+    ring.refill(slot, p, lane);
+    ++ahead;
+  };
+#pragma unroll 1
+  for (int i = 0; i < kDepth; ++i) issue(uint32_t(i));
+  Tile<D, NT> tile;
+  Sums<D, NT> sums;
+  tile.load(a, at.q, at.tile, int(at.head), lane);
+  sums.clear();
+#pragma unroll 1
+  for (int k = 0; k < count; ++k) {
+    const int page = at.q.page0 + first + k * stride;
+    ring.wait(lane);
+    if ((there >> ring.slot & 1) && !tile.sees_none(page)) {
+      float z[4][NT][4];
+      tile.scores(ring.stage(), lane, magic, z);
+      if (tile.sees_all(page)) sums.template add<true>(a, at, tile, page, ring.stage() + Kv<D>::kHalf, lane, magic, z);
+      else sums.template add<false>(a, at, tile, page, ring.stage() + Kv<D>::kHalf, lane, magic, z);
+    }
+    __syncwarp();
+    issue(ring.slot);
+    ring.next();
+  }
+  // the warp's sums to its own stages
+  const uint32_t q = uint32_t(lane) & 3, r = uint32_t(lane) >> 2;
+  float* const stages = reinterpret_cast<float*>(smem_raw + (smem - smem_u32(smem_raw)));
+  constexpr int kPart = kDepth * int(Src::kStage) / 4;
+  const float back = power_of_two(-sums.k);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = sums.l[n][e];
+#pragma unroll
+      for (int d = 4; d <= 16; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
+      const int row = 8 * n + 2 * int(q) + e;
+      if (r == 0) s_ml[warp][row] = make_float2(sums.m[n][e], l);
+#pragma unroll
+      for (int i = 0; i < Kv<D>::G; ++i)
+        *reinterpret_cast<float4*>(stages + warp * kPart + row * D + 32 * i + 4 * r) =
+            make_float4(sums.o[2 * i][n][e] * back, sums.o[2 * i][n][2 + e] * back, sums.o[2 * i + 1][n][e] * back,
+                        sums.o[2 * i + 1][n][2 + e] * back);
+    }
+  __syncthreads();
+  // join the warps: each takes some rows
+  const int parts = min(kWarps, max(0, at.q.pages - int(rank * kWarps)));
+  constexpr int kRows = (R + kWarps - 1) / kWarps;
+  float o[kRows][V];
+  float2 ml[kRows];
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    const int row = warp + j * kWarps;
+    if (row >= R) break;
+    float m = -INFINITY, l = 0.f;
+    for (int w = 0; w < parts; ++w) m = fmaxf(m, s_ml[w][row].x);
+    const float from = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[j][k] = 0.f;
+#pragma unroll 4
+    for (int w = 0; w < parts; ++w) {
+      const float2 x = s_ml[w][row];
+      const float f = exp2_approx(x.x - from);
+      l += f * x.y;
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[j][k] += f * stages[w * kPart + row * D + lane + 32 * k];
+    }
+    ml[j] = make_float2(m, l);
+  }
+  auto finish = [&](int row, float m, float l, const float (&x)[V]) {
+    int lo, hi;
+    const int64_t to = Tile<D, NT>::row(a, at.q, at.tile, int(at.head), row / 8, row % 2, row % 8 / 2, lo, hi);
+    if (to < 0) return;
+    const float f = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int k = 0; k < V; ++k) a.out[to * D + lane + 32 * k] = uint16_t(bf16x2_bits(x[k] * f, 0.f));
+    if (lane == 0) store_lse(a, to, m, l);
+  };
+  if (team == 1) {
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+      if (warp + j * kWarps < R) finish(warp + j * kWarps, ml[j].x, ml[j].y, o[j]);
+    return;
+  }
+  __syncthreads();  // the parts have been read
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    const int row = warp + j * kWarps;
+    if (row >= R) break;
+    if (lane == 0) s_joined[row] = ml[j];
+#pragma unroll
+    for (int k = 0; k < V; ++k) stages[row * D + lane + 32 * k] = o[j][k];
+  }
+  cluster_sync();
+  // join the blocks: a row a warp of all of them
+  for (int row = int(rank) + int(team) * warp; row < R; row += int(team) * kWarps) {
+    const float2 mine = lane < team ? make_float2(cluster_lds(smem_u32(&s_joined[row].x), lane),
+                                                  cluster_lds(smem_u32(&s_joined[row].y), lane))
+                                    : make_float2(-INFINITY, 0.f);
+    float m = mine.x;
+#pragma unroll
+    for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float f = exp2_approx(mine.x - (m == -INFINITY ? 0.f : m));
+    float l = 0.f, x[V] = {};
+#pragma unroll 4
+    for (uint32_t w = 0; w < team; ++w) {
+      const float g = __shfl_sync(0xffffffffu, f, w);
+      l += g * __shfl_sync(0xffffffffu, mine.y, w);
+#pragma unroll
+      for (int k = 0; k < V; ++k) x[k] += g * cluster_lds(smem + 4 * uint32_t(row * D + lane + 32 * k), w);
+    }
+    finish(row, m, l, x);
+  }
+  cluster_sync();  // a block's shared memory stays while others read it
 }
 
 // The weight of every token: the scores again, from the keys alone, against the
@@ -889,51 +1079,114 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(con
 }
 
 template <class K, class... ARGS>
-cudaError_t launch(K kernel, uint32_t grid, int threads, uint32_t smem, bool dependent, cudaStream_t s,
-                   const ARGS&... args) {
+cudaError_t launch(K kernel, uint32_t grid, int threads, uint32_t smem, bool dependent, uint32_t cluster,
+                   cudaStream_t s, const ARGS&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(uint32_t(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = dependent ? 1 : 0;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  if (dependent) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = cluster;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
   count_launches(1);
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Once a device: the kernels' shared memory and clusters of 16 allowed; how many of
+// those fit the GPU at a time (none, where no group of 16 SMs is near enough).
+template <int D, int NT>
+cudaError_t prepare(int dev, int* wide) {
+  static std::mutex mu;
+  static int known[64];  // and 1
+  std::lock_guard<std::mutex> g(mu);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!known[dev]) {
+    constexpr int smem = int(Shape<D, NT>::kSmem);
+    const auto limit = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t e = cudaFuncSetAttribute(kv4_attend_kernel<D, NT>, limit, smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kv4_mass_kernel<D, NT>, limit, smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kv4_attend_team_kernel<D, NT>, limit, smem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kv4_attend_team_kernel<D, NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kMaxTeam);
+    cfg.blockDim = dim3(uint32_t(Shape<D, NT>::kThreads));
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kMaxTeam;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kv4_attend_team_kernel<D, NT>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    known[dev] = 1 + std::max(n, 0);
+  }
+  *wide = known[dev] - 1;
+  return cudaSuccess;
+}
+
+// Blocks to a tile and head, or 0 where the units are cut anywhere: the largest
+// cluster that leaves all of them an SM of their own, if its warps get at most
+// two pages each by the table.
+template <int D, int NT>
+uint32_t team_of(const AttendArgs& a, int64_t segments, uint32_t sms, int wide) {
+  uint32_t team = 1;
+  while (team < kMaxTeam && segments * team * 2 <= sms) team *= 2;
+  if (team == kMaxTeam && segments > wide) team /= 2;
+  const int64_t pages = a.window ? std::min<int64_t>(a.s.width, (int64_t(a.window) + a.T) / kPage + 2) : a.s.width;
+  return segments <= sms && pages <= int64_t(2) * team * Shape<D, NT>::kWarps ? team : 0;
 }
 
 template <int D, int NT>
 int attend(AttendArgs& a, int dev, cudaStream_t s) {
   constexpr int kThreads = Shape<D, NT>::kThreads;
-  const uint32_t sms = uint32_t(std::min(sm_count(dev), kJoin - 2));  // a part a block, and two
   constexpr uint32_t smem = Shape<D, NT>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(kv4_attend_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  if (e == cudaSuccess && a.mass)
-    e = cudaFuncSetAttribute(kv4_mass_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  const uint32_t sms = uint32_t(std::min(sm_count(dev), kJoin - 2));  // a part a block, and two
+  int wide = 0;
+  cudaError_t e = prepare<D, NT>(dev, &wide);
   if (e != cudaSuccess) return map_cuda(e);
+  // places for the tiles of all sequences (tile_at)
+  const int64_t tiles = a.s.starts ? a.T * a.share / (8 * NT) + a.s.B + 1
+                                   : int64_t(a.s.B) * int64_t(cdiv(uint64_t(a.share), 8 * NT));
+  const uint32_t team = team_of<D, NT>(a, tiles * a.s.heads, sms, wide);
   a.warps = sms * Shape<D, NT>::kWarps;
   auto up = [](uint64_t x) { return (x + 255) & ~uint64_t(255); };
-  const uint64_t slots = uint64_t(2) * a.warps * 8 * NT;
-  const uint64_t b_prefix = up((uint64_t(a.s.B) + 1) * 8), b_lse = a.mass ? up(uint64_t(a.T) * a.q_heads * 4) : 0,
-                 b_ml = up(slots * 8), b_part = slots * D * 4;
+  const uint64_t slots = team ? 0 : uint64_t(2) * a.warps * 8 * NT;
+  const uint64_t b_prefix = team ? 0 : up((uint64_t(a.s.B) + 1) * 8),
+                 b_lse = a.mass ? up(uint64_t(a.T) * a.q_heads * 4) : 0, b_ml = up(slots * 8), b_part = slots * D * 4;
   uint8_t* ws = nullptr;
-  e = pool_alloc(reinterpret_cast<void**>(&ws), b_prefix + b_lse + b_ml + b_part, s);
-  if (e != cudaSuccess) return map_cuda(e);
+  if (b_prefix + b_lse + b_ml + b_part) {
+    e = pool_alloc(reinterpret_cast<void**>(&ws), b_prefix + b_lse + b_ml + b_part, s);
+    if (e != cudaSuccess) return map_cuda(e);
+  }
   a.prefix = reinterpret_cast<uint64_t*>(ws);
   a.lse2 = reinterpret_cast<float*>(ws + b_prefix);
   a.part_ml = reinterpret_cast<float2*>(ws + b_prefix + b_lse);
   a.part = reinterpret_cast<float*>(ws + b_prefix + b_lse + b_ml);
-  e = launch(kv4_attend_kernel<D, NT>, sms, kThreads, smem, false, s, a);
-  // places for the tiles of all sequences (kv4_join_kernel)
-  const int64_t tiles = a.s.starts ? a.T * a.share / (8 * NT) + a.s.B + 1
-                                   : int64_t(a.s.B) * int64_t(cdiv(a.share, 8 * NT));
-  const uint32_t joins = uint32_t(std::min<int64_t>(tiles * a.s.heads, int64_t(sms) * 64));
-  if (e == cudaSuccess) e = launch(kv4_join_kernel<D, NT>, joins, kJoin, 0, true, s, a, tiles);
-  if (e == cudaSuccess && a.mass) e = launch(kv4_mass_kernel<D, NT>, sms, kThreads, smem, true, s, a);
-  cudaFreeAsync(ws, s);
+  if (team) {
+    e = launch(kv4_attend_team_kernel<D, NT>, uint32_t(tiles * a.s.heads) * team, kThreads, smem, false, team, s, a, team);
+  } else {
+    e = launch(kv4_attend_kernel<D, NT>, sms, kThreads, smem, false, 1, s, a);
+    const uint32_t joins = uint32_t(std::min<int64_t>(tiles * a.s.heads, int64_t(sms) * 64));
+    if (e == cudaSuccess) e = launch(kv4_join_kernel<D, NT>, joins, kJoin, 0, true, 1, s, a, tiles);
+  }
+  if (e == cudaSuccess && a.mass) e = launch(kv4_mass_kernel<D, NT>, sms, kThreads, smem, true, 1, s, a);
+  if (ws) cudaFreeAsync(ws, s);
   return map_cuda(e);
 }
 
