@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(kJoin) kv4_join_kernel(const __grid_constant__
   constexpr int R = 8 * NT, K = Shape<D, NT>::kWarps, kItems = R * D / 4;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ int s_place[kJoin];  // of part p, or -1
+  __shared__ int s_place[kJoin], s_count[kJoin / 32];  // the parts' places; how many before each warp's
   const Runs runs{a.prefix[a.s.B], a.warps};
   for (int64_t unit = blockIdx.x; unit < tiles * a.s.heads; unit += gridDim.x) {
     const uint32_t head = uint32_t(unit % a.s.heads);
@@ -771,16 +771,25 @@ __global__ void __launch_bounds__(kJoin) kv4_join_kernel(const __grid_constant__
     const uint32_t w0 = runs.of(f0), w1 = runs.of(f1 - 1);
     if (w0 == w1 || w1 >= a.warps) continue;
     const uint32_t c0 = w0 / K, blocks = w1 / K - c0 + 1;
-    __syncthreads();
+    int at = -1;
     if (threadIdx.x < blocks + 2) {
       const uint32_t p = threadIdx.x;
-      int at = int(p == 0 ? (2 * w0 + 1) * R : 2 * w1 * R);
+      at = int(p == 0 ? (2 * w0 + 1) * R : 2 * w1 * R);
       if (p > 1) {
         const uint32_t lo = max(w0 + 1, (c0 + p - 2) * K), w = runs.of(runs.first(lo));
         at = w < min(w1, (c0 + p - 1) * K) ? int(2 * w * R) : -1;
       }
-      s_place[p] = at;
     }
+    const uint32_t some = __ballot_sync(0xffffffffu, at >= 0);
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) s_count[threadIdx.x / 32] = __popc(some);
+    __syncthreads();
+    int before = 0, parts = 0;
+    for (int w = 0; w < kJoin / 32; ++w) {
+      if (w < int(threadIdx.x / 32)) before += s_count[w];
+      parts += s_count[w];
+    }
+    if (at >= 0) s_place[before + __popc(some & ((1u << threadIdx.x % 32) - 1u))] = at;
     __syncthreads();
     for (int item = threadIdx.x; item < kItems; item += kJoin) {
       const int row = 4 * item / D, col = 4 * item % D;
@@ -790,19 +799,18 @@ __global__ void __launch_bounds__(kJoin) kv4_join_kernel(const __grid_constant__
       float m = -INFINITY, l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-      for (uint32_t p = 0; p < blocks + 2; ++p) {
-        const int at = s_place[p];
-        if (at < 0) continue;
-        const float2 ml = a.part_ml[at + row];
-        const float4 x = *reinterpret_cast<const float4*>(a.part + int64_t(at + row) * D + col);
-        const float next = fmaxf(m, ml.x), from = next == -INFINITY ? 0.f : next;
-        const float down = exp2f(m - from), f = exp2f(ml.x - from);
-        m = next;
-        l = l * down + ml.y * f;
-        o.x = o.x * down + x.x * f;
-        o.y = o.y * down + x.y * f;
-        o.z = o.z * down + x.z * f;
-        o.w = o.w * down + x.w * f;
+      for (int p = 0; p < parts; ++p) m = fmaxf(m, a.part_ml[s_place[p] + row].x);
+      const float from = m == -INFINITY ? 0.f : m;
+#pragma unroll 8
+      for (int p = 0; p < parts; ++p) {
+        const float2 ml = a.part_ml[s_place[p] + row];
+        const float4 x = *reinterpret_cast<const float4*>(a.part + int64_t(s_place[p] + row) * D + col);
+        const float f = exp2_approx(ml.x - from);
+        l += ml.y * f;
+        o.x += x.x * f;
+        o.y += x.y * f;
+        o.z += x.z * f;
+        o.w += x.w * f;
       }
       const float f = l == 0.f ? 0.f : 1.f / l;
       *reinterpret_cast<uint2*>(a.out + to * D + col) = make_uint2(bf16x2_bits(o.x * f, o.y * f), bf16x2_bits(o.z * f, o.w * f));
