@@ -62,6 +62,10 @@ struct AttendArgs {
 // ---------------------------------------------------------------------------
 // Units.
 // ---------------------------------------------------------------------------
+// u / d, by the short division where u has 32 bits.
+__device__ __forceinline__ uint64_t quotient(uint64_t u, uint64_t d) {
+  return (u | d) >> 32 ? u / d : uint32_t(u) / uint32_t(d);
+}
 struct Seq {
   int n, rows;     // tokens, and rows of the call
   int64_t first;   // first row
@@ -146,10 +150,10 @@ struct Walk {
       u -= w;
       q = load_seq<R, TILES>(a, ++b);
     }
-    const uint64_t seg = u / uint32_t(q.pages);
-    page = int(u % uint32_t(q.pages));
-    tile = int(seg / a.s.heads);
-    head = uint32_t(seg % a.s.heads);
+    const uint64_t seg = quotient(u, uint32_t(q.pages));
+    page = int(u - seg * uint32_t(q.pages));
+    tile = int(quotient(seg, a.s.heads));
+    head = uint32_t(seg - uint64_t(tile) * a.s.heads);
   }
   // The next unit, which there is.
   __device__ __forceinline__ void next(const AttendArgs& a) {
@@ -169,8 +173,8 @@ struct Walk {
 struct Runs {
   uint64_t total;
   uint32_t W;
-  __device__ __forceinline__ uint64_t first(uint32_t w) const { return total * w / W; }
-  __device__ __forceinline__ uint32_t of(uint64_t unit) const { return uint32_t(((unit + 1) * W - 1) / total); }
+  __device__ __forceinline__ uint64_t first(uint32_t w) const { return quotient(total * w, W); }
+  __device__ __forceinline__ uint32_t of(uint64_t unit) const { return uint32_t(quotient((unit + 1) * W - 1, total)); }
 };
 
 template <int D, bool VALUES>
