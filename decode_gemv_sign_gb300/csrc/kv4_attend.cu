@@ -21,7 +21,7 @@
 // going over to another scales exactly, by powers of two.
 //
 // Each warp takes an equal run of the call's (sequence, tile of rows, head, page)
-// units through a ring of its own.  Where a tile's pages fall on several warps, a
+// units through a ring of its own, a tile's beginning and end counted as one more.  Where a tile's pages fall on several warps, a
 // block joins its warps' parts in shared memory and a second kernel those of
 // blocks, always in the same order.  Lengths are on the device, so every block sums
 // up the work of all sequences first.
@@ -74,7 +74,10 @@ struct Seq {
 };
 
 // TILES: every tile of rows is work of its own; else a page is one unit for all of
-// them.  A sequence with rows has at least one page, also where it has no token.
+// them.  A sequence with rows has at least one page, also where it has no token.  A
+// tile and head has one unit before its pages: what it costs to begin and end.
+// (Without it the warps of 16 sequences of 0 to 16384 tokens that had the short ones
+// took twice as long as the others.)
 template <int R, bool TILES>
 __device__ __forceinline__ Seq load_seq(const AttendArgs& a, int b) {
   Seq q;
@@ -94,7 +97,7 @@ __device__ __forceinline__ Seq load_seq(const AttendArgs& a, int b) {
   return q;
 }
 __device__ __forceinline__ uint64_t seq_units(const AttendArgs& a, const Seq& q) {
-  return uint64_t(q.tiles) * a.s.heads * uint64_t(q.pages);
+  return uint64_t(q.tiles) * a.s.heads * (uint64_t(q.pages) + 1);
 }
 
 // Units before the sequences of each thread's share, [threads + 1] in shared
@@ -133,7 +136,7 @@ __device__ __forceinline__ void sum_units(const AttendArgs& a, uint64_t* s_befor
 // lane 0: registers are what the products want.
 template <int THREADS, int R, bool TILES>
 struct Walk {
-  int b, page, tile;
+  int b, page, tile;  // page -1: the unit before the pages
   uint32_t head;
   Seq q;
   __device__ __forceinline__ void find(const AttendArgs& a, const uint64_t* s_before, uint64_t u) {
@@ -150,15 +153,15 @@ struct Walk {
       u -= w;
       q = load_seq<R, TILES>(a, ++b);
     }
-    const uint64_t seg = quotient(u, uint32_t(q.pages));
-    page = int(u - seg * uint32_t(q.pages));
+    const uint64_t seg = quotient(u, uint32_t(q.pages) + 1);
+    page = int(u - seg * (uint32_t(q.pages) + 1)) - 1;
     tile = int(quotient(seg, a.s.heads));
     head = uint32_t(seg - uint64_t(tile) * a.s.heads);
   }
   // The next unit, which there is.
   __device__ __forceinline__ void next(const AttendArgs& a) {
     if (++page < q.pages) return;
-    page = 0;
+    page = -1;
     if (++head < a.s.heads) return;
     head = 0;
     if (++tile < q.tiles) return;
@@ -199,6 +202,12 @@ struct Pages {
   __device__ __forceinline__ Pages(WALK& walk, uint64_t count) : it(walk), left(count) {}
   __device__ __forceinline__ void enter(const AttendArgs& a, int lane) {
     __syncwarp();
+    if (it.page < 0) {
+      if (--left == 0) return;
+      __syncwarp();
+      if (lane == 0) it.page = 0;
+      __syncwarp();
+    }
     const int at = it.q.page0 + it.page;
     if (in != it.b || at < base || at >= base + 32) {
       in = it.b;
@@ -219,7 +228,10 @@ struct Pages {
   // by the cache's first, which nothing is read of.
   __device__ __forceinline__ void issue(const AttendArgs& a, RING& ring, uint32_t slot, int lane) {
     if (!left) return;
-    if (!run) enter(a, lane);
+    if (!run) {
+      enter(a, lane);
+      if (!left) return;
+    }
     const int page = __shfl_sync(0xffffffffu, id, from++);
     there = page >= 0 ? there | 1u << slot : there & ~(1u << slot);
     const uint8_t* p = head + uint64_t(uint32_t(max(page, 0))) * (a.s.heads * Kv<D>::kBlock);
@@ -421,20 +433,22 @@ struct Sums {
     const uint32_t r = uint32_t(lane) >> 2, q = uint32_t(lane) & 3;
     uint32_t seen[NT][2];  // bit 2 i + h: the token 16 i + 8 h + r
     if (!ALL) {
+      const int from = page * kPage + int(r);
+      auto below = [&](int end) {  // bits of the tokens before `end`
+        const int k = (end - from + 7) >> 3;
+        return k <= 0 ? 0u : k >= 8 ? 0xFFu : (1u << k) - 1u;
+      };
+      const bool alike = t.lo0 == t.lo1 && t.hi0 == t.hi1;  // all rows see the same
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          int lo, hi;
-          Tile<D, NT>::row(p, at.q, at.tile, int(at.head), n, e, lane, lo, hi);
-          seen[n][e] = 0;
+          int lo = t.lo0, hi = t.hi0;
+          if (!alike) Tile<D, NT>::row(p, at.q, at.tile, int(at.head), n, e, lane, lo, hi);
+          seen[n][e] = below(hi) & ~below(lo);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int pos = page * kPage + 8 * k + int(r);
-            const bool see = pos >= lo && pos < hi;
-            seen[n][e] |= uint32_t(see) << k;
-            if (!see) z[k / 2][n][e + 2 * (k % 2)] = -INFINITY;
-          }
+          for (int k = 0; k < 8; ++k)
+            if (!(seen[n][e] >> k & 1)) z[k / 2][n][e + 2 * (k % 2)] = -INFINITY;
         }
     }
     bool more = false;
@@ -623,6 +637,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
   const uint32_t q = uint32_t(lane) & 3, r = uint32_t(lane) >> 2;
   while (u < end) {
     // a tile's pages, or those of them that fall on this warp
+    if (at.page < 0) {
+      if (++u == end) break;
+      __syncwarp();
+      if (lane == 0) at.page = 0;
+      __syncwarp();
+    }
     const bool first = at.page == 0;
     int page = at.q.page0 + at.page;
     const int stop = int(min(int64_t(at.q.page0 + at.q.pages), int64_t(page) + int64_t(end - u)));
@@ -771,7 +791,7 @@ __global__ void __launch_bounds__(kJoin) kv4_join_kernel(const __grid_constant__
     int b, tile;
     Seq s;
     if (!tile_at<R>(a, place, b, tile, s)) continue;
-    const uint64_t f0 = a.prefix[b] + (uint64_t(tile) * a.s.heads + head) * uint32_t(s.pages), f1 = f0 + uint32_t(s.pages);
+    const uint64_t f0 = a.prefix[b] + (uint64_t(tile) * a.s.heads + head) * (uint32_t(s.pages) + 1) + 1, f1 = f0 + uint32_t(s.pages);
     const uint32_t w0 = runs.of(f0), w1 = runs.of(f1 - 1);
     if (w0 == w1 || w1 >= a.warps) continue;
     const uint32_t c0 = w0 / K, blocks = w1 / K - c0 + 1;
@@ -1037,6 +1057,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(con
   uint32_t head = 0;  // what the tile holds
   const uint32_t r = uint32_t(lane) >> 2, q = uint32_t(lane) & 3;
   for (; u < end; ++u) {
+    if (at.page < 0) {
+      __syncwarp();
+      if (lane == 0) at.page = 0;
+      __syncwarp();
+      continue;
+    }
     ring.wait(lane);
     const int page = at.q.page0 + at.page;
     if (pages.there >> ring.slot & 1) {
