@@ -29,23 +29,6 @@ struct Items {
   static constexpr int kRound = kLanes * kSteps;
 };
 
-// Two fp32 operations an instruction.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 // Quantise 8 columns, whose group's other columns the three neighbouring lanes have.
 // `w` gets the codes, 4 bits each; returns the scale's bits.
 __device__ __forceinline__ uint32_t quantise8(const uint32_t (&v)[4], uint32_t& w) {

@@ -517,21 +517,21 @@ struct Sums {
         k = to;
       }
     }
+    uint64_t w2[4][NT][2];  // weights under 2^k, a row's of the tokens 16 i + r and 16 i + 8 + r together
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float shift = float(k) - (m[n][e] == -INFINITY ? 0.f : m[n][e]);
-        float sum = 0.f;
+        const uint64_t c2 = pair(t.c[n][e], t.c[n][e]), shift2 = pair(shift, shift);
+        uint64_t sum = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int h = 0; h < 4; h += 2) {
-            const float x = exp2_approx(__fmaf_rn(z[i][n][e + h], t.c[n][e], shift));
-            sum += x;
-            z[i][n][e + h] = x;
-          }
-        l[n][e] = __fmaf_rn(sum, power_of_two(-k), l[n][e]);
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t x = fma2(pair(z[i][n][e], z[i][n][e + 2]), c2, shift2);
+          w2[i][n][e] = pair(exp2_approx(first(x)), exp2_approx(second(x)));
+          sum = i ? add2(sum, w2[i][n][e]) : w2[i][n][e];
+        }
+        l[n][e] = __fmaf_rn(first(sum) + second(sum), power_of_two(-k), l[n][e]);
       }
     uint32_t sc[G][4];
 #pragma unroll
@@ -547,13 +547,12 @@ struct Sums {
 #pragma unroll
         for (int side = 0; side < 2; ++side) {  // groups 2 a and 2 a + 1
           const int g = 2 * a + side;
-          const float s0 = bf16_lo(sc[g][i]), s1 = bf16_hi(sc[g][i]);
+          const uint64_t s2 = pair(bf16_lo(sc[g][i]), bf16_hi(sc[g][i]));
           uint32_t b[NT][2];
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            float x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = z[i][n][e] * (e < 2 ? s0 : s1);
+            const uint64_t x0 = mul2(w2[i][n][0], s2), x1 = mul2(w2[i][n][1], s2);
+            float x[4] = {first(x0), first(x1), second(x0), second(x1)};
             if (!ALL) {
 #pragma unroll
               for (int e = 0; e < 4; ++e)  // also where the scale is NaN
