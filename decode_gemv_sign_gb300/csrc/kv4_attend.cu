@@ -52,7 +52,6 @@ struct AttendArgs {
   int q_heads, share, window, q_vec;
   float scale;
   // workspace
-  uint64_t* prefix;  // [B + 1]: units before each sequence
   float* lse2;       // [T, q_heads], in base 2 (with mass)
   float* part;       // [2 warps][rows][D]: sums
   float2* part_ml;   // [2 warps][rows]: maximum (base 2) and sum
@@ -101,9 +100,9 @@ __device__ __forceinline__ uint64_t seq_units(const AttendArgs& a, const Seq& q)
 }
 
 // Units before the sequences of each thread's share, [threads + 1] in shared
-// memory.  `out` gets those before each sequence.
+// memory.
 template <int THREADS, int R, bool TILES>
-__device__ __forceinline__ void sum_units(const AttendArgs& a, uint64_t* s_before, uint64_t* s_warp, uint64_t* out) {
+__device__ __forceinline__ void sum_units(const AttendArgs& a, uint64_t* s_before, uint64_t* s_warp) {
   const int per = (a.s.B + THREADS - 1) / THREADS;
   const int b0 = min(a.s.B, int(threadIdx.x) * per), b1 = min(a.s.B, b0 + per);
   uint64_t sum = 0;
@@ -121,13 +120,6 @@ __device__ __forceinline__ void sum_units(const AttendArgs& a, uint64_t* s_befor
   for (int w = 0; w < warp; ++w) before += s_warp[w];
   s_before[threadIdx.x] = before;
   if (threadIdx.x == THREADS - 1) s_before[THREADS] = before + sum;
-  if (out) {
-    for (int b = b0; b < b1; ++b) {
-      out[b] = before;
-      before += seq_units(a, load_seq<R, TILES>(a, b));
-    }
-    if (threadIdx.x == THREADS - 1) out[a.s.B] = before;
-  }
   __syncthreads();
 }
 
@@ -614,7 +606,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
   const uint32_t magic = q4_magic();
   Ring<Src, kDepth> ring(smem + uint32_t(warp) * kDepth * Src::kStage,
                          smem + kWarps * kDepth * Src::kStage + uint32_t(warp) * kDepth * 8, a.s.err, lane);
-  sum_units<kThreads, R, true>(a, s_before, s_warp, blockIdx.x == 0 ? a.prefix : nullptr);
+  sum_units<kThreads, R, true>(a, s_before, s_warp);
   const Runs runs{s_before[kThreads], a.warps};
   const uint32_t me = blockIdx.x * kWarps + uint32_t(warp);
   if (threadIdx.x <= kWarps) s_first[threadIdx.x] = runs.first(blockIdx.x * kWarps + threadIdx.x);
@@ -775,22 +767,34 @@ __device__ __forceinline__ bool tile_at(const AttendArgs& a, int64_t place, int&
 
 // Join the blocks' parts of a tile and head: one block.  They are those of the first
 // and the last warp that have pages of it and, for every block between or around
-// them, of its first warp with none but the tile's.
-constexpr int kJoin = 256;
-template <int D, int NT>
-__global__ void __launch_bounds__(kJoin) kv4_join_kernel(const __grid_constant__ AttendArgs a, int64_t tiles) {
+// them, of its first warp with none but the tile's.  Where they are follows from the
+// lengths alone and is worked out while the attention still runs; then every load of
+// a thread is in flight at once.  (With places read from the workspace and eight
+// loads at a time the joins of one sequence of 262143 tokens took 12 us.)
+constexpr int kAtOnce = 8, kMaxParts = 256;
+template <int D, int NT, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv4_join_kernel(const __grid_constant__ AttendArgs a, int64_t tiles) {
   constexpr int R = 8 * NT, K = Shape<D, NT>::kWarps, kItems = R * D / 4;
+  constexpr int kGroups = THREADS / kItems;  // of threads that share a tile's parts
+  static_assert(kItems * kGroups == THREADS, "an item a thread");
+  __shared__ uint64_t s_before[THREADS + 1], s_warp[THREADS / 32];
+  __shared__ int s_place[kMaxParts], s_count[THREADS / 32];
+  __shared__ float4 s_o[kGroups][kItems];
+  __shared__ float2 s_ml[kGroups][R];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ int s_place[kJoin], s_count[kJoin / 32];  // the parts' places; how many before each warp's
-  const Runs runs{a.prefix[a.s.B], a.warps};
+  sum_units<THREADS, R, true>(a, s_before, s_warp);
+  const Runs runs{s_before[THREADS], a.warps};
+  bool waited = false;
   for (int64_t unit = blockIdx.x; unit < tiles * a.s.heads; unit += gridDim.x) {
     const uint32_t head = uint32_t(unit % a.s.heads);
     const int64_t place = unit / a.s.heads;
     int b, tile;
     Seq s;
     if (!tile_at<R>(a, place, b, tile, s)) continue;
-    const uint64_t f0 = a.prefix[b] + (uint64_t(tile) * a.s.heads + head) * (uint32_t(s.pages) + 1) + 1, f1 = f0 + uint32_t(s.pages);
+    const int per = (a.s.B + THREADS - 1) / THREADS;
+    uint64_t f0 = s_before[b / per] + (uint64_t(tile) * a.s.heads + head) * (uint32_t(s.pages) + 1) + 1;
+    for (int i = b / per * per; i < b; ++i) f0 += seq_units(a, load_seq<R, true>(a, i));
+    const uint64_t f1 = f0 + uint32_t(s.pages);
     const uint32_t w0 = runs.of(f0), w1 = runs.of(f1 - 1);
     if (w0 == w1 || w1 >= a.warps) continue;
     const uint32_t c0 = w0 / K, blocks = w1 / K - c0 + 1;
@@ -808,38 +812,78 @@ __global__ void __launch_bounds__(kJoin) kv4_join_kernel(const __grid_constant__
     if (threadIdx.x % 32 == 0) s_count[threadIdx.x / 32] = __popc(some);
     __syncthreads();
     int before = 0, parts = 0;
-    for (int w = 0; w < kJoin / 32; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
       if (w < int(threadIdx.x / 32)) before += s_count[w];
       parts += s_count[w];
     }
     if (at >= 0) s_place[before + __popc(some & ((1u << threadIdx.x % 32) - 1u))] = at;
+    const int group = int(threadIdx.x) / kItems, item = int(threadIdx.x) % kItems;
+    const int row = 4 * item / D, col = 4 * item % D;
+    int lo, hi;
+    const int64_t to = Tile<D, NT>::row(a, s, tile, int(head), row / 8, row % 2, row % 8 / 2, lo, hi);
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+    waited = true;
     __syncthreads();
-    for (int item = threadIdx.x; item < kItems; item += kJoin) {
-      const int row = 4 * item / D, col = 4 * item % D;
-      int lo, hi;
-      const int64_t to = Tile<D, NT>::row(a, s, tile, int(head), row / 8, row % 2, row % 8 / 2, lo, hi);
-      if (to < 0) continue;
-      float m = -INFINITY, l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int p = 0; p < parts; ++p) m = fmaxf(m, a.part_ml[s_place[p] + row].x);
-      const float from = m == -INFINITY ? 0.f : m;
-#pragma unroll 8
-      for (int p = 0; p < parts; ++p) {
-        const float2 ml = a.part_ml[s_place[p] + row];
-        const float4 x = *reinterpret_cast<const float4*>(a.part + int64_t(s_place[p] + row) * D + col);
-        const float f = exp2_approx(ml.x - from);
-        l += ml.y * f;
-        o.x += x.x * f;
-        o.y += x.y * f;
-        o.z += x.z * f;
-        o.w += x.w * f;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (to >= 0) {  // others have left nothing there
+      for (int p0 = group; p0 < parts; p0 += kGroups * kAtOnce) {
+        float2 ml[kAtOnce];
+        float4 x[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const int p = p0 + k * kGroups;
+          ml[k] = make_float2(-INFINITY, 0.f);
+          x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (p < parts) {
+            ml[k] = a.part_ml[s_place[p] + row];
+            x[k] = *reinterpret_cast<const float4*>(a.part + int64_t(s_place[p] + row) * D + col);
+          }
+        }
+        float next = m;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) next = fmaxf(next, ml[k].x);
+        const float from = next == -INFINITY ? 0.f : next, down = exp2_approx(m - from);
+        m = next;
+        l *= down;
+        o = make_float4(o.x * down, o.y * down, o.z * down, o.w * down);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const float f = exp2_approx(ml[k].x - from);
+          l += ml[k].y * f;
+          o.x += x[k].x * f;
+          o.y += x[k].y * f;
+          o.z += x[k].z * f;
+          o.w += x[k].w * f;
+        }
       }
+    }
+    if constexpr (kGroups > 1) {
+      s_o[group][item] = o;
+      if (col == 0) s_ml[group][row] = make_float2(m, l);
+      __syncthreads();
+      if (group == 0 && to >= 0) {
+        for (int g = 1; g < kGroups; ++g) m = fmaxf(m, s_ml[g][row].x);
+        const float from = m == -INFINITY ? 0.f : m;
+        l = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int g = 0; g < kGroups; ++g) {
+          const float2 ml = s_ml[g][row];
+          const float4 x = s_o[g][item];
+          const float f = exp2_approx(ml.x - from);
+          l += ml.y * f;
+          o = make_float4(o.x + x.x * f, o.y + x.y * f, o.z + x.z * f, o.w + x.w * f);
+        }
+      }
+    }
+    if (group == 0 && to >= 0) {
       const float f = l == 0.f ? 0.f : 1.f / l;
       *reinterpret_cast<uint2*>(a.out + to * D + col) = make_uint2(bf16x2_bits(o.x * f, o.y * f), bf16x2_bits(o.z * f, o.w * f));
       if (col == 0) store_lse(a, to, m, l);
     }
+    __syncthreads();
   }
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // A tile and head by one block, or by a cluster of up to 16: every warp takes every
@@ -1035,7 +1079,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(con
   const uint32_t magic = q4_magic();
   Ring<Src, kDepth> ring(smem + uint32_t(warp) * kDepth * Src::kStage,
                          smem + kWarps * kDepth * Src::kStage + uint32_t(warp) * kDepth * 8, a.s.err, lane);
-  sum_units<kThreads, R, false>(a, s_before, s_warp, nullptr);
+  sum_units<kThreads, R, false>(a, s_before, s_warp);
   const Runs runs{s_before[kThreads], a.warps};
   uint64_t u = runs.first(blockIdx.x * kWarps + uint32_t(warp));
   const uint64_t end = runs.first(blockIdx.x * kWarps + uint32_t(warp) + 1);
@@ -1193,7 +1237,7 @@ template <int D, int NT>
 int attend(AttendArgs& a, int dev, cudaStream_t s) {
   constexpr int kThreads = Shape<D, NT>::kThreads;
   constexpr uint32_t smem = Shape<D, NT>::kSmem;
-  const uint32_t sms = uint32_t(std::min(sm_count(dev), kJoin - 2));  // a part a block, and two
+  const uint32_t sms = uint32_t(std::min(sm_count(dev), kMaxParts - 2));  // a part a block, and two
   int wide = 0;
   cudaError_t e = prepare<D, NT>(dev, &wide);
   if (e != cudaSuccess) return map_cuda(e);
@@ -1204,23 +1248,27 @@ int attend(AttendArgs& a, int dev, cudaStream_t s) {
   a.warps = sms * Shape<D, NT>::kWarps;
   auto up = [](uint64_t x) { return (x + 255) & ~uint64_t(255); };
   const uint64_t slots = team ? 0 : uint64_t(2) * a.warps * 8 * NT;
-  const uint64_t b_prefix = team ? 0 : up((uint64_t(a.s.B) + 1) * 8),
-                 b_lse = a.mass ? up(uint64_t(a.T) * a.q_heads * 4) : 0, b_ml = up(slots * 8), b_part = slots * D * 4;
+  const uint64_t b_lse = a.mass ? up(uint64_t(a.T) * a.q_heads * 4) : 0, b_ml = up(slots * 8), b_part = slots * D * 4;
   uint8_t* ws = nullptr;
-  if (b_prefix + b_lse + b_ml + b_part) {
-    e = pool_alloc(reinterpret_cast<void**>(&ws), b_prefix + b_lse + b_ml + b_part, s);
+  if (b_lse + b_ml + b_part) {
+    e = pool_alloc(reinterpret_cast<void**>(&ws), b_lse + b_ml + b_part, s);
     if (e != cudaSuccess) return map_cuda(e);
   }
-  a.prefix = reinterpret_cast<uint64_t*>(ws);
-  a.lse2 = reinterpret_cast<float*>(ws + b_prefix);
-  a.part_ml = reinterpret_cast<float2*>(ws + b_prefix + b_lse);
-  a.part = reinterpret_cast<float*>(ws + b_prefix + b_lse + b_ml);
+  a.lse2 = reinterpret_cast<float*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + b_lse);
+  a.part = reinterpret_cast<float*>(ws + b_lse + b_ml);
   if (team) {
     e = launch(kv4_attend_team_kernel<D, NT>, uint32_t(tiles * a.s.heads) * team, kThreads, smem, false, team, s, a, team);
   } else {
     e = launch(kv4_attend_kernel<D, NT>, sms, kThreads, smem, false, 1, s, a);
-    const uint32_t joins = uint32_t(std::min<int64_t>(tiles * a.s.heads, int64_t(sms) * 64));
-    if (e == cudaSuccess) e = launch(kv4_join_kernel<D, NT>, joins, kJoin, 0, true, 1, s, a, tiles);
+    // few tiles have many parts: 1024 threads share them (one sequence of 262143 tokens,
+    // 8 heads: 12 -> 4 us); many have two or three
+    constexpr int kSmall = 8 * NT * D / 4 < 256 ? 256 : 8 * NT * D / 4;
+    const int64_t joins = tiles * a.s.heads;
+    if (e == cudaSuccess)
+      e = joins <= sms ? launch(kv4_join_kernel<D, NT, 1024>, uint32_t(joins), 1024, 0, true, 1, s, a, tiles)
+                       : launch(kv4_join_kernel<D, NT, kSmall>, uint32_t(std::min<int64_t>(joins, int64_t(sms) * 4)), kSmall,
+                                0, true, 1, s, a, tiles);
   }
   if (e == cudaSuccess && a.mass) e = launch(kv4_mass_kernel<D, NT>, sms, kThreads, smem, true, 1, s, a);
   if (ws) cudaFreeAsync(ws, s);
