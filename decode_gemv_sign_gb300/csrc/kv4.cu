@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(kChoose, 2) kv4_choose_kernel(EvictArgs a, uin
   };
 #pragma unroll
   for (int k = 0; k < kHeld; ++k) held[k] = load(k);
+#pragma unroll 8
   for (int k = kHeld; k < min(steps, kHeld + kShared); ++k) sh.keys[k - kHeld][tid] = load(k);
   auto key_at = [&](int k) {  // beyond the registers
     return k < kHeld + kShared ? sh.keys[k - kHeld][tid] : load(k);
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(kChoose, 2) kv4_choose_kernel(EvictArgs a, uin
   }
   const uint32_t ties = some ? uint32_t(m) - taken : 0u;  // of the equal ones, the first `ties`
   uint32_t seen = before[1], place = before[0] + min(before[1], ties);
-  auto emit = [&](int i, uint32_t k) {
+  auto emit = [&](int i, uint32_t k, float x) {
     const bool in = i < min(i1, n0) && some;
     const bool tie = in && k == key;
     const uint32_t tied = __ballot_sync(0xffffffffu, tie), lower = (1u << lane) - 1u;
@@ -403,15 +404,33 @@ __global__ void __launch_bounds__(kChoose, 2) kv4_choose_kernel(EvictArgs a, uin
     if (take) {
       const uint32_t to = place + __popc(takes & lower);
       kept[to] = i;
-      mass_out[to] = mass[i];
+      mass_out[to] = x;
     }
     seen += __popc(tied);
     place += __popc(takes);
   };
+  // eight masses at a time, before what is done with them waits for the first
+  float x[8];
+  auto masses = [&](int k) {
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k)
-    if (k < steps) emit(i0 + 32 * k + int(lane), held[k]);
-  for (int k = kHeld; k < steps; ++k) emit(i0 + 32 * k + int(lane), key_at(k));
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + 32 * (k + j) + int(lane);
+      x[j] = i < i1 ? mass[i] : 0.f;
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; k += 8)
+    if (k < steps) {
+      masses(k);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) emit(i0 + 32 * (k + j) + int(lane), held[k + j], x[j]);
+    }
+  for (int k = kHeld; k < steps; k += 8) {
+    masses(k);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (k + j < steps) emit(i0 + 32 * (k + j) + int(lane), key_at(k + j), x[j]);
+  }
   for (int i = m + int(rank * kChoose + tid); i < a.keep; i += int(team * kChoose)) kept[i] = -1;
   for (int i = m + int(rank * kChoose + tid); i < a.width_out * kPage; i += int(team * kChoose)) mass_out[i] = 0.f;
   if (team > 1) team_sync();  // a block's shared memory stays while others read it

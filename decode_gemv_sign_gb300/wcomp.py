@@ -659,12 +659,19 @@ def kv4_create(pages: int, heads: int, dim: int, stream=None) -> KV4:
     return KV4(h.value, pages, heads, dim, torch.device("cuda", torch.cuda.current_device()))
 
 
+def _stream_of(stream, device: torch.device) -> int:
+    """``stream``, or the current one of that device."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device.index)
+    return _stream(stream)
+
+
 def _array(t: torch.Tensor, what: str, dtype: torch.dtype, shape: tuple, device: torch.device) -> int:
     """The address of a contiguous tensor of that type and shape on that device."""
-    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype or not t.is_contiguous() \
-            or t.shape != shape:
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {list(shape)} on {device}")
-    return t.data_ptr()
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device \
+            and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {list(shape)} on {device}")
 
 
 def _kv4_seqs(c: KV4, table: torch.Tensor, lengths: torch.Tensor, starts: Optional[torch.Tensor]) -> Kv4Seqs:
@@ -695,7 +702,7 @@ def kv4_append(c: KV4, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, le
     T = k.shape[0]
     if v.shape[0] != T or (starts is None and T != s.B):
         raise ValueError("k and v must have the same rows, one a sequence without starts")
-    _check(lib().wcomp_kv4_append(c.handle, ctypes.byref(s), *kp, *vp, T, _stream(stream)), "wcomp_kv4_append")
+    _check(lib().wcomp_kv4_append(c.handle, ctypes.byref(s), *kp, *vp, T, _stream_of(stream, c.device)), "wcomp_kv4_append")
 
 
 def kv4_read(c: KV4, table: torch.Tensor, lengths: torch.Tensor, starts: Optional[torch.Tensor] = None, *,
@@ -717,7 +724,7 @@ def kv4_read(c: KV4, table: torch.Tensor, lengths: torch.Tensor, starts: Optiona
     shape = (rows, c.heads, c.dim)
     k, v = (torch.empty(shape, dtype=torch.bfloat16, device=c.device) if t is None else t for t in (k, v))
     _check(lib().wcomp_kv4_read(c.handle, ctypes.byref(s), _array(_bits16(k, "k"), "k", k.dtype, shape, c.device),
-                                _array(_bits16(v, "v"), "v", v.dtype, shape, c.device), rows, _stream(stream)),
+                                _array(_bits16(v, "v"), "v", v.dtype, shape, c.device), rows, _stream_of(stream, c.device)),
            "wcomp_kv4_read")
     return k, v
 
@@ -745,7 +752,7 @@ def kv4_attend(c: KV4, q: torch.Tensor, table: torch.Tensor, lengths: torch.Tens
                       None if mass is None else _array(mass, "mass", torch.float32, (s.B, c.heads, s.width * 64),
                                                        c.device),
                       T, Hq, window, c.dim ** -0.5 if scale is None else scale)
-    _check(lib().wcomp_kv4_attend(c.handle, ctypes.byref(a), _stream(stream)), "wcomp_kv4_attend")
+    _check(lib().wcomp_kv4_attend(c.handle, ctypes.byref(a), _stream_of(stream, c.device)), "wcomp_kv4_attend")
     return out
 
 
@@ -775,7 +782,7 @@ def kv4_evict(c: KV4, table: torch.Tensor, lengths: torch.Tensor, mass: torch.Te
                      _array(mass_out, "mass_out", torch.float32, (s.B, c.heads, wide * 64), c.device),
                      None if kept is None else _array(kept, "kept", torch.int32, (s.B, c.heads, keep), c.device),
                      s.B, s.width, wide, keep, recent)
-    _check(lib().wcomp_kv4_evict(c.handle, ctypes.byref(a), _stream(stream)), "wcomp_kv4_evict")
+    _check(lib().wcomp_kv4_evict(c.handle, ctypes.byref(a), _stream_of(stream, c.device)), "wcomp_kv4_evict")
     return lengths_out, mass_out
 
 
@@ -785,8 +792,8 @@ def logprobs(logits: torch.Tensor, ids: Optional[torch.Tensor] = None, top_k: in
 
     ``logits`` are float32 (what ``gemv`` gives) or bfloat16, a row's columns contiguous; ``ids`` (int64 [T]) are
     the given tokens: a negative one gets logprob 0, one beyond the vocabulary NaN.  logprob is None without
-    ids.  ``top_k`` (at most 64) alternatives, the largest first, ties by the lowest index; ids are int32.
-    ``lse`` (float32 [T]) receives the log of the sum of exponentials.
+    ids.  ``top_k`` (at most 64) alternatives, the largest first, ties by the lowest index; ids are int32; both are
+    None for 0.  ``lse`` (float32 [T]) receives the log of the sum of exponentials.
     """
     if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
         raise TypeError("logits must be a CUDA tensor")
@@ -797,17 +804,21 @@ def logprobs(logits: torch.Tensor, ids: Optional[torch.Tensor] = None, top_k: in
     if top_k < 0 or top_k > logits.shape[1]:
         raise ValueError("top_k must be within 0..V")
     (T, V), dev = logits.shape, logits.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError("logits must be on the current device")
     row = logits.stride(0) if T > 1 else V
     entropy = torch.empty(T, dtype=torch.float32, device=dev)
     logprob = None if ids is None else torch.empty(T, dtype=torch.float32, device=dev)
-    top = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    top_ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    top = top_ids = None
+    if top_k:
+        top = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        top_ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
     a = LogprobsArgs(logits.data_ptr(), None if ids is None else _array(ids, "ids", torch.int64, (T,), dev),
                      None if ids is None else logprob.data_ptr(), entropy.data_ptr(),
                      None if lse is None else _array(lse, "lse", torch.float32, (T,), dev),
                      top.data_ptr() if top_k else None, top_ids.data_ptr() if top_k else None, T, V, row,
                      0 if logits.dtype == torch.float32 else 1, top_k, scale)
-    _check(lib().wcomp_logprobs(ctypes.byref(a), _stream(stream)), "wcomp_logprobs")
+    _check(lib().wcomp_logprobs(ctypes.byref(a), _stream_of(stream, dev)), "wcomp_logprobs")
     return logprob, entropy, top, top_ids
 
 
