@@ -13,18 +13,23 @@
 // of its batches (up to 32 buckets) in shared memory.  If each of the eight warps
 // has ceil(k / 8) threads whose largest element is at least t, the k-th largest
 // element of the block's part is at least t; only buckets that may hold an element
-// of at least t are read again, some 2 k of 8192 in ordinary rows.
+// of at least t are read again, some 2 k of 8192 in ordinary rows, eight at a time.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
 
-#include "wcomp_impl.cuh"
+#include "pairs.cuh"
 
 namespace wc {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kVecs = 4;       // vectors of a batch
+// Vectors of a batch and blocks an SM: 1024 rows of 151552 fp32 logits, top 20, at 4
+// and 4 118, at 6 and 3 112 us; BF16 87 and 100 us.
+template <bool BF16>
+struct Batch {
+  static constexpr int kVecs = BF16 ? 4 : 6, kBlocks = BF16 ? 4 : 3;
+};
 constexpr int kBuckets = 32;
 constexpr int kMaxTop = 64;
 constexpr int kMaxTeam = 8;    // blocks that share a row
@@ -58,6 +63,11 @@ __device__ __forceinline__ uint64_t logit_key(float x, uint32_t i) {
   return uint64_t(k) << 32 | uint32_t(~i);
 }
 
+__device__ __forceinline__ float key_logit(uint64_t key) {
+  const uint32_t k = uint32_t(key >> 32);
+  return k == 0 ? NAN : __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -69,9 +79,9 @@ __device__ __forceinline__ float max_nan(float x, float y) {
   return z;
 }
 __device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int d = 16; d; d /= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-  return x;
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -126,40 +136,84 @@ __device__ __forceinline__ void st_cluster(uint32_t a, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 
-// A warp's largest keys, two a lane, in no order.
-struct Best {
-  uint64_t key[2] = {0, 0}, least = 0;  // least: below it nothing enters
-  __device__ __forceinline__ void offer(uint64_t k, int keep, int lane) {
-    for (uint32_t who; (who = __ballot_sync(0xffffffffu, k > least)) != 0;) {
-      const int from = __ffs(int(who)) - 1;
-      const uint64_t x = __shfl_sync(0xffffffffu, k, from);
-      if (lane == from) k = 0;
-      // takes the place of the least of `keep` places
-      const bool second = lane + 32 < keep;
-      uint64_t mine = lane < keep ? key[0] : ~uint64_t(0);
-      if (second && key[1] < mine) mine = key[1];
-      const uint64_t low = ~warp_max64(~mine);
-      const int at = __ffs(int(__ballot_sync(0xffffffffu, mine == low))) - 1;
-      if (lane == at) {
-        if (key[0] == low) key[0] = x;
-        else key[1] = x;
-      }
-      mine = lane < keep ? key[0] : ~uint64_t(0);
-      if (second && key[1] < mine) mine = key[1];
-      const uint64_t now = ~warp_max64(~mine);
-      if (now > least) least = now;
-    }
-  }
-};
+constexpr int kList = 128;   // candidates of a warp
+constexpr int kLook = 64;    // buckets that it reads again at once
 
 struct Shared {
   float top[kBuckets][kThreads];  // largest element of a thread's bucket
   Stats stats[kWarps > kMaxTeam ? kWarps : kMaxTeam];
-  uint64_t list[kWarps * kMaxTop];
+  uint64_t list[kWarps * kList];   // a warp's candidates; then all of them, or the cluster's
   uint64_t found[kMaxTop];
+  uint16_t buckets[kWarps][kLook]; // bucket and lane of those a warp reads again
   uint64_t bound[kWarps];
-  uint32_t count;
+  uint32_t counts[kWarps];         // candidates of each warp
 };
+
+// Where the elements of a block's part are.
+struct Part {
+  const uint8_t* z;
+  uint32_t head, v0, v1, group, buckets;
+};
+template <bool BF16>
+__device__ __forceinline__ uint64_t part_key(const Part& p, uint32_t bucket, uint32_t owner, uint32_t e) {
+  constexpr uint32_t E = BF16 ? 8 : 4, kVecs = Batch<BF16>::kVecs;
+  const uint32_t v = p.v0 + (bucket * p.group * kVecs + e / E) * kThreads + owner;
+  if (e >= p.group * kVecs * E || v >= p.v1) return 0;
+  const uint32_t i = p.head + v * E + e % E;
+  return logit_key(logit<BF16>(p.z, i), i);
+}
+// No element of the thread's bucket is larger than this.
+template <bool BF16>
+__device__ __forceinline__ uint64_t bucket_key(const Part& p, const Shared& sh, uint32_t bucket) {
+  constexpr uint32_t kVecs = Batch<BF16>::kVecs;
+  return logit_key(sh.top[bucket][threadIdx.x],
+                   p.head + (p.v0 + bucket * p.group * (kThreads * kVecs) + threadIdx.x) * (BF16 ? 8 : 4));
+}
+
+// A warp's `keep` largest, where more elements than the lists take come into
+// question (rows with few different values, or almost all masked): one bucket after
+// the other, the list cut back whenever it is full.  Returns how many there are.
+template <bool BF16>
+__device__ __noinline__ uint32_t search_all(const Part& p, Shared& sh, uint64_t least, int keep) {
+  constexpr uint32_t kVecs = Batch<BF16>::kVecs;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint64_t* const list = sh.list + warp * kList;
+  int count = 0;
+#pragma unroll 1
+  for (uint32_t b = 0; b < p.buckets; ++b) {
+#pragma unroll 1
+    for (uint32_t who = __ballot_sync(0xffffffffu, bucket_key<BF16>(p, sh, b) > least); who; who &= who - 1) {
+#pragma unroll 1
+      for (uint32_t e = lane; e - lane < p.group * kVecs * (BF16 ? 8 : 4); e += 32) {
+        const uint64_t k = part_key<BF16>(p, b, uint32_t(warp * 32 + __ffs(int(who)) - 1), e);
+        const uint32_t some = __ballot_sync(0xffffffffu, k > least);
+        if (k > least) list[count + __popc(some & ((1u << lane) - 1u))] = k;
+        count += __popc(some);
+        __syncwarp();
+        if (count <= kList - 32) continue;
+        uint64_t mine[kList / 32];
+        int rank[kList / 32] = {};
+#pragma unroll
+        for (int i = 0; i < kList / 32; ++i) mine[i] = lane + 32 * i < count ? list[lane + 32 * i] : 0;
+#pragma unroll 1
+        for (int j = 0; j < count; ++j) {
+          const uint64_t x = list[j];
+#pragma unroll
+          for (int i = 0; i < kList / 32; ++i) rank[i] += x > mine[i];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kList / 32; ++i)
+          if (mine[i] && rank[i] < keep) list[rank[i]] = mine[i];
+        __syncwarp();
+        count = min(count, keep);
+        if (list[keep - 1] > least) least = list[keep - 1];
+        __syncwarp();
+      }
+    }
+  }
+  return uint32_t(count);
+}
 
 // The `keep` largest of list[0 .. n), descending, to found; what is missing is 0.
 __device__ __forceinline__ void rank_list(Shared& sh, int n, int keep) {
@@ -176,8 +230,9 @@ __device__ __forceinline__ void rank_list(Shared& sh, int n, int keep) {
 }
 
 template <bool BF16, bool TOP>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_constant__ LogprobArgs a, uint32_t team) {
+__global__ void __launch_bounds__(kThreads, Batch<BF16>::kBlocks) logprobs_kernel(const __grid_constant__ LogprobArgs a, uint32_t team) {
   constexpr int E = BF16 ? 8 : 4;  // elements of a vector
+  constexpr int kVecs = Batch<BF16>::kVecs;
   __shared__ Shared sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t rank = team > 1 ? cluster_rank() : 0;
@@ -193,6 +248,13 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   const uint32_t group = (rounds + kBuckets - 1) / kBuckets;  // batches of a bucket
   const uint8_t* zv = z + head * (BF16 ? 2 : 4);
 
+  // the given token's logit, long before it is wanted
+  int64_t id = -1;
+  float given = NAN;
+  if (a.ids && threadIdx.x == 0 && rank == 0) {
+    id = a.ids[t];
+    if (id >= 0 && id < a.V) given = logit<BF16>(z, id);
+  }
   Stats st{-INFINITY, 0.f, 0.f, 0.f};
   float from = 0.f;  // m, but 0 while there is no element above -inf
   // Add a batch of N elements; `most`: their largest.
@@ -205,7 +267,21 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
       st.raise(all, c);
       from = all;
     }
-    if (all < st.m || st.m == -INFINITY) {
+    if (N % 2 == 0 && (all < st.m || st.m == -INFINITY)) {
+      // two elements an instruction, in two sums
+      const uint64_t minus = pair(-from, -from), c2 = pair(c, c);
+      uint64_t s2 = pair(st.s, 0.f), w2 = pair(st.w, 0.f);
+#pragma unroll
+      for (int i = 0; i + 1 < N; i += 2) {
+        const uint64_t x = mul2(add2(pair(get(i), get(i + 1)), minus), c2);
+        const uint64_t d = pair(max_nan(first(x), -200.f), max_nan(second(x), -200.f));
+        const uint64_t e = pair(exp2_approx(first(d)), exp2_approx(second(d)));
+        s2 = add2(s2, e);
+        w2 = fma2(e, d, w2);
+      }
+      st.s = first(s2) + second(s2);
+      st.w = first(w2) + second(w2);
+    } else if (all < st.m || st.m == -INFINITY) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float d = below(get(i)), e = exp2_approx(d);
@@ -294,37 +370,65 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     __syncthreads();
     uint64_t bound = sh.bound[0];
     for (int w = 1; w < kWarps; ++w) bound = min(bound, sh.bound[w]);
-    Best mostly;
-    mostly.least = bound ? bound - 1 : 0;
-    const uint32_t buckets = group ? (rounds + group - 1) / group : 0;
-    for (uint32_t b = 0; b < buckets; ++b) {
-      // no element of the bucket is larger than this
-      const uint32_t low = head + (v0 + b * group * (kThreads * kVecs) + threadIdx.x) * E;
-      uint32_t who = __ballot_sync(0xffffffffu, logit_key(sh.top[b][threadIdx.x], low) > mostly.least);
-      for (; who; who &= who - 1) {
-        const uint32_t owner = uint32_t(warp) * 32 + uint32_t(__ffs(int(who))) - 1;
-        const uint32_t n = group * kVecs * E;
-        for (uint32_t e0 = 0; e0 < n; e0 += 32) {
-          const uint32_t e = e0 + lane, v = v0 + (b * group * kVecs + e / E) * kThreads + owner;
-          uint64_t k = 0;
-          if (e < n && v < v1) {
-            const uint32_t i = head + v * E + e % E;
-            k = logit_key(logit<BF16>(z, i), i);
-          }
-          mostly.offer(k, keep, lane);
+    const uint64_t least = bound ? bound - 1 : 0;
+    const Part part{z, head, v0, v1, group, group ? (rounds + group - 1) / group : 0};
+    uint64_t* const list = sh.list + warp * kList;
+    if (lane == 0) sh.counts[warp] = 0;
+    uint32_t listed = 0;
+    for (uint32_t b = 0; b < part.buckets; ++b) {
+      const bool look = bucket_key<BF16>(part, sh, b) > least;
+      const uint32_t who = __ballot_sync(0xffffffffu, look), at = listed + __popc(who & ((1u << lane) - 1u));
+      if (look && at < kLook) sh.buckets[warp][at] = uint16_t(b * 32 + lane);
+      listed += __popc(who);
+    }
+    __syncwarp();
+    for (uint32_t b0 = 0; b0 < min(listed, uint32_t(kLook)); b0 += 8)
+      for (uint32_t e0 = 0; e0 < group * kVecs * E; e0 += 32) {
+        uint64_t k[8];
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) {
+          const uint32_t which = sh.buckets[warp][min(b0 + j, listed - 1)];
+          k[j] = b0 + j < listed ? part_key<BF16>(part, which / 32, uint32_t(warp) * 32 + which % 32, e0 + lane) : 0;
         }
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j)
+          if (k[j] > least) {
+            const uint32_t at = atomicAdd(&sh.counts[warp], 1u);  // in any order: they are ranked later
+            if (at < kList) list[at] = k[j];
+          }
+      }
+    if (uint32_t(warp) * 32 < edges && threadIdx.x < edges) {
+      const uint64_t k = logit_key(edge_x, edge);
+      const uint32_t at = k > least ? atomicAdd(&sh.counts[warp], 1u) : kList;
+      if (at < kList) list[at] = k;
+    }
+    __syncwarp();
+    uint32_t count = sh.counts[warp];
+    if (listed > kLook || count > kList) {
+      count = search_all<BF16>(part, sh, least, keep);
+      // the first warp's edges: the list has room for them
+      if (uint32_t(warp) * 32 < edges) {
+        if (threadIdx.x < edges) list[count + threadIdx.x] = logit_key(edge_x, edge);
+        count += edges;
       }
     }
-    if (uint32_t(warp) * 32 < edges)
-      mostly.offer(threadIdx.x < edges ? logit_key(edge_x, edge) : 0, keep, lane);
-    // the warps' keys together, those that are there
-    if (threadIdx.x == 0) sh.count = 0;
-    __syncthreads();
+    // the warps' candidates one behind the other
+    __syncwarp();
+    uint64_t mine4[kList / 32];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (mostly.key[i]) sh.list[atomicAdd(&sh.count, 1u)] = mostly.key[i];
+    for (int i = 0; i < kList / 32; ++i) mine4[i] = uint32_t(lane + 32 * i) < count ? list[lane + 32 * i] : 0;
+    if (lane == 0) sh.counts[warp] = count;
     __syncthreads();
-    rank_list(sh, int(sh.count), keep);
+    int before = 0, all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += int(sh.counts[w]);
+      all += int(sh.counts[w]);
+    }
+#pragma unroll
+    for (int i = 0; i < kList / 32; ++i)
+      if (uint32_t(lane + 32 * i) < count) sh.list[before + lane + 32 * i] = mine4[i];
+    __syncthreads();
+    rank_list(sh, all, keep);
   }
 
   if (team > 1) {
@@ -351,16 +455,12 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
   if (threadIdx.x == 0) {
     if (a.lse) a.lse[t] = st.m * a.scale + log_sum;
     if (a.entropy) a.entropy[t] = log_sum - st.w * kLn2 / (1.f + rest);
-    if (a.ids) {
-      const int64_t id = a.ids[t];
-      a.logprob[t] = id < 0 ? 0.f : id >= a.V ? NAN : (logit<BF16>(z, id) - st.m) * a.scale - log_sum;
-    }
+    if (a.ids) a.logprob[t] = id < 0 ? 0.f : (given - st.m) * a.scale - log_sum;
   }
   if constexpr (TOP) {
     for (int i = threadIdx.x; i < a.top_k; i += kThreads) {
-      const uint32_t id = ~uint32_t(sh.found[i]);
-      a.top_ids[t * a.top_k + i] = int32_t(id);
-      a.top_logprobs[t * a.top_k + i] = (logit<BF16>(z, id) - st.m) * a.scale - log_sum;
+      a.top_ids[t * a.top_k + i] = int32_t(~uint32_t(sh.found[i]));
+      a.top_logprobs[t * a.top_k + i] = (key_logit(sh.found[i]) - st.m) * a.scale - log_sum;
     }
   }
 }
@@ -400,7 +500,7 @@ extern "C" int wcomp_logprobs(const wcomp_logprobs_args* args, void* stream) {
                       a.T,        a.V,      a.row,       a.top_k,     a.scale};
   // blocks share a row while that leaves them a batch each and fits the GPU at once
   uint32_t team = 1;
-  const int64_t batch = int64_t(kThreads) * kVecs * (a.dtype == WCOMP_BF16 ? 8 : 4);
+  const int64_t batch = int64_t(kThreads) * (a.dtype == WCOMP_BF16 ? Batch<true>::kVecs * 8 : Batch<false>::kVecs * 4);
   while (team < kMaxTeam && a.T * team * 2 <= sm_count(dev) * 2 && a.V >= batch * team * 2) team *= 2;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = a.dtype == WCOMP_BF16
