@@ -313,7 +313,11 @@ __global__ void __launch_bounds__(kChoose, 2) kv4_choose_kernel(EvictArgs a, uin
         f(held[k + 2]);
         f(held[k + 3]);
       }
-    for (int k = kHeld; k < steps; ++k) f(key_at(k));
+    const int shared = min(steps, kHeld + kShared);
+#pragma unroll 8
+    for (int k = kHeld; k < shared; ++k) f(sh.keys[k - kHeld][tid]);
+#pragma unroll 4
+    for (int k = shared; k < steps; ++k) f(load(k));
   };
   // the sum of three counts over all tokens
   uint32_t parity = 0;
@@ -362,6 +366,7 @@ __global__ void __launch_bounds__(kChoose, 2) kv4_choose_kernel(EvictArgs a, uin
 #pragma unroll
   for (int k = 0; k < kHeld; ++k)
     if (k < steps) count(i0 + 32 * k + int(lane), held[k]);
+#pragma unroll 8
   for (int k = kHeld; k < steps; ++k) count(i0 + 32 * k + int(lane), key_at(k));
   // sums over the warps before this one, and the number taken above the key
   uint32_t before[2] = {0, 0}, taken;
