@@ -1511,6 +1511,7 @@ extern "C" int wcomp_debug_skip_first_copy(int on) {
   cudaError_t e = cudaMemcpyToSymbol(g_debug_skip_first_copy, &v, sizeof(v));
   if (e == cudaSuccess) e = debug_hooks_q4(uint32_t(on));
   if (e == cudaSuccess) e = debug_hooks_moe(uint32_t(on));
+  if (e == cudaSuccess) e = debug_hooks_kv4(uint32_t(on));
   if (e == cudaSuccess) {
     const cudaError_t e2 = cudaDeviceSynchronize();
     if (e2 != cudaSuccess) return map_cuda(e2);

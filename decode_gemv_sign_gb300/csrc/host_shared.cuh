@@ -6,6 +6,10 @@
 
 namespace wc {
 
+// Whether an array of T begins where a T may (null does).
+template <class T>
+bool natural(const T* p) { return reinterpret_cast<uintptr_t>(p) % alignof(T) == 0; }
+
 // The driver's tensor-map encoder, reached through the runtime (no link against
 // the driver library); null where it is missing.
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -46,8 +50,9 @@ inline cudaError_t stream_state(cudaStream_t s, cudaStreamCaptureStatus* capture
 // cache's calls that was out of range.
 constexpr uint32_t kErrBounds = 2;
 uint32_t* work_error_word(int dev);
-// Debug builds: which test hooks the launches of q4.cu and moe.cu follow.
+// Debug builds: which test hooks the launches of q4.cu, moe.cu and kv4_attend.cu follow.
 cudaError_t debug_hooks_q4(uint32_t bits);
 cudaError_t debug_hooks_moe(uint32_t bits);
+cudaError_t debug_hooks_kv4(uint32_t bits);
 
 }  // namespace wc

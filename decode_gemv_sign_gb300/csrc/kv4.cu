@@ -518,6 +518,7 @@ bool rows_vec(const uint16_t* p, int64_t row, int64_t head) {
 int kv_check(const wcomp_kv4* c, const wcomp_kv4_seqs& s, int64_t T) {
   if (!c || s.B < 0 || s.width < 1 || T < 0 || (s.B && (!s.d_table || !s.d_lengths))) return WCOMP_EINVAL;
   if (!s.d_starts && T != s.B) return WCOMP_EINVAL;
+  if (!natural(s.d_table) || !natural(s.d_lengths) || !natural(s.d_starts)) return WCOMP_EINVAL;
   if (int64_t(s.width) * kPage > (int64_t(1) << 30) || T >= (int64_t(1) << 31)) return WCOMP_EUNSUPPORTED;
   return WCOMP_OK;
 }
@@ -572,7 +573,8 @@ extern "C" int wcomp_kv4_create(int64_t pages, int heads, int dim, void* stream,
 extern "C" int wcomp_kv4_append(wcomp_kv4* c, const wcomp_kv4_seqs* seqs, const uint16_t* d_k, int64_t k_row,
                                 int64_t k_head, const uint16_t* d_v, int64_t v_row, int64_t v_head, int64_t T,
                                 void* stream) {
-  if (!seqs || (T && (!d_k || !d_v)) || k_row < 0 || k_head < 0 || v_row < 0 || v_head < 0) return WCOMP_EINVAL;
+  if (!seqs || (T && (!d_k || !d_v)) || k_row < 0 || k_head < 0 || v_row < 0 || v_head < 0 || !natural(d_k) || !natural(d_v))
+    return WCOMP_EINVAL;
   int st = kv_check(c, *seqs, T);
   if (st != WCOMP_OK) return st;
   KvSeqs s;
@@ -593,7 +595,7 @@ extern "C" int wcomp_kv4_append(wcomp_kv4* c, const wcomp_kv4_seqs* seqs, const 
 
 extern "C" int wcomp_kv4_read(const wcomp_kv4* c, const wcomp_kv4_seqs* seqs, uint16_t* d_k, uint16_t* d_v, int64_t T,
                               void* stream) {
-  if (!seqs || (T && (!d_k || !d_v))) return WCOMP_EINVAL;
+  if (!seqs || (T && (!d_k || !d_v)) || !natural(d_k) || !natural(d_v)) return WCOMP_EINVAL;
   int st = kv_check(c, *seqs, T);
   if (st != WCOMP_OK) return st;
   KvSeqs s;
@@ -619,7 +621,10 @@ extern "C" int wcomp_kv4_evict(wcomp_kv4* c, const wcomp_kv4_evict_args* args, v
       int64_t(a.width_out) * kPage < a.keep)
     return WCOMP_EINVAL;
   if (a.B && (!a.d_mass || !a.d_table_out || !a.d_lengths_out || !a.d_mass_out || a.d_mass == a.d_mass_out ||
-              a.d_table == a.d_table_out))
+              a.d_table == a.d_table_out || a.d_lengths == a.d_lengths_out))
+    return WCOMP_EINVAL;
+  if (!natural(a.d_mass) || !natural(a.d_table_out) || !natural(a.d_lengths_out) || !natural(a.d_mass_out) ||
+      !natural(a.d_kept))
     return WCOMP_EINVAL;
   int st = kv_check(c, {a.d_table, a.d_lengths, nullptr, a.B, a.width}, a.B);
   if (st != WCOMP_OK) return st;

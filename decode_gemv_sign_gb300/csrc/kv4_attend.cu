@@ -49,7 +49,8 @@ struct AttendArgs {
   float* lse;   // or null
   float* mass;  // or null
   int64_t T;
-  int q_heads, share, window, q_vec;
+  int q_heads, share, window;
+  int q_vec, out_vec;  // q's rows are 16-byte, out 8-byte aligned
   float scale;
   // workspace
   float* lse2;       // [T, q_heads], in base 2 (with mass)
@@ -574,6 +575,18 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
+// Four columns of a row of out.
+__device__ __forceinline__ void store_out(const AttendArgs& a, int64_t at, const float (&x)[4]) {
+  const uint32_t lo = bf16x2_bits(x[0], x[1]), hi = bf16x2_bits(x[2], x[3]);
+  if (a.out_vec) {
+    *reinterpret_cast<uint2*>(a.out + at) = make_uint2(lo, hi);
+  } else {
+    a.out[at] = uint16_t(lo);
+    a.out[at + 1] = uint16_t(lo >> 16);
+    a.out[at + 2] = uint16_t(hi);
+    a.out[at + 3] = uint16_t(hi >> 16);
+  }
+}
 __device__ __forceinline__ void store_lse(const AttendArgs& a, int64_t row, float m, float l) {
   const float y = m + log2f(l);  // -inf where nothing is seen
   if (a.lse) a.lse[row] = y * kLn2;
@@ -684,8 +697,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
 #pragma unroll
           for (int k = 0; k < 4; ++k) x[k] = x[k] * back * f;
           if (whole)
-            *reinterpret_cast<uint2*>(a.out + row * D + 32 * i + 4 * r) =
-                make_uint2(bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3]));
+            store_out(a, row * D + 32 * i + 4 * r, x);
           else
             *reinterpret_cast<float4*>(part + (8 * n + 2 * q + e) * D + 32 * i + 4 * r) =
                 make_float4(x[0], x[1], x[2], x[3]);
@@ -878,7 +890,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv4_join_kernel(const
     }
     if (group == 0 && to >= 0) {
       const float f = l == 0.f ? 0.f : 1.f / l;
-      *reinterpret_cast<uint2*>(a.out + to * D + col) = make_uint2(bf16x2_bits(o.x * f, o.y * f), bf16x2_bits(o.z * f, o.w * f));
+      const float x[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
+      store_out(a, to * D + col, x);
       if (col == 0) store_lse(a, to, m, l);
     }
     __syncthreads();
@@ -1276,6 +1289,8 @@ int attend(AttendArgs& a, int dev, cudaStream_t s) {
 }
 
 }  // namespace
+
+WCOMP_DEBUG_HOOKS(debug_hooks_kv4)
 }  // namespace wc
 
 using namespace wc;
@@ -1286,7 +1301,8 @@ extern "C" int wcomp_kv4_attend(const wcomp_kv4* c, const wcomp_kv4_attend_args*
   int st = kv_check(c, a.s, a.T);
   if (st != WCOMP_OK) return st;
   if (a.q_heads < 1 || a.q_heads % c->heads || a.window < 0 || !std::isfinite(a.scale) || a.q_row < 0 || a.q_head < 0 ||
-      (a.T && (!a.d_q || !a.d_out || a.d_out == a.d_q)))
+      (a.T && (!a.d_q || !a.d_out || a.d_out == a.d_q)) || !natural(a.d_q) || !natural(a.d_out) || !natural(a.d_lse) ||
+      !natural(a.d_mass))
     return WCOMP_EINVAL;
   if (a.T * a.q_heads >= (int64_t(1) << 31)) return WCOMP_EUNSUPPORTED;
   AttendArgs p{};
@@ -1299,6 +1315,7 @@ extern "C" int wcomp_kv4_attend(const wcomp_kv4* c, const wcomp_kv4_attend_args*
   p.q_head = a.q_head;
   p.q_vec = reinterpret_cast<uintptr_t>(a.d_q) % 16 == 0 && a.q_row % 8 == 0 && a.q_head % 8 == 0;
   p.out = a.d_out;
+  p.out_vec = reinterpret_cast<uintptr_t>(a.d_out) % 8 == 0;
   p.lse = a.d_lse;
   p.mass = a.d_mass;
   p.T = a.T;

@@ -18,6 +18,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "host_shared.cuh"
 #include "pairs.cuh"
 
 namespace wc {
@@ -491,6 +492,9 @@ extern "C" int wcomp_logprobs(const wcomp_logprobs_args* args, void* stream) {
   if (a.T < 0 || a.V < 1 || a.row < a.V || (a.dtype != WCOMP_FP32 && a.dtype != WCOMP_BF16) || a.top_k < 0 ||
       a.top_k > a.V || !(a.scale > 0.f) || !std::isfinite(a.scale) || (a.T && !a.d_logits) ||
       (a.T && a.top_k && (!a.d_top_logprobs || !a.d_top_ids)) || (a.T && a.d_ids && !a.d_logprob))
+    return WCOMP_EINVAL;
+  if (reinterpret_cast<uintptr_t>(a.d_logits) % (a.dtype == WCOMP_BF16 ? 2 : 4) || !natural(a.d_ids) || !natural(a.d_logprob) ||
+      !natural(a.d_entropy) || !natural(a.d_lse) || !natural(a.d_top_logprobs) || !natural(a.d_top_ids))
     return WCOMP_EINVAL;
   if (a.top_k > kMaxTop || a.V >= (int64_t(1) << 31) || a.T >= (int64_t(1) << 28)) return WCOMP_EUNSUPPORTED;
   if (a.T == 0) return WCOMP_OK;

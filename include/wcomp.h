@@ -260,8 +260,8 @@ WCOMP_API int wcomp_device_check(void* stream);
 /*
  * Test hooks for the bounded waits, in debug builds only (compiled with
  * WCOMP_DEBUG=1).  While `on` has bit 0 set, every warp of a GEMV launch (fused,
- * plain or 4-bit) or of wcomp_moe (but for BF16 experts that no tensor map
- * takes) leaves the first of its tensor copies unissued but still waits for it:
+ * plain or 4-bit), of wcomp_kv4_attend or of wcomp_moe (but for BF16 experts that
+ * no tensor map takes) leaves the first of its tensor copies unissued but still waits for it:
  * the wait runs out after about a second, the warp stops copying and waiting,
  * lets the copies it has in flight land and finishes, and wcomp_device_check
  * then reports WCOMP_ETIMEOUT.  With bit 1 set, the first thread block of
@@ -513,8 +513,10 @@ WCOMP_API int wcomp_moe(const wcomp_moe_args* args, void* stream);
  *     from the library's stream-ordered pool, and is released with wcomp_kv4_free.
  *     Calls that write to it are ordered by the caller against others on it, as
  *     for any buffer.
- *   - Limits: pages * heads and the rows of a call (times the query heads) below
- *     2^31, width * 64 at most 2^30, B * heads of an eviction below 2^28; beyond
+ *   - Arrays begin where their elements may (else WCOMP_EINVAL); no other alignment
+ *     is asked for.
+ *   - Limits: heads below 2^16, pages * heads and the rows of a call (times the query
+ *     heads) below 2^31, width * 64 at most 2^30, B * heads of an eviction below 2^28; beyond
  *     them WCOMP_EUNSUPPORTED.
  * ------------------------------------------------------------------------ */
 typedef struct wcomp_kv4 wcomp_kv4;
@@ -609,7 +611,7 @@ typedef struct {
   const int32_t* d_lengths;   /* [B] */
   const float* d_mass;        /* [B, heads, width * 64] */
   const int32_t* d_table_out; /* [B, width_out], width_out * 64 >= keep: other pages than any in d_table */
-  int32_t* d_lengths_out;     /* [B]: min(length, keep) */
+  int32_t* d_lengths_out;     /* [B]: min(length, keep); not d_lengths */
   float* d_mass_out;          /* [B, heads, width_out * 64]: of what was kept; 0 behind it */
   int32_t* d_kept;            /* [B, heads, keep] or NULL: the positions that were kept, then -1 */
   int32_t B, width, width_out;
@@ -623,7 +625,8 @@ typedef struct {
  * kept is copied bit for bit, in ascending order of its positions, to positions
  * 0, 1, ... of the pages in table_out, each head by its own choice; the old pages
  * are left as they are and may be shared with other sequences.  d_table_out ==
- * d_table is refused; pages that are in both tables leave the results undefined.
+ * d_table and d_lengths_out == d_lengths are refused; pages that are in both tables
+ * leave the results undefined.
  * mass may be mass_out of an earlier call but not of this one.  Asynchronous.
  */
 WCOMP_API int wcomp_kv4_evict(wcomp_kv4* c, const wcomp_kv4_evict_args* args, void* stream);

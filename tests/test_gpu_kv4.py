@@ -364,6 +364,26 @@ def test_a_page_named_twice_by_one_sequence(W):
     attend_matches(W, b, draw((1, 4, 64), np.random.default_rng(1)), [1])
 
 
+@pytest.mark.parametrize("lengths,rows", [([90], [1]), ([9000, 200], [1, 1]), ([3000, 70], [3, 2])])
+def test_unaligned_outputs(W, lengths, rows):
+    """out and q from 2-byte boundaries: the same bits, by each kernel."""
+    b = Batch(W, lengths, 2, 128, seed=8)
+    q = dev16(draw((sum(rows), 8, 128), np.random.default_rng(1)))
+    want = W.kv4_attend(b.cache, q, b.table, b.len, starts_of(rows))
+    for off in (1, 2, 3, 5):
+        flat = torch.full((2 * q.numel() + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+        odd_q, out = flat[off:off + q.numel()].view(q.shape), flat[q.numel() + 32 + off:][:q.numel()].view(q.shape)
+        odd_q.copy_(q)
+        W.kv4_attend(b.cache, odd_q, b.table, b.len, starts_of(rows), out=out)
+        assert torch.equal(out, want)
+        out.fill_(7.0), odd_q.fill_(7.0)
+        assert (flat == 7.0).all()
+    k = torch.empty(sum(lengths) * 256 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(-1, 2, 128)
+    W.kv4_read(b.cache, b.table, b.len, starts_of(lengths), k=k, v=torch.empty_like(k))
+    same_values(bits(k), K.held(b.k))
+    W.device_check()
+
+
 def test_no_rows_and_no_sequences(W):
     b = Batch(W, [10], 2, 64)
     none = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
@@ -467,7 +487,8 @@ def test_the_abi_refuses_bad_arguments_for_a_real_cache(W):
             setattr(x, n, v)
         return x
 
-    for x in (bad(d_table=None), bad(d_lengths=None), bad(B=-1), bad(width=0), bad(B=3)):
+    for x in (bad(d_table=None), bad(d_lengths=None), bad(d_table=s.d_table + 1), bad(d_lengths=s.d_lengths + 2),
+              bad(d_starts=s.d_table + 1), bad(B=-1), bad(width=0), bad(B=3)):
         assert L.wcomp_kv4_append(h, r(x), p, 128, 64, p, 128, 64, 2, None) == W.EINVAL
         assert L.wcomp_kv4_read(h, r(x), p, p, 2, None) == W.EINVAL
         assert L.wcomp_kv4_attend(h, r(W.Kv4AttendArgs(x, p, 128, 64, p, None, None, 2, 2, 0, 1.0)), None) == W.EINVAL
@@ -478,8 +499,9 @@ def test_the_abi_refuses_bad_arguments_for_a_real_cache(W):
     assert L.wcomp_kv4_append(h, None, p, 128, 64, p, 128, 64, 2, None) == W.EINVAL
     assert L.wcomp_kv4_read(h, r(s), None, p, 2, None) == W.EINVAL
     assert L.wcomp_kv4_read(h, r(bad(width=1 << 26)), p, p, 2, None) == W.EUNSUPPORTED
+    f0 = torch.zeros(8, device="cuda").data_ptr()
     ok = (s, p, 128, 64, p + 512, None, None, 2, 2, 0, 1.0)
-    for i, v in ((1, None), (4, p), (2, -1), (3, -1), (4, None), (7, -1), (8, 3), (8, 0), (9, -1), (10, float("nan")),
+    for i, v in ((1, None), (1, p + 1), (4, p), (4, p + 1), (5, f0 + 2), (6, f0 + 2), (2, -1), (3, -1), (4, None), (7, -1), (8, 3), (8, 0), (9, -1), (10, float("nan")),
                  (10, float("inf"))):
         a = list(ok)
         a[i] = v
@@ -488,7 +510,8 @@ def test_the_abi_refuses_bad_arguments_for_a_real_cache(W):
     g = torch.zeros(2, 2, 128, device="cuda").data_ptr()
     out = b.table.clone()
     ev = (s.d_table, s.d_lengths, f, out.data_ptr(), b.len.clone().data_ptr(), g, None, 2, 2, 2, 4, 1)
-    for i, v in ((0, None), (1, None), (2, None), (3, None), (3, s.d_table), (4, None), (5, None), (5, f), (7, -1),
+    for i, v in ((0, None), (1, None), (2, None), (3, None), (3, s.d_table), (4, None), (4, s.d_lengths), (5, None), (5, f),
+                 (0, s.d_table + 2), (2, f + 2), (6, f + 1), (7, -1),
                  (8, 0), (9, 0), (10, 0), (10, 129), (11, -1), (11, 5)):
         a = list(ev)
         a[i] = v
@@ -592,3 +615,36 @@ def test_eviction_into_bad_pages_is_reported(W):
     reported(W)
     same = b.everything()
     same_values(bits(same[0]), K.held(b.k))
+
+
+def test_a_cache_that_finds_no_memory(W):
+    """2^43 bytes are refused, and the next calls are as before."""
+    b = Batch(W, [70], 2, 64, seed=1)
+    q = dev16(draw((1, 4, 64), np.random.default_rng(1)))
+    want = W.kv4_attend(b.cache, q, b.table, b.len)
+    h = ctypes.c_void_p(1)
+    assert W.lib().wcomp_kv4_create((1 << 31) // 2 - 1, 1, 256, None, ctypes.byref(h)) == W.ENOMEM and not h.value
+    assert torch.equal(W.kv4_attend(b.cache, q, b.table, b.len), want)
+    W.device_check()
+
+
+def test_memory_comes_back(W):
+    """Caches made and dropped, calls with workspaces: the device's free memory does not shrink."""
+    def work():
+        b = Batch(W, [3000, 10], 4, 128, seed=1)
+        q = dev16(draw((2, 16, 128), np.random.default_rng(1)))
+        mass = torch.zeros(2, 4, b.width * 64, device="cuda")
+        for _ in range(5):
+            W.kv4_attend(b.cache, q, b.table, b.len, mass=mass)
+            W.kv4_evict(b.cache, b.table, b.len, mass, 10, 2, ints([[b.pages - 1], [b.pages - 2]]))
+        b.cache.free()
+        torch.cuda.synchronize()
+        return torch.cuda.mem_get_info()[0]
+
+    first = [work() for _ in range(3)][-1]
+    assert min(work() for _ in range(20)) >= first - (1 << 20)
+    b = Batch(W, [5], 1, 64)
+    b.cache.free()
+    b.cache.free()  # no-op
+    with pytest.raises(ValueError, match="freed"):
+        b.everything()

@@ -62,6 +62,7 @@ def test_logprobs_argument_errors_without_gpu(lib):
     assert lib.wcomp_logprobs(None, None) == wcomp.EINVAL
     for bad in (dict(d_logits=None), dict(d_logprob=None), dict(T=-1), dict(V=0), dict(row=99), dict(dtype=2),
                 dict(dtype=-1), dict(top_k=-1), dict(top_k=101), dict(d_top_ids=None), dict(d_top_logprobs=None),
+                dict(d_logits=258), dict(d_ids=260), dict(d_logprob=257), dict(d_entropy=258), dict(d_top_ids=258),
                 dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf"))):
         assert lib.wcomp_logprobs(ctypes.byref(logprob_args(**bad)), None) == wcomp.EINVAL, bad
     for bad in (dict(top_k=65), dict(V=1 << 31, row=1 << 31)):
