@@ -173,17 +173,18 @@ struct Runs {
   __device__ __forceinline__ uint32_t of(uint64_t unit) const { return uint32_t(quotient((unit + 1) * W - 1, total)); }
 };
 
-template <int D, bool VALUES>
+// A ring's stage: a block, or half of one.
+template <int D, bool HALF>
 struct KvSrc {
-  static constexpr uint32_t kStage = VALUES ? Kv<D>::kBlock : Kv<D>::kHalf;
+  static constexpr uint32_t kStage = HALF ? Kv<D>::kHalf : Kv<D>::kBlock;
   static constexpr bool kCopies = true;
   typedef const uint8_t* Cursor;
   static __device__ __forceinline__ void issue(Cursor& c, uint32_t st, uint32_t bar) { bulk_copy(st, c, kStage, bar); }
 };
 
-// The blocks (or, without VALUES, their keys) of a warp's units through its ring,
-// ahead of their use.
-template <int D, class RING, class WALK>
+// The blocks of a warp's units through its ring, ahead of their use: a block a stage,
+// their keys alone, or (VALUES) their keys and then their values in stages of halves.
+template <int D, class RING, class WALK, bool VALUES = false>
 struct Pages {
   WALK& it;
   uint64_t left = 0;      // units to come
@@ -192,6 +193,7 @@ struct Pages {
   int base = -1, in = -1; // lane l's id is that of page base + l of sequence `in`
   uint32_t there = 0;     // bit per slot: its page exists
   const uint8_t* head = nullptr;
+  const uint8_t* values = nullptr;
   __device__ __forceinline__ Pages(WALK& walk, uint64_t count) : it(walk), left(count) {}
   __device__ __forceinline__ void enter(const AttendArgs& a, int lane) {
     __syncwarp();
@@ -220,6 +222,11 @@ struct Pages {
   // Copy the next unit's block to `slot`.  A page that does not exist is stood in for
   // by the cache's first, which nothing is read of.
   __device__ __forceinline__ void issue(const AttendArgs& a, RING& ring, uint32_t slot, int lane) {
+    if (VALUES && values) {
+      ring.refill(slot, values, lane);
+      values = nullptr;
+      return;
+    }
     if (!left) return;
     if (!run) {
       enter(a, lane);
@@ -229,6 +236,7 @@ struct Pages {
     there = page >= 0 ? there | 1u << slot : there & ~(1u << slot);
     const uint8_t* p = head + uint64_t(uint32_t(max(page, 0))) * (a.s.heads * Kv<D>::kBlock);
     ring.refill(slot, p, lane);
+    if (VALUES) values = p + Kv<D>::kHalf;
     --left;
     --run;
   }
@@ -593,19 +601,25 @@ __device__ __forceinline__ void store_lse(const AttendArgs& a, int64_t row, floa
   if (a.mass) a.lse2[row] = y;
 }
 
-// Warps, and blocks of a warp's ring.  The rings fill an SM's shared memory.
+// Warps, and what a warp's ring holds: blocks, or halves of blocks (the weights'
+// kernel, which reads keys alone, and where two blocks of eight warps are too much).
+// The rings fill an SM's shared memory.  SHAPE_FIGURES
 template <int D, int NT>
 struct Shape {
-  static constexpr int kWarps = D == 64 ? (NT == 1 ? 16 : 12) : D == 128 ? (NT == 1 ? 12 : 8) : 6;
-  static constexpr int kDepth = D == 64 ? (NT == 1 ? 3 : 4) : D == 128 ? (NT == 1 ? 2 : 3) : 2;
+  static constexpr int kWarps = D == 64 ? (NT == 1 ? 16 : 12) : D == 128 ? (NT == 1 ? 12 : 8) : 8;
+  static constexpr int kBlocks = D == 64 ? (NT == 1 ? 3 : 4) : D == 128 ? (NT == 1 ? 2 : 3) : 1;
+  static constexpr int kHalves = D == 256 ? 3 : 2 * kBlocks;
+  static constexpr bool kSplit = D == 256;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr uint32_t kSmem = kWarps * kDepth * (Kv<D>::kBlock + 8) + 128;
+  static constexpr uint32_t kSmem = kWarps * kHalves * (Kv<D>::kHalf + 8) + 128;
 };
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(const __grid_constant__ AttendArgs a) {
-  constexpr int kThreads = Shape<D, NT>::kThreads, kWarps = Shape<D, NT>::kWarps, kDepth = Shape<D, NT>::kDepth, R = 8 * NT;
-  using Src = KvSrc<D, true>;
+  constexpr bool kSplit = Shape<D, NT>::kSplit;
+  constexpr int kThreads = Shape<D, NT>::kThreads, kWarps = Shape<D, NT>::kWarps, R = 8 * NT;
+  constexpr int kDepth = kSplit ? Shape<D, NT>::kHalves : Shape<D, NT>::kBlocks;
+  using Src = KvSrc<D, kSplit>;
   using W = Walk<kThreads, R, true>;
   __shared__ uint64_t s_before[kThreads + 1], s_warp[kWarps];
   __shared__ W s_at[kWarps][2];
@@ -633,7 +647,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
   }
   if (lane == 0) s_inner[warp] = 0;
   __syncwarp();
-  Pages<D, Ring<Src, kDepth>, W> pages(s_at[warp][1], end - u);
+  Pages<D, Ring<Src, kDepth>, W, kSplit> pages(s_at[warp][1], end - u);
 #pragma unroll 1
   for (int i = 0; i < kDepth; ++i) pages.issue(a, ring, uint32_t(i), lane);
   Tile<D, NT> tile;
@@ -657,11 +671,19 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
 #pragma unroll 1
     for (; page < stop; ++page) {
       ring.wait(lane);
-      if ((pages.there >> ring.slot & 1) && !tile.sees_none(page)) {
-        float z[4][NT][4];
-        tile.scores(ring.stage(), lane, magic, z);
-        if (tile.sees_all(page)) sums.template add<true>(a, at, tile, page, ring.stage() + Kv<D>::kHalf, lane, magic, z);
-        else sums.template add<false>(a, at, tile, page, ring.stage() + Kv<D>::kHalf, lane, magic, z);
+      const bool look = (pages.there >> ring.slot & 1) && !tile.sees_none(page);
+      float z[4][NT][4];
+      if (look) tile.scores(ring.stage(), lane, magic, z);
+      if (kSplit) {
+        __syncwarp();
+        pages.issue(a, ring, ring.slot, lane);
+        ring.next();
+        ring.wait(lane);
+      }
+      if (look) {
+        const uint32_t values = ring.stage() + (kSplit ? 0 : Kv<D>::kHalf);
+        if (tile.sees_all(page)) sums.template add<true>(a, at, tile, page, values, lane, magic, z);
+        else sums.template add<false>(a, at, tile, page, values, lane, magic, z);
       }
       __syncwarp();
       pages.issue(a, ring, ring.slot, lane);
@@ -924,8 +946,8 @@ constexpr uint32_t kMaxTeam = 16;
 template <int D, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     kv4_attend_team_kernel(const __grid_constant__ AttendArgs a, uint32_t team) {
-  constexpr int kWarps = Shape<D, NT>::kWarps, kDepth = Shape<D, NT>::kDepth, R = 8 * NT, V = D / 32;
-  using Src = KvSrc<D, true>;
+  constexpr int kWarps = Shape<D, NT>::kWarps, kDepth = Shape<D, NT>::kBlocks, R = 8 * NT, V = D / 32;
+  using Src = KvSrc<D, false>;
   struct At {
     Seq q;
     int tile;
@@ -1079,10 +1101,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
 // rows' log-sum-exps.
 template <int D, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(const __grid_constant__ AttendArgs a) {
-  // twice the stages: they hold keys alone
-  constexpr int kThreads = Shape<D, NT>::kThreads, kWarps = Shape<D, NT>::kWarps, kDepth = 2 * Shape<D, NT>::kDepth - 1,
+  constexpr int kThreads = Shape<D, NT>::kThreads, kWarps = Shape<D, NT>::kWarps, kDepth = Shape<D, NT>::kHalves,
                 R = 8 * NT;
-  using Src = KvSrc<D, false>;
+  using Src = KvSrc<D, true>;
   using W = Walk<kThreads, R, false>;
   __shared__ uint64_t s_before[kThreads + 1], s_warp[kWarps];
   __shared__ W s_at[kWarps][2];
