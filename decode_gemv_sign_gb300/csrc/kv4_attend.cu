@@ -1156,20 +1156,28 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(con
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int64_t row = Tile<D, NT>::row(a, at.q, t, int(head), n, e, lane, lo[n][e], hi[n][e]);
-              lse[n][e] = row >= 0 ? a.lse2[row] : 0.f;
+              lse[n][e] = row >= 0 ? a.lse2[row] : INFINITY;  // a place without a row adds 0
             }
         }
         if (tile.sees_none(page)) continue;
         float z[4][NT][4];
         tile.scores(ring.stage(), lane, magic, z);
+        const bool all = tile.sees_all(page);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
+          for (int e = 0; e < 2; ++e) {
+            if (all) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (page * kPage + 8 * k + int(r) >= lo[n][e] && page * kPage + 8 * k + int(r) < hi[n][e])
+              for (int k = 0; k < 8; ++k)
                 sum[k] += exp2_approx(__fmaf_rn(z[k / 2][n][e + 2 * (k % 2)], tile.c[n][e], -lse[n][e]));
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if (page * kPage + 8 * k + int(r) >= lo[n][e] && page * kPage + 8 * k + int(r) < hi[n][e])
+                  sum[k] += exp2_approx(__fmaf_rn(z[k / 2][n][e + 2 * (k % 2)], tile.c[n][e], -lse[n][e]));
+            }
+          }
       }
       // over the four lanes of a token: after each exchange a lane goes on with half of them
 #pragma unroll
