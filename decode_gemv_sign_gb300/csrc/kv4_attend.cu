@@ -21,15 +21,16 @@
 // going over to another scales exactly, by powers of two.
 //
 // Each warp takes an equal run of the call's (sequence, tile of rows, head, page)
-// units through a ring of its own, a tile's beginning and end counted as one more.  Where a tile's pages fall on several warps, a
-// block joins its warps' parts in shared memory and a second kernel those of
-// blocks, always in the same order.  Lengths are on the device, so every block sums
-// up the work of all sequences first.
+// units through a ring of its own, a tile's beginning and end counted as one more.
+// Where a tile's pages fall on several warps, a block joins its warps' parts in
+// shared memory and a second kernel those of blocks, always in the same order.
+// Lengths are on the device, so every block sums up the work of all sequences
+// first.
 //
 // Where the tables leave a warp few pages even if a tile is given to one block or
 // one cluster, that is done instead: one kernel without a workspace, the parts
 // joined through the cluster's shared memory.  One sequence of 4097 tokens, 32 query
-// and 8 cached heads: TEAM_FIGURES.
+// and 8 cached heads: 12.5 us, cut anywhere 20.8.
 #include <algorithm>
 #include <cmath>
 
@@ -362,6 +363,21 @@ struct Tile {
     return -1;
   }
 
+  // Scores (before c) to their distances from `ref`, which they are rounded before: where a
+  // score is 2^22 or more an fma would give the rounding as well, up to half a step above
+  // ref, and a power of two beside ref would be lost.
+  __device__ __forceinline__ void distances(const float (&ref)[NT][2], float (&z)[4][NT][4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float y = ref[n][k % 2];
+          z[i][n][k] = __fsub_rn(__fmul_rn(z[i][n][k], c[n][k % 2]), y == -INFINITY ? 0.f : y);
+        }
+  }
+
   // Scores (before c) of the keys at st: z[i][n][k + 2 h] of token 16 i + 8 h + r and row 8 n + 2 q + k.
   __device__ __forceinline__ void scores(uint32_t st, int lane, uint32_t magic, float (&z)[4][NT][4]) const {
     const uint32_t r = uint32_t(lane) >> 2, q = uint32_t(lane) & 3;
@@ -393,6 +409,17 @@ struct Tile {
   }
 };
 
+// Whether `ref`, of any row, is 2^22 or more from 0.
+template <int NT>
+__device__ __forceinline__ bool any_far(const float (&ref)[NT][2]) {
+  bool far = false;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) far |= fabsf(ref[n][e]) >= 0x1p22f && fabsf(ref[n][e]) < INFINITY;
+  return __any_sync(0xffffffffu, far);
+}
+
 // Sums of a tile so far, and the softmax's state.
 template <int D, int NT>
 struct Sums {
@@ -401,9 +428,11 @@ struct Sums {
   float m[NT][2], l[NT][2];  // reference (base 2, whole, or -inf) and, of the lane's tokens, sum
   float o[2 * G][NT][4];     // tile 2 g + i: column 32 g + 4 r + 2 i (+ 1: the last two) of the rows 2 q, 2 q + 1 (+ 8 n)
   int k;                     // o is under 2^k
+  bool far;                  // a reference is far from 0 (Tile::distances)
 
   __device__ __forceinline__ void clear() {
     k = kNoScale;
+    far = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -464,7 +493,7 @@ struct Sums {
 #pragma unroll
         for (int d = 4; d <= 16; d *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
         next[n][e] = fmaxf(m[n][e], ceilf(x * t.c[n][e]));
-        more |= next[n][e] > m[n][e];
+        more |= next[n][e] > m[n][e] || far;
       }
     if (__any_sync(0xffffffffu, more)) {
 #pragma unroll
@@ -478,6 +507,8 @@ struct Sums {
         }
         scale(n, f[0], f[1]);
       }
+      far = any_far<NT>(m);
+      if (far) t.distances(m, z);
     }
     // the largest scale of a value that some row sees: G words a lane, 2 tokens each
     uint32_t top[G];
@@ -523,8 +554,9 @@ struct Sums {
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float shift = float(k) - (m[n][e] == -INFINITY ? 0.f : m[n][e]);
-        const uint64_t c2 = pair(t.c[n][e], t.c[n][e]), shift2 = pair(shift, shift);
+        const float shift = far ? float(k) : float(k) - (m[n][e] == -INFINITY ? 0.f : m[n][e]);
+        const float c = far ? 1.f : t.c[n][e];
+        const uint64_t c2 = pair(c, c), shift2 = pair(shift, shift);
         uint64_t sum = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -603,7 +635,12 @@ __device__ __forceinline__ void store_lse(const AttendArgs& a, int64_t row, floa
 
 // Warps, and what a warp's ring holds: blocks, or halves of blocks (the weights'
 // kernel, which reads keys alone, and where two blocks of eight warps are too much).
-// The rings fill an SM's shared memory.  SHAPE_FIGURES
+// The rings fill an SM's shared memory.  64 sequences of 8192 tokens, 8 cached heads,
+// us by warps x blocks (h: halves), the shapes taken first:
+//   128 columns,  8 rows: 12 x 2 127, 12 x 1 140, 16 x 1 137, 20 x 1 160, 10 x 2 167;
+//                16 rows: 8 x 3 188, 12 x 2 257 (168 registers a thread spill);
+//    64 columns,  8 rows: 16 x 3 78, 12 x 4 80;
+//   256 columns,  8 rows: 8 x 3 h 247, 8 x 1 264, 6 x 2 307, 4 x 3 402.
 template <int D, int NT>
 struct Shape {
   static constexpr int kWarps = D == 64 ? (NT == 1 ? 16 : 12) : D == 128 ? (NT == 1 ? 12 : 8) : 8;
@@ -803,8 +840,8 @@ __device__ __forceinline__ bool tile_at(const AttendArgs& a, int64_t place, int&
 // and the last warp that have pages of it and, for every block between or around
 // them, of its first warp with none but the tile's.  Where they are follows from the
 // lengths alone and is worked out while the attention still runs; then every load of
-// a thread is in flight at once.  (With places read from the workspace and eight
-// loads at a time the joins of one sequence of 262143 tokens took 12 us.)
+// a thread is in flight at once.  (With places read from the workspace, after the
+// attention's end, one sequence of 262143 tokens, 64 query and 8 cached heads, took 80 us, now 76.)
 constexpr int kAtOnce = 8, kMaxParts = 256;
 template <int D, int NT, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv4_join_kernel(const __grid_constant__ AttendArgs a, int64_t tiles) {
@@ -941,7 +978,6 @@ __device__ __forceinline__ float cluster_lds(uint32_t at, uint32_t rank) {
                : "memory");
   return v;
 }
-constexpr uint32_t kMaxTeam = 16;
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
@@ -1132,6 +1168,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(con
   int lo[NT][2], hi[NT][2];
   int b = -1, held = 0;
   uint32_t head = 0;  // what the tile holds
+  bool far = false;
   const uint32_t r = uint32_t(lane) >> 2, q = uint32_t(lane) & 3;
   for (; u < end; ++u) {
     if (at.page < 0) {
@@ -1158,24 +1195,27 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(con
               const int64_t row = Tile<D, NT>::row(a, at.q, t, int(head), n, e, lane, lo[n][e], hi[n][e]);
               lse[n][e] = row >= 0 ? a.lse2[row] : INFINITY;  // a place without a row adds 0
             }
+          far = any_far<NT>(lse);
         }
         if (tile.sees_none(page)) continue;
         float z[4][NT][4];
         tile.scores(ring.stage(), lane, magic, z);
+        if (far) tile.distances(lse, z);
         const bool all = tile.sees_all(page);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+            const float c = far ? 1.f : tile.c[n][e], from = far ? 0.f : lse[n][e];
             if (all) {
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                sum[k] += exp2_approx(__fmaf_rn(z[k / 2][n][e + 2 * (k % 2)], tile.c[n][e], -lse[n][e]));
+                sum[k] += exp2_approx(__fmaf_rn(z[k / 2][n][e + 2 * (k % 2)], c, -from));
             } else {
 #pragma unroll
               for (int k = 0; k < 8; ++k)
                 if (page * kPage + 8 * k + int(r) >= lo[n][e] && page * kPage + 8 * k + int(r) < hi[n][e])
-                  sum[k] += exp2_approx(__fmaf_rn(z[k / 2][n][e + 2 * (k % 2)], tile.c[n][e], -lse[n][e]));
+                  sum[k] += exp2_approx(__fmaf_rn(z[k / 2][n][e + 2 * (k % 2)], c, -from));
             }
           }
       }
@@ -1225,15 +1265,22 @@ cudaError_t launch(K kernel, uint32_t grid, int threads, uint32_t smem, bool dep
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Once a device: the kernels' shared memory and clusters of 16 allowed; how many of
-// those fit the GPU at a time (none, where no group of 16 SMs is near enough).
+// Once a device: the kernels' shared memory and clusters of 16 allowed; how many
+// clusters of 1 << i blocks fit the GPU at a time: less than its SMs / 2^i where a
+// group of SMs has some left over.  (2 sequences of 512 tokens, 64 query and 8 cached
+// heads, in 16 clusters of 8, which do not fit at once: 18.4 us; in clusters of 4: 10.3.)
+struct Clusters {
+  bool known;
+  int fit[5];
+};
 template <int D, int NT>
-cudaError_t prepare(int dev, int* wide) {
+cudaError_t prepare(int dev, Clusters* out) {
   static std::mutex mu;
-  static int known[64];  // and 1
+  static Clusters all[64];
   std::lock_guard<std::mutex> g(mu);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!known[dev]) {
+  Clusters& c = all[dev];
+  if (!c.known) {
     constexpr int smem = int(Shape<D, NT>::kSmem);
     const auto limit = cudaFuncAttributeMaxDynamicSharedMemorySize;
     cudaError_t e = cudaFuncSetAttribute(kv4_attend_kernel<D, NT>, limit, smem);
@@ -1242,37 +1289,41 @@ cudaError_t prepare(int dev, int* wide) {
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(kv4_attend_team_kernel<D, NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kMaxTeam);
-    cfg.blockDim = dim3(uint32_t(Shape<D, NT>::kThreads));
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = kMaxTeam;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kv4_attend_team_kernel<D, NT>, &cfg) != cudaSuccess) {
-      cudaGetLastError();
-      n = 0;
+    for (int i = 0; i < 5; ++i) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(1u << i);
+      cfg.blockDim = dim3(uint32_t(Shape<D, NT>::kThreads));
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = 1u << i;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&c.fit[i], kv4_attend_team_kernel<D, NT>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        c.fit[i] = 0;
+      }
     }
-    known[dev] = 1 + std::max(n, 0);
+    c.known = true;
   }
-  *wide = known[dev] - 1;
+  *out = c;
   return cudaSuccess;
 }
 
 // Blocks to a tile and head, or 0 where the units are cut anywhere: the largest
-// cluster that leaves all of them an SM of their own, if its warps get at most
-// two pages each by the table.
+// cluster that all of them have room for at once, if its warps get at most four
+// pages each by the table.  8 sequences of 6144 tokens, 64 query and 8 cached heads:
+// 20.5 us by two blocks a tile and head, 28.8 cut anywhere; with all but the first an
+// eighth as long 20.5 and 20.7.  At eight pages a warp (8 x 12288) the first are 34.8
+// and 41.0, the second 30.8 and 24.6.
 template <int D, int NT>
-uint32_t team_of(const AttendArgs& a, int64_t segments, uint32_t sms, int wide) {
+uint32_t team_of(const AttendArgs& a, int64_t segments, uint32_t sms, const Clusters& c) {
+  if (segments > sms) return 0;
   uint32_t team = 1;
-  while (team < kMaxTeam && segments * team * 2 <= sms) team *= 2;
-  if (team == kMaxTeam && segments > wide) team /= 2;
+  for (int i = 1; i < 5 && segments << i <= sms && segments <= c.fit[i]; ++i) team = 1u << i;
   const int64_t pages = a.window ? std::min<int64_t>(a.s.width, (int64_t(a.window) + a.T) / kPage + 2) : a.s.width;
-  return segments <= sms && pages <= int64_t(2) * team * Shape<D, NT>::kWarps ? team : 0;
+  return pages <= int64_t(4) * team * Shape<D, NT>::kWarps ? team : 0;
 }
 
 template <int D, int NT>
@@ -1280,13 +1331,13 @@ int attend(AttendArgs& a, int dev, cudaStream_t s) {
   constexpr int kThreads = Shape<D, NT>::kThreads;
   constexpr uint32_t smem = Shape<D, NT>::kSmem;
   const uint32_t sms = uint32_t(std::min(sm_count(dev), kMaxParts - 2));  // a part a block, and two
-  int wide = 0;
-  cudaError_t e = prepare<D, NT>(dev, &wide);
+  Clusters clusters;
+  cudaError_t e = prepare<D, NT>(dev, &clusters);
   if (e != cudaSuccess) return map_cuda(e);
   // places for the tiles of all sequences (tile_at)
   const int64_t tiles = a.s.starts ? a.T * a.share / (8 * NT) + a.s.B + 1
                                    : int64_t(a.s.B) * int64_t(cdiv(uint64_t(a.share), 8 * NT));
-  const uint32_t team = team_of<D, NT>(a, tiles * a.s.heads, sms, wide);
+  const uint32_t team = team_of<D, NT>(a, tiles * a.s.heads, sms, clusters);
   a.warps = sms * Shape<D, NT>::kWarps;
   auto up = [](uint64_t x) { return (x + 255) & ~uint64_t(255); };
   const uint64_t slots = team ? 0 : uint64_t(2) * a.warps * 8 * NT;
@@ -1303,8 +1354,7 @@ int attend(AttendArgs& a, int dev, cudaStream_t s) {
     e = launch(kv4_attend_team_kernel<D, NT>, uint32_t(tiles * a.s.heads) * team, kThreads, smem, false, team, s, a, team);
   } else {
     e = launch(kv4_attend_kernel<D, NT>, sms, kThreads, smem, false, 1, s, a);
-    // few tiles have many parts: 1024 threads share them (one sequence of 262143 tokens,
-    // 8 heads: 12 -> 4 us); many have two or three
+    // few tiles have many parts: 1024 threads share them; many have two or three
     constexpr int kSmall = 8 * NT * D / 4 < 256 ? 256 : 8 * NT * D / 4;
     const int64_t joins = tiles * a.s.heads;
     if (e == cudaSuccess)
@@ -1352,7 +1402,9 @@ extern "C" int wcomp_kv4_attend(const wcomp_kv4* c, const wcomp_kv4_attend_args*
   p.share = a.q_heads / c->heads;
   p.window = a.window;
   p.scale = a.scale;
-  // one tile of 8 where a sequence has no more rows; dim 256 has no registers for 16
+  // One tile of 8 where a sequence has no more rows, else tiles of 16 that read a page
+  // once: 64 x 8192 tokens, 128 columns, 16 rows 190 us, in two tiles of 8 232
+  // (64 columns: 115 and 137).  With 256 columns the registers do not hold 16.
   const bool one = !a.s.d_starts && p.share <= 8;
   if (c->dim == 64) return one ? attend<64, 1>(p, c->device, s) : attend<64, 2>(p, c->device, s);
   if (c->dim == 128) return one ? attend<128, 1>(p, c->device, s) : attend<128, 2>(p, c->device, s);

@@ -2,7 +2,7 @@
 //
 // A row is read once, by a block of 256 threads or, where there are few rows, by a
 // cluster of blocks that share it; what it is bound by is the memory.  A thread
-// takes batches of four 16-byte vectors.  A warp keeps one running maximum m, so
+// takes batches of 16-byte vectors.  A warp keeps one running maximum m, so
 // that a new one is rare after the first batches, and sums, over the elements
 // below m,
 //     s += 2^d,   w += 2^d d,   d = (x - m) * scale * log2 e,

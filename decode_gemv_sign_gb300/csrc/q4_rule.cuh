@@ -31,7 +31,7 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t m) {
 // first constant, is on the right side of every halfway point, and exactly on
 // it where w / s is; the second constant then rounds half to even.  Scales
 // below 2^-100 (reciprocals near overflow, quotients above 7) divide and clamp.
-constexpr float kSnap = 3072.f;        // 1.5 * 2^11: ulp 2^-12
+constexpr float kSnap = 0x1.8p11f;        // 1.5 * 2^11: ulp 2^-12
 // Codes come as kBase + code, so that a word of eight is a sum of them times
 // powers of 16, less what the bases add up to: one integer multiply-add a code.
 constexpr float kRound = 12582920.f;   // 1.5 * 2^23 + 8: ulp 1, and the code's offset of 8

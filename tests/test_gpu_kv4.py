@@ -213,7 +213,7 @@ def attend_matches(W, b, q, rows, scale=None, window=0, starts=True, strided=Fal
         assert (np.abs(on[at:at + r] - wo) <= to).all(), (i, np.abs(on[at:at + r] - wo).max())
         empty = np.isneginf(wl)
         assert np.array_equal(np.isneginf(ln[at:at + r]), empty)
-        assert (np.abs(ln[at:at + r] - wl)[~empty] <= tl[~empty]).all(), i
+        assert (np.abs(ln[at:at + r][~empty] - wl[~empty]) <= tl[~empty]).all(), i
         n = b.lengths[i]
         err = np.abs(mn[i, :, :n] - m0[i, :, :n] - wm)
         assert (err <= tm + 4 * K.EPS * mn[i, :, :n]).all(), (i, err.max())
@@ -271,6 +271,36 @@ def test_attention_keeps_its_bits_at_every_magnitude(W, D, kq, kk, kv):
     b = Batch(W, [150, 40], 2, D, k=k, v=v)
     q = bf16(rng.standard_normal((2, 6, D)) * kq)
     attend_matches(W, b, q, [1, 1], starts=False)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("size", [2.0 ** 21, 2.0 ** 24, 2.0 ** 33, 2.0 ** 60, 2.0 ** 103])  # |q k| sums to less than 2^112
+@pytest.mark.parametrize("n", [150, 2000])  # joined in a cluster's shared memory, and cut anywhere
+def test_scores_far_apart_and_from_zero_choose_one_token(W, D, size, n):
+    """Scores that fp32 has whole steps between; the largest is alone by more than its error, so its token's value is
+    the result, its score the log-sum-exp and its mass 1, also as values that grow move the sums' power of two."""
+    rng = np.random.default_rng(n)
+    k = rng.standard_normal((n, 2, D)) * size
+    v = rng.standard_normal((n, 2, D)) * 2.0 ** np.repeat(rng.integers(-40, 40, (n + 63) // 64), 64)[:n, None, None]
+    b = Batch(W, [n], 2, D, k=bf16(k), v=bf16(v), width=3 if n < 500 else 800)
+    q = bf16(rng.standard_normal((1, 6, D)))
+    lse, mass = torch.empty(1, 6, device="cuda"), torch.zeros(1, 2, b.width * 64, device="cuda")
+    out = f64(bits(W.kv4_attend(b.cache, dev16(q), b.table, b.len, scale=1.0, lse=lse, mass=mass)))
+    weight = np.zeros((2, n))
+    for h in range(6):
+        z = b.ks[0][:, h // 3] @ f64(q[0, h])
+        mag = np.abs(b.ks[0][:, h // 3]) @ np.abs(f64(q[0, h]))
+        top, second = np.argsort(z)[:-3:-1]
+        off = K.EPS * (D / 4 + 8) * mag.max()
+        if z[top] - z[second] < 2 * off + 40:  # less, and what of the other is left shows
+            continue
+        want = b.vs[0][top, h // 3]
+        assert (np.abs(out[0, h] - want) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(want)).all(), h
+        assert abs(float(lse[0, h]) - z[top]) <= off + 4 * K.EPS * abs(z[top])
+        weight[h // 3, top] += 1
+    got = mass[0, :, :n].cpu().numpy().astype(np.float64)
+    assert np.isfinite(got).all() and (got >= weight * (1 - 2.0 ** -9)).all()
+    assert weight.sum() >= 3
 
 
 def test_attention_to_one_token_among_many(W):
