@@ -1,6 +1,7 @@
 // Writing, reading and evicting from the 4-bit key/value cache.
 #include <algorithm>
 #include <new>
+#include <type_traits>
 
 #include "kv4.cuh"
 #include "q4_rule.cuh"
@@ -8,7 +9,7 @@
 namespace wc {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;  // 256: 8% slower
 
 __device__ __forceinline__ float bf16_value(uint32_t bits) { return __uint_as_float(bits << 16); }
 __device__ __forceinline__ uint32_t bf16_bits(float v) {
@@ -18,23 +19,28 @@ __device__ __forceinline__ uint32_t bf16_bits(float v) {
 }
 
 // A row of keys or values is handled by D / 8 neighbouring lanes, lane u the columns
-// 8 u .. 8 u + 7; four of them share a group.  A warp takes one row of the call,
-// whose place it looks up once, and kRound heads of it: kLanes side by side, kSteps
-// one after the other, the loads of their keys and values in flight together.
-template <int D>
+// 8 u .. 8 u + 7; four of them share a group.  A warp takes `span` rows of the call,
+// whose places its lanes look up side by side, and kHeads heads of each: kLanes at a
+// time, STEPS of them with the loads of their keys and values in flight together.
+// Instructions bound the writing, some 60 for 8 columns, and the places' look-up
+// where many sequences have a few rows each.  65536 rows of 8 heads, one look-up for
+// four rows or (for every row), and the share of the copy rate:
+//   columns  write                 read
+//    64       38 (45) us  0.66      33 (37) us  0.77
+//   128       68 (84)     0.75      58 (64)     0.87
+//   256      130 (161)    0.78     110 (119)    0.92
+// Four steps in flight leave room for fewer warps: 88 us for 75 at 128 columns.
+template <int D, int STEPS>
 struct Items {
   static constexpr int kPer = D / 8;
   static constexpr int kLanes = 32 / kPer;
-  static constexpr int kSteps = 4;
-  static constexpr int kRound = kLanes * kSteps;
+  static constexpr int kHeads = kLanes * STEPS;
 };
 
 // Quantise 8 columns, whose group's other columns the three neighbouring lanes have.
 // `w` gets the codes, 4 bits each; returns the scale's bits.
 __device__ __forceinline__ uint32_t quantise8(const uint32_t (&v)[4], uint32_t& w) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = abs_max2(m, v[i]);
+  uint32_t m = abs_max2(abs_max2(v[0], v[1]), abs_max2(v[2], v[3]));
   m = abs_max2(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = abs_max2(m, __shfl_xor_sync(0xffffffffu, m, 2));
   m = abs_max2(m, m >> 16) & 0x7FFFu;
@@ -43,11 +49,11 @@ __device__ __forceinline__ uint32_t quantise8(const uint32_t (&v)[4], uint32_t& 
   if (s >= 0x1p-100f) {
     // code_fast for two columns at a time
     const float rs = reciprocal(s);
-    const uint64_t rs2 = pair(rs, rs), snap = pair(kSnap, kSnap), back = pair(-kSnap, -kSnap), round = pair(kRound, kRound);
+    const uint64_t rs2 = pair(rs, rs), snap = pair(kSnap, kSnap), round = pair(kRound - kSnap, kRound - kSnap);
     w = 0u - kBase * 0x11111111u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint64_t c = add2(add2(fma2(pair(bf16_lo(v[i]), bf16_hi(v[i])), rs2, snap), back), round);
+      const uint64_t c = add2(fma2(pair(bf16_lo(v[i]), bf16_hi(v[i])), rs2, snap), round);
       w += uint32_t(c) * (1u << (8 * i)) + uint32_t(c >> 32) * (16u << (8 * i));
     }
   } else {
@@ -81,69 +87,79 @@ struct Rows {
   int vec;  // rows are 16-byte aligned
 };
 
-// The place of row i: its page's first block, or null, and the token in it.
-// `mine`: whether the row is a sequence's at all.
-__device__ __forceinline__ uint8_t* row_place(const KvSeqs& s, uint8_t* cache, uint64_t page_bytes, int64_t i, uint32_t& t,
-                                              bool& mine) {
+// The place of row i: its page and the token in it.  Page -1: there is none; -2: the
+// row is no sequence's.
+__device__ __forceinline__ int row_place(const KvSeqs& s, int64_t i, uint32_t& t) {
   const int b = kv_sequence(s, i);
-  mine = b >= 0;
-  if (!mine) return nullptr;
+  if (b < 0) return -2;
   const int64_t pos = kv_position(s, b, i, kv_length(s, b));
-  const int page = pos < 0 ? -1 : kv_page(s, b, int(pos / kPage));
   t = uint32_t(pos) % kPage;
-  return page < 0 ? nullptr : cache + uint64_t(page) * page_bytes;
+  return pos < 0 ? -1 : kv_page(s, b, int(pos / kPage));
+}
+// The first row and head of a warp's unit: `rounds` units have the same rows.
+__device__ __forceinline__ int64_t unit_rows(int64_t unit, uint32_t rounds, uint32_t& round) {
+  if (rounds == 1) {
+    round = 0;
+    return unit;
+  }
+  const int64_t i = (unit >> 32) ? unit / rounds : int64_t(uint32_t(unit) / rounds);
+  round = uint32_t(unit - i * rounds);
+  return i;
 }
 
-template <int D>
+template <int D, int STEPS>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(KvSeqs s, uint8_t* cache, Rows k, Rows v, int64_t T,
-                                                              uint32_t rounds) {
-  using I = Items<D>;
+                                                              uint32_t rounds, uint32_t span) {
+  using I = Items<D, STEPS>;
   using L = Kv<D>;
   const uint32_t lane = threadIdx.x % 32, u = lane % I::kPer;
   const uint32_t key_byte = 4 * key_index<D>(u), value_byte = 4 * value_index<D>(u);
-  const int64_t units = T * rounds;
+  const int64_t units = (T + span - 1) / span * rounds;
   for (int64_t unit = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; unit < units;
        unit += int64_t(gridDim.x) * (kThreads / 32)) {
-    const int64_t i = unit / rounds;
-    const uint32_t h0 = uint32_t(unit % rounds) * I::kRound + lane / I::kPer;
-    uint32_t t = 0;
-    bool mine;
-    uint8_t* page = row_place(s, cache, uint64_t(s.heads) * L::kBlock, i, t, mine);
-    if (!page) continue;
-    uint32_t x[2][I::kSteps][4];
+    uint32_t round;
+    const int64_t i0 = unit_rows(unit, rounds, round) * span;
+    const uint32_t h0 = round * I::kHeads + lane / I::kPer, rows = uint32_t(min(int64_t(span), T - i0));
+    uint32_t its = 0;
+    const int it = lane < rows ? row_place(s, i0 + lane, its) : -2;
+#pragma unroll 1
+    for (uint32_t i = 0; i < rows; ++i) {
+      const int page = __shfl_sync(0xffffffffu, it, i);
+      const uint32_t t = __shfl_sync(0xffffffffu, its, i);
+      if (page < 0) continue;
+      uint32_t x[2][STEPS][4];
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      const Rows& r = part ? v : k;
-      const uint16_t* p = r.p + i * r.row + h0 * r.head + 8 * u;
+      for (int part = 0; part < 2; ++part) {
+        const Rows& r = part ? v : k;
+        const uint16_t* p = r.p + (i0 + i) * r.row + h0 * r.head + 8 * u;
+        if (r.vec) {
 #pragma unroll
-      for (int j = 0; j < I::kSteps; ++j, p += I::kLanes * r.head) {
-        uint4 y = make_uint4(0, 0, 0, 0);
-        if (h0 + j * I::kLanes < s.heads) {
-          if (r.vec) {
-            y = ld_stream_v4(p);
-          } else {
-            y.x = p[0] | uint32_t(p[1]) << 16;
-            y.y = p[2] | uint32_t(p[3]) << 16;
-            y.z = p[4] | uint32_t(p[5]) << 16;
-            y.w = p[6] | uint32_t(p[7]) << 16;
+          for (int j = 0; j < STEPS; ++j, p += I::kLanes * r.head) {
+            const uint4 y = h0 + j * I::kLanes < s.heads ? ld_stream_v4(p) : make_uint4(0, 0, 0, 0);
+            x[part][j][0] = y.x; x[part][j][1] = y.y; x[part][j][2] = y.z; x[part][j][3] = y.w;
           }
+        } else {
+#pragma unroll
+          for (int j = 0; j < STEPS; ++j, p += I::kLanes * r.head)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[part][j][e] = h0 + j * I::kLanes < s.heads ? p[2 * e] | uint32_t(p[2 * e + 1]) << 16 : 0u;
         }
-        x[part][j][0] = y.x; x[part][j][1] = y.y; x[part][j][2] = y.z; x[part][j][3] = y.w;
       }
-    }
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      uint8_t* half = page + h0 * L::kBlock + part * L::kHalf;
-      uint8_t* codes = half + L::at(t, part ? value_byte : key_byte);
-      uint8_t* scales = half + L::scale(t, u >> 2);
+      for (int part = 0; part < 2; ++part) {
+        uint8_t* half = cache + (uint64_t(uint32_t(page)) * s.heads + h0) * L::kBlock + part * L::kHalf;
+        uint8_t* codes = half + L::at(t, part ? value_byte : key_byte);
+        uint8_t* scales = half + L::scale(t, u >> 2);
 #pragma unroll
-      for (int j = 0; j < I::kSteps; ++j) {
-        uint32_t w;
-        const uint32_t scale = quantise8(x[part][j], w);  // every lane takes part in the exchanges
-        if (part) w = value_word(w, u);
-        if (h0 + j * I::kLanes >= s.heads) continue;
-        *reinterpret_cast<uint32_t*>(codes + j * I::kLanes * L::kBlock) = w;
-        if ((u & 3) == 0) *reinterpret_cast<uint16_t*>(scales + j * I::kLanes * L::kBlock) = uint16_t(scale);
+        for (int j = 0; j < STEPS; ++j) {
+          uint32_t w;
+          const uint32_t scale = quantise8(x[part][j], w);  // every lane takes part in the exchanges
+          if (part) w = value_word(w, u);
+          if (h0 + j * I::kLanes >= s.heads) continue;
+          *reinterpret_cast<uint32_t*>(codes + j * I::kLanes * L::kBlock) = w;
+          if ((u & 3) == 0) *reinterpret_cast<uint16_t*>(scales + j * I::kLanes * L::kBlock) = uint16_t(scale);
+        }
       }
     }
   }
@@ -163,50 +179,55 @@ __device__ __forceinline__ uint4 values8(uint32_t w, uint32_t scale) {
   return make_uint4(prmt(x[0], x[1], 0x5410), prmt(x[2], x[3], 0x5410), prmt(x[0], x[1], 0x7632), prmt(x[2], x[3], 0x7632));
 }
 
-template <int D>
+template <int D, int STEPS>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(KvSeqs s, const uint8_t* cache, uint16_t* k, uint16_t* v,
-                                                            int64_t T, uint32_t rounds, int vec) {
-  using I = Items<D>;
+                                                            int64_t T, uint32_t rounds, uint32_t span, int vec) {
+  using I = Items<D, STEPS>;
   using L = Kv<D>;
   const uint32_t lane = threadIdx.x % 32, u = lane % I::kPer;
   const uint32_t key_byte = 4 * key_index<D>(u), value_byte = 4 * value_index<D>(u);
-  const int64_t units = T * rounds;
+  const int64_t units = (T + span - 1) / span * rounds;
   for (int64_t unit = int64_t(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; unit < units;
        unit += int64_t(gridDim.x) * (kThreads / 32)) {
-    const int64_t i = unit / rounds;
-    const uint32_t h0 = uint32_t(unit % rounds) * I::kRound + lane / I::kPer;
-    uint32_t t = 0;
-    bool mine;
-    const uint8_t* page = row_place(s, const_cast<uint8_t*>(cache), uint64_t(s.heads) * L::kBlock, i, t, mine);
-    if (!mine) continue;
-    uint32_t w[2][I::kSteps], scale[2][I::kSteps];
+    uint32_t round;
+    const int64_t i0 = unit_rows(unit, rounds, round) * span;
+    const uint32_t h0 = round * I::kHeads + lane / I::kPer, rows = uint32_t(min(int64_t(span), T - i0));
+    uint32_t its = 0;
+    const int it = lane < rows ? row_place(s, i0 + lane, its) : -2;
+#pragma unroll 1
+    for (uint32_t i = 0; i < rows; ++i) {
+      const int page = __shfl_sync(0xffffffffu, it, i);
+      const uint32_t t = __shfl_sync(0xffffffffu, its, i);
+      if (page < -1) continue;
+      uint32_t w[2][STEPS], scale[2][STEPS];
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      const uint8_t* half = page + h0 * L::kBlock + part * L::kHalf;
-      const uint8_t* codes = half + L::at(t, part ? value_byte : key_byte);
-      const uint8_t* scales = half + L::scale(t, u >> 2);
+      for (int part = 0; part < 2; ++part) {
+        const uint8_t* half = cache + (uint64_t(uint32_t(page)) * s.heads + h0) * L::kBlock + part * L::kHalf;
+        const uint8_t* codes = half + L::at(t, part ? value_byte : key_byte);
+        const uint8_t* scales = half + L::scale(t, u >> 2);
 #pragma unroll
-      for (int j = 0; j < I::kSteps; ++j) {
-        w[part][j] = 0x88888888u;
-        scale[part][j] = 0;
-        if (!page || h0 + j * I::kLanes >= s.heads) continue;
-        w[part][j] = *reinterpret_cast<const uint32_t*>(codes + j * I::kLanes * L::kBlock);
-        scale[part][j] = *reinterpret_cast<const uint16_t*>(scales + j * I::kLanes * L::kBlock);
+        for (int j = 0; j < STEPS; ++j) {
+          w[part][j] = 0x88888888u;
+          scale[part][j] = 0;
+          if (page < 0 || h0 + j * I::kLanes >= s.heads) continue;
+          w[part][j] = *reinterpret_cast<const uint32_t*>(codes + j * I::kLanes * L::kBlock);
+          scale[part][j] = *reinterpret_cast<const uint16_t*>(scales + j * I::kLanes * L::kBlock);
+        }
       }
-    }
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      uint16_t* p = (part ? v : k) + (i * s.heads + h0) * D + 8 * u;
+      for (int part = 0; part < 2; ++part) {
+        uint16_t* p = (part ? v : k) + ((i0 + i) * s.heads + h0) * D + 8 * u;
 #pragma unroll
-      for (int j = 0; j < I::kSteps; ++j, p += I::kLanes * D) {
-        const uint4 x = values8(part ? value_word(w[part][j], u) : w[part][j], scale[part][j]);
-        if (h0 + j * I::kLanes >= s.heads) continue;
-        if (vec) {
-          *reinterpret_cast<uint4*>(p) = x;
-        } else {
-          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+        for (int j = 0; j < STEPS; ++j, p += I::kLanes * D) {
+          const uint4 x = values8(part ? value_word(w[part][j], u) : w[part][j], scale[part][j]);
+          if (h0 + j * I::kLanes >= s.heads) continue;
+          if (vec) {
+            *reinterpret_cast<uint4*>(p) = x;
+          } else {
+            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = uint16_t(y[e / 2] >> (16 * (e % 2)));
+            for (int e = 0; e < 8; ++e) p[e] = uint16_t(y[e / 2] >> (16 * (e % 2)));
+          }
         }
       }
     }
@@ -505,6 +526,8 @@ bool on_device(const wcomp_kv4* c) {
   return cudaGetDevice(&dev) == cudaSuccess && dev == c->device;
 }
 
+constexpr uint32_t kMaxSpan = 4;  // rows of a warp, once the GPU has 64 units an SM
+
 uint32_t grid_of(int64_t blocks, int dev) {
   return uint32_t(std::max<int64_t>(1, std::min<int64_t>(blocks, int64_t(sm_count(dev)) * 64)));
 }
@@ -532,6 +555,32 @@ int kv_seqs(const wcomp_kv4* c, const wcomp_kv4_seqs& s, KvSeqs* out) {
 }  // namespace wc
 
 using namespace wc;
+
+// Calls f with a kernel's dim and steps: as many as the cache's heads fill.
+template <class F>
+static void kv_rows_kernel(const wcomp_kv4* c, F f) {
+  auto steps = [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
+    if (c->heads <= Items<D, 1>::kHeads) f(dim, std::integral_constant<int, 1>{});
+    else f(dim, std::integral_constant<int, 2>{});
+  };
+  if (c->dim == 64) steps(std::integral_constant<int, 64>{});
+  else if (c->dim == 128) steps(std::integral_constant<int, 128>{});
+  else steps(std::integral_constant<int, 256>{});
+}
+// Units of rows x heads: how many share rows, and rows of a warp.
+struct RowUnits {
+  uint32_t rounds, span, grid;
+};
+template <int D, int STEPS>
+static RowUnits row_units(const wcomp_kv4* c, int64_t T) {
+  RowUnits r;
+  r.rounds = uint32_t(cdiv(uint64_t(c->heads), Items<D, STEPS>::kHeads));
+  r.span = 1;
+  while (r.span < kMaxSpan && T * r.rounds >= int64_t(sm_count(c->device)) * 64 * r.span) r.span *= 2;
+  r.grid = grid_of(int64_t(cdiv(cdiv(uint64_t(T), r.span) * r.rounds, kThreads / 32)), c->device);
+  return r;
+}
 
 #define WCOMP_KV_DIM(dim, CALL)       \
   do {                                \
@@ -581,14 +630,11 @@ extern "C" int wcomp_kv4_append(wcomp_kv4* c, const wcomp_kv4_seqs* seqs, const 
   if ((st = kv_seqs(c, *seqs, &s)) != WCOMP_OK) return st;
   if (T == 0 || s.B == 0) return WCOMP_OK;
   const Rows k{d_k, k_row, k_head, rows_vec(d_k, k_row, k_head)}, v{d_v, v_row, v_head, rows_vec(d_v, v_row, v_head)};
-#define CALL(D)                                                                                            \
-  do {                                                                                                     \
-    const uint32_t rounds = uint32_t(cdiv(uint64_t(c->heads), Items<D>::kRound));                      \
-    kv4_append_kernel<D><<<grid_of(int64_t(cdiv(T * rounds, kThreads / 32)), c->device), kThreads, 0,      \
-                           static_cast<cudaStream_t>(stream)>>>(s, c->d, k, v, T, rounds);                 \
-  } while (0)
-  WCOMP_KV_DIM(c->dim, CALL);
-#undef CALL
+  kv_rows_kernel(c, [&](auto dim, auto steps) {
+    constexpr int D = decltype(dim)::value, STEPS = decltype(steps)::value;
+    const RowUnits r = row_units<D, STEPS>(c, T);
+    kv4_append_kernel<D, STEPS><<<r.grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(s, c->d, k, v, T, r.rounds, r.span);
+  });
   count_launches(1);
   return map_cuda(cudaGetLastError());
 }
@@ -602,14 +648,11 @@ extern "C" int wcomp_kv4_read(const wcomp_kv4* c, const wcomp_kv4_seqs* seqs, ui
   if ((st = kv_seqs(c, *seqs, &s)) != WCOMP_OK) return st;
   if (T == 0 || s.B == 0) return WCOMP_OK;
   const int vec = rows_vec(d_k, 0, 0) && rows_vec(d_v, 0, 0);
-#define CALL(D)                                                                                          \
-  do {                                                                                                   \
-    const uint32_t rounds = uint32_t(cdiv(uint64_t(c->heads), Items<D>::kRound));                    \
-    kv4_read_kernel<D><<<grid_of(int64_t(cdiv(T * rounds, kThreads / 32)), c->device), kThreads, 0,      \
-                         static_cast<cudaStream_t>(stream)>>>(s, c->d, d_k, d_v, T, rounds, vec);        \
-  } while (0)
-  WCOMP_KV_DIM(c->dim, CALL);
-#undef CALL
+  kv_rows_kernel(c, [&](auto dim, auto steps) {
+    constexpr int D = decltype(dim)::value, STEPS = decltype(steps)::value;
+    const RowUnits r = row_units<D, STEPS>(c, T);
+    kv4_read_kernel<D, STEPS><<<r.grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(s, c->d, d_k, d_v, T, r.rounds, r.span, vec);
+  });
   count_launches(1);
   return map_cuda(cudaGetLastError());
 }

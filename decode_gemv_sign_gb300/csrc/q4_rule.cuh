@@ -29,7 +29,8 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t m) {
 // either exactly halfway between integers or at least 2^-10 away from it, so
 // w * (1 / s) (2^-22 relative error), rounded to a multiple of 2^-12 by the
 // first constant, is on the right side of every halfway point, and exactly on
-// it where w / s is; the second constant then rounds half to even.  Scales
+// it where w / s is; the second, added less the first (both sums are exact but for
+// the one rounding to a whole number), then rounds half to even.  Scales
 // below 2^-100 (reciprocals near overflow, quotients above 7) divide and clamp.
 constexpr float kSnap = 0x1.8p11f;        // 1.5 * 2^11: ulp 2^-12
 // Codes come as kBase + code, so that a word of eight is a sum of them times
@@ -37,7 +38,7 @@ constexpr float kSnap = 0x1.8p11f;        // 1.5 * 2^11: ulp 2^-12
 constexpr float kRound = 12582920.f;   // 1.5 * 2^23 + 8: ulp 1, and the code's offset of 8
 constexpr uint32_t kBase = 0x4B400000u;  // the bits of 1.5 * 2^23
 __device__ __forceinline__ uint32_t code_fast(float w, float rs) {
-  return __float_as_uint(__fadd_rn(__fadd_rn(__fmaf_rn(w, rs, kSnap), -kSnap), kRound));
+  return __float_as_uint(__fadd_rn(__fmaf_rn(w, rs, kSnap), kRound - kSnap));
 }
 __device__ __forceinline__ uint32_t code_slow(float w, float s) {
   if (!(s > 0.f)) return 8u;  // scale 0 or NaN

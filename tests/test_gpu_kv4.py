@@ -112,6 +112,46 @@ def test_tokens_one_by_one_are_the_tokens_at_once(W, D):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("chunk", [1, 7, 16, 33, 100, 400])
+def test_prompts_in_parts_are_the_prompts_at_once(W, D, chunk):
+    """Every chunk of up to `chunk` rows a sequence, few or many, from and to any place of a page; rows of nobody behind."""
+    lengths = [300, 1, 64, 129, 15]
+    whole = Batch(W, lengths, 3, D, seed=6)
+    other = W.kv4_create(whole.pages, 3, D)
+    at = np.concatenate([[0], np.cumsum(lengths)])
+    for step in range(0, max(lengths), chunk):
+        now = [min(n, step + chunk) for n in lengths]
+        rows = [max(0, n - step) for n in now]
+        pick = np.concatenate([np.arange(at[i] + step, at[i] + step + r) for i, r in enumerate(rows)] + [np.zeros(3, int)])
+        W.kv4_append(other, dev16(whole.k[pick]), dev16(whole.v[pick]), whole.table, ints(now), starts_of(rows))
+    a = whole.everything()
+    b = W.kv4_read(other, whole.table, whole.len, starts_of(lengths), rows=sum(lengths))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    W.device_check()
+
+
+@pytest.mark.parametrize("rows", [[3, 1, 2], [100, 70, 0], [130, 200, 65]])
+def test_reading_rows_from_anywhere_and_without_tokens(W, rows):
+    """The last rows of each sequence, which may be more than it holds: those read as zeros."""
+    lengths = [99, 130, 64]
+    b = Batch(W, lengths, 2, 128, seed=7)
+    n = (sum(rows) + 2) * 2 * 128
+    flat = torch.full((2 * (n + 2 * GUARD),), 7.0, dtype=torch.bfloat16, device="cuda")
+    for shift in (0, 1):  # 16-byte aligned or not
+        k, v = (flat[i * (n + 2 * GUARD) + GUARD + shift:][:n].view(-1, 2, 128) for i in range(2))
+        W.kv4_read(b.cache, b.table, b.len, starts_of(rows), k=k, v=v)
+        at = 0
+        for i, r in enumerate(rows):
+            for got, held in ((k, b.ks[i]), (v, b.vs[i])):
+                want = np.concatenate([np.zeros((max(0, r - lengths[i]), 2, 128)), held[max(0, lengths[i] - r):]])
+                same_values(bits(got[at:at + r]), want)
+            at += r
+        k[:at].fill_(7.0), v[:at].fill_(7.0)
+        assert (flat == 7.0).all()
+    W.device_check()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 def test_append_of_strided_and_unaligned_rows(W, D):
     rng = np.random.default_rng(2)
     T, H = 37, 3
