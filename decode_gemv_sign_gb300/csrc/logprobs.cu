@@ -13,7 +13,10 @@
 // of its batches (up to 32 buckets) in shared memory.  If each of the eight warps
 // has ceil(k / 8) threads whose largest element is at least t, the k-th largest
 // element of the block's part is at least t; only buckets that may hold an element
-// of at least t are read again, some 2 k of 8192 in ordinary rows, eight at a time.
+// of at least t are read again, some 2 k of 5000 in ordinary rows, eight at a time.
+//
+// 1024 rows of 151552: fp32 94 us (0.97 of the copy rate), top 1 or 20 107 (0.86); BF16
+// 62 (0.74: six instructions an element), top 20 83.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -25,11 +28,12 @@ namespace wc {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-// Vectors of a batch and blocks an SM: 1024 rows of 151552 fp32 logits, top 20, at 4
-// and 4 118, at 6 and 3 112 us; BF16 87 and 100 us.
+// Vectors of a batch and blocks an SM: 8192 rows of 8192 fp32 logits, top 20, at 8 and
+// 4 126, at 6 and 4 140, at 5 and 5 147 us; 1024 of 151552 BF16 at 4 and 4 83, at 6 and
+// 4 92, at 4 and 5 88.
 template <bool BF16>
 struct Batch {
-  static constexpr int kVecs = BF16 ? 4 : 6, kBlocks = BF16 ? 4 : 3;
+  static constexpr int kVecs = BF16 ? 4 : 8, kBlocks = 4;
 };
 constexpr int kBuckets = 32;
 constexpr int kMaxTop = 64;
@@ -109,15 +113,16 @@ struct Stats {
     n = 0.f;
     m = to;
   }
-  __device__ __forceinline__ void add(const Stats& o, float c) {
-    Stats x = o;
-    if (x.m > m) raise(x.m, c);
-    if (m > x.m) x.raise(m, c);
-    s += x.s;
-    w += x.w;
-    n += x.n;
-  }
 };
+
+// The sums of a list of N <= 32, by the whole warp.
+__device__ __forceinline__ Stats join(const Stats* list, uint32_t n, int lane, float c) {
+  Stats x{-INFINITY, 0.f, 0.f, 0.f};
+  if (uint32_t(lane) < n) x = list[lane];
+  const float m = warp_max(x.m);
+  if (m > x.m) x.raise(m, c);
+  return {m, warp_sum(x.s), warp_sum(x.w), warp_sum(x.n)};
+}
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -138,16 +143,20 @@ __device__ __forceinline__ void st_cluster(uint32_t a, uint32_t v) {
 }
 
 constexpr int kList = 128;   // candidates of a warp
-constexpr int kLook = 64;    // buckets that it reads again at once
+constexpr int kLook = 64;    // buckets that it may read again,
+constexpr uint32_t kAtOnce = 8;  // so many at a time
 
+// The loads in flight need L1, which shares its memory with this.
 struct Shared {
-  float top[kBuckets][kThreads];  // largest element of a thread's bucket
-  Stats stats[kWarps > kMaxTeam ? kWarps : kMaxTeam];
-  uint64_t list[kWarps * kList];   // a warp's candidates; then all of them, or the cluster's
+  union {
+    float top[kBuckets][kThreads];   // largest element of a thread's bucket
+    uint64_t all[kWarps * kList];    // then the candidates one behind the other, in any order
+  };
+  uint64_t list[kWarps * kList];   // each warp's candidates; then the cluster's blocks'
   uint64_t found[kMaxTop];
   uint16_t buckets[kWarps][kLook]; // bucket and lane of those a warp reads again
   uint64_t bound[kWarps];
-  uint32_t counts[kWarps];         // candidates of each warp
+  uint32_t total;                  // candidates
 };
 
 // Where the elements of a block's part are.
@@ -155,13 +164,13 @@ struct Part {
   const uint8_t* z;
   uint32_t head, v0, v1, group, buckets;
 };
+// Index of element e of a thread's bucket, or none.
+constexpr uint32_t kNoIndex = 0xFFFFFFFFu;
 template <bool BF16>
-__device__ __forceinline__ uint64_t part_key(const Part& p, uint32_t bucket, uint32_t owner, uint32_t e) {
+__device__ __forceinline__ uint32_t part_index(const Part& p, uint32_t bucket, uint32_t owner, uint32_t e) {
   constexpr uint32_t E = BF16 ? 8 : 4, kVecs = Batch<BF16>::kVecs;
   const uint32_t v = p.v0 + (bucket * p.group * kVecs + e / E) * kThreads + owner;
-  if (e >= p.group * kVecs * E || v >= p.v1) return 0;
-  const uint32_t i = p.head + v * E + e % E;
-  return logit_key(logit<BF16>(p.z, i), i);
+  return e >= p.group * kVecs * E || v >= p.v1 ? kNoIndex : p.head + v * E + e % E;
 }
 // No element of the thread's bucket is larger than this.
 template <bool BF16>
@@ -186,7 +195,8 @@ __device__ __noinline__ uint32_t search_all(const Part& p, Shared& sh, uint64_t 
     for (uint32_t who = __ballot_sync(0xffffffffu, bucket_key<BF16>(p, sh, b) > least); who; who &= who - 1) {
 #pragma unroll 1
       for (uint32_t e = lane; e - lane < p.group * kVecs * (BF16 ? 8 : 4); e += 32) {
-        const uint64_t k = part_key<BF16>(p, b, uint32_t(warp * 32 + __ffs(int(who)) - 1), e);
+        const uint32_t i = part_index<BF16>(p, b, uint32_t(warp * 32 + __ffs(int(who)) - 1), e);
+        const uint64_t k = i == kNoIndex ? 0 : logit_key(logit<BF16>(p.z, i), i);
         const uint32_t some = __ballot_sync(0xffffffffu, k > least);
         if (k > least) list[count + __popc(some & ((1u << lane) - 1u))] = k;
         count += __popc(some);
@@ -216,25 +226,25 @@ __device__ __noinline__ uint32_t search_all(const Part& p, Shared& sh, uint64_t 
   return uint32_t(count);
 }
 
-// The `keep` largest of list[0 .. n), descending, to found; what is missing is 0.
-__device__ __forceinline__ void rank_list(Shared& sh, int n, int keep) {
-  for (int i = threadIdx.x; i < keep; i += kThreads) sh.found[i] = 0;
-  __syncthreads();
+// The `keep` largest of list[0 .. n) but zeros, descending, to found.
+__device__ __forceinline__ void rank_list(Shared& sh, const uint64_t* list, int n, int keep) {
   for (int i = threadIdx.x; i < n; i += kThreads) {
-    const uint64_t k = sh.list[i];
+    const uint64_t k = list[i];
     if (!k) continue;
     int rank = 0;
-    for (int j = 0; j < n; ++j) rank += sh.list[j] > k;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) rank += list[j] > k;
     if (rank < keep) sh.found[rank] = k;
   }
-  __syncthreads();
 }
 
 template <bool BF16, bool TOP>
 __global__ void __launch_bounds__(kThreads, Batch<BF16>::kBlocks) logprobs_kernel(const __grid_constant__ LogprobArgs a, uint32_t team) {
   constexpr int E = BF16 ? 8 : 4;  // elements of a vector
   constexpr int kVecs = Batch<BF16>::kVecs;
-  __shared__ Shared sh;
+  using Lists = std::conditional_t<TOP, Shared, char>;
+  __shared__ Stats s_stats[kWarps > kMaxTeam ? kWarps : kMaxTeam];
+  __shared__ Lists sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t rank = team > 1 ? cluster_rank() : 0;
   const int64_t t = blockIdx.x / team;
@@ -354,11 +364,7 @@ __global__ void __launch_bounds__(kThreads, Batch<BF16>::kBlocks) logprobs_kerne
   st.s = warp_sum(st.s);
   st.w = warp_sum(st.w);
   st.n = warp_sum(st.n);
-  if (lane == 0) sh.stats[warp] = st;
-  __syncthreads();
-  st = sh.stats[0];
-  for (int w = 1; w < kWarps; ++w) st.add(sh.stats[w], c);
-
+  if (lane == 0) s_stats[warp] = st;
   if constexpr (TOP) {
     const int keep = a.top_k;
     // a bound that ceil(keep / 8) threads of every warp reach
@@ -368,43 +374,55 @@ __global__ void __launch_bounds__(kThreads, Batch<BF16>::kBlocks) logprobs_kerne
       if (mine == reached) mine = 0;
     }
     if (lane == 0) sh.bound[warp] = reached;
+    if (threadIdx.x == 0) sh.total = 0;
+    for (int i = threadIdx.x; i < keep; i += kThreads) sh.found[i] = 0;
     __syncthreads();
+    st = join(s_stats, kWarps, lane, c);
     uint64_t bound = sh.bound[0];
     for (int w = 1; w < kWarps; ++w) bound = min(bound, sh.bound[w]);
     const uint64_t least = bound ? bound - 1 : 0;
     const Part part{z, head, v0, v1, group, group ? (rounds + group - 1) / group : 0};
     uint64_t* const list = sh.list + warp * kList;
-    if (lane == 0) sh.counts[warp] = 0;
-    uint32_t listed = 0;
-    for (uint32_t b = 0; b < part.buckets; ++b) {
-      const bool look = bucket_key<BF16>(part, sh, b) > least;
-      const uint32_t who = __ballot_sync(0xffffffffu, look), at = listed + __popc(who & ((1u << lane) - 1u));
-      if (look && at < kLook) sh.buckets[warp][at] = uint16_t(b * 32 + lane);
-      listed += __popc(who);
-    }
-    __syncwarp();
-    for (uint32_t b0 = 0; b0 < min(listed, uint32_t(kLook)); b0 += 8)
-      for (uint32_t e0 = 0; e0 < group * kVecs * E; e0 += 32) {
-        uint64_t k[8];
+    const float floor = bound ? key_logit(bound) : -INFINITY;
+    uint32_t look = 0;  // buckets of this thread that may have such an element
+#pragma unroll 8
+    for (uint32_t b = 0; b < part.buckets; ++b) look |= uint32_t(sh.top[b][threadIdx.x] >= floor) << b;
+    uint32_t listed = __popc(look);
 #pragma unroll
-        for (uint32_t j = 0; j < 8; ++j) {
+    for (int d = 1; d < 32; d *= 2) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, listed, d);
+      if (lane >= d) listed += y;
+    }
+    for (uint32_t at = listed - __popc(look); look && at < kLook; ++at, look &= look - 1)
+      sh.buckets[warp][at] = uint16_t((__ffs(int(look)) - 1) * 32 + lane);
+    listed = __shfl_sync(0xffffffffu, listed, 31);
+    __syncwarp();
+    uint32_t count = 0;
+    // lanes with an element that may be one: to the list
+    auto take = [&](bool may, float x, uint32_t i) {
+      if (!__any_sync(0xffffffffu, may)) return;
+      const uint64_t k = may && i != kNoIndex ? logit_key(x, i) : 0;
+      const uint32_t who = __ballot_sync(0xffffffffu, k > least), at = count + __popc(who & ((1u << lane) - 1u));
+      if (k > least && at < kList) list[at] = k;
+      count += __popc(who);
+    };
+    for (uint32_t b0 = 0; b0 < min(listed, uint32_t(kLook)); b0 += kAtOnce)
+      for (uint32_t e0 = 0; e0 < group * kVecs * E; e0 += 32) {
+        auto index = [&](uint32_t j) {
           const uint32_t which = sh.buckets[warp][min(b0 + j, listed - 1)];
-          k[j] = b0 + j < listed ? part_key<BF16>(part, which / 32, uint32_t(warp) * 32 + which % 32, e0 + lane) : 0;
+          return b0 + j < listed ? part_index<BF16>(part, which / 32, uint32_t(warp) * 32 + which % 32, e0 + lane) : kNoIndex;
+        };
+        float x[kAtOnce];
+#pragma unroll
+        for (uint32_t j = 0; j < kAtOnce; ++j) {
+          const uint32_t i = index(j);
+          x[j] = i == kNoIndex ? -INFINITY : logit<BF16>(z, i);
         }
 #pragma unroll
-        for (uint32_t j = 0; j < 8; ++j)
-          if (k[j] > least) {
-            const uint32_t at = atomicAdd(&sh.counts[warp], 1u);  // in any order: they are ranked later
-            if (at < kList) list[at] = k[j];
-          }
+        for (uint32_t j = 0; j < kAtOnce; ++j) take(!(x[j] < floor), x[j], index(j));
       }
-    if (uint32_t(warp) * 32 < edges && threadIdx.x < edges) {
-      const uint64_t k = logit_key(edge_x, edge);
-      const uint32_t at = k > least ? atomicAdd(&sh.counts[warp], 1u) : kList;
-      if (at < kList) list[at] = k;
-    }
+    if (uint32_t(warp) * 32 < edges) take(threadIdx.x < edges, edge_x, edge);
     __syncwarp();
-    uint32_t count = sh.counts[warp];
     if (listed > kLook || count > kList) {
       count = search_all<BF16>(part, sh, least, keep);
       // the first warp's edges: the list has room for them
@@ -413,31 +431,29 @@ __global__ void __launch_bounds__(kThreads, Batch<BF16>::kBlocks) logprobs_kerne
         count += edges;
       }
     }
-    // the warps' candidates one behind the other
     __syncwarp();
-    uint64_t mine4[kList / 32];
-#pragma unroll
-    for (int i = 0; i < kList / 32; ++i) mine4[i] = uint32_t(lane + 32 * i) < count ? list[lane + 32 * i] : 0;
-    if (lane == 0) sh.counts[warp] = count;
+    uint32_t place = 0;
+    if (lane == 0) place = atomicAdd(&sh.total, count);
+    place = __shfl_sync(0xffffffffu, place, 0);
+    __syncthreads();  // nobody looks at the buckets any more
+    for (uint32_t i = lane; i < count; i += 32) sh.all[place + i] = list[i];
     __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += int(sh.counts[w]);
-      all += int(sh.counts[w]);
-    }
-#pragma unroll
-    for (int i = 0; i < kList / 32; ++i)
-      if (uint32_t(lane + 32 * i) < count) sh.list[before + lane + 32 * i] = mine4[i];
+    rank_list(sh, sh.all, int(sh.total), keep);
     __syncthreads();
-    rank_list(sh, all, keep);
+  } else {
+    __syncthreads();
+    st = join(s_stats, kWarps, lane, c);
   }
 
   if (team > 1) {
     // everything to the cluster's first block, whose lists are free once all are here
     cluster_sync();
-    if (threadIdx.x < 4) {
-      const float v[4] = {st.m, st.s, st.w, st.n};
-      st_cluster(in_first(&sh.stats[rank]) + 4 * threadIdx.x, __float_as_uint(v[threadIdx.x]));
+    if (threadIdx.x == 0) {
+      const uint32_t to = in_first(&s_stats[rank]);
+      st_cluster(to, __float_as_uint(st.m));
+      st_cluster(to + 4, __float_as_uint(st.s));
+      st_cluster(to + 8, __float_as_uint(st.w));
+      st_cluster(to + 12, __float_as_uint(st.n));
     }
     if constexpr (TOP) {
       const uint32_t* mine = reinterpret_cast<const uint32_t*>(sh.found);
@@ -446,9 +462,13 @@ __global__ void __launch_bounds__(kThreads, Batch<BF16>::kBlocks) logprobs_kerne
     }
     cluster_sync();
     if (rank) return;
-    st = sh.stats[0];
-    for (uint32_t w = 1; w < team; ++w) st.add(sh.stats[w], c);
-    if constexpr (TOP) rank_list(sh, int(team) * a.top_k, a.top_k);
+    st = join(s_stats, team, lane, c);
+    if constexpr (TOP) {
+      for (int i = threadIdx.x; i < a.top_k; i += kThreads) sh.found[i] = 0;
+      __syncthreads();
+      rank_list(sh, sh.list, int(team) * a.top_k, a.top_k);
+      __syncthreads();
+    }
   }
 
   const float rest = st.s + (st.n - 1.f);
