@@ -139,15 +139,19 @@ class ExpertBlock:
                 for to, value in zip((tokens, logprob, entropy), self.scored_step(tokens)):
                     to.copy_(value)
 
-        keep = tokens.clone()
+        keep, cached = tokens.clone(), self.attention
+        if cached is not None:
+            if (cached.lengths >= cached.most).any():
+                raise ValueError("the cache has no place for a token: evict first")
+            weights = cached.mass.clone()
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
             step()  # first calls set the library's buffers up
             tokens.copy_(keep)
-            if self.attention is not None:  # as if it had not been
-                self.attention.lengths -= 1
-                self.attention.mass.zero_()
+            if cached is not None:  # as if it had not been
+                cached.lengths -= 1
+                cached.mass.copy_(weights)
         torch.cuda.current_stream().wait_stream(side)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):

@@ -52,6 +52,26 @@ def test_graph_and_eager_steps_agree(make, T):
     wcomp.device_check()
 
 
+def test_a_graph_made_in_the_middle_leaves_the_cache_as_it_was(make):
+    """Ten steps, then a graph: its first replay is the eager block's eleventh step; none is made on a full cache."""
+    eager, block = make(2), make(2)
+    tokens = torch.arange(2, device="cuda") * 5
+    for b in (eager, block):
+        now = tokens.clone()
+        for _ in range(10):
+            now = b.scored_step(now)[0]
+    mine, scores, mass = now.clone(), torch.empty(2, 2, device="cuda"), block.attention.mass.clone()
+    graph = block.graph(mine, *scores)
+    assert torch.equal(block.attention.mass, mass) and (block.attention.lengths == 10).all()
+    graph.replay()
+    want = eager.scored_step(now)
+    assert torch.equal(mine, want[0]) and torch.equal(scores[0], want[1]) and torch.equal(scores[1], want[2])
+    assert torch.equal(block.attention.mass, eager.attention.mass)
+    block.attention.lengths.fill_(block.attention.most)
+    with pytest.raises(ValueError):
+        block.graph(mine, *scores)
+
+
 def test_the_attention_is_the_definition(make):
     """Keys, values and queries as the projection gives them; what is gathered decides an eviction."""
     from decode_gemv_sign_gb300 import wcomp

@@ -296,6 +296,28 @@ def test_attention_over_long_sequences(W, D, share, n):
     W.device_check()
 
 
+@pytest.mark.parametrize("D,share,window", [(64, 3, 0), (128, 1, 0), (128, 4, 100), (256, 2, 0)])
+def test_attention_of_whole_prompts(W, D, share, window):
+    """Every row of its prompt: many tiles of rows, each of which sees more pages than the one before."""
+    lengths = [333, 1, 150]
+    b = Batch(W, lengths, 2, D, seed=D)
+    q = draw((sum(lengths), 2 * share, D), np.random.default_rng(D + share), 1.5)
+    attend_matches(W, b, q, lengths, window=window)
+    W.device_check()
+
+
+@pytest.mark.parametrize("D,share", [(64, 8), (128, 4), (128, 12), (256, 1)])
+@pytest.mark.parametrize("B,width", [(1, 33), (2, 500), (3, 90), (9, 60), (20, 49), (40, 17), (76, 5), (77, 5)])
+def test_attention_by_blocks_and_clusters_of_any_size(W, D, share, B, width):
+    """Batches that leave a tile one to sixteen blocks, and those whose tables are too wide for that."""
+    rng = np.random.default_rng(B)
+    lengths = [int(n) for n in rng.integers(0, 64 * min(width, 12) + 1, B)]
+    lengths[-1] = min(64 * width, 1500)
+    b = Batch(W, lengths, 2, D, seed=B, width=width)
+    attend_matches(W, b, draw((B, 2 * share, D), rng, 1.5), [1] * B, starts=False)
+    W.device_check()
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.25, 1e-6, 3.0])
 def test_attention_with_other_scales(W, scale):
     b = Batch(W, [300, 64], 2, 128, seed=4)

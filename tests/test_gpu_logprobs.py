@@ -163,6 +163,25 @@ def test_many_rows_repeat_bit_for_bit(W):
     assert torch.equal(alone[3][0], a[3][17]) and abs(float(alone[0][0] - a[0][17])) < 1e-5
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_long_rows_by_one_block(W, dtype):
+    """Rows too many to be shared, and longer than one batch for each of a block's buckets."""
+    T, V = 310, 300007
+    g = torch.Generator(device="cuda").manual_seed(6)
+    logits = (torch.randn(T, V, device="cuda", generator=g) * 3).to(torch.float32 if dtype == "fp32" else torch.bfloat16)
+    logits[3] = 1.0
+    logits[4, :V - 70] = float("-inf")
+    ids = torch.randint(V - 70, V, (T,), device="cuda", generator=g)
+    lp, _, top, top_ids = W.logprobs(logits, ids, 64)
+    pick = [0, 1, 2, 3, 4, 151, 152, 303, 304, 309]
+    some = logits[pick].double()
+    order = torch.sort(logits[pick].float(), dim=1, descending=True, stable=True).indices[:, :64]
+    assert torch.equal(top_ids[pick].long(), order)
+    want = torch.log_softmax(some, 1)
+    assert (lp[pick].double() - want.gather(1, ids[pick, None])[:, 0]).abs().max() < 1e-5
+    assert (top[pick].double() - want.gather(1, order)).abs().max() < 1e-5
+
+
 def test_no_rows(W):
     lp, ent, top, ids = W.logprobs(torch.empty(0, 10, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda"), 3)
     assert lp.shape == ent.shape == (0,) and top.shape == ids.shape == (0, 3)
