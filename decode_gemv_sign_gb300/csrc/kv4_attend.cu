@@ -30,7 +30,9 @@
 // Where the tables leave a warp few pages even if a tile is given to one block or
 // one cluster, that is done instead: one kernel without a workspace, the parts
 // joined through the cluster's shared memory.  One sequence of 4097 tokens, 32 query
-// and 8 cached heads: 12.5 us, cut anywhere 20.8.
+// and 8 cached heads: 12.5 us, cut anywhere 20.8.  A cluster that has all rows of a
+// sequence and head adds their tokens' weights too: 16.4 us instead of 20.5 with the
+// kernel that else does it.
 #include <algorithm>
 #include <cmath>
 
@@ -54,7 +56,7 @@ struct AttendArgs {
   int q_vec, out_vec;  // q's rows are 16-byte, out 8-byte aligned
   float scale;
   // workspace
-  float* lse2;       // [T, q_heads], in base 2 (with mass)
+  float* lse2;       // [T, q_heads], in base 2, or null (with mass)
   float* part;       // [2 warps][rows][D]: sums
   float2* part_ml;   // [2 warps][rows]: maximum (base 2) and sum
   uint32_t warps;    // of the attention kernel
@@ -630,7 +632,67 @@ __device__ __forceinline__ void store_out(const AttendArgs& a, int64_t at, const
 __device__ __forceinline__ void store_lse(const AttendArgs& a, int64_t row, float m, float l) {
   const float y = m + log2f(l);  // -inf where nothing is seen
   if (a.lse) a.lse[row] = y * kLn2;
-  if (a.mass) a.lse2[row] = y;
+  if (a.lse2) a.lse2[row] = y;
+}
+
+// What a tile's rows give to the tokens' weights: exp2(score - log-sum-exp), summed.
+template <int D, int NT>
+struct Weights {
+  float lse[NT][2];  // base 2
+  int lo[NT][2], hi[NT][2];
+  bool far = false;
+  // lse_of(index in lse, row of the tile)
+  template <class F>
+  __device__ __forceinline__ void load(const AttendArgs& a, const Seq& s, int tile, int head, int lane, F lse_of) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int64_t row = Tile<D, NT>::row(a, s, tile, head, n, e, lane, lo[n][e], hi[n][e]);
+        const float y = lse_of(row, 8 * n + 2 * (lane & 3) + e);
+        lse[n][e] = row >= 0 ? y : INFINITY;  // a place without a row adds 0
+      }
+    far = any_far<NT>(lse);
+  }
+  // Add the scores z of a page to the sums of its tokens 8 k + r.
+  __device__ __forceinline__ void add(const Tile<D, NT>& tile, int page, int lane, float (&z)[4][NT][4],
+                                      float (&sum)[8]) const {
+    const int r = lane >> 2;
+    if (far) tile.distances(lse, z);
+    const bool all = tile.sees_all(page);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float c = far ? 1.f : tile.c[n][e], from = far ? 0.f : lse[n][e];
+        if (all) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sum[k] += exp2_approx(__fmaf_rn(z[k / 2][n][e + 2 * (k % 2)], c, -from));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (page * kPage + 8 * k + r >= lo[n][e] && page * kPage + 8 * k + r < hi[n][e])
+              sum[k] += exp2_approx(__fmaf_rn(z[k / 2][n][e + 2 * (k % 2)], c, -from));
+        }
+      }
+  }
+};
+// The sums of a page's tokens to mass.
+__device__ __forceinline__ void add_mass(const AttendArgs& a, int b, uint32_t head, int n, int page, int lane,
+                                         float (&sum)[8]) {
+  // over the four lanes of a token: after each exchange a lane goes on with half of them
+#pragma unroll
+  for (int d = 4, bit = 1; d >= 2; d /= 2, bit *= 2) {
+#pragma unroll
+    for (int k = 0; k < d; ++k) {
+      const float keep = (lane & bit) ? sum[k + d] : sum[k], give = (lane & bit) ? sum[k] : sum[k + d];
+      sum[k] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
+    }
+  }
+  const int pos = page * kPage + 8 * (4 * (lane & 1) + (lane & 2)) + (lane >> 2);
+  float* mass = a.mass + (uint64_t(b) * a.s.heads + head) * (uint64_t(a.s.width) * kPage) + pos;
+  if (pos < n) mass[0] += sum[0];
+  if (pos + 8 < n) mass[8] += sum[1];
 }
 
 // Warps, and what a warp's ring holds: blocks, or halves of blocks (the weights'
@@ -981,7 +1043,7 @@ __device__ __forceinline__ float cluster_lds(uint32_t at, uint32_t rank) {
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
-    kv4_attend_team_kernel(const __grid_constant__ AttendArgs a, uint32_t team) {
+    kv4_attend_team_kernel(const __grid_constant__ AttendArgs a, uint32_t team, bool weigh) {
   constexpr int kWarps = Shape<D, NT>::kWarps, kDepth = Shape<D, NT>::kBlocks, R = 8 * NT, V = D / 32;
   using Src = KvSrc<D, false>;
   struct At {
@@ -990,6 +1052,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     uint32_t head;
   };
   __shared__ float2 s_ml[kWarps][R], s_joined[R];
+  __shared__ float s_lse[R];  // base 2, of the rows that this block finishes
   extern __shared__ __align__(128) uint8_t smem_raw[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t smem = smem_u32(smem_raw) + (-smem_u32(smem_raw) & 127u);
@@ -1041,6 +1104,29 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     issue(ring.slot);
     ring.next();
   }
+  // The weights of its pages, once the rows' log-sum-exps are known (row's by lse_of); the
+  // stages' stores and loads are behind a barrier.
+  auto weigh_pages = [&](auto lse_of) {
+    Weights<D, NT> weights;
+    weights.load(a, at.q, at.tile, int(at.head), lane, [&](int64_t, int row) { return lse_of(row); });
+    ahead = 0;
+#pragma unroll 1
+    for (uint32_t i = 0, slot = ring.slot; i < kDepth; ++i, slot = slot + 1 == kDepth ? 0 : slot + 1) issue(slot);
+#pragma unroll 1
+    for (int k = 0; k < count; ++k) {
+      const int page = at.q.page0 + first + k * stride;
+      ring.wait(lane);
+      if ((there >> ring.slot & 1) && !tile.sees_none(page)) {
+        float z[4][NT][4], sum[8] = {};
+        tile.scores(ring.stage(), lane, magic, z);
+        weights.add(tile, page, lane, z, sum);
+        add_mass(a, b, at.head, at.q.n, page, lane, sum);
+      }
+      __syncwarp();
+      issue(ring.slot);
+      ring.next();
+    }
+  };
   // the warp's sums to its own stages
   const uint32_t q = uint32_t(lane) & 3, r = uint32_t(lane) >> 2;
   float* const stages = reinterpret_cast<float*>(smem_raw + (smem - smem_u32(smem_raw)));
@@ -1093,12 +1179,19 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     const float f = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int k = 0; k < V; ++k) a.out[to * D + lane + 32 * k] = uint16_t(bf16x2_bits(x[k] * f, 0.f));
-    if (lane == 0) store_lse(a, to, m, l);
+    if (lane == 0) {
+      store_lse(a, to, m, l);
+      s_lse[row] = m + log2f(l);
+    }
   };
   if (team == 1) {
 #pragma unroll
     for (int j = 0; j < kRows; ++j)
       if (warp + j * kWarps < R) finish(warp + j * kWarps, ml[j].x, ml[j].y, o[j]);
+    if (!weigh) return;
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // copies follow stores to the stages
+    __syncthreads();
+    weigh_pages([&](int row) { return s_lse[row]; });
     return;
   }
   __syncthreads();  // the parts have been read
@@ -1130,7 +1223,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     }
     finish(row, m, l, x);
   }
+  if (weigh) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   cluster_sync();  // a block's shared memory stays while others read it
+  if (!weigh) return;
+  weigh_pages([&](int row) { return cluster_lds(smem_u32(&s_lse[row]), uint32_t(row) % team); });
+  cluster_sync();
 }
 
 // The weight of every token: the scores again, from the keys alone, against the
@@ -1164,12 +1261,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(con
   for (int i = 0; i < kDepth; ++i) pages.issue(a, ring, uint32_t(i), lane);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the log-sum-exps are there
   Tile<D, NT> tile;
-  float lse[NT][2];
-  int lo[NT][2], hi[NT][2];
+  Weights<D, NT> weights;
   int b = -1, held = 0;
   uint32_t head = 0;  // what the tile holds
-  bool far = false;
-  const uint32_t r = uint32_t(lane) >> 2, q = uint32_t(lane) & 3;
   for (; u < end; ++u) {
     if (at.page < 0) {
       __syncwarp();
@@ -1188,50 +1282,14 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(con
           head = at.head;
           held = t;
           tile.load(a, at.q, t, int(head), lane);
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int64_t row = Tile<D, NT>::row(a, at.q, t, int(head), n, e, lane, lo[n][e], hi[n][e]);
-              lse[n][e] = row >= 0 ? a.lse2[row] : INFINITY;  // a place without a row adds 0
-            }
-          far = any_far<NT>(lse);
+          weights.load(a, at.q, t, int(head), lane, [&](int64_t row, int) { return row >= 0 ? a.lse2[row] : 0.f; });
         }
         if (tile.sees_none(page)) continue;
         float z[4][NT][4];
         tile.scores(ring.stage(), lane, magic, z);
-        if (far) tile.distances(lse, z);
-        const bool all = tile.sees_all(page);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float c = far ? 1.f : tile.c[n][e], from = far ? 0.f : lse[n][e];
-            if (all) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                sum[k] += exp2_approx(__fmaf_rn(z[k / 2][n][e + 2 * (k % 2)], c, -from));
-            } else {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                if (page * kPage + 8 * k + int(r) >= lo[n][e] && page * kPage + 8 * k + int(r) < hi[n][e])
-                  sum[k] += exp2_approx(__fmaf_rn(z[k / 2][n][e + 2 * (k % 2)], c, -from));
-            }
-          }
+        weights.add(tile, page, lane, z, sum);
       }
-      // over the four lanes of a token: after each exchange a lane goes on with half of them
-#pragma unroll
-      for (int d = 4, bit = 1; d >= 2; d /= 2, bit *= 2) {
-#pragma unroll
-        for (int k = 0; k < d; ++k) {
-          const float keep = (lane & bit) ? sum[k + d] : sum[k], give = (lane & bit) ? sum[k] : sum[k + d];
-          sum[k] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
-        }
-      }
-      const int pos = page * kPage + 8 * (4 * int(q & 1) + 2 * int(q >> 1)) + int(r);
-      float* mass = a.mass + (uint64_t(at.b) * a.s.heads + at.head) * (uint64_t(a.s.width) * kPage) + pos;
-      if (pos < at.q.n) mass[0] += sum[0];
-      if (pos + 8 < at.q.n) mass[8] += sum[1];
+      add_mass(a, at.b, at.head, at.q.n, page, lane, sum);
     }
     __syncwarp();
     pages.issue(a, ring, ring.slot, lane);
@@ -1341,17 +1399,19 @@ int attend(AttendArgs& a, int dev, cudaStream_t s) {
   a.warps = sms * Shape<D, NT>::kWarps;
   auto up = [](uint64_t x) { return (x + 255) & ~uint64_t(255); };
   const uint64_t slots = team ? 0 : uint64_t(2) * a.warps * 8 * NT;
-  const uint64_t b_lse = a.mass ? up(uint64_t(a.T) * a.q_heads * 4) : 0, b_ml = up(slots * 8), b_part = slots * D * 4;
+  // where a cluster has all rows of a sequence and head it weighs the tokens too
+  const bool weigh = a.mass && team && !a.s.starts && a.share <= 8 * NT;
+  const uint64_t b_lse = a.mass && !weigh ? up(uint64_t(a.T) * a.q_heads * 4) : 0, b_ml = up(slots * 8), b_part = slots * D * 4;
   uint8_t* ws = nullptr;
   if (b_lse + b_ml + b_part) {
     e = pool_alloc(reinterpret_cast<void**>(&ws), b_lse + b_ml + b_part, s);
     if (e != cudaSuccess) return map_cuda(e);
   }
-  a.lse2 = reinterpret_cast<float*>(ws);
+  a.lse2 = a.mass && !weigh ? reinterpret_cast<float*>(ws) : nullptr;
   a.part_ml = reinterpret_cast<float2*>(ws + b_lse);
   a.part = reinterpret_cast<float*>(ws + b_lse + b_ml);
   if (team) {
-    e = launch(kv4_attend_team_kernel<D, NT>, uint32_t(tiles * a.s.heads) * team, kThreads, smem, false, team, s, a, team);
+    e = launch(kv4_attend_team_kernel<D, NT>, uint32_t(tiles * a.s.heads) * team, kThreads, smem, false, team, s, a, team, weigh);
   } else {
     e = launch(kv4_attend_kernel<D, NT>, sms, kThreads, smem, false, 1, s, a);
     // few tiles have many parts: 1024 threads share them; many have two or three
@@ -1362,7 +1422,7 @@ int attend(AttendArgs& a, int dev, cudaStream_t s) {
                        : launch(kv4_join_kernel<D, NT, kSmall>, uint32_t(std::min<int64_t>(joins, int64_t(sms) * 4)), kSmall,
                                 0, true, 1, s, a, tiles);
   }
-  if (e == cudaSuccess && a.mass) e = launch(kv4_mass_kernel<D, NT>, sms, kThreads, smem, true, 1, s, a);
+  if (e == cudaSuccess && a.mass && !weigh) e = launch(kv4_mass_kernel<D, NT>, sms, kThreads, smem, true, 1, s, a);
   if (ws) cudaFreeAsync(ws, s);
   return map_cuda(e);
 }
