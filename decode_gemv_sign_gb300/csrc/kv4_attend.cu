@@ -57,6 +57,7 @@ struct AttendArgs {
   float scale;
   // workspace
   float* lse2;       // [T, q_heads], in base 2, or null (with mass)
+  float* scores;     // [B, heads, width, share, 64], in base 2, or null (with mass)
   float* part;       // [2 warps][rows][D]: sums
   float2* part_ml;   // [2 warps][rows]: maximum (base 2) and sum
   uint32_t warps;    // of the attention kernel
@@ -377,6 +378,22 @@ struct Tile {
         for (int k = 0; k < 4; ++k) {
           const float y = ref[n][k % 2];
           z[i][n][k] = __fsub_rn(__fmul_rn(z[i][n][k], c[n][k % 2]), y == -INFINITY ? 0.f : y);
+        }
+  }
+
+  // Keep the scores of a page for kv4_weigh_kernel: the tile has all rows of the sequence.
+  __device__ __forceinline__ void keep(const AttendArgs& p, int b, uint32_t head, int page, int lane,
+                                       const float (&z)[4][NT][4]) const {
+    const int r = lane >> 2, q = lane & 3;
+    float* to = p.scores + ((uint64_t(b) * p.s.heads + head) * uint32_t(p.s.width) + uint32_t(page)) * uint32_t(p.share * kPage);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (8 * n + 2 * q + e < p.share) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            to[(8 * n + 2 * q + e) * kPage + 8 * k + r] = z[k / 2][n][e + 2 * (k % 2)] * c[n][e];
         }
   }
 
@@ -772,7 +789,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
       ring.wait(lane);
       const bool look = (pages.there >> ring.slot & 1) && !tile.sees_none(page);
       float z[4][NT][4];
-      if (look) tile.scores(ring.stage(), lane, magic, z);
+      if (look) {
+        tile.scores(ring.stage(), lane, magic, z);
+        if (a.scores) tile.keep(a, at.b, at.head, page, lane, z);
+      }
       if (kSplit) {
         __syncwarp();
         pages.issue(a, ring, ring.slot, lane);
@@ -1299,6 +1319,74 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(con
   }
 }
 
+// The weight of every token from the scores that the attention has kept: for sequences
+// of one row.  16 sequences of 16384 tokens, 128 columns, 4 query rows a cached head: the
+// stores take 4 us of the attention's time and this 18, the keys again 54; 8 rows 32 and
+// 55.
+constexpr int kWeigh = 512, kPagesAtOnce = 4;
+__global__ void __launch_bounds__(kWeigh, 3) kv4_weigh_kernel(const __grid_constant__ AttendArgs a) {
+  constexpr int kWarps = kWeigh / 32;
+  using W = Walk<kWeigh, 8, false>;
+  __shared__ uint64_t s_before[kWeigh + 1], s_warp[kWarps];
+  __shared__ W s_at[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  sum_units<kWeigh, 8, false>(a, s_before, s_warp);
+  const Runs runs{s_before[kWeigh], gridDim.x * kWarps};
+  uint64_t u = runs.first(blockIdx.x * kWarps + uint32_t(warp));
+  const uint64_t end = runs.first(blockIdx.x * kWarps + uint32_t(warp) + 1);
+  W& at = s_at[warp];
+  if (lane == 0 && u < end) at.find(a, s_before, u);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // scores and log-sum-exps are there
+  __syncwarp();
+  while (u < end) {
+    if (at.page < 0) {
+      if (++u == end) break;
+      __syncwarp();
+      if (lane == 0) at.page = 0;
+      __syncwarp();
+    }
+    const int n = at.q.n, lo = a.window ? n - a.window : 0;
+    const int from = at.q.page0 + at.page, stop = int(min(int64_t(at.q.page0 + at.q.pages), int64_t(from) + int64_t(end - u)));
+    u += uint64_t(stop - from);
+    const uint64_t first = (uint64_t(at.b) * a.s.heads + at.head) * uint32_t(a.s.width);  // of the sequence and head's pages
+    const float lse = lane < a.share ? a.lse2[int64_t(at.b) * a.q_heads + at.head * uint32_t(a.share) + lane] : 0.f;
+    for (int base = from; base < stop; base += 32) {
+      const bool there = base + lane < stop && (base + lane) * kPage < n && kv_page(a.s, at.b, base + lane) >= 0;
+      const uint32_t some = __ballot_sync(0xffffffffu, there);
+      for (int j0 = 0; j0 < 32; j0 += kPagesAtOnce) {
+        if (!(some >> j0 & ((1u << kPagesAtOnce) - 1u))) continue;
+        const float2* x = reinterpret_cast<const float2*>(a.scores + (first + uint32_t(base + j0)) * uint32_t(a.share * kPage)) + lane;
+        float2 sum[kPagesAtOnce] = {};
+#pragma unroll 2
+        for (int row = 0; row < a.share; ++row) {
+          const float y = __shfl_sync(0xffffffffu, lse, row);
+#pragma unroll
+          for (int j = 0; j < kPagesAtOnce; ++j)
+            if (some >> (j0 + j) & 1) {
+              const float2 z = x[(j * a.share + row) * (kPage / 2)];
+              sum[j].x += exp2_approx(z.x - y);
+              sum[j].y += exp2_approx(z.y - y);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kPagesAtOnce; ++j)
+          if (some >> (j0 + j) & 1) {
+            const int pos = (base + j0 + j) * kPage + 2 * lane;
+            float* mass = a.mass + first * kPage + pos;
+            if (pos >= lo && pos < n) mass[0] += sum[j].x;
+            if (pos + 1 >= lo && pos + 1 < n) mass[1] += sum[j].y;
+          }
+      }
+    }
+    __syncwarp();
+    if (lane == 0 && u < end) {
+      at.page = at.q.pages - 1;
+      at.next(a);
+    }
+    __syncwarp();
+  }
+}
+
 template <class K, class... ARGS>
 cudaError_t launch(K kernel, uint32_t grid, int threads, uint32_t smem, bool dependent, uint32_t cluster,
                    cudaStream_t s, const ARGS&... args) {
@@ -1384,6 +1472,8 @@ uint32_t team_of(const AttendArgs& a, int64_t segments, uint32_t sms, const Clus
   return pages <= int64_t(4) * team * Shape<D, NT>::kWarps ? team : 0;
 }
 
+constexpr uint64_t kMostScores = uint64_t(256) << 20;
+
 template <int D, int NT>
 int attend(AttendArgs& a, int dev, cudaStream_t s) {
   constexpr int kThreads = Shape<D, NT>::kThreads;
@@ -1401,15 +1491,21 @@ int attend(AttendArgs& a, int dev, cudaStream_t s) {
   const uint64_t slots = team ? 0 : uint64_t(2) * a.warps * 8 * NT;
   // where a cluster has all rows of a sequence and head it weighs the tokens too
   const bool weigh = a.mass && team && !a.s.starts && a.share <= 8 * NT;
-  const uint64_t b_lse = a.mass && !weigh ? up(uint64_t(a.T) * a.q_heads * 4) : 0, b_ml = up(slots * 8), b_part = slots * D * 4;
+  // Scores are kept rather than computed again where each sequence has one tile of
+  // them and they are not too many.
+  const uint64_t scores = uint64_t(a.s.B) * a.s.heads * uint64_t(a.s.width) * uint64_t(a.share) * (kPage * 4);
+  const bool kept = a.mass && !team && !a.s.starts && a.share <= 8 * NT && scores <= kMostScores;
+  const uint64_t b_lse = a.mass && !weigh ? up(uint64_t(a.T) * a.q_heads * 4) : 0, b_ml = up(slots * 8), b_part = slots * D * 4,
+                 b_scores = kept ? scores : 0;
   uint8_t* ws = nullptr;
-  if (b_lse + b_ml + b_part) {
-    e = pool_alloc(reinterpret_cast<void**>(&ws), b_lse + b_ml + b_part, s);
+  if (b_lse + b_ml + b_part + b_scores) {
+    e = pool_alloc(reinterpret_cast<void**>(&ws), b_lse + b_ml + b_part + b_scores, s);
     if (e != cudaSuccess) return map_cuda(e);
   }
   a.lse2 = a.mass && !weigh ? reinterpret_cast<float*>(ws) : nullptr;
   a.part_ml = reinterpret_cast<float2*>(ws + b_lse);
   a.part = reinterpret_cast<float*>(ws + b_lse + b_ml);
+  a.scores = kept ? reinterpret_cast<float*>(ws + b_lse + b_ml + b_part) : nullptr;
   if (team) {
     e = launch(kv4_attend_team_kernel<D, NT>, uint32_t(tiles * a.s.heads) * team, kThreads, smem, false, team, s, a, team, weigh);
   } else {
@@ -1422,7 +1518,8 @@ int attend(AttendArgs& a, int dev, cudaStream_t s) {
                        : launch(kv4_join_kernel<D, NT, kSmall>, uint32_t(std::min<int64_t>(joins, int64_t(sms) * 4)), kSmall,
                                 0, true, 1, s, a, tiles);
   }
-  if (e == cudaSuccess && a.mass && !weigh) e = launch(kv4_mass_kernel<D, NT>, sms, kThreads, smem, true, 1, s, a);
+  if (e == cudaSuccess && kept) e = launch(kv4_weigh_kernel, sms * 3, kWeigh, 0, true, 1, s, a);
+  else if (e == cudaSuccess && a.mass && !weigh) e = launch(kv4_mass_kernel<D, NT>, sms, kThreads, smem, true, 1, s, a);
   if (ws) cudaFreeAsync(ws, s);
   return map_cuda(e);
 }

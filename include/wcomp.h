@@ -599,8 +599,8 @@ typedef struct {
  * definition, those of tokens that a row does not see change nothing.  The sums
  * of |q k| have to stay below 2^112.  The order of the sums is fixed: repeated calls
  * give identical bits.
- * Memory: parts of sums come from the library's stream-ordered pool for the
- * duration of the call.  The device's error word is allocated with cudaMalloc on
+ * Memory: parts of sums, and with d_mass up to 256 MiB of scores, come from the
+ * library's stream-ordered pool for the duration of the call.  The device's error word is allocated with cudaMalloc on
  * first use (of any call on a cache or a 4-bit product): make the first call before any stream
  * capture.  T may be 0.
  */

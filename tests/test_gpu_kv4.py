@@ -307,14 +307,17 @@ def test_attention_of_whole_prompts(W, D, share, window):
 
 
 @pytest.mark.parametrize("D,share", [(64, 8), (128, 4), (128, 12), (256, 1)])
-@pytest.mark.parametrize("B,width", [(1, 33), (2, 500), (3, 90), (9, 60), (20, 49), (40, 17), (76, 5), (77, 5)])
+@pytest.mark.parametrize("B,width", [(1, 33), (2, 500), (3, 90), (9, 60), (20, 49), (40, 17), (76, 5), (77, 5),
+                                     (2, 1100), (20, 160), (100, 9)])
 def test_attention_by_blocks_and_clusters_of_any_size(W, D, share, B, width):
     """Batches that leave a tile one to sixteen blocks, and those whose tables are too wide for that."""
     rng = np.random.default_rng(B)
     lengths = [int(n) for n in rng.integers(0, 64 * min(width, 12) + 1, B)]
     lengths[-1] = min(64 * width, 1500)
     b = Batch(W, lengths, 2, D, seed=B, width=width)
-    attend_matches(W, b, draw((B, 2 * share, D), rng, 1.5), [1] * B, starts=False)
+    q = draw((B, 2 * share, D), rng, 1.5)
+    attend_matches(W, b, q, [1] * B, starts=False)
+    attend_matches(W, b, q, [1] * B, starts=False, window=100)
     W.device_check()
 
 
