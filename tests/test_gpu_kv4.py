@@ -436,6 +436,35 @@ def test_queries_that_are_not_finite(W):
     assert np.array_equal(got[0, rest], want[0, rest])
 
 
+@pytest.mark.parametrize("D,share", [(64, 16), (128, 8)])
+def test_weights_do_not_depend_on_how_they_are_found(W, D, share):
+    """From kept scores, from the keys again (too many scores to keep; rows given by starts), by a cluster."""
+    rng = np.random.default_rng(21)
+    H, width, B = 8, 1300, 16 if share == 8 else 8
+    n = 64 * width - 5
+    b = Batch(W, [3000], H, D, seed=2)
+    pages = b.table_np[0, :46]  # every sequence reads these again and again
+    table = ints(np.resize(pages, (B, width)))
+    lengths = ints([n, 0, 1, 700] + [100 * i for i in range(4, B)])
+    q = dev16(draw((B, H * share, D), rng, 1.5))
+
+    def weights(rows, wide=width, starts=None):
+        mass = torch.zeros(rows, H, wide * 64, device="cuda")
+        W.kv4_attend(b.cache, q[:rows], table[:rows, :wide].contiguous(), lengths[:rows].clamp(max=64 * wide), starts,
+                     mass=mass)
+        return mass.double().cpu()
+
+    again, kept, started = weights(B), weights(4), weights(B, starts=ints(range(B + 1)))
+    for got in (kept, started[:4]):
+        # scores and log-sum-exps of at most 32 are rounded at other places, 2^-19 each; sums of exponentials run in
+        # parts of at most 48 tokens a lane and 304 parts, 352 EPS; both in either call: below 2^-14
+        assert ((got - again[:4]).abs() <= 2 ** -14 * again[:4] + 1e-30).all()
+    few = weights(B, wide=30)[4:]
+    assert ((few - again[4:, :, :30 * 64]).abs() <= 2 ** -14 * few + 1e-30).all()
+    assert (again[0].sum(1) - share).abs().max() <= 2 ** -14 * share and (again[1] == 0).all()
+    W.device_check()
+
+
 def test_sequences_that_share_pages(W):
     """A common prefix is held once; sequences go on in pages of their own."""
     b = Batch(W, [128, 0, 0], 2, 128, width=4)
