@@ -1559,10 +1559,12 @@ extern "C" int wcomp_kv4_attend(const wcomp_kv4* c, const wcomp_kv4_attend_args*
   p.share = a.q_heads / c->heads;
   p.window = a.window;
   p.scale = a.scale;
-  // One tile of 8 where a sequence has no more rows, else tiles of 16 that read a page
-  // once: 64 x 8192 tokens, 128 columns, 16 rows 190 us, in two tiles of 8 232
-  // (64 columns: 115 and 137).  With 256 columns the registers do not hold 16.
-  const bool one = !a.s.d_starts && p.share <= 8;
+  // Tiles of 8 where sequences have no more (rows, heads of a group) on the average, else of
+  // 16, which read a page once: 64 x 8192 tokens, 128 columns, 16 of each sequence 190 us,
+  // in two tiles of 8 232; 8 of each 131, in half a tile of 16 187; 64 of every eighth
+  // sequence, which the average takes for 8, 111 and 125.  With 256 columns the registers
+  // do not hold 16.
+  const bool one = p.share <= 8 && a.T * p.share <= int64_t(8) * a.s.B;
   if (c->dim == 64) return one ? attend<64, 1>(p, c->device, s) : attend<64, 2>(p, c->device, s);
   if (c->dim == 128) return one ? attend<128, 1>(p, c->device, s) : attend<128, 2>(p, c->device, s);
   return attend<256, 1>(p, c->device, s);
