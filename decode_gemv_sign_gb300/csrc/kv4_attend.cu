@@ -23,7 +23,9 @@
 // Each warp takes an equal run of the call's (sequence, tile of rows, head, page)
 // units through a ring of its own, a tile's beginning and end counted as one more.
 // Where a tile's pages fall on several warps, a block joins its warps' parts in
-// shared memory and a second kernel those of blocks, always in the same order.
+// shared memory and a second kernel those of blocks, always in the same order.  A
+// part's sums are kept under a power of two that brings its sum of weights l to 1/8: the
+// sums of large values over many tokens are beyond fp32, their means are not.
 // Lengths are on the device, so every block sums up the work of all sequences
 // first.
 //
@@ -58,7 +60,7 @@ struct AttendArgs {
   // workspace
   float* lse2;       // [T, q_heads], in base 2, or null (with mass)
   float* scores;     // [B, heads, width, share, 64], in base 2, or null (with mass)
-  float* part;       // [2 warps][rows][D]: sums
+  float* part;       // [2 warps][rows][D]: sums times down_of(sum of weights)
   float2* part_ml;   // [2 warps][rows]: maximum (base 2) and sum
   uint32_t warps;    // of the attention kernel
 };
@@ -427,6 +429,13 @@ struct Tile {
     }
   }
 };
+
+// The power of two that brings a sum of weights to 1/8 .. 1/4, and back; one that is not
+// 0 is at least 1/2.
+__device__ __forceinline__ uint32_t exponent_of(float l) { return max(__float_as_uint(l) & 0x7F800000u, 126u << 23); }
+__device__ __forceinline__ float down_of(float l) { return __uint_as_float((251u << 23) - exponent_of(l)); }
+__device__ __forceinline__ float up_of(float l) { return __uint_as_float((3u << 23) + exponent_of(l)); }
+constexpr float kFew = 16.f;  // parts of up to so many warps or blocks, whose largest l is `most`, are summed under down_of(most) / kFew
 
 // Whether `ref`, of any row, is 2^22 or more from 0.
 template <int NT>
@@ -831,12 +840,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
           if (whole) store_lse(a, row, sums.m[n][e], l);
           else ml[8 * n + 2 * q + e] = make_float2(sums.m[n][e], l);
         }
-        const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+        const float f = !whole ? down_of(l) : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
         for (int i = 0; i < Kv<D>::G; ++i) {
           float x[4] = {sums.o[2 * i][n][e], sums.o[2 * i][n][2 + e], sums.o[2 * i + 1][n][e], sums.o[2 * i + 1][n][2 + e]};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = x[k] * back * f;
+          for (int k = 0; k < 4; ++k) x[k] = x[k] * f * back;
           if (whole)
             store_out(a, row * D + 32 * i + 4 * r, x);
           else
@@ -853,7 +862,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
     __syncwarp();
   }
   // Join the inner parts of neighbouring warps, which are one tile's: each of them takes
-  // some rows; the result is the first one's.
+  // some rows; the result is the first one's.  (Unrolled, these loops cost the one over the
+  // pages registers: 192 to 195 us with 16 rows of 128 columns, 64 sequences of 8192.)
   __syncthreads();
   if (!s_inner[warp]) return;
   auto same = [&](int w) {
@@ -872,16 +882,22 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
   }
   const uint64_t out = uint64_t(2 * (blockIdx.x * kWarps + w0)) * R;
   constexpr int V = D / 32;
+#pragma unroll 1
   for (int row = mine; row < R; row += parts) {
-    float m = -INFINITY, l = 0.f, o[V] = {};
+    float m = -INFINITY, most = 0.f, l = 0.f, o[V] = {};
+#pragma unroll 1
     for (int w = w0; w < w1; ++w)
-      if (s_inner[w]) m = fmaxf(m, s_ml[w][row].x);
-    const float from = m == -INFINITY ? 0.f : m;
+      if (s_inner[w]) {
+        m = fmaxf(m, s_ml[w][row].x);
+        most = fmaxf(most, s_ml[w][row].y);
+      }
+    const float from = m == -INFINITY ? 0.f : m, down = down_of(most) / kFew;
+#pragma unroll 1
     for (int w = w0; w < w1; ++w) {
       if (!s_inner[w]) continue;
       const float2 ml = s_ml[w][row];
-      const float f = exp2_approx(ml.x - from);
-      l += f * ml.y;
+      const float e = exp2_approx(ml.x - from), f = e * up_of(ml.y) * down;
+      l += e * ml.y;
       const float* x = reinterpret_cast<const float*>(smem_raw + (smem - smem_u32(smem_raw)) + w * kDepth * Src::kStage) +
                        row * D + lane;
 #pragma unroll
@@ -889,7 +905,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
     }
     if (lane == 0) a.part_ml[out + row] = make_float2(m, l);
 #pragma unroll
-    for (int k = 0; k < V; ++k) a.part[(out + row) * D + lane + 32 * k] = o[k];
+    for (int k = 0; k < V; ++k) a.part[(out + row) * D + lane + 32 * k] = o[k] * (down_of(l) * (up_of(most) * kFew));
   }
 }
 
@@ -996,14 +1012,20 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv4_join_kernel(const
         float next = m;
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) next = fmaxf(next, ml[k].x);
-        const float from = next == -INFINITY ? 0.f : next, down = exp2_approx(m - from);
+        const float from = next == -INFINITY ? 0.f : next, before = exp2_approx(m - from), had = before * up_of(l);
         m = next;
-        l *= down;
-        o = make_float4(o.x * down, o.y * down, o.z * down, o.w * down);
+        l *= before;
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
           const float f = exp2_approx(ml[k].x - from);
           l += ml[k].y * f;
+          ml[k].x = f * up_of(ml[k].y);
+        }
+        const float down = down_of(l);
+        o = make_float4(o.x * (had * down), o.y * (had * down), o.z * (had * down), o.w * (had * down));
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const float f = ml[k].x * down;
           o.x += x[k].x * f;
           o.y += x[k].y * f;
           o.z += x[k].z * f;
@@ -1019,18 +1041,18 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv4_join_kernel(const
         for (int g = 1; g < kGroups; ++g) m = fmaxf(m, s_ml[g][row].x);
         const float from = m == -INFINITY ? 0.f : m;
         l = 0.f;
+        for (int g = 0; g < kGroups; ++g) l += s_ml[g][row].y * exp2_approx(s_ml[g][row].x - from);
         o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int g = 0; g < kGroups; ++g) {
           const float2 ml = s_ml[g][row];
           const float4 x = s_o[g][item];
-          const float f = exp2_approx(ml.x - from);
-          l += ml.y * f;
+          const float f = exp2_approx(ml.x - from) * up_of(ml.y) * down_of(l);
           o = make_float4(o.x + x.x * f, o.y + x.y * f, o.z + x.z * f, o.w + x.w * f);
         }
       }
     }
     if (group == 0 && to >= 0) {
-      const float f = l == 0.f ? 0.f : 1.f / l;
+      const float f = l == 0.f ? 0.f : up_of(l) / l;
       const float x[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
       store_out(a, to * D + col, x);
       if (col == 0) store_lse(a, to, m, l);
@@ -1161,42 +1183,47 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       for (int d = 4; d <= 16; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
       const int row = 8 * n + 2 * int(q) + e;
       if (r == 0) s_ml[warp][row] = make_float2(sums.m[n][e], l);
+      const float f = down_of(l);
 #pragma unroll
       for (int i = 0; i < Kv<D>::G; ++i)
         *reinterpret_cast<float4*>(stages + warp * kPart + row * D + 32 * i + 4 * r) =
-            make_float4(sums.o[2 * i][n][e] * back, sums.o[2 * i][n][2 + e] * back, sums.o[2 * i + 1][n][e] * back,
-                        sums.o[2 * i + 1][n][2 + e] * back);
+            make_float4(sums.o[2 * i][n][e] * f * back, sums.o[2 * i][n][2 + e] * f * back,
+                        sums.o[2 * i + 1][n][e] * f * back, sums.o[2 * i + 1][n][2 + e] * f * back);
     }
   __syncthreads();
   // join the warps: each takes some rows
   const int parts = min(kWarps, max(0, at.q.pages - int(rank * kWarps)));
   constexpr int kRows = (R + kWarps - 1) / kWarps;
-  float o[kRows][V];
+  float o[kRows][V], up[kRows];  // o is under 1 / up
   float2 ml[kRows];
 #pragma unroll
   for (int j = 0; j < kRows; ++j) {
     const int row = warp + j * kWarps;
     if (row >= R) break;
-    float m = -INFINITY, l = 0.f;
-    for (int w = 0; w < parts; ++w) m = fmaxf(m, s_ml[w][row].x);
-    const float from = m == -INFINITY ? 0.f : m;
+    float m = -INFINITY, most = 0.f, l = 0.f;
+    for (int w = 0; w < parts; ++w) {
+      m = fmaxf(m, s_ml[w][row].x);
+      most = fmaxf(most, s_ml[w][row].y);
+    }
+    const float from = m == -INFINITY ? 0.f : m, down = down_of(most) / kFew;
 #pragma unroll
     for (int k = 0; k < V; ++k) o[j][k] = 0.f;
 #pragma unroll 4
     for (int w = 0; w < parts; ++w) {
       const float2 x = s_ml[w][row];
-      const float f = exp2_approx(x.x - from);
-      l += f * x.y;
+      const float e = exp2_approx(x.x - from), f = e * up_of(x.y) * down;
+      l += e * x.y;
 #pragma unroll
       for (int k = 0; k < V; ++k) o[j][k] += f * stages[w * kPart + row * D + lane + 32 * k];
     }
     ml[j] = make_float2(m, l);
+    up[j] = up_of(most) * kFew;
   }
-  auto finish = [&](int row, float m, float l, const float (&x)[V]) {
+  auto finish = [&](int row, float m, float l, float up, const float (&x)[V]) {  // x under 1 / up
     int lo, hi;
     const int64_t to = Tile<D, NT>::row(a, at.q, at.tile, int(at.head), row / 8, row % 2, row % 8 / 2, lo, hi);
     if (to < 0) return;
-    const float f = l == 0.f ? 0.f : 1.f / l;
+    const float f = l == 0.f ? 0.f : up / l;
 #pragma unroll
     for (int k = 0; k < V; ++k) a.out[to * D + lane + 32 * k] = uint16_t(bf16x2_bits(x[k] * f, 0.f));
     if (lane == 0) {
@@ -1207,7 +1234,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
   if (team == 1) {
 #pragma unroll
     for (int j = 0; j < kRows; ++j)
-      if (warp + j * kWarps < R) finish(warp + j * kWarps, ml[j].x, ml[j].y, o[j]);
+      if (warp + j * kWarps < R) finish(warp + j * kWarps, ml[j].x, ml[j].y, up[j], o[j]);
     if (!weigh) return;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // copies follow stores to the stages
     __syncthreads();
@@ -1220,8 +1247,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     const int row = warp + j * kWarps;
     if (row >= R) break;
     if (lane == 0) s_joined[row] = ml[j];
+    const float f = down_of(ml[j].y) * up[j];
 #pragma unroll
-    for (int k = 0; k < V; ++k) stages[row * D + lane + 32 * k] = o[j][k];
+    for (int k = 0; k < V; ++k) stages[row * D + lane + 32 * k] = o[j][k] * f;
   }
   cluster_sync();
   // join the blocks: a row a warp of all of them
@@ -1232,16 +1260,18 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     float m = mine.x;
 #pragma unroll
     for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float f = exp2_approx(mine.x - (m == -INFINITY ? 0.f : m));
+    const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mine.y)));
+    const float f = exp2_approx(mine.x - (m == -INFINITY ? 0.f : m)), down = down_of(most) / kFew;
+    const float to = f * up_of(mine.y) * down;
     float l = 0.f, x[V] = {};
 #pragma unroll 4
     for (uint32_t w = 0; w < team; ++w) {
-      const float g = __shfl_sync(0xffffffffu, f, w);
-      l += g * __shfl_sync(0xffffffffu, mine.y, w);
+      const float g = __shfl_sync(0xffffffffu, to, w);
+      l += __shfl_sync(0xffffffffu, f * mine.y, w);
 #pragma unroll
       for (int k = 0; k < V; ++k) x[k] += g * cluster_lds(smem + 4 * uint32_t(row * D + lane + 32 * k), w);
     }
-    finish(row, m, l, x);
+    finish(row, m, l, up_of(most) * kFew, x);
   }
   if (weigh) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   cluster_sync();  // a block's shared memory stays while others read it
