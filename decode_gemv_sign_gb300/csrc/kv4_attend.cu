@@ -16,7 +16,9 @@
 // A value row is read by token and transposed by a byte permutation of two
 // tokens' words.  vs * P is rounded to fp16 under a power of two that follows the
 // largest scale seen, which the sums O are kept under: one rounding of 2^-11, full
-// precision for products down to 2^-28 of the largest scale's.  The softmax's
+// precision for products down to 2^-28 of the largest scale's.  0 to 31 of its exponent
+// are in the weights' own (ordinary values then cost nothing; their sum is freed of it),
+// what is beyond that multiplies the scales, so that no weight is lost.  The softmax's
 // reference is the running maximum rounded up to a whole power of two, so that
 // going over to another scales exactly, by powers of two.
 //
@@ -448,11 +450,27 @@ __device__ __forceinline__ bool any_far(const float (&ref)[NT][2]) {
   return __any_sync(0xffffffffu, far);
 }
 
+// Multiply a page's scales of values by 2^d, in the warp's own stage: exact, but for those
+// below 2^-140 of the largest.  Copies to the stage follow behind.
+template <int D>
+__device__ __forceinline__ void scale_scales(uint32_t at, int d, int lane) {
+  const uint32_t f = __float_as_uint(power_of_two(d)) >> 16, f2 = f | f << 16;
+  __syncwarp();
+#pragma unroll
+  for (uint32_t i = 0; i < Kv<D>::G; ++i) {
+    uint32_t x = lds_u32(at + 4 * (32 * i + lane));
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(f2));
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * (32 * i + lane)), "r"(x) : "memory");
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+}
+
 // Sums of a tile so far, and the softmax's state.
 template <int D, int NT>
 struct Sums {
   static constexpr int G = Kv<D>::G;
-  static constexpr int kNoScale = 120;
+  static constexpr int kNoScale = 14 + 133;  // the least scale above 0 is 2^-133
   float m[NT][2], l[NT][2];  // reference (base 2, whole, or -inf) and, of the lane's tokens, sum
   float o[2 * G][NT][4];     // tile 2 g + i: column 32 g + 4 r + 2 i (+ 1: the last two) of the rows 2 q, 2 q + 1 (+ 8 n)
   int k;                     // o is under 2^k
@@ -565,10 +583,12 @@ struct Sums {
     if (hi > 0x7F80u) hi = 0;
     if (lo > 0x7F80u) lo = 0;
     const uint32_t largest = __reduce_max_sync(0xffffffffu, max(hi, lo));
-    if (largest) {
-      const int to = min(kNoScale, 14 - (int(largest >> 7) - 127));
-      if (to < k) {
-        const int d = to - k;
+    int kw = k;  // of k, what is in the weights
+    if (int(largest >> 7) + k > 14 + 127 || uint32_t(k) > 31u) {
+      // 14 less the exponent of the largest, BF16's normal numbers or those below
+      const int to = largest < 0x80u ? kNoScale - 31 + __clz(largest) : 14 + 127 - int(largest >> 7);
+      if (largest && to < k) {
+        const int d = max(to - k, -252);  // beyond it nothing is left either
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           scale(n, power_of_two(d / 2), power_of_two(d / 2));
@@ -576,13 +596,15 @@ struct Sums {
         }
         k = to;
       }
+      kw = min(max(k, 0), 31);
+      if (k != kw) scale_scales<D>(st + Kv<D>::kCodes, k - kw, lane);
     }
-    uint64_t w2[4][NT][2];  // weights under 2^k, a row's of the tokens 16 i + r and 16 i + 8 + r together
+    uint64_t w2[4][NT][2];  // weights under 2^kw, a row's of the tokens 16 i + r and 16 i + 8 + r together
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float shift = far ? float(k) : float(k) - (m[n][e] == -INFINITY ? 0.f : m[n][e]);
+        const float shift = far ? float(kw) : float(kw) - (m[n][e] == -INFINITY ? 0.f : m[n][e]);
         const float c = far ? 1.f : t.c[n][e];
         const uint64_t c2 = pair(c, c), shift2 = pair(shift, shift);
         uint64_t sum = 0;
@@ -592,7 +614,7 @@ struct Sums {
           w2[i][n][e] = pair(exp2_approx(first(x)), exp2_approx(second(x)));
           sum = i ? add2(sum, w2[i][n][e]) : w2[i][n][e];
         }
-        l[n][e] = __fmaf_rn(first(sum) + second(sum), power_of_two(-k), l[n][e]);
+        l[n][e] = __fmaf_rn(first(sum) + second(sum), power_of_two(-kw), l[n][e]);
       }
     uint32_t sc[G][4];
 #pragma unroll
@@ -817,7 +839,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
       pages.issue(a, ring, ring.slot, lane);
       ring.next();
     }
-    const float back = power_of_two(-sums.k);
+    const float back0 = power_of_two(-sums.k / 2), back1 = power_of_two(sums.k / 2 - sums.k);
     // an inner part goes to the warp's own stages, which nothing is copied to any more
     float* part = inner ? reinterpret_cast<float*>(smem_raw + (smem - smem_u32(smem_raw)) + warp * kDepth * Src::kStage)
                         : a.part + (uint64_t(2 * me + first) * R) * D;
@@ -840,12 +862,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
           if (whole) store_lse(a, row, sums.m[n][e], l);
           else ml[8 * n + 2 * q + e] = make_float2(sums.m[n][e], l);
         }
-        const float f = !whole ? down_of(l) : l == 0.f ? 0.f : 1.f / l;
+        const float f = back0 * (!whole ? down_of(l) : l == 0.f ? 0.f : 1.f / l);
 #pragma unroll
         for (int i = 0; i < Kv<D>::G; ++i) {
           float x[4] = {sums.o[2 * i][n][e], sums.o[2 * i][n][2 + e], sums.o[2 * i + 1][n][e], sums.o[2 * i + 1][n][2 + e]};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = x[k] * f * back;
+          for (int k = 0; k < 4; ++k) x[k] = x[k] * f * back1;
           if (whole)
             store_out(a, row * D + 32 * i + 4 * r, x);
           else
@@ -1173,7 +1195,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
   const uint32_t q = uint32_t(lane) & 3, r = uint32_t(lane) >> 2;
   float* const stages = reinterpret_cast<float*>(smem_raw + (smem - smem_u32(smem_raw)));
   constexpr int kPart = kDepth * int(Src::kStage) / 4;
-  const float back = power_of_two(-sums.k);
+  const float back0 = power_of_two(-sums.k / 2), back1 = power_of_two(sums.k / 2 - sums.k);
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -1183,12 +1205,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
       for (int d = 4; d <= 16; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
       const int row = 8 * n + 2 * int(q) + e;
       if (r == 0) s_ml[warp][row] = make_float2(sums.m[n][e], l);
-      const float f = down_of(l);
+      const float f = back0 * down_of(l);
 #pragma unroll
       for (int i = 0; i < Kv<D>::G; ++i)
         *reinterpret_cast<float4*>(stages + warp * kPart + row * D + 32 * i + 4 * r) =
-            make_float4(sums.o[2 * i][n][e] * f * back, sums.o[2 * i][n][2 + e] * f * back,
-                        sums.o[2 * i + 1][n][e] * f * back, sums.o[2 * i + 1][n][2 + e] * f * back);
+            make_float4(sums.o[2 * i][n][e] * f * back1, sums.o[2 * i][n][2 + e] * f * back1,
+                        sums.o[2 * i + 1][n][e] * f * back1, sums.o[2 * i + 1][n][2 + e] * f * back1);
     }
   __syncthreads();
   // join the warps: each takes some rows

@@ -595,7 +595,9 @@ typedef struct {
  * the row's largest keeps its bits); softmax statistics and sums are fp32.  The
  * weights that multiply V are rounded to fp16 times the values' scales under a
  * power of two (half a step: 2^-11 of each; a product that is below 2^-28 of the
- * sequence's largest scale may err by 2^-39 of that).  Infinities and NaN follow the
+ * sequence's largest scale may err by 2^-39 of that).  Up to 31 of that power's exponent
+ * are added to a weight's own before it is raised, which rounds the weight by 2^-20 of
+ * itself; the log-sum-exps and mass are sums of such weights.  Infinities and NaN follow the
  * definition, those of tokens that a row does not see change nothing.  The sums
  * of |q k| have to stay below 2^112.  The order of the sums is fixed: repeated calls
  * give identical bits.

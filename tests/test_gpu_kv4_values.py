@@ -6,8 +6,9 @@ is at most the largest value, so nothing overflows on the way.
 import numpy as np
 import pytest
 
-from oracle.q4_moe_oracle import bf16
-from test_gpu_kv4 import Batch, attend_matches, draw
+from oracle import kv4_oracle as K
+from oracle.q4_moe_oracle import bf16, f64
+from test_gpu_kv4 import Batch, attend_matches, bits, dev16, draw
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -26,6 +27,24 @@ def W():
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("size", [2.0 ** -130, 2.0 ** -120, 1.0, 2.0 ** 90, 2.0 ** 121, 2.0 ** 125])
+@pytest.mark.parametrize("way", WAYS)
+def test_tokens_far_below_the_largest_score_count(W, D, size, way):
+    """One token 5 to 14.8 nats above 4096 others: together they are some of the sum, each alone is little."""
+    width, rows = WAYS[way]
+    rng = np.random.default_rng(D)
+    n = 4097
+    k = np.zeros((n, 2, D))
+    k[rng.integers(0, n - rows), :, 0] = 14.8
+    v = np.clip(rng.standard_normal((n, 2, D)) * size, -2.0 ** 127, 2.0 ** 127)
+    b = Batch(W, [n], 2, D, k=bf16(k), v=bf16(v), width=width)
+    q = np.zeros((rows, 8, D))
+    q[..., 0] = np.linspace(0.33, 1.0, 8)
+    attend_matches(W, b, bf16(q), [rows], scale=1.0, starts=way == "rows")
+    W.device_check()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("way", WAYS)
 @pytest.mark.parametrize("n", [300, 4097])
 def test_many_tokens_of_the_largest_values(W, D, way, n):
@@ -37,4 +56,27 @@ def test_many_tokens_of_the_largest_values(W, D, way, n):
     b = Batch(W, [n], 2, D, k=bf16(rng.standard_normal((n, 2, D)) / 8), v=bf16(v), width=width)
     on, _, _ = attend_matches(W, b, draw((rows, 8, D), rng), [rows], starts=way == "rows")
     assert np.isfinite(on).all()
+    W.device_check()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_small_weights_of_tiny_values(W, D):
+    """Products 2^-25.6 of the largest scale's, 2^-120: their sum is the result where the heavy token's value is 0.
+
+    Each is off by at most 2^-11 of itself and 2^-39 of the largest scale, times a code of 7; the result is a BF16 number
+    below its normal range, off by half a step of 2^-133 besides.  So many sequences, of the same pages, that a warp has
+    all of one.
+    """
+    n, B, H, s = 2048, 300, 8, 2.0 ** -120
+    k, v = np.zeros((n, H, D)), np.full((n, H, D), 7 * s)
+    k[0, :, 0], v[0] = 17.72, 0.0
+    b = Batch(W, [n], H, D, k=bf16(k), v=bf16(v), width=32)
+    q = np.zeros((B, H, D))
+    q[..., 0] = 1.0
+    out = f64(bits(W.kv4_attend(b.cache, dev16(bf16(q)), b.table.expand(B, 32).contiguous(), b.len.expand(B).contiguous(),
+                                scale=1.0)))
+    p = 1.0 / (np.exp(b.ks[0][0, 0, 0]) + n - 1)
+    want = (n - 1) * p * 7 * s
+    tol = (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -20 + n * K.EPS) * want + n * 7 * s * 2.0 ** -39 + 2.0 ** -134
+    assert want > 2.0 ** -132 and (np.abs(out - want) <= tol).all(), (out.min(), out.max(), want, tol)
     W.device_check()
