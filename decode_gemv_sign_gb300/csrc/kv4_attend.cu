@@ -683,6 +683,15 @@ __device__ __forceinline__ void store_lse(const AttendArgs& a, int64_t row, floa
   if (a.lse2) a.lse2[row] = y;
 }
 
+// What a row of sequence b gets in place of 1 / its sum of weights where that is 0: 0 if it
+// sees no token; NaN, for 0 / 0, if all scores are -inf.
+__device__ __noinline__ float no_weight(const AttendArgs& a, int b, int lo, int hi) {
+#pragma unroll 1
+  for (int page = lo / kPage; page * kPage < hi; ++page)
+    if (kv_page(a.s, b, page) >= 0) return NAN;
+  return 0.f;
+}
+
 // What a tile's rows give to the tokens' weights: exp2(score - log-sum-exp), summed.
 template <int D, int NT>
 struct Weights {
@@ -862,7 +871,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_attend_kernel(c
           if (whole) store_lse(a, row, sums.m[n][e], l);
           else ml[8 * n + 2 * q + e] = make_float2(sums.m[n][e], l);
         }
-        const float f = back0 * (!whole ? down_of(l) : l == 0.f ? 0.f : 1.f / l);
+        const float f = back0 * (!whole ? down_of(l) : l == 0.f ? no_weight(a, at.b, lo, hi) : 1.f / l);
 #pragma unroll
         for (int i = 0; i < Kv<D>::G; ++i) {
           float x[4] = {sums.o[2 * i][n][e], sums.o[2 * i][n][2 + e], sums.o[2 * i + 1][n][e], sums.o[2 * i + 1][n][2 + e]};
@@ -1074,7 +1083,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv4_join_kernel(const
       }
     }
     if (group == 0 && to >= 0) {
-      const float f = l == 0.f ? 0.f : up_of(l) / l;
+      const float f = l == 0.f ? no_weight(a, b, lo, hi) : up_of(l) / l;
       const float x[4] = {o.x * f, o.y * f, o.z * f, o.w * f};
       store_out(a, to * D + col, x);
       if (col == 0) store_lse(a, to, m, l);
@@ -1245,7 +1254,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     int lo, hi;
     const int64_t to = Tile<D, NT>::row(a, at.q, at.tile, int(at.head), row / 8, row % 2, row % 8 / 2, lo, hi);
     if (to < 0) return;
-    const float f = l == 0.f ? 0.f : up / l;
+    const float f = l == 0.f ? no_weight(a, b, lo, hi) : up / l;
 #pragma unroll
     for (int k = 0; k < V; ++k) a.out[to * D + lane + 32 * k] = uint16_t(bf16x2_bits(x[k] * f, 0.f));
     if (lane == 0) {

@@ -8,7 +8,7 @@ import pytest
 
 from oracle import kv4_oracle as K
 from oracle.q4_moe_oracle import bf16, f64
-from test_gpu_kv4 import Batch, attend_matches, bits, dev16, draw
+from test_gpu_kv4 import Batch, attend_matches, bits, dev16, draw, ints
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -79,4 +79,27 @@ def test_small_weights_of_tiny_values(W, D):
     want = (n - 1) * p * 7 * s
     tol = (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -20 + n * K.EPS) * want + n * 7 * s * 2.0 ** -39 + 2.0 ** -134
     assert want > 2.0 ** -132 and (np.abs(out - want) <= tol).all(), (out.min(), out.max(), want, tol)
+    W.device_check()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("way", WAYS)
+def test_scores_that_are_all_minus_infinity(W, D, way):
+    """exp(z - lse) is then NaN, and so are out and the weights; rows that see no token have 0 and add nothing."""
+    width, rows = WAYS[way]
+    rng = np.random.default_rng(1)
+    k = rng.standard_normal((70, 2, D)) / 8
+    k[:, :, 3] = -1.0  # a code that is not 0
+    b = Batch(W, [70, 0], 2, D, k=bf16(k), width=width)
+    q = draw((2 * rows, 8, D), rng)
+    q[:, 5, 3] = 0x7F80
+    q[:rows, 1, 3] = 0xFF80
+    lse, mass = torch.empty(2 * rows, 8, device="cuda"), torch.zeros(2, 2, b.width * 64, device="cuda")
+    out = f64(bits(W.kv4_attend(b.cache, dev16(q), b.table, b.len, ints([0, rows, 2 * rows]) if way == "rows" else None,
+                                scale=1.0, lse=lse, mass=mass)))
+    lse, mass = lse.cpu().numpy(), mass.cpu().numpy()
+    assert np.isnan(out[:rows, [1, 5]]).all() and np.isfinite(np.delete(out[:rows], [1, 5], 1)).all()
+    assert np.isneginf(lse[:rows, 5]).all() and np.isfinite(np.delete(lse[:rows], [1, 5], 1)).all()
+    assert (out[rows:] == 0).all() and np.isneginf(lse[rows:]).all()
+    assert np.isnan(mass[0, :, :70 - rows + 1]).all() and (mass[0, :, 70:] == 0).all() and (mass[1] == 0).all()
     W.device_check()
