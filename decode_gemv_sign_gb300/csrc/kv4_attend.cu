@@ -99,7 +99,8 @@ __device__ __forceinline__ Seq load_seq(const AttendArgs& a, int b) {
     q.rows = 1;
   }
   q.tiles = TILES ? (q.rows * a.share + R - 1) / R : q.rows ? 1 : 0;
-  const int lo = a.window ? max(0, q.n - q.rows - a.window + 1) : 0;
+  const int at = q.n - q.rows;  // position of the first row; at - window alone may leave 32 bits
+  const int lo = a.window && at >= a.window ? at - a.window + 1 : 0;
   q.page0 = min(lo, max(q.n - 1, 0)) / kPage;
   q.pages = max(1, (q.n + kPage - 1) / kPage - q.page0);
   return q;
