@@ -464,25 +464,28 @@ __global__ void __launch_bounds__(kChoose, 2) kv4_choose_kernel(EvictArgs a, uin
 
 constexpr int kMove = 128;
 template <int D>
-__global__ void __launch_bounds__(kMove) kv4_move_kernel(EvictArgs a) {
+__global__ void __launch_bounds__(kMove, D == 256 ? 5 : 10) kv4_move_kernel(EvictArgs a) {
   using L = Kv<D>;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ int64_t s_src[kPage];  // the block's source, or -1, and the token in it
+  __shared__ int64_t s_src[kPage];  // the block's source and the token in it, or
+  constexpr int64_t kNothing = -1, kMissing = -2;  // no token; one of a page that does not exist
   __shared__ uint32_t s_at[kPage];
   const int64_t tiles = (a.keep + kPage - 1) / kPage;
   const int64_t units = int64_t(a.s.B) * a.s.heads * tiles;
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int64_t bh = unit / tiles;
     const int tile = int(unit % tiles), b = int(bh / a.s.heads), h = int(bh % a.s.heads);
+    bool missing = false;
     __syncthreads();
     if (threadIdx.x < kPage) {
       const int i = tile * kPage + int(threadIdx.x);
       const int pos = i < a.keep ? a.kept[bh * a.keep + i] : -1;
       const int page = pos < 0 ? -1 : kv_page(a.s, b, pos / kPage);
-      s_src[threadIdx.x] = page < 0 ? -1 : (int64_t(page) * a.s.heads + h) * L::kBlock;
+      missing = pos >= 0 && page < 0;
+      s_src[threadIdx.x] = pos < 0 ? kNothing : missing ? kMissing : (int64_t(page) * a.s.heads + h) * L::kBlock;
       s_at[threadIdx.x] = uint32_t(pos) % kPage;
     }
-    __syncthreads();
+    missing = __syncthreads_or(missing);
     if (a.kept[bh * a.keep + tile * kPage] < 0) continue;  // a shorter sequence: nothing here, no page needed
     const int out = a.table_out[int64_t(b) * a.width_out + tile];
     if (uint32_t(out) >= a.s.pages) {
@@ -517,6 +520,17 @@ __global__ void __launch_bounds__(kMove) kv4_move_kernel(EvictArgs a) {
     for (int k = 0; k < kScaleRounds; ++k) {
       const uint32_t j = threadIdx.x + k * kMove, t = j % kPage, g = j / kPage;
       if (s_src[t] >= 0) *reinterpret_cast<uint16_t*>(dst + g / L::G * L::kHalf + L::scale(t, g % L::G)) = y[k];
+    }
+    if (!missing) continue;
+    // rows of zeros in their places
+#pragma unroll 1
+    for (uint32_t j = threadIdx.x; j < kPage * kPieces; j += kMove) {
+      const uint32_t t = j / kPieces, piece = j % kPieces, part = piece / (kPieces / 2) * L::kHalf;
+      if (s_src[t] != kMissing) continue;
+      *reinterpret_cast<uint4*>(dst + part + L::at(t, piece % (kPieces / 2) * 16)) =
+          make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+      static_assert(kPieces == 2 * L::G, "as many scales as pieces");
+      *reinterpret_cast<uint16_t*>(dst + piece / L::G * L::kHalf + L::scale(t, piece % L::G)) = 0;
     }
   }
 }

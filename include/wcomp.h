@@ -626,7 +626,8 @@ typedef struct {
  * lowest position; a NaN ranks below everything), of shorter ones all.  What is
  * kept is copied bit for bit, in ascending order of its positions, to positions
  * 0, 1, ... of the pages in table_out, each head by its own choice; the old pages
- * are left as they are and may be shared with other sequences.  d_table_out ==
+ * are left as they are and may be shared with other sequences.  A kept token of a page
+ * outside the cache becomes a row of zeros.  d_table_out ==
  * d_table and d_lengths_out == d_lengths are refused; pages that are in both tables
  * leave the results undefined.
  * mass may be mass_out of an earlier call but not of this one.  Asynchronous.

@@ -1,10 +1,10 @@
-"""Eviction from long sequences, against its definition: weights beyond a block's registers, beyond its shared memory, and
-over the blocks of a cluster."""
+"""Eviction from long sequences, against its definition: weights beyond a block's registers, beyond its shared memory,
+and over the blocks of a cluster; and from tables with pages that do not exist."""
 import numpy as np
 import pytest
 
 from oracle import kv4_oracle as K
-from test_gpu_kv4 import Batch, dev16, ints
+from test_gpu_kv4 import Batch, bits, dev16, draw, ints, reported, same_values
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -82,3 +82,32 @@ def test_long_sequences_of_a_large_batch(W, kind):
     lengths = [int(n) for n in rng.integers(0, 30001, 160)]
     lengths[7], lengths[100] = 30000, 19457
     evicts(W, lengths, 469, 2, kind, 300, 20)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_tokens_of_pages_that_do_not_exist_become_zeros(W, D):
+    """What is kept of them is rows of zeros, not what the output pages held before."""
+    b = Batch(W, [200, 130], 2, D, width=4, spare=6)
+    free = [p for p in range(b.pages) if p not in set(b.table_np.flatten())]
+    out = ints(np.array(free[:4]).reshape(2, 2))
+    junk = dev16(draw((256, 2, D), np.random.default_rng(1)))
+    rng = np.random.default_rng(2)
+    m = rng.random((2, 2, 256)).astype(np.float32)
+    for page in (-1, b.pages, 2 ** 31 - 1, -2 ** 31):
+        W.kv4_append(b.cache, junk, junk, out, ints([128, 128]), ints([0, 128, 256]))
+        W.device_check()
+        table = b.table.clone()
+        table[0, 1] = page
+        kept = torch.empty(2, 2, 100, dtype=torch.int32, device="cuda")
+        n, mass = W.kv4_evict(b.cache, table, b.len, torch.from_numpy(m).cuda(), 100, 10, out, kept=kept)
+        reported(W)
+        k, v = (bits(t).reshape(2, 100, 2, D) for t in W.kv4_read(b.cache, out, n, ints([0, 100, 200]), rows=200))
+        for i, x in enumerate(b.lengths):
+            for h in range(2):
+                want = K.evict(m[i, h], x, 100, 10)
+                assert np.array_equal(kept[i, h].cpu().numpy(), want)
+                assert np.array_equal(mass[i, h, :100].cpu().numpy(), m[i, h, want])
+                there = ((want // 64 != 1) | (i == 1))[:, None]
+                same_values(k[i, :, h], np.where(there, b.ks[i][want, h], 0.0))
+                same_values(v[i, :, h], np.where(there, b.vs[i][want, h], 0.0))
+        W.device_check()
