@@ -108,7 +108,7 @@ __device__ __forceinline__ int64_t unit_rows(int64_t unit, uint32_t rounds, uint
 }
 
 template <int D, int STEPS>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(KvSeqs s, uint8_t* cache, Rows k, Rows v, int64_t T,
+__global__ void __launch_bounds__(kThreads, STEPS == 1 ? 10 : 9) kv4_append_kernel(KvSeqs s, uint8_t* cache, Rows k, Rows v, int64_t T,
                                                               uint32_t rounds, uint32_t span) {
   using I = Items<D, STEPS>;
   using L = Kv<D>;
@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(KvSeqs s, uint8_t*
       }
     }
   }
+  kv_check_starts(s, T, blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads);
 }
 
 // Eight codes times a scale, in pairs of BF16: a code under the exponent of 128 is 128
@@ -180,7 +181,7 @@ __device__ __forceinline__ uint4 values8(uint32_t w, uint32_t scale) {
 }
 
 template <int D, int STEPS>
-__global__ void __launch_bounds__(kThreads) kv4_read_kernel(KvSeqs s, const uint8_t* cache, uint16_t* k, uint16_t* v,
+__global__ void __launch_bounds__(kThreads, 12) kv4_read_kernel(KvSeqs s, const uint8_t* cache, uint16_t* k, uint16_t* v,
                                                             int64_t T, uint32_t rounds, uint32_t span, int vec) {
   using I = Items<D, STEPS>;
   using L = Kv<D>;
@@ -232,6 +233,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(KvSeqs s, const uint
       }
     }
   }
+  kv_check_starts(s, T, blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads);
 }
 
 // ---------------------------------------------------------------------------

@@ -95,6 +95,14 @@ __device__ __forceinline__ int64_t kv_position(const KvSeqs& s, int b, int64_t i
   return s.starts ? int64_t(n) - (s.starts[b + 1] - i) : int64_t(n) - 1;
 }
 
+// Report starts that descend, are negative or pass the call's T rows: thread `at` of `threads`.
+__device__ __forceinline__ void kv_check_starts(const KvSeqs& s, int64_t T, uint32_t at, uint32_t threads) {
+  if (!s.starts) return;
+#pragma unroll 1
+  for (int64_t b = at; b < s.B; b += threads)
+    if (s.starts[b] < 0 || s.starts[b + 1] < s.starts[b] || s.starts[b + 1] > T) kv_bad(s.err);
+}
+
 // Checks of a call's sequences on the host.
 int kv_check(const wcomp_kv4* c, const wcomp_kv4_seqs& s, int64_t T);
 int kv_seqs(const wcomp_kv4* c, const wcomp_kv4_seqs& s, KvSeqs* out);

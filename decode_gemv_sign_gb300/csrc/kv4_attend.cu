@@ -984,6 +984,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv4_join_kernel(const
   __shared__ float2 s_ml[kGroups][R];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   sum_units<THREADS, R, true>(a, s_before, s_warp);
+  if (blockIdx.x == 0) kv_check_starts(a.s, a.T, threadIdx.x, THREADS);  // for the attention too, which still runs
   const Runs runs{s_before[THREADS], a.warps};
   bool waited = false;
   for (int64_t unit = blockIdx.x; unit < tiles * a.s.heads; unit += gridDim.x) {
@@ -1139,7 +1140,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
   int b;
   at.head = blockIdx.x / team % a.s.heads;
   // the same for all of a cluster
-  if (!tile_at<R>(a, blockIdx.x / team / a.s.heads, b, at.tile, at.q)) return;
+  if (!tile_at<R>(a, blockIdx.x / team / a.s.heads, b, at.tile, at.q)) {
+    if (blockIdx.x == 0) kv_check_starts(a.s, a.T, threadIdx.x, 32 * kWarps);
+    return;
+  }
   // a warp's pages in the sequence: first + k * stride; the ids of 32 of them at a time
   const int first = int(rank * kWarps) + warp, stride = int(team * kWarps);
   const int count = max(0, (at.q.pages - first + stride - 1) / stride), pages = (at.q.n + kPage - 1) / kPage;
@@ -1267,6 +1271,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
 #pragma unroll
     for (int j = 0; j < kRows; ++j)
       if (warp + j * kWarps < R) finish(warp + j * kWarps, ml[j].x, ml[j].y, up[j], o[j]);
+    if (blockIdx.x == 0) kv_check_starts(a.s, a.T, threadIdx.x, 32 * kWarps);
     if (!weigh) return;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // copies follow stores to the stages
     __syncthreads();
@@ -1306,6 +1311,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     finish(row, m, l, up_of(most) * kFew, x);
   }
   if (weigh) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  if (blockIdx.x == 0) kv_check_starts(a.s, a.T, threadIdx.x, 32 * kWarps);
   cluster_sync();  // a block's shared memory stays while others read it
   if (!weigh) return;
   weigh_pages([&](int row) { return cluster_lds(smem_u32(&s_lse[row]), uint32_t(row) % team); });

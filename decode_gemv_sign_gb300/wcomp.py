@@ -620,8 +620,8 @@ class KV4:
     The calls on it take ``table`` (int32 [B, width]: the pages of each sequence; position p is place p % 64 of
     page table[b, p // 64]), ``lengths`` (int32 [B]: the tokens that each sequence holds, the call's own rows
     among them) and ``starts`` (int32 [B + 1]: rows starts[b] to starts[b + 1] - 1 are the newest tokens of
-    sequence b; None: one row a sequence).  All three are on the device; a page, length or row out of range is
-    skipped there and reported by ``device_check``.
+    sequence b; None: one row a sequence).  All three are on the device; a page or length out of range is
+    skipped there, starts that descend or leave the call's rows reach no others, and ``device_check`` reports them.
     """
 
     def __init__(self, handle: int, pages: int, heads: int, dim: int, device: torch.device):
@@ -827,7 +827,7 @@ def version() -> int:
 
 
 def device_check(stream=None) -> None:
-    """Raise if a kernel on this device reported a timed-out wait (clears the report)."""
+    """Raise if a kernel on this device reported a timed-out wait or an index out of range (clears the report)."""
     _check(lib().wcomp_device_check(P(_stream(stream))), "wcomp_device_check")
 
 

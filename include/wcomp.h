@@ -71,7 +71,7 @@ typedef enum {
   WCOMP_ETIMEOUT = -6,      /* a kernel's bounded wait on its own copies ran out */
   WCOMP_EINTERNAL = -7,     /* an internal consistency check failed; no result was returned */
   WCOMP_EBOUNDS = -8        /* an index check failed inside a kernel (the access was skipped): in a debug build, or
-                               a page, length or row of the 4-bit cache's calls outside its range */
+                               a page, length or start of the 4-bit cache's calls outside its range */
 } wcomp_status;
 
 typedef struct wcomp_container wcomp_container;
@@ -248,7 +248,7 @@ WCOMP_API int wcomp_gemv_batched(const wcomp_container* const* containers, const
  * bounded wait on its own tensor copies, or on its other thread blocks, runs
  * out records it there and finishes without waiting instead of hanging; its
  * outputs are then undefined.  The calls on a 4-bit key/value cache record there
- * a page, length or row that is out of range.  Other and later calls are not
+ * a page, length or start that is out of range.  Other and later calls are not
  * touched, by it or by this check, which may be made while others run.  In a debug build (compiled with WCOMP_DEBUG=1)
  * the kernels on containers and plain weights also check their indexes before
  * memory accesses, skip an access that fails and record it.  Synchronizes
@@ -537,7 +537,8 @@ typedef struct {
  * are no sequence's (from starts[B] on) are left as they were.
  * What cannot be checked on the host is checked in the kernels: a length above
  * width * 64 is taken as width * 64, a page outside the cache as if its tokens
- * were not there, and wcomp_device_check then reports WCOMP_EBOUNDS.
+ * were not there, and starts that are negative, descend or pass T leave the rows around
+ * them undefined but reach no others; wcomp_device_check then reports WCOMP_EBOUNDS.
  */
 typedef struct {
   const int32_t* d_table;   /* [B, width] pages */
