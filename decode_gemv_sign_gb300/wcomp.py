@@ -654,6 +654,8 @@ class KV4:
 
 def kv4_create(pages: int, heads: int, dim: int, stream=None) -> KV4:
     """A new cache on the current device; ``dim`` is 64, 128 or 256.  Its rows read as zeros."""
+    if not (-2 ** 63 <= pages < 2 ** 63 and -2 ** 31 <= heads < 2 ** 31 and -2 ** 31 <= dim < 2 ** 31):
+        raise ValueError("heads and dim must be within 32 bits, pages within 64")  # ctypes would cut them off
     h = P()
     _check(lib().wcomp_kv4_create(pages, heads, dim, _stream(stream), ctypes.byref(h)), "wcomp_kv4_create")
     return KV4(h.value, pages, heads, dim, torch.device("cuda", torch.cuda.current_device()))
@@ -745,6 +747,8 @@ def kv4_attend(c: KV4, q: torch.Tensor, table: torch.Tensor, lengths: torch.Tens
     T, Hq = q.shape[:2]
     if Hq < 1 or Hq % c.heads or (starts is None and T != s.B):
         raise ValueError("q must have a multiple of the cache's heads, and one row a sequence without starts")
+    if not 0 <= window < 2 ** 31:
+        raise ValueError("window must be within 0..2^31 - 1")
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=c.device)
     a = Kv4AttendArgs(s, *qp, _array(_bits16(out, "out"), "out", out.dtype, (T, Hq, c.dim), c.device),
