@@ -510,7 +510,7 @@ extern "C" int wcomp_logprobs(const wcomp_logprobs_args* args, void* stream) {
   if (!args) return WCOMP_EINVAL;
   const wcomp_logprobs_args& a = *args;
   if (a.T < 0 || a.V < 1 || a.row < a.V || (a.dtype != WCOMP_FP32 && a.dtype != WCOMP_BF16) || a.top_k < 0 ||
-      a.top_k > a.V || !(a.scale > 0.f) || !std::isfinite(a.scale) || (a.T && !a.d_logits) ||
+      a.top_k > a.V || !(a.scale > 0.f) || !std::isfinite(a.scale * kLog2e) || (a.T && !a.d_logits) ||
       (a.T && a.top_k && (!a.d_top_logprobs || !a.d_top_ids)) || (a.T && a.d_ids && !a.d_logprob))
     return WCOMP_EINVAL;
   if (reinterpret_cast<uintptr_t>(a.d_logits) % (a.dtype == WCOMP_BF16 ? 2 : 4) || !natural(a.d_ids) || !natural(a.d_logprob) ||

@@ -794,7 +794,8 @@ def logprobs(logits: torch.Tensor, ids: Optional[torch.Tensor] = None, top_k: in
              lse: Optional[torch.Tensor] = None, stream=None) -> tuple:
     """(logprob [T], entropy [T], top_logprobs [T, top_k], top_ids [T, top_k]) of logits [T, V] times ``scale``.
 
-    ``logits`` are float32 (what ``gemv`` gives) or bfloat16, a row's columns contiguous; ``ids`` (int64 [T]) are
+    ``logits`` are float32 (what ``gemv`` gives) or bfloat16, a row's columns contiguous; ``scale`` is above 0 and at
+    most 2^127; ``ids`` (int64 [T]) are
     the given tokens: a negative one gets logprob 0, one beyond the vocabulary NaN.  logprob is None without
     ids.  ``top_k`` (at most 64) alternatives, the largest first, ties by the lowest index; ids are int32; both are
     None for 0.  ``lse`` (float32 [T]) receives the log of the sum of exponentials.

@@ -657,7 +657,7 @@ typedef struct {
   int64_t T, V, row;
   int32_t dtype;         /* wcomp_dtype */
   int32_t top_k;         /* 0 <= top_k <= min(V, 64) */
-  float scale;           /* multiplies the logits (1 / temperature); above 0 */
+  float scale;           /* multiplies the logits (1 / temperature); above 0, at most 2^127 */
 } wcomp_logprobs_args;
 
 /*
@@ -671,7 +671,8 @@ typedef struct {
  * +inf, or with nothing but -inf, has NaN results, and its top_ids all the same.
  * Sums are fp32 and leave the row's largest term out until the end, so that small
  * entropies and log probabilities near 0 keep their bits.  The order of
- * the sums is fixed: repeated calls give identical bits.  V below 2^31.  T may be 0.
+ * the sums is fixed: repeated calls give identical bits.  V below 2^31, T below 2^28.  T may
+ * be 0.
  */
 WCOMP_API int wcomp_logprobs(const wcomp_logprobs_args* args, void* stream);
 
