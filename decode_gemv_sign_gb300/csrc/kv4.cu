@@ -3,6 +3,7 @@
 #include <new>
 #include <type_traits>
 
+#include "cluster.cuh"
 #include "kv4.cuh"
 #include "q4_rule.cuh"
 
@@ -12,11 +13,6 @@ namespace {
 constexpr int kThreads = 128;  // 256: 8% slower
 
 __device__ __forceinline__ float bf16_value(uint32_t bits) { return __uint_as_float(bits << 16); }
-__device__ __forceinline__ uint32_t bf16_bits(float v) {
-  uint16_t h;
-  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
-  return h;
-}
 
 // A row of keys or values is handled by D / 8 neighbouring lanes, lane u the columns
 // 8 u .. 8 u + 7; four of them share a group.  A warp takes `span` rows of the call,
@@ -29,7 +25,8 @@ __device__ __forceinline__ uint32_t bf16_bits(float v) {
 //    64       38 (45) us  0.66      33 (37) us  0.77
 //   128       68 (84)     0.75      58 (64)     0.87
 //   256      130 (161)    0.78     110 (119)    0.92
-// Four steps in flight leave room for fewer warps: 88 us for 75 at 128 columns.
+// Four steps in flight leave room for fewer warps: 88 us for 75 at 128 columns.  The least
+// numbers of blocks keep the compiler at the registers of these figures (56, not 72).
 template <int D, int STEPS>
 struct Items {
   static constexpr int kPer = D / 8;
@@ -263,24 +260,6 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ uint32_t team_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void team_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A word of block `rank`'s shared memory, at the place that p has in this one.
-__device__ __forceinline__ uint32_t team_load(const uint32_t* p, uint32_t rank) {
-  uint32_t v;
-  asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.u32 %0, [r];\n\t}"
-               : "=r"(v)
-               : "r"(smem_u32(p)), "r"(rank)
-               : "memory");
-  return v;
-}
-
 // The tokens of one sequence and head that are kept: one block, or a cluster of
 // them for long sequences.  A warp has a run of consecutive tokens, their keys in
 // registers as far as those go, so a step of the search for the last key taken is
@@ -298,7 +277,7 @@ __global__ void __launch_bounds__(kChoose, 2) kv4_choose_kernel(EvictArgs a, uin
   __shared__ Choose sh;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t rank = team > 1 ? team_rank() : 0;
+  const uint32_t rank = team > 1 ? cluster_rank() : 0;
   const int64_t unit = blockIdx.x / team;
   const int b = int(unit / a.s.heads);
   const int n = kv_length(a.s, b);
@@ -356,10 +335,10 @@ __global__ void __launch_bounds__(kChoose, 2) kv4_choose_kernel(EvictArgs a, uin
       c[j] = __reduce_add_sync(0xffffffffu, lane < kChooseWarps ? sh.sums[parity][lane][j] : 0u);
     if (team > 1) {
       if (tid < 3) sh.team[parity][tid] = c[tid];
-      team_sync();
+      cluster_sync();
 #pragma unroll
       for (int j = 0; j < 3; ++j)
-        c[j] = __reduce_add_sync(0xffffffffu, lane < team ? team_load(&sh.team[parity][j], lane) : 0u);
+        c[j] = __reduce_add_sync(0xffffffffu, lane < team ? cluster_lds_u32(smem_u32(&sh.team[parity][j]), lane) : 0u);
     }
     parity ^= 1;
   };
@@ -409,10 +388,10 @@ __global__ void __launch_bounds__(kChoose, 2) kv4_choose_kernel(EvictArgs a, uin
     }
     if (team > 1) {
       if (tid < 2) sh.team[parity][tid] = own[tid];
-      team_sync();
+      cluster_sync();
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const uint32_t v = lane < team ? team_load(&sh.team[parity][j], lane) : 0u;
+        const uint32_t v = lane < team ? cluster_lds_u32(smem_u32(&sh.team[parity][j]), lane) : 0u;
         before[j] += __reduce_add_sync(0xffffffffu, lane < rank ? v : 0u);
         c[j] = __reduce_add_sync(0xffffffffu, v);
       }
@@ -461,7 +440,7 @@ __global__ void __launch_bounds__(kChoose, 2) kv4_choose_kernel(EvictArgs a, uin
   }
   for (int i = m + int(rank * kChoose + tid); i < a.keep; i += int(team * kChoose)) kept[i] = -1;
   for (int i = m + int(rank * kChoose + tid); i < a.width_out * kPage; i += int(team * kChoose)) mass_out[i] = 0.f;
-  if (team > 1) team_sync();  // a block's shared memory stays while others read it
+  if (team > 1) cluster_sync();  // a block's shared memory stays while others read it
 }
 
 constexpr int kMove = 128;

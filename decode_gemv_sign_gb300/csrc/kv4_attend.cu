@@ -40,6 +40,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "cluster.cuh"
 #include "kv4.cuh"
 
 namespace wc {
@@ -254,11 +255,6 @@ struct Pages {
 // ---------------------------------------------------------------------------
 // Products.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint2 lds_v2(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
@@ -1097,25 +1093,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv4_join_kernel(const
 
 // A tile and head by one block, or by a cluster of up to 16: every warp takes every
 // (blocks x warps)-th page.
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A float of block `rank` at the shared-memory address that `at` is in this one.
-__device__ __forceinline__ float cluster_lds(uint32_t at, uint32_t rank) {
-  float v;
-  asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.f32 %0, [r];\n\t}"
-               : "=f"(v)
-               : "r"(at), "r"(rank)
-               : "memory");
-  return v;
-}
-
 template <int D, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1)
     kv4_attend_team_kernel(const __grid_constant__ AttendArgs a, uint32_t team, bool weigh) {

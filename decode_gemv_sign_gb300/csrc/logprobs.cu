@@ -21,6 +21,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "cluster.cuh"
 #include "host_shared.cuh"
 #include "pairs.cuh"
 
@@ -73,11 +74,6 @@ __device__ __forceinline__ float key_logit(uint64_t key) {
   return k == 0 ? NAN : __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float max_nan(float x, float y) {
   float z;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
@@ -124,14 +120,6 @@ __device__ __forceinline__ Stats join(const Stats* list, uint32_t n, int lane, f
   return {m, warp_sum(x.s), warp_sum(x.w), warp_sum(x.n)};
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // The address that a place of this block's shared memory has in the cluster's first.
 __device__ __forceinline__ uint32_t in_first(const void* p) {
   uint32_t a;

@@ -1,9 +1,15 @@
-// Two fp32 operations an instruction, on pairs of registers.
+// Two fp32 operations an instruction, on pairs of registers; and 2^x.
 #pragma once
 
 #include "wcomp_impl.cuh"
 
 namespace wc {
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
   uint64_t d;

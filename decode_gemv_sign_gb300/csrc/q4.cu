@@ -11,6 +11,7 @@
 #include <mutex>
 #include <new>
 
+#include "cluster.cuh"
 #include "q4_rule.cuh"
 #include "tile.cuh"
 
@@ -420,20 +421,6 @@ constexpr int kDepth = 2;  // stages of a warp: a third takes L1 from the activa
 // 4.4; with more units than blocks it lost 0.7 us on the GPU (16384 x 6144).
 constexpr uint32_t kXRecords = 8 * kWarps;
 constexpr uint32_t kXShared = kXRecords * (kRecord + 16 + factor_pitch<1>() * 4);
-
-__device__ __forceinline__ void cluster_sync() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A float of the cluster's CTA `rank` at the place that `a` has in this one.
-__device__ __forceinline__ float cluster_lds(uint32_t a, uint32_t rank) {
-  float v;
-  asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.f32 %0, [r];\n\t}"
-               : "=f"(v)
-               : "r"(a), "r"(rank)
-               : "memory");
-  return v;
-}
 
 template <int NG, int TILES, bool SHARED>
 constexpr uint32_t q4_smem() {
