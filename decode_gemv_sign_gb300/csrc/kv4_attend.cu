@@ -1367,7 +1367,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_mass_kernel(con
 // The weight of every token from the scores that the attention has kept: for sequences
 // of one row.  16 sequences of 16384 tokens, 128 columns, 4 query rows a cached head: the
 // stores take 4 us of the attention's time and this 18, the keys again 54; 8 rows 32 and
-// 55.
+// 55 (by columns and rows: at the launch).
 constexpr int kWeigh = 512, kPagesAtOnce = 4;
 __global__ void __launch_bounds__(kWeigh, 3) kv4_weigh_kernel(const __grid_constant__ AttendArgs a) {
   constexpr int kWarps = kWeigh / 32;
@@ -1536,10 +1536,14 @@ int attend(AttendArgs& a, int dev, cudaStream_t s) {
   const uint64_t slots = team ? 0 : uint64_t(2) * a.warps * 8 * NT;
   // where a cluster has all rows of a sequence and head it weighs the tokens too
   const bool weigh = a.mass && team && !a.s.starts && a.share <= 8 * NT;
-  // Scores are kept rather than computed again where each sequence has one tile of
-  // them and they are not too many.
+  // Scores are kept rather than computed again where each sequence has one tile of them,
+  // they are not too many, and they are no more than the keys are worth.  16 sequences of
+  // 16384 tokens, 8 cached heads, the whole call kept / again: 64 columns, 1 query row a cached
+  // head 63 / 88 us, 8 80 / 88, 9 108 / 116, 12 118 / 116, 16 130 / 117; 128 columns, 1 85 / 121,
+  // 8 103 / 124, 16 165 / 180; 256 columns, 1 148 / 215, 8 167 / 218.
   const uint64_t scores = uint64_t(a.s.B) * a.s.heads * uint64_t(a.s.width) * uint64_t(a.share) * (kPage * 4);
-  const bool kept = a.mass && !team && !a.s.starts && a.share <= 8 * NT && scores <= kMostScores;
+  const bool kept =
+      a.mass && !team && !a.s.starts && a.share <= 8 * NT && a.share * 6 <= D && scores <= kMostScores;
   const uint64_t b_lse = a.mass && !weigh ? up(uint64_t(a.T) * a.q_heads * 4) : 0, b_ml = up(slots * 8), b_part = slots * D * 4,
                  b_scores = kept ? scores : 0;
   uint8_t* ws = nullptr;
