@@ -18,8 +18,8 @@ __device__ __forceinline__ float bf16_value(uint32_t bits) { return __uint_as_fl
 // 8 u .. 8 u + 7; four of them share a group.  A warp takes `span` rows of the call,
 // whose places its lanes look up side by side, and kHeads heads of each: kLanes at a
 // time, STEPS of them with the loads of their keys and values in flight together.
-// Instructions bound the writing, some 60 for 8 columns, and the places' look-up
-// where many sequences have a few rows each.  65536 rows of 8 heads, one look-up for
+// Instructions bound the writing, 102 for 8 columns, some 60 of them their codes and
+// scale, and the places' look-up where many sequences have a few rows each.  65536 rows of 8 heads, one look-up for
 // four rows or (for every row), and the share of the copy rate:
 //   columns  write                 read
 //    64       38 (45) us  0.66      33 (37) us  0.77
