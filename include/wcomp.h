@@ -538,7 +538,8 @@ typedef struct {
  * What cannot be checked on the host is checked in the kernels: a length above
  * width * 64 is taken as width * 64, a page outside the cache as if its tokens
  * were not there, and starts that are negative, descend or pass T leave the rows around
- * them undefined but reach no others; wcomp_device_check then reports WCOMP_EBOUNDS.
+ * them undefined but reach no others; wcomp_device_check then reports WCOMP_EBOUNDS.  (A
+ * call without rows or sequences launches nothing and reports nothing.)
  */
 typedef struct {
   const int32_t* d_table;   /* [B, width] pages */
